@@ -15,7 +15,8 @@ import threading
 
 from . import workloads  # noqa: F401  (seeded synthetic inputs)
 
-__all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache", "pva_get_status", "pva_schedule", "pva_status_string",
+__all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache",
+           "pva_block_tables", "pva_rope_axes", "pva_gqa_tree", "pva_kvcache_accept", "pva_get_status", "pva_schedule", "pva_status_string",
            "pva_last_error", "pva_release", "pva_version", "pva_profile", "pva_kernel_times",
            "pva_selftest_wait", "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
 
@@ -26,7 +27,7 @@ PVA_OK, PVA_ERR_INVALID_ARG, PVA_ERR_UNSUPPORTED, PVA_ERR_CUDA, PVA_ERR_OOM = 0,
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 DEV_FLAGS = {"cu_q_start": 0x1, "cu_kv_start": 0x2, "cu_q_order": 0x4, "cu_kv_order": 0x8,
              "too_many": 0x10, "null_tensor": 0x20, "kv_len": 0x40, "kv_cache": 0x80,
-             "wait_timeout": 0x100}
+             "wait_timeout": 0x100, "tree": 0x200, "blocks": 0x400, "rope": 0x800}
 
 _lock = threading.Lock()
 _lib = None
@@ -70,6 +71,18 @@ def load_library(path: str | None = None):
         lib.pva_gqa_kvcache.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i,
                                         i, i, i, i, i, f, f, i, i, vp]
         lib.pva_gqa_kvcache.restype = i
+        i64 = ctypes.c_int64
+        lib.pva_block_tables.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i64, vp]
+        lib.pva_block_tables.restype = i
+        lib.pva_rope_axes.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i64, i64, i64, i64,
+                                      i, i, i, i, vp, i, i, i, vp, i64, vp, vp, vp, i, i, i, vp]
+        lib.pva_rope_axes.restype = i
+        lib.pva_gqa_tree.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i,
+                                     i, i, i, i, i, i, i, i, vp, i, i, f, f, i, i, vp]
+        lib.pva_gqa_tree.restype = i
+        lib.pva_kvcache_accept.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i64, i, i, i, i, i,
+                                           i, vp]
+        lib.pva_kvcache_accept.restype = i
         lib.pva_get_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.pva_get_status.restype = i
         lib.pva_schedule.argtypes = [vp, vp, i, i, i, i, i, i, i,
@@ -222,6 +235,218 @@ def pva_gqa_kvcache(q, k_new, v_new, k_cache, v_cache, seqlens_k, out, num_heads
                              rows, int(bool(rotary_interleaved)), rot_code, float(scale),
                              float(softcap), int(local_window), code, _stream_ptr(stream))
     _check(rc)
+
+
+def _need(ok: bool, message: str) -> None:
+    if not ok:
+        raise PvaError(PVA_ERR_INVALID_ARG, message)
+
+
+def _same_device(first, *others) -> None:
+    """Every tensor on the device of ``first``, which has to be the current one."""
+    dev = first.device
+    for t in others:
+        _need(t is None or t.device == dev, "the tensors are on different devices")
+    if first.is_cuda:
+        import torch
+        _need(dev.index == torch.cuda.current_device(),
+              f"the tensors are on {dev}, which is not the current device")
+
+
+def _plain(t, name: str, dtype, shape) -> None:
+    """A contiguous tensor of this type and shape (None in the shape: any extent)."""
+    if t is None:
+        return
+    _need(t.dtype == dtype, f"{name} must be {dtype}")
+    _need(t.dim() == len(shape) and all(w is None or w == n for w, n in zip(shape, t.shape)),
+          f"{name} must have the shape {tuple('any' if w is None else w for w in shape)}, "
+          f"not {tuple(t.shape)}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _rotary(cos_cache, sin_cache, sections):
+    """(rotary_dim, table rows, table type code, host sections or None)."""
+    _need(sin_cache is not None, "cos_cache and sin_cache come together")
+    _plain(cos_cache, "cos_cache", cos_cache.dtype, (None, None))
+    _plain(sin_cache, "sin_cache", cos_cache.dtype, tuple(cos_cache.shape))
+    host = None if sections is None else (ctypes.c_int32 * len(sections))(*sections)
+    return 2 * int(cos_cache.shape[1]), int(cos_cache.shape[0]), _dtype_code(cos_cache), host
+
+
+def pva_block_tables(lens, block_table, held, free_blocks, free_count, page_size: int, cu_new=None,
+                     slot_map=None, stream=None) -> None:
+    """Give every sequence the blocks its length needs, on the device: lens,
+    held int32 [B], block_table int32 [B, max_blocks], free_blocks int32 [pool]
+    (a stack of *free_count int32 [1]* blocks).  With ``cu_new`` int32 [B + 1]
+    and ``slot_map`` int64 [n], also the cache slot of every new packed token.
+    See include/pva.h for the order and the errors (``blocks`` bit)."""
+    import torch
+    _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
+    B, width = block_table.shape
+    i32 = torch.int32
+    _plain(lens, "lens", i32, (B,))
+    _plain(held, "held", i32, (B,))
+    _plain(block_table, "block_table", i32, (B, width))
+    _plain(free_blocks, "free_blocks", i32, (None,))
+    _plain(free_count, "free_count", i32, (1,))
+    _plain(cu_new, "cu_new", i32, (B + 1,))
+    _plain(slot_map, "slot_map", torch.int64, (None,))
+    _need((cu_new is None) == (slot_map is None), "cu_new and slot_map come together")
+    _same_device(block_table, lens, held, free_blocks, free_count, cu_new, slot_map)
+    _check(load_library().pva_block_tables(
+        lens.data_ptr(), block_table.data_ptr(), held.data_ptr(), free_blocks.data_ptr(),
+        free_count.data_ptr(), _ptr_or_none(cu_new), _ptr_or_none(slot_map), B, width,
+        int(page_size), free_blocks.shape[0], 0 if slot_map is None else slot_map.shape[0],
+        _stream_ptr(stream)))
+
+
+def _token_rows(t, name: str, like):
+    """Heads and token stride of a [tokens, heads, d] tensor whose tokens are
+    each contiguous."""
+    _need(t.dim() == 3 and t.dtype == like.dtype and t.shape[0] == like.shape[0]
+          and t.shape[2] == like.shape[2],
+          f"{name} must be [tokens, heads, head_size] of one type with the others")
+    heads, d = t.shape[1], t.shape[2]
+    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == d),
+          f"{name}: the heads of a token must be contiguous")
+    return heads, max(t.stride(0), heads * d) if t.shape[0] <= 1 else t.stride(0)
+
+
+def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=None, sections=None,
+                  rotary_interleaved: bool = False, axes_interleaved: bool = False,
+                  inverse: bool = False, v=None, k_cache=None, v_cache=None, slot_map=None,
+                  stream=None) -> None:
+    """Rotate packed q [tokens, H, d] and/or k [tokens, Hkv, d] (token strides
+    allowed) into q_out / k_out by cos/sin tables [rows, rotary_dim/2], with
+    position_ids int64 [n_axes, tokens] and ``sections`` naming how many pairs
+    turn with each axis.  ``inverse`` is the rotation's gradient.  With v, the
+    caches [n_blocks, Hkv, page, d] and slot_map int64 [tokens], rotated keys
+    and values are also written to the cache."""
+    import torch
+    first = q if q is not None else k
+    _need(first is not None, "q or k is needed")
+    _need(first.dim() == 3, "q and k must be [tokens, heads, head_size]")
+    tokens, _, d = first.shape
+    H = Hkv = qs = ks = qos = kos = vs = 0
+    if q is not None:
+        H, qs = _token_rows(q, "q", first)
+        _need(q_out is not None and q_out.shape == q.shape, "q_out must have q's shape")
+        _, qos = _token_rows(q_out, "q_out", first)
+    else:
+        _need(q_out is None, "q and q_out come together")
+    if k is not None:
+        Hkv, ks = _token_rows(k, "k", first)
+        if k_out is not None:
+            _need(k_out.shape == k.shape, "k_out must have k's shape")
+            _, kos = _token_rows(k_out, "k_out", first)
+    _need(position_ids.dim() == 2, "position_ids must be [n_axes, tokens]")
+    n_axes = position_ids.shape[0]
+    _plain(position_ids, "position_ids", torch.int64, (None, tokens))
+    _need(sections is None or len(sections) == n_axes, "sections needs one entry per axis")
+    rot, rows, code, host = _rotary(cos_cache, sin_cache, sections)
+    blocks = page = 0
+    if k_cache is not None:
+        _need(k is not None and v is not None and v_cache is not None and slot_map is not None,
+              "the cache write needs k, v, both caches and slot_map")
+        _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_heads, page, head_size]")
+        blocks, page = k_cache.shape[0], k_cache.shape[2]
+        _plain(k_cache, "k_cache", first.dtype, (blocks, Hkv, page, d))
+        _plain(v_cache, "v_cache", first.dtype, (blocks, Hkv, page, d))
+        _plain(slot_map, "slot_map", torch.int64, (tokens,))
+        _need(v.shape == k.shape, "v must have k's shape")
+        _, vs = _token_rows(v, "v", first)
+    _same_device(first, q_out, k, k_out, v, cos_cache, sin_cache, position_ids, k_cache, v_cache,
+                 slot_map)
+    _check(load_library().pva_rope_axes(
+        _ptr_or_none(q), _ptr_or_none(k), _ptr_or_none(q_out), _ptr_or_none(k_out),
+        cos_cache.data_ptr(), sin_cache.data_ptr(), position_ids.data_ptr(), tokens, H, Hkv, d, qs,
+        ks, qos, kos, rot, rows, int(bool(rotary_interleaved)), n_axes, host,
+        int(bool(axes_interleaved)), int(bool(inverse)), code, _ptr_or_none(v), vs,
+        _ptr_or_none(k_cache), _ptr_or_none(v_cache), _ptr_or_none(slot_map), blocks, page,
+        _dtype_code(first), _stream_ptr(stream)))
+
+
+def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: int,
+                 kv_num_heads: int, parents=None, tree_lens=None, block_table=None, cos_cache=None,
+                 sin_cache=None, position_ids=None, sections=None,
+                 rotary_interleaved: bool = False, axes_interleaved: bool = False,
+                 scale: float = 0.0, softcap: float = 0.0, local_window: int = 0,
+                 stream=None) -> None:
+    """One GroupQueryAttention step of a tree of drafted tokens (``parents``
+    int32 [B, T], -1 a root; None: a chain) on a KV cache: q [B, T, H, d],
+    k_new/v_new [B, T, Hkv, d], caches [n_blocks, Hkv, page, d] with
+    ``block_table`` int32 [B, max_blocks] (None: sequence b owns block b),
+    past_lens int32 [B] rows before the step, tree_lens int32 [B] nodes in use;
+    optional rotation by cos/sin tables with position_ids int64 [n_axes, B, T]
+    (None: past + depth); out [B, T, H, d]."""
+    import torch
+    _need(q.dim() == 4, "q must be [B, tokens, num_heads, head_size]")
+    B, T, H, d = q.shape
+    H, Hkv = int(num_heads), int(kv_num_heads)
+    dt, i32 = q.dtype, torch.int32
+    _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_num_heads, page, head_size]")
+    blocks, page = k_cache.shape[0], k_cache.shape[2]
+    _plain(q, "q", dt, (B, T, H, d))
+    _plain(out, "out", dt, (B, T, H, d))
+    _plain(k_new, "k_new", dt, (B, T, Hkv, d))
+    _plain(v_new, "v_new", dt, (B, T, Hkv, d))
+    _plain(k_cache, "k_cache", dt, (blocks, Hkv, page, d))
+    _plain(v_cache, "v_cache", dt, (blocks, Hkv, page, d))
+    _plain(past_lens, "past_lens", i32, (B,))
+    _plain(parents, "parents", i32, (B, T))
+    _plain(tree_lens, "tree_lens", i32, (B,))
+    _plain(block_table, "block_table", i32, (B, None))
+    rot = rows = code = 0
+    n_axes, host = 1, None
+    if cos_cache is not None:
+        n_axes = 1 if position_ids is None else position_ids.shape[0]
+        if position_ids is None and sections is not None:
+            n_axes = len(sections)
+        _plain(position_ids, "position_ids", torch.int64, (n_axes, B, T))
+        _need(sections is None or len(sections) == n_axes, "sections needs one entry per axis")
+        rot, rows, code, host = _rotary(cos_cache, sin_cache, sections)
+    else:
+        _need(sin_cache is None and position_ids is None and sections is None,
+              "positions and sections need the cos and sin tables")
+    _same_device(q, k_new, v_new, k_cache, v_cache, past_lens, out, parents, tree_lens,
+                 block_table, cos_cache, sin_cache, position_ids)
+    _check(load_library().pva_gqa_tree(
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        past_lens.data_ptr(), _ptr_or_none(tree_lens), _ptr_or_none(parents),
+        _ptr_or_none(block_table), _ptr_or_none(cos_cache), _ptr_or_none(sin_cache),
+        _ptr_or_none(position_ids), out.data_ptr(), B, T, blocks, page,
+        0 if block_table is None else block_table.shape[1], H, Hkv, d, rot, rows,
+        int(bool(rotary_interleaved)), n_axes, host, int(bool(axes_interleaved)), code,
+        float(scale), float(softcap), int(local_window), _dtype_code(q), _stream_ptr(stream)))
+
+
+def pva_kvcache_accept(k_cache, v_cache, past_lens, path, path_lens, new_lens, block_table=None,
+                       stream=None) -> None:
+    """Move the accepted path's rows of a drafted tree: cache row past + path[i]
+    becomes row past + i for i < path_lens, for every head and layer.  Caches
+    [n_blocks, Hkv, page, d] or [layers, n_blocks, Hkv, page, d], path int32
+    [B, width], past_lens, path_lens, new_lens (= past + path_lens) int32 [B]."""
+    import torch
+    _need(k_cache.dim() in (4, 5), "k_cache must be [layers,] [n_blocks, heads, page, head_size]")
+    _need(path.dim() == 2, "path must be [B, width]")
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    blocks, Hkv, page, d = k_cache.shape[-4:]
+    B, width = path.shape
+    i32 = torch.int32
+    _plain(k_cache, "k_cache", k_cache.dtype, tuple(k_cache.shape))
+    _plain(v_cache, "v_cache", k_cache.dtype, tuple(k_cache.shape))
+    _plain(path, "path", i32, (B, width))
+    _plain(past_lens, "past_lens", i32, (B,))
+    _plain(path_lens, "path_lens", i32, (B,))
+    _plain(new_lens, "new_lens", i32, (B,))
+    _plain(block_table, "block_table", i32, (B, None))
+    _same_device(k_cache, v_cache, past_lens, path, path_lens, new_lens, block_table)
+    _check(load_library().pva_kvcache_accept(
+        k_cache.data_ptr(), v_cache.data_ptr(), past_lens.data_ptr(), path.data_ptr(),
+        path_lens.data_ptr(), _ptr_or_none(block_table), new_lens.data_ptr(), B, width, layers,
+        blocks * Hkv * page * d, blocks, Hkv, page, d,
+        0 if block_table is None else block_table.shape[1], _dtype_code(k_cache),
+        _stream_ptr(stream)))
 
 
 def pva_forward_noalloc(q, k, v, cu_seqlens_q, cu_seqlens_kv, out, B: int, num_heads: int,

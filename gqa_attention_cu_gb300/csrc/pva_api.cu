@@ -16,6 +16,7 @@
 #include <mutex>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include <climits>
 
@@ -60,9 +61,11 @@ struct DeviceInfo {
 };
 
 struct Workspace {
-  uint32_t* status = nullptr;  // sticky status word (never moves)
+  uint32_t* status = nullptr;  // sticky status word (never moves); 256 bytes, zeroed once
   void* buf = nullptr;         // int region + partials
   size_t bytes = 0;
+  bool in_graph = false;       // handed to a call that was being captured
+  std::vector<void*> retired;  // outgrown buffers that a captured graph may still use
 };
 
 std::mutex g_mu;
@@ -252,8 +255,8 @@ int get_workspace(int dev, cudaStream_t stream, size_t need, Workspace** out) {
                   "first call on a stream must not be captured (workspace allocation)");
     cudaError_t e = cudaMalloc(&w.status, 256);
     if (e != cudaSuccess) return fail(PVA_ERR_OOM, "status word allocation failed");
-    e = cudaMemset(w.status, 0, 256);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset");
+    e = cudaMemsetAsync(w.status, 0, 256, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   }
   if (w.bytes < need) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -263,9 +266,15 @@ int get_workspace(int dev, cudaStream_t stream, size_t need, Workspace** out) {
                   "workspace must grow but the stream is being captured; warm it up first");
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    if (w.buf) cudaFree(w.buf);
+    // A graph captured on this stream keeps the address it was captured with,
+    // so a buffer that went into one lives until pva_release.
+    if (w.buf && w.in_graph)
+      w.retired.push_back(w.buf);
+    else if (w.buf)
+      cudaFree(w.buf);
     w.buf = nullptr;
     w.bytes = 0;
+    w.in_graph = false;
     size_t sz = need < (1u << 20) ? (1u << 20) : need;
     e = cudaMalloc(&w.buf, sz);
     if (e != cudaSuccess) {
@@ -273,6 +282,11 @@ int get_workspace(int dev, cudaStream_t stream, size_t need, Workspace** out) {
       return fail(PVA_ERR_OOM, "workspace allocation failed");
     }
     w.bytes = sz;
+  }
+  if (!w.in_graph) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaStreamIsCapturing(stream, &cs);
+    w.in_graph = cs != cudaStreamCaptureStatusNone;
   }
   *out = &w;
   return PVA_OK;
@@ -323,6 +337,34 @@ int prepare(const void* q, const void* k, const void* v, const int32_t* cu_q,
   P.dec_cap_units = plan->cap_units;
   return PVA_OK;
 }
+
+}  // namespace
+
+namespace pva {
+namespace host {
+
+std::mutex& api_mutex() { return g_mu; }
+
+int acquire(cudaStream_t stream, size_t need, CallContext* c) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  DeviceInfo di;
+  int rc = device_info(dev, &di);
+  if (rc != PVA_OK) return rc;
+  Workspace* w = nullptr;
+  rc = get_workspace(dev, stream, need, &w);
+  if (rc != PVA_OK) return rc;
+  c->num_sms = di.num_sms;
+  c->status = w->status;
+  c->buf = static_cast<uint8_t*>(w->buf);
+  return PVA_OK;
+}
+
+}  // namespace host
+}  // namespace pva
+
+namespace {
 
 // What one call computes, whichever entry point it came through.
 struct Spec {
@@ -665,8 +707,8 @@ int pva_get_status(void* stream_, uint32_t* device_flags) {
   uint32_t v = 0;
   e = cudaMemcpy(&v, it->second.status, sizeof v, cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy status");
-  e = cudaMemset(it->second.status, 0, sizeof v);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemset status");
+  e = cudaMemsetAsync(it->second.status, 0, sizeof v, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync status");
   *device_flags = v;
   return PVA_OK;
 }
@@ -781,6 +823,7 @@ void pva_release(void) {
   for (auto it = g_ws.begin(); it != g_ws.end();) {
     if (it->first.first == dev) {
       if (it->second.buf) cudaFree(it->second.buf);
+      for (void* old : it->second.retired) cudaFree(old);
       if (it->second.status) cudaFree(it->second.status);
       it = g_ws.erase(it);
     } else {

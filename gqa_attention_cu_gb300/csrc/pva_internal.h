@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <string>
 #include <type_traits>
 
@@ -139,6 +140,27 @@ int cuda_fail(cudaError_t e, const char* what);
 int get_encoder();
 int encode_map(CUtensorMap* map, const void* base, int dtype, int dim, int heads, int box_dim,
                int box_heads, int box_tokens, bool swizzle128);
+int encode_plane_map(CUtensorMap* map, const void* base, int dtype, int dim, int rows,
+                     long long planes, int box_dim, int box_rows, bool swizzle128);
+// What a call gets from the library for its device and stream (under api_mutex).
+struct CallContext {
+  int num_sms = 0;
+  uint32_t* status = nullptr;  // [0] sticky PVA_DEV_* bits; words 16 to 63 start at zero and are
+                               // returned to zero by every kernel that uses them
+  uint8_t* buf = nullptr;      // workspace of at least the bytes asked for
+};
+std::mutex& api_mutex();
+int acquire(cudaStream_t stream, size_t need, CallContext* c);
+// Runs the body of a C entry point: an exception (host memory running out)
+// becomes an error code instead of leaving through the C interface.
+template <typename F>
+int guarded(F&& body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return PVA_ERR_OOM;
+  }
+}
 // Drops pva_forward_noalloc's cached address of its static scratch on `dev`
 // (the next call looks it up again in the current context).
 void noalloc_forget_device(int dev);

@@ -1,0 +1,568 @@
+// One step of a tree of drafted tokens over a KV cache (pva_gqa_tree): host
+// side, front end, fp32 attention and the join of split items.  The f16/bf16
+// attention kernel is in pva_tree_tc.cu, rotation and append in pva_rope.cu.
+//
+//   pva_tree_front_kernel  one CTA per sequence: bounds, the block table,
+//       positions and parents; each node's ancestors as a bit mask and its
+//       depth; the key tiles of each q tile.  The last CTA to finish adds the
+//       tiles up and cuts the line of tiles (pva_tree.h) -- or rejects the
+//       step, all of it, when any CTA found something wrong.
+//   pva_rope_kernel        rotated queries to scratch, new rows to the cache,
+//       zeros for unused nodes.
+//   attention              one piece of the line per CTA.
+//   pva_tree_join_kernel   adds up the parts of items that lie across a cut.
+#include <limits.h>
+#include <math.h>
+
+#include "pva_rope.cuh"
+#include "pva_tree.h"
+
+using namespace pva;
+using namespace pva::host;
+
+namespace pva {
+namespace {
+
+constexpr int kFrontThreads = 256;
+constexpr int kMaxTreeNodes = 1024;
+constexpr int kTreeRowsF32 = 32, kTreeKeysF32 = 32;
+// Words of the status block (zero between calls).
+constexpr int kWordArrived = 16, kWordBad = 17;
+
+__global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParams p) {
+  allow_next_grid();
+  wait_prior_grid();
+  __shared__ int s_parent[kMaxTreeNodes];
+  __shared__ uint32_t s_bad;
+  __shared__ int s_last;
+  __shared__ long long s_sum[kFrontThreads / 32 + 1];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int past = p.past[b], n = tree_nodes(p, b);
+  if (tid == 0) {
+    s_bad = 0;
+    const long long total = (long long)past + n;
+    if (n < 0 || n > p.T) s_bad |= PVA_DEV_TREE;
+    if (past < 0 || total > (long long)p.max_blocks * p.page) s_bad |= PVA_DEV_KV_CACHE;
+  }
+  __syncthreads();
+  const bool sane = s_bad == 0;
+  __syncthreads();
+  if (sane && n > 0) {
+    // the blocks that hold the rows this step reads and writes
+    if (p.table) {
+      const long long from = p.window > 0 ? (long long)past + 1 - p.window : 0;
+      const int first = from > 0 ? (int)(from / p.page) : 0, end = (past + n - 1) / p.page + 1;
+      bool bad = false;
+      for (int i = first + tid; i < end; i += kFrontThreads) {
+        const int block = p.table[(size_t)b * p.max_blocks + i];
+        bad = bad || block < 0 || block >= p.n_blocks;
+      }
+      if (bad) atomicOr(&s_bad, PVA_DEV_BLOCKS);
+    }
+    if (p.parents) {
+      bool bad = false;
+      for (int i = tid; i < n; i += kFrontThreads) {
+        const int up = p.parents[(size_t)b * p.T + i];
+        s_parent[i] = up;
+        bad = bad || up < -1 || up >= i;
+      }
+      if (bad) atomicOr(&s_bad, PVA_DEV_TREE);
+    }
+    __syncthreads();
+    const bool walk = s_bad == 0;
+    bool off_table = false;
+    for (int i = tid; i < n && walk; i += kFrontThreads) {
+      int depth = i;
+      if (p.parents) {
+        // The way up visits falling node indices, so the words of the mask
+        // are completed from the node's own word downwards.
+        uint32_t* row = p.mask + ((size_t)b * p.T + i) * p.W32;
+        for (int w = p.W32 - 1; w > i >> 5; --w) row[w] = 0;
+        int w = i >> 5;
+        uint32_t bits = 0;
+        depth = 0;
+        for (int a = i; a >= 0; a = s_parent[a], ++depth) {
+          while (w > a >> 5) {
+            row[w--] = bits;
+            bits = 0;
+          }
+          if (p.window <= 0 || depth < p.window) bits |= 1u << (a & 31);
+        }
+        --depth;
+        for (; w >= 0; --w, bits = 0) row[w] = bits;
+        p.depth[(size_t)b * p.T + i] = depth;
+      }
+      if (p.rot > 0) {
+        for (int a = 0; a < p.n_axes; ++a) {
+          const long long at = p.pos ? p.pos[((size_t)a * p.B + b) * p.T + i] : (long long)past + depth;
+          off_table = off_table || at < 0 || at >= p.cache_rows;
+        }
+      }
+    }
+    if (off_table) atomicOr(&s_bad, PVA_DEV_ROPE);
+  }
+  // tiles of each q tile, and where it starts within a kv head
+  if (tid < 32) {
+    int32_t* qs = p.q_start + (size_t)b * (p.QT + 1);
+    long long carry = 0;
+    const int qt = sane ? (int)(((long long)n * p.G + p.rows - 1) / p.rows) : 0;
+    for (int t0 = 0; t0 <= p.QT; t0 += 32) {
+      const int t = t0 + tid;
+      int x = 0;
+      if (t < qt) {
+        int lo, hi;
+        tree_item_range(p, past, n, t, lo, hi);
+        x = (hi + p.bn - 1) / p.bn - lo / p.bn;
+      }
+      int upto = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (tid >= o) upto += y;
+      }
+      if (t <= p.QT) qs[t] = (int)(carry + upto - x);
+      carry += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    // carry may pass 31 bits only where the line does too, which is refused below
+    if (tid == 0) {
+      const long long all = carry * p.Hkv;
+      if (all > INT_MAX) atomicOr(&s_bad, PVA_DEV_TOO_MANY);
+      p.tile_start[b] = all > INT_MAX ? 0 : (int)all;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    if (s_bad) atomicOr(p.status + kWordBad, s_bad);
+    __threadfence();
+    s_last = atomicAdd(p.status + kWordArrived, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  // The last CTA: sums of the sequences' tiles, in place.
+  __threadfence();
+  long long carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kFrontThreads) {
+    const int i = b0 + tid;
+    const long long x = i < p.B ? __ldcg(p.tile_start + i) : 0;
+    long long upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if ((tid & 31) >= o) upto += y;
+    }
+    if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
+    __syncthreads();
+    long long before = carry, all = carry;
+    for (int w = 0; w < kFrontThreads / 32; ++w) {
+      if (w < tid >> 5) before += s_sum[w];
+      all += s_sum[w];
+    }
+    if (i < p.B) p.tile_start[i] = (int)(before + upto - x);
+    carry = all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    uint32_t bad = atomicExch(p.status + kWordBad, 0u);
+    atomicExch(p.status + kWordArrived, 0u);
+    if (carry > INT_MAX - 4 * (long long)p.pieces) bad |= PVA_DEV_TOO_MANY;
+    // a step after a rejected one would append after rows that are missing
+    const bool latched = (atomicOr(p.status, 0u) & PVA_DEV_KV_CACHE) != 0;
+    if (bad) atomicOr(p.status, bad | PVA_DEV_KV_CACHE);
+    const bool ok = bad == 0 && !latched;
+    const int tiles = ok ? (int)carry : 0;
+    const int even = (tiles + p.pieces - 1) / p.pieces;
+    p.tile_start[p.B] = tiles;
+    p.hdr[0] = ok ? 1 : 0;
+    p.hdr[1] = tiles;
+    p.hdr[2] = even > p.min_chunk ? even : p.min_chunk;
+  }
+}
+
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over an item's parts c, in
+// the order of the line; M = max m_c.  One warp per row, 4 channels a lane at a
+// time; rows of items that were not split are left to the attention kernel.
+template <typename T>
+__global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
+  allow_next_grid();
+  wait_prior_grid();
+  if (p.hdr[0] == 0) return;
+  const int chunk = p.hdr[2];
+  const int lane = threadIdx.x & 31;
+  const long long n_rows = (long long)p.B * p.T * p.H;
+  for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < n_rows;
+       x += (long long)gridDim.x * 8) {
+    const int head = (int)(x % p.H);
+    const long long tok = x / p.H;
+    const int b = (int)(tok / p.T), node = (int)(tok - (long long)b * p.T);
+    if (node >= tree_nodes(p, b)) continue;
+    const int h = head / p.G, row = node * p.G + head % p.G, t = row / p.rows;
+    const int32_t* qs = p.q_start + (size_t)b * (p.QT + 1);
+    const int start = p.tile_start[b] + h * qs[p.QT] + qs[t], end = start + qs[t + 1] - qs[t];
+    const int c0 = start / chunk, c1 = (end - 1) / chunk;
+    if (c0 == c1) continue;
+    const int r = row - t * p.rows;
+    float m = __int_as_float(0xff800000);
+    for (int c = c0 + lane; c <= c1; c += 32)
+      m = fmaxf(m, p.part_ml[(size_t)tree_slot(c, c == c0) * p.rows + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float top = m == __int_as_float(0xff800000) ? 0.0f : m;
+    float l = 0.0f;
+    for (int c = c0; c <= c1; ++c) {
+      const float2 ml = p.part_ml[(size_t)tree_slot(c, c == c0) * p.rows + r];
+      l += exp2f(ml.x - top) * ml.y;
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    T* out = static_cast<T*>(p.out) + (size_t)x * p.d;
+    for (int d0 = lane; d0 < p.d; d0 += 32) {
+      float acc = 0.0f;
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const size_t at = (size_t)tree_slot(c, c == c0) * p.rows + r;
+        acc = fmaf(exp2f(p.part_ml[at].x - top), p.part_o[at * p.d + d0], acc);
+      }
+      out[d0] = static_cast<T>(acc * inv);
+    }
+  }
+}
+
+// fp32 attention on the CUDA cores, exact fp32 products (no TF32).  A CTA of 4
+// warps holds 32 query rows and walks over its piece's tiles of 32 keys; a warp
+// owns 8 rows, lane j scores key j, lane c sums channels c, c + 32, ...  Keys
+// outside the item's range and invisible ones take part with weight 0; their
+// rows are not read (the range) or have value 0 (p = 0 times a finite row).
+constexpr int kWarpsF32 = 4, kRowsPerWarpF32 = kTreeRowsF32 / kWarpsF32, kChanF32 = 8;
+
+__global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams p) {
+  extern __shared__ float smem[];
+  const int d = p.d, kstride = d + 1;
+  float* sq = smem;                          // [32][d]
+  float* sk = sq + kTreeRowsF32 * d;         // [32][d + 1]
+  float* sv = sk + kTreeKeysF32 * kstride;   // [32][d]
+  allow_next_grid();
+  wait_prior_grid();
+  const int tiles = p.hdr[1], chunk = p.hdr[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float NEG_INF = __int_as_float(0xff800000);
+  const float* q = static_cast<const float*>(p.q);
+  const float* kc = static_cast<const float*>(p.k_cache);
+  const float* vc = static_cast<const float*>(p.v_cache);
+  const int piece = blockIdx.x;
+  const long long from = (long long)piece * chunk;
+  const int end = (int)(from + chunk < tiles ? from + chunk : tiles);
+  for (long long x = from; x < end;) {
+    const TreeSegment s = tree_segment(p, piece, (int)x, end);
+    x += s.count;
+    const int n_rows = min(p.rows, s.n * p.G - s.t * p.rows);
+    const int total = s.past + s.n;
+    __syncthreads();
+    const float* q0 = q + (((size_t)s.b * p.Hkv + s.h) * p.T * p.G + (size_t)s.t * p.rows) * d;
+    for (int e = threadIdx.x; e < kTreeRowsF32 * d; e += blockDim.x)
+      sq[e] = e < n_rows * d ? q0[e] : 0.0f;
+    float m[kRowsPerWarpF32], l[kRowsPerWarpF32], acc[kRowsPerWarpF32][kChanF32];
+    int row_lo[kRowsPerWarpF32], row_hi[kRowsPerWarpF32];
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarpF32; ++r) {
+      m[r] = NEG_INF;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kChanF32; ++u) acc[r][u] = 0.0f;
+      const int lr = warp * kRowsPerWarpF32 + r;
+      const int node = lr < n_rows ? (s.t * p.rows + lr) / p.G : 0;
+      const int depth = p.parents ? p.depth[(size_t)s.b * p.T + node] : node;
+      row_lo[r] = p.window > 0 ? s.past + depth + 1 - p.window : 0;
+      row_hi[r] = p.parents ? s.past : s.past + node + 1;
+    }
+    for (int j = s.j0; j < s.j0 + s.count; ++j) {
+      const int k0 = j * kTreeKeysF32;
+      __syncthreads();
+      for (int e = threadIdx.x; e < kTreeKeysF32 * d; e += blockDim.x) {
+        const int i = e / d, c = e - i * d, key = k0 + i;
+        float kk = 0.0f, vv = 0.0f;
+        if (key >= s.lo && key < total) {
+          const int in = key / p.page;
+          const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+          const size_t at = (((size_t)block * p.Hkv + s.h) * p.page + (key - in * p.page)) * d + c;
+          kk = kc[at];
+          vv = vc[at];
+        }
+        sk[i * kstride + c] = kk;
+        sv[i * d + c] = vv;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarpF32; ++r) {
+        const int lr = warp * kRowsPerWarpF32 + r;
+        if (lr >= n_rows) continue;  // warp-uniform
+        const int key = k0 + lane;
+        bool seen = key >= row_lo[r] && key < row_hi[r];
+        const int other = key - s.past;
+        if (p.parents && other >= 0 && other < s.n) {
+          const int node = (s.t * p.rows + lr) / p.G;
+          seen = (p.mask[((size_t)s.b * p.T + node) * p.W32 + (other >> 5)] >> (other & 31)) & 1;
+        }
+        float sc = 0.0f;
+        const float* qr = sq + lr * d;
+        const float* kr = sk + lane * kstride;
+        for (int c = 0; c < d; ++c) sc = fmaf(qr[c], kr[c], sc);
+        sc *= p.scale;
+        if (p.softcap != 0.0f) sc = p.softcap * tanhf(sc / p.softcap);
+        // base-2 units, as the join expects
+        const float xs = seen ? sc * 1.4426950408889634f : NEG_INF;
+        float mt = xs;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        const float m_new = fmaxf(m[r], mt);
+        if (!__any_sync(0xffffffffu, seen)) continue;
+        const float base = m_new == NEG_INF ? 0.0f : m_new;
+        const float alpha = exp2f(m[r] - base);
+        const float pr = seen ? exp2f(xs - base) : 0.0f;
+        float ps = pr;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+        l[r] = l[r] * alpha + ps;
+        m[r] = m_new;
+#pragma unroll
+        for (int u = 0; u < kChanF32; ++u) acc[r][u] *= alpha;
+        for (int i = 0; i < kTreeKeysF32; ++i) {
+          const float w = __shfl_sync(0xffffffffu, pr, i);
+          if (w == 0.0f) continue;  // an unseen key's row may hold anything
+#pragma unroll
+          for (int u = 0; u < kChanF32; ++u) {
+            const int c = lane + 32 * u;
+            if (c < d) acc[r][u] = fmaf(w, sv[i * d + c], acc[r][u]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarpF32; ++r) {
+      const int lr = warp * kRowsPerWarpF32 + r;
+      if (lr >= n_rows) continue;
+      if (s.slot < 0) {
+        const int row = s.t * p.rows + lr, node = row / p.G, g = row - node * p.G;
+        float* o = static_cast<float*>(p.out) +
+                   (((size_t)s.b * p.T + node) * p.H + (size_t)s.h * p.G + g) * d;
+        const float inv = l[r] != 0.0f ? 1.0f / l[r] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < kChanF32; ++u)
+          if (lane + 32 * u < d) o[lane + 32 * u] = acc[r][u] * inv;
+      } else {
+        const size_t at = (size_t)s.slot * p.rows + lr;
+        if (lane == 0) p.part_ml[at] = make_float2(m[r], l[r]);
+#pragma unroll
+        for (int u = 0; u < kChanF32; ++u)
+          if (lane + 32 * u < d) p.part_o[at * d + lane + 32 * u] = acc[r][u];
+      }
+    }
+  }
+}
+
+cudaError_t launch_join(const TreeParams& p, int dtype, int num_sms, cudaStream_t s) {
+  const long long want = ((long long)p.B * p.T * p.H + 7) / 8;
+  const dim3 grid((unsigned)(want < num_sms * 8 ? want : num_sms * 8));
+  switch (dtype) {
+    case PVA_F32: return launch_dependent(pva_tree_join_kernel<float>, grid, dim3(256), 0, s, p);
+    case PVA_F16: return launch_dependent(pva_tree_join_kernel<__half>, grid, dim3(256), 0, s, p);
+    default:
+      return launch_dependent(pva_tree_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_f32(const TreeParams& p, cudaStream_t s) {
+  const size_t smem = sizeof(float) * ((size_t)kTreeRowsF32 * p.d + (size_t)kTreeKeysF32 * (p.d + 1) +
+                                       (size_t)kTreeKeysF32 * p.d);
+  cudaError_t e = cudaFuncSetAttribute(pva_tree_f32_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(pva_tree_f32_kernel, dim3(p.pieces), dim3(kWarpsF32 * 32), smem, s, p);
+}
+
+}  // namespace pva
+
+namespace {
+
+int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+             const int32_t* past_lens, const int32_t* tree_lens, const int32_t* parents,
+             const int32_t* block_table, const void* cos_cache, const void* sin_cache,
+             const int64_t* position_ids, void* out, int B, int T, int n_blocks, int page_size,
+             int max_blocks, int H, int Hkv, int d, int rot, int cache_rows,
+             int rotary_interleaved, int n_axes, const int32_t* sections, int axes_interleaved,
+             int rotary_dtype, float scale, float softcap, int window, int dtype,
+             cudaStream_t stream) {
+  if (!q || !k_new || !v_new || !k_cache || !v_cache || !past_lens || !out)
+    return fail(PVA_ERR_INVALID_ARG, "null q, k_new, v_new, cache, past_lens or out pointer");
+  if (B < 1 || T < 1 || n_blocks < 1 || page_size < 1)
+    return fail(PVA_ERR_INVALID_ARG, "need B >= 1, tokens >= 1, n_blocks >= 1, page_size >= 1");
+  if (H < 1 || Hkv < 1 || H % Hkv != 0)
+    return fail(PVA_ERR_INVALID_ARG,
+                "num_heads must be a positive multiple of a positive kv_num_heads");
+  if (dtype != PVA_F32 && dtype != PVA_F16 && dtype != PVA_BF16)
+    return fail(PVA_ERR_INVALID_ARG, "dtype must be 0 (f32), 1 (f16) or 2 (bf16)");
+  if (!isfinite(scale) || !isfinite(softcap))
+    return fail(PVA_ERR_INVALID_ARG, "scale and softcap must be finite");
+  const bool tc = dtype != PVA_F32;
+  if (tc ? d != 64 && d != 96 && d != 128 && d != 192 && d != 256
+         : d < 2 || d > 256 || d % 2 != 0)
+    return fail(PVA_ERR_UNSUPPORTED,
+                "head_size must be 64, 96, 128, 192 or 256 (f16/bf16), or even and at most 256 (f32)");
+  const int G = H / Hkv;
+  if (parents && T > kMaxTreeNodes)
+    return fail(PVA_ERR_UNSUPPORTED, "a tree has at most 1024 nodes");
+  if (block_table) {
+    if (max_blocks < 1) return fail(PVA_ERR_INVALID_ARG, "max_blocks must be >= 1");
+    if (page_size < 16 || (page_size & (page_size - 1)) != 0)
+      return fail(PVA_ERR_UNSUPPORTED, "page_size must be a power of two of at least 16");
+  } else {
+    if (n_blocks != B)
+      return fail(PVA_ERR_INVALID_ARG, "without a block table the cache has one block a sequence");
+    max_blocks = 1;
+  }
+  if ((long long)B * T > INT_MAX || (long long)T * G > INT_MAX / 2 ||
+      (long long)max_blocks * page_size > INT_MAX - 65536 ||
+      (long long)n_blocks * Hkv > INT_MAX)
+    return fail(PVA_ERR_INVALID_ARG, "cache or token extents do not fit in int32");
+  RopeStep r{};
+  int rc;
+  if (rot != 0) {
+    rc = check_rope(cos_cache, sin_cache, rot, cache_rows, rotary_interleaved, n_axes, sections,
+                    axes_interleaved, rotary_dtype, dtype, d, &r.rt);
+    if (rc != PVA_OK) return rc;
+  }
+  const size_t size = tc ? 2 : 4;
+  const uintptr_t mis = (uintptr_t)q | (uintptr_t)k_new | (uintptr_t)v_new | (uintptr_t)k_cache |
+                        (uintptr_t)v_cache | (uintptr_t)out;
+  if (tc && (mis & 15))
+    return fail(PVA_ERR_INVALID_ARG, "q, k_new, v_new, caches and out must be 16-byte aligned");
+  if (mis % size) return fail(PVA_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+
+  TreeParams p{};
+  p.past = past_lens;
+  p.lens = tree_lens;
+  p.parents = parents;
+  p.table = block_table;
+  p.pos = rot ? position_ids : nullptr;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.d = d;
+  p.page = page_size;
+  p.max_blocks = max_blocks;
+  p.n_blocks = n_blocks;
+  p.window = window > 0 ? window : 0;
+  const float s = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
+  p.scale = fabsf(s);
+  p.softcap = fabsf(softcap);
+  p.rot = rot;
+  p.n_axes = rot ? n_axes : 1;
+  p.cache_rows = cache_rows;
+  p.rows = tc ? kTcRows : kTreeRowsF32;
+  p.bn = tc ? tree_keys(d) : kTreeKeysF32;
+  p.QT = (int)(((long long)T * G + p.rows - 1) / p.rows);
+  p.W32 = parents ? (T + 31) / 32 : 0;
+  p.min_chunk = 1;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.out = out;
+
+  std::lock_guard<std::mutex> lock(api_mutex());
+  CallContext c;
+  if ((rc = acquire(stream, 0, &c)) != PVA_OK) return rc;
+  p.pieces = tc ? c.num_sms : 2 * c.num_sms;
+  // workspace, in 256-byte steps
+  size_t used = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = used;
+    used += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t at_hdr = take(16), at_tiles = take(4 * ((size_t)B + 1));
+  const size_t at_q_start = take(4 * (size_t)B * (p.QT + 1));
+  const size_t at_depth = take(parents ? 4 * (size_t)B * T : 0);
+  const size_t at_mask = take(4 * (size_t)B * T * p.W32);
+  const size_t at_q = take((size_t)B * T * H * d * size);
+  const size_t at_o = take(sizeof(float) * 2 * p.pieces * p.rows * (size_t)d);
+  const size_t at_ml = take(sizeof(float2) * 2 * p.pieces * (size_t)p.rows);
+  if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
+  p.status = c.status;
+  p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
+  p.tile_start = reinterpret_cast<int32_t*>(c.buf + at_tiles);
+  p.q_start = reinterpret_cast<int32_t*>(c.buf + at_q_start);
+  p.depth = reinterpret_cast<int32_t*>(c.buf + at_depth);
+  p.mask = reinterpret_cast<uint32_t*>(c.buf + at_mask);
+  p.q = c.buf + at_q;
+  p.part_o = reinterpret_cast<float*>(c.buf + at_o);
+  p.part_ml = reinterpret_cast<float2*>(c.buf + at_ml);
+
+  CUtensorMap tq, tk, tv;
+  if (tc) {
+    // boxes of one page's rows (a page shorter than a key tile), or of a tile
+    const int box = block_table && page_size < p.bn ? page_size : p.bn;
+    const long long planes = (long long)n_blocks * Hkv;
+    if ((rc = get_encoder()) != PVA_OK ||
+        (rc = encode_plane_map(&tq, p.q, dtype, d, T * G, (long long)B * Hkv, 64, p.rows, true)) !=
+            PVA_OK ||
+        (rc = encode_plane_map(&tk, k_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK ||
+        (rc = encode_plane_map(&tv, v_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK)
+      return rc;
+  }
+
+  r.q = q;
+  r.k = k_new;
+  r.v = v_new;
+  r.q_out = p.q;
+  r.k_cache = k_cache;
+  r.v_cache = v_cache;
+  r.q_stride = (long long)H * d;
+  r.k_stride = r.v_stride = (long long)Hkv * d;
+  r.tokens = B * T;
+  r.H = H;
+  r.Hkv = Hkv;
+  r.d = d;
+  r.pos = p.pos;
+  r.page = page_size;
+  r.hdr = p.hdr;
+  r.past = past_lens;
+  r.lens = tree_lens;
+  r.depth = parents ? p.depth : nullptr;
+  r.table = block_table;
+  r.T = T;
+  r.max_blocks = max_blocks;
+  r.negate_q = s < 0.0f;
+  r.out = out;
+  r.status = c.status;
+
+  cudaError_t e = launch_dependent(pva_tree_front_kernel, dim3(B), dim3(kFrontThreads), 0, stream, p);
+  if (e != cudaSuccess) return cuda_fail(e, "tree front-end launch");
+  e = launch_rope(r, dtype, true, c.num_sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "tree append launch");
+  e = tc ? launch_tree_tc(p, dtype, tq, tk, tv, stream) : launch_tree_f32(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+  e = launch_join(p, dtype, c.num_sms, stream);
+  return e == cudaSuccess ? PVA_OK : cuda_fail(e, "tree join launch");
+}
+
+}  // namespace
+
+extern "C" int pva_gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                            void* v_cache, const int32_t* past_lens, const int32_t* tree_lens,
+                            const int32_t* parents, const int32_t* block_table,
+                            const void* cos_cache, const void* sin_cache,
+                            const int64_t* position_ids, void* out, int B, int tokens,
+                            int n_blocks, int page_size, int max_blocks, int num_heads,
+                            int kv_num_heads, int head_size, int rotary_dim, int cache_rows,
+                            int rotary_interleaved, int n_axes, const int32_t* sections,
+                            int axes_interleaved, int rotary_dtype, float scale, float softcap,
+                            int local_window, int dtype, void* stream) {
+  return guarded([&]() -> int {
+    return gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, tree_lens, parents, block_table,
+                    cos_cache, sin_cache, position_ids, out, B, tokens, n_blocks, page_size,
+                    max_blocks, num_heads, kv_num_heads, head_size, rotary_dim, cache_rows,
+                    rotary_interleaved, n_axes, sections, axes_interleaved, rotary_dtype, scale,
+                    softcap, local_window, dtype, static_cast<cudaStream_t>(stream));
+  });
+}

@@ -1,0 +1,626 @@
+// Tree attention over a KV cache on the 5th-generation tensor cores (tcgen05,
+// operands staged by TMA, accumulators in TMEM), f16/bf16.
+//
+// The work is memory bound for any draft: a key tile of BN keys is read once
+// for up to 128 query rows (nodes x heads of the group), 4 * 128 * BN * d
+// operations per 4 * BN * d bytes.  So the kernel is built to keep the cache
+// read going: each CTA takes one piece of the line of key tiles (pva_tree.h),
+// every piece equally long, and streams its keys and values through a ring as
+// deep as shared memory allows; the tile arithmetic of one 128-row tile stays
+// below the time its bytes take.
+//
+// Per CTA (192 threads):
+//   warp 0      TMA producer: walks the piece's segments, publishes each one
+//               through a ring in shared memory, and loads the Q tile, then
+//               K_j and V_j, into one ring of slots.  Pages shorter than a key
+//               tile are copied one page per lane, from the block table.
+//   warp 1      MMA issuer and TMEM owner.  S = Q K^T (Q in TMEM) is
+//               double-buffered, so S(j+1) runs while tile j is exponentiated;
+//               P(j) replaces S(j) and feeds O += P V with A from TMEM.
+//   warps 2..5  softmax and epilogue, one thread per query row.
+// TMEM: S buffers [0, BN) and [BN, 2 BN), O [2 BN, 2 BN + D), Q after it.
+//
+// Masks: a row sees the cache rows [lo, past) and its ancestors among the new
+// rows.  Tiles wholly inside that range of every row of a warp need no mask;
+// the others build a bit per key from the range and the row's ancestor mask.
+// V rows outside the item's keys are zeroed in shared memory before the
+// product (cache rows there may hold anything, and 0 * NaN is NaN); their
+// scores are masked whatever they are.
+#include "pva_device.cuh"
+#include "pva_tree.h"
+
+namespace pva {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the max grows > 2^8
+constexpr int kItemSlots = 4;
+constexpr int kSoftmaxWarps = 4;
+
+template <int D>
+struct TreeCfg {
+  static constexpr int BN = tree_keys(D);
+  static constexpr int CH = (D + 63) / 64;        // 128-byte column chunks of a row
+  static constexpr int Q_CHUNK = kTcRows * 128;   // bytes of one chunk of the Q tile
+  static constexpr int KV_CHUNK = BN * 128;       // bytes of one chunk of a K or V tile
+  static constexpr int KV_TILE = CH * KV_CHUNK;   // one ring slot
+  static constexpr int Q_PER_SLOT = KV_TILE / Q_CHUNK;
+  static_assert(Q_PER_SLOT >= 1, "a Q chunk fits a ring slot");
+  static constexpr int Q_SLOTS = (CH + Q_PER_SLOT - 1) / Q_PER_SLOT;
+  static constexpr int SLOTS_FIT = (232448 - 64 - 2048) / KV_TILE;
+  static constexpr int SLOTS = SLOTS_FIT < 16 ? SLOTS_FIT : 16;
+  static_assert(SLOTS >= Q_SLOTS + 2, "ring depth");
+  static constexpr int OFF_BAR = SLOTS * KV_TILE;
+  static constexpr int SMEM = OFF_BAR + 1024 + 1024;  // barriers and segments + alignment slack
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int COL_S = 0;
+  static constexpr int COL_O = 2 * BN;
+  static constexpr int COL_Q = COL_O + D;
+  static_assert(COL_Q + D / 2 <= TMEM_COLS, "TMEM budget");
+  static_assert(SMEM <= 232448 - 64, "shared memory budget");
+};
+
+struct ItemSlot {
+  TreeSegment s;
+  int last;
+};
+
+struct Bars {
+  uint64_t q_tmem, o_ready, o_done, o_free, drain;
+  uint64_t s_full[2], p_full[2];
+  uint64_t ring_full[16], ring_empty[16];
+  uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+  ItemSlot items[kItemSlots];
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+template <int BN>
+struct Mask {
+  uint32_t w[BN / 32];
+};
+
+template <int BN, bool MASKED>
+__device__ __forceinline__ bool seen(const Mask<BN>& m, int c) {
+  return !MASKED || ((m.w[c >> 5] >> (c & 31)) & 1u);
+}
+
+// Bits [lo, hi) of 32.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  if (hi <= lo) return 0u;
+  return (0xffffffffu >> (32 - (hi - lo))) << lo;
+}
+
+// Extreme raw scores of a tile (max, and with a softcap nothing else: both
+// transforms are increasing, a negative scale having moved into Q).
+template <int BN, bool MASKED>
+__device__ __forceinline__ float row_max(const uint32_t (&v)[BN / 32][32], const Mask<BN>& m) {
+  const float ninf = __int_as_float(0xff800000);
+  float a[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+  for (int e = 0; e < BN; e += 2) {
+    const float x0 = __uint_as_float(v[e >> 5][e & 31]);
+    const float x1 = __uint_as_float(v[e >> 5][(e + 1) & 31]);
+    float& t = a[(e >> 1) & 3];
+    t = fmax3f(t, seen<BN, MASKED>(m, e) ? x0 : ninf, seen<BN, MASKED>(m, e + 1) ? x1 : ninf);
+  }
+  return fmaxf(fmax3f(a[0], a[1], a[2]), a[3]);
+}
+
+// 2^(x - m) over 64 columns from c0 on, their sum, and P as 16-bit pairs.  P is
+// rounded to the storage type for the tensor-core product (relative error half
+// a step of an element, the error that V has already); the row sum adds the
+// fp32 values.
+template <typename T, int BN, bool CAP, bool MASKED>
+__device__ __forceinline__ float exp_half(const uint32_t (&v)[BN / 32][32], int c0,
+                                          const Mask<BN>& m, float s_mul, float cap_mul,
+                                          float m_eff, uint32_t (&pw)[32]) {
+  const float ninf = __int_as_float(0xff800000);
+  const float2 mul2 = make_float2(s_mul, s_mul), neg_m = make_float2(-m_eff, -m_eff);
+  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+  for (int g = 0; g < 32; g += 8) {
+    float2 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int e = c0 + 2 * (g + k);
+      const float2 s = make_float2(__uint_as_float(v[e >> 5][e & 31]),
+                                   __uint_as_float(v[e >> 5][(e + 1) & 31]));
+      if (CAP) {
+        x[k].x = fmaf(cap_mul, tanh_via_exp2(s.x * s_mul), -m_eff);
+        x[k].y = fmaf(cap_mul, tanh_via_exp2(s.y * s_mul), -m_eff);
+      } else {
+        x[k] = ffma2(s, mul2, neg_m);
+      }
+      x[k].x = seen<BN, MASKED>(m, e) ? x[k].x : ninf;
+      x[k].y = seen<BN, MASKED>(m, e + 1) ? x[k].y : ninf;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2_approx(x[k].x), ex2_approx(x[k].y));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      acc[k & 1] = fadd2(acc[k & 1], x[k]);
+      pw[g + k] = pack2<T>(x[k].x, x[k].y);
+    }
+  }
+  const float2 r = fadd2(acc[0], acc[1]);
+  return r.x + r.y;
+}
+
+template <typename T, int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    pva_tree_tc_kernel(TreeParams p, const __grid_constant__ CUtensorMap tmap_q,
+                       const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v) {
+  using C = TreeCfg<D>;
+  constexpr int BN = C::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  __shared__ uint32_t s_tmem_base;
+  __shared__ int s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* status = p.status;
+  volatile int* abort = &s_abort;
+
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    mbar_init(&bars->q_tmem, 32 * kSoftmaxWarps);
+    mbar_init(&bars->o_ready, 1);
+    mbar_init(&bars->o_done, 1);
+    mbar_init(&bars->o_free, 32 * kSoftmaxWarps);
+    mbar_init(&bars->drain, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->p_full[b], 32 * kSoftmaxWarps);
+    }
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(&bars->ring_full[s], 1);
+      mbar_init(&bars->ring_empty[s], 1);
+    }
+    for (int s = 0; s < kItemSlots; ++s) {
+      mbar_init(&bars->item_full[s], 1);
+      mbar_init(&bars->item_empty[s], 1 + kSoftmaxWarps);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc<C::TMEM_COLS>(&s_tmem_base);
+  if (warp == 0 && lane == 0) {
+    prefetch_tensor_map(&tmap_q);
+    prefetch_tensor_map(&tmap_k);
+    prefetch_tensor_map(&tmap_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem_base;
+  allow_next_grid();
+  wait_prior_grid();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int tiles = p.hdr[1], chunk = p.hdr[2];
+    const long long from = (long long)blockIdx.x * chunk;
+    const int end = (int)(from + chunk < tiles ? from + chunk : tiles);
+    // rows of one copy, copies side by side in a tile
+    const int box = p.table && p.page < BN ? p.page : BN;
+    const int copies = BN / box;
+    uint32_t loads = 0, published = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, abort, status));
+    };
+    auto publish = [&](const ItemSlot& v) -> bool {
+      const int sl = published % kItemSlots;
+      if (!wait(&bars->item_empty[sl], ((published / kItemSlots) & 1) ^ 1)) return false;
+      if (lane == 0) {
+        bars->items[sl] = v;
+        mbar_arrive(&bars->item_full[sl]);
+      }
+      __syncwarp();
+      ++published;
+      return true;
+    };
+    for (long long x = from; ok && x < end;) {
+      ItemSlot v;
+      v.s = tree_segment(p, blockIdx.x, (int)x, end);
+      v.last = 0;
+      x += v.s.count;
+      if (!(ok = publish(v))) break;
+      const TreeSegment& s = v.s;
+      const int plane_q = s.b * p.Hkv + s.h;
+      for (int qs = 0; ok && qs < C::Q_SLOTS; ++qs, ++loads) {
+        const int sl = loads % C::SLOTS;
+        if (!(ok = wait(&bars->ring_empty[sl], ((loads / C::SLOTS) & 1) ^ 1))) break;
+        if (lane == 0) {
+          const int c_lo = qs * C::Q_PER_SLOT, c_hi = min(C::CH, c_lo + C::Q_PER_SLOT);
+          mbar_arrive_expect_tx(&bars->ring_full[sl], (uint32_t)(c_hi - c_lo) * C::Q_CHUNK);
+          for (int c = c_lo; c < c_hi; ++c)
+            tma_load_3d(smem + sl * C::KV_TILE + (c - c_lo) * C::Q_CHUNK, &tmap_q,
+                        &bars->ring_full[sl], c * 64, s.t * kTcRows, plane_q);
+        }
+        __syncwarp();
+      }
+      const int total = s.past + s.n;
+      for (int j = s.j0; ok && j < s.j0 + s.count; ++j) {
+        // this lane's copy of the tile: rows [r0, r0 + box) of the sequence
+        const int r0 = j * BN + lane * box;
+        const bool mine = lane < copies && r0 < total && r0 + box > s.lo;
+        int plane = 0, y = 0;
+        if (mine) {
+          const int in = r0 / p.page;
+          const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+          plane = block * p.Hkv + s.h;
+          y = r0 - in * p.page;
+        }
+        const uint32_t n_copies = __popc(__ballot_sync(0xffffffffu, mine));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++loads) {
+          const int sl = loads % C::SLOTS;
+          if (!(ok = wait(&bars->ring_empty[sl], ((loads / C::SLOTS) & 1) ^ 1))) break;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&bars->ring_full[sl], n_copies * C::CH * (uint32_t)box * 128u);
+          __syncwarp();
+          if (mine) {
+            uint8_t* dst = smem + sl * C::KV_TILE + lane * box * 128;
+#pragma unroll
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_3d(dst + c * C::KV_CHUNK, kv ? &tmap_v : &tmap_k, &bars->ring_full[sl],
+                          c * 64, y, plane);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (ok) {
+      ItemSlot v{};
+      v.last = 1;
+      publish(v);
+    }
+    // Drain: every copy this warp issued must land before the CTA exits.
+    for (int s = 0; s < C::SLOTS; ++s) {
+      const uint32_t fills = loads > (uint32_t)s ? (loads - 1 - s) / C::SLOTS + 1 : 0;
+      if (fills) mbar_wait<false>(&bars->ring_full[s], (fills - 1) & 1, abort, status);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_sync();
+    constexpr uint32_t idesc_s = idesc_f16<T>(kTcRows, BN, false, false);
+    constexpr uint32_t idesc_o = idesc_f16<T>(kTcRows, D, false, true);
+    const uint64_t kdesc = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t vdesc = sdesc_sw128(smem_u32(smem), C::KV_CHUNK, 1024);
+    uint32_t q_cnt = 0, loads = 0, gt = 0, items = 0, taken = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, abort, status));
+    };
+    auto wait_slot = [&](uint32_t L) -> bool {
+      const bool r = wait(&bars->ring_full[L % C::SLOTS], (L / C::SLOTS) & 1);
+      tc_fence_after();
+      return r;
+    };
+    auto issue_s = [&](uint32_t T_, uint32_t L) {
+      const uint64_t ka = sdesc_advance(kdesc, (L % C::SLOTS) * C::KV_TILE);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ts(tmem + C::COL_S + (T_ & 1) * BN, tmem + C::COL_Q + kk * 8,
+                 sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s,
+                 kk > 0 ? 1u : 0u);
+        mma_commit(&bars->s_full[T_ & 1]);
+        mma_commit(&bars->ring_empty[L % C::SLOTS]);
+      }
+    };
+    while (ok) {
+      const int isl = taken % kItemSlots;
+      if (!(ok = wait(&bars->item_full[isl], (taken / kItemSlots) & 1))) break;
+      const int n = bars->items[isl].s.count, last = bars->items[isl].last;
+      __syncwarp();
+      if (leader) mbar_arrive(&bars->item_empty[isl]);
+      ++taken;
+      if (last) break;
+      // Q is in TMEM once every softmax thread has copied its share.
+      if (!(ok = wait(&bars->q_tmem, q_cnt & 1))) break;
+      tc_fence_after();
+      if (leader)
+        for (int qs = 0; qs < C::Q_SLOTS; ++qs)
+          mbar_arrive(&bars->ring_empty[(loads + qs) % C::SLOTS]);
+      loads += C::Q_SLOTS;
+      for (int j = 0; ok && j < 2 && j < n; ++j) {
+        if (!(ok = wait_slot(loads + 2 * j))) break;
+        issue_s(gt + j, loads + 2 * j);
+      }
+      if (!ok) break;
+      for (int j = 0; ok && j < n; ++j) {
+        const uint32_t T_ = gt + j, Lv = loads + 2 * j + 1;
+        if (!(ok = wait_slot(Lv))) break;
+        if (j == 0 && !(ok = wait(&bars->o_free, (items & 1) ^ 1))) break;
+        if (!(ok = wait(&bars->p_full[T_ & 1], (T_ >> 1) & 1))) break;
+        tc_fence_after();
+        const uint64_t va = sdesc_advance(vdesc, (Lv % C::SLOTS) * C::KV_TILE);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + C::COL_O, tmem + C::COL_S + (T_ & 1) * BN + kk * 8,
+                   sdesc_advance(va, kk * 16 * 128), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bars->o_ready);
+          if (j + 1 == n) mma_commit(&bars->o_done);
+          mma_commit(&bars->ring_empty[Lv % C::SLOTS]);
+        }
+        if (j + 2 < n) {
+          if (!(ok = wait_slot(loads + 2 * (j + 2)))) break;
+          issue_s(T_ + 2, loads + 2 * (j + 2));
+        }
+      }
+      loads += 2 * n;
+      gt += n;
+      ++q_cnt;
+      ++items;
+    }
+    // Drain: all issued MMAs complete before TMEM is released.
+    if (leader) mma_commit(&bars->drain);
+    wait(&bars->drain, 0);
+  } else {
+    // ------------------------------------------------- softmax + epilogue
+    const int quarter = warp & 3;  // TMEM lanes this warp may access
+    const int r = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float NEG_INF = __int_as_float(0xff800000);
+    const float s_mul = CAP ? p.scale / p.softcap : p.scale * kLog2e;
+    const float cap_mul = p.softcap * kLog2e;
+    uint32_t gt = 0, taken = 0, done = 0;
+    uint32_t lq = 0;  // ring loads accounted for (the producer's order)
+    bool ok = true, q_pre = false;
+    T* out = static_cast<T*>(p.out);
+    // Copies the next Q tile from its ring slots into TMEM.
+    auto copy_q = [&]() -> bool {
+      bool got = true;
+      for (int qs = 0; qs < C::Q_SLOTS; ++qs) {
+        const uint32_t L = lq + qs;
+        got = got && mbar_wait<false>(&bars->ring_full[L % C::SLOTS], (L / C::SLOTS) & 1, abort,
+                                      status);
+      }
+      if (!__all_sync(0xffffffffu, got)) return false;
+#pragma unroll 1
+      for (int c = 0; c < C::CH; ++c) {
+        const uint32_t L = lq + c / C::Q_PER_SLOT;
+        const uint8_t* src =
+            smem + (L % C::SLOTS) * C::KV_TILE + (c % C::Q_PER_SLOT) * C::Q_CHUNK + r * 128;
+        uint32_t w[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {  // 16-byte unit u of the row, 128-byte swizzle
+          const uint4 x = *reinterpret_cast<const uint4*>(src + ((u ^ (r & 7)) << 4));
+          w[4 * u] = x.x;
+          w[4 * u + 1] = x.y;
+          w[4 * u + 2] = x.z;
+          w[4 * u + 3] = x.w;
+        }
+        if (D % 64 == 0 || c + 1 < C::CH) {
+          tmem_st32(t_lane + C::COL_Q + c * 32, w);
+        } else {  // a 32-column tail chunk
+          uint32_t w16[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w16[e] = w[e];
+          tmem_st16(t_lane + C::COL_Q + c * 32, w16);
+        }
+      }
+      tmem_wait_st();
+      fence_proxy_async_smem();  // the slots are refilled by the TMA unit next
+      tc_fence_before();
+      mbar_arrive(&bars->q_tmem);
+      lq += C::Q_SLOTS;
+      return true;
+    };
+
+    while (ok) {
+      const int isl = taken % kItemSlots;
+      ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->item_full[isl],
+                                                    (taken / kItemSlots) & 1, abort, status));
+      if (!ok) break;
+      const ItemSlot it = bars->items[isl];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->item_empty[isl]);
+      ++taken;
+      if (it.last) break;
+      const TreeSegment& s = it.s;
+      const int n = s.count;
+      const int row = s.t * kTcRows + r;
+      const bool own = row < s.n * p.G;
+      const int node = own ? row / p.G : 0;
+      if (!q_pre && !(ok = copy_q())) break;
+      q_pre = false;
+      const uint32_t l0 = lq;  // the segment's first K load
+      lq += 2 * n;
+      const int total = s.past + s.n;
+      const int depth = p.parents ? p.depth[(size_t)s.b * p.T + node] : node;
+      const int row_lo = p.window > 0 ? max(0, s.past + depth + 1 - p.window) : 0;
+      const int row_hi = p.parents ? s.past : s.past + node + 1;
+      const uint32_t* anc = p.parents ? p.mask + ((size_t)s.b * p.T + node) * p.W32 : nullptr;
+      const bool any_own = __any_sync(0xffffffffu, own);
+      float m_used = NEG_INF, l = 0.0f;
+
+      for (int j = 0; j < n; ++j) {
+        const uint32_t T_ = gt + j;
+        const int k0 = (s.j0 + j) * BN;
+        if (k0 < s.lo || k0 + BN > total) {
+          // V rows outside the item's keys: zeros
+          const uint32_t L = l0 + 2 * j + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->ring_full[L % C::SLOTS],
+                                                        (L / C::SLOTS) & 1, abort, status));
+          if (!ok) break;
+          if (r < BN && (k0 + r < s.lo || k0 + r >= total)) {
+            uint8_t* v = smem + (L % C::SLOTS) * C::KV_TILE + r * 128;
+#pragma unroll
+            for (int c = 0; c < C::CH; ++c)
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4*>(v + c * C::KV_CHUNK + u * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait<false>(&bars->s_full[T_ & 1], (T_ >> 1) & 1, abort, status));
+        if (!ok) break;
+        if (any_own) {
+          tc_fence_after();
+          const uint32_t col_s = C::COL_S + (T_ & 1) * BN;
+          uint32_t v[BN / 32][32];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) tmem_ld32(t_lane + col_s + c * 32, v[c]);
+          tmem_wait_ld();
+          const int lo_c = row_lo - k0, hi_c = row_hi - k0;  // visible columns [lo_c, hi_c)
+          const bool masked = !__all_sync(0xffffffffu, lo_c <= 0 && hi_c >= BN);
+          Mask<BN> mk;
+          if (masked) {
+#pragma unroll
+            for (int w = 0; w < BN / 32; ++w) {
+              mk.w[w] = bit_range(lo_c - 32 * w, hi_c - 32 * w);
+              // node that column 32 w stands for; its bits continue in the next word
+              const int first = k0 + 32 * w - s.past;
+              if (p.parents && first > -32 && first < 32 * p.W32) {
+                const int word = first >> 5;
+                const uint32_t a = word >= 0 ? anc[word] : 0u;
+                const uint32_t b = word + 1 < p.W32 ? anc[word + 1] : 0u;
+                mk.w[w] |= __funnelshift_r(a, b, first & 31);
+              }
+            }
+          }
+          const float mx = masked ? row_max<BN, true>(v, mk) : row_max<BN, false>(v, mk);
+          float mt = NEG_INF;
+          if (mx != NEG_INF) mt = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
+          const float m_new = fmaxf(m_used, mt);
+          float alpha = 1.0f;
+          if (m_new > m_used + kRescaleThreshold) {
+            alpha = ex2_approx(m_used - m_new);  // 0 when m_used is -inf
+            m_used = m_new;
+          }
+          const float m_eff = m_used == NEG_INF ? 0.0f : m_used;
+          float rs = 0.0f;
+#pragma unroll
+          for (int half = 0; half < BN / 64; ++half) {
+            uint32_t pw[32];
+            rs += masked ? exp_half<T, BN, CAP, true>(v, half * 64, mk, s_mul, cap_mul, m_eff, pw)
+                         : exp_half<T, BN, CAP, false>(v, half * 64, mk, s_mul, cap_mul, m_eff, pw);
+            // P (16-bit pairs) over the columns of S read above
+            tmem_st32(t_lane + col_s + half * 32, pw);
+          }
+          l = l * alpha + rs;
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            // O must hold PV(j-1) before it is rescaled; PV(j-2) precedes S(j),
+            // so the parity of the outstanding phase is unambiguous.
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait<false>(&bars->o_ready, (T_ - 1) & 1, abort, status));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_lane + C::COL_O + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(t_lane + C::COL_O + c, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[T_ & 1]);
+      }
+      if (!ok) break;
+
+      // The next segment's Q goes to TMEM before this one's epilogue, so that
+      // its first S MMAs run meanwhile.
+      {
+        const int nsl = taken % kItemSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->item_full[nsl],
+                                                      (taken / kItemSlots) & 1, abort, status));
+        if (!ok) break;
+        if (!bars->items[nsl].last) {
+          if (!(ok = copy_q())) break;
+          q_pre = true;
+        }
+      }
+
+      ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->o_done, done & 1, abort, status));
+      ++done;
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = s.slot < 0;
+      const float inv = !whole ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
+      const int g = row - node * p.G;
+      T* o_row = out + (((size_t)s.b * p.T + node) * p.H + (size_t)s.h * p.G + g) * D;
+      const size_t at = (size_t)(whole ? 0 : s.slot) * kTcRows + r;
+      float* part = p.part_o + at * D;
+      if (own && !whole) p.part_ml[at] = make_float2(m_used, l);
+      if (any_own) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(t_lane + C::COL_O + c, v);
+          tmem_wait_ld();
+          if (own && whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 w;
+              w.x = pack2<T>(__uint_as_float(v[e + 0]) * inv, __uint_as_float(v[e + 1]) * inv);
+              w.y = pack2<T>(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+              w.z = pack2<T>(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
+              w.w = pack2<T>(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
+              *reinterpret_cast<uint4*>(o_row + c + e) = w;
+            }
+          } else if (own) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars->o_free);
+      gt += n;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<C::TMEM_COLS>(tmem);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, cudaStream_t s) {
+  constexpr int smem = TreeCfg<D>::SMEM;
+  auto kern = p.softcap != 0.0f ? pva_tree_tc_kernel<T, D, true> : pva_tree_tc_kernel<T, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(p.pieces), dim3(kThreads), smem, s, p, tq, tk, tv);
+}
+
+template <typename T>
+cudaError_t launch_type(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, cudaStream_t s) {
+  switch (p.d) {
+    case 64: return launch_d<T, 64>(p, tq, tk, tv, s);
+    case 96: return launch_d<T, 96>(p, tq, tk, tv, s);
+    case 128: return launch_d<T, 128>(p, tq, tk, tv, s);
+    case 192: return launch_d<T, 192>(p, tq, tk, tv, s);
+    case 256: return launch_d<T, 256>(p, tq, tk, tv, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const TreeParams& p, int dtype, const CUtensorMap& tq,
+                           const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  return dtype == PVA_BF16 ? launch_type<__nv_bfloat16>(p, tq, tk, tv, s)
+                           : launch_type<__half>(p, tq, tk, tv, s);
+}
+
+}  // namespace pva

@@ -60,6 +60,9 @@ typedef enum { PVA_F32 = 0, PVA_F16 = 1, PVA_BF16 = 2 } pva_dtype;
 #define PVA_DEV_KV_CACHE 0x80u    /* pva_gqa_kvcache: a step outside the cache's bounds, or one
                                      after such a step (see there) */
 #define PVA_DEV_WAIT_TIMEOUT 0x100u /* a pipeline wait in a kernel gave up (never expected) */
+#define PVA_DEV_TREE 0x200u   /* pva_gqa_tree, pva_kvcache_accept: a bad tree, node count or path */
+#define PVA_DEV_BLOCKS 0x400u /* a block table entry outside the pool; pva_block_tables: see there */
+#define PVA_DEV_ROPE 0x800u   /* a rotary position outside the tables, or a slot outside the cache */
 
 /*
  * pva_forward -- out = attention(q, k, v) over packed sequences.
@@ -284,6 +287,186 @@ int pva_forward_noalloc(const void* q, const void* k, const void* v,
                         void* out, int B, int num_heads, int kv_num_heads,
                         int head_size, int v_head_size, float scale, int is_causal,
                         float softcap, int dtype, uint32_t* device_status, void* stream);
+
+/*
+ * Paged caches.  The entry points below take a KV cache as a pool of blocks
+ *   k_cache, v_cache : [n_blocks, kv_num_heads, page_size, head_size]
+ * and a block table int32 [B, max_blocks]: row j of sequence b lies in block
+ * block_table[b][j / page_size] at row j % page_size of each head.  A NULL
+ * block table means that sequence b owns block b alone: the pool is then the
+ * fixed-capacity BNSH cache of pva_gqa_kvcache, with page_size its capacity.
+ * Blocks may be shared between sequences as long as no step writes to them.
+ *
+ * These entry points keep their scratch in the same per-(device, stream)
+ * workspace as pva_forward, with the same rules for growth and capture; a
+ * buffer that a captured call used is kept until pva_release, so a graph stays
+ * valid when later calls need a larger one.  Graphs captured on one stream
+ * share that stream's workspace: replay them one after another, and not beside
+ * other calls on that stream.
+ */
+
+/*
+ * pva_block_tables -- gives every sequence the blocks that its length needs,
+ * from a stack of free blocks, and names the cache slot of every new token.
+ *
+ * lens        : device int32 [B]: rows that sequence b has to have room for
+ *               from now on; need_b = ceil(lens[b] / page_size) blocks.
+ * block_table : device int32 [B, max_blocks], entries 0 .. held[b]-1 in use.
+ * held        : device int32 [B]: blocks that sequence b has; need_b afterwards.
+ * free_blocks : device int32 [pool]: the free blocks are entries 0 ..
+ *               *free_count - 1, the last one on top of the stack.
+ * free_count  : device int32 [1].
+ * cu_new      : device int32 [B + 1] offsets of the new tokens of the packed
+ *               batch, or NULL (no slot map).  Sequence b's tokens
+ *               cu_new[b] .. cu_new[b+1]-1 are its last rows, up to lens[b]-1.
+ * slot_map    : device int64 [n_slots]: token t's slot, block * page_size +
+ *               row in the block; -1 for t >= cu_new[B] (a padded batch).
+ * A sequence with held[b] > need_b gives back its blocks from need_b on (their
+ * table entries become -1), then one with held[b] < need_b takes what it lacks:
+ * in the order of b, and within b of the table, the e-th given back goes to
+ * stack entry c + S - 1 - e and the e-th taken comes from it (c: the count
+ * before, S: all that was given back).  So a call that grows the sequences and
+ * one that takes the growth back leave the stack as it was, and blocks that one
+ * sequence frees serve another in the same call.
+ * All or nothing: PVA_DEV_BLOCKS is latched, and nothing is written, when a
+ * length, a held count or the free count is negative or a count is larger than
+ * its array (need_b or held[b] > max_blocks, stack > pool), when the free
+ * blocks do not suffice, or when cu_new does not start at 0, decreases, ends
+ * past n_slots or names more tokens of a sequence than lens[b].
+ * Host errors: null pointers (cu_new and slot_map come together), B < 1,
+ * max_blocks < 1, page_size < 1, pool < 1, n_slots < 0.
+ */
+int pva_block_tables(const int32_t* lens, int32_t* block_table, int32_t* held,
+                     int32_t* free_blocks, int32_t* free_count, const int32_t* cu_new,
+                     int64_t* slot_map, int B, int max_blocks, int page_size, int pool,
+                     int64_t n_slots, void* stream);
+
+/*
+ * pva_rope_axes -- rotary embedding of packed query and key rows with positions
+ * on 1 to 4 axes (text; time, height and width of an image or a film), and
+ * optionally the write of the keys and values to a cache.
+ *
+ * q, q_out : [tokens, num_heads, head_size], or both NULL; k, k_out likewise
+ *            with kv_num_heads (k_out may be NULL when the cache is written).
+ *            A token's heads are contiguous; tokens lie q_stride, k_stride,
+ *            q_out_stride, k_out_stride elements apart (slices of one
+ *            projection's output are fine).  An output may be its own input
+ *            (same address and stride), and must not overlap anything else.
+ * cos_cache, sin_cache, rotary_dim, cache_rows, rotary_interleaved,
+ * rotary_dtype : as in pva_gqa_kvcache (rotary_dim >= 2), with the same
+ *            arithmetic: f32, each product and sum rounded on its own, then one
+ *            rounding to dtype.
+ * position_ids : device int64 [n_axes, tokens].
+ * sections : HOST int32 [n_axes], read by the call (NULL with one axis): how
+ *            many of the rotary_dim / 2 pairs turn with each axis.  With
+ *            axes_interleaved = 0 axis 0 has the first sections[0] pairs, axis
+ *            1 the next, and so on; with axes_interleaved = 1 pair k has axis
+ *            a = k mod n_axes where k < n_axes * sections[a], else axis 0.
+ * inverse  : nonzero turns by the negative angle.  That is the gradient of the
+ *            rotation: with dq_out, dk_out as q, k it gives dq, dk.
+ * v, k_cache, v_cache, slot_map : all NULL, or the cache write: rotated k and v
+ *            ([tokens, kv_num_heads, head_size], stride v_stride) of token t go
+ *            to slot slot_map[t] (device int64 [tokens]) of the pool of
+ *            n_blocks blocks of page_size rows; slot -1 is not written.
+ *            Slots must differ.  Not with inverse.
+ * A token with a position outside [0, cache_rows) or a slot outside [-1,
+ * n_blocks * page_size) is left out of all outputs and PVA_DEV_ROPE is latched.
+ * head_size: even, 2 to 256.  tokens = 0 does nothing.
+ */
+int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const void* cos_cache,
+                  const void* sin_cache, const int64_t* position_ids, int tokens, int num_heads,
+                  int kv_num_heads, int head_size, int64_t q_stride, int64_t k_stride,
+                  int64_t q_out_stride, int64_t k_out_stride, int rotary_dim, int cache_rows,
+                  int rotary_interleaved, int n_axes, const int32_t* sections,
+                  int axes_interleaved, int inverse, int rotary_dtype, const void* v,
+                  int64_t v_stride, void* k_cache, void* v_cache, const int64_t* slot_map,
+                  int n_blocks, int page_size, int dtype, void* stream);
+
+/*
+ * pva_gqa_tree -- one GroupQueryAttention step of a tree of drafted tokens over
+ * a paged or fixed-capacity KV cache: append, rotary embedding and attention,
+ * as pva_gqa_kvcache does for a chain of tokens.
+ *
+ * q     : [B, tokens, num_heads, head_size]
+ * k_new, v_new : [B, tokens, kv_num_heads, head_size]
+ * k_cache, v_cache, block_table : see "Paged caches" above; max_blocks is the
+ *         table's width (ignored without a table, where n_blocks = B).
+ * past_lens : device int32 [B]: rows in the cache before the step.  Node i of
+ *         sequence b goes to cache row past_lens[b] + i.
+ * tree_lens : device int32 [B], or NULL: sequence b uses its first
+ *         tree_lens[b] of the `tokens` nodes (NULL: all).  Unused nodes are not
+ *         appended and their rows of out are zeros.
+ * parents : device int32 [B, tokens], or NULL: the parent of each node, -1 for
+ *         one that follows the cache directly; a parent comes before its
+ *         children.  Node i sees the cache rows before the step, its ancestors
+ *         and itself.  NULL is a chain (node i follows node i - 1): a plain
+ *         decode step or prompt chunk on the cache.
+ * local_window : W > 0: a node of depth e (-1 parent: depth 0) sees the rows
+ *         j >= past + e + 1 - W and its ancestors less than W levels up.  Table
+ *         entries of blocks wholly before past + 1 - W are not looked at.
+ * cos_cache .. rotary_dtype, sections, n_axes : as pva_rope_axes; rotary_dim 0:
+ *         no rotation.  position_ids: device int64 [n_axes, B, tokens], or NULL:
+ *         past_lens[b] + depth on every axis.
+ * out   : [B, tokens, num_heads, head_size] (every row written).
+ * scale, softcap, dtype, stream : as pva_forward.
+ *
+ * Arithmetic: products of dtype (f16/bf16 on tensor cores), scores, softmax and
+ * sums in f32.  The rotated queries are rounded to dtype, as the keys in the
+ * cache are, and so are the softmax weights that multiply V (f16/bf16).
+ * Results do not depend on timing: parts of a split row are added in order.
+ *
+ * Limits: f16/bf16: head_size in {64, 96, 128, 192, 256}, 16-byte aligned
+ * tensors; f32: even head_size up to 256.  Trees up to 1024 nodes (chains: any).
+ * page_size with a block table: a power of two, at least 16.
+ * Host errors: null pointers, B < 1, tokens < 1, counts out of int32, and the
+ * rules above.
+ * Device errors: the step is all or nothing, as in pva_gqa_kvcache.  It is
+ * rejected if past_lens[b] < 0 or past_lens[b] + nodes exceeds the table's (or
+ * the block's) rows (PVA_DEV_KV_CACHE), if tree_lens or a parent is out of
+ * range (PVA_DEV_TREE), a needed table entry is outside [0, n_blocks)
+ * (PVA_DEV_BLOCKS), a position is outside the tables (PVA_DEV_ROPE), the work
+ * does not fit 32-bit indices (PVA_DEV_TOO_MANY), or PVA_DEV_KV_CACHE is
+ * already latched on the stream.  A rejected step latches PVA_DEV_KV_CACHE
+ * beside the reason's bit and writes neither the cache nor out.
+ * Cache rows at or past past + nodes may hold anything, NaN included; so may
+ * rows before every node's window.  A value row that some node of the sequence
+ * sees should be finite: an infinity or NaN there can reach its other nodes.
+ */
+int pva_gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                 void* v_cache, const int32_t* past_lens, const int32_t* tree_lens,
+                 const int32_t* parents, const int32_t* block_table, const void* cos_cache,
+                 const void* sin_cache, const int64_t* position_ids, void* out, int B,
+                 int tokens, int n_blocks, int page_size, int max_blocks, int num_heads,
+                 int kv_num_heads, int head_size, int rotary_dim, int cache_rows,
+                 int rotary_interleaved, int n_axes, const int32_t* sections,
+                 int axes_interleaved, int rotary_dtype, float scale, float softcap,
+                 int local_window, int dtype, void* stream);
+
+/*
+ * pva_kvcache_accept -- after a drafted tree was verified, moves the rows of
+ * the accepted path to where the sequence goes on: for every layer, kv head and
+ * i < path_lens[b], cache row past_lens[b] + path[b][i] becomes row
+ * past_lens[b] + i, of k_cache and of v_cache, as if all were moved at once.
+ *
+ * k_cache, v_cache : `layers` pools of n_blocks blocks, layer_stride elements
+ *         apart (any value >= a pool's size; ignored for one layer).
+ * block_table, page_size, max_blocks : as pva_gqa_tree, one table for all layers.
+ * path    : device int32 [B, path_width]: the accepted nodes of the tree from
+ *         the root on, so rising; path_lens: device int32 [B].
+ * new_lens : device int32 [B]: past_lens[b] + path_lens[b].  Must not overlap
+ *         past_lens.
+ * dtype   : any of the codes; rows are moved bit by bit.
+ * A sequence is left as it is, with new_lens[b] = past_lens[b], when past_lens
+ * or path_lens is out of range or the path does not rise, starts below 0 or
+ * passes the cache's end (PVA_DEV_TREE is latched), when a table entry that it
+ * needs is outside [0, n_blocks) (PVA_DEV_BLOCKS), or when PVA_DEV_KV_CACHE is
+ * latched on the stream: the rejected step before has not written the rows.
+ */
+int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* past_lens,
+                       const int32_t* path, const int32_t* path_lens,
+                       const int32_t* block_table, int32_t* new_lens, int B, int path_width,
+                       int layers, int64_t layer_stride, int n_blocks, int kv_num_heads,
+                       int page_size, int head_size, int max_blocks, int dtype, void* stream);
 
 /*
  * pva_get_status -- synchronises `stream`, then reads and clears the device
