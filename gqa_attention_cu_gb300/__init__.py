@@ -13,6 +13,8 @@ import ctypes
 import os
 import threading
 
+import torch
+
 from . import workloads  # noqa: F401  (seeded synthetic inputs)
 
 __all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache",
@@ -242,35 +244,57 @@ def _need(ok: bool, message: str) -> None:
         raise PvaError(PVA_ERR_INVALID_ARG, message)
 
 
-def _same_device(first, *others) -> None:
-    """Every tensor on the device of ``first``, which has to be the current one."""
-    dev = first.device
+def _same_device(first, *others) -> int:
+    """Every tensor on the device of ``first``, which has to be the current one
+    if it is a GPU; returns its index."""
+    at = first.get_device()
+    if at < 0:  # the host (or no storage): compare in full
+        for t in others:
+            _need(t is None or t.device == first.device, "the tensors are on different devices")
+        return at
     for t in others:
-        _need(t is None or t.device == dev, "the tensors are on different devices")
-    if first.is_cuda:
-        import torch
-        _need(dev.index == torch.cuda.current_device(),
-              f"the tensors are on {dev}, which is not the current device")
+        if t is not None and t.get_device() != at:
+            raise PvaError(PVA_ERR_INVALID_ARG, "the tensors are on different devices")
+    if at != torch.cuda.current_device():
+        raise PvaError(PVA_ERR_INVALID_ARG,
+                       f"the tensors are on cuda:{at}, which is not the current device")
+    return at
+
+
+def _stream_on(stream, device: int) -> int:
+    """The given stream, or the device's current one (as a number: making a
+    stream object costs more than the rest of a small call's checks)."""
+    if stream is None and device >= 0:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream_ptr(stream)
 
 
 def _plain(t, name: str, dtype, shape) -> None:
-    """A contiguous tensor of this type and shape (None in the shape: any extent)."""
-    if t is None:
+    """A contiguous tensor of this type and shape."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         return
-    _need(t.dtype == dtype, f"{name} must be {dtype}")
-    _need(t.dim() == len(shape) and all(w is None or w == n for w, n in zip(shape, t.shape)),
-          f"{name} must have the shape {tuple('any' if w is None else w for w in shape)}, "
-          f"not {tuple(t.shape)}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    _need(t.dtype is dtype, f"{name} must be {dtype}")
+    _need(t.shape == shape, f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    _need(False, f"{name} must be contiguous")
 
 
 def _rotary(cos_cache, sin_cache, sections):
     """(rotary_dim, table rows, table type code, host sections or None)."""
     _need(sin_cache is not None, "cos_cache and sin_cache come together")
-    _plain(cos_cache, "cos_cache", cos_cache.dtype, (None, None))
-    _plain(sin_cache, "sin_cache", cos_cache.dtype, tuple(cos_cache.shape))
+    shape = cos_cache.shape
+    _need(len(shape) == 2, "cos_cache must be [rows, rotary_dim / 2]")
+    _plain(cos_cache, "cos_cache", cos_cache.dtype, shape)
+    _plain(sin_cache, "sin_cache", cos_cache.dtype, shape)
     host = None if sections is None else (ctypes.c_int32 * len(sections))(*sections)
-    return 2 * int(cos_cache.shape[1]), int(cos_cache.shape[0]), _dtype_code(cos_cache), host
+    return 2 * shape[1], shape[0], _type_code(cos_cache), host
+
+
+_TYPE_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _type_code(t) -> int:
+    code = _TYPE_CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 def pva_block_tables(lens, block_table, held, free_blocks, free_count, page_size: int, cu_new=None,
@@ -280,36 +304,39 @@ def pva_block_tables(lens, block_table, held, free_blocks, free_count, page_size
     (a stack of *free_count int32 [1]* blocks).  With ``cu_new`` int32 [B + 1]
     and ``slot_map`` int64 [n], also the cache slot of every new packed token.
     See include/pva.h for the order and the errors (``blocks`` bit)."""
-    import torch
     _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
     B, width = block_table.shape
     i32 = torch.int32
     _plain(lens, "lens", i32, (B,))
     _plain(held, "held", i32, (B,))
     _plain(block_table, "block_table", i32, (B, width))
-    _plain(free_blocks, "free_blocks", i32, (None,))
+    _need(free_blocks.dim() == 1, "free_blocks must be [pool]")
+    _plain(free_blocks, "free_blocks", i32, free_blocks.shape)
     _plain(free_count, "free_count", i32, (1,))
     _plain(cu_new, "cu_new", i32, (B + 1,))
-    _plain(slot_map, "slot_map", torch.int64, (None,))
+    if slot_map is not None:
+        _need(slot_map.dim() == 1, "slot_map must be [slots]")
+        _plain(slot_map, "slot_map", torch.int64, slot_map.shape)
     _need((cu_new is None) == (slot_map is None), "cu_new and slot_map come together")
-    _same_device(block_table, lens, held, free_blocks, free_count, cu_new, slot_map)
-    _check(load_library().pva_block_tables(
+    at = _same_device(block_table, lens, held, free_blocks, free_count, cu_new, slot_map)
+    _check((_lib or load_library()).pva_block_tables(
         lens.data_ptr(), block_table.data_ptr(), held.data_ptr(), free_blocks.data_ptr(),
         free_count.data_ptr(), _ptr_or_none(cu_new), _ptr_or_none(slot_map), B, width,
         int(page_size), free_blocks.shape[0], 0 if slot_map is None else slot_map.shape[0],
-        _stream_ptr(stream)))
+        _stream_on(stream, at)))
 
 
 def _token_rows(t, name: str, like):
     """Heads and token stride of a [tokens, heads, d] tensor whose tokens are
     each contiguous."""
-    _need(t.dim() == 3 and t.dtype == like.dtype and t.shape[0] == like.shape[0]
-          and t.shape[2] == like.shape[2],
-          f"{name} must be [tokens, heads, head_size] of one type with the others")
-    heads, d = t.shape[1], t.shape[2]
-    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == d),
-          f"{name}: the heads of a token must be contiguous")
-    return heads, max(t.stride(0), heads * d) if t.shape[0] <= 1 else t.stride(0)
+    shape, want = t.shape, like.shape
+    if len(shape) != 3 or t.dtype is not like.dtype or shape[0] != want[0] or shape[2] != want[2]:
+        _need(False, f"{name} must be [tokens, heads, head_size] of one type with the others")
+    tokens, heads, d = shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        _need(False, f"{name}: the heads of a token must be contiguous")
+    return heads, max(s0, heads * d) if tokens <= 1 else s0
 
 
 def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=None, sections=None,
@@ -322,7 +349,6 @@ def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=No
     turn with each axis.  ``inverse`` is the rotation's gradient.  With v, the
     caches [n_blocks, Hkv, page, d] and slot_map int64 [tokens], rotated keys
     and values are also written to the cache."""
-    import torch
     first = q if q is not None else k
     _need(first is not None, "q or k is needed")
     _need(first.dim() == 3, "q and k must be [tokens, heads, head_size]")
@@ -341,7 +367,7 @@ def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=No
             _, kos = _token_rows(k_out, "k_out", first)
     _need(position_ids.dim() == 2, "position_ids must be [n_axes, tokens]")
     n_axes = position_ids.shape[0]
-    _plain(position_ids, "position_ids", torch.int64, (None, tokens))
+    _plain(position_ids, "position_ids", torch.int64, (n_axes, tokens))
     _need(sections is None or len(sections) == n_axes, "sections needs one entry per axis")
     rot, rows, code, host = _rotary(cos_cache, sin_cache, sections)
     blocks = page = 0
@@ -355,15 +381,17 @@ def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=No
         _plain(slot_map, "slot_map", torch.int64, (tokens,))
         _need(v.shape == k.shape, "v must have k's shape")
         _, vs = _token_rows(v, "v", first)
-    _same_device(first, q_out, k, k_out, v, cos_cache, sin_cache, position_ids, k_cache, v_cache,
-                 slot_map)
-    _check(load_library().pva_rope_axes(
+    at = _same_device(first, q_out, k, k_out, v, cos_cache, sin_cache, position_ids, k_cache,
+                      v_cache, slot_map)
+    if tokens == 0:
+        return
+    _check((_lib or load_library()).pva_rope_axes(
         _ptr_or_none(q), _ptr_or_none(k), _ptr_or_none(q_out), _ptr_or_none(k_out),
         cos_cache.data_ptr(), sin_cache.data_ptr(), position_ids.data_ptr(), tokens, H, Hkv, d, qs,
         ks, qos, kos, rot, rows, int(bool(rotary_interleaved)), n_axes, host,
         int(bool(axes_interleaved)), int(bool(inverse)), code, _ptr_or_none(v), vs,
         _ptr_or_none(k_cache), _ptr_or_none(v_cache), _ptr_or_none(slot_map), blocks, page,
-        _dtype_code(first), _stream_ptr(stream)))
+        _type_code(first), _stream_on(stream, at)))
 
 
 def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: int,
@@ -379,7 +407,6 @@ def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: i
     past_lens int32 [B] rows before the step, tree_lens int32 [B] nodes in use;
     optional rotation by cos/sin tables with position_ids int64 [n_axes, B, T]
     (None: past + depth); out [B, T, H, d]."""
-    import torch
     _need(q.dim() == 4, "q must be [B, tokens, num_heads, head_size]")
     B, T, H, d = q.shape
     H, Hkv = int(num_heads), int(kv_num_heads)
@@ -395,7 +422,11 @@ def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: i
     _plain(past_lens, "past_lens", i32, (B,))
     _plain(parents, "parents", i32, (B, T))
     _plain(tree_lens, "tree_lens", i32, (B,))
-    _plain(block_table, "block_table", i32, (B, None))
+    width = 0
+    if block_table is not None:
+        _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
+        width = block_table.shape[1]
+        _plain(block_table, "block_table", i32, (B, width))
     rot = rows = code = 0
     n_axes, host = 1, None
     if cos_cache is not None:
@@ -408,16 +439,16 @@ def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: i
     else:
         _need(sin_cache is None and position_ids is None and sections is None,
               "positions and sections need the cos and sin tables")
-    _same_device(q, k_new, v_new, k_cache, v_cache, past_lens, out, parents, tree_lens,
-                 block_table, cos_cache, sin_cache, position_ids)
-    _check(load_library().pva_gqa_tree(
+    at = _same_device(q, k_new, v_new, k_cache, v_cache, past_lens, out, parents, tree_lens,
+                      block_table, cos_cache, sin_cache, position_ids)
+    _check((_lib or load_library()).pva_gqa_tree(
         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         past_lens.data_ptr(), _ptr_or_none(tree_lens), _ptr_or_none(parents),
         _ptr_or_none(block_table), _ptr_or_none(cos_cache), _ptr_or_none(sin_cache),
         _ptr_or_none(position_ids), out.data_ptr(), B, T, blocks, page,
-        0 if block_table is None else block_table.shape[1], H, Hkv, d, rot, rows,
+        width, H, Hkv, d, rot, rows,
         int(bool(rotary_interleaved)), n_axes, host, int(bool(axes_interleaved)), code,
-        float(scale), float(softcap), int(local_window), _dtype_code(q), _stream_ptr(stream)))
+        float(scale), float(softcap), int(local_window), _type_code(q), _stream_on(stream, at)))
 
 
 def pva_kvcache_accept(k_cache, v_cache, past_lens, path, path_lens, new_lens, block_table=None,
@@ -426,27 +457,29 @@ def pva_kvcache_accept(k_cache, v_cache, past_lens, path, path_lens, new_lens, b
     becomes row past + i for i < path_lens, for every head and layer.  Caches
     [n_blocks, Hkv, page, d] or [layers, n_blocks, Hkv, page, d], path int32
     [B, width], past_lens, path_lens, new_lens (= past + path_lens) int32 [B]."""
-    import torch
     _need(k_cache.dim() in (4, 5), "k_cache must be [layers,] [n_blocks, heads, page, head_size]")
     _need(path.dim() == 2, "path must be [B, width]")
     layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
     blocks, Hkv, page, d = k_cache.shape[-4:]
     B, width = path.shape
     i32 = torch.int32
-    _plain(k_cache, "k_cache", k_cache.dtype, tuple(k_cache.shape))
-    _plain(v_cache, "v_cache", k_cache.dtype, tuple(k_cache.shape))
+    _plain(k_cache, "k_cache", k_cache.dtype, k_cache.shape)
+    _plain(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
     _plain(path, "path", i32, (B, width))
     _plain(past_lens, "past_lens", i32, (B,))
     _plain(path_lens, "path_lens", i32, (B,))
     _plain(new_lens, "new_lens", i32, (B,))
-    _plain(block_table, "block_table", i32, (B, None))
-    _same_device(k_cache, v_cache, past_lens, path, path_lens, new_lens, block_table)
-    _check(load_library().pva_kvcache_accept(
+    table_width = 0
+    if block_table is not None:
+        _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
+        table_width = block_table.shape[1]
+        _plain(block_table, "block_table", i32, (B, table_width))
+    at = _same_device(k_cache, v_cache, past_lens, path, path_lens, new_lens, block_table)
+    _check((_lib or load_library()).pva_kvcache_accept(
         k_cache.data_ptr(), v_cache.data_ptr(), past_lens.data_ptr(), path.data_ptr(),
         path_lens.data_ptr(), _ptr_or_none(block_table), new_lens.data_ptr(), B, width, layers,
         blocks * Hkv * page * d, blocks, Hkv, page, d,
-        0 if block_table is None else block_table.shape[1], _dtype_code(k_cache),
-        _stream_ptr(stream)))
+        table_width, _type_code(k_cache), _stream_on(stream, at)))
 
 
 def pva_forward_noalloc(q, k, v, cu_seqlens_q, cu_seqlens_kv, out, B: int, num_heads: int,

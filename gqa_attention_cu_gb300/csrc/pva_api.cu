@@ -345,6 +345,16 @@ namespace host {
 
 std::mutex& api_mutex() { return g_mu; }
 
+int sm_count(int* n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  DeviceInfo di;
+  const int rc = device_info(dev, &di);
+  *n = di.num_sms;
+  return rc;
+}
+
 int acquire(cudaStream_t stream, size_t need, CallContext* c) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -150,6 +150,7 @@ struct CallContext {
   uint8_t* buf = nullptr;      // workspace of at least the bytes asked for
 };
 std::mutex& api_mutex();
+int sm_count(int* n);  // of the current device (under api_mutex)
 int acquire(cudaStream_t stream, size_t need, CallContext* c);
 // Runs the body of a C entry point: an exception (host memory running out)
 // becomes an error code instead of leaving through the C interface.

@@ -24,210 +24,22 @@ using namespace pva::host;
 namespace pva {
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kRopeRows = 4;  // head rows a thread has in flight
-
-template <typename T>
-__device__ __forceinline__ float load_f(T x) { return static_cast<float>(x); }
-template <typename T>
-__device__ __forceinline__ T round_to(float x);
-template <>
-__device__ __forceinline__ float round_to<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half round_to<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-  T v[VEC];
-};
-
-__device__ __forceinline__ float table_at(const void* t, long long i, int is_f16) {
-  return is_f16 ? __half2float(static_cast<const __half*>(t)[i])
-                : static_cast<const float*>(t)[i];
-}
-
-// VEC pairs of a head row per thread: 16-byte accesses where sizes and
-// alignment allow (VEC = 16 / sizeof(T)), single elements otherwise.
+// One token per CTA at a time.
 template <typename T, int VEC, bool TREE>
 __global__ void __launch_bounds__(kRopeThreads) pva_rope_kernel(RopeStep s) {
-  using P = Pack<T, VEC>;
   allow_next_grid();
   wait_prior_grid();
   if (TREE && s.hdr[0] == 0) return;
-  const RopeTable& rt = s.rt;
-  const int half = rt.rot / 2;
-  const int units = s.d / (2 * VEC);  // of 2 * VEC dims
-  const int u = threadIdx.x % units, r0 = threadIdx.x / units, step = kRopeThreads / units;
-  const bool idle = r0 >= step;
-  const bool turned = u * VEC < half;
-  // the unit's two packs of dims: d0 .. d0 + VEC and d1 .. d1 + VEC
-  int d0, d1;
-  if (!turned) {
-    d0 = rt.rot + (u - half / VEC) * 2 * VEC;
-    d1 = d0 + VEC;
-  } else if (rt.interleaved) {
-    d0 = u * 2 * VEC;
-    d1 = d0 + VEC;
-  } else {
-    d0 = u * VEC;
-    d1 = d0 + half;
-  }
-  const int nq = s.q ? s.H : 0, nk = s.k ? s.Hkv : 0, nv = s.v ? s.Hkv : 0;
-  const int n_rows = nq + nk + nv;
-  const T* q = static_cast<const T*>(s.q);
-  const T* k = static_cast<const T*>(s.k);
-  const T* v = static_cast<const T*>(s.v);
-  T* q_out = static_cast<T*>(s.q_out);
-  T* k_out = static_cast<T*>(s.k_out);
-  T* k_cache = static_cast<T*>(s.k_cache);
-  T* v_cache = static_cast<T*>(s.v_cache);
-  const int G = TREE ? s.H / s.Hkv : 1;
-
   for (int tok = blockIdx.x; tok < s.tokens; tok += gridDim.x) {
-    int b = 0, node = tok;
-    long long slot = -1;
-    long long at[kMaxAxes];
-    if (TREE) {
-      b = tok / s.T;
-      node = tok - b * s.T;
-      if (node >= (s.lens ? s.lens[b] : s.T)) {  // an unused node: zeros out
-        P z;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) z.v[e] = round_to<T>(0.0f);
-        P* o = reinterpret_cast<P*>(static_cast<T*>(s.out) + (size_t)tok * s.H * s.d);
-        for (int e = threadIdx.x; e < s.H * s.d / VEC; e += kRopeThreads) o[e] = z;
-        continue;
-      }
-      const int row = s.past[b] + node;
-      const int in_table = row / s.page;
-      const int block = s.table ? s.table[(size_t)b * s.max_blocks + in_table] : b;
-      slot = (long long)block * s.page + (row - in_table * s.page);
-      const int depth = s.depth ? s.depth[tok] : node;
-#pragma unroll
-      for (int a = 0; a < kMaxAxes; ++a)
-        at[a] = !s.pos ? (long long)s.past[b] + depth
-                       : a < rt.n_axes ? s.pos[(size_t)a * s.tokens + tok] : 0;
-    } else {
-      bool bad = false;
-#pragma unroll
-      for (int a = 0; a < kMaxAxes; ++a) {
-        at[a] = a < rt.n_axes ? s.pos[(size_t)a * s.tokens + tok] : 0;
-        bad = bad || at[a] < 0 || at[a] >= rt.rows;
-      }
-      if (k_cache) {
-        slot = s.slots[tok];
-        bad = bad || slot < -1 || slot >= s.n_slots;
-      }
-      if (bad) {  // the token is left out, and the caller told
-        if (threadIdx.x == 0) atomicOr(s.status, PVA_DEV_ROPE);
-        continue;
-      }
-    }
-    float c[VEC], n[VEC];
-    if (turned) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int p = u * VEC + e, a = axis_of_pair(rt, p);
-        long long x = at[0];
-#pragma unroll
-        for (int y = 1; y < kMaxAxes; ++y) x = a == y ? at[y] : x;
-        const long long i = x * half + p;
-        c[e] = table_at(rt.cos, i, rt.is_f16);
-        n[e] = table_at(rt.sin, i, rt.is_f16);
-        if (rt.inverse) n[e] = -n[e];
-      }
-    }
-    const long long cached = slot < 0 ? -1 : slot / s.page;
-    const size_t cache_row = slot < 0 ? 0 : (size_t)(slot - cached * s.page);
-    if (idle) continue;
-    for (int r = r0; r < n_rows; r += step * kRopeRows) {
-      P x0[kRopeRows], x1[kRopeRows];
-#pragma unroll
-      for (int y = 0; y < kRopeRows; ++y) {
-        const int row = r + y * step;
-        if (row >= n_rows) continue;
-        const T* src = row < nq ? q + (size_t)tok * s.q_stride + (size_t)row * s.d
-                       : row < nq + nk
-                           ? k + (size_t)tok * s.k_stride + (size_t)(row - nq) * s.d
-                           : v + (size_t)tok * s.v_stride + (size_t)(row - nq - nk) * s.d;
-        x0[y] = *reinterpret_cast<const P*>(src + d0);
-        x1[y] = *reinterpret_cast<const P*>(src + d1);
-      }
-#pragma unroll
-      for (int y = 0; y < kRopeRows; ++y) {
-        const int row = r + y * step;
-        if (row >= n_rows) continue;
-        const bool is_q = row < nq, is_v = row >= nq + nk;
-        if (turned && !is_v) {
-          P y0, y1;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            // pair e of the unit: interleaved pairs lie side by side across the packs
-            const bool il = rt.interleaved;
-            const float a = il ? load_f(2 * e < VEC ? x0[y].v[(2 * e) % VEC] : x1[y].v[(2 * e) % VEC])
-                               : load_f(x0[y].v[e]);
-            const float f = il ? load_f(2 * e + 1 < VEC ? x0[y].v[(2 * e + 1) % VEC]
-                                                        : x1[y].v[(2 * e + 1) % VEC])
-                               : load_f(x1[y].v[e]);
-            const T g0 = round_to<T>(__fsub_rn(__fmul_rn(c[e], a), __fmul_rn(n[e], f)));
-            const T g1 = round_to<T>(__fadd_rn(__fmul_rn(n[e], a), __fmul_rn(c[e], f)));
-            if (il) {
-              if (2 * e < VEC) y0.v[(2 * e) % VEC] = g0; else y1.v[(2 * e) % VEC] = g0;
-              if (2 * e + 1 < VEC) y0.v[(2 * e + 1) % VEC] = g1; else y1.v[(2 * e + 1) % VEC] = g1;
-            } else {
-              y0.v[e] = g0;
-              y1.v[e] = g1;
-            }
-          }
-          x0[y] = y0;
-          x1[y] = y1;
-        }
-        if (is_q) {
-          if (TREE && s.negate_q) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              x0[y].v[e] = -x0[y].v[e];
-              x1[y].v[e] = -x1[y].v[e];
-            }
-          }
-          T* dst = TREE ? q_out + ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d
-                        : q_out + (size_t)tok * s.q_out_stride + (size_t)row * s.d;
-          *reinterpret_cast<P*>(dst + d0) = x0[y];
-          *reinterpret_cast<P*>(dst + d1) = x1[y];
-          continue;
-        }
-        const int h = is_v ? row - nq - nk : row - nq;
-        if (k_out && !is_v) {
-          T* dst = k_out + (size_t)tok * s.k_out_stride + (size_t)h * s.d;
-          *reinterpret_cast<P*>(dst + d0) = x0[y];
-          *reinterpret_cast<P*>(dst + d1) = x1[y];
-        }
-        if (cached >= 0) {
-          T* dst = (is_v ? v_cache : k_cache) +
-                   (((size_t)cached * s.Hkv + h) * s.page + cache_row) * s.d;
-          *reinterpret_cast<P*>(dst + d0) = x0[y];
-          *reinterpret_cast<P*>(dst + d1) = x1[y];
-        }
-      }
-    }
+    const int depth = TREE && s.depth ? s.depth[tok] : TREE ? tok % s.T : 0;
+    rope_token<T, VEC, TREE>(s, tok, threadIdx.x, depth);
   }
 }
 
 template <typename T>
 cudaError_t launch_rope_type(const RopeStep& s, bool tree, int num_sms, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(T);
-  const uintptr_t ptrs = (uintptr_t)s.q | (uintptr_t)s.k | (uintptr_t)s.v | (uintptr_t)s.q_out |
-                         (uintptr_t)s.k_out | (uintptr_t)s.k_cache | (uintptr_t)s.v_cache |
-                         (uintptr_t)s.out;
-  const long long strides = s.q_stride | s.k_stride | s.v_stride | s.q_out_stride | s.k_out_stride;
-  // 16-byte accesses: whole packs in the rotated and in the copied dims, and
-  // every row on a 16-byte boundary
-  const bool wide = (ptrs & 15) == 0 && strides % VEC == 0 && s.rt.rot / 2 % VEC == 0 &&
-                    (s.d - s.rt.rot) % (2 * VEC) == 0;
+  const bool wide = rope_wide(s, VEC);
   const int most = num_sms * 16;  // CTAs of 128 threads an SM holds
   const dim3 grid(s.tokens < most ? s.tokens : most);
   if (wide)

@@ -9,6 +9,7 @@
 //       step, all of it, when any CTA found something wrong.
 //   pva_rope_kernel        rotated queries to scratch, new rows to the cache,
 //       zeros for unused nodes.
+//   pva_tree_small_front_kernel  both of these for small steps.
 //   attention              one piece of the line per CTA.
 //   pva_tree_join_kernel   adds up the parts of items that lie across a cut.
 #include <limits.h>
@@ -29,85 +30,85 @@ constexpr int kTreeRowsF32 = 32, kTreeKeysF32 = 32;
 // Words of the status block (zero between calls).
 constexpr int kWordArrived = 16, kWordBad = 17;
 
-__global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParams p) {
-  allow_next_grid();
-  wait_prior_grid();
-  __shared__ int s_parent[kMaxTreeNodes];
-  __shared__ uint32_t s_bad;
-  __shared__ int s_last;
-  __shared__ long long s_sum[kFrontThreads / 32 + 1];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int past = p.past[b], n = tree_nodes(p, b);
-  if (tid == 0) {
-    s_bad = 0;
-    const long long total = (long long)past + n;
-    if (n < 0 || n > p.T) s_bad |= PVA_DEV_TREE;
-    if (past < 0 || total > (long long)p.max_blocks * p.page) s_bad |= PVA_DEV_KV_CACHE;
-  }
-  __syncthreads();
-  const bool sane = s_bad == 0;
-  __syncthreads();
+// Steps up to these sizes are checked by every CTA that rotates rows.
+constexpr int kSmallB = 64, kSmallT = 64, kSmallNodes = 1024, kSmallBlocks = 1024;
+
+// Checks sequence b and finds its masks, depths and tiles.  N threads (32: a
+// warp, else the CTA) work on one sequence; i0 is the caller's place among
+// them.  Returns the PVA_DEV_* bits this thread has found; `tiles` is set in the
+// group's first warp.  write: store masks, depths and tile starts.
+template <int N>
+__device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, int past, int n,
+                                                   int i0, bool write, int* s_parent,
+                                                   int* s_depth, long long& tiles) {
+  uint32_t bad = 0;
+  if (n < 0 || n > p.T) bad |= PVA_DEV_TREE;
+  if (past < 0 || (long long)past + n > (long long)p.max_blocks * p.page) bad |= PVA_DEV_KV_CACHE;
+  const bool sane = bad == 0;
   if (sane && n > 0) {
     // the blocks that hold the rows this step reads and writes
     if (p.table) {
       const long long from = p.window > 0 ? (long long)past + 1 - p.window : 0;
       const int first = from > 0 ? (int)(from / p.page) : 0, end = (past + n - 1) / p.page + 1;
-      bool bad = false;
-      for (int i = first + tid; i < end; i += kFrontThreads) {
-        const int block = p.table[(size_t)b * p.max_blocks + i];
-        bad = bad || block < 0 || block >= p.n_blocks;
-      }
-      if (bad) atomicOr(&s_bad, PVA_DEV_BLOCKS);
+      const int32_t* table = p.table + (size_t)b * p.max_blocks;
+#pragma unroll 8
+      for (int i = first + i0; i < end; i += N)
+        if ((unsigned)table[i] >= (unsigned)p.n_blocks) bad |= PVA_DEV_BLOCKS;
     }
     if (p.parents) {
-      bool bad = false;
-      for (int i = tid; i < n; i += kFrontThreads) {
+      for (int i = i0; i < n; i += N) {
         const int up = p.parents[(size_t)b * p.T + i];
         s_parent[i] = up;
-        bad = bad || up < -1 || up >= i;
+        if (up < -1 || up >= i) bad |= PVA_DEV_TREE;
       }
-      if (bad) atomicOr(&s_bad, PVA_DEV_TREE);
     }
-    __syncthreads();
-    const bool walk = s_bad == 0;
-    bool off_table = false;
-    for (int i = tid; i < n && walk; i += kFrontThreads) {
+    bool walk;
+    if (N == 32) {
+      walk = !__any_sync(0xffffffffu, bad);
+      __syncwarp();
+    } else {
+      walk = !__syncthreads_or(bad);
+    }
+    for (int i = i0; i < n && walk; i += N) {
       int depth = i;
       if (p.parents) {
         // The way up visits falling node indices, so the words of the mask
         // are completed from the node's own word downwards.
         uint32_t* row = p.mask + ((size_t)b * p.T + i) * p.W32;
-        for (int w = p.W32 - 1; w > i >> 5; --w) row[w] = 0;
+        if (write)
+          for (int w = p.W32 - 1; w > i >> 5; --w) row[w] = 0;
         int w = i >> 5;
         uint32_t bits = 0;
         depth = 0;
         for (int a = i; a >= 0; a = s_parent[a], ++depth) {
-          while (w > a >> 5) {
-            row[w--] = bits;
-            bits = 0;
-          }
+          for (; w > a >> 5; --w, bits = 0)
+            if (write) row[w] = bits;
           if (p.window <= 0 || depth < p.window) bits |= 1u << (a & 31);
         }
         --depth;
-        for (; w >= 0; --w, bits = 0) row[w] = bits;
-        p.depth[(size_t)b * p.T + i] = depth;
+        if (write) {
+          for (; w >= 0; --w, bits = 0) row[w] = bits;
+          p.depth[(size_t)b * p.T + i] = depth;
+        }
+        if (s_depth) s_depth[i] = depth;
       }
       if (p.rot > 0) {
         for (int a = 0; a < p.n_axes; ++a) {
-          const long long at = p.pos ? p.pos[((size_t)a * p.B + b) * p.T + i] : (long long)past + depth;
-          off_table = off_table || at < 0 || at >= p.cache_rows;
+          const long long at =
+              p.pos ? p.pos[((size_t)a * p.B + b) * p.T + i] : (long long)past + depth;
+          if (at < 0 || at >= p.cache_rows) bad |= PVA_DEV_ROPE;
         }
       }
     }
-    if (off_table) atomicOr(&s_bad, PVA_DEV_ROPE);
   }
   // tiles of each q tile, and where it starts within a kv head
-  if (tid < 32) {
+  tiles = 0;
+  if (i0 < 32) {
     int32_t* qs = p.q_start + (size_t)b * (p.QT + 1);
     long long carry = 0;
     const int qt = sane ? (int)(((long long)n * p.G + p.rows - 1) / p.rows) : 0;
     for (int t0 = 0; t0 <= p.QT; t0 += 32) {
-      const int t = t0 + tid;
+      const int t = t0 + i0;
       int x = 0;
       if (t < qt) {
         int lo, hi;
@@ -118,17 +119,50 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParam
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (tid >= o) upto += y;
+        if (i0 >= o) upto += y;
       }
-      if (t <= p.QT) qs[t] = (int)(carry + upto - x);
+      if (t <= p.QT && write) qs[t] = (int)(carry + upto - x);
       carry += __shfl_sync(0xffffffffu, upto, 31);
     }
-    // carry may pass 31 bits only where the line does too, which is refused below
-    if (tid == 0) {
-      const long long all = carry * p.Hkv;
-      if (all > INT_MAX) atomicOr(&s_bad, PVA_DEV_TOO_MANY);
-      p.tile_start[b] = all > INT_MAX ? 0 : (int)all;
-    }
+    tiles = carry * p.Hkv;
+  }
+  return bad;
+}
+
+// What the step comes to: `tiles` in all, `bad` found, `latched` before.
+__device__ __forceinline__ void front_publish(const TreeParams& p, long long tiles, uint32_t bad,
+                                              bool latched) {
+  if (bad) atomicOr(p.status, bad | PVA_DEV_KV_CACHE);
+  const bool ok = bad == 0 && !latched;
+  const int all = ok ? (int)tiles : 0;
+  const int even = (all + p.pieces - 1) / p.pieces;
+  p.tile_start[p.B] = all;
+  p.hdr[0] = ok ? 1 : 0;
+  p.hdr[1] = all;
+  p.hdr[2] = even > p.min_chunk ? even : p.min_chunk;
+}
+
+__device__ __forceinline__ bool too_many(const TreeParams& p, long long tiles) {
+  return tiles > INT_MAX - 4 * (long long)p.pieces;
+}
+
+__global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParams p) {
+  allow_next_grid();
+  wait_prior_grid();
+  __shared__ int s_parent[kMaxTreeNodes];
+  __shared__ uint32_t s_bad;
+  __shared__ int s_last;
+  __shared__ long long s_sum[kFrontThreads / 32];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  if (tid == 0) s_bad = 0;
+  long long tiles;
+  const uint32_t bad = front_sequence<kFrontThreads>(p, b, p.past[b], tree_nodes(p, b), tid, true,
+                                                     s_parent, nullptr, tiles);
+  __syncthreads();
+  if (bad) atomicOr(&s_bad, bad);
+  if (tid == 0) {
+    if (too_many(p, tiles)) atomicOr(&s_bad, PVA_DEV_TOO_MANY);
+    p.tile_start[b] = too_many(p, tiles) ? 0 : (int)tiles;
   }
   __syncthreads();
   if (tid == 0) {
@@ -162,31 +196,77 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParam
     __syncthreads();
   }
   if (tid == 0) {
-    uint32_t bad = atomicExch(p.status + kWordBad, 0u);
+    const uint32_t all_bad = atomicExch(p.status + kWordBad, 0u) |
+                             (too_many(p, carry) ? PVA_DEV_TOO_MANY : 0u);
     atomicExch(p.status + kWordArrived, 0u);
-    if (carry > INT_MAX - 4 * (long long)p.pieces) bad |= PVA_DEV_TOO_MANY;
     // a step after a rejected one would append after rows that are missing
-    const bool latched = (atomicOr(p.status, 0u) & PVA_DEV_KV_CACHE) != 0;
-    if (bad) atomicOr(p.status, bad | PVA_DEV_KV_CACHE);
-    const bool ok = bad == 0 && !latched;
-    const int tiles = ok ? (int)carry : 0;
-    const int even = (tiles + p.pieces - 1) / p.pieces;
-    p.tile_start[p.B] = tiles;
-    p.hdr[0] = ok ? 1 : 0;
-    p.hdr[1] = tiles;
-    p.hdr[2] = even > p.min_chunk ? even : p.min_chunk;
+    front_publish(p, carry, all_bad, (atomicOr(p.status, 0u) & PVA_DEV_KV_CACHE) != 0);
   }
 }
 
-// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over an item's parts c, in
-// the order of the line; M = max m_c.  One warp per row, 4 channels a lane at a
-// time; rows of items that were not split are left to the attention kernel.
-template <typename T>
-__global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
+// A small step's front end and append in one launch.  Every CTA checks the
+// whole step, so that none has to wait for another before it writes rows: a
+// warp per sequence, a few loads deep.  The first CTA writes the results.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kFrontThreads) pva_tree_small_front_kernel(TreeParams p,
+                                                                             RopeStep r) {
   allow_next_grid();
   wait_prior_grid();
-  if (p.hdr[0] == 0) return;
-  const int chunk = p.hdr[2];
+  constexpr int kWarps = kFrontThreads / 32;
+  __shared__ int s_parent[kWarps][kSmallT];
+  __shared__ int s_depth[kSmallNodes];
+  __shared__ long long s_tiles[kSmallB];
+  __shared__ uint32_t s_bad;
+  __shared__ int s_past[kSmallB], s_n[kSmallB];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool first = blockIdx.x == 0;
+  // read before the first CTA may latch this step's own errors, or after: the
+  // step is refused either way
+  const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
+  if (tid == 0) s_bad = 0;
+  if (tid < p.B) {
+    s_past[tid] = p.past[tid];
+    s_n[tid] = tree_nodes(p, tid);
+  }
+  __syncthreads();
+  for (int b = warp; b < p.B; b += kWarps) {
+    long long tiles;
+    const uint32_t bad = front_sequence<32>(p, b, s_past[b], s_n[b], lane, first, s_parent[warp],
+                                            s_depth + b * p.T, tiles);
+    if (bad) atomicOr(&s_bad, bad);
+    if (lane == 0) s_tiles[b] = tiles;
+    __syncwarp();
+  }
+  __syncthreads();
+  long long before = 0, all = 0;
+  for (int b = 0; b < p.B; ++b) {
+    before += b < tid ? s_tiles[b] : 0;
+    all += s_tiles[b];
+  }
+  const uint32_t bad = s_bad | (too_many(p, all) ? PVA_DEV_TOO_MANY : 0u);
+  if (first) {
+    if (tid < p.B) p.tile_start[tid] = too_many(p, before) ? 0 : (int)before;
+    if (tid == 0) front_publish(p, all, bad, latched);
+  }
+  if (bad || latched) return;
+  constexpr int kAtOnce = kFrontThreads / kRopeThreads;
+  for (int tok = blockIdx.x * kAtOnce + tid / kRopeThreads; tok < r.tokens;
+       tok += gridDim.x * kAtOnce)
+    rope_token<T, VEC, true>(r, tok, tid % kRopeThreads, p.parents ? s_depth[tok] : tok % p.T);
+}
+
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over an item's parts c, in
+// the order of the line; M = max m_c.  One warp per row: lanes hold the weights
+// of 32 parts at a time and V channels of the row, V * 32 at once.  Rows of
+// items that were not split are left to the attention kernel.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
+  struct alignas(4 * V) Part { float v[V]; };
+  struct alignas(sizeof(T) * V) Out { T v[V]; };
+  allow_next_grid();
+  wait_prior_grid();
+  const int tiles = p.hdr[1], chunk = p.hdr[2];
+  if (tiles == 0) return;
   const int lane = threadIdx.x & 31;
   const long long n_rows = (long long)p.B * p.T * p.H;
   for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < n_rows;
@@ -194,34 +274,55 @@ __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
     const int head = (int)(x % p.H);
     const long long tok = x / p.H;
     const int b = (int)(tok / p.T), node = (int)(tok - (long long)b * p.T);
-    if (node >= tree_nodes(p, b)) continue;
     const int h = head / p.G, row = node * p.G + head % p.G, t = row / p.rows;
     const int32_t* qs = p.q_start + (size_t)b * (p.QT + 1);
     const int start = p.tile_start[b] + h * qs[p.QT] + qs[t], end = start + qs[t + 1] - qs[t];
-    const int c0 = start / chunk, c1 = (end - 1) / chunk;
-    if (c0 == c1) continue;
-    const int r = row - t * p.rows;
+    if (node >= tree_nodes(p, b)) continue;
+    const int c0 = start / chunk, n = (end - 1) / chunk - c0 + 1;
+    if (n == 1) continue;
+    // part i: slots of consecutive pieces lie two apart, but for the first
+    const float2* ml = p.part_ml + (row - t * p.rows);
+    const float* po = p.part_o + (size_t)(row - t * p.rows) * p.d;
+    auto slot = [&](int i) { return (size_t)tree_slot(c0 + i, i == 0) * p.rows; };
     float m = __int_as_float(0xff800000);
-    for (int c = c0 + lane; c <= c1; c += 32)
-      m = fmaxf(m, p.part_ml[(size_t)tree_slot(c, c == c0) * p.rows + r].x);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[slot(i)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float top = m == __int_as_float(0xff800000) ? 0.0f : m;
-    float l = 0.0f;
-    for (int c = c0; c <= c1; ++c) {
-      const float2 ml = p.part_ml[(size_t)tree_slot(c, c == c0) * p.rows + r];
-      l += exp2f(ml.x - top) * ml.y;
-    }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     T* out = static_cast<T*>(p.out) + (size_t)x * p.d;
-    for (int d0 = lane; d0 < p.d; d0 += 32) {
-      float acc = 0.0f;
+    for (int d0 = 0; d0 < p.d; d0 += 32 * V) {
+      const int at = d0 + lane * V;
+      const bool in = at < p.d;
+      float acc[V], l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        float w = 0.0f, wl = 0.0f;
+        if (i0 + lane < n) {
+          const float2 v = ml[slot(i0 + lane)];
+          w = exp2f(v.x - top);
+          wl = w * v.y;
+        }
+        const int k = min(32, n - i0);
 #pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const size_t at = (size_t)tree_slot(c, c == c0) * p.rows + r;
-        acc = fmaf(exp2f(p.part_ml[at].x - top), p.part_o[at * p.d + d0], acc);
+        for (int i = 0; i < k; ++i) {
+          Part o;
+          if (in) o = *reinterpret_cast<const Part*>(po + slot(i0 + i) * p.d + at);
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          l += __shfl_sync(0xffffffffu, wl, i);
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(wi, o.v[e], acc[e]);
+          }
+        }
       }
-      out[d0] = static_cast<T>(acc * inv);
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      if (in) {
+        Out o;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o.v[e] = static_cast<T>(acc[e] * inv);
+        *reinterpret_cast<Out*>(out + at) = o;
+      }
     }
   }
 }
@@ -358,14 +459,45 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
   }
 }
 
+template <typename T>
+cudaError_t launch_small_front(const TreeParams& p, const RopeStep& r, int num_sms,
+                               cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(T);
+  constexpr int at_once = kFrontThreads / kRopeThreads;
+  const int want = (r.tokens + at_once - 1) / at_once, most = 2 * num_sms;
+  const dim3 grid(want < most ? want : most);
+  return rope_wide(r, VEC)
+             ? launch_dependent(pva_tree_small_front_kernel<T, VEC>, grid, dim3(kFrontThreads), 0, s, p, r)
+             : launch_dependent(pva_tree_small_front_kernel<T, 1>, grid, dim3(kFrontThreads), 0, s, p, r);
+}
+
+cudaError_t launch_front(const TreeParams& p, const RopeStep& r, int dtype, int num_sms,
+                         cudaStream_t s) {
+  if (p.B <= kSmallB && p.T <= kSmallT && p.B * p.T <= kSmallNodes && p.max_blocks <= kSmallBlocks) {
+    switch (dtype) {
+      case PVA_F32: return launch_small_front<float>(p, r, num_sms, s);
+      case PVA_F16: return launch_small_front<__half>(p, r, num_sms, s);
+      default: return launch_small_front<__nv_bfloat16>(p, r, num_sms, s);
+    }
+  }
+  cudaError_t e = launch_dependent(pva_tree_front_kernel, dim3(p.B), dim3(kFrontThreads), 0, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_rope(r, dtype, true, num_sms, s);
+}
+
 cudaError_t launch_join(const TreeParams& p, int dtype, int num_sms, cudaStream_t s) {
   const long long want = ((long long)p.B * p.T * p.H + 7) / 8;
   const dim3 grid((unsigned)(want < num_sms * 8 ? want : num_sms * 8));
+  // four channels a lane; one where rows of fp32 do not lie on 16-byte boundaries
   switch (dtype) {
-    case PVA_F32: return launch_dependent(pva_tree_join_kernel<float>, grid, dim3(256), 0, s, p);
-    case PVA_F16: return launch_dependent(pva_tree_join_kernel<__half>, grid, dim3(256), 0, s, p);
+    case PVA_F32:
+      return p.d % 4 == 0 && ((uintptr_t)p.out & 15) == 0
+                 ? launch_dependent(pva_tree_join_kernel<float, 4>, grid, dim3(256), 0, s, p)
+                 : launch_dependent(pva_tree_join_kernel<float, 1>, grid, dim3(256), 0, s, p);
+    case PVA_F16:
+      return launch_dependent(pva_tree_join_kernel<__half, 4>, grid, dim3(256), 0, s, p);
     default:
-      return launch_dependent(pva_tree_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p);
+      return launch_dependent(pva_tree_join_kernel<__nv_bfloat16, 4>, grid, dim3(256), 0, s, p);
   }
 }
 
@@ -470,9 +602,9 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   p.out = out;
 
   std::lock_guard<std::mutex> lock(api_mutex());
-  CallContext c;
-  if ((rc = acquire(stream, 0, &c)) != PVA_OK) return rc;
-  p.pieces = tc ? c.num_sms : 2 * c.num_sms;
+  int sms = 0;
+  if ((rc = sm_count(&sms)) != PVA_OK) return rc;
+  p.pieces = tc ? sms : 2 * sms;
   // workspace, in 256-byte steps
   size_t used = 0;
   auto take = [&](size_t bytes) {
@@ -487,6 +619,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   const size_t at_q = take((size_t)B * T * H * d * size);
   const size_t at_o = take(sizeof(float) * 2 * p.pieces * p.rows * (size_t)d);
   const size_t at_ml = take(sizeof(float2) * 2 * p.pieces * (size_t)p.rows);
+  CallContext c;
   if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
   p.status = c.status;
   p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
@@ -536,10 +669,8 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   r.out = out;
   r.status = c.status;
 
-  cudaError_t e = launch_dependent(pva_tree_front_kernel, dim3(B), dim3(kFrontThreads), 0, stream, p);
+  cudaError_t e = launch_front(p, r, dtype, c.num_sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "tree front-end launch");
-  e = launch_rope(r, dtype, true, c.num_sms, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "tree append launch");
   e = tc ? launch_tree_tc(p, dtype, tq, tk, tv, stream) : launch_tree_f32(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   e = launch_join(p, dtype, c.num_sms, stream);

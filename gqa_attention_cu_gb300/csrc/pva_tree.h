@@ -82,17 +82,24 @@ __device__ __forceinline__ int tree_nodes(const TreeParams& p, int b) {
   return p.lens ? p.lens[b] : p.T;
 }
 
-// Index of the last entry of start[0 .. n) that is <= x (entries ascend).
+// Index of the last entry of start[0 .. n) that is <= x (entries ascend, the
+// first one is <= x).  Called by a whole warp: 32 entries are compared at once,
+// so few dependent loads stand between a piece and its first copy.
 __device__ __forceinline__ int tree_find(const int32_t* start, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= x) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 32) {  // 32 probes a step
+    const int stride = (n + 31) / 32;
+    const int i = lo + min(lane * stride, n - 1);
+    const int hits = __popc(__ballot_sync(0xffffffffu, lane * stride < n && start[i] <= x));
+    lo += (hits - 1) * stride;
+    n = min(stride, n - (hits - 1) * stride);
   }
-  return lo;
+  return lo + __popc(__ballot_sync(0xffffffffu, lane < n && start[lo + min(lane, n - 1)] <= x)) - 1;
 }
 
-// The segment at tile x of the line, for a piece that ends at `end`.
+// The segment at tile x of the line, for a piece that ends at `end` (a whole
+// warp calls).
 __device__ __forceinline__ TreeSegment tree_segment(const TreeParams& p, int piece, int x,
                                                     int end) {
   TreeSegment s;
