@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libpva.so")
 
 SOURCES = ["pva_api.cu", "pva_scheduler.cu", "pva_prefill_f32.cu", "pva_prefill_tc.cu",
            "pva_prefill_pair.cu", "pva_decode.cu", "pva_noalloc.cu", "pva_kvcache.cu",
-           "pva_tree.cu", "pva_tree_tc.cu", "pva_rope.cu", "pva_blocks.cu"]
+           "pva_tree.cu", "pva_tree_tc.cu", "pva_tree_pair.cu", "pva_rope.cu", "pva_blocks.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

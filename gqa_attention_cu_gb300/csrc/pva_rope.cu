@@ -30,9 +30,10 @@ __global__ void __launch_bounds__(kRopeThreads) pva_rope_kernel(RopeStep s) {
   allow_next_grid();
   wait_prior_grid();
   if (TREE && s.hdr[0] == 0) return;
+  const uint32_t axes = rope_axes<VEC>(s, threadIdx.x);
   for (int tok = blockIdx.x; tok < s.tokens; tok += gridDim.x) {
     const int depth = TREE && s.depth ? s.depth[tok] : TREE ? tok % s.T : 0;
-    rope_token<T, VEC, TREE>(s, tok, threadIdx.x, depth);
+    rope_token<T, VEC, TREE>(s, tok, threadIdx.x, axes, depth);
   }
 }
 

@@ -62,7 +62,7 @@ struct RopeStep {
   const int64_t* pos;       // [n_axes, tokens]; tree form: may be nullptr
   const int64_t* slots;     // [tokens], -1: not cached
   int page;                 // rows of a cache block
-  long long n_slots;        // blocks * page
+  long long n_slots;        // blocks * page (both forms)
   // Tree form (TREE): token b * T + i is node i of sequence b; it goes to
   // cache row past[b] + i, and its query rows to [B][Hkv][T * G][d].
   const int32_t* hdr;       // hdr[0] == 0: the step was rejected, nothing is written
@@ -102,11 +102,47 @@ __device__ __forceinline__ float table_at(const void* t, long long i, int is_f16
                 : static_cast<const float*>(t)[i];
 }
 
+// Neighbouring pairs across two packs <-> first and second members.
+template <typename T, int VEC>
+__device__ __forceinline__ void split_pairs(Pack<T, VEC>& x, Pack<T, VEC>& y) {
+  Pack<T, VEC> a, b;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    a.v[e] = 2 * e < VEC ? x.v[2 * e % VEC] : y.v[2 * e % VEC];
+    b.v[e] = 2 * e + 1 < VEC ? x.v[(2 * e + 1) % VEC] : y.v[(2 * e + 1) % VEC];
+  }
+  x = a;
+  y = b;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void join_pairs(Pack<T, VEC>& x, Pack<T, VEC>& y) {
+  Pack<T, VEC> a, b;
+#pragma unroll
+  for (int e = 0; e < 2 * VEC; ++e) {
+    const T v = e % 2 ? y.v[e / 2] : x.v[e / 2];
+    if (e < VEC) a.v[e % VEC] = v; else b.v[e % VEC] = v;
+  }
+  x = a;
+  y = b;
+}
+
+// Axes of the VEC pairs that thread tid turns, two bits each.
+template <int VEC>
+__device__ __forceinline__ uint32_t rope_axes(const RopeStep& s, int tid) {
+  uint32_t axes = 0;
+  if (s.rt.n_axes == 1) return 0;
+  const int u = tid % (s.d / (2 * VEC));
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) axes |= (uint32_t)axis_of_pair(s.rt, u * VEC + e) << (2 * e);
+  return axes;
+}
+
 // Does token tok (tid: one of kRopeThreads threads).  VEC pairs of a head row
 // per thread: 16-byte accesses where sizes and alignment allow (VEC = 16 /
 // sizeof(T)), single elements otherwise.
 template <typename T, int VEC, bool TREE>
-__device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, int depth) {
+__device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, uint32_t axes,
+                                           int depth) {
   using P = Pack<T, VEC>;
   const RopeTable& rt = s.rt;
   const int half = rt.rot / 2;
@@ -137,6 +173,22 @@ __device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, 
   T* v_cache = static_cast<T*>(s.v_cache);
   const int G = TREE ? s.H / s.Hkv : 1;
 
+  // The first rows are on their way while the position, the tables' entries
+  // and the slot are looked up, one after the other.
+  P x0[kRopeRows], x1[kRopeRows];
+  auto load_rows = [&](int r) {
+#pragma unroll
+    for (int y = 0; y < kRopeRows; ++y) {
+      const int row = r + y * step;
+      if (row >= n_rows) continue;
+      const T* src = row < nq ? q + (size_t)tok * s.q_stride + (size_t)row * s.d
+                     : row < nq + nk ? k + (size_t)tok * s.k_stride + (size_t)(row - nq) * s.d
+                                     : v + (size_t)tok * s.v_stride + (size_t)(row - nq - nk) * s.d;
+      x0[y] = *reinterpret_cast<const P*>(src + d0);
+      x1[y] = *reinterpret_cast<const P*>(src + d1);
+    }
+  };
+  if (!idle) load_rows(r0);
   int b = 0, node = tok;
   long long slot = -1;
   long long at[kMaxAxes];
@@ -179,7 +231,7 @@ __device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, 
   if (turned) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const int p = u * VEC + e, a = axis_of_pair(rt, p);
+      const int p = u * VEC + e, a = (axes >> (2 * e)) & 3;
       long long x = at[0];
 #pragma unroll
       for (int y = 1; y < kMaxAxes; ++y) x = a == y ? at[y] : x;
@@ -189,50 +241,29 @@ __device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, 
       if (rt.inverse) n[e] = -n[e];
     }
   }
-  const long long cached = slot < 0 ? -1 : slot / s.page;
-  const size_t cache_row = slot < 0 ? 0 : (size_t)(slot - cached * s.page);
+  long long cached = -1;
+  size_t cache_row = 0;
+  if (slot >= 0) {
+    cached = s.n_slots >> 32 ? slot / s.page : (uint32_t)slot / (uint32_t)s.page;
+    cache_row = (size_t)(slot - cached * s.page);
+  }
   if (idle) return;
   for (int r = r0; r < n_rows; r += step * kRopeRows) {
-    P x0[kRopeRows], x1[kRopeRows];
-#pragma unroll
-    for (int y = 0; y < kRopeRows; ++y) {
-      const int row = r + y * step;
-      if (row >= n_rows) continue;
-      const T* src = row < nq ? q + (size_t)tok * s.q_stride + (size_t)row * s.d
-                     : row < nq + nk
-                         ? k + (size_t)tok * s.k_stride + (size_t)(row - nq) * s.d
-                         : v + (size_t)tok * s.v_stride + (size_t)(row - nq - nk) * s.d;
-      x0[y] = *reinterpret_cast<const P*>(src + d0);
-      x1[y] = *reinterpret_cast<const P*>(src + d1);
-    }
+    if (r != r0) load_rows(r);
 #pragma unroll
     for (int y = 0; y < kRopeRows; ++y) {
       const int row = r + y * step;
       if (row >= n_rows) continue;
       const bool is_q = row < nq, is_v = row >= nq + nk;
       if (turned && !is_v) {
-        P y0, y1;
+        if (rt.interleaved) split_pairs(x0[y], x1[y]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          // pair e of the unit: interleaved pairs lie side by side across the packs
-          const bool il = rt.interleaved;
-          const float a = il ? load_f(2 * e < VEC ? x0[y].v[(2 * e) % VEC] : x1[y].v[(2 * e) % VEC])
-                             : load_f(x0[y].v[e]);
-          const float f = il ? load_f(2 * e + 1 < VEC ? x0[y].v[(2 * e + 1) % VEC]
-                                                      : x1[y].v[(2 * e + 1) % VEC])
-                             : load_f(x1[y].v[e]);
-          const T g0 = round_to<T>(__fsub_rn(__fmul_rn(c[e], a), __fmul_rn(n[e], f)));
-          const T g1 = round_to<T>(__fadd_rn(__fmul_rn(n[e], a), __fmul_rn(c[e], f)));
-          if (il) {
-            if (2 * e < VEC) y0.v[(2 * e) % VEC] = g0; else y1.v[(2 * e) % VEC] = g0;
-            if (2 * e + 1 < VEC) y0.v[(2 * e + 1) % VEC] = g1; else y1.v[(2 * e + 1) % VEC] = g1;
-          } else {
-            y0.v[e] = g0;
-            y1.v[e] = g1;
-          }
+          const float a = load_f(x0[y].v[e]), f = load_f(x1[y].v[e]);
+          x0[y].v[e] = round_to<T>(__fsub_rn(__fmul_rn(c[e], a), __fmul_rn(n[e], f)));
+          x1[y].v[e] = round_to<T>(__fadd_rn(__fmul_rn(n[e], a), __fmul_rn(c[e], f)));
         }
-        x0[y] = y0;
-        x1[y] = y1;
+        if (rt.interleaved) join_pairs(x0[y], x1[y]);
       }
       if (is_q) {
         if (TREE && s.negate_q) {

@@ -31,7 +31,7 @@ constexpr int kTreeRowsF32 = 32, kTreeKeysF32 = 32;
 constexpr int kWordArrived = 16, kWordBad = 17;
 
 // Steps up to these sizes are checked by every CTA that rotates rows.
-constexpr int kSmallB = 64, kSmallT = 64, kSmallNodes = 1024, kSmallBlocks = 1024;
+constexpr int kSmallB = 16, kSmallT = 64, kSmallNodes = 256, kSmallBlocks = 1024;
 
 // Checks sequence b and finds its masks, depths and tiles.  N threads (32: a
 // warp, else the CTA) work on one sequence; i0 is the caller's place among
@@ -61,6 +61,13 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
         s_parent[i] = up;
         if (up < -1 || up >= i) bad |= PVA_DEV_TREE;
       }
+    }
+    if (p.rot > 0 && p.pos) {
+      for (int a = 0; a < p.n_axes; ++a)
+        for (int i = i0; i < n; i += N) {
+          const int64_t at = p.pos[((size_t)a * p.B + b) * p.T + i];
+          if (at < 0 || at >= p.cache_rows) bad |= PVA_DEV_ROPE;
+        }
     }
     bool walk;
     if (N == 32) {
@@ -92,13 +99,7 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
         }
         if (s_depth) s_depth[i] = depth;
       }
-      if (p.rot > 0) {
-        for (int a = 0; a < p.n_axes; ++a) {
-          const long long at =
-              p.pos ? p.pos[((size_t)a * p.B + b) * p.T + i] : (long long)past + depth;
-          if (at < 0 || at >= p.cache_rows) bad |= PVA_DEV_ROPE;
-        }
-      }
+      if (p.rot > 0 && !p.pos && (long long)past + depth >= p.cache_rows) bad |= PVA_DEV_ROPE;
     }
   }
   // tiles of each q tile, and where it starts within a kv head
@@ -250,46 +251,44 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_small_front_kernel(Tre
   }
   if (bad || latched) return;
   constexpr int kAtOnce = kFrontThreads / kRopeThreads;
+  const uint32_t axes = rope_axes<VEC>(r, tid % kRopeThreads);
   for (int tok = blockIdx.x * kAtOnce + tid / kRopeThreads; tok < r.tokens;
        tok += gridDim.x * kAtOnce)
-    rope_token<T, VEC, true>(r, tok, tid % kRopeThreads, p.parents ? s_depth[tok] : tok % p.T);
+    rope_token<T, VEC, true>(r, tok, tid % kRopeThreads, axes,
+                             p.parents ? s_depth[tok] : tok % p.T);
 }
 
 // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over an item's parts c, in
-// the order of the line; M = max m_c.  One warp per row: lanes hold the weights
-// of 32 parts at a time and V channels of the row, V * 32 at once.  Rows of
-// items that were not split are left to the attention kernel.
+// the order of the line; M = max m_c.  CTAs (c, y) look at the cut at the start
+// of piece c: the first cut of an item has its rows joined, one warp per row.
+// Lanes hold the weights of 32 parts at a time and V channels of the row, V *
+// 32 at once.  So the work is that of the cut items, however many there are.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
   struct alignas(4 * V) Part { float v[V]; };
   struct alignas(sizeof(T) * V) Out { T v[V]; };
   allow_next_grid();
   wait_prior_grid();
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int tiles = p.hdr[1], chunk = p.hdr[2];
-  if (tiles == 0) return;
-  const int lane = threadIdx.x & 31;
-  const long long n_rows = (long long)p.B * p.T * p.H;
-  for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < n_rows;
-       x += (long long)gridDim.x * 8) {
-    const int head = (int)(x % p.H);
-    const long long tok = x / p.H;
-    const int b = (int)(tok / p.T), node = (int)(tok - (long long)b * p.T);
-    const int h = head / p.G, row = node * p.G + head % p.G, t = row / p.rows;
-    const int32_t* qs = p.q_start + (size_t)b * (p.QT + 1);
-    const int start = p.tile_start[b] + h * qs[p.QT] + qs[t], end = start + qs[t + 1] - qs[t];
-    if (node >= tree_nodes(p, b)) continue;
-    const int c0 = start / chunk, n = (end - 1) / chunk - c0 + 1;
-    if (n == 1) continue;
+  for (long long c = blockIdx.x + 1; c * chunk < tiles; c += gridDim.x) {
+    const TreeItem it = tree_item(p, (int)(c * chunk));
+    const int c0 = it.start / chunk;
+    if (it.start == c * chunk || c0 != c - 1) continue;
+    const int row = it.t * p.rows + r, node = row / p.G;
+    if (node >= tree_nodes(p, it.b)) continue;
+    const int n = (it.end - 1) / chunk - c0 + 1;
     // part i: slots of consecutive pieces lie two apart, but for the first
-    const float2* ml = p.part_ml + (row - t * p.rows);
-    const float* po = p.part_o + (size_t)(row - t * p.rows) * p.d;
+    const float2* ml = p.part_ml + r;
+    const float* po = p.part_o + (size_t)r * p.d;
     auto slot = [&](int i) { return (size_t)tree_slot(c0 + i, i == 0) * p.rows; };
     float m = __int_as_float(0xff800000);
     for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[slot(i)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float top = m == __int_as_float(0xff800000) ? 0.0f : m;
-    T* out = static_cast<T*>(p.out) + (size_t)x * p.d;
+    T* out = static_cast<T*>(p.out) +
+             (((size_t)it.b * p.T + node) * p.H + it.h * p.G + row - node * p.G) * p.d;
     for (int d0 = 0; d0 < p.d; d0 += 32 * V) {
       const int at = d0 + lane * V;
       const bool in = at < p.d;
@@ -473,7 +472,8 @@ cudaError_t launch_small_front(const TreeParams& p, const RopeStep& r, int num_s
 
 cudaError_t launch_front(const TreeParams& p, const RopeStep& r, int dtype, int num_sms,
                          cudaStream_t s) {
-  if (p.B <= kSmallB && p.T <= kSmallT && p.B * p.T <= kSmallNodes && p.max_blocks <= kSmallBlocks) {
+  if (p.B <= kSmallB && p.T <= kSmallT && p.B * p.T <= kSmallNodes &&
+      (long long)p.B * p.max_blocks <= kSmallBlocks) {
     switch (dtype) {
       case PVA_F32: return launch_small_front<float>(p, r, num_sms, s);
       case PVA_F16: return launch_small_front<__half>(p, r, num_sms, s);
@@ -485,9 +485,9 @@ cudaError_t launch_front(const TreeParams& p, const RopeStep& r, int dtype, int 
   return launch_rope(r, dtype, true, num_sms, s);
 }
 
-cudaError_t launch_join(const TreeParams& p, int dtype, int num_sms, cudaStream_t s) {
-  const long long want = ((long long)p.B * p.T * p.H + 7) / 8;
-  const dim3 grid((unsigned)(want < num_sms * 8 ? want : num_sms * 8));
+cudaError_t launch_join(const TreeParams& p, int dtype, cudaStream_t s) {
+  const long long rows = (long long)p.T * p.G;
+  const dim3 grid(p.pieces - 1, (unsigned)((rows < p.rows ? rows : p.rows) + 7) / 8);
   // four channels a lane; one where rows of fp32 do not lie on 16-byte boundaries
   switch (dtype) {
     case PVA_F32:
@@ -592,7 +592,9 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   p.rot = rot;
   p.n_axes = rot ? n_axes : 1;
   p.cache_rows = cache_rows;
-  p.rows = tc ? kTcRows : kTreeRowsF32;
+  // two query tiles an item where a sequence can have more rows than one holds
+  const bool pair = tc && (long long)T * G > kTcRows && d <= 192;
+  p.rows = pair ? 2 * kTcRows : tc ? kTcRows : kTreeRowsF32;
   p.bn = tc ? tree_keys(d) : kTreeKeysF32;
   p.QT = (int)(((long long)T * G + p.rows - 1) / p.rows);
   p.W32 = parents ? (T + 31) / 32 : 0;
@@ -637,7 +639,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
     const int box = block_table && page_size < p.bn ? page_size : p.bn;
     const long long planes = (long long)n_blocks * Hkv;
     if ((rc = get_encoder()) != PVA_OK ||
-        (rc = encode_plane_map(&tq, p.q, dtype, d, T * G, (long long)B * Hkv, 64, p.rows, true)) !=
+        (rc = encode_plane_map(&tq, p.q, dtype, d, T * G, (long long)B * Hkv, 64, kTcRows, true)) !=
             PVA_OK ||
         (rc = encode_plane_map(&tk, k_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK ||
         (rc = encode_plane_map(&tv, v_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK)
@@ -658,6 +660,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   r.d = d;
   r.pos = p.pos;
   r.page = page_size;
+  r.n_slots = (long long)n_blocks * page_size;
   r.hdr = p.hdr;
   r.past = past_lens;
   r.lens = tree_lens;
@@ -671,9 +674,11 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
 
   cudaError_t e = launch_front(p, r, dtype, c.num_sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "tree front-end launch");
-  e = tc ? launch_tree_tc(p, dtype, tq, tk, tv, stream) : launch_tree_f32(p, stream);
+  e = pair ? launch_tree_pair(p, dtype, tq, tk, tv, stream)
+      : tc ? launch_tree_tc(p, dtype, tq, tk, tv, stream)
+           : launch_tree_f32(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
-  e = launch_join(p, dtype, c.num_sms, stream);
+  e = launch_join(p, dtype, stream);
   return e == cudaSuccess ? PVA_OK : cuda_fail(e, "tree join launch");
 }
 

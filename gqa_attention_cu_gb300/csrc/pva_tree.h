@@ -98,19 +98,34 @@ __device__ __forceinline__ int tree_find(const int32_t* start, int n, int x) {
   return lo + __popc(__ballot_sync(0xffffffffu, lane < n && start[lo + min(lane, n - 1)] <= x)) - 1;
 }
 
+// The item at tile x of the line (a whole warp calls).
+struct TreeItem {
+  int b, h, t;
+  int start, end;  // its tiles on the line
+};
+__device__ __forceinline__ TreeItem tree_item(const TreeParams& p, int x) {
+  TreeItem i;
+  i.b = tree_find(p.tile_start, p.B, x);
+  const int32_t* qs = p.q_start + (size_t)i.b * (p.QT + 1);
+  const int per_head = qs[p.QT], first = p.tile_start[i.b];
+  i.h = (x - first) / per_head;
+  const int base = first + i.h * per_head;
+  i.t = tree_find(qs, p.QT, x - base);
+  i.start = base + qs[i.t];
+  i.end = base + qs[i.t + 1];
+  return i;
+}
+
 // The segment at tile x of the line, for a piece that ends at `end` (a whole
 // warp calls).
 __device__ __forceinline__ TreeSegment tree_segment(const TreeParams& p, int piece, int x,
                                                     int end) {
+  const TreeItem i = tree_item(p, x);
   TreeSegment s;
-  s.b = tree_find(p.tile_start, p.B, x);
-  const int32_t* qs = p.q_start + (size_t)s.b * (p.QT + 1);
-  const int per_head = qs[p.QT];
-  const int rel = x - p.tile_start[s.b];
-  s.h = rel / per_head;
-  const int r = rel - s.h * per_head;
-  s.t = tree_find(qs, p.QT, r);
-  const int in = r - qs[s.t], all = qs[s.t + 1] - qs[s.t];
+  s.b = i.b;
+  s.h = i.h;
+  s.t = i.t;
+  const int in = x - i.start, all = i.end - i.start;
   s.past = p.past[s.b];
   s.n = tree_nodes(p, s.b);
   int hi;
@@ -124,6 +139,9 @@ __device__ __forceinline__ TreeSegment tree_segment(const TreeParams& p, int pie
 
 cudaError_t launch_tree_tc(const TreeParams& p, int dtype, const CUtensorMap& tq,
                            const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+// Two query tiles per item (p.rows = 256), head sizes up to 192.
+cudaError_t launch_tree_pair(const TreeParams& p, int dtype, const CUtensorMap& tq,
+                             const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
 cudaError_t launch_tree_f32(const TreeParams& p, cudaStream_t s);
 
 }  // namespace pva

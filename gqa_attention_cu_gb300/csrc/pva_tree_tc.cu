@@ -26,15 +26,14 @@
 // V rows outside the item's keys are zeroed in shared memory before the
 // product (cache rows there may hold anything, and 0 * NaN is NaN); their
 // scores are masked whatever they are.
-#include "pva_device.cuh"
-#include "pva_tree.h"
+#include "pva_tree_tile.cuh"
 
 namespace pva {
 namespace {
 
+using namespace tile;
+
 constexpr int kThreads = 192;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the max grows > 2^8
 constexpr int kItemSlots = 4;
 constexpr int kSoftmaxWarps = 4;
 
@@ -74,80 +73,6 @@ struct Bars {
   ItemSlot items[kItemSlots];
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
-
-template <int BN>
-struct Mask {
-  uint32_t w[BN / 32];
-};
-
-template <int BN, bool MASKED>
-__device__ __forceinline__ bool seen(const Mask<BN>& m, int c) {
-  return !MASKED || ((m.w[c >> 5] >> (c & 31)) & 1u);
-}
-
-// Bits [lo, hi) of 32.
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 32);
-  if (hi <= lo) return 0u;
-  return (0xffffffffu >> (32 - (hi - lo))) << lo;
-}
-
-// Extreme raw scores of a tile (max, and with a softcap nothing else: both
-// transforms are increasing, a negative scale having moved into Q).
-template <int BN, bool MASKED>
-__device__ __forceinline__ float row_max(const uint32_t (&v)[BN / 32][32], const Mask<BN>& m) {
-  const float ninf = __int_as_float(0xff800000);
-  float a[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll
-  for (int e = 0; e < BN; e += 2) {
-    const float x0 = __uint_as_float(v[e >> 5][e & 31]);
-    const float x1 = __uint_as_float(v[e >> 5][(e + 1) & 31]);
-    float& t = a[(e >> 1) & 3];
-    t = fmax3f(t, seen<BN, MASKED>(m, e) ? x0 : ninf, seen<BN, MASKED>(m, e + 1) ? x1 : ninf);
-  }
-  return fmaxf(fmax3f(a[0], a[1], a[2]), a[3]);
-}
-
-// 2^(x - m) over 64 columns from c0 on, their sum, and P as 16-bit pairs.  P is
-// rounded to the storage type for the tensor-core product (relative error half
-// a step of an element, the error that V has already); the row sum adds the
-// fp32 values.
-template <typename T, int BN, bool CAP, bool MASKED>
-__device__ __forceinline__ float exp_half(const uint32_t (&v)[BN / 32][32], int c0,
-                                          const Mask<BN>& m, float s_mul, float cap_mul,
-                                          float m_eff, uint32_t (&pw)[32]) {
-  const float ninf = __int_as_float(0xff800000);
-  const float2 mul2 = make_float2(s_mul, s_mul), neg_m = make_float2(-m_eff, -m_eff);
-  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-  for (int g = 0; g < 32; g += 8) {
-    float2 x[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int e = c0 + 2 * (g + k);
-      const float2 s = make_float2(__uint_as_float(v[e >> 5][e & 31]),
-                                   __uint_as_float(v[e >> 5][(e + 1) & 31]));
-      if (CAP) {
-        x[k].x = fmaf(cap_mul, tanh_via_exp2(s.x * s_mul), -m_eff);
-        x[k].y = fmaf(cap_mul, tanh_via_exp2(s.y * s_mul), -m_eff);
-      } else {
-        x[k] = ffma2(s, mul2, neg_m);
-      }
-      x[k].x = seen<BN, MASKED>(m, e) ? x[k].x : ninf;
-      x[k].y = seen<BN, MASKED>(m, e + 1) ? x[k].y : ninf;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2_approx(x[k].x), ex2_approx(x[k].y));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      acc[k & 1] = fadd2(acc[k & 1], x[k]);
-      pw[g + k] = pack2<T>(x[k].x, x[k].y);
-    }
-  }
-  const float2 r = fadd2(acc[0], acc[1]);
-  return r.x + r.y;
-}
 
 template <typename T, int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -206,9 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tiles = p.hdr[1], chunk = p.hdr[2];
     const long long from = (long long)blockIdx.x * chunk;
     const int end = (int)(from + chunk < tiles ? from + chunk : tiles);
-    // rows of one copy, copies side by side in a tile
-    const int box = p.table && p.page < BN ? p.page : BN;
-    const int copies = BN / box;
+    const TileCopies tc(p, BN);
     uint32_t loads = 0, published = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -245,28 +168,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      const int total = s.past + s.n;
       for (int j = s.j0; ok && j < s.j0 + s.count; ++j) {
-        // this lane's copy of the tile: rows [r0, r0 + box) of the sequence
-        const int r0 = j * BN + lane * box;
-        const bool mine = lane < copies && r0 < total && r0 + box > s.lo;
         int plane = 0, y = 0;
-        if (mine) {
-          const int in = r0 / p.page;
-          const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
-          plane = block * p.Hkv + s.h;
-          y = r0 - in * p.page;
-        }
+        const bool mine = tc.locate(p, s, BN, j, lane, plane, y);
         const uint32_t n_copies = __popc(__ballot_sync(0xffffffffu, mine));
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++loads) {
           const int sl = loads % C::SLOTS;
           if (!(ok = wait(&bars->ring_empty[sl], ((loads / C::SLOTS) & 1) ^ 1))) break;
           if (lane == 0)
-            mbar_arrive_expect_tx(&bars->ring_full[sl], n_copies * C::CH * (uint32_t)box * 128u);
+            mbar_arrive_expect_tx(&bars->ring_full[sl], n_copies * C::CH * (uint32_t)tc.box * 128u);
           __syncwarp();
           if (mine) {
-            uint8_t* dst = smem + sl * C::KV_TILE + lane * box * 128;
+            uint8_t* dst = smem + sl * C::KV_TILE + lane * tc.box * 128;
 #pragma unroll
             for (int c = 0; c < C::CH; ++c)
               tma_load_3d(dst + c * C::KV_CHUNK, kv ? &tmap_v : &tmap_k, &bars->ring_full[sl],
@@ -375,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gt = 0, taken = 0, done = 0;
     uint32_t lq = 0;  // ring loads accounted for (the producer's order)
     bool ok = true, q_pre = false;
-    T* out = static_cast<T*>(p.out);
     // Copies the next Q tile from its ring slots into TMEM.
     auto copy_q = [&]() -> bool {
       bool got = true;
@@ -436,10 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t l0 = lq;  // the segment's first K load
       lq += 2 * n;
       const int total = s.past + s.n;
-      const int depth = p.parents ? p.depth[(size_t)s.b * p.T + node] : node;
-      const int row_lo = p.window > 0 ? max(0, s.past + depth + 1 - p.window) : 0;
-      const int row_hi = p.parents ? s.past : s.past + node + 1;
-      const uint32_t* anc = p.parents ? p.mask + ((size_t)s.b * p.T + node) * p.W32 : nullptr;
+      const RowView view = row_view(p, s, node);
       const bool any_own = __any_sync(0xffffffffu, own);
       float m_used = NEG_INF, l = 0.0f;
 
@@ -452,63 +362,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->ring_full[L % C::SLOTS],
                                                         (L / C::SLOTS) & 1, abort, status));
           if (!ok) break;
-          if (r < BN && (k0 + r < s.lo || k0 + r >= total)) {
-            uint8_t* v = smem + (L % C::SLOTS) * C::KV_TILE + r * 128;
-#pragma unroll
-            for (int c = 0; c < C::CH; ++c)
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(v + c * C::KV_CHUNK + u * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+          zero_v_rows<BN, C::CH>(smem + (L % C::SLOTS) * C::KV_TILE, r, k0, s.lo, total);
         }
         ok = __all_sync(0xffffffffu,
                         mbar_wait<false>(&bars->s_full[T_ & 1], (T_ >> 1) & 1, abort, status));
         if (!ok) break;
         if (any_own) {
           tc_fence_after();
-          const uint32_t col_s = C::COL_S + (T_ & 1) * BN;
-          uint32_t v[BN / 32][32];
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) tmem_ld32(t_lane + col_s + c * 32, v[c]);
-          tmem_wait_ld();
-          const int lo_c = row_lo - k0, hi_c = row_hi - k0;  // visible columns [lo_c, hi_c)
-          const bool masked = !__all_sync(0xffffffffu, lo_c <= 0 && hi_c >= BN);
+          const uint32_t t_s = t_lane + C::COL_S + (T_ & 1) * BN;
+          const bool all = __all_sync(0xffffffffu, view.lo <= k0 && view.hi >= k0 + BN);
           Mask<BN> mk;
-          if (masked) {
-#pragma unroll
-            for (int w = 0; w < BN / 32; ++w) {
-              mk.w[w] = bit_range(lo_c - 32 * w, hi_c - 32 * w);
-              // node that column 32 w stands for; its bits continue in the next word
-              const int first = k0 + 32 * w - s.past;
-              if (p.parents && first > -32 && first < 32 * p.W32) {
-                const int word = first >> 5;
-                const uint32_t a = word >= 0 ? anc[word] : 0u;
-                const uint32_t b = word + 1 < p.W32 ? anc[word + 1] : 0u;
-                mk.w[w] |= __funnelshift_r(a, b, first & 31);
-              }
-            }
-          }
-          const float mx = masked ? row_max<BN, true>(v, mk) : row_max<BN, false>(v, mk);
-          float mt = NEG_INF;
-          if (mx != NEG_INF) mt = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
-          const float m_new = fmaxf(m_used, mt);
-          float alpha = 1.0f;
-          if (m_new > m_used + kRescaleThreshold) {
-            alpha = ex2_approx(m_used - m_new);  // 0 when m_used is -inf
-            m_used = m_new;
-          }
-          const float m_eff = m_used == NEG_INF ? 0.0f : m_used;
-          float rs = 0.0f;
-#pragma unroll
-          for (int half = 0; half < BN / 64; ++half) {
-            uint32_t pw[32];
-            rs += masked ? exp_half<T, BN, CAP, true>(v, half * 64, mk, s_mul, cap_mul, m_eff, pw)
-                         : exp_half<T, BN, CAP, false>(v, half * 64, mk, s_mul, cap_mul, m_eff, pw);
-            // P (16-bit pairs) over the columns of S read above
-            tmem_st32(t_lane + col_s + half * 32, pw);
-          }
-          l = l * alpha + rs;
+          if (!all) mk = row_mask<BN>(p, view, s.past, k0);
+          const float alpha = all ? softmax_tile<T, BN, CAP, false>(t_s, mk, s_mul, cap_mul, m_used, l)
+                                  : softmax_tile<T, BN, CAP, true>(t_s, mk, s_mul, cap_mul, m_used, l);
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // O must hold PV(j-1) before it is rescaled; PV(j-2) precedes S(j),
             // so the parity of the outstanding phase is unambiguous.
@@ -516,15 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_wait<false>(&bars->o_ready, (T_ - 1) & 1, abort, status));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_lane + C::COL_O + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(t_lane + C::COL_O + c, o);
-            }
+            scale_o<D>(t_lane + C::COL_O, alpha);
           }
           tmem_wait_st();
         }
@@ -550,36 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++done;
       if (!ok) break;
       tc_fence_after();
-      const bool whole = s.slot < 0;
-      const float inv = !whole ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
-      const int g = row - node * p.G;
-      T* o_row = out + (((size_t)s.b * p.T + node) * p.H + (size_t)s.h * p.G + g) * D;
-      const size_t at = (size_t)(whole ? 0 : s.slot) * kTcRows + r;
-      float* part = p.part_o + at * D;
-      if (own && !whole) p.part_ml[at] = make_float2(m_used, l);
-      if (any_own) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(t_lane + C::COL_O + c, v);
-          tmem_wait_ld();
-          if (own && whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 w;
-              w.x = pack2<T>(__uint_as_float(v[e + 0]) * inv, __uint_as_float(v[e + 1]) * inv);
-              w.y = pack2<T>(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
-              w.z = pack2<T>(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
-              w.w = pack2<T>(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
-              *reinterpret_cast<uint4*>(o_row + c + e) = w;
-            }
-          } else if (own) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(part + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-          }
-        }
-      }
+      if (any_own) store_row<T, D>(p, s, t_lane + C::COL_O, own, row, node, m_used, l);
       tc_fence_before();
       mbar_arrive(&bars->o_free);
       gt += n;

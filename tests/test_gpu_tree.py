@@ -82,6 +82,20 @@ def test_many_query_tiles():
     parity(2, 150, 6, 2, 128, "bf16", [10, 260], 8, chain=True, rot=64)
 
 
+@pytest.mark.parametrize("d", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("rows", [129, 200, 256, 257, 400, 520])
+def test_rows_around_two_query_tiles(rows, d):
+    parity(2, rows, 2, 2, d, "bf16", [75, 0], rows + d, chain=True, page=32, lens=[rows, rows // 2], rot=d)
+
+
+def test_trees_of_two_query_tiles():
+    parity(2, 64, 8, 2, 128, "bf16", [700, 129], 70, page=64, rot=128, lens=[64, 33])
+    parity(3, 50, 24, 2, 96, "f16", [127, 0, 333], 71, page=16, softcap=3.0)
+    parity(1, 64, 8, 2, 192, "f16", [500], 72, rot=192, window=130, page=32)
+    parity(1, 61, 4, 1, 128, "bf16", [9001], 73, page=128, rot=128)
+    parity(2, 90, 4, 1, 64, "f16", [300, 40], 74, chain=True, window=50, softcap=200.0, page=16)
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 def test_pages(page):
     parity(3, 8, 8, 2, 128, "bf16", [5, 131, 517], page, page=page, rot=128)
