@@ -3,13 +3,16 @@
 //
 // pva_block_tables is all latency: a few words per sequence and eight bytes per
 // new token.  One CTA does the allocation (the stack is shared by all
-// sequences): checks, prefix sums of what is given back and taken, then the
-// blocks, a warp per sequence.  Slots are written by the same CTA while they
-// are few, and by a grid of their own where they are many.
+// sequences): a thread per sequence adds up what is given back and taken, then
+// a thread per block moves it, finding its sequence by bisection of the sums in
+// shared memory.  Slots are written by the same CTA while they are few, and by
+// a grid of their own where they are many.
 //
 // pva_kvcache_accept moves rows in place.  A path rises, path[i] >= i, so row i
 // is read (as some path[j], j <= i) before or when it is written if each thread
 // keeps to one 16-byte column and goes through i in order: no copy is needed.
+// A sequence's path and blocks are looked up once per CTA, which then moves the
+// columns of many heads and layers with eight rows in flight per thread.
 #include <limits.h>
 
 #include "pva_device.cuh"
@@ -24,6 +27,7 @@ constexpr int kBlockThreads = 1024;
 constexpr int kWordRefused = 18;  // status block: 1 while the last allocation was refused
 // New tokens up to which the allocating CTA writes the slot map itself.
 constexpr long long kSlotsInOne = 4096;
+constexpr int kOffsetsMax = 4096;  // sequences whose offsets a slot CTA keeps in shared memory
 
 struct BlockParams {
   const int32_t* lens;
@@ -43,133 +47,197 @@ __device__ __forceinline__ int blocks_for(int rows, int page) {
   return (int)(((long long)rows + page - 1) / page);
 }
 
-// Sum over the CTA of x, and of the threads before this one (exclusive).
-__device__ __forceinline__ long long block_scan(long long x, long long* sums, long long& all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long upto = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
+// The last index of start[0 .. n) that is <= x (entries ascend, start[0] <= x).
+template <typename I>
+__device__ __forceinline__ int last_at(const I* start, int n, I x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid - 1;
   }
-  if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  long long before = 0;
-  all = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-    const long long s = sums[w];
-    before += w < warp ? s : 0;
-    all += s;
-  }
-  __syncthreads();
-  return before + upto - x;
+  return lo;
 }
 
-// Slot of token t of sequence b.
-__device__ __forceinline__ int64_t slot_of(const BlockParams& p, int b, int t) {
-  const int row = p.lens[b] - (p.cu_new[b + 1] - t);
-  return (int64_t)p.table[(size_t)b * p.max_blocks + row / p.page] * p.page + row % p.page;
+// Sums over the CTA of two values, and over the threads before this one.
+__device__ __forceinline__ void block_scan(long long& x, long long& y, long long* sums,
+                                           long long& all_x, long long& all_y) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  long long ux = x, uy = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, ux, o), b = __shfl_up_sync(0xffffffffu, uy, o);
+    if (lane >= o) {
+      ux += a;
+      uy += b;
+    }
+  }
+  if (lane == 31) {
+    sums[warp] = ux;
+    sums[32 + warp] = uy;
+  }
+  __syncthreads();
+  // every warp sums the warps' sums, a lane per warp
+  long long sx = lane < warps ? sums[lane] : 0, sy = lane < warps ? sums[32 + lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, sx, o), b = __shfl_up_sync(0xffffffffu, sy, o);
+    if (lane >= o) {
+      sx += a;
+      sy += b;
+    }
+  }
+  all_x = __shfl_sync(0xffffffffu, sx, 31);
+  all_y = __shfl_sync(0xffffffffu, sy, 31);
+  const int w = warp > 0 ? warp - 1 : 0;
+  const long long bx = __shfl_sync(0xffffffffu, sx, w), by = __shfl_sync(0xffffffffu, sy, w);
+  x = ux - x + (warp > 0 ? bx : 0);
+  y = uy - y + (warp > 0 ? by : 0);
+  __syncthreads();
+}
+
+// Slot of token t of sequence b, whose new tokens end at `end`.
+__device__ __forceinline__ int64_t slot_of(const BlockParams& p, int b, int t, int end) {
+  const int row = p.lens[b] - (end - t), in = row / p.page;
+  return (int64_t)p.table[(size_t)b * p.max_blocks + in] * p.page + (row - in * p.page);
 }
 
 __global__ void __launch_bounds__(kBlockThreads) pva_block_alloc_kernel(BlockParams p) {
-  allow_next_grid();
-  wait_prior_grid();
-  __shared__ long long s_sums[32];
+  __shared__ long long s_sums[64];
   __shared__ int s_bad;
-  const int tid = threadIdx.x;
+  // of the sequences of one round: blocks moved before each, the first column
+  // moved, and the offsets of the new tokens
+  __shared__ long long s_given[kBlockThreads], s_taken[kBlockThreads];
+  __shared__ int s_from[kBlockThreads];
+  allow_next_grid();
+  const int tid = threadIdx.x, threads = blockDim.x;
   if (tid == 0) s_bad = 0;
   __syncthreads();
+  wait_prior_grid();
   const int count = *p.free_count;
+  const int rounds = (p.B + threads - 1) / threads;
+  // Totals first: the step is refused as a whole.
+  long long all_given = 0, all_taken = 0;
+  long long given = 0, taken = 0;  // of this thread's sequence, in the last round
+  int held = 0, need = 0;
   bool bad = count < 0 || count > p.pool;
-  long long given = 0, taken = 0;
-  for (int b = tid; b < p.B; b += kBlockThreads) {
-    const int len = p.lens[b], held = p.held[b];
-    if (len < 0 || held < 0 || held > p.max_blocks || blocks_for(len, p.page) > p.max_blocks) {
-      bad = true;
-      continue;
+  for (int r = 0; r < rounds; ++r) {
+    const int b = r * threads + tid;
+    given = taken = 0;
+    held = need = 0;
+    if (b < p.B) {
+      const int len = p.lens[b];
+      held = p.held[b];
+      if (p.cu_new) {
+        const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1];
+        bad = bad || (b == 0 && c0 != 0) || c1 < c0 || (long long)c1 - c0 > len ||
+              (b == p.B - 1 && c1 > p.n_slots);
+      }
+      need = blocks_for(len, p.page);
+      if (len < 0 || held < 0 || held > p.max_blocks || need > p.max_blocks) {
+        bad = true;
+        held = need = 0;
+      }
+      given = max(0, held - need);
+      taken = max(0, need - held);
     }
-    const int more = blocks_for(len, p.page) - held;
-    if (more > 0) taken += more; else given -= more;
-    if (p.cu_new) {
-      const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1];
-      bad = bad || (b == 0 && c0 != 0) || c1 < c0 || (long long)c1 - c0 > len ||
-            (b == p.B - 1 && c1 > p.n_slots);
-    }
+    long long x = given, y = taken, all_x, all_y;
+    if (bad) s_bad = 1;
+    block_scan(x, y, s_sums, all_x, all_y);
+    all_given += all_x;
+    all_taken += all_y;
+    given = x;
+    taken = y;
   }
-  if (bad) s_bad = 1;
-  long long all_given, all_taken;
-  block_scan(given, s_sums, all_given);
-  block_scan(taken, s_sums, all_taken);
   const bool refuse = s_bad || count + all_given > p.pool || all_taken > count + all_given;
   if (tid == 0 && !p.in_one) p.status[kWordRefused] = refuse ? 1u : 0u;
   if (refuse) {
     if (tid == 0) atomicOr(p.status, PVA_DEV_BLOCKS);
     return;
   }
-  const int lane = tid & 31, warp = tid >> 5;
   const long long top = count + all_given - 1;
-  // Two passes, given back first: both need the sequences' places on the
-  // stack, found a thread per sequence, and move blocks, a warp per sequence.
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int pass = 0; pass < 2; ++pass) {  // all is given back before any is taken
     if ((pass == 0 ? all_given : all_taken) == 0) continue;
-    long long carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kBlockThreads) {
-      const int b = b0 + tid;
-      int held = 0, need = 0;
-      if (b < p.B) {
-        held = p.held[b];
-        need = blocks_for(p.lens[b], p.page);
+    long long before = 0;
+    for (int r = 0; r < rounds; ++r) {
+      long long moved;
+      if (rounds == 1) {
+        moved = pass == 0 ? all_given : all_taken;
+      } else {
+        const int b = r * threads + tid;
+        held = b < p.B ? p.held[b] : 0;
+        need = b < p.B ? blocks_for(p.lens[b], p.page) : 0;
+        given = max(0, held - need);
+        taken = max(0, need - held);
+        long long x, y;
+        block_scan(given, taken, s_sums, x, y);
+        moved = pass == 0 ? x : y;
       }
-      const int n = pass == 0 ? max(0, held - need) : max(0, need - held);
-      long long all;
-      long long at = carry + block_scan(n, s_sums, all);
-      carry += all;
-      // the warp goes through its 32 sequences together
-      for (unsigned todo = __ballot_sync(0xffffffffu, n > 0); todo; todo &= todo - 1) {
-        const int src = __ffs(todo) - 1;
-        const int nn = __shfl_sync(0xffffffffu, n, src);
-        const int from = __shfl_sync(0xffffffffu, min(held, need), src);
-        const long long first = top - __shfl_sync(0xffffffffu, at, src);
-        int32_t* row = p.table + (size_t)(b0 + warp * 32 + src) * p.max_blocks + from;
-        for (int i = lane; i < nn; i += 32) {
-          if (pass == 0) {
-            p.free_blocks[first - i] = row[i];
-            row[i] = -1;
-          } else {
-            row[i] = p.free_blocks[first - i];
-          }
+      long long* start = pass == 0 ? s_given : s_taken;
+      start[tid] = pass == 0 ? given : taken;
+      s_from[tid] = min(held, need);
+      __syncthreads();
+      for (long long e = tid; e < moved; e += threads) {
+        const int i = last_at(start, threads, e);
+        int32_t* entry = p.table + (size_t)(r * threads + i) * p.max_blocks + s_from[i] + (e - start[i]);
+        int32_t* place = p.free_blocks + (top - before - e);
+        if (pass == 0) {
+          *place = *entry;
+          *entry = -1;
+        } else {
+          *entry = *place;
         }
       }
+      before += moved;
+      __syncthreads();
     }
-    __syncthreads();
   }
-  for (int b = tid; b < p.B; b += kBlockThreads) p.held[b] = blocks_for(p.lens[b], p.page);
+  if (rounds == 1) {
+    if (tid < p.B) p.held[tid] = need;
+  } else {
+    for (int b = tid; b < p.B; b += threads) p.held[b] = blocks_for(p.lens[b], p.page);
+  }
   if (tid == 0) *p.free_count = (int)(count + all_given - all_taken);
   if (!p.in_one || !p.cu_new) return;
-  __syncthreads();
-  for (int b = warp; b < p.B; b += kBlockThreads / 32)
-    for (int t = p.cu_new[b] + lane; t < p.cu_new[b + 1]; t += 32) p.slots[t] = slot_of(p, b, t);
-  for (long long t = p.cu_new[p.B] + tid; t < p.n_slots; t += kBlockThreads) p.slots[t] = -1;
+  if (rounds == 1) {
+    // offsets to shared memory; sequences behind the last start at the end
+    const int end = p.cu_new[p.B];
+    s_from[tid] = tid < p.B ? p.cu_new[tid] : end + 1;
+    __syncthreads();
+    for (int t = tid; t < p.n_slots; t += threads) {
+      const int b = last_at(s_from, threads, t);
+      p.slots[t] = t >= end ? -1 : slot_of(p, b, t, b + 1 < p.B ? s_from[b + 1] : end);
+    }
+  } else {
+    const int end = p.cu_new[p.B];
+    for (int t = tid; t < p.n_slots; t += threads) {
+      const int b = t < end ? last_at(p.cu_new, p.B, t) : 0;
+      p.slots[t] = t >= end ? -1 : slot_of(p, b, t, p.cu_new[b + 1]);
+    }
+  }
 }
 
-// A thread per token; the sequence by bisection of the offsets.
+// A thread per token; the sequence by bisection of the offsets, from shared
+// memory where they fit.
 __global__ void __launch_bounds__(256) pva_block_slots_kernel(BlockParams p) {
+  __shared__ int s_cu[kOffsetsMax + 1];
   allow_next_grid();
   wait_prior_grid();
   if (p.status[kWordRefused]) return;
-  const int end = p.cu_new[p.B];
+  const bool fits = p.B <= kOffsetsMax;
+  if (fits) {
+    for (int b = threadIdx.x; b <= p.B; b += blockDim.x) s_cu[b] = p.cu_new[b];
+    __syncthreads();
+  }
+  const int* cu = fits ? s_cu : p.cu_new;
+  const int end = cu[p.B];
   for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < p.n_slots;
        t += (long long)gridDim.x * blockDim.x) {
     if (t >= end) {
       p.slots[t] = -1;
       continue;
     }
-    int lo = 0, hi = p.B - 1;  // the last b with cu_new[b] <= t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.cu_new[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    p.slots[t] = slot_of(p, lo, (int)t);
+    const int b = last_at(cu, p.B, (int)t);
+    p.slots[t] = slot_of(p, b, (int)t, cu[b + 1]);
   }
 }
 
@@ -187,14 +255,17 @@ struct AcceptParams {
   uint32_t* status;
 };
 
-// One CTA per (kv head, layer, sequence): threads are (K or V, column of 16,
-// 4 or 2 bytes), each walking down the path.
+constexpr int kAcceptThreads = 128, kPathRows = 128, kAcceptAhead = 8;
+
+// CTA (c, b): a share of the columns (layer, K or V, kv head, unit U of a row) of
+// sequence b.  The path is taken kPathRows nodes at a time; a column's thread is
+// the same throughout, which is what makes the move in place safe.
 template <typename U>
-__global__ void __launch_bounds__(128) pva_accept_kernel(AcceptParams p) {
+__global__ void __launch_bounds__(kAcceptThreads) pva_accept_kernel(AcceptParams p) {
+  __shared__ long long s_from[kPathRows], s_to[kPathRows];  // rows of head 0; from -1: stays
   allow_next_grid();
   wait_prior_grid();
-  constexpr int kAhead = 8;
-  const int b = blockIdx.z, layer = blockIdx.y, h = blockIdx.x;
+  const int b = blockIdx.y, tid = threadIdx.x;
   const int past = p.past[b], n = p.path_lens[b];
   const int32_t* path = p.path + (size_t)b * p.width;
   const int32_t* table = p.table ? p.table + (size_t)b * p.max_blocks : nullptr;
@@ -202,18 +273,29 @@ __global__ void __launch_bounds__(128) pva_accept_kernel(AcceptParams p) {
   const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
   bool bad_path = past < 0 || n < 0 || n > p.width, bad_block = false;
   const long long rows = (long long)p.max_blocks * p.page;
-  for (int i = threadIdx.x; i < n && !bad_path; i += blockDim.x) {
-    const int x = path[i];
-    if (x < 0 || (i > 0 && path[i - 1] >= x) || past + (long long)x >= rows) {
-      bad_path = true;
-    } else if (table) {
-      const int to = table[(past + i) / p.page], from = table[(past + x) / p.page];
-      bad_block = bad_block || to < 0 || to >= p.n_blocks || from < 0 || from >= p.n_blocks;
+  auto place = [&](int row, bool& bad) {
+    const int in = row / p.page;
+    const int block = table ? table[in] : b;
+    bad = bad || block < 0 || block >= p.n_blocks;
+    return (long long)block * p.Hkv * p.page + (row - in * p.page);
+  };
+  auto look_up = [&](int i0) {
+    const int i = i0 + tid;
+    if (i < n && !bad_path) {
+      const int x = path[i];
+      if (x < 0 || (i > 0 && path[i - 1] >= x) || past + (long long)x >= rows) {
+        bad_path = true;
+      } else {
+        s_to[tid] = place(past + i, bad_block);
+        const long long from = place(past + x, bad_block);
+        s_from[tid] = x == i ? -1 : from;
+      }
     }
-  }
+  };
+  for (int i0 = 0; i0 < n && !bad_path; i0 += kPathRows) look_up(i0);
   const bool wrong_path = __syncthreads_or(bad_path);
   const bool wrong = __syncthreads_or(bad_block) || wrong_path;
-  const bool first = layer == 0 && h == 0 && threadIdx.x == 0;
+  const bool first = blockIdx.x == 0 && tid == 0;
   if (latched || wrong) {
     if (first) {
       p.new_lens[b] = past;
@@ -222,24 +304,34 @@ __global__ void __launch_bounds__(128) pva_accept_kernel(AcceptParams p) {
     return;
   }
   if (first) p.new_lens[b] = past + n;
-  const int columns = p.row_bytes / (int)sizeof(U);
-  auto at = [&](uint8_t* base, int row) {
-    const int in = row / p.page;
-    const long long block = table ? table[in] : b;
-    return reinterpret_cast<U*>(base + ((block * p.Hkv + h) * p.page + (row - in * p.page)) *
-                                           (long long)p.row_bytes);
-  };
-  for (int c = threadIdx.x; c < 2 * columns; c += blockDim.x) {
-    uint8_t* base = (c < columns ? p.k : p.v) + layer * p.layer_bytes;
-    const int col = c < columns ? c : c - columns;
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-      U x[kAhead];
+  const int units = p.row_bytes / (int)sizeof(U);
+  const long long columns = 2LL * p.layers * p.Hkv * units;
+  for (int i0 = 0; i0 < n; i0 += kPathRows) {
+    if (n > kPathRows) {
+      __syncthreads();
+      look_up(i0);
+      __syncthreads();
+    }
+    const int m = min(n - i0, kPathRows);
+    for (long long c = (long long)blockIdx.x * kAcceptThreads + tid; c < columns;
+         c += (long long)gridDim.x * kAcceptThreads) {
+      const int unit = (int)(c % units);
+      const long long rest = c / units;
+      const int h = (int)(rest % p.Hkv);
+      const long long layer = rest / p.Hkv >> 1;
+      uint8_t* base = ((rest / p.Hkv) & 1 ? p.v : p.k) + layer * p.layer_bytes +
+                      (long long)h * p.page * p.row_bytes + (long long)unit * sizeof(U);
+      for (int j = 0; j < m; j += kAcceptAhead) {
+        U x[kAcceptAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (i0 + i < n) x[i] = at(base, past + path[i0 + i])[col];
+        for (int i = 0; i < kAcceptAhead; ++i)
+          if (j + i < m && s_from[j + i] >= 0)
+            x[i] = *reinterpret_cast<const U*>(base + s_from[j + i] * p.row_bytes);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (i0 + i < n && path[i0 + i] != i0 + i) at(base, past + i0 + i)[col] = x[i];
+        for (int i = 0; i < kAcceptAhead; ++i)
+          if (j + i < m && s_from[j + i] >= 0)
+            *reinterpret_cast<U*>(base + s_to[j + i] * p.row_bytes) = x[i];
+      }
     }
   }
 }
@@ -266,8 +358,9 @@ extern "C" int pva_block_tables(const int32_t* lens, int32_t* block_table, int32
     if (rc != PVA_OK) return rc;
     BlockParams p{lens, block_table, held, free_blocks, free_count, cu_new, slot_map, B,
                   max_blocks, page_size, pool, n_slots, n_slots <= kSlotsInOne ? 1 : 0, c.status};
-    cudaError_t e = launch_dependent(pva_block_alloc_kernel, dim3(1), dim3(kBlockThreads), 0,
-                                     stream, p);
+    // few sequences: fewer warps to wait for
+    const int threads = B <= 128 ? 256 : kBlockThreads;
+    cudaError_t e = launch_dependent(pva_block_alloc_kernel, dim3(1), dim3(threads), 0, stream, p);
     if (e == cudaSuccess && cu_new && !p.in_one) {
       const long long want = (n_slots + 255) / 256, most = (long long)c.num_sms * 8;
       e = launch_dependent(pva_block_slots_kernel, dim3((unsigned)(want < most ? want : most)),
@@ -296,8 +389,7 @@ extern "C" int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* p
                   block_table ? "max_blocks must be >= 1"
                               : "without a block table the cache has one block a sequence");
     if (!block_table) max_blocks = 1;
-    if (B > 65535 || layers > 65535)
-      return fail(PVA_ERR_UNSUPPORTED, "at most 65535 sequences and layers");
+    if (B > 65535) return fail(PVA_ERR_UNSUPPORTED, "at most 65535 sequences");
     if ((long long)max_blocks * page_size > INT_MAX)
       return fail(PVA_ERR_INVALID_ARG, "cache extents do not fit in int32");
     const long long size = dtype == PVA_F32 ? 4 : 2;
@@ -333,12 +425,16 @@ extern "C" int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* p
     const int rc = acquire(stream, 0, &c);
     if (rc != PVA_OK) return rc;
     p.status = c.status;
-    const dim3 grid(kv_num_heads, layers, B);
+    // as many CTAs a sequence as it has columns for, up to about 16 per SM in all
+    const int unit = mis % 16 == 0 ? 16 : mis % 4 == 0 ? 4 : 2;
+    const long long columns = 2LL * layers * kv_num_heads * (p.row_bytes / unit);
+    const long long want = (columns + kAcceptThreads - 1) / kAcceptThreads;
+    const long long most = (16LL * c.num_sms + B - 1) / B;
+    const dim3 grid((unsigned)(want < most ? want : most), B), block(kAcceptThreads);
     const cudaError_t e =
-        mis % 16 == 0 ? launch_dependent(pva_accept_kernel<uint4>, grid, dim3(128), 0, stream, p)
-        : mis % 4 == 0
-            ? launch_dependent(pva_accept_kernel<uint32_t>, grid, dim3(128), 0, stream, p)
-            : launch_dependent(pva_accept_kernel<uint16_t>, grid, dim3(128), 0, stream, p);
+        unit == 16  ? launch_dependent(pva_accept_kernel<uint4>, grid, block, 0, stream, p)
+        : unit == 4 ? launch_dependent(pva_accept_kernel<uint32_t>, grid, block, 0, stream, p)
+                    : launch_dependent(pva_accept_kernel<uint16_t>, grid, block, 0, stream, p);
     return e == cudaSuccess ? PVA_OK : cuda_fail(e, "accept launch");
   });
 }

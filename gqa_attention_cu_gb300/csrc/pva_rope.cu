@@ -24,24 +24,21 @@ using namespace pva::host;
 namespace pva {
 namespace {
 
-// One token per CTA at a time.
 template <typename T, int VEC, bool TREE>
-__global__ void __launch_bounds__(kRopeThreads) pva_rope_kernel(RopeStep s) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) pva_rope_kernel(RopeStep s) {
+  __shared__ RopeToken sh[2];
   allow_next_grid();
   wait_prior_grid();
   if (TREE && s.hdr[0] == 0) return;
-  const uint32_t axes = rope_axes<VEC>(s, threadIdx.x);
-  for (int tok = blockIdx.x; tok < s.tokens; tok += gridDim.x) {
-    const int depth = TREE && s.depth ? s.depth[tok] : TREE ? tok % s.T : 0;
-    rope_token<T, VEC, TREE>(s, tok, threadIdx.x, axes, depth);
-  }
+  rope_tokens<T, VEC, TREE>(s, blockIdx.x, gridDim.x, threadIdx.x, 0, sh,
+                            [&](int tok) { return s.depth ? s.depth[tok] : tok % s.T; });
 }
 
 template <typename T>
 cudaError_t launch_rope_type(const RopeStep& s, bool tree, int num_sms, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(T);
   const bool wide = rope_wide(s, VEC);
-  const int most = num_sms * 16;  // CTAs of 128 threads an SM holds
+  const int most = num_sms * kRopeCtas;
   const dim3 grid(s.tokens < most ? s.tokens : most);
   if (wide)
     return tree ? launch_dependent(pva_rope_kernel<T, VEC, true>, grid, dim3(kRopeThreads), 0, st, s)
@@ -126,7 +123,8 @@ extern "C" int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_
   return guarded([&]() -> int {
     if (dtype != PVA_F32 && dtype != PVA_F16 && dtype != PVA_BF16)
       return fail(PVA_ERR_INVALID_ARG, "dtype must be 0 (f32), 1 (f16) or 2 (bf16)");
-    if (tokens < 0) return fail(PVA_ERR_INVALID_ARG, "tokens must be >= 0");
+    if (tokens < 0 || tokens > INT_MAX - 65536)
+      return fail(PVA_ERR_INVALID_ARG, "tokens must be >= 0 and fit in int32");
     if (tokens == 0) return PVA_OK;
     if (!q && !k) return fail(PVA_ERR_INVALID_ARG, "q or k is needed");
     if ((q && num_heads < 1) || (k && kv_num_heads < 1))

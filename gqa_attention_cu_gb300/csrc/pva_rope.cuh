@@ -77,7 +77,8 @@ struct RopeStep {
 };
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeRows = 4;  // head rows a thread has in flight
+constexpr int kRopeCtas = 8;  // CTAs an SM holds
+constexpr int kRopeRows = 2;  // head rows a thread has in flight
 
 template <typename T>
 __device__ __forceinline__ float load_f(T x) { return static_cast<float>(x); }
@@ -126,29 +127,28 @@ __device__ __forceinline__ void join_pairs(Pack<T, VEC>& x, Pack<T, VEC>& y) {
   y = b;
 }
 
-// Axes of the VEC pairs that thread tid turns, two bits each.
-template <int VEC>
-__device__ __forceinline__ uint32_t rope_axes(const RopeStep& s, int tid) {
-  uint32_t axes = 0;
-  if (s.rt.n_axes == 1) return 0;
-  const int u = tid % (s.d / (2 * VEC));
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) axes |= (uint32_t)axis_of_pair(s.rt, u * VEC + e) << (2 * e);
-  return axes;
-}
+// cos and sin of a token's pairs, and whether a position is off the tables.
+struct RopeToken {
+  float2 cs[128];
+  int bad[kMaxAxes];
+};
 
-// Does token tok (tid: one of kRopeThreads threads).  VEC pairs of a head row
-// per thread: 16-byte accesses where sizes and alignment allow (VEC = 16 /
-// sizeof(T)), single elements otherwise.
-template <typename T, int VEC, bool TREE>
-__device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, uint32_t axes,
-                                           int depth) {
+// Does the tokens first, first + stride, ... (tid: one of kRopeThreads threads,
+// which share `sh` and the named barrier `bar`).  VEC pairs of a head row per
+// thread: 16-byte accesses where sizes and alignment allow (VEC = 16 /
+// sizeof(T)), single elements otherwise.  depth_of(tok): a tree node's depth.
+//
+// A token's table entries are fetched once, a pair per thread, into shared
+// memory, and one token ahead: while the rows of token i are turned, the
+// positions of token i + 2 and the entries of token i + 1 are on their way.
+template <typename T, int VEC, bool TREE, typename Depth>
+__device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int stride, int tid,
+                                            int bar, RopeToken (&sh)[2], Depth depth_of) {
   using P = Pack<T, VEC>;
   const RopeTable& rt = s.rt;
   const int half = rt.rot / 2;
   const int units = s.d / (2 * VEC);  // of 2 * VEC dims
   const int u = tid % units, r0 = tid / units, step = kRopeThreads / units;
-  const bool idle = r0 >= step;
   const bool turned = u * VEC < half;
   // the unit's two packs of dims: d0 .. d0 + VEC and d1 .. d1 + VEC
   int d0, d1;
@@ -163,7 +163,7 @@ __device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, 
     d1 = d0 + half;
   }
   const int nq = s.q ? s.H : 0, nk = s.k ? s.Hkv : 0, nv = s.v ? s.Hkv : 0;
-  const int n_rows = nq + nk + nv;
+  const int n_rows = r0 < step ? nq + nk + nv : 0;
   const T* q = static_cast<const T*>(s.q);
   const T* k = static_cast<const T*>(s.k);
   const T* v = static_cast<const T*>(s.v);
@@ -172,11 +172,50 @@ __device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, 
   T* k_cache = static_cast<T*>(s.k_cache);
   T* v_cache = static_cast<T*>(s.v_cache);
   const int G = TREE ? s.H / s.Hkv : 1;
+  const int axis = tid < half ? axis_of_pair(rt, tid) : 0;  // of the pair this thread fetches
 
-  // The first rows are on their way while the position, the tables' entries
-  // and the slot are looked up, one after the other.
+  struct Info {
+    int64_t at, check;  // position on this thread's axis, and of axis tid
+    int64_t slot;
+  };
+  auto fetch_info = [&](int tok) {
+    Info f{0, 0, -1};
+    if (tok >= s.tokens) return f;
+    if (TREE) {
+      const int b = tok / s.T, node = tok - b * s.T;
+      const int row = s.past[b] + node;
+      if (node < (s.lens ? s.lens[b] : s.T)) {
+        const int in = row / s.page;
+        const int block = s.table ? s.table[(size_t)b * s.max_blocks + in] : b;
+        f.slot = (int64_t)block * s.page + (row - in * s.page);
+        if (half) f.at = s.pos ? s.pos[(size_t)axis * s.tokens + tok] : (int64_t)s.past[b] + depth_of(tok);
+      }
+    } else {
+      f.at = s.pos[(size_t)axis * s.tokens + tok];
+      if (tid < rt.n_axes) f.check = s.pos[(size_t)tid * s.tokens + tok];
+      if (k_cache) f.slot = s.slots[tok];
+    }
+    return f;
+  };
+  // a pair per thread: half <= 128 = kRopeThreads
+  auto fetch_entry = [&](const Info& f) {
+    float2 e = make_float2(1.0f, 0.0f);
+    if (tid < half && f.at >= 0 && f.at < rt.rows) {
+      const int64_t i = f.at * half + tid;
+      e.x = table_at(rt.cos, i, rt.is_f16);
+      e.y = table_at(rt.sin, i, rt.is_f16);
+      if (rt.inverse) e.y = -e.y;
+    }
+    return e;
+  };
+  auto share = [&](RopeToken& t, float2 e, const Info& f) {
+    if (tid < half) t.cs[tid] = e;
+    if (!TREE && tid < kMaxAxes) t.bad[tid] = f.check < 0 || f.check >= rt.rows;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kRopeThreads) : "memory");
+  };
+
   P x0[kRopeRows], x1[kRopeRows];
-  auto load_rows = [&](int r) {
+  auto load_rows = [&](int tok, int r) {
 #pragma unroll
     for (int y = 0; y < kRopeRows; ++y) {
       const int row = r + y * step;
@@ -188,110 +227,96 @@ __device__ __forceinline__ void rope_token(const RopeStep& s, int tok, int tid, 
       x1[y] = *reinterpret_cast<const P*>(src + d1);
     }
   };
-  if (!idle) load_rows(r0);
-  int b = 0, node = tok;
-  long long slot = -1;
-  long long at[kMaxAxes];
-  if (TREE) {
-    b = tok / s.T;
-    node = tok - b * s.T;
-    if (node >= (s.lens ? s.lens[b] : s.T)) {  // an unused node: zeros out
-      P z;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) z.v[e] = round_to<T>(0.0f);
-      P* o = reinterpret_cast<P*>(static_cast<T*>(s.out) + (size_t)tok * s.H * s.d);
-      for (int e = tid; e < s.H * s.d / VEC; e += kRopeThreads) o[e] = z;
-      return;
-    }
-    const int row = s.past[b] + node;
-    const int in_table = row / s.page;
-    const int block = s.table ? s.table[(size_t)b * s.max_blocks + in_table] : b;
-    slot = (long long)block * s.page + (row - in_table * s.page);
-#pragma unroll
-    for (int a = 0; a < kMaxAxes; ++a)
-      at[a] = !s.pos ? (long long)s.past[b] + depth
-                     : a < rt.n_axes ? s.pos[(size_t)a * s.tokens + tok] : 0;
-  } else {
-    bool bad = false;
-#pragma unroll
-    for (int a = 0; a < kMaxAxes; ++a) {
-      at[a] = a < rt.n_axes ? s.pos[(size_t)a * s.tokens + tok] : 0;
-      bad = bad || at[a] < 0 || at[a] >= rt.rows;
-    }
-    if (k_cache) {
-      slot = s.slots[tok];
-      bad = bad || slot < -1 || slot >= s.n_slots;
-    }
-    if (bad) {  // the token is left out, and the caller told
-      if (tid == 0) atomicOr(s.status, PVA_DEV_ROPE);
-      return;
-    }
+
+  if (first >= s.tokens) return;
+  Info now = fetch_info(first), next = fetch_info(first + stride);
+  {
+    const float2 e = fetch_entry(now);
+    share(sh[0], e, now);
   }
-  float c[VEC], n[VEC];
-  if (turned) {
+  int buf = 0;
+  for (int tok = first; tok < s.tokens; tok += stride, buf ^= 1) {
+    load_rows(tok, r0);
+    const Info after = fetch_info(tok + 2 * stride);
+    const float2 entry = fetch_entry(next);
+    bool write = true;
+    int b = 0, node = tok;
+    if (TREE) {
+      b = tok / s.T;
+      node = tok - b * s.T;
+      if (now.slot < 0) {  // an unused node: zeros out
+        write = false;
+        P z;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int p = u * VEC + e, a = (axes >> (2 * e)) & 3;
-      long long x = at[0];
-#pragma unroll
-      for (int y = 1; y < kMaxAxes; ++y) x = a == y ? at[y] : x;
-      const long long i = x * half + p;
-      c[e] = table_at(rt.cos, i, rt.is_f16);
-      n[e] = table_at(rt.sin, i, rt.is_f16);
-      if (rt.inverse) n[e] = -n[e];
-    }
-  }
-  long long cached = -1;
-  size_t cache_row = 0;
-  if (slot >= 0) {
-    cached = s.n_slots >> 32 ? slot / s.page : (uint32_t)slot / (uint32_t)s.page;
-    cache_row = (size_t)(slot - cached * s.page);
-  }
-  if (idle) return;
-  for (int r = r0; r < n_rows; r += step * kRopeRows) {
-    if (r != r0) load_rows(r);
-#pragma unroll
-    for (int y = 0; y < kRopeRows; ++y) {
-      const int row = r + y * step;
-      if (row >= n_rows) continue;
-      const bool is_q = row < nq, is_v = row >= nq + nk;
-      if (turned && !is_v) {
-        if (rt.interleaved) split_pairs(x0[y], x1[y]);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float a = load_f(x0[y].v[e]), f = load_f(x1[y].v[e]);
-          x0[y].v[e] = round_to<T>(__fsub_rn(__fmul_rn(c[e], a), __fmul_rn(n[e], f)));
-          x1[y].v[e] = round_to<T>(__fadd_rn(__fmul_rn(n[e], a), __fmul_rn(c[e], f)));
-        }
-        if (rt.interleaved) join_pairs(x0[y], x1[y]);
+        for (int e = 0; e < VEC; ++e) z.v[e] = round_to<T>(0.0f);
+        P* o = reinterpret_cast<P*>(static_cast<T*>(s.out) + (size_t)tok * s.H * s.d);
+        for (int e = tid; e < s.H * s.d / VEC; e += kRopeThreads) o[e] = z;
       }
-      if (is_q) {
-        if (TREE && s.negate_q) {
+    } else {
+      const int4 bad = *reinterpret_cast<const int4*>(sh[buf].bad);
+      if (bad.x | bad.y | bad.z | bad.w || now.slot < -1 || now.slot >= (k_cache ? s.n_slots : 0)) {
+        // the token is left out, and the caller told
+        write = false;
+        if (tid == 0) atomicOr(s.status, PVA_DEV_ROPE);
+      }
+    }
+    if (write) {
+      int64_t cached = -1;
+      size_t cache_row = 0;
+      if (now.slot >= 0) {
+        cached = s.n_slots >> 32 ? now.slot / s.page : (uint32_t)now.slot / (uint32_t)s.page;
+        cache_row = (size_t)(now.slot - cached * s.page);
+      }
+      for (int r = r0; r < n_rows; r += step * kRopeRows) {
+        if (r != r0) load_rows(tok, r);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            x0[y].v[e] = -x0[y].v[e];
-            x1[y].v[e] = -x1[y].v[e];
+        for (int y = 0; y < kRopeRows; ++y) {
+          const int row = r + y * step;
+          if (row >= n_rows) continue;
+          const bool is_q = row < nq, is_v = row >= nq + nk;
+          if (turned && !is_v) {
+            if (rt.interleaved) split_pairs(x0[y], x1[y]);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              const float2 cs = sh[buf].cs[u * VEC + e];
+              const float a = load_f(x0[y].v[e]), f = load_f(x1[y].v[e]);
+              x0[y].v[e] = round_to<T>(__fsub_rn(__fmul_rn(cs.x, a), __fmul_rn(cs.y, f)));
+              x1[y].v[e] = round_to<T>(__fadd_rn(__fmul_rn(cs.y, a), __fmul_rn(cs.x, f)));
+            }
+            if (rt.interleaved) join_pairs(x0[y], x1[y]);
+          }
+          if (is_q) {
+            if (TREE && s.negate_q) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                x0[y].v[e] = -x0[y].v[e];
+                x1[y].v[e] = -x1[y].v[e];
+              }
+            }
+            T* dst = TREE ? q_out + ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d
+                          : q_out + (size_t)tok * s.q_out_stride + (size_t)row * s.d;
+            *reinterpret_cast<P*>(dst + d0) = x0[y];
+            *reinterpret_cast<P*>(dst + d1) = x1[y];
+            continue;
+          }
+          const int h = is_v ? row - nq - nk : row - nq;
+          if (k_out && !is_v) {
+            T* dst = k_out + (size_t)tok * s.k_out_stride + (size_t)h * s.d;
+            *reinterpret_cast<P*>(dst + d0) = x0[y];
+            *reinterpret_cast<P*>(dst + d1) = x1[y];
+          }
+          if (cached >= 0) {
+            T* dst = (is_v ? v_cache : k_cache) +
+                     (((size_t)cached * s.Hkv + h) * s.page + cache_row) * s.d;
+            *reinterpret_cast<P*>(dst + d0) = x0[y];
+            *reinterpret_cast<P*>(dst + d1) = x1[y];
           }
         }
-        T* dst = TREE ? q_out + ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d
-                      : q_out + (size_t)tok * s.q_out_stride + (size_t)row * s.d;
-        *reinterpret_cast<P*>(dst + d0) = x0[y];
-        *reinterpret_cast<P*>(dst + d1) = x1[y];
-        continue;
-      }
-      const int h = is_v ? row - nq - nk : row - nq;
-      if (k_out && !is_v) {
-        T* dst = k_out + (size_t)tok * s.k_out_stride + (size_t)h * s.d;
-        *reinterpret_cast<P*>(dst + d0) = x0[y];
-        *reinterpret_cast<P*>(dst + d1) = x1[y];
-      }
-      if (cached >= 0) {
-        T* dst = (is_v ? v_cache : k_cache) +
-                 (((size_t)cached * s.Hkv + h) * s.page + cache_row) * s.d;
-        *reinterpret_cast<P*>(dst + d0) = x0[y];
-        *reinterpret_cast<P*>(dst + d1) = x1[y];
       }
     }
+    if (tok + stride < s.tokens) share(sh[buf ^ 1], entry, next);
+    now = next;
+    next = after;
   }
 }
 

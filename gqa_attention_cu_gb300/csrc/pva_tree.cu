@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_small_front_kernel(Tre
                                                                              RopeStep r) {
   allow_next_grid();
   wait_prior_grid();
-  constexpr int kWarps = kFrontThreads / 32;
+  constexpr int kWarps = kFrontThreads / 32, kAtOnce = kFrontThreads / kRopeThreads;
+  __shared__ RopeToken s_rope[kAtOnce][2];
   __shared__ int s_parent[kWarps][kSmallT];
   __shared__ int s_depth[kSmallNodes];
   __shared__ long long s_tiles[kSmallB];
@@ -250,12 +251,10 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_small_front_kernel(Tre
     if (tid == 0) front_publish(p, all, bad, latched);
   }
   if (bad || latched) return;
-  constexpr int kAtOnce = kFrontThreads / kRopeThreads;
-  const uint32_t axes = rope_axes<VEC>(r, tid % kRopeThreads);
-  for (int tok = blockIdx.x * kAtOnce + tid / kRopeThreads; tok < r.tokens;
-       tok += gridDim.x * kAtOnce)
-    rope_token<T, VEC, true>(r, tok, tid % kRopeThreads, axes,
-                             p.parents ? s_depth[tok] : tok % p.T);
+  const int group = tid / kRopeThreads;
+  rope_tokens<T, VEC, true>(r, blockIdx.x * kAtOnce + group, gridDim.x * kAtOnce,
+                            tid % kRopeThreads, 1 + group, s_rope[group],
+                            [&](int tok) { return p.parents ? s_depth[tok] : tok % p.T; });
 }
 
 // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over an item's parts c, in
@@ -552,7 +551,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
       return fail(PVA_ERR_INVALID_ARG, "without a block table the cache has one block a sequence");
     max_blocks = 1;
   }
-  if ((long long)B * T > INT_MAX || (long long)T * G > INT_MAX / 2 ||
+  if ((long long)B * T > INT_MAX - 65536 || (long long)T * G > INT_MAX / 2 ||
       (long long)max_blocks * page_size > INT_MAX - 65536 ||
       (long long)n_blocks * Hkv > INT_MAX)
     return fail(PVA_ERR_INVALID_ARG, "cache or token extents do not fit in int32");
