@@ -29,9 +29,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) pva_rope_kernel(RopeS
   __shared__ RopeToken sh[2];
   allow_next_grid();
   wait_prior_grid();
-  if (TREE && s.hdr[0] == 0) return;
   rope_tokens<T, VEC, TREE>(s, blockIdx.x, gridDim.x, threadIdx.x, 0, sh,
-                            [&](int tok) { return s.depth ? s.depth[tok] : tok % s.T; });
+                            [&](int tok) { return s.depth ? s.depth[tok] : tok % s.T; },
+                            [&]() { return !TREE || s.hdr[0] != 0; });
 }
 
 template <typename T>

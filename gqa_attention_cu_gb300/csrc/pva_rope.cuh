@@ -141,9 +141,10 @@ struct RopeToken {
 // A token's table entries are fetched once, a pair per thread, into shared
 // memory, and one token ahead: while the rows of token i are turned, the
 // positions of token i + 2 and the entries of token i + 1 are on their way.
-template <typename T, int VEC, bool TREE, typename Depth>
+// go(): asked once, after the first loads are out, whether rows may be written.
+template <typename T, int VEC, bool TREE, typename Depth, typename Go>
 __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int stride, int tid,
-                                            int bar, RopeToken (&sh)[2], Depth depth_of) {
+                                            int bar, RopeToken (&sh)[2], Depth depth_of, Go go) {
   using P = Pack<T, VEC>;
   const RopeTable& rt = s.rt;
   const int half = rt.rot / 2;
@@ -183,12 +184,13 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
     if (tok >= s.tokens) return f;
     if (TREE) {
       const int b = tok / s.T, node = tok - b * s.T;
-      const int row = s.past[b] + node;
-      if (node < (s.lens ? s.lens[b] : s.T)) {
-        const int in = row / s.page;
+      // also called for steps that will be refused: nothing is taken for granted
+      const int past = s.past[b], in = past >= 0 ? (int)(((uint32_t)past + node) / (uint32_t)s.page) : -1;
+      if (node < (s.lens ? s.lens[b] : s.T) && (unsigned)in < (unsigned)s.max_blocks) {
+        const int row = past + node;
         const int block = s.table ? s.table[(size_t)b * s.max_blocks + in] : b;
         f.slot = (int64_t)block * s.page + (row - in * s.page);
-        if (half) f.at = s.pos ? s.pos[(size_t)axis * s.tokens + tok] : (int64_t)s.past[b] + depth_of(tok);
+        if (half) f.at = s.pos ? s.pos[(size_t)axis * s.tokens + tok] : (int64_t)past + depth_of(tok);
       }
     } else {
       f.at = s.pos[(size_t)axis * s.tokens + tok];
@@ -229,14 +231,16 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
   };
 
   if (first >= s.tokens) return;
+  load_rows(first, r0);
   Info now = fetch_info(first), next = fetch_info(first + stride);
+  if (!go()) return;
   {
     const float2 e = fetch_entry(now);
     share(sh[0], e, now);
   }
   int buf = 0;
   for (int tok = first; tok < s.tokens; tok += stride, buf ^= 1) {
-    load_rows(tok, r0);
+    if (tok != first) load_rows(tok, r0);
     const Info after = fetch_info(tok + 2 * stride);
     const float2 entry = fetch_entry(next);
     bool write = true;

@@ -41,7 +41,19 @@ template <int N>
 __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, int past, int n,
                                                    int i0, bool write, int* s_parent,
                                                    int* s_depth, long long& tiles) {
+  // Parents and positions of all T nodes are read beside the lengths, whether
+  // they are in use or not; the table has to wait for the lengths.
   uint32_t bad = 0;
+  if (p.parents)
+    for (int i = i0; i < p.T; i += N) s_parent[i] = p.parents[(size_t)b * p.T + i];
+  int off_table = p.T;  // the first node with a position outside the tables
+  if (p.rot > 0 && p.pos) {
+    for (int a = 0; a < p.n_axes; ++a)
+      for (int i = i0; i < p.T; i += N) {
+        const int64_t at = p.pos[((size_t)a * p.B + b) * p.T + i];
+        if (at < 0 || at >= p.cache_rows) off_table = min(off_table, i);
+      }
+  }
   if (n < 0 || n > p.T) bad |= PVA_DEV_TREE;
   if (past < 0 || (long long)past + n > (long long)p.max_blocks * p.page) bad |= PVA_DEV_KV_CACHE;
   const bool sane = bad == 0;
@@ -57,18 +69,11 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
     }
     if (p.parents) {
       for (int i = i0; i < n; i += N) {
-        const int up = p.parents[(size_t)b * p.T + i];
-        s_parent[i] = up;
+        const int up = s_parent[i];  // this thread's own entries
         if (up < -1 || up >= i) bad |= PVA_DEV_TREE;
       }
     }
-    if (p.rot > 0 && p.pos) {
-      for (int a = 0; a < p.n_axes; ++a)
-        for (int i = i0; i < n; i += N) {
-          const int64_t at = p.pos[((size_t)a * p.B + b) * p.T + i];
-          if (at < 0 || at >= p.cache_rows) bad |= PVA_DEV_ROPE;
-        }
-    }
+    if (off_table < n) bad |= PVA_DEV_ROPE;
     bool walk;
     if (N == 32) {
       walk = !__any_sync(0xffffffffu, bad);
@@ -112,9 +117,8 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
       const int t = t0 + i0;
       int x = 0;
       if (t < qt) {
-        int lo, hi;
-        tree_item_range(p, past, n, t, lo, hi);
-        x = (hi + p.bn - 1) / p.bn - lo / p.bn;
+        int lo, first;
+        x = tree_item_tiles(p, past, n, t, lo, first) + kItemPlaces;
       }
       int upto = x;
 #pragma unroll
@@ -131,8 +135,8 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
 }
 
 // What the step comes to: `tiles` in all, `bad` found, `latched` before.
-__device__ __forceinline__ void front_publish(const TreeParams& p, long long tiles, uint32_t bad,
-                                              bool latched) {
+__device__ __forceinline__ void front_publish(const TreeParams& p, long long tiles,
+                                              long long items, uint32_t bad, bool latched) {
   if (bad) atomicOr(p.status, bad | PVA_DEV_KV_CACHE);
   const bool ok = bad == 0 && !latched;
   const int all = ok ? (int)tiles : 0;
@@ -140,7 +144,10 @@ __device__ __forceinline__ void front_publish(const TreeParams& p, long long til
   p.tile_start[p.B] = all;
   p.hdr[0] = ok ? 1 : 0;
   p.hdr[1] = all;
+  const bool whole = ok && p.may_take_items && items >= 6LL * p.pieces && items <= INT_MAX / 2;
   p.hdr[2] = even > p.min_chunk ? even : p.min_chunk;
+  p.hdr[3] = whole ? (int)items : 0;
+  p.hdr[4] = 0;
 }
 
 __device__ __forceinline__ bool too_many(const TreeParams& p, long long tiles) {
@@ -155,6 +162,8 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParam
   __shared__ int s_last;
   __shared__ long long s_sum[kFrontThreads / 32];
   const int b = blockIdx.x, tid = threadIdx.x;
+  // what the CTA that finishes last needs besides the others' results
+  const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
   if (tid == 0) s_bad = 0;
   long long tiles;
   const uint32_t bad = front_sequence<kFrontThreads>(p, b, p.past[b], tree_nodes(p, b), tid, true,
@@ -175,33 +184,45 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParam
   if (!s_last) return;
   // The last CTA: sums of the sequences' tiles, in place.
   __threadfence();
-  long long carry = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kFrontThreads) {
-    const int i = b0 + tid;
-    const long long x = i < p.B ? __ldcg(p.tile_start + i) : 0;
-    long long upto = x;
+  auto sum_up = [&](auto value, int32_t* start) {
+    long long carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kFrontThreads) {
+      const int i = b0 + tid;
+      const long long x = i < p.B ? value(i) : 0;
+      long long upto = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-      if ((tid & 31) >= o) upto += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        if ((tid & 31) >= o) upto += y;
+      }
+      if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
+      __syncthreads();
+      long long before = carry, all = carry;
+      for (int w = 0; w < kFrontThreads / 32; ++w) {
+        if (w < tid >> 5) before += s_sum[w];
+        all += s_sum[w];
+      }
+      if (i < p.B) start[i] = (int)(before + upto - x);
+      carry = all;
+      __syncthreads();
     }
-    if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
-    __syncthreads();
-    long long before = carry, all = carry;
-    for (int w = 0; w < kFrontThreads / 32; ++w) {
-      if (w < tid >> 5) before += s_sum[w];
-      all += s_sum[w];
-    }
-    if (i < p.B) p.tile_start[i] = (int)(before + upto - x);
-    carry = all;
-    __syncthreads();
-  }
+    return carry;
+  };
+  const long long carry = sum_up([&](int i) { return (long long)__ldcg(p.tile_start + i); }, p.tile_start);
+  long long items = 0;
+  if (p.may_take_items)
+    items = sum_up(
+        [&](int i) {
+          const int n = min(max(tree_nodes(p, i), 0), p.T);
+          return (long long)((n * p.G + p.rows - 1) / p.rows) * p.Hkv;
+        },
+        p.item_start);
   if (tid == 0) {
-    const uint32_t all_bad = atomicExch(p.status + kWordBad, 0u) |
-                             (too_many(p, carry) ? PVA_DEV_TOO_MANY : 0u);
-    atomicExch(p.status + kWordArrived, 0u);
+    const uint32_t all_bad = __ldcg(p.status + kWordBad) | (too_many(p, carry) ? PVA_DEV_TOO_MANY : 0u);
+    p.status[kWordBad] = 0;  // for the next step
+    p.status[kWordArrived] = 0;
     // a step after a rejected one would append after rows that are missing
-    front_publish(p, carry, all_bad, (atomicOr(p.status, 0u) & PVA_DEV_KV_CACHE) != 0);
+    front_publish(p, carry, items, all_bad, latched);
   }
 }
 
@@ -248,18 +269,19 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_small_front_kernel(Tre
   const uint32_t bad = s_bad | (too_many(p, all) ? PVA_DEV_TOO_MANY : 0u);
   if (first) {
     if (tid < p.B) p.tile_start[tid] = too_many(p, before) ? 0 : (int)before;
-    if (tid == 0) front_publish(p, all, bad, latched);
+    if (tid == 0) front_publish(p, all, 0, bad, latched);  // few items: by pieces
   }
   if (bad || latched) return;
   const int group = tid / kRopeThreads;
   rope_tokens<T, VEC, true>(r, blockIdx.x * kAtOnce + group, gridDim.x * kAtOnce,
                             tid % kRopeThreads, 1 + group, s_rope[group],
-                            [&](int tok) { return p.parents ? s_depth[tok] : tok % p.T; });
+                            [&](int tok) { return p.parents ? s_depth[tok] : tok % p.T; },
+                            []() { return true; });
 }
 
 // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over an item's parts c, in
-// the order of the line; M = max m_c.  CTAs (c, y) look at the cut at the start
-// of piece c: the first cut of an item has its rows joined, one warp per row.
+// the order of the line; M = max m_c.  CTAs (c, y) take the item that piece c
+// began and did not finish (the attention kernel names it), one warp per row.
 // Lanes hold the weights of 32 parts at a time and V channels of the row, V *
 // 32 at once.  So the work is that of the cut items, however many there are.
 template <typename T, int V>
@@ -269,14 +291,10 @@ __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
   allow_next_grid();
   wait_prior_grid();
   const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int tiles = p.hdr[1], chunk = p.hdr[2];
-  for (long long c = blockIdx.x + 1; c * chunk < tiles; c += gridDim.x) {
-    const TreeItem it = tree_item(p, (int)(c * chunk));
-    const int c0 = it.start / chunk;
-    if (it.start == c * chunk || c0 != c - 1) continue;
-    const int row = it.t * p.rows + r, node = row / p.G;
-    if (node >= tree_nodes(p, it.b)) continue;
-    const int n = (it.end - 1) / chunk - c0 + 1;
+  const int c0 = blockIdx.x;
+  const TreeCut it = p.cuts[c0];
+  if (r < it.rows) {
+    const int row = it.t * p.rows + r, node = row / p.G, n = it.parts;
     // part i: slots of consecutive pieces lie two apart, but for the first
     const float2* ml = p.part_ml + r;
     const float* po = p.part_o + (size_t)r * p.d;
@@ -340,18 +358,27 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
   float* sv = sk + kTreeKeysF32 * kstride;   // [32][d]
   allow_next_grid();
   wait_prior_grid();
-  const int tiles = p.hdr[1], chunk = p.hdr[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float NEG_INF = __int_as_float(0xff800000);
   const float* q = static_cast<const float*>(p.q);
   const float* kc = static_cast<const float*>(p.k_cache);
   const float* vc = static_cast<const float*>(p.v_cache);
-  const int piece = blockIdx.x;
-  const long long from = (long long)piece * chunk;
-  const int end = (int)(from + chunk < tiles ? from + chunk : tiles);
-  for (long long x = from; x < end;) {
-    const TreeSegment s = tree_segment(p, piece, (int)x, end);
-    x += s.count;
+  __shared__ TreeSegment s_segment;
+  __shared__ int s_more;
+  TreeWalk walk(p, blockIdx.x);  // every warp keeps one; the first one's counts
+  while (true) {
+    __syncthreads();
+    if (warp == 0) {
+      TreeSegment next;
+      const bool more = walk.next(p, next);
+      if (lane == 0) {
+        s_more = more;
+        s_segment = next;
+      }
+    }
+    __syncthreads();
+    if (!s_more) break;
+    const TreeSegment s = s_segment;
     const int n_rows = min(p.rows, s.n * p.G - s.t * p.rows);
     const int total = s.past + s.n;
     __syncthreads();
@@ -486,7 +513,7 @@ cudaError_t launch_front(const TreeParams& p, const RopeStep& r, int dtype, int 
 
 cudaError_t launch_join(const TreeParams& p, int dtype, cudaStream_t s) {
   const long long rows = (long long)p.T * p.G;
-  const dim3 grid(p.pieces - 1, (unsigned)((rows < p.rows ? rows : p.rows) + 7) / 8);
+  const dim3 grid(p.pieces, (unsigned)((rows < p.rows ? rows : p.rows) + 7) / 8);
   // four channels a lane; one where rows of fp32 do not lie on 16-byte boundaries
   switch (dtype) {
     case PVA_F32:
@@ -598,6 +625,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   p.QT = (int)(((long long)T * G + p.rows - 1) / p.rows);
   p.W32 = parents ? (T + 31) / 32 : 0;
   p.min_chunk = 1;
+  p.may_take_items = tc && p.QT > 1;
   p.k_cache = k_cache;
   p.v_cache = v_cache;
   p.out = out;
@@ -613,7 +641,8 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
     used += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t at_hdr = take(16), at_tiles = take(4 * ((size_t)B + 1));
+  const size_t at_cuts = take(sizeof(TreeCut) * p.pieces);
+  const size_t at_hdr = take(32), at_tiles = take(4 * ((size_t)B + 1)), at_items = take(4 * ((size_t)B + 1));
   const size_t at_q_start = take(4 * (size_t)B * (p.QT + 1));
   const size_t at_depth = take(parents ? 4 * (size_t)B * T : 0);
   const size_t at_mask = take(4 * (size_t)B * T * p.W32);
@@ -623,8 +652,10 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   CallContext c;
   if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
   p.status = c.status;
+  p.cuts = reinterpret_cast<TreeCut*>(c.buf + at_cuts);
   p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
   p.tile_start = reinterpret_cast<int32_t*>(c.buf + at_tiles);
+  p.item_start = reinterpret_cast<int32_t*>(c.buf + at_items);
   p.q_start = reinterpret_cast<int32_t*>(c.buf + at_q_start);
   p.depth = reinterpret_cast<int32_t*>(c.buf + at_depth);
   p.mask = reinterpret_cast<uint32_t*>(c.buf + at_mask);

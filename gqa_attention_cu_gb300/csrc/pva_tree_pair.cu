@@ -132,9 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const int tiles = p.hdr[1], chunk = p.hdr[2];
-    const long long from = (long long)blockIdx.x * chunk;
-    const int end = (int)(from + chunk < tiles ? from + chunk : tiles);
+    TreeWalk walk(p, blockIdx.x);
     const TileCopies tc(p, BN);
     uint32_t loads = 0, published = 0;
     bool ok = true;
@@ -150,11 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     uint32_t q_loads = 0;
-    for (long long x = from; ok && x < end;) {
-      ItemSlot v;
-      v.s = tree_segment(p, blockIdx.x, (int)x, end);
-      v.last = 0;
-      x += v.s.count;
+    ItemSlot v;
+    v.last = 0;
+    while (ok && walk.next(p, v.s)) {
       if (!(ok = publish(v))) break;
       const TreeSegment& s = v.s;
       // the Q tiles, once the S MMAs of the segment before are done with them
@@ -192,7 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok) {
-      ItemSlot v{};
       v.last = 1;
       publish(v);
     }
@@ -315,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any_own = __any_sync(0xffffffffu, own);
       const int total = s.past + s.n;
       const RowView view = row_view(p, s, node);
-      float m = __int_as_float(0xff800000), l = 0.0f;
+      RowState st(own);
       for (int j = 0; j < n; ++j, ++tiles) {
         const int k0 = (s.j0 + j) * BN;
         // the first tile's warps clean V for both: its product is issued first
@@ -327,11 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(&bars->s_full[x], tiles & 1))) break;
         if (any_own) {
           tc_fence_after();
-          const bool all = __all_sync(0xffffffffu, view.lo <= k0 && view.hi >= k0 + BN);
-          Mask<BN> mk;
-          if (!all) mk = row_mask<BN>(p, view, s.past, k0);
-          const float alpha = all ? softmax_tile<T, BN, CAP, false>(t_s, mk, s_mul, cap_mul, m, l)
-                                  : softmax_tile<T, BN, CAP, true>(t_s, mk, s_mul, cap_mul, m, l);
+          const float alpha = softmax_tile<T, BN, CAP>(p, view, s.past, k0, t_s, s_mul, cap_mul, st);
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // O must hold PV(j-1); every earlier phase has passed, since S(j)
             // was issued after it, in order
@@ -348,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(&bars->o_done[x], done & 1))) break;
       ++done;
       tc_fence_after();
-      if (any_own) store_row<T, D>(p, s, t_o, own, row, node, m, l);
+      if (any_own) store_row<T, D>(p, s, t_o, own, row, node, st.m, st.l);
       tc_fence_before();
       mbar_arrive(&bars->o_free[x]);
     }

@@ -128,9 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const int tiles = p.hdr[1], chunk = p.hdr[2];
-    const long long from = (long long)blockIdx.x * chunk;
-    const int end = (int)(from + chunk < tiles ? from + chunk : tiles);
+    TreeWalk walk(p, blockIdx.x);
     const TileCopies tc(p, BN);
     uint32_t loads = 0, published = 0;
     bool ok = true;
@@ -148,11 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++published;
       return true;
     };
-    for (long long x = from; ok && x < end;) {
-      ItemSlot v;
-      v.s = tree_segment(p, blockIdx.x, (int)x, end);
-      v.last = 0;
-      x += v.s.count;
+    ItemSlot v;
+    v.last = 0;
+    while (ok && walk.next(p, v.s)) {
       if (!(ok = publish(v))) break;
       const TreeSegment& s = v.s;
       const int plane_q = s.b * p.Hkv + s.h;
@@ -191,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok) {
-      ItemSlot v{};
       v.last = 1;
       publish(v);
     }
@@ -283,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;  // TMEM lanes this warp may access
     const int r = quarter * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-    const float NEG_INF = __int_as_float(0xff800000);
     const float s_mul = CAP ? p.scale / p.softcap : p.scale * kLog2e;
     const float cap_mul = p.softcap * kLog2e;
     uint32_t gt = 0, taken = 0, done = 0;
@@ -351,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int total = s.past + s.n;
       const RowView view = row_view(p, s, node);
       const bool any_own = __any_sync(0xffffffffu, own);
-      float m_used = NEG_INF, l = 0.0f;
+      RowState st(own);
 
       for (int j = 0; j < n; ++j) {
         const uint32_t T_ = gt + j;
@@ -370,11 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any_own) {
           tc_fence_after();
           const uint32_t t_s = t_lane + C::COL_S + (T_ & 1) * BN;
-          const bool all = __all_sync(0xffffffffu, view.lo <= k0 && view.hi >= k0 + BN);
-          Mask<BN> mk;
-          if (!all) mk = row_mask<BN>(p, view, s.past, k0);
-          const float alpha = all ? softmax_tile<T, BN, CAP, false>(t_s, mk, s_mul, cap_mul, m_used, l)
-                                  : softmax_tile<T, BN, CAP, true>(t_s, mk, s_mul, cap_mul, m_used, l);
+          const float alpha = softmax_tile<T, BN, CAP>(p, view, s.past, k0, t_s, s_mul, cap_mul, st);
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // O must hold PV(j-1) before it is rescaled; PV(j-2) precedes S(j),
             // so the parity of the outstanding phase is unambiguous.
@@ -408,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++done;
       if (!ok) break;
       tc_fence_after();
-      if (any_own) store_row<T, D>(p, s, t_lane + C::COL_O, own, row, node, m_used, l);
+      if (any_own) store_row<T, D>(p, s, t_lane + C::COL_O, own, row, node, st.m, st.l);
       tc_fence_before();
       mbar_arrive(&bars->o_free);
       gt += n;

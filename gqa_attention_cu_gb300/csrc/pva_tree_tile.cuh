@@ -7,6 +7,8 @@
 // tile is that small; otherwise from 1 - 2 / (exp(2t) + 1).
 #pragma once
 
+#include <math.h>
+
 #include "pva_device.cuh"
 #include "pva_tree.h"
 
@@ -70,53 +72,50 @@ __device__ __forceinline__ Mask<BN> row_mask(const TreeParams& p, const RowView&
   return m;
 }
 
-// Largest score of 64 columns of a tile (c0: the first), and with a softcap the
+// Largest score of 32 columns of a tile (c0: the first), and with a softcap the
 // smallest, for the series' range.
 template <int BN, bool MASKED, bool CAP>
-__device__ __forceinline__ void extremes(const uint32_t (&v)[2][32], int c0, const Mask<BN>& m,
+__device__ __forceinline__ void extremes(const uint32_t (&v)[32], int c0, const Mask<BN>& m,
                                          float& mx, float& mn) {
   const float ninf = __int_as_float(0xff800000), pinf = __int_as_float(0x7f800000);
-  float a[4] = {mx, ninf, ninf, ninf}, b[4] = {mn, pinf, pinf, pinf};
+  float a[2] = {mx, ninf}, b[2] = {mn, pinf};
 #pragma unroll
-  for (int e = 0; e < 64; e += 2) {
-    const float x0 = __uint_as_float(v[e >> 5][e & 31]);
-    const float x1 = __uint_as_float(v[e >> 5][(e + 1) & 31]);
+  for (int e = 0; e < 32; e += 2) {
+    const float x0 = __uint_as_float(v[e]), x1 = __uint_as_float(v[e + 1]);
     const bool s0 = seen<BN, MASKED>(m, c0 + e), s1 = seen<BN, MASKED>(m, c0 + e + 1);
-    float& t = a[(e >> 1) & 3];
+    float& t = a[(e >> 1) & 1];
     t = fmax3f(t, s0 ? x0 : ninf, s1 ? x1 : ninf);
     if (CAP) {
-      float& u = b[(e >> 1) & 3];
+      float& u = b[(e >> 1) & 1];
       u = fmin3f(u, s0 ? x0 : pinf, s1 ? x1 : pinf);
     }
   }
-  mx = fmaxf(fmax3f(a[0], a[1], a[2]), a[3]);
-  if (CAP) mn = fminf(fmin3f(b[0], b[1], b[2]), b[3]);
+  mx = fmaxf(a[0], a[1]);
+  if (CAP) mn = fminf(b[0], b[1]);
 }
 
-// 2^(x - m) over 64 columns, their sum, and P as 16-bit pairs.  MODE 0: x =
-// s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by its series (1) or
-// by exp (2).  P is rounded to the storage type for the tensor-core product:
-// at most half a step of each weight, as V's own elements carry; the row sum
-// adds the fp32 values.
+// 2^(x - m) over 32 columns, added to the two partial sums, and P as 16-bit
+// pairs.  MODE 0: x = s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by
+// its series (1) or by exp (2).  P is rounded to the storage type for the
+// tensor-core product: at most half a step of each weight, as V's own elements
+// carry; the row sum adds the fp32 values.
 template <typename T, int BN, int MODE, bool MASKED>
-__device__ __forceinline__ float exponentials(const uint32_t (&v)[2][32], int c0,
-                                              const Mask<BN>& m, float s_mul, float cap_mul,
-                                              float m_eff, uint32_t (&pw)[32]) {
+__device__ __forceinline__ void exponentials(const uint32_t (&v)[32], int c0, const Mask<BN>& m,
+                                             float s_mul, float cap_mul, float m_eff,
+                                             float2 (&acc)[2], uint32_t* pw) {
   const float ninf = __int_as_float(0xff800000);
   const float2 z = make_float2(0.0f, 0.0f);
   const float2 mul2 = make_float2(s_mul, s_mul), neg_m = make_float2(-m_eff, -m_eff);
   const float2 a2 = make_float2(cap_mul, cap_mul);
   const float2 c1 = make_float2(cap_mul * (-1.0f / 3.0f), cap_mul * (-1.0f / 3.0f));
   const float2 c2 = make_float2(cap_mul * (2.0f / 15.0f), cap_mul * (2.0f / 15.0f));
-  float2 acc[2] = {z, z};
 #pragma unroll
-  for (int g = 0; g < 32; g += 8) {
+  for (int g = 0; g < 16; g += 8) {
     float2 x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int e = 2 * (g + k);
-      const float2 s = make_float2(__uint_as_float(v[e >> 5][e & 31]),
-                                   __uint_as_float(v[e >> 5][(e + 1) & 31]));
+      const float2 s = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
       if (MODE == 0) {
         x[k] = ffma2(s, mul2, neg_m);
       } else if (MODE == 1) {
@@ -137,61 +136,154 @@ __device__ __forceinline__ float exponentials(const uint32_t (&v)[2][32], int c0
       pw[g + k] = pack2<T>(x[k].x, x[k].y);
     }
   }
-  const float2 r = fadd2(acc[0], acc[1]);
-  return r.x + r.y;
 }
 
-// Softmax of the tile at TMEM address t_s (BN score columns of this thread's
-// row): P over its first BN / 2 columns, the running maximum m and sum l (base-2
-// units) brought forward.  Returns the factor O has to be scaled by.  A whole
-// warp calls.  The scores are read twice, 64 columns at a time: reading tensor
-// memory again costs less than holding a tile's row in registers.
-template <typename T, int BN, bool CAP, bool MASKED>
-__device__ __forceinline__ float softmax_tile(uint32_t t_s, const Mask<BN>& mk, float s_mul,
-                                              float cap_mul, float& m, float& l) {
+// The running state of one query row.
+struct RowState {
+  float m;            // reference of the exponentials, base-2 units; -inf: no key seen yet
+  float l = 0.0f;     // sum of 2^(x - m)
+  bool wide = false;  // the warp has met scores beyond the series' range
+  // Lanes without a row have a reference from the start: they ask for nothing.
+  __device__ __forceinline__ explicit RowState(bool own) : m(own ? -INFINITY : 0.0f) {}
+};
+
+// The reference of rows that see their first keys in this tile: its maximum.
+// (Their O and l are zero, so nothing has to be scaled.)
+template <int BN, bool CAP, bool MASKED>
+__device__ __forceinline__ void first_reference(uint32_t t_s, const Mask<BN>& mk, float s_mul,
+                                                float cap_mul, RowState& st) {
+  const float ninf = __int_as_float(0xff800000);
+  float mx = ninf, mn = 0.0f;
+  uint32_t v[2][32];
+  tmem_ld32(t_s, v[0]);
+#pragma unroll
+  for (int c = 0; c < BN / 32; ++c) {
+    tmem_wait_ld_of(v[c & 1]);
+    if (c + 1 < BN / 32) tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
+    extremes<BN, MASKED, false>(v[c & 1], c * 32, mk, mx, mn);
+  }
+  if (st.m == ninf && mx != ninf) st.m = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
+}
+
+// Exponentials of a tile against the reference as it is, in one pass over the
+// scores: the next 32 columns are on their way from tensor memory while 32 are
+// worked on.  Returns false, with nothing changed, where a row's maximum passes
+// the reference by more than 2^8 (or a score the series' range).
+template <typename T, int BN, int MODE, bool MASKED>
+__device__ __forceinline__ bool softmax_fast(uint32_t t_s, const Mask<BN>& mk, float s_mul,
+                                             float cap_mul, RowState& st) {
+  constexpr bool CAP = MODE != 0;
+  float mx = __int_as_float(0xff800000), mn = __int_as_float(0x7f800000);
+  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  uint32_t v[2][32], pw[BN / 2];
+  tmem_ld32(t_s, v[0]);
+#pragma unroll
+  for (int c = 0; c < BN / 32; ++c) {
+    tmem_wait_ld_of(v[c & 1]);
+    if (c + 1 < BN / 32) tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
+    extremes<BN, MASKED, MODE == 1>(v[c & 1], c * 32, mk, mx, mn);
+    exponentials<T, BN, MODE, MASKED>(v[c & 1], c * 32, mk, s_mul, cap_mul, st.m, acc, pw + c * 16);
+  }
+  // the transforms rise, so the largest score is the row's maximum
+  // (a row that has seen no key yet has none here: every weight is 0)
+  const float top = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
+  bool again = mx != __int_as_float(0xff800000) && top > st.m + kRescaleThreshold;
+  if (MODE == 1)
+    again = again || (mx != __int_as_float(0xff800000) &&
+                      fmaxf(fabsf(mx * s_mul), fabsf(mn * s_mul)) > kSeriesLimit);
+  if (__any_sync(0xffffffffu, again)) return false;
+#pragma unroll
+  for (int c = 0; c < BN / 64; ++c) {
+    uint32_t w[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) w[e] = pw[c * 32 + e];
+    tmem_st32(t_s + c * 32, w);
+  }
+  const float2 r = fadd2(acc[0], acc[1]);
+  st.l += r.x + r.y;
+  return true;
+}
+
+// The same in two passes, maximum first; moves the reference where the maximum
+// passes it by more than 2^8, and returns the factor O then has to be scaled by.
+template <typename T, int BN, bool CAP>
+__device__ __forceinline__ float softmax_full(uint32_t t_s, const Mask<BN>& mk, float s_mul,
+                                              float cap_mul, RowState& st) {
   const float NEG_INF = __int_as_float(0xff800000);
   float mx = NEG_INF, mn = __int_as_float(0x7f800000);
-  uint32_t v[2][32];
+  uint32_t v[32];
 #pragma unroll
-  for (int half = BN / 64 - 1; half >= 0; --half) {
-    tmem_ld32(t_s + half * 64, v[0]);
-    tmem_ld32(t_s + half * 64 + 32, v[1]);
-    tmem_wait_ld();
-    extremes<BN, MASKED, CAP>(v, half * 64, mk, mx, mn);
+  for (int c = 0; c < BN / 32; ++c) {
+    tmem_ld32(t_s + c * 32, v);
+    tmem_wait_ld_of(v);
+    extremes<BN, true, CAP>(v, c * 32, mk, mx, mn);
   }
   float mt = NEG_INF;
   if (mx != NEG_INF) mt = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
-  const float m_new = fmaxf(m, mt);
   float alpha = 1.0f;
-  if (m_new > m + kRescaleThreshold) {
-    alpha = ex2_approx(m - m_new);  // 0 when m is -inf
-    m = m_new;
+  if (mt > st.m + kRescaleThreshold) {
+    alpha = ex2_approx(st.m - mt);  // 0 when m is -inf
+    st.m = mt;
   }
-  const float m_eff = m == NEG_INF ? 0.0f : m;
-  const bool series =
-      CAP && __all_sync(0xffffffffu, mx == NEG_INF ||
-                                         fmaxf(fabsf(mx * s_mul), fabsf(mn * s_mul)) <= kSeriesLimit);
-  float rs = 0.0f;
+  const float m_eff = st.m == NEG_INF ? 0.0f : st.m;
+  if (CAP)
+    st.wide = __any_sync(0xffffffffu, mx != NEG_INF && fmaxf(fabsf(mx * s_mul), fabsf(mn * s_mul)) >
+                                                           kSeriesLimit);
+  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  // P of 64 columns lies over the first 32 of them: columns already read
 #pragma unroll
   for (int half = 0; half < BN / 64; ++half) {
-    // The first half is still in registers.  Its P covers score columns of
-    // that half alone; the second half's covers columns of the first.
-    if (half > 0) {
-      tmem_ld32(t_s + half * 64, v[0]);
-      tmem_ld32(t_s + half * 64 + 32, v[1]);
-      tmem_wait_ld();
-    }
     uint32_t pw[32];
-    if (!CAP)
-      rs += exponentials<T, BN, 0, MASKED>(v, half * 64, mk, s_mul, cap_mul, m_eff, pw);
-    else if (series)
-      rs += exponentials<T, BN, 1, MASKED>(v, half * 64, mk, s_mul, cap_mul, m_eff, pw);
-    else
-      rs += exponentials<T, BN, 2, MASKED>(v, half * 64, mk, s_mul, cap_mul, m_eff, pw);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      tmem_ld32(t_s + half * 64 + c * 32, v);
+      tmem_wait_ld_of(v);
+      const int c0 = half * 64 + c * 32;
+      if (!CAP)
+        exponentials<T, BN, 0, true>(v, c0, mk, s_mul, cap_mul, m_eff, acc, pw + c * 16);
+      else if (!st.wide)
+        exponentials<T, BN, 1, true>(v, c0, mk, s_mul, cap_mul, m_eff, acc, pw + c * 16);
+      else
+        exponentials<T, BN, 2, true>(v, c0, mk, s_mul, cap_mul, m_eff, acc, pw + c * 16);
+    }
     tmem_st32(t_s + half * 32, pw);
   }
-  l = l * alpha + rs;
+  const float2 r = fadd2(acc[0], acc[1]);
+  st.l = st.l * alpha + r.x + r.y;
   return alpha;
+}
+
+// Softmax of the tile at TMEM address t_s (BN score columns of this thread's
+// row, keys [k0, k0 + BN)): P over its first BN / 2 columns.  Returns the factor
+// O has to be scaled by.  A whole warp calls.
+template <typename T, int BN, bool CAP>
+__device__ __forceinline__ float softmax_tile(const TreeParams& p, const RowView& view, int past,
+                                              int k0, uint32_t t_s, float s_mul, float cap_mul,
+                                              RowState& st) {
+  const bool all = __all_sync(0xffffffffu, view.lo <= k0 && view.hi >= k0 + BN);
+  Mask<BN> mk;
+  if (!all) {
+    mk = row_mask<BN>(p, view, past, k0);
+  } else {
+#pragma unroll
+    for (int w = 0; w < BN / 32; ++w) mk.w[w] = 0xffffffffu;
+  }
+  if (__any_sync(0xffffffffu, st.m == __int_as_float(0xff800000))) {
+    if (all)
+      first_reference<BN, CAP, false>(t_s, mk, s_mul, cap_mul, st);
+    else
+      first_reference<BN, CAP, true>(t_s, mk, s_mul, cap_mul, st);
+  }
+  bool done;
+  if (!CAP)
+    done = all ? softmax_fast<T, BN, 0, false>(t_s, mk, s_mul, cap_mul, st)
+               : softmax_fast<T, BN, 0, true>(t_s, mk, s_mul, cap_mul, st);
+  else if (!st.wide)
+    done = all ? softmax_fast<T, BN, 1, false>(t_s, mk, s_mul, cap_mul, st)
+               : softmax_fast<T, BN, 1, true>(t_s, mk, s_mul, cap_mul, st);
+  else
+    done = softmax_fast<T, BN, 2, true>(t_s, mk, s_mul, cap_mul, st);
+  return done ? 1.0f : softmax_full<T, BN, CAP>(t_s, mk, s_mul, cap_mul, st);
 }
 
 // O columns [0, D) at TMEM address t_o times f.
