@@ -166,13 +166,18 @@ struct TreeWalk {
       next_item = draw(p);
     } else if (x < end) {
       b = tree_find(p.tile_start, p.B, (int)x);
-      const int32_t* qs = p.q_start + (size_t)b * (p.QT + 1);
-      const int per_head = qs[p.QT], rel = (int)x - p.tile_start[b];
+      const int first = p.tile_start[b], rel = (int)x - first;
+      const int per_head = (p.tile_start[b + 1] - first) / p.Hkv;
       past = p.past[b];
       n = tree_nodes(p, b);
       h = rel / per_head;
-      t = tree_find(qs, p.QT, rel - h * per_head);
-      into = rel - h * per_head - qs[t];
+      t = 0;
+      into = rel - h * per_head;
+      if (p.QT > 1) {
+        const int32_t* qs = p.q_start + (size_t)b * (p.QT + 1);
+        t = tree_find(qs, p.QT, into);
+        into -= qs[t];
+      }
     }
     if ((items || x >= end) && (threadIdx.x & 31) == 0) tree_note_cut(p, piece, nullptr);
   }

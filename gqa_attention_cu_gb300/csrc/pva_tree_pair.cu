@@ -165,10 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       ++q_loads;
+      // the block of the next tile's copy is looked up while this tile's slots
+      // are waited for
+      TileCopy copy = tc.locate(p, s, BN, s.j0, lane);
       for (int j = s.j0; ok && j < s.j0 + s.count; ++j) {
-        int plane = 0, y = 0;
-        const bool mine = tc.locate(p, s, BN, j, lane, plane, y);
-        const uint32_t n_copies = __popc(__ballot_sync(0xffffffffu, mine));
+        const TileCopy next = tc.locate(p, s, BN, j + 1, lane);
+        const uint32_t n_copies = __popc(__ballot_sync(0xffffffffu, copy.mine));
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++loads) {
           const int sl = loads % C::SLOTS;
@@ -176,15 +178,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0)
             mbar_arrive_expect_tx(&bars->ring_full[sl], n_copies * C::CH * (uint32_t)tc.box * 128u);
           __syncwarp();
-          if (mine) {
+          if (copy.mine) {
             uint8_t* dst = ring + sl * C::KV_TILE + lane * tc.box * 128;
 #pragma unroll
             for (int c = 0; c < C::CH; ++c)
               tma_load_3d(dst + c * C::KV_CHUNK, kv ? &tmap_v : &tmap_k, &bars->ring_full[sl],
-                          c * 64, y, plane);
+                          c * 64, copy.y, copy.plane(p, s));
           }
           __syncwarp();
         }
+        copy = next;
       }
     }
     if (ok) {

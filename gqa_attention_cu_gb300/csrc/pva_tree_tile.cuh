@@ -349,21 +349,29 @@ __device__ __forceinline__ void store_row(const TreeParams& p, const TreeSegment
   }
 }
 
-// What the copies of a key tile need: one lane per page (or one for the tile).
+// A lane's share of the copies of a key tile: one lane per page, or one for the
+// whole tile.
+struct TileCopy {
+  bool mine;
+  int block, y;  // cache block and first row in it
+  __device__ __forceinline__ int plane(const TreeParams& p, const TreeSegment& s) const {
+    return block * p.Hkv + s.h;
+  }
+};
 struct TileCopies {
   int box, copies;  // rows of one copy, copies side by side
   __device__ __forceinline__ TileCopies(const TreeParams& p, int bn)
       : box(p.table && p.page < bn ? p.page : bn), copies(bn / box) {}
-  // This lane's copy of key tile j: its plane and first row; false: none.
-  __device__ __forceinline__ bool locate(const TreeParams& p, const TreeSegment& s, int bn, int j,
-                                         int lane, int& plane, int& y) const {
-    const int r0 = j * bn + lane * box;
-    if (lane >= copies || r0 >= s.past + s.n || r0 + box <= s.lo) return false;
-    const int in = r0 / p.page;
-    const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
-    plane = block * p.Hkv + s.h;
-    y = r0 - in * p.page;
-    return true;
+  __device__ __forceinline__ TileCopy locate(const TreeParams& p, const TreeSegment& s, int bn,
+                                             int j, int lane) const {
+    TileCopy c{false, 0, 0};
+    const long long r0 = (long long)j * bn + lane * box;
+    if (lane >= copies || r0 >= s.past + s.n || r0 + box <= s.lo) return c;
+    const int in = (int)r0 / p.page;
+    c.mine = true;
+    c.block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+    c.y = (int)r0 - in * p.page;
+    return c;
   }
 };
 
