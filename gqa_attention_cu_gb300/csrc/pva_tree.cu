@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
           wl = w * v.y;
         }
         const int k = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < k; ++i) {
           Part o;
           if (in) o = *reinterpret_cast<const Part*>(po + slot(i0 + i) * p.d + at);
@@ -344,28 +344,48 @@ __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
 }
 
 // fp32 attention on the CUDA cores, exact fp32 products (no TF32).  A CTA of 4
-// warps holds 32 query rows and walks over its piece's tiles of 32 keys; a warp
-// owns 8 rows, lane j scores key j, lane c sums channels c, c + 32, ...  Keys
-// outside the item's range and invisible ones take part with weight 0; their
-// rows are not read (the range) or have value 0 (p = 0 times a finite row).
-constexpr int kWarpsF32 = 4, kRowsPerWarpF32 = kTreeRowsF32 / kWarpsF32, kChanF32 = 8;
+// warps holds 32 query rows and streams tiles of 32 keys, the next tile on its
+// way (cp.async) while one is worked on.  A warp owns 8 rows throughout: a
+// thread scores 2 rows x 4 keys, then the warp's lanes hold a key each for the
+// softmax, then 4 (or 8) channels each of its 8 rows for the weighted sum, so
+// warps meet only where a tile is complete.  Per thread 12 16-byte shared
+// loads feed 128 multiply-adds of the sum, 6 feed 32 of the scores: bound by
+// the FMA pipe and shared memory together for many rows, by latency for a small
+// draft.  Keys outside the item's range are zeros in shared memory, whatever
+// the cache holds there.
+constexpr int kWarpsF32 = 4, kRowsPerWarpF32 = kTreeRowsF32 / kWarpsF32;
 
+__host__ __device__ constexpr int f32_stride(int d) { return (d + 3) / 4 * 4 + 4; }
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+
+// C: 16-byte channel groups a lane sums (1: d <= 128, 2: d <= 256); WIDE: rows of
+// the cache lie on 16-byte boundaries.
+template <int C, bool WIDE>
 __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams p) {
   extern __shared__ float smem[];
-  const int d = p.d, kstride = d + 1;
-  float* sq = smem;                          // [32][d]
-  float* sk = sq + kTreeRowsF32 * d;         // [32][d + 1]
-  float* sv = sk + kTreeKeysF32 * kstride;   // [32][d]
+  const int d = p.d, stride = f32_stride(d), groups = (d + 3) / 4;
+  constexpr int kTile = kTreeKeysF32;
+  float* sq = smem;                               // [32][stride]
+  float* skv = sq + kTreeRowsF32 * stride;        // [2][K, V][32][stride]
+  float* sp = skv + 4 * kTile * stride;           // [32][36] weights
+  __shared__ TreeSegment s_segment;
+  __shared__ int s_more;
   allow_next_grid();
   wait_prior_grid();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float NEG_INF = __int_as_float(0xff800000);
   const float* q = static_cast<const float*>(p.q);
   const float* kc = static_cast<const float*>(p.k_cache);
   const float* vc = static_cast<const float*>(p.v_cache);
-  __shared__ TreeSegment s_segment;
-  __shared__ int s_more;
-  TreeWalk walk(p, blockIdx.x);  // every warp keeps one; the first one's counts
+  // the padding channels of every row stay zero
+  for (int e = tid; e < (kTreeRowsF32 + 4 * kTile) * (stride - d); e += kWarpsF32 * 32)
+    smem[e / (stride - d) * stride + d + e % (stride - d)] = 0.0f;
+  TreeWalk walk(p, blockIdx.x);  // the first warp's counts
   while (true) {
     __syncthreads();
     if (warp == 0) {
@@ -381,104 +401,167 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
     const TreeSegment s = s_segment;
     const int n_rows = min(p.rows, s.n * p.G - s.t * p.rows);
     const int total = s.past + s.n;
-    __syncthreads();
+    auto load = [&](int j) {  // key tile j into its buffer
+      float* dst = skv + (j & 1) * 2 * kTile * stride;
+      // a warp takes every fourth key, its lanes the row's channels
+      for (int i = warp; i < kTile; i += kWarpsF32) {
+        const int key = j * kTile + i;
+        const bool valid = key >= s.lo && key < total;
+        size_t at = 0;
+        if (valid) {
+          const int in = key / p.page;
+          const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+          at = (((size_t)block * p.Hkv + s.h) * p.page + (key - in * p.page)) * d;
+        }
+        if (WIDE) {
+          for (int c = lane; c < groups; c += 32) {
+            copy_async16(dst + i * stride + 4 * c, kc + at + 4 * c, valid);
+            copy_async16(dst + (kTile + i) * stride + 4 * c, vc + at + 4 * c, valid);
+          }
+        } else {
+          for (int c = lane; c < d; c += 32) {
+            dst[i * stride + c] = valid ? kc[at + c] : 0.0f;
+            dst[(kTile + i) * stride + c] = valid ? vc[at + c] : 0.0f;
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(s.j0);
     const float* q0 = q + (((size_t)s.b * p.Hkv + s.h) * p.T * p.G + (size_t)s.t * p.rows) * d;
-    for (int e = threadIdx.x; e < kTreeRowsF32 * d; e += blockDim.x)
-      sq[e] = e < n_rows * d ? q0[e] : 0.0f;
-    float m[kRowsPerWarpF32], l[kRowsPerWarpF32], acc[kRowsPerWarpF32][kChanF32];
+    for (int r = warp; r < kTreeRowsF32; r += kWarpsF32)
+      for (int c = lane; c < d; c += 32) sq[r * stride + c] = r < n_rows ? q0[r * d + c] : 0.0f;
+    const int row0 = warp * kRowsPerWarpF32;
+    float m[kRowsPerWarpF32], l[kRowsPerWarpF32], acc[kRowsPerWarpF32][4 * C];
     int row_lo[kRowsPerWarpF32], row_hi[kRowsPerWarpF32];
 #pragma unroll
     for (int r = 0; r < kRowsPerWarpF32; ++r) {
       m[r] = NEG_INF;
       l[r] = 0.0f;
 #pragma unroll
-      for (int u = 0; u < kChanF32; ++u) acc[r][u] = 0.0f;
-      const int lr = warp * kRowsPerWarpF32 + r;
-      const int node = lr < n_rows ? (s.t * p.rows + lr) / p.G : 0;
+      for (int u = 0; u < 4 * C; ++u) acc[r][u] = 0.0f;
+      const int node = row0 + r < n_rows ? (s.t * p.rows + row0 + r) / p.G : 0;
       const int depth = p.parents ? p.depth[(size_t)s.b * p.T + node] : node;
-      row_lo[r] = p.window > 0 ? s.past + depth + 1 - p.window : 0;
+      const long long lo = p.window > 0 ? (long long)s.past + depth + 1 - p.window : 0;
+      row_lo[r] = lo > 0 ? (int)lo : 0;
       row_hi[r] = p.parents ? s.past : s.past + node + 1;
     }
     for (int j = s.j0; j < s.j0 + s.count; ++j) {
-      const int k0 = j * kTreeKeysF32;
-      __syncthreads();
-      for (int e = threadIdx.x; e < kTreeKeysF32 * d; e += blockDim.x) {
-        const int i = e / d, c = e - i * d, key = k0 + i;
-        float kk = 0.0f, vv = 0.0f;
-        if (key >= s.lo && key < total) {
-          const int in = key / p.page;
-          const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
-          const size_t at = (((size_t)block * p.Hkv + s.h) * p.page + (key - in * p.page)) * d + c;
-          kk = kc[at];
-          vv = vc[at];
-        }
-        sk[i * kstride + c] = kk;
-        sv[i * d + c] = vv;
+      if (j + 1 < s.j0 + s.count) {
+        load(j + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-      __syncthreads();
+      __syncthreads();  // tile j (and Q) is complete
+      const float* sk = skv + (j & 1) * 2 * kTile * stride;
+      const float* sv = sk + kTile * stride;
+      if (row0 < n_rows) {  // warp-uniform
+        // scores of rows row0 + 2 y, + 1 and keys x, x + 8, x + 16, x + 24
+        const int y = lane >> 3, x = lane & 7;
+        float sc[2][4] = {};
+        const float* qa = sq + (row0 + 2 * y) * stride;
+#pragma unroll 4
+        for (int c = 0; c < groups; ++c) {
+          const float4 a0 = *reinterpret_cast<const float4*>(qa + 4 * c);
+          const float4 a1 = *reinterpret_cast<const float4*>(qa + stride + 4 * c);
 #pragma unroll
-      for (int r = 0; r < kRowsPerWarpF32; ++r) {
-        const int lr = warp * kRowsPerWarpF32 + r;
-        if (lr >= n_rows) continue;  // warp-uniform
-        const int key = k0 + lane;
-        bool seen = key >= row_lo[r] && key < row_hi[r];
-        const int other = key - s.past;
-        if (p.parents && other >= 0 && other < s.n) {
-          const int node = (s.t * p.rows + lr) / p.G;
-          seen = (p.mask[((size_t)s.b * p.T + node) * p.W32 + (other >> 5)] >> (other & 31)) & 1;
+          for (int k = 0; k < 4; ++k) {
+            const float4 b = *reinterpret_cast<const float4*>(sk + (x + 8 * k) * stride + 4 * c);
+            sc[0][k] = fmaf(a0.w, b.w, fmaf(a0.z, b.z, fmaf(a0.y, b.y, fmaf(a0.x, b.x, sc[0][k]))));
+            sc[1][k] = fmaf(a1.w, b.w, fmaf(a1.z, b.z, fmaf(a1.y, b.y, fmaf(a1.x, b.x, sc[1][k]))));
+          }
         }
-        float sc = 0.0f;
-        const float* qr = sq + lr * d;
-        const float* kr = sk + lane * kstride;
-        for (int c = 0; c < d; ++c) sc = fmaf(qr[c], kr[c], sc);
-        sc *= p.scale;
-        if (p.softcap != 0.0f) sc = p.softcap * tanhf(sc / p.softcap);
-        // base-2 units, as the join expects
-        const float xs = seen ? sc * 1.4426950408889634f : NEG_INF;
-        float mt = xs;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        const float m_new = fmaxf(m[r], mt);
-        if (!__any_sync(0xffffffffu, seen)) continue;
-        const float base = m_new == NEG_INF ? 0.0f : m_new;
-        const float alpha = exp2f(m[r] - base);
-        const float pr = seen ? exp2f(xs - base) : 0.0f;
-        float ps = pr;
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-        l[r] = l[r] * alpha + ps;
-        m[r] = m_new;
+          for (int k = 0; k < 4; ++k) sp[(row0 + 2 * y + r) * 36 + x + 8 * k] = sc[r][k];
+        __syncwarp();
+        // softmax: lane = key
+        const int key = j * kTile + lane, other = key - s.past;
+        float w[kRowsPerWarpF32], top[kRowsPerWarpF32];
 #pragma unroll
-        for (int u = 0; u < kChanF32; ++u) acc[r][u] *= alpha;
-        for (int i = 0; i < kTreeKeysF32; ++i) {
-          const float w = __shfl_sync(0xffffffffu, pr, i);
-          if (w == 0.0f) continue;  // an unseen key's row may hold anything
+        for (int r = 0; r < kRowsPerWarpF32; ++r) {
+          bool seen = key >= row_lo[r] && key < row_hi[r];
+          if (p.parents && other >= 0 && other < s.n && row0 + r < n_rows) {
+            const int node = (s.t * p.rows + row0 + r) / p.G;
+            seen = (p.mask[((size_t)s.b * p.T + node) * p.W32 + (other >> 5)] >> (other & 31)) & 1;
+          }
+          float v = sp[(row0 + r) * 36 + lane] * p.scale;
+          if (p.softcap != 0.0f) v = p.softcap * tanhf(v / p.softcap);
+          w[r] = seen ? v * 1.4426950408889634f : NEG_INF;  // base-2 units, as the join expects
+          top[r] = w[r];
+        }
 #pragma unroll
-          for (int u = 0; u < kChanF32; ++u) {
-            const int c = lane + 32 * u;
-            if (c < d) acc[r][u] = fmaf(w, sv[i * d + c], acc[r][u]);
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int r = 0; r < kRowsPerWarpF32; ++r)
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarpF32; ++r) {
+          const float m_new = fmaxf(m[r], top[r]);
+          const float base = m_new == NEG_INF ? 0.0f : m_new;
+          const float alpha = exp2f(m[r] - base);
+          m[r] = m_new;
+          w[r] = exp2f(w[r] - base);  // 0 where unseen
+          top[r] = w[r];
+          l[r] *= alpha;
+#pragma unroll
+          for (int u = 0; u < 4 * C; ++u) acc[r][u] *= alpha;
+          sp[(row0 + r) * 36 + lane] = w[r];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int r = 0; r < kRowsPerWarpF32; ++r)
+            top[r] += __shfl_xor_sync(0xffffffffu, top[r], o);
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarpF32; ++r) l[r] += top[r];
+        __syncwarp();
+        // weighted sums: lane = channels 4 lane .. (and 128 on)
+#pragma unroll 2
+        for (int i = 0; i < kTile; i += 4) {
+          float4 v[4][C];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int u = 0; u < C; ++u)
+              if (lane + 32 * u < groups)
+                v[k][u] = *reinterpret_cast<const float4*>(sv + (i + k) * stride + 4 * (lane + 32 * u));
+#pragma unroll
+          for (int r = 0; r < kRowsPerWarpF32; ++r) {
+            const float4 wr = *reinterpret_cast<const float4*>(sp + (row0 + r) * 36 + i);
+            const float wk[4] = {wr.x, wr.y, wr.z, wr.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int u = 0; u < C; ++u) {
+                acc[r][4 * u + 0] = fmaf(wk[k], v[k][u].x, acc[r][4 * u + 0]);
+                acc[r][4 * u + 1] = fmaf(wk[k], v[k][u].y, acc[r][4 * u + 1]);
+                acc[r][4 * u + 2] = fmaf(wk[k], v[k][u].z, acc[r][4 * u + 2]);
+                acc[r][4 * u + 3] = fmaf(wk[k], v[k][u].w, acc[r][4 * u + 3]);
+              }
           }
         }
       }
+      __syncthreads();  // before tile j + 2 goes over tile j
     }
 #pragma unroll
     for (int r = 0; r < kRowsPerWarpF32; ++r) {
-      const int lr = warp * kRowsPerWarpF32 + r;
+      const int lr = row0 + r;
       if (lr >= n_rows) continue;
-      if (s.slot < 0) {
-        const int row = s.t * p.rows + lr, node = row / p.G, g = row - node * p.G;
-        float* o = static_cast<float*>(p.out) +
-                   (((size_t)s.b * p.T + node) * p.H + (size_t)s.h * p.G + g) * d;
-        const float inv = l[r] != 0.0f ? 1.0f / l[r] : 0.0f;
+      const int row = s.t * p.rows + lr, node = row / p.G, g = row - node * p.G;
+      const size_t at = (size_t)(s.slot < 0 ? 0 : s.slot) * p.rows + lr;
+      const bool whole = s.slot < 0;
+      float* o = whole ? static_cast<float*>(p.out) +
+                             (((size_t)s.b * p.T + node) * p.H + (size_t)s.h * p.G + g) * d
+                       : p.part_o + at * d;
+      const float f = !whole ? 1.0f : l[r] != 0.0f ? 1.0f / l[r] : 0.0f;
+      if (!whole && lane == 0) p.part_ml[at] = make_float2(m[r], l[r]);
 #pragma unroll
-        for (int u = 0; u < kChanF32; ++u)
-          if (lane + 32 * u < d) o[lane + 32 * u] = acc[r][u] * inv;
-      } else {
-        const size_t at = (size_t)s.slot * p.rows + lr;
-        if (lane == 0) p.part_ml[at] = make_float2(m[r], l[r]);
-#pragma unroll
-        for (int u = 0; u < kChanF32; ++u)
-          if (lane + 32 * u < d) p.part_o[at * d + lane + 32 * u] = acc[r][u];
+      for (int u = 0; u < 4 * C; ++u) {
+        const int c = 4 * (lane + 32 * (u >> 2)) + (u & 3);
+        if (c < d) o[c] = acc[r][u] * f;
       }
     }
   }
@@ -530,12 +613,14 @@ cudaError_t launch_join(const TreeParams& p, int dtype, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_f32(const TreeParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(float) * ((size_t)kTreeRowsF32 * p.d + (size_t)kTreeKeysF32 * (p.d + 1) +
-                                       (size_t)kTreeKeysF32 * p.d);
-  cudaError_t e = cudaFuncSetAttribute(pva_tree_f32_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = sizeof(float) * ((size_t)(kTreeRowsF32 + 4 * kTreeKeysF32) * f32_stride(p.d) +
+                                       kTreeRowsF32 * 36);
+  const bool wide = p.d % 4 == 0 && (((uintptr_t)p.k_cache | (uintptr_t)p.v_cache) & 15) == 0;
+  auto kern = p.d <= 128 ? (wide ? pva_tree_f32_kernel<1, true> : pva_tree_f32_kernel<1, false>)
+                         : (wide ? pva_tree_f32_kernel<2, true> : pva_tree_f32_kernel<2, false>);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(pva_tree_f32_kernel, dim3(p.pieces), dim3(kWarpsF32 * 32), smem, s, p);
+  return launch_dependent(kern, dim3(p.pieces), dim3(kWarpsF32 * 32), smem, s, p);
 }
 
 }  // namespace pva
