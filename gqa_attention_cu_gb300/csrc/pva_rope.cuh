@@ -72,6 +72,7 @@ struct RopeStep {
   const int32_t* table;     // [B, max_blocks]; nullptr: block b
   int T, max_blocks;
   int negate_q;             // a negative scale, moved into the queries
+  void* q_rest;             // nullptr, or what rounding took off the queries, laid out like them
   void* out;                // attention output: rows of unused nodes are zeroed
   uint32_t* status;
 };
@@ -280,14 +281,43 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
           const bool is_q = row < nq, is_v = row >= nq + nk;
           if (turned && !is_v) {
             if (rt.interleaved) split_pairs(x0[y], x1[y]);
+            P rest0, rest1;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
               const float2 cs = sh[buf].cs[u * VEC + e];
               const float a = load_f(x0[y].v[e]), f = load_f(x1[y].v[e]);
-              x0[y].v[e] = round_to<T>(__fsub_rn(__fmul_rn(cs.x, a), __fmul_rn(cs.y, f)));
-              x1[y].v[e] = round_to<T>(__fadd_rn(__fmul_rn(cs.y, a), __fmul_rn(cs.x, f)));
+              const float g0 = __fsub_rn(__fmul_rn(cs.x, a), __fmul_rn(cs.y, f));
+              const float g1 = __fadd_rn(__fmul_rn(cs.y, a), __fmul_rn(cs.x, f));
+              x0[y].v[e] = round_to<T>(g0);
+              x1[y].v[e] = round_to<T>(g1);
+              if (TREE) {
+                rest0.v[e] = round_to<T>(g0 - load_f(x0[y].v[e]));
+                rest1.v[e] = round_to<T>(g1 - load_f(x1[y].v[e]));
+              }
             }
             if (rt.interleaved) join_pairs(x0[y], x1[y]);
+            if (TREE && is_q && s.q_rest) {
+              if (rt.interleaved) join_pairs(rest0, rest1);
+              T* dst = static_cast<T*>(s.q_rest) +
+                       ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d;
+              if (s.negate_q) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                  rest0.v[e] = -rest0.v[e];
+                  rest1.v[e] = -rest1.v[e];
+                }
+              }
+              *reinterpret_cast<P*>(dst + d0) = rest0;
+              *reinterpret_cast<P*>(dst + d1) = rest1;
+            }
+          } else if (TREE && is_q && s.q_rest) {  // dims that are only copied are exact
+            P z;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) z.v[e] = round_to<T>(0.0f);
+            T* dst = static_cast<T*>(s.q_rest) +
+                     ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d;
+            *reinterpret_cast<P*>(dst + d0) = z;
+            *reinterpret_cast<P*>(dst + d1) = z;
           }
           if (is_q) {
             if (TREE && s.negate_q) {

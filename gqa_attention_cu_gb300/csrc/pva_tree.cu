@@ -118,7 +118,7 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
       int x = 0;
       if (t < qt) {
         int lo, first;
-        x = tree_item_tiles(p, past, n, t, lo, first) + kItemPlaces;
+        x = tree_item_tiles(p, past, n, t, lo, first) + p.item_places;
       }
       int upto = x;
 #pragma unroll
@@ -706,6 +706,9 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   // two query tiles an item where a sequence can have more rows than one holds
   const bool pair = tc && (long long)T * G > kTcRows && d <= 192;
   p.rows = pair ? 2 * kTcRows : tc ? kTcRows : kTreeRowsF32;
+  // without a rotation the queries are exact as they are
+  p.q_parts = tc && !pair && rot ? tree_q_parts(d) : 1;
+  p.item_places = 2;
   p.bn = tc ? tree_keys(d) : kTreeKeysF32;
   p.QT = (int)(((long long)T * G + p.rows - 1) / p.rows);
   p.W32 = parents ? (T + 31) / 32 : 0;
@@ -731,7 +734,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   const size_t at_q_start = take(4 * (size_t)B * (p.QT + 1));
   const size_t at_depth = take(parents ? 4 * (size_t)B * T : 0);
   const size_t at_mask = take(4 * (size_t)B * T * p.W32);
-  const size_t at_q = take((size_t)B * T * H * d * size);
+  const size_t at_q = take((size_t)p.q_parts * B * T * H * d * size);
   const size_t at_o = take(sizeof(float) * 2 * p.pieces * p.rows * (size_t)d);
   const size_t at_ml = take(sizeof(float2) * 2 * p.pieces * (size_t)p.rows);
   CallContext c;
@@ -754,7 +757,8 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
     const int box = block_table && page_size < p.bn ? page_size : p.bn;
     const long long planes = (long long)n_blocks * Hkv;
     if ((rc = get_encoder()) != PVA_OK ||
-        (rc = encode_plane_map(&tq, p.q, dtype, d, T * G, (long long)B * Hkv, 64, kTcRows, true)) !=
+        (rc = encode_plane_map(&tq, p.q, dtype, d, T * G, (long long)p.q_parts * B * Hkv, 64, kTcRows,
+                               true)) !=
             PVA_OK ||
         (rc = encode_plane_map(&tk, k_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK ||
         (rc = encode_plane_map(&tv, v_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK)
@@ -765,6 +769,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   r.k = k_new;
   r.v = v_new;
   r.q_out = p.q;
+  r.q_rest = p.q_parts == 2 ? c.buf + at_q + (size_t)B * T * H * d * size : nullptr;
   r.k_cache = k_cache;
   r.v_cache = v_cache;
   r.q_stride = (long long)H * d;

@@ -5,7 +5,7 @@
 // rows [t * rows, (t + 1) * rows) of the n * G rows (row = node * G + head of
 // the group) that sequence b has on one kv head, against the key tiles
 // [item_lo / bn, ceil(item_hi / bn)): a place for each key tile, after
-// kItemPlaces for what an item costs whatever its length (queries, pipeline,
+// `item_places` for what an item costs whatever its length (queries, pipeline,
 // output).  All items' places form one line (sequence, kv head, q tile, key
 // tile), which is cut into pieces of `chunk` places, one piece per CTA: every
 // CTA gets the same amount of work whatever the lengths are.  An item that lies across a cut is computed
@@ -17,16 +17,14 @@
 // items in turn from a counter: then the q tiles of one kv head run side by
 // side and find each other's keys in L2, where pieces of the line would be at
 // far-apart places of the cache at any time.  (2048-token chunks of 8 sequences
-// on 4.6k rows, d = 128: 1.31 ms by pieces, whose copies alone take 1.11 ms,
-// against MEASURED_WHOLE.)  With fewer than 6 items per CTA the last ones would
+// on 4.6k rows, d = 128: 1.31 ms by pieces, bound by copies at 5.3 TB/s,
+// against 1.10 ms.)  With fewer than 6 items per CTA the last ones would
 // leave too many CTAs idle.
 #pragma once
 
 #include "pva_internal.h"
 
 namespace pva {
-
-constexpr int kItemPlaces = 2;
 
 // The item that a piece began and later pieces go on with.
 struct alignas(16) TreeCut {
@@ -38,6 +36,9 @@ struct alignas(16) TreeCut {
 
 // Keys per key tile of the tensor-core kernel (TMEM holds two score tiles, O and Q).
 __host__ __device__ constexpr int tree_keys(int d) { return d <= 128 ? 128 : 64; }
+
+// Parts of the rotated queries that the one-tile kernel takes (pva_tree_tc.cu).
+__host__ __device__ constexpr int tree_q_parts(int d) { return d <= 192 ? 2 : 1; }
 
 struct TreeParams {
   const int32_t* past;     // [B] cache rows before the step
@@ -51,6 +52,7 @@ struct TreeParams {
   float scale, softcap;
   int rot, n_axes, cache_rows;  // rotary positions checked by the front end
   int rows, bn;            // query rows and keys of a tile
+  int item_places;         // an item's fixed cost, in key tiles
   int QT;                  // q tiles of T nodes
   int W32;                 // mask words per node (0: chain)
   int pieces;              // CTAs of the attention kernel
@@ -64,7 +66,9 @@ struct TreeParams {
   int32_t* q_start;        // [B][QT + 1] tiles before each q tile, within one kv head
   int32_t* depth;          // [B, T]
   uint32_t* mask;          // [B, T, W32] bit j: node j is seen
-  void* q;                 // [B][Hkv][T * G][d] rotated queries
+  void* q;                 // [q_parts][B][Hkv][T * G][d] rotated queries: the rounded values,
+                           // and what rounding took off them
+  int q_parts;
   float* part_o;           // [2 * pieces][rows][d]
   float2* part_ml;         // [2 * pieces][rows]
   TreeCut* cuts;           // [pieces]
@@ -211,11 +215,11 @@ struct TreeWalk {
       s.past = past;
       s.n = n;
       int first;
-      const int tiles = tree_item_tiles(p, past, n, t, s.lo, first), places = tiles + kItemPlaces;
+      const int tiles = tree_item_tiles(p, past, n, t, s.lo, first), places = tiles + p.item_places;
       const int take = places - into < end - (int)x ? places - into : end - (int)x;
-      // the item's first kItemPlaces places stand for its fixed cost
-      const int from = into > kItemPlaces ? into - kItemPlaces : 0;
-      const int to = into + take > kItemPlaces ? into + take - kItemPlaces : 0;
+      // the item's first p.item_places places stand for its fixed cost
+      const int from = into > p.item_places ? into - p.item_places : 0;
+      const int to = into + take > p.item_places ? into + take - p.item_places : 0;
       s.j0 = first + from;
       s.count = to - from;
       s.slot = from == 0 && to == tiles ? -1 : tree_slot(piece, from == 0);

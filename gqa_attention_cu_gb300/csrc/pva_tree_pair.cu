@@ -41,16 +41,15 @@ struct PairCfg {
   static constexpr int KV_CHUNK = BN * 128;
   static constexpr int KV_TILE = CH * KV_CHUNK;
   static constexpr int OFF_RING = 2 * Q_TILE;
-  static constexpr int SLOTS_FIT = (232448 - 64 - 2048 - OFF_RING) / KV_TILE;
+  static constexpr int SLOTS_FIT = (232448 - kHeadBytes - OFF_RING) / KV_TILE;
   static constexpr int SLOTS = SLOTS_FIT < 16 ? SLOTS_FIT : 16;
   static_assert(SLOTS >= 4, "ring depth");
-  static constexpr int OFF_BAR = OFF_RING + SLOTS * KV_TILE;
-  static constexpr int SMEM = OFF_BAR + 1024 + 1024;
+  static constexpr int SMEM = kHeadBytes + OFF_RING + SLOTS * KV_TILE;
   static constexpr int TMEM_COLS = 512;
   static constexpr int COL_S = 0;
   static constexpr int COL_O = 2 * BN;
   static_assert(COL_O + 2 * D <= TMEM_COLS, "TMEM budget");
-  static_assert(SMEM <= 232448 - 64, "shared memory budget");
+  static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct ItemSlot {
@@ -64,8 +63,10 @@ struct Bars {
   uint64_t ring_full[16], ring_empty[16];
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   ItemSlot items[kItemSlots];
+  uint32_t tmem_base;
+  int abort;
 };
-static_assert(sizeof(Bars) <= 1024, "barrier block");
+static_assert(sizeof(Bars) <= kHeadBytes, "barriers and segments");
 
 // Whether the item's second tile has rows.
 __device__ __forceinline__ bool has_second(const TreeParams& p, const TreeSegment& s) {
@@ -79,29 +80,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tmap_v) {
   using C = PairCfg<D>;
   constexpr int BN = C::BN;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (misplaced(smem_raw, p.status)) return;
+  Bars* bars = reinterpret_cast<Bars*>(smem_raw);
+  uint8_t* smem = smem_raw + kHeadBytes;
   uint8_t* ring = smem + C::OFF_RING;
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
-  __shared__ uint32_t s_tmem_base;
-  __shared__ int s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = p.status;
-  volatile int* abort = &s_abort;
+  volatile int* abort = &bars->abort;
 
   if (threadIdx.x == 0) {
-    s_abort = 0;
+    bars->abort = 0;
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->drain, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x], 32 * kGroupWarps);
+      mbar_init(&bars->p_full[x], kGroupWarps);
       mbar_init(&bars->o_ready[x], 1);
       mbar_init(&bars->o_done[x], 1);
-      mbar_init(&bars->o_free[x], 32 * kGroupWarps);
+      mbar_init(&bars->o_free[x], kGroupWarps);
     }
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(&bars->ring_full[s], 1);
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc<C::TMEM_COLS>(&s_tmem_base);
+  if (warp == 1) tmem_alloc<C::TMEM_COLS>(&bars->tmem_base);
   if (warp == 0 && lane == 0) {
     prefetch_tensor_map(&tmap_q);
     prefetch_tensor_map(&tmap_k);
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem_base;
+  const uint32_t tmem = bars->tmem_base;
   allow_next_grid();
   wait_prior_grid();
 
@@ -313,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any_own = __any_sync(0xffffffffu, own);
       const int total = s.past + s.n;
       const RowView view = row_view(p, s, node);
-      RowState st(own);
+      RowState st;
+      RowAlone alone;
       for (int j = 0; j < n; ++j, ++tiles) {
         const int k0 = (s.j0 + j) * BN;
         // the first tile's warps clean V for both: its product is issued first
@@ -325,26 +325,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(&bars->s_full[x], tiles & 1))) break;
         if (any_own) {
           tc_fence_after();
-          const float alpha = softmax_tile<T, BN, CAP>(p, view, s.past, k0, t_s, s_mul, cap_mul, st);
+          float alpha;
+          softmax_columns<T, BN, CAP>(p, view, s.past, k0, t_s, s_mul, cap_mul, alone, st, alpha);
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // O must hold PV(j-1); every earlier phase has passed, since S(j)
             // was issued after it, in order
             if (!(ok = wait(&bars->o_ready[x], (tiles - 1) & 1))) break;
             tc_fence_after();
-            scale_o<D>(t_o, alpha);
+            scale_o(t_o, Columns{0, D}, alpha);
           }
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&bars->p_full[x]);
+        warp_arrive(&bars->p_full[x]);
       }
       if (!ok) break;
       if (!(ok = wait(&bars->o_done[x], done & 1))) break;
       ++done;
       tc_fence_after();
-      if (any_own) store_row<T, D>(p, s, t_o, own, row, node, st.m, st.l);
+      if (any_own) store_row<T, D>(p, s, t_o, own, row, node, Columns{0, D}, st.m, st.l);
       tc_fence_before();
-      mbar_arrive(&bars->o_free[x]);
+      warp_arrive(&bars->o_free[x]);
     }
   }
 

@@ -9,7 +9,7 @@
 // deep as shared memory allows; the tile arithmetic of one 128-row tile stays
 // below the time its bytes take.
 //
-// Per CTA (192 threads):
+// Per CTA (320 threads):
 //   warp 0      TMA producer: walks the piece's segments, publishes each one
 //               through a ring in shared memory, and loads the Q tile, then
 //               K_j and V_j, into one ring of slots.  Pages shorter than a key
@@ -17,8 +17,17 @@
 //   warp 1      MMA issuer and TMEM owner.  S = Q K^T (Q in TMEM) is
 //               double-buffered, so S(j+1) runs while tile j is exponentiated;
 //               P(j) replaces S(j) and feeds O += P V with A from TMEM.
-//   warps 2..5  softmax and epilogue, one thread per query row.
+//   warps 2..9  softmax and epilogue, two threads per query row, each with half
+//               of a tile's columns: a tile's latency is what a short request
+//               and a piece's last tiles wait for (a thread per row: 22.2
+//               against 20.1 us for one request with 8 nodes on 500 rows).
 // TMEM: S buffers [0, BN) and [BN, 2 BN), O [2 BN, 2 BN + D), Q after it.
+//
+// The rotated queries come in two parts, rounded to the storage type and the
+// rest rounded again, and S adds the products of both: the second costs d / 16
+// MMA steps of a time the copies leave over, and takes one of the three equal
+// roundings (queries, weights, output) out of the result.  At d = 256 tensor
+// memory holds the first part only.
 //
 // Masks: a row sees the cache rows [lo, past) and its ancestors among the new
 // rows.  Tiles wholly inside that range of every row of a warp need no mask;
@@ -33,9 +42,9 @@ namespace {
 
 using namespace tile;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kItemSlots = 4;
-constexpr int kSoftmaxWarps = 4;
+constexpr int kSoftmaxWarps = 8;
 
 template <int D>
 struct TreeCfg {
@@ -46,18 +55,18 @@ struct TreeCfg {
   static constexpr int KV_TILE = CH * KV_CHUNK;   // one ring slot
   static constexpr int Q_PER_SLOT = KV_TILE / Q_CHUNK;
   static_assert(Q_PER_SLOT >= 1, "a Q chunk fits a ring slot");
-  static constexpr int Q_SLOTS = (CH + Q_PER_SLOT - 1) / Q_PER_SLOT;
-  static constexpr int SLOTS_FIT = (232448 - 64 - 2048) / KV_TILE;
+  static constexpr int Q_PARTS = tree_q_parts(D);
+  static constexpr int Q_SLOTS = (CH + Q_PER_SLOT - 1) / Q_PER_SLOT;  // of one part
+  static constexpr int SLOTS_FIT = (232448 - kHeadBytes) / KV_TILE;
   static constexpr int SLOTS = SLOTS_FIT < 16 ? SLOTS_FIT : 16;
-  static_assert(SLOTS >= Q_SLOTS + 2, "ring depth");
-  static constexpr int OFF_BAR = SLOTS * KV_TILE;
-  static constexpr int SMEM = OFF_BAR + 1024 + 1024;  // barriers and segments + alignment slack
+  static_assert(SLOTS >= Q_PARTS * Q_SLOTS + 2, "ring depth");
+  static constexpr int SMEM = kHeadBytes + SLOTS * KV_TILE;
   static constexpr int TMEM_COLS = 512;
   static constexpr int COL_S = 0;
   static constexpr int COL_O = 2 * BN;
   static constexpr int COL_Q = COL_O + D;
-  static_assert(COL_Q + D / 2 <= TMEM_COLS, "TMEM budget");
-  static_assert(SMEM <= 232448 - 64, "shared memory budget");
+  static_assert(COL_Q + Q_PARTS * D / 2 <= TMEM_COLS, "TMEM budget");
+  static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct ItemSlot {
@@ -68,11 +77,15 @@ struct ItemSlot {
 struct Bars {
   uint64_t q_tmem, o_ready, o_done, o_free, drain;
   uint64_t s_full[2], p_full[2];
+  uint64_t meet[4];
   uint64_t ring_full[16], ring_empty[16];
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   ItemSlot items[kItemSlots];
+  float rows[2][kTcRows][2];  // [turn][row][half]
+  uint32_t tmem_base;
+  int abort;
 };
-static_assert(sizeof(Bars) <= 1024, "barrier block");
+static_assert(sizeof(Bars) <= kHeadBytes, "barriers, segments and meeting places");
 
 template <typename T, int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -81,27 +94,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_v) {
   using C = TreeCfg<D>;
   constexpr int BN = C::BN;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
-  __shared__ uint32_t s_tmem_base;
-  __shared__ int s_abort;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (misplaced(smem_raw, p.status)) return;
+  Bars* bars = reinterpret_cast<Bars*>(smem_raw);
+  uint8_t* smem = smem_raw + kHeadBytes;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = p.status;
-  volatile int* abort = &s_abort;
+  volatile int* abort = &bars->abort;
+  const int q_slots = C::Q_SLOTS * (C::Q_PARTS == 2 && p.q_parts == 2 ? 2 : 1);
 
   if (threadIdx.x == 0) {
-    s_abort = 0;
-    mbar_init(&bars->q_tmem, 32 * kSoftmaxWarps);
+    bars->abort = 0;
+    mbar_init(&bars->q_tmem, kSoftmaxWarps);
     mbar_init(&bars->o_ready, 1);
     mbar_init(&bars->o_done, 1);
-    mbar_init(&bars->o_free, 32 * kSoftmaxWarps);
+    mbar_init(&bars->o_free, kSoftmaxWarps);
+    for (int w = 0; w < 4; ++w) mbar_init(&bars->meet[w], 2);
     mbar_init(&bars->drain, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
-      mbar_init(&bars->p_full[b], 32 * kSoftmaxWarps);
+      mbar_init(&bars->p_full[b], kSoftmaxWarps);
     }
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(&bars->ring_full[s], 1);
@@ -113,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc<C::TMEM_COLS>(&s_tmem_base);
+  if (warp == 1) tmem_alloc<C::TMEM_COLS>(&bars->tmem_base);
   if (warp == 0 && lane == 0) {
     prefetch_tensor_map(&tmap_q);
     prefetch_tensor_map(&tmap_k);
@@ -122,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem_base;
+  const uint32_t tmem = bars->tmem_base;
   allow_next_grid();
   wait_prior_grid();
 
@@ -152,15 +165,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = publish(v))) break;
       const TreeSegment& s = v.s;
       const int plane_q = s.b * p.Hkv + s.h;
-      for (int qs = 0; ok && qs < C::Q_SLOTS; ++qs, ++loads) {
+      for (int qs = 0; ok && qs < q_slots; ++qs, ++loads) {
         const int sl = loads % C::SLOTS;
         if (!(ok = wait(&bars->ring_empty[sl], ((loads / C::SLOTS) & 1) ^ 1))) break;
         if (lane == 0) {
-          const int c_lo = qs * C::Q_PER_SLOT, c_hi = min(C::CH, c_lo + C::Q_PER_SLOT);
+          const int part = qs / C::Q_SLOTS, c_lo = (qs % C::Q_SLOTS) * C::Q_PER_SLOT;
+          const int c_hi = min(C::CH, c_lo + C::Q_PER_SLOT);
           mbar_arrive_expect_tx(&bars->ring_full[sl], (uint32_t)(c_hi - c_lo) * C::Q_CHUNK);
           for (int c = c_lo; c < c_hi; ++c)
             tma_load_3d(smem + sl * C::KV_TILE + (c - c_lo) * C::Q_CHUNK, &tmap_q,
-                        &bars->ring_full[sl], c * 64, s.t * kTcRows, plane_q);
+                        &bars->ring_full[sl], c * 64, s.t * kTcRows, part * p.B * p.Hkv + plane_q);
         }
         __syncwarp();
       }
@@ -223,6 +237,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts(tmem + C::COL_S + (T_ & 1) * BN, tmem + C::COL_Q + kk * 8,
                  sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s,
                  kk > 0 ? 1u : 0u);
+        if (q_slots > C::Q_SLOTS) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ts(tmem + C::COL_S + (T_ & 1) * BN, tmem + C::COL_Q + D / 2 + kk * 8,
+                   sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s, 1u);
+        }
         mma_commit(&bars->s_full[T_ & 1]);
         mma_commit(&bars->ring_empty[L % C::SLOTS]);
       }
@@ -239,9 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(&bars->q_tmem, q_cnt & 1))) break;
       tc_fence_after();
       if (leader)
-        for (int qs = 0; qs < C::Q_SLOTS; ++qs)
+        for (int qs = 0; qs < q_slots; ++qs)
           mbar_arrive(&bars->ring_empty[(loads + qs) % C::SLOTS]);
-      loads += C::Q_SLOTS;
+      loads += q_slots;
       for (int j = 0; ok && j < 2 && j < n; ++j) {
         if (!(ok = wait_slot(loads + 2 * j))) break;
         issue_s(gt + j, loads + 2 * j);
@@ -257,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + C::COL_O, tmem + C::COL_S + (T_ & 1) * BN + kk * 8,
+            mma_ts(tmem + C::COL_O, tmem + C::COL_S + (T_ & 1) * BN + p_column<BN>(kk),
                    sdesc_advance(va, kk * 16 * 128), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&bars->o_ready);
           if (j + 1 == n) mma_commit(&bars->o_done);
@@ -278,26 +298,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait(&bars->drain, 0);
   } else {
     // ------------------------------------------------- softmax + epilogue
-    const int quarter = warp & 3;  // TMEM lanes this warp may access
+    const int half = (warp - 2) >> 2;  // of the columns
+    const int quarter = warp & 3;      // TMEM lanes this warp may access
     const int r = quarter * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     const float s_mul = CAP ? p.scale / p.softcap : p.scale * kLog2e;
     const float cap_mul = p.softcap * kLog2e;
+    RowPair pair{&bars->rows[0][r][0], &bars->meet[quarter], half, abort, status};
     uint32_t gt = 0, taken = 0, done = 0;
     uint32_t lq = 0;  // ring loads accounted for (the producer's order)
     bool ok = true, q_pre = false;
     // Copies the next Q tile from its ring slots into TMEM.
     auto copy_q = [&]() -> bool {
       bool got = true;
-      for (int qs = 0; qs < C::Q_SLOTS; ++qs) {
+      for (int qs = 0; qs < q_slots; ++qs) {
         const uint32_t L = lq + qs;
         got = got && mbar_wait<false>(&bars->ring_full[L % C::SLOTS], (L / C::SLOTS) & 1, abort,
                                       status);
       }
       if (!__all_sync(0xffffffffu, got)) return false;
+      // the chunks of both parts, every other one each half's
+      const int chunks = q_slots > C::Q_SLOTS ? 2 * C::CH : C::CH;
 #pragma unroll 1
-      for (int c = 0; c < C::CH; ++c) {
-        const uint32_t L = lq + c / C::Q_PER_SLOT;
+      for (int i = half; i < chunks; i += 2) {
+        const int part = i / C::CH, c = i - part * C::CH;
+        const uint32_t L = lq + part * C::Q_SLOTS + c / C::Q_PER_SLOT;
+        const uint32_t t_q = t_lane + C::COL_Q + part * (D / 2) + c * 32;
         const uint8_t* src =
             smem + (L % C::SLOTS) * C::KV_TILE + (c % C::Q_PER_SLOT) * C::Q_CHUNK + r * 128;
         uint32_t w[32];
@@ -310,19 +336,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[4 * u + 3] = x.w;
         }
         if (D % 64 == 0 || c + 1 < C::CH) {
-          tmem_st32(t_lane + C::COL_Q + c * 32, w);
+          tmem_st32(t_q, w);
         } else {  // a 32-column tail chunk
           uint32_t w16[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) w16[e] = w[e];
-          tmem_st16(t_lane + C::COL_Q + c * 32, w16);
+          tmem_st16(t_q, w16);
         }
       }
       tmem_wait_st();
       fence_proxy_async_smem();  // the slots are refilled by the TMA unit next
       tc_fence_before();
-      mbar_arrive(&bars->q_tmem);
-      lq += C::Q_SLOTS;
+      warp_arrive(&bars->q_tmem);
+      lq += q_slots;
       return true;
     };
 
@@ -348,12 +374,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int total = s.past + s.n;
       const RowView view = row_view(p, s, node);
       const bool any_own = __any_sync(0xffffffffu, own);
-      RowState st(own);
+      RowState st;
 
       for (int j = 0; j < n; ++j) {
         const uint32_t T_ = gt + j;
         const int k0 = (s.j0 + j) * BN;
-        if (k0 < s.lo || k0 + BN > total) {
+        if (half == 0 && (k0 < s.lo || k0 + BN > total)) {
           // V rows outside the item's keys: zeros
           const uint32_t L = l0 + 2 * j + 1;
           ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->ring_full[L % C::SLOTS],
@@ -366,8 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (any_own) {
           tc_fence_after();
-          const uint32_t t_s = t_lane + C::COL_S + (T_ & 1) * BN;
-          const float alpha = softmax_tile<T, BN, CAP>(p, view, s.past, k0, t_s, s_mul, cap_mul, st);
+          const uint32_t t_s = t_lane + C::COL_S + (T_ & 1) * BN + half * (BN / 2);
+          float alpha;
+          ok = softmax_columns<T, BN / 2, CAP>(p, view, s.past, k0 + half * (BN / 2), t_s, s_mul, cap_mul,
+                                            pair, st, alpha);
+          if (!ok) break;
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // O must hold PV(j-1) before it is rescaled; PV(j-2) precedes S(j),
             // so the parity of the outstanding phase is unambiguous.
@@ -375,12 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_wait<false>(&bars->o_ready, (T_ - 1) & 1, abort, status));
             if (!ok) break;
             tc_fence_after();
-            scale_o<D>(t_lane + C::COL_O, alpha);
+            scale_o(t_lane + C::COL_O, half_columns<D>(half), alpha);
           }
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&bars->p_full[T_ & 1]);
+        warp_arrive(&bars->p_full[T_ & 1]);
       }
       if (!ok) break;
 
@@ -401,9 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++done;
       if (!ok) break;
       tc_fence_after();
-      if (any_own) store_row<T, D>(p, s, t_lane + C::COL_O, own, row, node, st.m, st.l);
+      if (any_own) {
+        float l;
+        if (!(ok = pair.exchange(st.l, l))) break;
+        store_row<T, D>(p, s, t_lane + C::COL_O, own, row, node, half_columns<D>(half), st.m, st.l + l);
+      }
       tc_fence_before();
-      mbar_arrive(&bars->o_free);
+      warp_arrive(&bars->o_free);
       gt += n;
     }
   }

@@ -1,5 +1,5 @@
 // Softmax of one key tile of the tree attention's tensor-core kernels: key
-// masks, row extremes and exponentials of one row per thread.
+// masks, row extremes and exponentials.
 //
 // Softcap: tanh(t) of t = s * scale / softcap comes from the first three terms
 // of its series, t - t^3/3 + 2t^5/15 (error below the next term, 17/315 |t|^7 <
@@ -19,15 +19,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the max grows > 2^8
 constexpr float kSeriesLimit = 0.25f;      // |t| up to which tanh is summed
 
-// One bit per key of a tile, for one query row.
-template <int BN>
-struct Mask {
-  uint32_t w[BN / 32];
-};
-
-template <int BN, bool MASKED>
-__device__ __forceinline__ bool seen(const Mask<BN>& m, int c) {
-  return !MASKED || ((m.w[c >> 5] >> (c & 31)) & 1u);
+// Whether a row sees key c of 32, from its mask (one bit per key).
+template <bool MASKED>
+__device__ __forceinline__ bool seen(uint32_t mask, int c) {
+  return !MASKED || ((mask >> c) & 1u);
 }
 
 // Bits [lo, hi) of 32.
@@ -52,63 +47,57 @@ __device__ __forceinline__ RowView row_view(const TreeParams& p, const TreeSegme
   v.anc = p.parents ? p.mask + ((size_t)s.b * p.T + node) * p.W32 : nullptr;
   return v;
 }
-// The mask of the keys [k0, k0 + BN).
-template <int BN>
-__device__ __forceinline__ Mask<BN> row_mask(const TreeParams& p, const RowView& v, int past,
+// The mask of the keys [k0, k0 + 32).
+__device__ __forceinline__ uint32_t row_mask(const TreeParams& p, const RowView& v, int past,
                                              int k0) {
-  Mask<BN> m;
-#pragma unroll
-  for (int w = 0; w < BN / 32; ++w) {
-    const int key = k0 + 32 * w, first = key - past;
-    m.w[w] = bit_range(v.lo - key, v.hi - key);
-    // `first` is the node that the word's first key stands for
-    if (v.anc && first > -32 && first < 32 * p.W32) {
-      const int word = first >> 5;
-      const uint32_t a = word >= 0 ? v.anc[word] : 0u;
-      const uint32_t b = word + 1 < p.W32 ? v.anc[word + 1] : 0u;
-      m.w[w] |= __funnelshift_r(a, b, first & 31);
-    }
+  uint32_t m = bit_range(v.lo - k0, v.hi - k0);
+  const int first = k0 - past;  // the node that the first key stands for
+  if (v.anc && first > -32 && first < 32 * p.W32) {
+    const int word = first >> 5;
+    const uint32_t a = word >= 0 ? v.anc[word] : 0u;
+    const uint32_t b = word + 1 < p.W32 ? v.anc[word + 1] : 0u;
+    m |= __funnelshift_r(a, b, first & 31);
   }
   return m;
 }
 
-// Largest score of 32 columns of a tile (c0: the first), and with a softcap the
-// smallest, for the series' range.
-template <int BN, bool MASKED, bool CAP>
-__device__ __forceinline__ void extremes(const uint32_t (&v)[32], int c0, const Mask<BN>& m,
-                                         float& mx, float& mn) {
+// Largest of 32 scores, and with a softcap the smallest, for the series' range.
+template <bool MASKED, bool CAP>
+__device__ __forceinline__ void extremes(const uint32_t (&v)[32], uint32_t m, float& mx,
+                                         float& mn) {
   const float ninf = __int_as_float(0xff800000), pinf = __int_as_float(0x7f800000);
-  float a[2] = {mx, ninf}, b[2] = {mn, pinf};
+  float a[4] = {mx, ninf, ninf, ninf}, b[2] = {mn, pinf};
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     const float x0 = __uint_as_float(v[e]), x1 = __uint_as_float(v[e + 1]);
-    const bool s0 = seen<BN, MASKED>(m, c0 + e), s1 = seen<BN, MASKED>(m, c0 + e + 1);
-    float& t = a[(e >> 1) & 1];
+    const bool s0 = seen<MASKED>(m, e), s1 = seen<MASKED>(m, e + 1);
+    float& t = a[(e >> 1) & 3];
     t = fmax3f(t, s0 ? x0 : ninf, s1 ? x1 : ninf);
     if (CAP) {
       float& u = b[(e >> 1) & 1];
       u = fmin3f(u, s0 ? x0 : pinf, s1 ? x1 : pinf);
     }
   }
-  mx = fmaxf(a[0], a[1]);
+  mx = fmaxf(fmax3f(a[0], a[1], a[2]), a[3]);
   if (CAP) mn = fminf(b[0], b[1]);
 }
 
-// 2^(x - m) over 32 columns, added to the two partial sums, and P as 16-bit
-// pairs.  MODE 0: x = s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by
-// its series (1) or by exp (2).  P is rounded to the storage type for the
+// 2^(x - m) of 32 scores, added to the two partial sums, and P as 16-bit pairs.
+// MODE 0: x = s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by its
+// series (1) or by exp (2).  P is rounded to the storage type for the
 // tensor-core product: at most half a step of each weight, as V's own elements
 // carry; the row sum adds the fp32 values.
-template <typename T, int BN, int MODE, bool MASKED>
-__device__ __forceinline__ void exponentials(const uint32_t (&v)[32], int c0, const Mask<BN>& m,
-                                             float s_mul, float cap_mul, float m_eff,
-                                             float2 (&acc)[2], uint32_t* pw) {
+template <typename T, int MODE, bool MASKED>
+__device__ __forceinline__ void exponentials(const uint32_t (&v)[32], uint32_t m, float s_mul,
+                                             float cap_mul, float m_eff, float2 (&acc)[2],
+                                             uint32_t (&pw)[16]) {
   const float ninf = __int_as_float(0xff800000);
   const float2 z = make_float2(0.0f, 0.0f);
   const float2 mul2 = make_float2(s_mul, s_mul), neg_m = make_float2(-m_eff, -m_eff);
-  const float2 a2 = make_float2(cap_mul, cap_mul);
-  const float2 c1 = make_float2(cap_mul * (-1.0f / 3.0f), cap_mul * (-1.0f / 3.0f));
-  const float2 c2 = make_float2(cap_mul * (2.0f / 15.0f), cap_mul * (2.0f / 15.0f));
+  // cap_mul * tanh(u) with u = s * s_mul, as a polynomial in s
+  const float q1 = cap_mul * s_mul, q3 = q1 * s_mul * s_mul * (-1.0f / 3.0f);
+  const float q5 = q1 * (s_mul * s_mul) * (s_mul * s_mul) * (2.0f / 15.0f);
+  const float2 c1 = make_float2(q1, q1), c3 = make_float2(q3, q3), c5 = make_float2(q5, q5);
 #pragma unroll
   for (int g = 0; g < 16; g += 8) {
     float2 x[8];
@@ -119,14 +108,14 @@ __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], int c0, co
       if (MODE == 0) {
         x[k] = ffma2(s, mul2, neg_m);
       } else if (MODE == 1) {
-        const float2 u = ffma2(s, mul2, z), w = ffma2(u, u, z);
-        x[k] = ffma2(u, ffma2(w, ffma2(w, c2, c1), a2), neg_m);
+        const float2 w = ffma2(s, s, z);
+        x[k] = ffma2(s, ffma2(w, ffma2(w, c5, c3), c1), neg_m);
       } else {
         x[k].x = fmaf(cap_mul, tanh_via_exp2(s.x * s_mul), -m_eff);
         x[k].y = fmaf(cap_mul, tanh_via_exp2(s.y * s_mul), -m_eff);
       }
-      x[k].x = seen<BN, MASKED>(m, c0 + e) ? x[k].x : ninf;
-      x[k].y = seen<BN, MASKED>(m, c0 + e + 1) ? x[k].y : ninf;
+      x[k].x = seen<MASKED>(m, e) ? x[k].x : ninf;
+      x[k].y = seen<MASKED>(m, e + 1) ? x[k].y : ninf;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2_approx(x[k].x), ex2_approx(x[k].y));
@@ -138,162 +127,179 @@ __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], int c0, co
   }
 }
 
-// The running state of one query row.
+// The running state of a query row, or of half of one.
 struct RowState {
-  float m;            // reference of the exponentials, base-2 units; -inf: no key seen yet
-  float l = 0.0f;     // sum of 2^(x - m)
-  bool wide = false;  // the warp has met scores beyond the series' range
-  // Lanes without a row have a reference from the start: they ask for nothing.
-  __device__ __forceinline__ explicit RowState(bool own) : m(own ? -INFINITY : 0.0f) {}
+  float m = -INFINITY;  // reference of the exponentials, base-2 units (the row's)
+  float l = 0.0f;       // sum of 2^(x - m) over this thread's columns
 };
 
-// The reference of rows that see their first keys in this tile: its maximum.
-// (Their O and l are zero, so nothing has to be scaled.)
-template <int BN, bool CAP, bool MASKED>
-__device__ __forceinline__ void first_reference(uint32_t t_s, const Mask<BN>& mk, float s_mul,
-                                                float cap_mul, RowState& st) {
-  const float ninf = __int_as_float(0xff800000);
-  float mx = ninf, mn = 0.0f;
-  uint32_t v[2][32];
-  tmem_ld32(t_s, v[0]);
-#pragma unroll
-  for (int c = 0; c < BN / 32; ++c) {
-    tmem_wait_ld_of(v[c & 1]);
-    if (c + 1 < BN / 32) tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
-    extremes<BN, MASKED, false>(v[c & 1], c * 32, mk, mx, mn);
-  }
-  if (st.m == ninf && mx != ninf) st.m = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
+// One arrival for the whole warp, after what all of its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// Exponentials of a tile against the reference as it is, in one pass over the
-// scores: the next 32 columns are on their way from tensor memory while 32 are
-// worked on.  Returns false, with nothing changed, where a row's maximum passes
-// the reference by more than 2^8 (or a score the series' range).
-template <typename T, int BN, int MODE, bool MASKED>
-__device__ __forceinline__ bool softmax_fast(uint32_t t_s, const Mask<BN>& mk, float s_mul,
-                                             float cap_mul, RowState& st) {
-  constexpr bool CAP = MODE != 0;
-  float mx = __int_as_float(0xff800000), mn = __int_as_float(0x7f800000);
-  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-  uint32_t v[2][32], pw[BN / 2];
-  tmem_ld32(t_s, v[0]);
-#pragma unroll
-  for (int c = 0; c < BN / 32; ++c) {
-    tmem_wait_ld_of(v[c & 1]);
-    if (c + 1 < BN / 32) tmem_ld32(t_s + (c + 1) * 32, v[(c + 1) & 1]);
-    extremes<BN, MASKED, MODE == 1>(v[c & 1], c * 32, mk, mx, mn);
-    exponentials<T, BN, MODE, MASKED>(v[c & 1], c * 32, mk, s_mul, cap_mul, st.m, acc, pw + c * 16);
+// A row that one thread has to itself.
+struct RowAlone {
+  __device__ __forceinline__ bool exchange(float mine, float& other) {
+    other = mine;
+    return true;
   }
-  // the transforms rise, so the largest score is the row's maximum
-  // (a row that has seen no key yet has none here: every weight is 0)
-  const float top = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
-  bool again = mx != __int_as_float(0xff800000) && top > st.m + kRescaleThreshold;
-  if (MODE == 1)
-    again = again || (mx != __int_as_float(0xff800000) &&
-                      fmaxf(fabsf(mx * s_mul), fabsf(mn * s_mul)) > kSeriesLimit);
-  if (__any_sync(0xffffffffu, again)) return false;
-#pragma unroll
-  for (int c = 0; c < BN / 64; ++c) {
-    uint32_t w[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) w[e] = pw[c * 32 + e];
-    tmem_st32(t_s + c * 32, w);
+};
+
+// A row whose columns two threads share: warps of the same rows, one half each.
+// A value's place alternates between two, since a warp may be at the next tile's
+// scores while the other has yet to read this tile's value.
+struct RowPair {
+  float* place;   // [turn][row][half] in shared memory, at this thread's row
+  uint64_t* bar;  // of the two warps; an arrival each
+  int half;
+  volatile int* abort;
+  uint32_t* status;
+  uint32_t met = 0, turn = 0;
+  __device__ __forceinline__ bool meet() {
+    warp_arrive(bar);
+    return __all_sync(0xffffffffu, mbar_wait<false>(bar, met++ & 1, abort, status));
   }
-  const float2 r = fadd2(acc[0], acc[1]);
-  st.l += r.x + r.y;
+  // The other thread's value; false: the wait for it was given up.
+  __device__ __forceinline__ bool exchange(float mine, float& other) {
+    float* at = place + (turn & 1) * (2 * kTcRows);
+    ++turn;
+    at[half] = mine;
+    if (!meet()) return false;
+    other = at[half ^ 1];
+    return true;
+  }
+};
+
+// The kernels' shared memory: barriers, segments and the rows' meeting places
+// first, then the tiles, which have to lie on 1024-byte boundaries.  The first
+// part fills the 3 KB that the largest rings leave, so there is no room to round
+// addresses up: the kernels use no other shared memory, whose start then is such
+// a boundary, and refuse to run if it is not.
+constexpr int kHeadBytes = 3072;
+__device__ __forceinline__ bool misplaced(const void* smem, uint32_t* status) {
+  if ((smem_u32(smem) & 1023) == 0) return false;
+  if (threadIdx.x == 0) atomicOr(status, PVA_DEV_WAIT_TIMEOUT);
   return true;
 }
 
-// The same in two passes, maximum first; moves the reference where the maximum
-// passes it by more than 2^8, and returns the factor O then has to be scaled by.
-template <typename T, int BN, bool CAP>
-__device__ __forceinline__ float softmax_full(uint32_t t_s, const Mask<BN>& mk, float s_mul,
-                                              float cap_mul, RowState& st) {
+// Softmax of N score columns of this thread's row (TMEM address t_s, keys [k0, k0
+// + N)): P over the first N / 2 of them.  The reference moves where the row's
+// maximum passes it by more than 2^8; alpha is the factor that O then has to be
+// scaled by.  All warps of the rows call; false: a wait was given up.
+//
+// Tiles without a mask (and without a softcap) are read once and worked on in
+// registers.  The others go over the columns twice, 32 at a time in a loop:
+// reading tensor memory again is about 18 cycles, while unrolled code for every
+// kind of mask and softcap spills and does not stay in the instruction cache
+// (a window and a softcap at d = 64, 500-token chunks: 214 us, in a loop 189 us;
+// but 2048-token chunks of 8 sequences at d = 128: 1.13 ms, in a loop 1.26 ms).
+template <typename T, int N, bool CAP, typename Row>
+__device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowView& view, int past,
+                                                int k0, uint32_t t_s, float s_mul, float cap_mul,
+                                                Row& others, RowState& st, float& alpha) {
   const float NEG_INF = __int_as_float(0xff800000);
-  float mx = NEG_INF, mn = __int_as_float(0x7f800000);
-  uint32_t v[32];
-#pragma unroll
-  for (int c = 0; c < BN / 32; ++c) {
-    tmem_ld32(t_s + c * 32, v);
-    tmem_wait_ld_of(v);
-    extremes<BN, true, CAP>(v, c * 32, mk, mx, mn);
-  }
-  float mt = NEG_INF;
-  if (mx != NEG_INF) mt = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
-  float alpha = 1.0f;
-  if (mt > st.m + kRescaleThreshold) {
-    alpha = ex2_approx(st.m - mt);  // 0 when m is -inf
-    st.m = mt;
-  }
-  const float m_eff = st.m == NEG_INF ? 0.0f : st.m;
-  if (CAP)
-    st.wide = __any_sync(0xffffffffu, mx != NEG_INF && fmaxf(fabsf(mx * s_mul), fabsf(mn * s_mul)) >
-                                                           kSeriesLimit);
-  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-  // P of 64 columns lies over the first 32 of them: columns already read
-#pragma unroll
-  for (int half = 0; half < BN / 64; ++half) {
-    uint32_t pw[32];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      tmem_ld32(t_s + half * 64 + c * 32, v);
-      tmem_wait_ld_of(v);
-      const int c0 = half * 64 + c * 32;
-      if (!CAP)
-        exponentials<T, BN, 0, true>(v, c0, mk, s_mul, cap_mul, m_eff, acc, pw + c * 16);
-      else if (!st.wide)
-        exponentials<T, BN, 1, true>(v, c0, mk, s_mul, cap_mul, m_eff, acc, pw + c * 16);
-      else
-        exponentials<T, BN, 2, true>(v, c0, mk, s_mul, cap_mul, m_eff, acc, pw + c * 16);
+  const bool all = __all_sync(0xffffffffu, view.lo <= k0 && view.hi >= k0 + N);
+  float mx = NEG_INF, mn = __int_as_float(0x7f800000), m_eff;
+  // mx: this thread's largest score; the transforms rise, so the row's largest
+  // score is its maximum
+  auto new_maximum = [&]() -> bool {
+    float other;
+    if (!others.exchange(mx, other)) return false;
+    mx = fmaxf(mx, other);
+    float mt = NEG_INF;
+    if (mx != NEG_INF) mt = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
+    alpha = 1.0f;
+    if (mt > st.m + kRescaleThreshold) {
+      alpha = ex2_approx(st.m - mt);  // 0 when m is -inf
+      st.m = mt;
     }
-    tmem_st32(t_s + half * 32, pw);
+    m_eff = st.m == NEG_INF ? 0.0f : st.m;
+    return true;
+  };
+  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  if (!CAP && all) {
+    uint32_t v[N / 32][32];
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) tmem_ld32(t_s + c * 32, v[c]);
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) {
+      tmem_wait_ld_of(v[c]);
+      extremes<false, false>(v[c], 0u, mx, mn);
+    }
+    if (!new_maximum()) return false;
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) {
+      uint32_t pw[16];
+      exponentials<T, 0, false>(v[c], 0u, s_mul, cap_mul, m_eff, acc, pw);
+      tmem_st16(t_s + c * 16, pw);
+    }
+  } else {
+    uint32_t v[32];
+#pragma unroll 1
+    for (int c = 0; c < N; c += 32) {
+      tmem_ld32(t_s + c, v);
+      const uint32_t mask = all ? 0xffffffffu : row_mask(p, view, past, k0 + c);
+      tmem_wait_ld_of(v);
+      if (CAP && all)
+        extremes<false, CAP>(v, mask, mx, mn);
+      else
+        extremes<true, CAP>(v, mask, mx, mn);
+    }
+    // a softcap's series has to hold for the warp's own columns
+    const bool series =
+        CAP && __all_sync(0xffffffffu, mx == NEG_INF || fmaxf(fabsf(mx * s_mul), fabsf(mn * s_mul)) <=
+                                                            kSeriesLimit);
+    if (!new_maximum()) return false;
+#pragma unroll 1
+    for (int c = 0; c < N; c += 32) {
+      tmem_ld32(t_s + c, v);
+      const uint32_t mask = all ? 0xffffffffu : row_mask(p, view, past, k0 + c);
+      tmem_wait_ld_of(v);
+      uint32_t pw[16];
+      if (!CAP)
+        exponentials<T, 0, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
+      else if (series && all)
+        exponentials<T, 1, false>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
+      else if (series)
+        exponentials<T, 1, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
+      else
+        exponentials<T, 2, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
+      // over columns whose scores have been read in this pass
+      tmem_st16(t_s + c / 2, pw);
+    }
   }
   const float2 r = fadd2(acc[0], acc[1]);
   st.l = st.l * alpha + r.x + r.y;
-  return alpha;
+  return true;
 }
 
-// Softmax of the tile at TMEM address t_s (BN score columns of this thread's
-// row, keys [k0, k0 + BN)): P over its first BN / 2 columns.  Returns the factor
-// O has to be scaled by.  A whole warp calls.
-template <typename T, int BN, bool CAP>
-__device__ __forceinline__ float softmax_tile(const TreeParams& p, const RowView& view, int past,
-                                              int k0, uint32_t t_s, float s_mul, float cap_mul,
-                                              RowState& st) {
-  const bool all = __all_sync(0xffffffffu, view.lo <= k0 && view.hi >= k0 + BN);
-  Mask<BN> mk;
-  if (!all) {
-    mk = row_mask<BN>(p, view, past, k0);
-  } else {
-#pragma unroll
-    for (int w = 0; w < BN / 32; ++w) mk.w[w] = 0xffffffffu;
-  }
-  if (__any_sync(0xffffffffu, st.m == __int_as_float(0xff800000))) {
-    if (all)
-      first_reference<BN, CAP, false>(t_s, mk, s_mul, cap_mul, st);
-    else
-      first_reference<BN, CAP, true>(t_s, mk, s_mul, cap_mul, st);
-  }
-  bool done;
-  if (!CAP)
-    done = all ? softmax_fast<T, BN, 0, false>(t_s, mk, s_mul, cap_mul, st)
-               : softmax_fast<T, BN, 0, true>(t_s, mk, s_mul, cap_mul, st);
-  else if (!st.wide)
-    done = all ? softmax_fast<T, BN, 1, false>(t_s, mk, s_mul, cap_mul, st)
-               : softmax_fast<T, BN, 1, true>(t_s, mk, s_mul, cap_mul, st);
-  else
-    done = softmax_fast<T, BN, 2, true>(t_s, mk, s_mul, cap_mul, st);
-  return done ? 1.0f : softmax_full<T, BN, CAP>(t_s, mk, s_mul, cap_mul, st);
+// Score column where the 16 weights of MMA step kk lie: each half's weights over
+// its own columns, so that no thread writes over scores another still reads.
+template <int BN>
+__device__ __forceinline__ int p_column(int kk) {
+  constexpr int steps = BN / 32;  // of one half
+  return kk < steps ? kk * 8 : BN / 2 + (kk - steps) * 8;
 }
 
-// O columns [0, D) at TMEM address t_o times f.
+// Columns [begin, end) of O that a thread of the row scales and stores.
+struct Columns {
+  int begin, end;
+};
 template <int D>
-__device__ __forceinline__ void scale_o(uint32_t t_o, float f) {
+__device__ __forceinline__ Columns half_columns(int half) {
+  constexpr int split = (D / 2 + 31) / 32 * 32;
+  return half ? Columns{split, D} : Columns{0, split};
+}
+
+// Columns of O (TMEM address t_o) times f.
+__device__ __forceinline__ void scale_o(uint32_t t_o, Columns cols, float f) {
 #pragma unroll 1
-  for (int c = 0; c < D; c += 32) {
+  for (int c = cols.begin; c < cols.end; c += 32) {
     uint32_t o[32];
     tmem_ld32(t_o + c, o);
-    tmem_wait_ld();
+    tmem_wait_ld_of(o);
 #pragma unroll
     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
     tmem_st32(t_o + c, o);
@@ -315,22 +321,23 @@ __device__ __forceinline__ void zero_v_rows(uint8_t* v_tile, int r, int k0, int 
   fence_proxy_async_smem();
 }
 
-// A row's result: O / l to the output, or the unnormalised sums to its slot.
+// Columns of a row's result: O / l to the output, or the unnormalised sums to its
+// slot.
 template <typename T, int D>
 __device__ __forceinline__ void store_row(const TreeParams& p, const TreeSegment& s, uint32_t t_o,
-                                          bool own, int row, int node, float m, float l) {
+                                          bool own, int row, int node, Columns cols, float m, float l) {
   const bool whole = s.slot < 0;
   const float inv = !whole ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
   T* out = static_cast<T*>(p.out) + (((size_t)s.b * p.T + node) * p.H + (size_t)s.h * p.G +
                                      (row - node * p.G)) * D;
   const size_t at = whole ? 0 : (size_t)s.slot * p.rows + (row - s.t * p.rows);
   float* part = p.part_o + at * D;
-  if (own && !whole) p.part_ml[at] = make_float2(m, l);
+  if (own && !whole && cols.begin == 0) p.part_ml[at] = make_float2(m, l);
 #pragma unroll 1
-  for (int c = 0; c < D; c += 32) {
+  for (int c = cols.begin; c < cols.end; c += 32) {
     uint32_t v[32];
     tmem_ld32(t_o + c, v);
-    tmem_wait_ld();
+    tmem_wait_ld_of(v);
     if (own && whole) {
 #pragma unroll
       for (int e = 0; e < 32; e += 8) {

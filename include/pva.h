@@ -411,8 +411,10 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  * scale, softcap, dtype, stream : as pva_forward.
  *
  * Arithmetic: products of dtype (f16/bf16 on tensor cores), scores, softmax and
- * sums in f32.  The rotated queries are rounded to dtype, as the keys in the
- * cache are, and so are the softmax weights that multiply V (f16/bf16).
+ * sums in f32.  The softmax weights that multiply V are rounded to dtype
+ * (f16/bf16).  Rotated queries are too in steps of more than 128 query rows per
+ * kv head (tokens * num_heads / kv_num_heads) and at head_size 256; otherwise
+ * what the rounding takes off them is multiplied as well.
  * Results do not depend on timing: parts of a split row are added in order.
  *
  * Limits: f16/bf16: head_size in {64, 96, 128, 192, 256}, 16-byte aligned

@@ -25,9 +25,9 @@ def axis_of_pair(half: int, n_axes: int, sections, interleaved: bool):
 
 
 def rope_rows(x, cos, sin, positions, sections=None, pairs_interleaved=False,
-              axes_interleaved=False, inverse=False):
+              axes_interleaved=False, inverse=False, keep_f32=False):
     """x [N, heads, d] (torch, any type) turned at positions [n_axes, N]; the
-    result in x's type."""
+    result in x's type, or as float32 before that rounding."""
     c, s = np.asarray(cos.float()), np.asarray(sin.float())
     half = c.shape[1]
     pos = np.asarray(positions, dtype=np.int64)
@@ -36,7 +36,7 @@ def rope_rows(x, cos, sin, positions, sections=None, pairs_interleaved=False,
     pair = np.arange(half)
     cr, sr = c[at, pair][:, None], s[at, pair][:, None]
     y = rotate(x.float().numpy(), cr, -sr if inverse else sr, 2 * half, pairs_interleaved)
-    return torch.from_numpy(y).to(x.dtype)
+    return torch.from_numpy(y) if keep_f32 else torch.from_numpy(y).to(x.dtype)
 
 
 def ancestors(parents, n: int):
@@ -79,7 +79,8 @@ def tree_step(q, k_new, v_new, k_cache, v_cache, past, parents=None, tree_lens=N
             n_axes = len(sections) if sections is not None else 1
             at = (np.tile(p0 + np.array(depth, dtype=np.int64), (n_axes, 1)) if positions is None
                   else np.asarray(positions)[:, b, :n])
-            qb = rope_rows(qb, cos, sin, at, sections, pairs_interleaved, axes_interleaved)
+            qb = rope_rows(qb, cos, sin, at, sections, pairs_interleaved, axes_interleaved,
+                           keep_f32=True)
             kb = rope_rows(kb, cos, sin, at, sections, pairs_interleaved, axes_interleaved)
         for i in range(n):
             blk, r = place(block_table, b, p0 + i, page)
@@ -106,16 +107,21 @@ def tree_step(q, k_new, v_new, k_cache, v_cache, past, parents=None, tree_lens=N
     return out, mass, spread, count, kc, vc
 
 
-def tolerance(out, mass, spread, count, d: int, dtype, v_max: float):
+def tolerance(out, mass, spread, count, d: int, dtype, v_max: float, q_rounded=False):
     """Largest deviation that the operator's roundings allow, element by element.
     Half a step of the type: once for the output (relative to it), and for
-    f16/bf16 once per softmax weight (relative to sum w |v|).  f32 arithmetic:
+    f16/bf16 once per softmax weight (relative to sum w |v|).  Rotated queries
+    of f16/bf16 are rounded once (q_rounded) or kept as a rounded value and its
+    rounded rest, off by half a step squared: each element's error reaches the
+    score times |k|, so by at most that much of |q|.|k|.  f32 arithmetic:
     a score of d products is off by at most d * 2^-23 * |q|.|k|, its exponential
     and softcap by a few 2^-21 of its size, which move a weight by expm1 of
     twice that; sums over the keys add (keys + 8) * 2^-23.  f16 weights below
     2^-14 of the largest are off by up to 2^-25 each instead."""
     half_step = torch.finfo(dtype).eps / 2
     err = d * 2.0 ** -23 * spread + 2.0 ** -20 * (spread + 1)
+    if dtype != torch.float32:
+        err = err + (half_step if q_rounded else half_step ** 2) * spread
     part = torch.expm1(2 * err) + (count + 8) * 2.0 ** -23
     if dtype != torch.float32:
         part = part + half_step * 1.01
