@@ -244,20 +244,16 @@ def _need(ok: bool, message: str) -> None:
         raise PvaError(PVA_ERR_INVALID_ARG, message)
 
 
-def _same_device(first, *others) -> int:
-    """Every tensor on the device of ``first``, which has to be the current one
-    if it is a GPU; returns its index."""
+def _device(first, *others) -> int:
+    """Index of the device of ``first``, which has to be the current one if it is
+    a GPU.  The ``_plain`` checks compare the other tensors' indices with it; on
+    the host, where the index says little, ``others`` are compared in full."""
     at = first.get_device()
-    if at < 0:  # the host (or no storage): compare in full
+    if at < 0:
         for t in others:
             _need(t is None or t.device == first.device, "the tensors are on different devices")
-        return at
-    for t in others:
-        if t is not None and t.get_device() != at:
-            raise PvaError(PVA_ERR_INVALID_ARG, "the tensors are on different devices")
-    if at != torch.cuda.current_device():
-        raise PvaError(PVA_ERR_INVALID_ARG,
-                       f"the tensors are on cuda:{at}, which is not the current device")
+    elif at != torch._C._cuda_getDevice():
+        _need(False, f"the tensors are on cuda:{at}, which is not the current device")
     return at
 
 
@@ -269,24 +265,37 @@ def _stream_on(stream, device: int) -> int:
     return _stream_ptr(stream)
 
 
-def _plain(t, name: str, dtype, shape) -> None:
-    """A contiguous tensor of this type and shape."""
-    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        return
+def _plain(t, name: str, dtype, shape, at: int):
+    """The address of a contiguous tensor of this type and shape on device ``at``
+    (None: none)."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == at):
+        return t.data_ptr()
     _need(t.dtype is dtype, f"{name} must be {dtype}")
     _need(t.shape == shape, f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    _need(False, f"{name} must be contiguous")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+    _need(False, "the tensors are on different devices")
 
 
-def _rotary(cos_cache, sin_cache, sections):
-    """(rotary_dim, table rows, table type code, host sections or None)."""
+_sections = {}  # C arrays of the section lists met so far
+
+
+def _rotary(cos_cache, sin_cache, sections, at: int):
+    """(cos, sin, rotary_dim, table rows, table type code, host sections or None)."""
     _need(sin_cache is not None, "cos_cache and sin_cache come together")
     shape = cos_cache.shape
     _need(len(shape) == 2, "cos_cache must be [rows, rotary_dim / 2]")
-    _plain(cos_cache, "cos_cache", cos_cache.dtype, shape)
-    _plain(sin_cache, "sin_cache", cos_cache.dtype, shape)
-    host = None if sections is None else (ctypes.c_int32 * len(sections))(*sections)
-    return 2 * shape[1], shape[0], _type_code(cos_cache), host
+    host = None
+    if sections is not None:
+        key = tuple(sections)
+        host = _sections.get(key)
+        if host is None:
+            host = _sections[key] = (ctypes.c_int32 * len(key))(*key)
+    dtype = cos_cache.dtype
+    return (_plain(cos_cache, "cos_cache", dtype, shape, at),
+            _plain(sin_cache, "sin_cache", dtype, shape, at), 2 * shape[1], shape[0],
+            _type_code(cos_cache), host)
 
 
 _TYPE_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -307,36 +316,36 @@ def pva_block_tables(lens, block_table, held, free_blocks, free_count, page_size
     _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
     B, width = block_table.shape
     i32 = torch.int32
-    _plain(lens, "lens", i32, (B,))
-    _plain(held, "held", i32, (B,))
-    _plain(block_table, "block_table", i32, (B, width))
     _need(free_blocks.dim() == 1, "free_blocks must be [pool]")
-    _plain(free_blocks, "free_blocks", i32, free_blocks.shape)
-    _plain(free_count, "free_count", i32, (1,))
-    _plain(cu_new, "cu_new", i32, (B + 1,))
+    _need((cu_new is None) == (slot_map is None), "cu_new and slot_map come together")
+    slots = 0
     if slot_map is not None:
         _need(slot_map.dim() == 1, "slot_map must be [slots]")
-        _plain(slot_map, "slot_map", torch.int64, slot_map.shape)
-    _need((cu_new is None) == (slot_map is None), "cu_new and slot_map come together")
-    at = _same_device(block_table, lens, held, free_blocks, free_count, cu_new, slot_map)
+        slots = slot_map.shape[0]
+    at = _device(block_table, lens, held, free_blocks, free_count, cu_new, slot_map)
     _check((_lib or load_library()).pva_block_tables(
-        lens.data_ptr(), block_table.data_ptr(), held.data_ptr(), free_blocks.data_ptr(),
-        free_count.data_ptr(), _ptr_or_none(cu_new), _ptr_or_none(slot_map), B, width,
-        int(page_size), free_blocks.shape[0], 0 if slot_map is None else slot_map.shape[0],
-        _stream_on(stream, at)))
+        _plain(lens, "lens", i32, (B,), at),
+        _plain(block_table, "block_table", i32, (B, width), at),
+        _plain(held, "held", i32, (B,), at),
+        _plain(free_blocks, "free_blocks", i32, free_blocks.shape, at),
+        _plain(free_count, "free_count", i32, (1,), at),
+        _plain(cu_new, "cu_new", i32, (B + 1,), at),
+        _plain(slot_map, "slot_map", torch.int64, (slots,), at), B, width, int(page_size),
+        free_blocks.shape[0], slots, _stream_on(stream, at)))
 
 
-def _token_rows(t, name: str, like):
-    """Heads and token stride of a [tokens, heads, d] tensor whose tokens are
-    each contiguous."""
-    shape, want = t.shape, like.shape
-    if len(shape) != 3 or t.dtype is not like.dtype or shape[0] != want[0] or shape[2] != want[2]:
-        _need(False, f"{name} must be [tokens, heads, head_size] of one type with the others")
-    tokens, heads, d = shape
+def _token_rows(t, name: str, dtype, tokens: int, d: int, at: int):
+    """Address, heads and token stride of a [tokens, heads, d] tensor whose tokens
+    are each contiguous."""
+    shape = t.shape
+    if (len(shape) != 3 or t.dtype is not dtype or shape[0] != tokens or shape[2] != d
+            or t.get_device() != at):
+        _need(False, f"{name} must be [tokens, heads, head_size] of one type and device with the others")
+    heads = shape[1]
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
         _need(False, f"{name}: the heads of a token must be contiguous")
-    return heads, max(s0, heads * d) if tokens <= 1 else s0
+    return t.data_ptr(), heads, max(s0, heads * d) if tokens <= 1 else s0
 
 
 def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=None, sections=None,
@@ -353,45 +362,51 @@ def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=No
     _need(first is not None, "q or k is needed")
     _need(first.dim() == 3, "q and k must be [tokens, heads, head_size]")
     tokens, _, d = first.shape
+    dt = first.dtype
+    at = _device(first, q_out, k, k_out, v, cos_cache, sin_cache, position_ids, k_cache, v_cache,
+                 slot_map)
     H = Hkv = qs = ks = qos = kos = vs = 0
+    pq = pk = pqo = pko = pv = None
     if q is not None:
-        H, qs = _token_rows(q, "q", first)
+        pq, H, qs = _token_rows(q, "q", dt, tokens, d, at)
         _need(q_out is not None and q_out.shape == q.shape, "q_out must have q's shape")
-        _, qos = _token_rows(q_out, "q_out", first)
+        pqo, _, qos = _token_rows(q_out, "q_out", dt, tokens, d, at)
     else:
         _need(q_out is None, "q and q_out come together")
     if k is not None:
-        Hkv, ks = _token_rows(k, "k", first)
+        pk, Hkv, ks = _token_rows(k, "k", dt, tokens, d, at)
         if k_out is not None:
             _need(k_out.shape == k.shape, "k_out must have k's shape")
-            _, kos = _token_rows(k_out, "k_out", first)
+            pko, _, kos = _token_rows(k_out, "k_out", dt, tokens, d, at)
+    else:
+        _need(k_out is None, "k_out without k")
     _need(position_ids.dim() == 2, "position_ids must be [n_axes, tokens]")
     n_axes = position_ids.shape[0]
-    _plain(position_ids, "position_ids", torch.int64, (n_axes, tokens))
     _need(sections is None or len(sections) == n_axes, "sections needs one entry per axis")
-    rot, rows, code, host = _rotary(cos_cache, sin_cache, sections)
+    pos = _plain(position_ids, "position_ids", torch.int64, (n_axes, tokens), at)
+    pc, ps, rot, rows, code, host = _rotary(cos_cache, sin_cache, sections, at)
     blocks = page = 0
-    if k_cache is not None:
+    kc = vc = slots = None
+    if k_cache is None:
+        _need(v is None and v_cache is None and slot_map is None,
+              "v, v_cache and slot_map come with k_cache")
+    else:
         _need(k is not None and v is not None and v_cache is not None and slot_map is not None,
               "the cache write needs k, v, both caches and slot_map")
         _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_heads, page, head_size]")
-        blocks, page = k_cache.shape[0], k_cache.shape[2]
-        _plain(k_cache, "k_cache", first.dtype, (blocks, Hkv, page, d))
-        _plain(v_cache, "v_cache", first.dtype, (blocks, Hkv, page, d))
-        _plain(slot_map, "slot_map", torch.int64, (tokens,))
+        blocks, _, page, _ = k_cache.shape
+        kc = _plain(k_cache, "k_cache", dt, (blocks, Hkv, page, d), at)
+        vc = _plain(v_cache, "v_cache", dt, (blocks, Hkv, page, d), at)
+        slots = _plain(slot_map, "slot_map", torch.int64, (tokens,), at)
         _need(v.shape == k.shape, "v must have k's shape")
-        _, vs = _token_rows(v, "v", first)
-    at = _same_device(first, q_out, k, k_out, v, cos_cache, sin_cache, position_ids, k_cache,
-                      v_cache, slot_map)
+        pv, _, vs = _token_rows(v, "v", dt, tokens, d, at)
     if tokens == 0:
         return
     _check((_lib or load_library()).pva_rope_axes(
-        _ptr_or_none(q), _ptr_or_none(k), _ptr_or_none(q_out), _ptr_or_none(k_out),
-        cos_cache.data_ptr(), sin_cache.data_ptr(), position_ids.data_ptr(), tokens, H, Hkv, d, qs,
-        ks, qos, kos, rot, rows, int(bool(rotary_interleaved)), n_axes, host,
-        int(bool(axes_interleaved)), int(bool(inverse)), code, _ptr_or_none(v), vs,
-        _ptr_or_none(k_cache), _ptr_or_none(v_cache), _ptr_or_none(slot_map), blocks, page,
-        _type_code(first), _stream_on(stream, at)))
+        pq, pk, pqo, pko, pc, ps, pos, tokens, H, Hkv, d, qs, ks, qos, kos, rot, rows,
+        1 if rotary_interleaved else 0, n_axes, host, 1 if axes_interleaved else 0,
+        1 if inverse else 0, code, pv, vs, kc, vc, slots, blocks, page, _type_code(first),
+        _stream_on(stream, at)))
 
 
 def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: int,
@@ -408,46 +423,39 @@ def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: i
     optional rotation by cos/sin tables with position_ids int64 [n_axes, B, T]
     (None: past + depth); out [B, T, H, d]."""
     _need(q.dim() == 4, "q must be [B, tokens, num_heads, head_size]")
-    B, T, H, d = q.shape
+    B, T, _, d = q.shape
     H, Hkv = int(num_heads), int(kv_num_heads)
     dt, i32 = q.dtype, torch.int32
     _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_num_heads, page, head_size]")
-    blocks, page = k_cache.shape[0], k_cache.shape[2]
-    _plain(q, "q", dt, (B, T, H, d))
-    _plain(out, "out", dt, (B, T, H, d))
-    _plain(k_new, "k_new", dt, (B, T, Hkv, d))
-    _plain(v_new, "v_new", dt, (B, T, Hkv, d))
-    _plain(k_cache, "k_cache", dt, (blocks, Hkv, page, d))
-    _plain(v_cache, "v_cache", dt, (blocks, Hkv, page, d))
-    _plain(past_lens, "past_lens", i32, (B,))
-    _plain(parents, "parents", i32, (B, T))
-    _plain(tree_lens, "tree_lens", i32, (B,))
+    blocks, _, page, _ = k_cache.shape
+    at = _device(q, k_new, v_new, k_cache, v_cache, past_lens, out, parents, tree_lens, block_table,
+                 cos_cache, sin_cache, position_ids)
+    rows_q, rows_k, cache = (B, T, H, d), (B, T, Hkv, d), (blocks, Hkv, page, d)
     width = 0
     if block_table is not None:
         _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
         width = block_table.shape[1]
-        _plain(block_table, "block_table", i32, (B, width))
     rot = rows = code = 0
-    n_axes, host = 1, None
+    n_axes, pc, ps, pos, host = 1, None, None, None, None
     if cos_cache is not None:
-        n_axes = 1 if position_ids is None else position_ids.shape[0]
-        if position_ids is None and sections is not None:
+        if position_ids is not None:
+            n_axes = position_ids.shape[0]
+            pos = _plain(position_ids, "position_ids", torch.int64, (n_axes, B, T), at)
+        elif sections is not None:
             n_axes = len(sections)
-        _plain(position_ids, "position_ids", torch.int64, (n_axes, B, T))
         _need(sections is None or len(sections) == n_axes, "sections needs one entry per axis")
-        rot, rows, code, host = _rotary(cos_cache, sin_cache, sections)
+        pc, ps, rot, rows, code, host = _rotary(cos_cache, sin_cache, sections, at)
     else:
         _need(sin_cache is None and position_ids is None and sections is None,
               "positions and sections need the cos and sin tables")
-    at = _same_device(q, k_new, v_new, k_cache, v_cache, past_lens, out, parents, tree_lens,
-                      block_table, cos_cache, sin_cache, position_ids)
     _check((_lib or load_library()).pva_gqa_tree(
-        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        past_lens.data_ptr(), _ptr_or_none(tree_lens), _ptr_or_none(parents),
-        _ptr_or_none(block_table), _ptr_or_none(cos_cache), _ptr_or_none(sin_cache),
-        _ptr_or_none(position_ids), out.data_ptr(), B, T, blocks, page,
-        width, H, Hkv, d, rot, rows,
-        int(bool(rotary_interleaved)), n_axes, host, int(bool(axes_interleaved)), code,
+        _plain(q, "q", dt, rows_q, at), _plain(k_new, "k_new", dt, rows_k, at),
+        _plain(v_new, "v_new", dt, rows_k, at), _plain(k_cache, "k_cache", dt, cache, at),
+        _plain(v_cache, "v_cache", dt, cache, at), _plain(past_lens, "past_lens", i32, (B,), at),
+        _plain(tree_lens, "tree_lens", i32, (B,), at), _plain(parents, "parents", i32, (B, T), at),
+        _plain(block_table, "block_table", i32, (B, width), at), pc, ps, pos,
+        _plain(out, "out", dt, rows_q, at), B, T, blocks, page, width, H, Hkv, d, rot, rows,
+        1 if rotary_interleaved else 0, n_axes, host, 1 if axes_interleaved else 0, code,
         float(scale), float(softcap), int(local_window), _type_code(q), _stream_on(stream, at)))
 
 
@@ -459,27 +467,23 @@ def pva_kvcache_accept(k_cache, v_cache, past_lens, path, path_lens, new_lens, b
     [B, width], past_lens, path_lens, new_lens (= past + path_lens) int32 [B]."""
     _need(k_cache.dim() in (4, 5), "k_cache must be [layers,] [n_blocks, heads, page, head_size]")
     _need(path.dim() == 2, "path must be [B, width]")
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    blocks, Hkv, page, d = k_cache.shape[-4:]
+    shape = k_cache.shape
+    layers = shape[0] if len(shape) == 5 else 1
+    blocks, Hkv, page, d = shape[-4:]
     B, width = path.shape
-    i32 = torch.int32
-    _plain(k_cache, "k_cache", k_cache.dtype, k_cache.shape)
-    _plain(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
-    _plain(path, "path", i32, (B, width))
-    _plain(past_lens, "past_lens", i32, (B,))
-    _plain(path_lens, "path_lens", i32, (B,))
-    _plain(new_lens, "new_lens", i32, (B,))
+    i32, dt = torch.int32, k_cache.dtype
     table_width = 0
     if block_table is not None:
         _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
         table_width = block_table.shape[1]
-        _plain(block_table, "block_table", i32, (B, table_width))
-    at = _same_device(k_cache, v_cache, past_lens, path, path_lens, new_lens, block_table)
+    at = _device(k_cache, v_cache, past_lens, path, path_lens, new_lens, block_table)
     _check((_lib or load_library()).pva_kvcache_accept(
-        k_cache.data_ptr(), v_cache.data_ptr(), past_lens.data_ptr(), path.data_ptr(),
-        path_lens.data_ptr(), _ptr_or_none(block_table), new_lens.data_ptr(), B, width, layers,
-        blocks * Hkv * page * d, blocks, Hkv, page, d,
-        table_width, _type_code(k_cache), _stream_on(stream, at)))
+        _plain(k_cache, "k_cache", dt, shape, at), _plain(v_cache, "v_cache", dt, shape, at),
+        _plain(past_lens, "past_lens", i32, (B,), at), _plain(path, "path", i32, (B, width), at),
+        _plain(path_lens, "path_lens", i32, (B,), at),
+        _plain(block_table, "block_table", i32, (B, table_width), at),
+        _plain(new_lens, "new_lens", i32, (B,), at), B, width, layers, blocks * Hkv * page * d,
+        blocks, Hkv, page, d, table_width, _type_code(k_cache), _stream_on(stream, at)))
 
 
 def pva_forward_noalloc(q, k, v, cu_seqlens_q, cu_seqlens_kv, out, B: int, num_heads: int,

@@ -24,14 +24,36 @@ using namespace pva::host;
 namespace pva {
 namespace {
 
+// Depth of a node by the way up, for kernels that do not wait for the front end's:
+// whatever the parents are, at most T steps.
+__device__ __forceinline__ int walk_up(const RopeStep& s, int tok) {
+  const int node = tok % s.T;
+  const int32_t* parents = s.parents + (tok - node);
+  int depth = 0;
+  for (int a = node, up; (up = load<true>(parents + a)) >= 0 && up < a; a = up) ++depth;
+  return depth;
+}
+
+// The tree form looks everything up before the front end has finished, which it
+// follows on the stream: the front end lets it start only when all work before
+// the step is complete.  What it waits for is the permission to write -- and
+// the depths of large trees, whose way up is too long to walk here.
+constexpr int kWalkT = 64;
+
 template <typename T, int VEC, bool TREE>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) pva_rope_kernel(RopeStep s) {
+__global__ void __launch_bounds__(kRopeThreads, TREE ? 6 : kRopeCtas) pva_rope_kernel(RopeStep s) {
   __shared__ RopeToken sh[2];
   allow_next_grid();
-  wait_prior_grid();
-  rope_tokens<T, VEC, TREE>(s, blockIdx.x, gridDim.x, threadIdx.x, 0, sh,
-                            [&](int tok) { return s.depth ? s.depth[tok] : tok % s.T; },
-                            [&]() { return !TREE || s.hdr[0] != 0; });
+  const bool walk = TREE && s.parents && !s.pos && s.rt.rot > 0 && s.T <= kWalkT;
+  const bool wait_first = !TREE || (s.parents && !s.pos && s.rt.rot > 0 && !walk);
+  if (wait_first) wait_prior_grid();
+  rope_tokens<T, VEC, TREE>(
+      s, blockIdx.x, gridDim.x, threadIdx.x, 0, sh,
+      [&](int tok) { return !s.parents ? tok % s.T : walk ? walk_up(s, tok) : s.depth[tok]; },
+      [&]() {
+        if (!wait_first) wait_prior_grid();
+        return !TREE || s.hdr[0] != 0;
+      });
 }
 
 template <typename T>

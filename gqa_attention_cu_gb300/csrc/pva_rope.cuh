@@ -69,6 +69,7 @@ struct RopeStep {
   const int32_t* past;
   const int32_t* lens;      // nodes in use per sequence; nullptr: T
   const int32_t* depth;     // [B, T], or nullptr: i
+  const int32_t* parents;   // [B, T], or nullptr: a chain
   const int32_t* table;     // [B, max_blocks]; nullptr: block b
   int T, max_blocks;
   int negate_q;             // a negative scale, moved into the queries
@@ -99,9 +100,24 @@ struct alignas(sizeof(T) * VEC) Pack {
   T v[VEC];
 };
 
-__device__ __forceinline__ float table_at(const void* t, long long i, int is_f16) {
-  return is_f16 ? __half2float(static_cast<const __half*>(t)[i])
-                : static_cast<const float*>(t)[i];
+
+template <bool PAST_L1, typename T>
+__device__ __forceinline__ T load(const T* p) {
+  if constexpr (!PAST_L1) {
+    return *p;
+  } else if constexpr (sizeof(T) == 16) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+    return *reinterpret_cast<const T*>(&v);
+  } else if constexpr (sizeof(T) == 8) {
+    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
+    return *reinterpret_cast<const T*>(&v);
+  } else if constexpr (sizeof(T) == 4) {
+    const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(p));
+    return *reinterpret_cast<const T*>(&v);
+  } else {
+    const unsigned short v = __ldcg(reinterpret_cast<const unsigned short*>(p));
+    return *reinterpret_cast<const T*>(&v);
+  }
 }
 
 // Neighbouring pairs across two packs <-> first and second members.
@@ -128,6 +144,12 @@ __device__ __forceinline__ void join_pairs(Pack<T, VEC>& x, Pack<T, VEC>& y) {
   y = b;
 }
 
+template <bool PAST_L1>
+__device__ __forceinline__ float table_at(const void* t, long long i, int is_f16) {
+  return is_f16 ? __half2float(load<PAST_L1>(static_cast<const __half*>(t) + i))
+                : load<PAST_L1>(static_cast<const float*>(t) + i);
+}
+
 // cos and sin of a token's pairs, and whether a position is off the tables.
 struct RopeToken {
   float2 cs[128];
@@ -142,7 +164,9 @@ struct RopeToken {
 // A token's table entries are fetched once, a pair per thread, into shared
 // memory, and one token ahead: while the rows of token i are turned, the
 // positions of token i + 2 and the entries of token i + 1 are on their way.
-// go(): asked once, after the first loads are out, whether rows may be written.
+// go(): asked once, before the first write, whether rows may be written.  TREE
+// reads past L1: its inputs may be older than this kernel's launch, but not than
+// whatever the SM still holds of the last step's.
 template <typename T, int VEC, bool TREE, typename Depth, typename Go>
 __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int stride, int tid,
                                             int bar, RopeToken (&sh)[2], Depth depth_of, Go go) {
@@ -186,12 +210,12 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
     if (TREE) {
       const int b = tok / s.T, node = tok - b * s.T;
       // also called for steps that will be refused: nothing is taken for granted
-      const int past = s.past[b], in = past >= 0 ? (int)(((uint32_t)past + node) / (uint32_t)s.page) : -1;
-      if (node < (s.lens ? s.lens[b] : s.T) && (unsigned)in < (unsigned)s.max_blocks) {
+      const int past = load<TREE>(s.past + b), in = past >= 0 ? (int)(((uint32_t)past + node) / (uint32_t)s.page) : -1;
+      if (node < (s.lens ? load<TREE>(s.lens + b) : s.T) && (unsigned)in < (unsigned)s.max_blocks) {
         const int row = past + node;
-        const int block = s.table ? s.table[(size_t)b * s.max_blocks + in] : b;
+        const int block = s.table ? load<TREE>(s.table + (size_t)b * s.max_blocks + in) : b;
         f.slot = (int64_t)block * s.page + (row - in * s.page);
-        if (half) f.at = s.pos ? s.pos[(size_t)axis * s.tokens + tok] : (int64_t)past + depth_of(tok);
+        if (half) f.at = s.pos ? load<TREE>(s.pos + (size_t)axis * s.tokens + tok) : (int64_t)past + depth_of(tok);
       }
     } else {
       f.at = s.pos[(size_t)axis * s.tokens + tok];
@@ -205,8 +229,8 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
     float2 e = make_float2(1.0f, 0.0f);
     if (tid < half && f.at >= 0 && f.at < rt.rows) {
       const int64_t i = f.at * half + tid;
-      e.x = table_at(rt.cos, i, rt.is_f16);
-      e.y = table_at(rt.sin, i, rt.is_f16);
+      e.x = table_at<TREE>(rt.cos, i, rt.is_f16);
+      e.y = table_at<TREE>(rt.sin, i, rt.is_f16);
       if (rt.inverse) e.y = -e.y;
     }
     return e;
@@ -226,19 +250,17 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
       const T* src = row < nq ? q + (size_t)tok * s.q_stride + (size_t)row * s.d
                      : row < nq + nk ? k + (size_t)tok * s.k_stride + (size_t)(row - nq) * s.d
                                      : v + (size_t)tok * s.v_stride + (size_t)(row - nq - nk) * s.d;
-      x0[y] = *reinterpret_cast<const P*>(src + d0);
-      x1[y] = *reinterpret_cast<const P*>(src + d1);
+      x0[y] = load<TREE>(reinterpret_cast<const P*>(src + d0));
+      x1[y] = load<TREE>(reinterpret_cast<const P*>(src + d1));
     }
   };
 
   if (first >= s.tokens) return;
   load_rows(first, r0);
   Info now = fetch_info(first), next = fetch_info(first + stride);
+  const float2 first_entry = fetch_entry(now);
   if (!go()) return;
-  {
-    const float2 e = fetch_entry(now);
-    share(sh[0], e, now);
-  }
+  share(sh[0], first_entry, now);
   int buf = 0;
   for (int tok = first; tok < s.tokens; tok += stride, buf ^= 1) {
     if (tok != first) load_rows(tok, r0);

@@ -9,6 +9,7 @@
 //       step, all of it, when any CTA found something wrong.
 //   pva_rope_kernel        rotated queries to scratch, new rows to the cache,
 //       zeros for unused nodes.
+//   pva_tree_warp_front_kernel   the first of these for up to 32 sequences.
 //   pva_tree_small_front_kernel  both of these for small steps.
 //   attention              one piece of the line per CTA.
 //   pva_tree_join_kernel   adds up the parts of items that lie across a cut.
@@ -32,6 +33,9 @@ constexpr int kWordArrived = 16, kWordBad = 17;
 
 // Steps up to these sizes are checked by every CTA that rotates rows.
 constexpr int kSmallB = 16, kSmallT = 64, kSmallNodes = 256, kSmallBlocks = 1024;
+
+// And these by one CTA, a warp per sequence (up to 32 of them).
+constexpr int kWarpFrontT = 128, kWarpFrontBlocks = 512;
 
 // Checks sequence b and finds its masks, depths and tiles.  N threads (32: a
 // warp, else the CTA) work on one sequence; i0 is the caller's place among
@@ -155,8 +159,8 @@ __device__ __forceinline__ bool too_many(const TreeParams& p, long long tiles) {
 }
 
 __global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParams p) {
-  allow_next_grid();
   wait_prior_grid();
+  allow_next_grid();  // not before: the next kernel reads the step's inputs at once
   __shared__ int s_parent[kMaxTreeNodes];
   __shared__ uint32_t s_bad;
   __shared__ int s_last;
@@ -226,13 +230,46 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_front_kernel(TreeParam
   }
 }
 
+// The same for up to 32 sequences of short trees, a warp each: one CTA, which
+// adds up in shared memory and waits for no other.
+__global__ void __launch_bounds__(1024) pva_tree_warp_front_kernel(TreeParams p) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ int s_parent[32][kWarpFrontT];
+  __shared__ long long s_tiles[32];
+  __shared__ uint32_t s_bad;
+  const int tid = threadIdx.x, b = tid >> 5, lane = tid & 31;
+  const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  long long tiles;
+  const uint32_t bad = front_sequence<32>(p, b, p.past[b], tree_nodes(p, b), lane, true, s_parent[b],
+                                          nullptr, tiles);
+  if (bad) atomicOr(&s_bad, bad);
+  if (lane == 0) s_tiles[b] = tiles;
+  __syncthreads();
+  if (b > 0) return;
+  const int B = blockDim.x >> 5;
+  const long long x = lane < B ? s_tiles[lane] : 0;
+  long long upto = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const long long all = __shfl_sync(0xffffffffu, upto, 31);
+  if (lane < B) p.tile_start[lane] = too_many(p, all) ? 0 : (int)(upto - x);
+  // few items: by pieces
+  if (lane == 0) front_publish(p, all, 0, s_bad | (too_many(p, all) ? PVA_DEV_TOO_MANY : 0u), latched);
+}
+
 // A small step's front end and append in one launch.  Every CTA checks the
 // whole step, so that none has to wait for another before it writes rows: a
 // warp per sequence, a few loads deep.  The first CTA writes the results.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kFrontThreads) pva_tree_small_front_kernel(TreeParams p,
                                                                              RopeStep r) {
-  allow_next_grid();
+  allow_next_grid();  // the attention waits for all of this kernel
   wait_prior_grid();
   constexpr int kWarps = kFrontThreads / 32, kAtOnce = kFrontThreads / kRopeThreads;
   __shared__ RopeToken s_rope[kAtOnce][2];
@@ -589,7 +626,10 @@ cudaError_t launch_front(const TreeParams& p, const RopeStep& r, int dtype, int 
       default: return launch_small_front<__nv_bfloat16>(p, r, num_sms, s);
     }
   }
-  cudaError_t e = launch_dependent(pva_tree_front_kernel, dim3(p.B), dim3(kFrontThreads), 0, s, p);
+  const cudaError_t e =
+      p.B <= 32 && p.T <= kWarpFrontT && p.max_blocks <= kWarpFrontBlocks
+          ? launch_dependent(pva_tree_warp_front_kernel, dim3(1), dim3(32 * p.B), 0, s, p)
+          : launch_dependent(pva_tree_front_kernel, dim3(p.B), dim3(kFrontThreads), 0, s, p);
   if (e != cudaSuccess) return e;
   return launch_rope(r, dtype, true, num_sms, s);
 }
@@ -707,7 +747,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   const bool pair = tc && (long long)T * G > kTcRows && d <= 192;
   p.rows = pair ? 2 * kTcRows : tc ? kTcRows : kTreeRowsF32;
   // without a rotation the queries are exact as they are
-  p.q_parts = tc && !pair && rot ? tree_q_parts(d) : 1;
+  p.q_parts = !tc || !rot ? 1 : pair ? tree_pair_q_parts(d) : tree_q_parts(d);
   p.item_places = 2;
   p.bn = tc ? tree_keys(d) : kTreeKeysF32;
   p.QT = (int)(((long long)T * G + p.rows - 1) / p.rows);
@@ -785,6 +825,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   r.past = past_lens;
   r.lens = tree_lens;
   r.depth = parents ? p.depth : nullptr;
+  r.parents = parents;
   r.table = block_table;
   r.T = T;
   r.max_blocks = max_blocks;

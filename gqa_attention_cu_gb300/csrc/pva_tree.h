@@ -37,8 +37,10 @@ struct alignas(16) TreeCut {
 // Keys per key tile of the tensor-core kernel (TMEM holds two score tiles, O and Q).
 __host__ __device__ constexpr int tree_keys(int d) { return d <= 128 ? 128 : 64; }
 
-// Parts of the rotated queries that the one-tile kernel takes (pva_tree_tc.cu).
+// Parts of the rotated queries that the one-tile and the paired kernel take (see
+// there).
 __host__ __device__ constexpr int tree_q_parts(int d) { return d <= 192 ? 2 : 1; }
+__host__ __device__ constexpr int tree_pair_q_parts(int d) { return d <= 64 ? 2 : 1; }
 
 struct TreeParams {
   const int32_t* past;     // [B] cache rows before the step

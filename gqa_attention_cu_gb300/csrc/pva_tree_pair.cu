@@ -18,9 +18,10 @@
 // TMEM: S_x at [x BN, (x+1) BN), O_x at 2 BN + x D: all 512 columns at D = 128
 // and D = 192.
 //
-// Q is rounded to the storage type here (half a step of each element, as K is):
-// the residual product that the one-tile kernel adds would need the shared
-// memory that the ring has.
+// At d = 64 the queries come in two parts, as in the one-tile kernel.  At larger
+// head sizes Q is rounded to the storage type once (half a step of each element,
+// as K is): the second part would take the shared memory that the ring has, and
+// d / 16 more MMA steps of a kernel whose chain they are in.
 #include "pva_tree_tile.cuh"
 
 namespace pva {
@@ -40,7 +41,8 @@ struct PairCfg {
   static constexpr int Q_TILE = CH * Q_CHUNK;     // one query tile
   static constexpr int KV_CHUNK = BN * 128;
   static constexpr int KV_TILE = CH * KV_CHUNK;
-  static constexpr int OFF_RING = 2 * Q_TILE;
+  static constexpr int Q_PARTS = tree_pair_q_parts(D);
+  static constexpr int OFF_RING = 2 * Q_PARTS * Q_TILE;
   static constexpr int SLOTS_FIT = (232448 - kHeadBytes - OFF_RING) / KV_TILE;
   static constexpr int SLOTS = SLOTS_FIT < 16 ? SLOTS_FIT : 16;
   static_assert(SLOTS >= 4, "ring depth");
@@ -155,12 +157,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the Q tiles, once the S MMAs of the segment before are done with them
       if (!(ok = wait(&bars->q_empty, (q_loads & 1) ^ 1))) break;
       if (lane == 0) {
-        const int n_q = has_second(p, s) ? 2 : 1;
-        mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(n_q * C::Q_TILE));
-        for (int y = 0; y < n_q; ++y)
-          for (int c = 0; c < C::CH; ++c)
-            tma_load_3d(smem + y * C::Q_TILE + c * C::Q_CHUNK, &tmap_q, &bars->q_full, c * 64,
-                        s.t * p.rows + y * kTcRows, s.b * p.Hkv + s.h);
+        const int n_q = has_second(p, s) ? 2 : 1, parts = min(p.q_parts, C::Q_PARTS);
+        mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(n_q * parts * C::Q_TILE));
+        for (int part = 0; part < parts; ++part)
+          for (int y = 0; y < n_q; ++y)
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_3d(smem + (2 * part + y) * C::Q_TILE + c * C::Q_CHUNK, &tmap_q, &bars->q_full,
+                          c * 64, s.t * p.rows + y * kTcRows, (part * p.B + s.b) * p.Hkv + s.h);
       }
       __syncwarp();
       ++q_loads;
@@ -225,6 +228,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss(tmem + C::COL_S + x * BN, sdesc_advance(qa, (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32),
                  sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s,
                  kk > 0 ? 1u : 0u);
+        if (C::Q_PARTS == 2 && p.q_parts == 2) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + C::COL_S + x * BN,
+                   sdesc_advance(qa, 2 * C::Q_TILE + (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32),
+                   sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s, 1u);
+        }
         mma_commit(&bars->s_full[x]);
       }
     };

@@ -114,6 +114,18 @@ def test_tree_sizes_differ():
     parity(2, 40, 8, 2, 128, "f16", [9, 90], 12, lens=[0, 25], chain=True)
 
 
+def test_numbers_of_sequences_and_nodes():
+    """The front end by every CTA, by a warp and by a CTA per sequence; node
+    depths walked up by the rotation or taken from the front end."""
+    parity(16, 3, 4, 2, 64, "bf16", list(range(0, 160, 10)), 80, rot=64, page=16)
+    parity(17, 5, 4, 2, 64, "f16", list(range(0, 170, 10)), 81, rot=64, lens=[5, 0, 3, 1] * 4 + [2])
+    parity(40, 3, 4, 2, 64, "bf16", [(7 * i) % 90 for i in range(40)], 82, rot=64, page=32)
+    parity(3, 70, 2, 1, 64, "bf16", [5, 60, 200], 83, rot=64, page=16, lens=[70, 1, 66])
+    parity(2, 129, 1, 1, 64, "bf16", [5, 60], 84, rot=64)
+    parity(33, 66, 2, 2, 64, "f16", [3] * 33, 85, rot=64, page=64)
+    parity(300, 1, 2, 1, 64, "bf16", [i % 70 for i in range(300)], 86, chain=True, rot=64)
+
+
 def test_nothing_in_use():
     s = make_tree(2, 4, 8, 2, 128, "bf16", [9, 0], 13, lens=[0, 0])
     out, kc, _ = call(s, 8, 2)
