@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kFrontThreads = 256;
 constexpr int kMaxTreeNodes = 1024;
+static_assert(kMaxTreeNodes <= 4 * kFrontThreads, "a thread of the front end reads four parents");
 constexpr int kTreeRowsF32 = 32, kTreeKeysF32 = 32;
 // Words of the status block (zero between calls).
 constexpr int kWordArrived = 16, kWordBad = 17;
@@ -35,7 +36,8 @@ constexpr int kWordArrived = 16, kWordBad = 17;
 constexpr int kSmallB = 16, kSmallT = 64, kSmallNodes = 256, kSmallBlocks = 1024;
 
 // And these by one CTA, a warp per sequence (up to 32 of them).
-constexpr int kWarpFrontT = 128, kWarpFrontBlocks = 512;
+constexpr int kWarpFrontT = 128,  // four nodes a lane
+              kWarpFrontBlocks = 512;
 
 // Checks sequence b and finds its masks, depths and tiles.  N threads (32: a
 // warp, else the CTA) work on one sequence; i0 is the caller's place among
@@ -46,13 +48,19 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
                                                    int i0, bool write, int* s_parent,
                                                    int* s_depth, long long& tiles) {
   // Parents and positions of all T nodes are read beside the lengths, whether
-  // they are in use or not; the table has to wait for the lengths.
+  // they are in use or not, and all before any is looked at; the table has to
+  // wait for the lengths.  (A tree has at most 4 N nodes.)
   uint32_t bad = 0;
-  if (p.parents)
-    for (int i = i0; i < p.T; i += N) s_parent[i] = p.parents[(size_t)b * p.T + i];
+  int up[4];
+  if (p.parents) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k * N < p.T) up[k] = p.parents[(size_t)b * p.T + i0 + k * N];
+  }
   int off_table = p.T;  // the first node with a position outside the tables
   if (p.rot > 0 && p.pos) {
     for (int a = 0; a < p.n_axes; ++a)
+#pragma unroll 4
       for (int i = i0; i < p.T; i += N) {
         const int64_t at = p.pos[((size_t)a * p.B + b) * p.T + i];
         if (at < 0 || at >= p.cache_rows) off_table = min(off_table, i);
@@ -72,9 +80,12 @@ __device__ __forceinline__ uint32_t front_sequence(const TreeParams& p, int b, i
         if ((unsigned)table[i] >= (unsigned)p.n_blocks) bad |= PVA_DEV_BLOCKS;
     }
     if (p.parents) {
-      for (int i = i0; i < n; i += N) {
-        const int up = s_parent[i];  // this thread's own entries
-        if (up < -1 || up >= i) bad |= PVA_DEV_TREE;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * N;
+        if (i >= n) continue;
+        s_parent[i] = up[k];
+        if (up[k] < -1 || up[k] >= i) bad |= PVA_DEV_TREE;
       }
     }
     if (off_table < n) bad |= PVA_DEV_ROPE;

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = PairCfg<D>;
   constexpr int BN = C::BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (misplaced(smem_raw, p.status)) return;
+  if (misplaced(smem_raw, p)) return;
   Bars* bars = reinterpret_cast<Bars*>(smem_raw);
   uint8_t* smem = smem_raw + kHeadBytes;
   uint8_t* ring = smem + C::OFF_RING;
@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       v.last = 1;
       publish(v);
+    } else if (lane == 0) {
+      tree_note_cut(p, blockIdx.x, nullptr);  // nothing to join
     }
     // Drain: every copy this warp issued must land before the CTA exits.
     if (q_loads) mbar_wait<false>(&bars->q_full, (q_loads - 1) & 1, abort, status);

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = TreeCfg<D>;
   constexpr int BN = C::BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (misplaced(smem_raw, p.status)) return;
+  if (misplaced(smem_raw, p)) return;
   Bars* bars = reinterpret_cast<Bars*>(smem_raw);
   uint8_t* smem = smem_raw + kHeadBytes;
 
@@ -206,6 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       v.last = 1;
       publish(v);
+    } else if (lane == 0) {
+      tree_note_cut(p, blockIdx.x, nullptr);  // nothing to join
     }
     // Drain: every copy this warp issued must land before the CTA exits.
     for (int s = 0; s < C::SLOTS; ++s) {

@@ -178,9 +178,13 @@ struct RowPair {
 // addresses up: the kernels use no other shared memory, whose start then is such
 // a boundary, and refuse to run if it is not.
 constexpr int kHeadBytes = 3072;
-__device__ __forceinline__ bool misplaced(const void* smem, uint32_t* status) {
+__device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p) {
   if ((smem_u32(smem) & 1023) == 0) return false;
-  if (threadIdx.x == 0) atomicOr(status, PVA_DEV_WAIT_TIMEOUT);
+  if (threadIdx.x == 0) {
+    wait_prior_grid();
+    atomicOr(p.status, PVA_DEV_WAIT_TIMEOUT);
+    tree_note_cut(p, blockIdx.x, nullptr);
+  }
   return true;
 }
 
@@ -247,10 +251,12 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       else
         extremes<true, CAP>(v, mask, mx, mn);
     }
-    // a softcap's series has to hold for the warp's own columns
+    // a softcap's series has to hold for the warp's own columns (and the scores'
+    // squares have to be finite)
+    const float far = fmaxf(fabsf(mx), fabsf(mn));
     const bool series =
-        CAP && __all_sync(0xffffffffu, mx == NEG_INF || fmaxf(fabsf(mx * s_mul), fabsf(mn * s_mul)) <=
-                                                            kSeriesLimit);
+        CAP && __all_sync(0xffffffffu,
+                          mx == NEG_INF || (far * fabsf(s_mul) <= kSeriesLimit && far < 1e9f));
     if (!new_maximum()) return false;
 #pragma unroll 1
     for (int c = 0; c < N; c += 32) {

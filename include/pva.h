@@ -49,7 +49,9 @@ typedef enum {
 typedef enum { PVA_F32 = 0, PVA_F16 = 1, PVA_BF16 = 2 } pva_dtype;
 
 /* Device-side status bits, latched by the on-device scheduler and read with
- * pva_get_status.  When any bit is set the call wrote nothing to `out`. */
+ * pva_get_status.  When any bit is set the call wrote nothing to `out` (but see
+ * pva_rope_axes and pva_kvcache_accept, which leave out single tokens and
+ * sequences). */
 #define PVA_DEV_CU_Q_START 0x1u   /* cu_seqlens_q[0] != 0 */
 #define PVA_DEV_CU_KV_START 0x2u  /* cu_seqlens_kv[0] != 0 */
 #define PVA_DEV_CU_Q_ORDER 0x4u   /* cu_seqlens_q decreases somewhere */
@@ -412,9 +414,10 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  *
  * Arithmetic: products of dtype (f16/bf16 on tensor cores), scores, softmax and
  * sums in f32.  The softmax weights that multiply V are rounded to dtype
- * (f16/bf16).  Rotated queries are too in steps of more than 128 query rows per
- * kv head (tokens * num_heads / kv_num_heads) and at head_size 256; otherwise
- * what the rounding takes off them is multiplied as well.
+ * (f16/bf16).  Rotated queries are too at head_size 256, and above head_size 64
+ * in steps of more than 128 query rows per kv head (tokens * num_heads /
+ * kv_num_heads); otherwise what the rounding takes off them is multiplied as
+ * well.
  * Results do not depend on timing: parts of a split row are added in order.
  *
  * Limits: f16/bf16: head_size in {64, 96, 128, 192, 256}, 16-byte aligned
