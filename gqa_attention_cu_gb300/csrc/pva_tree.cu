@@ -28,7 +28,7 @@ namespace {
 constexpr int kFrontThreads = 256;
 constexpr int kMaxTreeNodes = 1024;
 static_assert(kMaxTreeNodes <= 4 * kFrontThreads, "a thread of the front end reads four parents");
-constexpr int kTreeRowsF32 = 32, kTreeKeysF32 = 32;
+constexpr int kTreeKeysF32 = 32;
 // Words of the status block (zero between calls).
 constexpr int kWordArrived = 16, kWordBad = 17;
 
@@ -392,18 +392,30 @@ __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
 }
 
 // fp32 attention on the CUDA cores, exact fp32 products (no TF32).  A CTA of 4
-// warps holds 32 query rows and streams tiles of 32 keys, the next tile on its
-// way (cp.async) while one is worked on.  A warp owns 8 rows throughout: a
-// thread scores 2 rows x 4 keys, then the warp's lanes hold a key each for the
-// softmax, then 4 (or 8) channels each of its 8 rows for the weighted sum, so
-// warps meet only where a tile is complete.  Per thread 12 16-byte shared
-// loads feed 128 multiply-adds of the sum, 6 feed 32 of the scores: bound by
-// the FMA pipe and shared memory together for many rows, by latency for a small
-// draft.  Keys outside the item's range are zeros in shared memory, whatever
-// the cache holds there.
-constexpr int kWarpsF32 = 4, kRowsPerWarpF32 = kTreeRowsF32 / kWarpsF32;
+// warps holds 4 R query rows (R = 2, 4 or 6, as many as the step can have) and
+// streams tiles of 32 keys, the next tile on its way (cp.async) while one is
+// worked on.  A warp owns R rows throughout: its threads score up to 3 rows x 2
+// keys each, then its lanes hold a key each for the softmax, then 4 (or 8)
+// channels of each of its rows for the weighted sum, so warps meet only where a
+// tile is complete.  Each step waits on shared memory and shuffles, so what
+// counts is how many warps an SM has to switch between: 24 rows and three CTAs
+// an SM against 32 rows and two, 146 against 188 us (7 nodes x 3 query heads on
+// 20,000 rows of 3 sequences x 4 kv heads, d = 96); 8 rows and four CTAs for one
+// node, 34 against 50 us (8 sequences of 1000 to 2000 rows).  Keys outside the
+// item's range are zeros in shared memory, whatever the cache holds there.
+constexpr int kWarpsF32 = 4;
 
 __host__ __device__ constexpr int f32_stride(int d) { return (d + 3) / 4 * 4 + 4; }
+
+size_t f32_smem(int rows, int d) {
+  return sizeof(float) * ((size_t)(rows + 4 * kTreeKeysF32) * f32_stride(d) + rows * 36);
+}
+// CTAs an SM holds by their shared memory (1 KB of it each is the system's) and
+// by their registers: 4 of 8 rows, 3 of 16 or 24.
+int f32_ctas(int rows, int d) {
+  const int by_smem = (int)((228 * 1024) / (f32_smem(rows, d) + 2048)), by_regs = rows <= 8 ? 4 : 3;
+  return by_smem < by_regs ? by_smem : by_regs;
+}
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
@@ -413,14 +425,15 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src, bool va
 
 // C: 16-byte channel groups a lane sums (1: d <= 128, 2: d <= 256); WIDE: rows of
 // the cache lie on 16-byte boundaries.
-template <int C, bool WIDE>
+template <int R, int C, bool WIDE>
 __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams p) {
+  constexpr int kRows = kWarpsF32 * R;
   extern __shared__ float smem[];
   const int d = p.d, stride = f32_stride(d), groups = (d + 3) / 4;
   constexpr int kTile = kTreeKeysF32;
-  float* sq = smem;                               // [32][stride]
-  float* skv = sq + kTreeRowsF32 * stride;        // [2][K, V][32][stride]
-  float* sp = skv + 4 * kTile * stride;           // [32][36] weights
+  float* sq = smem;                               // [kRows][stride]
+  float* skv = sq + kRows * stride;               // [2][K, V][32][stride]
+  float* sp = skv + 4 * kTile * stride;           // [kRows][36] weights
   __shared__ TreeSegment s_segment;
   __shared__ int s_more;
   allow_next_grid();
@@ -431,7 +444,7 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
   const float* kc = static_cast<const float*>(p.k_cache);
   const float* vc = static_cast<const float*>(p.v_cache);
   // the padding channels of every row stay zero
-  for (int e = tid; e < (kTreeRowsF32 + 4 * kTile) * (stride - d); e += kWarpsF32 * 32)
+  for (int e = tid; e < (kRows + 4 * kTile) * (stride - d); e += kWarpsF32 * 32)
     smem[e / (stride - d) * stride + d + e % (stride - d)] = 0.0f;
   TreeWalk walk(p, blockIdx.x);  // the first warp's counts
   while (true) {
@@ -477,18 +490,24 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
     };
     load(s.j0);
     const float* q0 = q + (((size_t)s.b * p.Hkv + s.h) * p.T * p.G + (size_t)s.t * p.rows) * d;
-    for (int r = warp; r < kTreeRowsF32; r += kWarpsF32)
-      for (int c = lane; c < d; c += 32) sq[r * stride + c] = r < n_rows ? q0[r * d + c] : 0.0f;
-    const int row0 = warp * kRowsPerWarpF32;
-    float m[kRowsPerWarpF32], l[kRowsPerWarpF32], acc[kRowsPerWarpF32][4 * C];
-    int row_lo[kRowsPerWarpF32], row_hi[kRowsPerWarpF32];
+    // This warp's row r is row warp + 4 r of the item (dealt out, so that no warp
+    // idles), in slot warp R + r of shared memory (side by side, so that the lanes'
+    // reads of different rows meet different banks).
+    const int my_rows = n_rows > warp ? (n_rows - warp + kWarpsF32 - 1) / kWarpsF32 : 0;
+    auto row_of = [&](int r) { return warp + kWarpsF32 * r; };
+    auto slot_of = [&](int r) { return warp * R + r; };
+    for (int r = 0; r < R; ++r)
+      for (int c = lane; c < d; c += 32)
+        sq[slot_of(r) * stride + c] = r < my_rows ? q0[row_of(r) * d + c] : 0.0f;
+    float m[R], l[R], acc[R][4 * C];
+    int row_lo[R], row_hi[R];
 #pragma unroll
-    for (int r = 0; r < kRowsPerWarpF32; ++r) {
+    for (int r = 0; r < R; ++r) {
       m[r] = NEG_INF;
       l[r] = 0.0f;
 #pragma unroll
       for (int u = 0; u < 4 * C; ++u) acc[r][u] = 0.0f;
-      const int node = row0 + r < n_rows ? (s.t * p.rows + row0 + r) / p.G : 0;
+      const int node = r < my_rows ? (s.t * p.rows + row_of(r)) / p.G : 0;
       const int depth = p.parents ? p.depth[(size_t)s.b * p.T + node] : node;
       const long long lo = p.window > 0 ? (long long)s.past + depth + 1 - p.window : 0;
       row_lo[r] = lo > 0 ? (int)lo : 0;
@@ -504,38 +523,43 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
       __syncthreads();  // tile j (and Q) is complete
       const float* sk = skv + (j & 1) * 2 * kTile * stride;
       const float* sv = sk + kTile * stride;
-      if (row0 < n_rows) {  // warp-uniform
-        // scores of rows row0 + 2 y, + 1 and keys x, x + 8, x + 16, x + 24
-        const int y = lane >> 3, x = lane & 7;
-        float sc[2][4] = {};
-        const float* qa = sq + (row0 + 2 * y) * stride;
+      if (my_rows > 0) {  // warp-uniform
+        // scores: LANES lanes side by side on a row's keys, RT rows a thread
+        constexpr int LANES = R % 4 == 0 ? 8 : 16, RT = R * LANES / 32, KT = kTile / LANES;
+        const int y = lane / LANES, x = lane % LANES;
+        float sc[RT][KT] = {};
+        const float* qa = sq + slot_of(RT * y) * stride;
 #pragma unroll 4
         for (int c = 0; c < groups; ++c) {
-          const float4 a0 = *reinterpret_cast<const float4*>(qa + 4 * c);
-          const float4 a1 = *reinterpret_cast<const float4*>(qa + stride + 4 * c);
+          float4 a[RT];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 b = *reinterpret_cast<const float4*>(sk + (x + 8 * k) * stride + 4 * c);
-            sc[0][k] = fmaf(a0.w, b.w, fmaf(a0.z, b.z, fmaf(a0.y, b.y, fmaf(a0.x, b.x, sc[0][k]))));
-            sc[1][k] = fmaf(a1.w, b.w, fmaf(a1.z, b.z, fmaf(a1.y, b.y, fmaf(a1.x, b.x, sc[1][k]))));
+          for (int r = 0; r < RT; ++r)
+            a[r] = *reinterpret_cast<const float4*>(qa + r * stride + 4 * c);
+#pragma unroll
+          for (int k = 0; k < KT; ++k) {
+            const float4 b = *reinterpret_cast<const float4*>(sk + (x + LANES * k) * stride + 4 * c);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              sc[r][k] = fmaf(a[r].w, b.w,
+                              fmaf(a[r].z, b.z, fmaf(a[r].y, b.y, fmaf(a[r].x, b.x, sc[r][k]))));
           }
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sp[(row0 + 2 * y + r) * 36 + x + 8 * k] = sc[r][k];
+          for (int k = 0; k < KT; ++k) sp[slot_of(RT * y + r) * 36 + x + LANES * k] = sc[r][k];
         __syncwarp();
         // softmax: lane = key
         const int key = j * kTile + lane, other = key - s.past;
-        float w[kRowsPerWarpF32], top[kRowsPerWarpF32];
+        float w[R], top[R];
 #pragma unroll
-        for (int r = 0; r < kRowsPerWarpF32; ++r) {
+        for (int r = 0; r < R; ++r) {
           bool seen = key >= row_lo[r] && key < row_hi[r];
-          if (p.parents && other >= 0 && other < s.n && row0 + r < n_rows) {
-            const int node = (s.t * p.rows + row0 + r) / p.G;
+          if (p.parents && other >= 0 && other < s.n && r < my_rows) {
+            const int node = (s.t * p.rows + row_of(r)) / p.G;
             seen = (p.mask[((size_t)s.b * p.T + node) * p.W32 + (other >> 5)] >> (other & 31)) & 1;
           }
-          float v = sp[(row0 + r) * 36 + lane] * p.scale;
+          float v = sp[slot_of(r) * 36 + lane] * p.scale;
           if (p.softcap != 0.0f) v = p.softcap * tanhf(v / p.softcap);
           w[r] = seen ? v * 1.4426950408889634f : NEG_INF;  // base-2 units, as the join expects
           top[r] = w[r];
@@ -543,10 +567,9 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-          for (int r = 0; r < kRowsPerWarpF32; ++r)
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
+          for (int r = 0; r < R; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
 #pragma unroll
-        for (int r = 0; r < kRowsPerWarpF32; ++r) {
+        for (int r = 0; r < R; ++r) {
           const float m_new = fmaxf(m[r], top[r]);
           const float base = m_new == NEG_INF ? 0.0f : m_new;
           const float alpha = exp2f(m[r] - base);
@@ -556,15 +579,14 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
           l[r] *= alpha;
 #pragma unroll
           for (int u = 0; u < 4 * C; ++u) acc[r][u] *= alpha;
-          sp[(row0 + r) * 36 + lane] = w[r];
+          sp[slot_of(r) * 36 + lane] = w[r];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-          for (int r = 0; r < kRowsPerWarpF32; ++r)
-            top[r] += __shfl_xor_sync(0xffffffffu, top[r], o);
+          for (int r = 0; r < R; ++r) top[r] += __shfl_xor_sync(0xffffffffu, top[r], o);
 #pragma unroll
-        for (int r = 0; r < kRowsPerWarpF32; ++r) l[r] += top[r];
+        for (int r = 0; r < R; ++r) l[r] += top[r];
         __syncwarp();
         // weighted sums: lane = channels 4 lane .. (and 128 on)
 #pragma unroll 2
@@ -577,8 +599,8 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
               if (lane + 32 * u < groups)
                 v[k][u] = *reinterpret_cast<const float4*>(sv + (i + k) * stride + 4 * (lane + 32 * u));
 #pragma unroll
-          for (int r = 0; r < kRowsPerWarpF32; ++r) {
-            const float4 wr = *reinterpret_cast<const float4*>(sp + (row0 + r) * 36 + i);
+          for (int r = 0; r < R; ++r) {
+            const float4 wr = *reinterpret_cast<const float4*>(sp + slot_of(r) * 36 + i);
             const float wk[4] = {wr.x, wr.y, wr.z, wr.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -595,9 +617,9 @@ __global__ void __launch_bounds__(kWarpsF32 * 32) pva_tree_f32_kernel(TreeParams
       __syncthreads();  // before tile j + 2 goes over tile j
     }
 #pragma unroll
-    for (int r = 0; r < kRowsPerWarpF32; ++r) {
-      const int lr = row0 + r;
-      if (lr >= n_rows) continue;
+    for (int r = 0; r < R; ++r) {
+      if (r >= my_rows) break;
+      const int lr = row_of(r);
       const int row = s.t * p.rows + lr, node = row / p.G, g = row - node * p.G;
       const size_t at = (size_t)(s.slot < 0 ? 0 : s.slot) * p.rows + lr;
       const bool whole = s.slot < 0;
@@ -663,15 +685,23 @@ cudaError_t launch_join(const TreeParams& p, int dtype, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_tree_f32(const TreeParams& p, cudaStream_t s) {
-  const size_t smem = sizeof(float) * ((size_t)(kTreeRowsF32 + 4 * kTreeKeysF32) * f32_stride(p.d) +
-                                       kTreeRowsF32 * 36);
+namespace {
+template <int R>
+cudaError_t launch_f32_rows(const TreeParams& p, cudaStream_t s) {
+  const size_t smem = f32_smem(kWarpsF32 * R, p.d);
   const bool wide = p.d % 4 == 0 && (((uintptr_t)p.k_cache | (uintptr_t)p.v_cache) & 15) == 0;
-  auto kern = p.d <= 128 ? (wide ? pva_tree_f32_kernel<1, true> : pva_tree_f32_kernel<1, false>)
-                         : (wide ? pva_tree_f32_kernel<2, true> : pva_tree_f32_kernel<2, false>);
+  auto kern = p.d <= 128 ? (wide ? pva_tree_f32_kernel<R, 1, true> : pva_tree_f32_kernel<R, 1, false>)
+                         : (wide ? pva_tree_f32_kernel<R, 2, true> : pva_tree_f32_kernel<R, 2, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(p.pieces), dim3(kWarpsF32 * 32), smem, s, p);
+}
+}  // namespace
+
+cudaError_t launch_tree_f32(const TreeParams& p, cudaStream_t s) {
+  return p.rows == 8    ? launch_f32_rows<2>(p, s)
+         : p.rows == 16 ? launch_f32_rows<4>(p, s)
+                        : launch_f32_rows<6>(p, s);
 }
 
 }  // namespace pva
@@ -756,14 +786,18 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   p.cache_rows = cache_rows;
   // two query tiles an item where a sequence can have more rows than one holds
   const bool pair = tc && (long long)T * G > kTcRows && d <= 192;
-  p.rows = pair ? 2 * kTcRows : tc ? kTcRows : kTreeRowsF32;
+  const int rows_f32 = T * G <= 8 ? 8 : T * G <= 16 ? 16 : 24;
+  p.rows = pair ? 2 * kTcRows : tc ? kTcRows : rows_f32;
   // without a rotation the queries are exact as they are
   p.q_parts = !tc || !rot ? 1 : pair ? tree_pair_q_parts(d) : tree_q_parts(d);
   p.item_places = 2;
   p.bn = tc ? tree_keys(d) : kTreeKeysF32;
   p.QT = (int)(((long long)T * G + p.rows - 1) / p.rows);
   p.W32 = parents ? (T + 31) / 32 : 0;
-  p.min_chunk = 1;
+  // Two tiles at least: half the parts to join for one more tile's time (one
+  // request, 8 nodes on 2000 rows: 26.0 against 23.9 us), but not where a tile
+  // is the paired kernel's (60 nodes on 500 rows: 30.3 against 31.6 us).
+  p.min_chunk = pair ? 1 : 2;
   p.may_take_items = tc && p.QT > 1;
   p.k_cache = k_cache;
   p.v_cache = v_cache;
@@ -772,7 +806,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   std::lock_guard<std::mutex> lock(api_mutex());
   int sms = 0;
   if ((rc = sm_count(&sms)) != PVA_OK) return rc;
-  p.pieces = tc ? sms : 2 * sms;
+  p.pieces = tc ? sms : f32_ctas(p.rows, d) * sms;
   // workspace, in 256-byte steps
   size_t used = 0;
   auto take = [&](size_t bytes) {
