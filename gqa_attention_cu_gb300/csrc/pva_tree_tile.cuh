@@ -222,42 +222,49 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
     m_eff = st.m == NEG_INF ? 0.0f : st.m;
     return true;
   };
+  // a softcap's series has to hold for the warp's own columns (and the scores'
+  // squares have to be finite)
+  auto small_scores = [&]() {
+    const float far = fmaxf(fabsf(mx), fabsf(mn));
+    return CAP && __all_sync(0xffffffffu, mx == NEG_INF || (far * fabsf(s_mul) <= kSeriesLimit &&
+                                                            far < 1e9f));
+  };
   float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-  if (!CAP && all) {
+  bool series, done = false;
+  if (all) {
     uint32_t v[N / 32][32];
 #pragma unroll
     for (int c = 0; c < N / 32; ++c) tmem_ld32(t_s + c * 32, v[c]);
 #pragma unroll
     for (int c = 0; c < N / 32; ++c) {
       tmem_wait_ld_of(v[c]);
-      extremes<false, false>(v[c], 0u, mx, mn);
+      extremes<false, CAP>(v[c], 0u, mx, mn);
     }
+    series = small_scores();
     if (!new_maximum()) return false;
+    if (!CAP || series) {
+      done = true;
 #pragma unroll
-    for (int c = 0; c < N / 32; ++c) {
-      uint32_t pw[16];
-      exponentials<T, 0, false>(v[c], 0u, s_mul, cap_mul, m_eff, acc, pw);
-      tmem_st16(t_s + c * 16, pw);
+      for (int c = 0; c < N / 32; ++c) {
+        uint32_t pw[16];
+        exponentials<T, CAP ? 1 : 0, false>(v[c], 0u, s_mul, cap_mul, m_eff, acc, pw);
+        tmem_st16(t_s + c * 16, pw);
+      }
     }
   } else {
     uint32_t v[32];
 #pragma unroll 1
     for (int c = 0; c < N; c += 32) {
       tmem_ld32(t_s + c, v);
-      const uint32_t mask = all ? 0xffffffffu : row_mask(p, view, past, k0 + c);
+      const uint32_t mask = row_mask(p, view, past, k0 + c);
       tmem_wait_ld_of(v);
-      if (CAP && all)
-        extremes<false, CAP>(v, mask, mx, mn);
-      else
-        extremes<true, CAP>(v, mask, mx, mn);
+      extremes<true, CAP>(v, mask, mx, mn);
     }
-    // a softcap's series has to hold for the warp's own columns (and the scores'
-    // squares have to be finite)
-    const float far = fmaxf(fabsf(mx), fabsf(mn));
-    const bool series =
-        CAP && __all_sync(0xffffffffu,
-                          mx == NEG_INF || (far * fabsf(s_mul) <= kSeriesLimit && far < 1e9f));
+    series = small_scores();
     if (!new_maximum()) return false;
+  }
+  if (!done) {
+    uint32_t v[32];
 #pragma unroll 1
     for (int c = 0; c < N; c += 32) {
       tmem_ld32(t_s + c, v);
@@ -266,8 +273,6 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       uint32_t pw[16];
       if (!CAP)
         exponentials<T, 0, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
-      else if (series && all)
-        exponentials<T, 1, false>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       else if (series)
         exponentials<T, 1, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       else
