@@ -785,11 +785,10 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   p.n_axes = rot ? n_axes : 1;
   p.cache_rows = cache_rows;
   // two query tiles an item where a sequence can have more rows than one holds
-  const bool pair = tc && (long long)T * G > kTcRows && d <= 192;
+  p.q_parts = tc && rot ? 2 : 1;  // without a rotation the queries are exact as they are
+  const bool pair = tc && tree_takes_pair((long long)T * G, d, p.q_parts);
   const int rows_f32 = T * G <= 8 ? 8 : T * G <= 16 ? 16 : 24;
   p.rows = pair ? 2 * kTcRows : tc ? kTcRows : rows_f32;
-  // without a rotation the queries are exact as they are
-  p.q_parts = !tc || !rot ? 1 : pair ? tree_pair_q_parts(d) : tree_q_parts(d);
   p.item_places = 2;
   p.bn = tc ? tree_keys(d) : kTreeKeysF32;
   p.QT = (int)(((long long)T * G + p.rows - 1) / p.rows);

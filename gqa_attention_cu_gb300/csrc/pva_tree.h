@@ -37,10 +37,19 @@ struct alignas(16) TreeCut {
 // Keys per key tile of the tensor-core kernel (TMEM holds two score tiles, O and Q).
 __host__ __device__ constexpr int tree_keys(int d) { return d <= 128 ? 128 : 64; }
 
-// Parts of the rotated queries that the one-tile and the paired kernel take (see
-// there).
-__host__ __device__ constexpr int tree_q_parts(int d) { return d <= 192 ? 2 : 1; }
-__host__ __device__ constexpr int tree_pair_q_parts(int d) { return d <= 64 ? 2 : 1; }
+// Whether the paired kernel takes a step of `rows` query rows per kv head.  Both
+// parts of the queries of two tiles fit shared memory beside the ring up to d =
+// 128, and then leave it three slots and the tensor cores half as much work again,
+// so a pair has to be 7/8 full (4 query heads per kv head, d = 128, the paired
+// kernel against the one-tile kernel, us: 8 sequences of 500 to 8000 rows, 40
+// nodes 117 and 98, 64 nodes 129 and 130, 128 nodes 218 and 215; 4 sequences of
+// 100,000 rows and more, 61 nodes 490 and 560).  Queries in one part: 87 and 92 us
+// at 40 nodes already.
+constexpr bool tree_takes_pair(long long rows, int d, int q_parts) {
+  if (rows <= 128) return false;
+  if (q_parts == 1) return d <= 192;
+  return d <= 128 && 8 * rows >= 7 * ((rows + 255) / 256 * 256);
+}
 
 struct TreeParams {
   const int32_t* past;     // [B] cache rows before the step

@@ -1,6 +1,7 @@
 // Tree attention over a KV cache on the tensor cores for steps with more than
 // 128 query rows per kv head (drafts of many nodes, prompt chunks): two 128-row
-// query tiles per CTA share every key tile, f16/bf16, head sizes up to 192.
+// query tiles per CTA share every key tile, f16/bf16, head sizes up to 192 (128
+// where the step rotates its queries).
 //
 // Two tiles halve the cache traffic per row, and give the tensor cores and the
 // softmax something to do at the same time: while one warpgroup exponentiates
@@ -18,10 +19,13 @@
 // TMEM: S_x at [x BN, (x+1) BN), O_x at 2 BN + x D: all 512 columns at D = 128
 // and D = 192.
 //
-// At d = 64 the queries come in two parts, as in the one-tile kernel.  At larger
-// head sizes Q is rounded to the storage type once (half a step of each element,
-// as K is): the second part would take the shared memory that the ring has, and
-// d / 16 more MMA steps of a kernel whose chain they are in.
+// Rotated queries come in two parts, as in the one-tile kernel.  Here the second
+// part costs more: at d = 128 half as many MMA steps again in a kernel that they
+// bound, and a ring slot (2048-token chunks of 8 sequences: 1.51 against 1.13 ms;
+// 61 nodes on 4 sequences of 100,000 rows and more: 0.49 against 0.36 ms), for
+// one rounding less of three equal ones (bf16 results off by 0.0023 of their size in
+// the mean square against 0.0029, 0.0017 being their own rounding).
+// Queries that the caller rotated are taken as they are, at the smaller figures.
 #include "pva_tree_tile.cuh"
 
 namespace pva {
@@ -33,7 +37,7 @@ constexpr int kThreads = 320;
 constexpr int kItemSlots = 4;
 constexpr int kGroupWarps = 4;
 
-template <int D>
+template <int D, int PARTS>
 struct PairCfg {
   static constexpr int BN = tree_keys(D);
   static constexpr int CH = (D + 63) / 64;
@@ -41,11 +45,10 @@ struct PairCfg {
   static constexpr int Q_TILE = CH * Q_CHUNK;     // one query tile
   static constexpr int KV_CHUNK = BN * 128;
   static constexpr int KV_TILE = CH * KV_CHUNK;
-  static constexpr int Q_PARTS = tree_pair_q_parts(D);
-  static constexpr int OFF_RING = 2 * Q_PARTS * Q_TILE;
+  static constexpr int OFF_RING = 2 * PARTS * Q_TILE;
   static constexpr int SLOTS_FIT = (232448 - kHeadBytes - OFF_RING) / KV_TILE;
   static constexpr int SLOTS = SLOTS_FIT < 16 ? SLOTS_FIT : 16;
-  static_assert(SLOTS >= 4, "ring depth");
+  static_assert(SLOTS >= 3, "V_j, K_j+1 and a slot on its way");
   static constexpr int SMEM = kHeadBytes + OFF_RING + SLOTS * KV_TILE;
   static constexpr int TMEM_COLS = 512;
   static constexpr int COL_S = 0;
@@ -75,12 +78,12 @@ __device__ __forceinline__ bool has_second(const TreeParams& p, const TreeSegmen
   return s.n * p.G - s.t * p.rows > kTcRows;
 }
 
-template <typename T, int D, bool CAP>
+template <typename T, int D, int PARTS, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     pva_tree_pair_kernel(TreeParams p, const __grid_constant__ CUtensorMap tmap_q,
                          const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v) {
-  using C = PairCfg<D>;
+  using C = PairCfg<D, PARTS>;
   constexpr int BN = C::BN;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (misplaced(smem_raw, p)) return;
@@ -157,9 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the Q tiles, once the S MMAs of the segment before are done with them
       if (!(ok = wait(&bars->q_empty, (q_loads & 1) ^ 1))) break;
       if (lane == 0) {
-        const int n_q = has_second(p, s) ? 2 : 1, parts = min(p.q_parts, C::Q_PARTS);
-        mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(n_q * parts * C::Q_TILE));
-        for (int part = 0; part < parts; ++part)
+        const int n_q = has_second(p, s) ? 2 : 1;
+        mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(n_q * PARTS * C::Q_TILE));
+        for (int part = 0; part < PARTS; ++part)
           for (int y = 0; y < n_q; ++y)
             for (int c = 0; c < C::CH; ++c)
               tma_load_3d(smem + (2 * part + y) * C::Q_TILE + c * C::Q_CHUNK, &tmap_q, &bars->q_full,
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss(tmem + C::COL_S + x * BN, sdesc_advance(qa, (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32),
                  sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s,
                  kk > 0 ? 1u : 0u);
-        if (C::Q_PARTS == 2 && p.q_parts == 2) {
+        if (PARTS == 2) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_ss(tmem + C::COL_S + x * BN,
@@ -367,14 +370,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc<C::TMEM_COLS>(tmem);
 }
 
-template <typename T, int D>
-cudaError_t launch_d(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                     const CUtensorMap& tv, cudaStream_t s) {
-  constexpr int smem = PairCfg<D>::SMEM;
-  auto kern = p.softcap != 0.0f ? pva_tree_pair_kernel<T, D, true> : pva_tree_pair_kernel<T, D, false>;
+template <typename T, int D, int PARTS>
+cudaError_t launch_parts(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, cudaStream_t s) {
+  constexpr int smem = PairCfg<D, PARTS>::SMEM;
+  auto kern = p.softcap != 0.0f ? pva_tree_pair_kernel<T, D, PARTS, true>
+                                : pva_tree_pair_kernel<T, D, PARTS, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(p.pieces), dim3(kThreads), smem, s, p, tq, tk, tv);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, cudaStream_t s) {
+  if constexpr (tree_takes_pair(256, D, 2))
+    if (p.q_parts == 2) return launch_parts<T, D, 2>(p, tq, tk, tv, s);
+  if (p.q_parts != 1) return cudaErrorInvalidValue;
+  return launch_parts<T, D, 1>(p, tq, tk, tv, s);
 }
 
 template <typename T>

@@ -27,7 +27,7 @@
 // rest rounded again, and S adds the products of both: the second costs d / 16
 // MMA steps of a time the copies leave over, and takes one of the three equal
 // roundings (queries, weights, output) out of the result.  At d = 256 tensor
-// memory holds the first part only.
+// memory has no room for the second part, which stays in shared memory.
 //
 // Masks: a row sees the cache rows [lo, past) and its ancestors among the new
 // rows.  Tiles wholly inside that range of every row of a warp need no mask;
@@ -55,17 +55,20 @@ struct TreeCfg {
   static constexpr int KV_TILE = CH * KV_CHUNK;   // one ring slot
   static constexpr int Q_PER_SLOT = KV_TILE / Q_CHUNK;
   static_assert(Q_PER_SLOT >= 1, "a Q chunk fits a ring slot");
-  static constexpr int Q_PARTS = tree_q_parts(D);
+  static constexpr bool REST_IN_SMEM = D > 192;  // the queries' second part
+  static constexpr int TMEM_PARTS = REST_IN_SMEM ? 1 : 2;
+  static constexpr int REST = REST_IN_SMEM ? CH * Q_CHUNK : 0;
   static constexpr int Q_SLOTS = (CH + Q_PER_SLOT - 1) / Q_PER_SLOT;  // of one part
-  static constexpr int SLOTS_FIT = (232448 - kHeadBytes) / KV_TILE;
+  static constexpr int SLOTS_FIT = (232448 - kHeadBytes - REST) / KV_TILE;
   static constexpr int SLOTS = SLOTS_FIT < 16 ? SLOTS_FIT : 16;
-  static_assert(SLOTS >= Q_PARTS * Q_SLOTS + 2, "ring depth");
-  static constexpr int SMEM = kHeadBytes + SLOTS * KV_TILE;
+  static_assert(SLOTS >= TMEM_PARTS * Q_SLOTS + 2, "ring depth");
+  static constexpr int OFF_REST = SLOTS * KV_TILE;
+  static constexpr int SMEM = kHeadBytes + OFF_REST + REST;
   static constexpr int TMEM_COLS = 512;
   static constexpr int COL_S = 0;
   static constexpr int COL_O = 2 * BN;
   static constexpr int COL_Q = COL_O + D;
-  static_assert(COL_Q + Q_PARTS * D / 2 <= TMEM_COLS, "TMEM budget");
+  static_assert(COL_Q + TMEM_PARTS * D / 2 <= TMEM_COLS, "TMEM budget");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -76,6 +79,7 @@ struct ItemSlot {
 
 struct Bars {
   uint64_t q_tmem, o_ready, o_done, o_free, drain;
+  uint64_t rest_full, rest_empty;
   uint64_t s_full[2], p_full[2];
   uint64_t meet[4];
   uint64_t ring_full[16], ring_empty[16];
@@ -102,7 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* status = p.status;
   volatile int* abort = &bars->abort;
-  const int q_slots = C::Q_SLOTS * (C::Q_PARTS == 2 && p.q_parts == 2 ? 2 : 1);
+  const int q_slots = C::Q_SLOTS * (C::REST_IN_SMEM ? 1 : p.q_parts);
+  const bool rest_in_smem = C::REST_IN_SMEM && p.q_parts == 2;
 
   if (threadIdx.x == 0) {
     bars->abort = 0;
@@ -112,6 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->o_free, kSoftmaxWarps);
     for (int w = 0; w < 4; ++w) mbar_init(&bars->meet[w], 2);
     mbar_init(&bars->drain, 1);
+    mbar_init(&bars->rest_full, 1);
+    mbar_init(&bars->rest_empty, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
       mbar_init(&bars->p_full[b], kSoftmaxWarps);
@@ -143,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     TreeWalk walk(p, blockIdx.x);
     const TileCopies tc(p, BN);
-    uint32_t loads = 0, published = 0;
+    uint32_t loads = 0, published = 0, rests = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, abort, status));
@@ -178,6 +185,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      if (rest_in_smem) {
+        // once the S MMAs of the segment before are done with it
+        if (!ok || !(ok = wait(&bars->rest_empty, (rests & 1) ^ 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->rest_full, C::REST);
+          for (int c = 0; c < C::CH; ++c)
+            tma_load_3d(smem + C::OFF_REST + c * C::Q_CHUNK, &tmap_q, &bars->rest_full, c * 64,
+                        s.t * kTcRows, p.B * p.Hkv + plane_q);
+        }
+        __syncwarp();
+        ++rests;
+      }
       // the block of the next tile's copy is looked up while this tile's slots
       // are waited for
       TileCopy copy = tc.locate(p, s, BN, s.j0, lane);
@@ -210,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tree_note_cut(p, blockIdx.x, nullptr);  // nothing to join
     }
     // Drain: every copy this warp issued must land before the CTA exits.
+    if (rests) mbar_wait<false>(&bars->rest_full, (rests - 1) & 1, abort, status);
     for (int s = 0; s < C::SLOTS; ++s) {
       const uint32_t fills = loads > (uint32_t)s ? (loads - 1 - s) / C::SLOTS + 1 : 0;
       if (fills) mbar_wait<false>(&bars->ring_full[s], (fills - 1) & 1, abort, status);
@@ -220,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_s = idesc_f16<T>(kTcRows, BN, false, false);
     constexpr uint32_t idesc_o = idesc_f16<T>(kTcRows, D, false, true);
     const uint64_t kdesc = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t restdesc = sdesc_sw128(smem_u32(smem + C::OFF_REST), 16, 1024);
     const uint64_t vdesc = sdesc_sw128(smem_u32(smem), C::KV_CHUNK, 1024);
     uint32_t q_cnt = 0, loads = 0, gt = 0, items = 0, taken = 0;
     bool ok = true;
@@ -231,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return r;
     };
-    auto issue_s = [&](uint32_t T_, uint32_t L) {
+    auto issue_s = [&](uint32_t T_, uint32_t L, bool last_of_segment) {
       const uint64_t ka = sdesc_advance(kdesc, (L % C::SLOTS) * C::KV_TILE);
       if (leader) {
 #pragma unroll
@@ -239,7 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts(tmem + C::COL_S + (T_ & 1) * BN, tmem + C::COL_Q + kk * 8,
                  sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s,
                  kk > 0 ? 1u : 0u);
-        if (q_slots > C::Q_SLOTS) {
+        if (C::REST_IN_SMEM) {
+          if (rest_in_smem) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + C::COL_S + (T_ & 1) * BN,
+                     sdesc_advance(restdesc, (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32),
+                     sdesc_advance(ka, (kk >> 2) * C::KV_CHUNK + (kk & 3) * 32), idesc_s, 1u);
+            if (last_of_segment) mma_commit(&bars->rest_empty);
+          }
+        } else if (q_slots > C::Q_SLOTS) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_ts(tmem + C::COL_S + (T_ & 1) * BN, tmem + C::COL_Q + D / 2 + kk * 8,
@@ -259,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (last) break;
       // Q is in TMEM once every softmax thread has copied its share.
       if (!(ok = wait(&bars->q_tmem, q_cnt & 1))) break;
+      if (rest_in_smem && !(ok = wait(&bars->rest_full, q_cnt & 1))) break;
       tc_fence_after();
       if (leader)
         for (int qs = 0; qs < q_slots; ++qs)
@@ -266,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       loads += q_slots;
       for (int j = 0; ok && j < 2 && j < n; ++j) {
         if (!(ok = wait_slot(loads + 2 * j))) break;
-        issue_s(gt + j, loads + 2 * j);
+        issue_s(gt + j, loads + 2 * j, j + 1 == n);
       }
       if (!ok) break;
       for (int j = 0; ok && j < n; ++j) {
@@ -287,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j + 2 < n) {
           if (!(ok = wait_slot(loads + 2 * (j + 2)))) break;
-          issue_s(T_ + 2, loads + 2 * (j + 2));
+          issue_s(T_ + 2, loads + 2 * (j + 2), j + 3 == n);
         }
       }
       loads += 2 * n;

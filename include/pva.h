@@ -414,10 +414,9 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  *
  * Arithmetic: products of dtype (f16/bf16 on tensor cores), scores, softmax and
  * sums in f32.  The softmax weights that multiply V are rounded to dtype
- * (f16/bf16).  Rotated queries are too at head_size 256, and above head_size 64
- * in steps of more than 128 query rows per kv head (tokens * num_heads /
- * kv_num_heads); otherwise what the rounding takes off them is multiplied as
- * well.
+ * (f16/bf16); what rounding takes off the rotated queries is multiplied as well.
+ * That costs up to a third of the rate of a long prompt chunk, which queries and
+ * keys rotated before by pva_rope_axes (rotary_dim 0 here) do without.
  * Results do not depend on timing: parts of a split row are added in order.
  *
  * Limits: f16/bf16: head_size in {64, 96, 128, 192, 256}, 16-byte aligned

@@ -107,13 +107,13 @@ def tree_step(q, k_new, v_new, k_cache, v_cache, past, parents=None, tree_lens=N
     return out, mass, spread, count, kc, vc
 
 
-def tolerance(out, mass, spread, count, d: int, dtype, v_max: float, q_rounded=False):
+def tolerance(out, mass, spread, count, d: int, dtype, v_max: float):
     """Largest deviation that the operator's roundings allow, element by element.
     Half a step of the type: once for the output (relative to it), and for
     f16/bf16 once per softmax weight (relative to sum w |v|).  Rotated queries
-    of f16/bf16 are rounded once (q_rounded) or kept as a rounded value and its
-    rounded rest, off by half a step squared: each element's error reaches the
-    score times |k|, so by at most that much of |q|.|k|.  f32 arithmetic:
+    of f16/bf16 are kept as a rounded value and its rounded rest, off by half a
+    step squared: each element's error reaches the score times |k|, so by at most
+    that much of |q|.|k|.  f32 arithmetic:
     a score of d products is off by at most d * 2^-23 * |q|.|k|, its exponential
     and softcap by a few 2^-21 of its size, which move a weight by expm1 of
     twice that; sums over the keys add (keys + 8) * 2^-23.  f16 weights below
@@ -121,7 +121,7 @@ def tolerance(out, mass, spread, count, d: int, dtype, v_max: float, q_rounded=F
     half_step = torch.finfo(dtype).eps / 2
     err = d * 2.0 ** -23 * spread + 2.0 ** -20 * (spread + 1)
     if dtype != torch.float32:
-        err = err + (half_step if q_rounded else half_step ** 2) * spread
+        err = err + half_step ** 2 * spread
     part = torch.expm1(2 * err) + (count + 8) * 2.0 ** -23
     if dtype != torch.float32:
         part = part + half_step * 1.01
