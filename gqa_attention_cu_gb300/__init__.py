@@ -18,9 +18,10 @@ import torch
 from . import workloads  # noqa: F401  (seeded synthetic inputs)
 
 __all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache",
-           "pva_block_tables", "pva_rope_axes", "pva_gqa_tree", "pva_kvcache_accept", "pva_get_status", "pva_schedule", "pva_status_string",
-           "pva_last_error", "pva_release", "pva_version", "pva_profile", "pva_kernel_times",
-           "pva_selftest_wait", "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
+           "pva_block_tables", "pva_rope_axes", "pva_gqa_tree", "pva_kvcache_accept",
+           "pva_get_status", "pva_schedule", "pva_status_string", "pva_last_error",
+           "pva_release", "pva_version", "pva_profile", "pva_kernel_times", "pva_selftest_wait",
+           "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpva.so")

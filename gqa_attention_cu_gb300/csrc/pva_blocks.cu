@@ -8,14 +8,18 @@
 // than 64 blocks are moved by all threads together.  700 sequences that take or
 // give back 15,700 blocks: 10.3 us; a thread per block that finds its
 // sequence by bisection 15.7 us, bound by the one SM's instructions; a thread
-// per sequence 21 and 13 us, bound by its scattered words.  Slots are written by the same CTA while they are few, and by
-// a grid of their own where they are many.
+// per sequence 21 and 13 us, bound by its scattered words.  16 sequences with 8 new
+// tokens each: 3 us, a launch and four dependent reads.  Slots are written by the
+// same CTA while they are few, and by a grid of their own where they are many
+// (250,000: 6 us after the allocation).
 //
 // pva_kvcache_accept moves rows in place.  A path rises, path[i] >= i, so row i
 // is read (as some path[j], j <= i) before or when it is written if each thread
 // keeps to one 16-byte column and goes through i in order: no copy is needed.
 // A sequence's path and blocks are looked up once per CTA, which then moves the
-// columns of many heads and layers with eight rows in flight per thread.
+// columns of many heads and layers with eight rows in flight per thread.  64
+// sequences x 32 layers x 8 heads of 128 bf16, paths of up to 8 nodes (75 MB read
+// and written): 11 us where they are in L2, 6.8 TB/s; 15 us where they are not.
 #include <limits.h>
 
 #include "pva_device.cuh"

@@ -210,7 +210,8 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
     if (TREE) {
       const int b = tok / s.T, node = tok - b * s.T;
       // also called for steps that will be refused: nothing is taken for granted
-      const int past = load<TREE>(s.past + b), in = past >= 0 ? (int)(((uint32_t)past + node) / (uint32_t)s.page) : -1;
+      const int past = load<TREE>(s.past + b);
+      const int in = past >= 0 ? (int)(((uint32_t)past + node) / (uint32_t)s.page) : -1;
       if (node < (s.lens ? load<TREE>(s.lens + b) : s.T) && (unsigned)in < (unsigned)s.max_blocks) {
         const int row = past + node;
         const int block = s.table ? load<TREE>(s.table + (size_t)b * s.max_blocks + in) : b;

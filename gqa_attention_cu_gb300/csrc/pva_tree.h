@@ -8,17 +8,17 @@
 // `item_places` for what an item costs whatever its length (queries, pipeline,
 // output).  All items' places form one line (sequence, kv head, q tile, key
 // tile), which is cut into pieces of `chunk` places, one piece per CTA: every
-// CTA gets the same amount of work whatever the lengths are.  An item that lies across a cut is computed
-// by several CTAs, each of which leaves its unnormalised sums (O, the running
-// maximum m and the sum l, all fp32) in a slot; the join kernel adds them in
-// the order of the line, so results do not depend on timing.
+// CTA gets the same amount of work whatever the lengths are.  An item that lies
+// across a cut is computed by several CTAs, each of which leaves its unnormalised
+// sums (O, the running maximum m and the sum l, all fp32) in a slot; the join
+// kernel adds them in the order of the line, so results do not depend on timing.
 //
 // Where q tiles share keys and there are many items, CTAs instead take whole
 // items in turn from a counter: then the q tiles of one kv head run side by
 // side and find each other's keys in L2, where pieces of the line would be at
 // far-apart places of the cache at any time.  (2048-token chunks of 8 sequences
-// on 4.6k rows, d = 128: 1.31 ms by pieces, bound by copies at 5.3 TB/s,
-// against 1.10 ms.)  With fewer than 6 items per CTA the last ones would
+// on 4.6k rows, d = 128, queries rotated before: 1.31 ms by pieces, bound by copies
+// at 5.3 TB/s, against 1.10 ms.)  With fewer than 6 items per CTA the last ones would
 // leave too many CTAs idle.
 #pragma once
 

@@ -193,12 +193,15 @@ __device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p)
 // maximum passes it by more than 2^8; alpha is the factor that O then has to be
 // scaled by.  All warps of the rows call; false: a wait was given up.
 //
-// Tiles without a mask (and without a softcap) are read once and worked on in
-// registers.  The others go over the columns twice, 32 at a time in a loop:
-// reading tensor memory again is about 18 cycles, while unrolled code for every
-// kind of mask and softcap spills and does not stay in the instruction cache
-// (a window and a softcap at d = 64, 500-token chunks: 214 us, in a loop 189 us;
-// but 2048-token chunks of 8 sequences at d = 128: 1.13 ms, in a loop 1.26 ms).
+// Tiles without a mask are read once and worked on in registers (2048-token
+// chunks of 8 sequences, d = 128, queries rotated before: 1.13 ms, in a loop 1.26
+// ms; long contexts with a softcap, while its series holds: 401 us, in a loop 453
+// us).  The others go over the columns twice, 32 at a time in a loop: reading
+// tensor memory again is about 18 cycles, while unrolled code for every kind of
+// mask and softcap spills and does not stay in the instruction cache (a window and
+// a softcap at d = 64, 500-token chunks: 214 us, in loops 185 us).  Bound by
+// instructions, not by exponentials: a quarter of them by a polynomial on the FMA
+// pipe made those chunks 203 us.
 template <typename T, int N, bool CAP, typename Row>
 __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowView& view, int past,
                                                 int k0, uint32_t t_s, float s_mul, float cap_mul,
