@@ -268,10 +268,15 @@ int get_workspace(int dev, cudaStream_t stream, size_t need, Workspace** out) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
     // A graph captured on this stream keeps the address it was captured with,
     // so a buffer that went into one lives until pva_release.
-    if (w.buf && w.in_graph)
-      w.retired.push_back(w.buf);
-    else if (w.buf)
+    if (w.buf && w.in_graph) {
+      try {
+        w.retired.push_back(w.buf);
+      } catch (...) {
+        return fail(PVA_ERR_OOM, "host memory ran out");
+      }
+    } else if (w.buf) {
       cudaFree(w.buf);
+    }
     w.buf = nullptr;
     w.bytes = 0;
     w.in_graph = false;

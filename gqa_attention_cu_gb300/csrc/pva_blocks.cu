@@ -31,7 +31,7 @@ namespace pva {
 namespace {
 
 constexpr int kBlockThreads = 1024;
-constexpr int kWordRefused = 18;  // status block: 1 while the last allocation was refused
+constexpr int kWordRefused = 18;  // status block: 1 where the last allocation was refused
 // New tokens up to which the allocating CTA writes the slot map itself.
 constexpr long long kSlotsInOne = 4096;
 constexpr int kAhead = 8;          // loads a thread has under way
@@ -470,7 +470,8 @@ extern "C" int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* p
                               : "without a block table the cache has one block a sequence");
     if (!block_table) max_blocks = 1;
     if (B > 65535) return fail(PVA_ERR_UNSUPPORTED, "at most 65535 sequences");
-    if ((long long)max_blocks * page_size > INT_MAX)
+    if ((long long)max_blocks * page_size > INT_MAX || (long long)head_size * 4 > INT_MAX ||
+        (long long)n_blocks * kv_num_heads > INT_MAX)
       return fail(PVA_ERR_INVALID_ARG, "cache extents do not fit in int32");
     const long long size = dtype == PVA_F32 ? 4 : 2;
     const long long one = (long long)n_blocks * kv_num_heads * page_size * head_size;

@@ -145,8 +145,8 @@ int encode_plane_map(CUtensorMap* map, const void* base, int dtype, int dim, int
 // What a call gets from the library for its device and stream (under api_mutex).
 struct CallContext {
   int num_sms = 0;
-  uint32_t* status = nullptr;  // [0] sticky PVA_DEV_* bits; words 16 to 63 start at zero and are
-                               // returned to zero by every kernel that uses them
+  uint32_t* status = nullptr;  // [0] sticky PVA_DEV_* bits; words 16 and 17 are zero between
+                               // calls; 18 is what a call's first kernel tells its second
   uint8_t* buf = nullptr;      // workspace of at least the bytes asked for
 };
 std::mutex& api_mutex();

@@ -167,3 +167,16 @@ def test_accept_after_a_rejected_step_moves_nothing():
     pva.pva_kvcache_accept(kg, vg, i32([1, 2]).to(DEV), path.to(DEV), m.to(DEV), new, block_table=table.to(DEV))
     assert pva.pva_get_status() & pva.DEV_FLAGS["kv_cache"]
     assert same_bits(kg.cpu(), kc[0]) and new.tolist() == [1, 2]
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_accept_paths_longer_than_one_look_up(page):
+    B, width, past = 3, 300, [5, 0, 77]
+    kc, vc, table, path, m = make_accept(B, width, 2, 2, 64, torch.bfloat16, page, past, 9, 420)
+    m[:] = i32([300, 129, 128])
+    kg, vg, new = kc.to(DEV), vc.to(DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    pva.pva_kvcache_accept(kg, vg, i32(past).to(DEV), path.to(DEV), m.to(DEV), new,
+                           block_table=None if table is None else table.to(DEV))
+    assert pva.pva_get_status() == 0
+    kr, vr, lens = paged.accept(kc, vc, past, path, m, table)
+    assert same_bits(kg.cpu(), kr) and same_bits(vg.cpu(), vr) and new.tolist() == lens

@@ -159,6 +159,44 @@ def test_f32(d):
     parity(1, 40, 3, 3, d, "f32", [333], d + 1, chain=True)
 
 
+@pytest.mark.parametrize("T,G", [(1, 1), (2, 4), (3, 3), (16, 1), (17, 1), (8, 3), (5, 5), (49, 1)])
+def test_f32_rows_of_a_head(T, G):
+    parity(3, T, 2 * G, 2, 96, "f32", [300, 0, 65], T + G, page=32, rot=96)
+    parity(2, T, G, 1, 30, "f32", [70, 5], T + G + 1, chain=True)
+
+
+@pytest.mark.parametrize("T,d,rot", [(300, 64, 0), (129, 256, 256), (500, 128, 128)])
+def test_more_items_than_the_grid_takes_in_pieces(T, d, rot):
+    """A chain of more than one query tile on 57 sequences x 8 heads: at least 912
+    items, which CTAs take one after another."""
+    B, Hkv, td = 57, 8, torch.bfloat16
+    past = [(37 * b) % 150 for b in range(B)]
+    s = make_tree(B, T, Hkv, Hkv, d, "bf16", past, 75, chain=True, rot=rot)
+    out, kc, _ = call(s, Hkv, Hkv)
+    assert pva.pva_get_status() == 0
+    worst = 0.0
+    for b in range(B):
+        n = past[b] + T
+        at = torch.arange(past[b], n)
+        q, k_new = s["q"][b].to(DEV).double(), s["k_new"][b]
+        if rot:
+            k_new = paged.rope_rows(k_new, s["cos"], s["sin"], at[None])
+            c, w = (s[x][at, :].to(DEV).double()[:, None] for x in ("cos", "sin"))
+            q = torch.cat([q[..., :d // 2] * c - q[..., d // 2:] * w, q[..., :d // 2] * w + q[..., d // 2:] * c], -1)
+        k, v = (torch.cat([s[x][b, :, :past[b]], new.transpose(0, 1)], 1).to(DEV).double()
+                for x, new in (("k_cache", k_new), ("v_cache", s["v_new"][b])))
+        hidden = torch.arange(n, device=DEV)[None] > at.to(DEV)[:, None]
+        q = q.transpose(0, 1) / d ** 0.5
+        w = torch.softmax((q @ k.mT).masked_fill(hidden, -torch.inf), -1)
+        spread = (q.abs() @ k.abs().mT).masked_fill(hidden, 0).amax(-1)
+        ref, mass = w @ v, w @ v.abs()
+        count = (at + 1).to(DEV).expand(Hkv, T)
+        tol = paged.tolerance(ref, mass, spread, count, d, td, 6.0)
+        worst = max(worst, float(((out[b].transpose(0, 1).double() - ref).abs() / tol).max()))
+        assert same_bits(kc[b, :, past[b]:n].cpu(), k_new.transpose(0, 1))
+    assert worst <= 1, f"off by {worst:.2f} of the bound"
+
+
 def test_a_thousand_nodes():
     s = make_tree(1, 1024, 2, 1, 64, "bf16", [5], 21)
     # a comb: long ways up, across many mask words
@@ -399,6 +437,94 @@ def test_rounds_of_drafting_on_a_paged_cache():
         assert new_lens.tolist() == past
         resize(past)
     assert pva.pva_get_status() == 0
+
+
+def test_a_round_captured_on_a_side_stream():
+    """Blocks, tree step and accepted path in one graph: replayed with new
+    inputs, round after round."""
+    B, T, H, Hkv, d, page, pool = 2, 7, 8, 2, 64, 16, 24
+    gen = torch.Generator().manual_seed(61)
+    td = torch.float16
+    randn = lambda *sh: torch.randn(sh, generator=gen).to(td)  # noqa: E731
+    cos, sin = paged_tables(100, d)
+    kc, vc = randn(pool, Hkv, page, d), randn(pool, Hkv, page, d)
+    table = torch.full((B, 6), -1, dtype=torch.int32)
+    table[0, :2], table[1, :1] = torch.tensor([3, 9]), torch.tensor([20])
+    left = [i for i in range(pool) if i not in (3, 9, 20)]
+    past = [30, 12]
+    state = [table.tolist(), [2, 1], left + [0] * (pool - len(left)), len(left)]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    dev = {n: t.to(DEV) for n, t in dict(
+        q=randn(B, T, H, d), k=randn(B, T, Hkv, d), v=randn(B, T, Hkv, d), kc=kc, vc=vc, table=table,
+        held=i32(state[1]), free=i32(state[2]), count=i32([state[3]]), room=i32(past), past=i32(past),
+        parents=i32([[-1] * T] * B), path=i32([[0] * T] * B), m=i32([0] * B), new=i32([0] * B),
+        cos=cos, sin=sin, out=randn(B, T, H, d)).items()}
+
+    def step(t):
+        pva.pva_block_tables(t["room"], t["table"], t["held"], t["free"], t["count"], page)
+        pva.pva_gqa_tree(t["q"], t["k"], t["v"], t["kc"], t["vc"], t["past"], t["out"], H, Hkv,
+                         parents=t["parents"], block_table=t["table"], cos_cache=t["cos"], sin_cache=t["sin"])
+        pva.pva_kvcache_accept(t["kc"], t["vc"], t["past"], t["path"], t["m"], t["new"],
+                               block_table=t["table"])
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        trial = {n: t.clone() for n, t in dev.items()}
+        trial["room"] += T
+        step(trial)
+        stream.synchronize()
+        assert pva.pva_get_status(stream) == 0
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(dev)
+        for _ in range(3):
+            i = torch.arange(T)
+            parents = (i - 1 - (torch.rand(B, T, generator=gen) * 3).long()).clamp(min=-1).int()
+            path = []
+            for b in range(B):
+                node, way = T - 1 - b, []
+                while node >= 0:
+                    way.append(node)
+                    node = int(parents[b, node])
+                path.append(way[::-1])
+            m, room = [len(w) for w in path], [p + T for p in past]
+            wide = i32([w + [-1] * (T - len(w)) for w in path])
+            q, k, v = randn(B, T, H, d), randn(B, T, Hkv, d), randn(B, T, Hkv, d)
+            for name, x in dict(q=q, k=k, v=v, parents=parents, path=wide, m=i32(m), room=i32(room),
+                                past=i32(past)).items():
+                dev[name].copy_(x)
+            graph.replay()
+            stream.synchronize()
+            assert pva.pva_get_status(stream) == 0
+            state = list(paged.block_tables(room, *state, page)[:4])
+            assert dev["table"].tolist() == state[0]
+            ref = paged.tree_step(q, k, v, kc, vc, past, parents, None, i32(state[0]), cos, sin)
+            tol = paged.tolerance(*ref[:4], d, td, 6.0)
+            assert ((dev["out"].double().cpu() - ref[0]).abs() <= tol).all()
+            kr, vr, past = paged.accept(ref[4][None], ref[5][None], past, wide, m, state[0])
+            kc, vc = kr[0], vr[0]
+            assert same_bits(dev["kc"].cpu(), kc) and same_bits(dev["vc"].cpu(), vc)
+            assert dev["new"].tolist() == past
+
+
+@pytest.mark.parametrize("T", [5, 70])
+def test_f16_queries_that_rotate_past_the_largest_f16(T):
+    """Finite, and off by the parts' roundings alone: below 65504 sqrt(2) the
+    second part is under 2^15, so at most 8 off."""
+    d, scale = 64, 2e-6
+    s = make_tree(1, T, 4, 2, d, "f16", [40], 70, rot=d, page=16)
+    sign = torch.where(s["q"] < 0, -1.0, 1.0)
+    s["q"] = (sign * (60000 + 2000 * s["q"].float().clamp(-2, 2))).to(torch.float16)
+    out, _, _ = call(s, 4, 2, scale=scale)
+    assert pva.pva_get_status() == 0
+    ref, mass, spread, count, kr, vr = paged.tree_step(
+        s["q"], s["k_new"], s["v_new"], s["k_cache"], s["v_cache"], s["past"], s["parents"], None,
+        s["block_table"], s["cos"], s["sin"], None, None, False, False, scale)
+    assert torch.isfinite(out).all()
+    k_sum = float(torch.nan_to_num(kr.double()).abs().sum(-1).max())
+    # tolerance() allows half a step squared, 2^-22, of |q|.|k|
+    tol = paged.tolerance(ref, mass, spread + 2.0 ** 22 * scale * 8 * k_sum, count, d, torch.float16, 6.0)
+    assert ((out.double().cpu() - ref).abs() <= tol).all()
 
 
 def paged_tables(rows, rot):

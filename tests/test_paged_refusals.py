@@ -100,7 +100,8 @@ def accept(lib, **kw):
     (dict(kc=None), -1), (dict(vc=None), -1), (dict(past=None), -1), (dict(path=None), -1), (dict(m=None), -1),
     (dict(new=None), -1), (dict(B=0), -1), (dict(width=0), -1), (dict(layers=0), -1), (dict(page=0), -1), (dict(d=0), -1),
     (dict(tw=0), -1), (dict(table=None), -1), (dict(dtype=9), -1), (dict(B=70000), -2),
-    (dict(layers=2, stride=100), -1), (dict(new=(1 << 20) + 4), -1), (dict(kc=17), -1), (dict(tw=1 << 28), -1)])
+    (dict(layers=2, stride=100), -1), (dict(new=(1 << 20) + 4), -1), (dict(kc=17), -1), (dict(tw=1 << 28), -1),
+    (dict(d=1 << 30), -1), (dict(blocks=1 << 30), -1)])
 def test_accept_refusals(lib, kw, code):
     assert accept(lib, **kw) == code
     assert pva.pva_last_error() != ""
