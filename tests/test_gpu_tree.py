@@ -507,6 +507,42 @@ def test_a_round_captured_on_a_side_stream():
             assert dev["new"].tolist() == past
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_blocks_past_32_bit_offsets(dtype):
+    """The same step, path and prompt rows with the sequences' blocks at the start
+    of a small pool and behind 2^31 elements of a large one: the same bits."""
+    B, T, H, Hkv, d, page = 2, 6, 4, 2, 128, 64
+    s = make_tree(B, T, H, Hkv, d, dtype, [100, 30], 90, page=page, rot=d)
+    pool, first = s["k_cache"].shape[0], 2 ** 31 // (Hkv * page * d) + 5
+    free = [b for b in range(pool) if b not in s["block_table"].flatten().tolist()][0]
+    path = torch.tensor([[0, 2, 5], [1, 3, 4]], dtype=torch.int32, device=DEV)
+    g = torch.Generator().manual_seed(91)
+    k, v = (torch.randn(3, Hkv, d, generator=g).to(DT[dtype]).to(DEV) for _ in range(2))
+    pos = torch.tensor([[7, 0, 50]], device=DEV)
+    results = []
+    for shift in (0, first):
+        t = {n: x.to(DEV) if torch.is_tensor(x) else x for n, x in s.items()}
+        table = torch.where(t["block_table"] >= 0, t["block_table"] + shift, -1).int()
+        caches = []
+        for c in (t["k_cache"], t["v_cache"]):
+            big = torch.empty((shift + pool, *c.shape[1:]), dtype=c.dtype, device=DEV)
+            big[shift:] = c
+            caches.append(big)
+        out = torch.empty_like(t["q"])
+        pva.pva_gqa_tree(t["q"], t["k_new"], t["v_new"], *caches, t["past"], out, H, Hkv, parents=t["parents"],
+                         block_table=table, cos_cache=t["cos"], sin_cache=t["sin"])
+        new = torch.empty(B, dtype=torch.int32, device=DEV)
+        pva.pva_kvcache_accept(*caches, t["past"], path, torch.full_like(new, 3), new, block_table=table)
+        slots = (shift + free) * page + torch.tensor([3, 0, 63], device=DEV)
+        pva.pva_rope_axes(None, k, t["cos"], t["sin"], pos, v=v, k_cache=caches[0], v_cache=caches[1],
+                          slot_map=slots)
+        assert pva.pva_get_status() == 0
+        results.append([out.cpu(), *(c[shift:].cpu() for c in caches)])
+        del caches, big
+    for x, y in zip(*results):
+        assert same_bits(x, y)
+
+
 @pytest.mark.parametrize("T", [5, 70])
 def test_f16_queries_that_rotate_past_the_largest_f16(T):
     """Finite, and off by the parts' roundings alone: below 65504 sqrt(2) the
