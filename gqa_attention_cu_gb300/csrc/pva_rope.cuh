@@ -95,17 +95,6 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-// A value that rounds to a finite one, for the first of a query's two parts: the
-// rest of an infinity would be a NaN.  (Only f16 overflows within f32's range.)
-template <typename T>
-__device__ __forceinline__ float finite(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ float finite<__half>(float x) {
-  return x != x ? x : fminf(fmaxf(x, -65504.0f), 65504.0f);
-}
-
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Pack {
   T v[VEC];
@@ -322,9 +311,8 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
               const float a = load_f(x0[y].v[e]), f = load_f(x1[y].v[e]);
               const float g0 = __fsub_rn(__fmul_rn(cs.x, a), __fmul_rn(cs.y, f));
               const float g1 = __fadd_rn(__fmul_rn(cs.y, a), __fmul_rn(cs.x, f));
-              const bool parted = TREE && is_q && s.q_rest;
-              x0[y].v[e] = round_to<T>(parted ? finite<T>(g0) : g0);
-              x1[y].v[e] = round_to<T>(parted ? finite<T>(g1) : g1);
+              x0[y].v[e] = round_to<T>(g0);
+              x1[y].v[e] = round_to<T>(g1);
               if (TREE) {
                 rest0.v[e] = round_to<T>(g0 - load_f(x0[y].v[e]));
                 rest1.v[e] = round_to<T>(g1 - load_f(x1[y].v[e]));
