@@ -42,9 +42,13 @@ __device__ __forceinline__ int walk_up(const RopeStep& s, int tok) {
 // the step is complete.  What it waits for is the permission to write -- and
 // the depths of large trees, whose way up is too long to walk here.
 constexpr int kWalkT = 64;
+// CTAs an SM holds of the tree form, and as many are launched (500-token chunks of 6
+// sequences in bf16, the whole step: 6 an SM 186.4, 7 184.0, 8 with a few registers
+// spilled 189.6 us).
+constexpr int kTreeCtas = 7;
 
 template <typename T, int VEC, bool TREE>
-__global__ void __launch_bounds__(kRopeThreads, TREE ? 6 : kRopeCtas) pva_rope_kernel(RopeStep s) {
+__global__ void __launch_bounds__(kRopeThreads, TREE ? kTreeCtas : kRopeCtas) pva_rope_kernel(RopeStep s) {
   __shared__ RopeToken sh[2];
   allow_next_grid();
   const bool walk = TREE && s.parents && !s.pos && s.rt.rot > 0 && s.T <= kWalkT;
@@ -63,7 +67,7 @@ template <typename T>
 cudaError_t launch_rope_type(const RopeStep& s, bool tree, int num_sms, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(T);
   const bool wide = rope_wide(s, VEC);
-  const int most = num_sms * kRopeCtas;
+  const int most = num_sms * (tree ? kTreeCtas : kRopeCtas);
   const dim3 grid(s.tokens < most ? s.tokens : most);
   if (wide)
     return tree ? launch_dependent(pva_rope_kernel<T, VEC, true>, grid, dim3(kRopeThreads), 0, st, s)

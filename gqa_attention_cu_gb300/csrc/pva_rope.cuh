@@ -72,6 +72,8 @@ struct RopeStep {
   const int32_t* parents;   // [B, T], or nullptr: a chain
   const int32_t* table;     // [B, max_blocks]; nullptr: block b
   int T, max_blocks;
+  uint32_t group_inv;       // ceil(2^32 / G): row / G is the high word of row * this while
+                            // row * G < 2^32; 0: divide
   int negate_q;             // a negative scale, moved into the queries
   void* q_rest;             // nullptr, or what rounding took off the queries, laid out like them
   void* out;                // attention output: rows of unused nodes are zeroed
@@ -295,6 +297,9 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
         cached = s.n_slots >> 32 ? now.slot / s.page : (uint32_t)now.slot / (uint32_t)s.page;
         cache_row = (size_t)(now.slot - cached * s.page);
       }
+      // where the token's query rows go: kv head h's group at h * group_stride
+      const size_t group_stride = TREE ? (size_t)s.T * G * s.d : 0;
+      const size_t to = TREE ? ((size_t)b * s.Hkv * s.T + node) * G * s.d : (size_t)tok * s.q_out_stride;
       for (int r = r0; r < n_rows; r += step * kRopeRows) {
         if (r != r0) load_rows(tok, r);
 #pragma unroll
@@ -302,6 +307,8 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
           const int row = r + y * step;
           if (row >= n_rows) continue;
           const bool is_q = row < nq, is_v = row >= nq + nk;
+          const int head = !TREE ? 0 : s.group_inv ? (int)__umulhi(row, s.group_inv) : row / G;
+          const size_t q_to = to + head * group_stride + (size_t)(row - head * G) * s.d;
           if (turned && !is_v) {
             if (rt.interleaved) split_pairs(x0[y], x1[y]);
             P rest0, rest1;
@@ -321,8 +328,7 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
             if (rt.interleaved) join_pairs(x0[y], x1[y]);
             if (TREE && is_q && s.q_rest) {
               if (rt.interleaved) join_pairs(rest0, rest1);
-              T* dst = static_cast<T*>(s.q_rest) +
-                       ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d;
+              T* dst = static_cast<T*>(s.q_rest) + q_to;
               if (s.negate_q) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
@@ -337,8 +343,7 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
             P z;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) z.v[e] = round_to<T>(0.0f);
-            T* dst = static_cast<T*>(s.q_rest) +
-                     ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d;
+            T* dst = static_cast<T*>(s.q_rest) + q_to;
             *reinterpret_cast<P*>(dst + d0) = z;
             *reinterpret_cast<P*>(dst + d1) = z;
           }
@@ -350,8 +355,7 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
                 x1[y].v[e] = -x1[y].v[e];
               }
             }
-            T* dst = TREE ? q_out + ((((size_t)b * s.Hkv + row / G) * s.T + node) * G + row % G) * s.d
-                          : q_out + (size_t)tok * s.q_out_stride + (size_t)row * s.d;
+            T* dst = q_out + q_to;
             *reinterpret_cast<P*>(dst + d0) = x0[y];
             *reinterpret_cast<P*>(dst + d1) = x1[y];
             continue;

@@ -882,6 +882,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   r.T = T;
   r.max_blocks = max_blocks;
   r.negate_q = s < 0.0f;
+  r.group_inv = G > 1 && (long long)H * G < (1ll << 32) ? (uint32_t)(((1ull << 32) + G - 1) / G) : 0;
   r.out = out;
   r.status = c.status;
 
