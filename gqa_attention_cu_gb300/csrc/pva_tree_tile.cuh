@@ -177,7 +177,7 @@ struct RowPair {
 // part fills the 3 KB that the largest rings leave, so there is no room to round
 // addresses up: the kernels use no other shared memory, whose start then is such
 // a boundary, and refuse to run if it is not.
-constexpr int kHeadBytes = 3072;
+constexpr int kHeadBytes = 3 * 1024;
 __device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p) {
   if ((smem_u32(smem) & 1023) == 0) return false;
   if (threadIdx.x == 0) {
