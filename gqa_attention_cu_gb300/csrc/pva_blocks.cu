@@ -23,6 +23,7 @@
 #include <limits.h>
 
 #include "pva_device.cuh"
+#include "pva_path.h"
 
 using namespace pva;
 using namespace pva::host;
@@ -362,10 +363,10 @@ __global__ void __launch_bounds__(kAcceptThreads) pva_accept_kernel(AcceptParams
   auto look_up = [&](int i0) {
     const int i = i0 + tid;
     if (i < n && !bad_path) {
-      const int x = path[i];
-      if (x < 0 || (i > 0 && path[i - 1] >= x) || past + (long long)x >= rows) {
+      if (!path_node_ok(path, i, past, rows)) {
         bad_path = true;
       } else {
+        const int x = path[i];
         s_to[tid] = place(past + i, bad_block);
         const long long from = place(past + x, bad_block);
         s_from[tid] = x == i ? -1 : from;

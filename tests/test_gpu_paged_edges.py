@@ -1,0 +1,45 @@
+"""Edges of the paged-cache operators: what the entry points promise to refuse or
+to keep the same, at the sizes where it can go wrong."""
+import pytest
+import torch
+
+import gqa_attention_cu_gb300 as pva
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def bits(t):
+    return t.contiguous().view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+# ---- accepted paths -------------------------------------------------------------
+def falls_then_rises():
+    """128 nodes of which each but one follows a smaller one."""
+    return list(range(64)) + [0, 1] + list(range(2, 64))
+
+
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("bad_path", [falls_then_rises(), list(range(-100, 28))], ids=["falls", "starts below 0"])
+def test_path_longer_than_its_table(page, bad_path):
+    """A path that does not rise from 0 on and is longer than the table has rows:
+    that sequence is left as it is.  (Which look-ups the check lets pass:
+    test_accepted_path_check.py.)"""
+    B, width, Hkv, d, rows = 2, 128, 2, 64, 64
+    n = rows // page
+    room = torch.full((B * n + 256,), 2 ** 30, dtype=torch.int32, device=DEV)
+    table = room[:B * n].view(B, n)
+    table.copy_(torch.arange(B * n, device=DEV).view(B, n))
+    g = torch.Generator().manual_seed(page)
+    kc, vc = (torch.randn(B * n, Hkv, page, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    k0, v0 = kc.clone(), vc.clone()
+    path = i32([list(range(0, 128)), bad_path])
+    new = i32([-9, -9])
+    pva.pva_kvcache_accept(kc, vc, i32([3, 0]), path, i32([2, width]), new, block_table=table)
+    assert pva.pva_get_status() == pva.DEV_FLAGS["tree"]
+    assert new.tolist() == [5, 0]
+    assert torch.equal(bits(kc), bits(k0)) and torch.equal(bits(vc), bits(v0))
