@@ -274,13 +274,25 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
     if (TREE) {
       b = tok / s.T;
       node = tok - b * s.T;
-      if (now.slot < 0) {  // an unused node: zeros out
+      if (now.slot < 0) {
+        // an unused node: zeros out
         write = false;
         P z;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) z.v[e] = round_to<T>(0.0f);
         P* o = reinterpret_cast<P*>(static_cast<T*>(s.out) + (size_t)tok * s.H * s.d);
         for (int e = tid; e < s.H * s.d / VEC; e += kRopeThreads) o[e] = z;
+        // Its queries are zeros where the attention has them in one warp (32 rows) with
+        // used ones: a warp's rows are rounded alike, and what the workspace held must
+        // not decide how.
+        const int used = s.lens ? load<TREE>(s.lens + b) : s.T;
+        const int group = (long long)node * G < ((long long)used * G + 31) / 32 * 32 ? G * s.d / VEC : 0;
+        for (int e = tid; e < s.Hkv * group; e += kRopeThreads) {
+          const int h = e / group;
+          const size_t at = (((size_t)b * s.Hkv + h) * s.T + node) * group + (e - h * group);
+          reinterpret_cast<P*>(q_out)[at] = z;
+          if (s.q_rest) reinterpret_cast<P*>(s.q_rest)[at] = z;
+        }
       }
     } else {
       const int4 bad = *reinterpret_cast<const int4*>(sh[buf].bad);

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import gqa_attention_cu_gb300 as pva
+from paged_cases import DT, make_tree
+from test_gpu_tree import call
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -43,3 +45,22 @@ def test_path_longer_than_its_table(page, bad_path):
     assert pva.pva_get_status() == pva.DEV_FLAGS["tree"]
     assert new.tolist() == [5, 0]
     assert torch.equal(bits(kc), bits(k0)) and torch.equal(bits(vc), bits(v0))
+
+
+# ---- softcapped steps -------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,T,lens,d,rot", [(2, 6, [5, 3], 128, 128), (1, 6, [5], 64, 0), (2, 70, [65, 33], 64, 64),
+                                            (1, 140, [139], 192, 0), (1, 9, [7], 256, 256)])
+def test_unused_nodes_leave_the_bits_of_the_used(B, T, lens, d, rot, dtype):
+    """What the calls before left where unused nodes' queries would lie, small
+    scores or very large ones, must not show in a softcapped step's output."""
+    H, Hkv = 8, 2
+    s = make_tree(B, T, H, Hkv, d, dtype, [150, 300][:B], 5, lens=lens, rot=rot)
+    s["q"] = (s["q"].float() * 0.8).to(DT[dtype])
+    outs = []
+    for factor in (0.0, 1000.0, 0.0, 1000.0):
+        before = dict(s, tree_lens=None, q=(s["q"].float() * factor).to(DT[dtype]))
+        call(before, H, Hkv, softcap=30.0)
+        outs.append(call(s, H, Hkv, softcap=30.0)[0])
+    assert pva.pva_get_status() == 0
+    assert all(torch.equal(bits(o), bits(outs[0])) for o in outs[1:])
