@@ -97,6 +97,19 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// The first of a query's two parts: finite for any finite x, or there would be no
+// rest of it (only f16 overflows within f32's range).  An infinity's rest is one.
+template <typename T>
+__device__ __forceinline__ T round_finite(float x) {
+  return round_to<T>(x);
+}
+template <>
+__device__ __forceinline__ __half round_finite<__half>(float x) {
+  unsigned short h;
+  asm("cvt.rn.satfinite.f16.f32 %0, %1;" : "=h"(h) : "f"(x));
+  return __ushort_as_half(h);
+}
+
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Pack {
   T v[VEC];
@@ -324,14 +337,15 @@ __device__ __forceinline__ void rope_tokens(const RopeStep& s, int first, int st
           if (turned && !is_v) {
             if (rt.interleaved) split_pairs(x0[y], x1[y]);
             P rest0, rest1;
+            const bool parted = TREE && std::is_same<T, __half>::value && is_q && s.q_rest;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
               const float2 cs = sh[buf].cs[u * VEC + e];
               const float a = load_f(x0[y].v[e]), f = load_f(x1[y].v[e]);
               const float g0 = __fsub_rn(__fmul_rn(cs.x, a), __fmul_rn(cs.y, f));
               const float g1 = __fadd_rn(__fmul_rn(cs.y, a), __fmul_rn(cs.x, f));
-              x0[y].v[e] = round_to<T>(g0);
-              x1[y].v[e] = round_to<T>(g1);
+              x0[y].v[e] = parted ? round_finite<T>(g0) : round_to<T>(g0);
+              x1[y].v[e] = parted ? round_finite<T>(g1) : round_to<T>(g1);
               if (TREE) {
                 rest0.v[e] = round_to<T>(g0 - load_f(x0[y].v[e]));
                 rest1.v[e] = round_to<T>(g1 - load_f(x1[y].v[e]));

@@ -416,9 +416,9 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  * sums in f32.  The softmax weights that multiply V are rounded to dtype
  * (f16/bf16); what rounding takes off the rotated queries is multiplied as well.
  * That costs up to a third of the rate of a long prompt chunk, which queries and
- * keys rotated before by pva_rope_axes (rotary_dim 0 here) do without.  Rotated
- * f16 queries have to stay within 65504, as the cached keys do: the output rows
- * of one that does not are NaN.
+ * keys rotated before by pva_rope_axes (rotary_dim 0 here) do without.  f16
+ * queries may rotate past f16's range, to twice 65504 (the second part holds what
+ * is above 65504, rounded to f16); the keys may not, which the cache holds as f16.
  * Results do not depend on timing: parts of a split row are added in order.
  *
  * Limits: f16/bf16: head_size in {64, 96, 128, 192, 256}, 16-byte aligned

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import gqa_attention_cu_gb300 as pva
+from oracle import paged
 from paged_cases import DT, make_tree
 from test_gpu_tree import call
 
@@ -64,3 +65,38 @@ def test_unused_nodes_leave_the_bits_of_the_used(B, T, lens, d, rot, dtype):
         outs.append(call(s, H, Hkv, softcap=30.0)[0])
     assert pva.pva_get_status() == 0
     assert all(torch.equal(bits(o), bits(outs[0])) for o in outs[1:])
+
+
+# ---- f16 queries that rotate past the type's range ----------------------------------
+@pytest.mark.parametrize("T", [5, 70])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale", [2e-6, -2e-6])
+def test_f16_queries_that_rotate_past_the_largest_f16(T, d, scale):
+    """Elements of 56000 to 64000, so that pairs rotate to at most 64000 sqrt(2) <
+    65504 + 2^15: the second part is then off by half of f16's step below 2^15, 8,
+    and what that makes of a score is at most scale * 8 * sum |k|."""
+    s = make_tree(1, T, 4, 2, d, "f16", [40], 70, rot=d, page=16)
+    sign = torch.where(s["q"] < 0, -1.0, 1.0)
+    s["q"] = (sign * (60000 + 2000 * s["q"].float().clamp(-2, 2))).to(torch.float16)
+    out, _, _ = call(s, 4, 2, scale=scale)
+    assert pva.pva_get_status() == 0
+    ref, mass, spread, count, kr, _ = paged.tree_step(
+        s["q"], s["k_new"], s["v_new"], s["k_cache"], s["v_cache"], s["past"], s["parents"], None,
+        s["block_table"], s["cos"], s["sin"], scale=scale)
+    assert torch.isfinite(out).all()
+    k_sum = float(torch.nan_to_num(kr.double()).abs().sum(-1).max())
+    # tolerance() allows half a step squared, 2^-22, of its `spread`
+    tol = paged.tolerance(ref, mass, spread + 2.0 ** 22 * abs(scale) * 8 * k_sum, count, d, torch.float16, 6.0)
+    assert ((out.double().cpu() - ref).abs() <= tol).all()
+
+
+def test_an_infinite_f16_query_is_no_large_one():
+    """Its row is NaN, as the definition's; the others are what they are without it."""
+    s = make_tree(1, 6, 4, 2, 64, "f16", [40], 71, rot=64, page=16)
+    good = call(s, 4, 2)[0]
+    s["q"][0, 3, 1, 5] = float("inf")
+    out = call(s, 4, 2)[0]
+    assert pva.pva_get_status() == 0
+    assert torch.isnan(out[0, 3, 1]).all()
+    out[0, 3, 1] = good[0, 3, 1]
+    assert torch.equal(bits(out), bits(good))
