@@ -789,6 +789,10 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   const float s = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
   p.scale = fabsf(s);
   p.softcap = fabsf(softcap);
+  if (p.softcap != 0.0f) {  // pva_tree_tile.cuh; and the products' squares have to be finite
+    const double cap = p.softcap, t = fmin(0.25, pow(ldexp(1.0, -14) * 315.0 / 17.0 / cap, 1.0 / 7.0));
+    p.series_to = (float)fmin(t * cap / p.scale, 1e9);
+  }
   p.rot = rot;
   p.n_axes = rot ? n_axes : 1;
   p.cache_rows = cache_rows;

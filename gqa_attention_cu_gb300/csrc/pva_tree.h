@@ -61,6 +61,7 @@ struct TreeParams {
   int page, max_blocks, n_blocks;
   int window;
   float scale, softcap;
+  float series_to;         // largest |q . k| whose softcap the tensor-core kernels take by series
   int rot, n_axes, cache_rows;  // rotary positions checked by the front end
   int rows, bn;            // query rows and keys of a tile
   int item_places;         // an item's fixed cost, in key tiles

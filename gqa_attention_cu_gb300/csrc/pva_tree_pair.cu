@@ -78,7 +78,7 @@ __device__ __forceinline__ bool has_second(const TreeParams& p, const TreeSegmen
   return s.n * p.G - s.t * p.rows > kTcRows;
 }
 
-template <typename T, int D, int PARTS, bool CAP>
+template <typename T, int D, int PARTS, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     pva_tree_pair_kernel(TreeParams p, const __grid_constant__ CUtensorMap tmap_q,
                          const __grid_constant__ CUtensorMap tmap_k,
@@ -374,8 +374,10 @@ template <typename T, int D, int PARTS>
 cudaError_t launch_parts(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                          const CUtensorMap& tv, cudaStream_t s) {
   constexpr int smem = PairCfg<D, PARTS>::SMEM;
-  auto kern = p.softcap != 0.0f ? pva_tree_pair_kernel<T, D, PARTS, true>
-                                : pva_tree_pair_kernel<T, D, PARTS, false>;
+  const int cap = cap_form(p.softcap);
+  auto kern = cap == kNoCap ? pva_tree_pair_kernel<T, D, PARTS, kNoCap>
+              : cap == kCap ? pva_tree_pair_kernel<T, D, PARTS, kCap>
+                            : pva_tree_pair_kernel<T, D, PARTS, kLargeCap>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(p.pieces), dim3(kThreads), smem, s, p, tq, tk, tv);

@@ -91,7 +91,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= kHeadBytes, "barriers, segments and meeting places");
 
-template <typename T, int D, bool CAP>
+template <typename T, int D, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     pva_tree_tc_kernel(TreeParams p, const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_k,
@@ -484,7 +484,10 @@ template <typename T, int D>
 cudaError_t launch_d(const TreeParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, cudaStream_t s) {
   constexpr int smem = TreeCfg<D>::SMEM;
-  auto kern = p.softcap != 0.0f ? pva_tree_tc_kernel<T, D, true> : pva_tree_tc_kernel<T, D, false>;
+  const int cap = cap_form(p.softcap);
+  auto kern = cap == kNoCap ? pva_tree_tc_kernel<T, D, kNoCap>
+              : cap == kCap ? pva_tree_tc_kernel<T, D, kCap>
+                            : pva_tree_tc_kernel<T, D, kLargeCap>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(p.pieces), dim3(kThreads), smem, s, p, tq, tk, tv);

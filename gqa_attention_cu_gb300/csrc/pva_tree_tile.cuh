@@ -1,10 +1,14 @@
 // Softmax of one key tile of the tree attention's tensor-core kernels: key
 // masks, row extremes and exponentials.
 //
-// Softcap: tanh(t) of t = s * scale / softcap comes from the first three terms
-// of its series, t - t^3/3 + 2t^5/15 (error below the next term, 17/315 |t|^7 <
-// 3.3e-6 for |t| <= 1/4), on the FMA pipe, whenever every score of the warp's
-// tile is that small; otherwise from 1 - 2 / (exp(2t) + 1).
+// Softcap: tanh(t) of t = s * scale / softcap comes from the first three terms of
+// its series, t - t^3/3 + 2t^5/15, on the FMA pipe, whenever every score of the
+// warp's tile is small enough for that; otherwise element by element.  What is cut
+// off is below the next term, 17/315 |t|^7, and reaches the score times softcap;
+// tiles of one row may take different forms, so it counts in full.  The series is
+// taken up to |t| = 1/4 and only where softcap times that term stays below 2^-14, an
+// eighth of the half step that a weight is rounded by in f16 (softcap 30: |t| <=
+// 0.233; 1000: 0.142).
 #pragma once
 
 #include <math.h>
@@ -17,7 +21,25 @@ namespace tile {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the max grows > 2^8
-constexpr float kSeriesLimit = 0.25f;      // |t| up to which tanh is summed
+
+// Kernels without a softcap, with one, and with one above kCapOfExp, where 3e-7 of
+// it passes 2^-14.  Taking tanh_of for all of them: softcap 5 on 500-token chunks 281
+// against 387 us, on long contexts 772 against 1175; and its code beside the other
+// form in one kernel: drafts with a softcap of 50 83 against 85 us.
+constexpr int kNoCap = 0, kCap = 1, kLargeCap = 2;
+constexpr float kCapOfExp = 200.0f;
+inline int cap_form(float softcap) {
+  return softcap == 0.0f ? kNoCap : softcap <= kCapOfExp ? kCap : kLargeCap;
+}
+
+// tanh(t), off by at most 2^-19 of its size: up to 1/4 by four terms of the series
+// (the next, 62/2835 t^9, is 2^-21.5 of t there), else 1 - 2 / (exp(2t) + 1), whose
+// error of 3e-7 is more than that of smaller values.
+__device__ __forceinline__ float tanh_of(float t) {
+  const float w = t * t;
+  const float p = fmaf(w, fmaf(w, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f);
+  return fabsf(t) <= 0.25f ? fmaf(t * w, p, t) : tanh_via_exp2(t);
+}
 
 // Whether a row sees key c of 32, from its mask (one bit per key).
 template <bool MASKED>
@@ -62,7 +84,7 @@ __device__ __forceinline__ uint32_t row_mask(const TreeParams& p, const RowView&
 }
 
 // Largest of 32 scores, and with a softcap the smallest, for the series' range.
-template <bool MASKED, bool CAP>
+template <bool MASKED, int CAP>
 __device__ __forceinline__ void extremes(const uint32_t (&v)[32], uint32_t m, float& mx,
                                          float& mn) {
   const float ninf = __int_as_float(0xff800000), pinf = __int_as_float(0x7f800000);
@@ -83,10 +105,10 @@ __device__ __forceinline__ void extremes(const uint32_t (&v)[32], uint32_t m, fl
 }
 
 // 2^(x - m) of 32 scores, added to the two partial sums, and P as 16-bit pairs.
-// MODE 0: x = s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by its
-// series (1) or by exp (2).  P is rounded to the storage type for the
-// tensor-core product: at most half a step of each weight, as V's own elements
-// carry; the row sum adds the fp32 values.
+// MODE 0: x = s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by the
+// series' three terms (1), by exp (2) or by tanh_of (3).  P is rounded to the
+// storage type for the tensor-core product: at most half a step of each weight, as
+// V's own elements carry; the row sum adds the fp32 values.
 template <typename T, int MODE, bool MASKED>
 __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], uint32_t m, float s_mul,
                                              float cap_mul, float m_eff, float2 (&acc)[2],
@@ -110,9 +132,12 @@ __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], uint32_t m
       } else if (MODE == 1) {
         const float2 w = ffma2(s, s, z);
         x[k] = ffma2(s, ffma2(w, ffma2(w, c5, c3), c1), neg_m);
-      } else {
+      } else if (MODE == 2) {
         x[k].x = fmaf(cap_mul, tanh_via_exp2(s.x * s_mul), -m_eff);
         x[k].y = fmaf(cap_mul, tanh_via_exp2(s.y * s_mul), -m_eff);
+      } else {
+        x[k].x = fmaf(cap_mul, tanh_of(s.x * s_mul), -m_eff);
+        x[k].y = fmaf(cap_mul, tanh_of(s.y * s_mul), -m_eff);
       }
       x[k].x = seen<MASKED>(m, e) ? x[k].x : ninf;
       x[k].y = seen<MASKED>(m, e + 1) ? x[k].y : ninf;
@@ -202,7 +227,7 @@ __device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p)
 // a softcap at d = 64, 500-token chunks: 214 us, in loops 185 us).  Bound by
 // instructions, not by exponentials: a quarter of them by a polynomial on the FMA
 // pipe made those chunks 203 us.
-template <typename T, int N, bool CAP, typename Row>
+template <typename T, int N, int CAP, typename Row>
 __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowView& view, int past,
                                                 int k0, uint32_t t_s, float s_mul, float cap_mul,
                                                 Row& others, RowState& st, float& alpha) {
@@ -216,7 +241,10 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
     if (!others.exchange(mx, other)) return false;
     mx = fmaxf(mx, other);
     float mt = NEG_INF;
-    if (mx != NEG_INF) mt = CAP ? cap_mul * tanh_via_exp2(mx * s_mul) : mx * s_mul;
+    if (mx != NEG_INF) {
+      const float t = mx * s_mul;
+      mt = CAP == kLargeCap ? cap_mul * tanh_of(t) : CAP ? cap_mul * tanh_via_exp2(t) : t;
+    }
     alpha = 1.0f;
     if (mt > st.m + kRescaleThreshold) {
       alpha = ex2_approx(st.m - mt);  // 0 when m is -inf
@@ -225,12 +253,9 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
     m_eff = st.m == NEG_INF ? 0.0f : st.m;
     return true;
   };
-  // a softcap's series has to hold for the warp's own columns (and the scores'
-  // squares have to be finite)
+  // a softcap's series has to hold for the warp's own columns
   auto small_scores = [&]() {
-    const float far = fmaxf(fabsf(mx), fabsf(mn));
-    return CAP && __all_sync(0xffffffffu, mx == NEG_INF || (far * fabsf(s_mul) <= kSeriesLimit &&
-                                                            far < 1e9f));
+    return CAP && __all_sync(0xffffffffu, mx == NEG_INF || fmaxf(fabsf(mx), fabsf(mn)) <= p.series_to);
   };
   float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   bool series, done = false;
@@ -279,7 +304,7 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       else if (series)
         exponentials<T, 1, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       else
-        exponentials<T, 2, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
+        exponentials<T, CAP == kLargeCap ? 3 : 2, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       // over columns whose scores have been read in this pass
       tmem_st16(t_s + c / 2, pw);
     }

@@ -413,7 +413,8 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  * scale, softcap, dtype, stream : as pva_forward.
  *
  * Arithmetic: products of dtype (f16/bf16 on tensor cores), scores, softmax and
- * sums in f32.  The softmax weights that multiply V are rounded to dtype
+ * sums in f32; with a softcap a score of f16/bf16 is off by at most 2^-14 and 2^-19
+ * of its size (the tanh is taken by a series or by exp, tile by tile).  The softmax weights that multiply V are rounded to dtype
  * (f16/bf16); what rounding takes off the rotated queries is multiplied as well.
  * That costs up to a third of the rate of a long prompt chunk, which queries and
  * keys rotated before by pva_rope_axes (rotary_dim 0 here) do without.  f16

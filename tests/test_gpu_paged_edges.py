@@ -1,5 +1,7 @@
 """Edges of the paged-cache operators: what the entry points promise to refuse or
 to keep the same, at the sizes where it can go wrong."""
+import math
+
 import pytest
 import torch
 
@@ -100,3 +102,34 @@ def test_an_infinite_f16_query_is_no_large_one():
     assert torch.isnan(out[0, 3, 1]).all()
     out[0, 3, 1] = good[0, 3, 1]
     assert torch.equal(bits(out), bits(good))
+
+
+# ---- large softcaps --------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,softcap", [("f16", 200.0), ("f16", 1000.0), ("f16", 4000.0), ("bf16", 16000.0),
+                                           ("f16", 1e6), ("bf16", 1e9)])
+@pytest.mark.parametrize("T", [1, 140])
+@pytest.mark.parametrize("d", [64, 256])
+def test_softcapped_tiles_weigh_alike(T, dtype, softcap, d):
+    """Keys of one score, |t| = 0.248 of the softcap, over several tiles, of which some
+    hold a far lower score too: how a tile takes its tanh must not show between
+    them.  Queries and keys have one element, so a score is one exact product."""
+    td, past = DT[dtype], 400 if T > 1 else 255
+    a = 2.0 ** round(math.log2(softcap / 62))
+    b = 0.248 * softcap / a
+    s = make_tree(1, T, 1, 1, d, dtype, [past], 1, chain=True, capacity=past + T)
+    for name, x in (("q", a), ("k_new", b), ("k_cache", b)):
+        s[name] = torch.zeros_like(s[name])
+        s[name][..., 3] = x
+    s["k_cache"][:, :, [140, 200], 3] = -1.5 * b
+    s["v_new"], s["v_cache"] = -torch.ones_like(s["v_new"]), -torch.ones_like(s["v_cache"])
+    s["v_cache"][:, :, :128] = 1.0
+    out, _, _ = call(s, 1, 1, scale=1.0, softcap=softcap)
+    assert pva.pva_get_status() == 0
+    ref, mass, spread, count, _, _ = paged.tree_step(s["q"], s["k_new"], s["v_new"], s["k_cache"], s["v_cache"],
+                                                     s["past"], scale=1.0, softcap=softcap)
+    half_step = torch.finfo(td).eps / 2
+    # a score: the softcap's 2^-14, f32's roundings, one product; then a weight's half step, sums and the output's
+    err = 2.0 ** -14 + 2.0 ** -20 * (spread + 1) + 2.0 ** -23 * spread
+    part = torch.expm1(2 * err) + (count + 8) * 2.0 ** -23 + 1.01 * half_step
+    tol = mass * part[..., None] + 1.01 * half_step * ref.abs()
+    assert torch.isfinite(out).all() and ((out.double().cpu() - ref).abs() <= tol).all()
