@@ -478,9 +478,15 @@ extern "C" int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* p
     const long long one = (long long)n_blocks * kv_num_heads * page_size * head_size;
     if (layers > 1 && layer_stride < one)
       return fail(PVA_ERR_INVALID_ARG, "layer_stride is smaller than a layer's cache");
-    const uintptr_t old0 = (uintptr_t)past_lens, new0 = (uintptr_t)new_lens;
-    if (old0 < new0 + 4 * (uintptr_t)B && new0 < old0 + 4 * (uintptr_t)B)
-      return fail(PVA_ERR_INVALID_ARG, "new_lens must not overlap past_lens");
+    // one CTA of a sequence writes its new length while the others read these
+    auto on_new_lens = [&](const int32_t* a, long long n) {
+      const uintptr_t x = (uintptr_t)a, y = (uintptr_t)new_lens;
+      return a && x < y + 4 * (uintptr_t)B && y < x + 4 * (uintptr_t)n;
+    };
+    if (on_new_lens(past_lens, B) || on_new_lens(path_lens, B) ||
+        on_new_lens(path, (long long)B * path_width) ||
+        on_new_lens(block_table, (long long)B * max_blocks))
+      return fail(PVA_ERR_INVALID_ARG, "new_lens must not overlap an input");
     AcceptParams p{};
     p.k = static_cast<uint8_t*>(k_cache);
     p.v = static_cast<uint8_t*>(v_cache);

@@ -461,7 +461,7 @@ int pva_gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_ca
  * path    : device int32 [B, path_width]: the accepted nodes of the tree from
  *         the root on, so rising; path_lens: device int32 [B].
  * new_lens : device int32 [B]: past_lens[b] + path_lens[b].  Must not overlap
- *         past_lens.
+ *         past_lens, path, path_lens or block_table.
  * dtype   : any of the codes; rows are moved bit by bit.
  * A sequence is left as it is, with new_lens[b] = past_lens[b], when past_lens
  * or path_lens is out of range or the path does not rise, starts below 0 or
