@@ -352,8 +352,8 @@ __global__ void __launch_bounds__(kAcceptThreads) pva_accept_kernel(AcceptParams
   const int32_t* table = p.table ? p.table + (size_t)b * p.max_blocks : nullptr;
   // every CTA of a sequence checks it, and finds the same
   const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
-  bool bad_path = past < 0 || n < 0 || n > p.width, bad_block = false;
   const long long rows = (long long)p.max_blocks * p.page;
+  bool bad_path = past < 0 || past > rows || n < 0 || n > p.width, bad_block = false;
   auto place = [&](int row, bool& bad) {
     const int in = row / p.page;
     const int block = table ? table[in] : b;

@@ -50,6 +50,16 @@ def test_path_longer_than_its_table(page, bad_path):
     assert torch.equal(bits(kc), bits(k0)) and torch.equal(bits(vc), bits(v0))
 
 
+@pytest.mark.parametrize("past,status", [(64, 0), (65, "tree"), (2 ** 31 - 1, "tree"), (-1, "tree")])
+def test_lengths_outside_the_cache_with_an_empty_path(past, status):
+    """A cache of 64 rows that is full may keep nothing more; one that claims more is bad."""
+    kc = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16, device=DEV)
+    new = i32([-9])
+    pva.pva_kvcache_accept(kc, kc.clone(), i32([past]), i32([[0, 1]]), i32([0]), new)
+    assert pva.pva_get_status() == (pva.DEV_FLAGS[status] if status else 0)
+    assert new.tolist() == [past]
+
+
 # ---- softcapped steps -------------------------------------------------------------
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("B,T,lens,d,rot", [(2, 6, [5, 3], 128, 128), (1, 6, [5], 64, 0), (2, 70, [65, 33], 64, 64),
