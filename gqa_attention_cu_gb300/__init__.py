@@ -10,6 +10,7 @@ PyTorch provides device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -279,7 +280,7 @@ def _plain(t, name: str, dtype, shape, at: int):
     _need(False, "the tensors are on different devices")
 
 
-_sections = {}  # C arrays of the section lists met so far
+_sections = {}  # C arrays of the section lists met so far, by their numbers
 
 
 def _rotary(cos_cache, sin_cache, sections, at: int):
@@ -289,9 +290,13 @@ def _rotary(cos_cache, sin_cache, sections, at: int):
     _need(len(shape) == 2, "cos_cache must be [rows, rotary_dim / 2]")
     host = None
     if sections is not None:
-        key = tuple(sections)
+        try:
+            key = tuple(map(operator.index, sections))
+        except TypeError:
+            _need(False, "sections must be whole numbers")
         host = _sections.get(key)
         if host is None:
+            _need(all(-2**31 <= x < 2**31 for x in key), "a section does not fit in int32")
             host = _sections[key] = (ctypes.c_int32 * len(key))(*key)
     dtype = cos_cache.dtype
     return (_plain(cos_cache, "cos_cache", dtype, shape, at),

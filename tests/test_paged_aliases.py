@@ -34,3 +34,43 @@ def test_accept_takes_new_lens_beside_its_inputs(lib, new):
     """Refused for another reason, which is looked at later: a cache off its elements."""
     assert accept(lib, new=new, kc=17) == pva.PVA_ERR_INVALID_ARG
     assert "aligned" in pva.pva_last_error()
+
+
+# ---- the binding ------------------------------------------------------------------
+class Calls(list):
+    def __getattr__(self, name):
+        return lambda *args: self.append((name, args)) or 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    c = Calls()
+    monkeypatch.setattr(pva, "_lib", c)
+    return c
+
+
+def tree_arguments():
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    table = z(50, 16, dtype=torch.float32)
+    return dict(q=z(2, 3, 8, 64), k_new=z(2, 3, 2, 64), v_new=z(2, 3, 2, 64), k_cache=z(7, 2, 16, 64), v_cache=z(7, 2, 16, 64),
+                past_lens=z(2, dtype=torch.int32), out=z(2, 3, 8, 64), num_heads=8, kv_num_heads=2,
+                block_table=z(2, 5, dtype=torch.int32), cos_cache=table, sin_cache=table.clone(),
+                position_ids=z(3, 2, 3, dtype=torch.int64), sections=[8, 4, 4], stream=9)
+
+
+@pytest.mark.parametrize("sections", [(8, 4, 4), torch.tensor([8, 4, 4])])
+def test_section_lists_of_one_content_are_kept_once(calls, monkeypatch, sections):
+    """Their C arrays are kept by content; a tensor's elements are new objects every
+    time and must not make an entry a call."""
+    monkeypatch.setattr(pva, "_sections", {})
+    for _ in range(3):
+        pva.pva_gqa_tree(**{**tree_arguments(), "sections": sections})
+        assert list(calls[-1][1][25]) == [8, 4, 4]
+    assert len(pva._sections) == 1
+
+
+@pytest.mark.parametrize("sections", [(8.0, 4, 4), (8, 4, "4"), (2 ** 32 + 8, 4, 4)])
+def test_sections_that_are_no_int32_are_refused(calls, sections):
+    with pytest.raises(pva.PvaError):
+        pva.pva_gqa_tree(**{**tree_arguments(), "sections": sections})
+    assert not calls
