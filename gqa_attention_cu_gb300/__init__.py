@@ -445,6 +445,7 @@ def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: i
     n_axes, pc, ps, pos, host = 1, None, None, None, None
     if cos_cache is not None:
         if position_ids is not None:
+            _need(position_ids.dim() == 3, "position_ids must be [n_axes, B, tokens]")
             n_axes = position_ids.shape[0]
             pos = _plain(position_ids, "position_ids", torch.int64, (n_axes, B, T), at)
         elif sections is not None:

@@ -74,3 +74,10 @@ def test_sections_that_are_no_int32_are_refused(calls, sections):
     with pytest.raises(pva.PvaError):
         pva.pva_gqa_tree(**{**tree_arguments(), "sections": sections})
     assert not calls
+
+
+def test_position_ids_without_axes_are_refused(calls):
+    for bad in (torch.zeros((), dtype=torch.int64), torch.zeros(2, 3, dtype=torch.int64)):
+        with pytest.raises(pva.PvaError):
+            pva.pva_gqa_tree(**{**tree_arguments(), "position_ids": bad, "sections": None})
+    assert not calls
