@@ -262,7 +262,8 @@ def _device(first, *others) -> int:
 def _stream_on(stream, device: int) -> int:
     """The given stream, or the device's current one (as a number: making a
     stream object costs more than the rest of a small call's checks)."""
-    if stream is None and device >= 0:
+    if stream is None:
+        _need(device >= 0, "the tensors must be on a GPU")
         return torch._C._cuda_getCurrentRawStream(device)
     return _stream_ptr(stream)
 

@@ -81,3 +81,17 @@ def test_position_ids_without_axes_are_refused(calls):
         with pytest.raises(pva.PvaError):
             pva.pva_gqa_tree(**{**tree_arguments(), "position_ids": bad, "sections": None})
     assert not calls
+
+
+def test_host_tensors_on_the_current_stream_are_refused(calls):
+    """Without a stream of the caller's choice the work would run on the current GPU,
+    which none of the tensors is on."""
+    z = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype)  # noqa: E731
+    t = {**tree_arguments(), "stream": None}
+    x, cos, cache = z(3, 2, 64, dtype=torch.bfloat16), z(5, 32, dtype=torch.float32), z(4, 2, 16, 64, dtype=torch.bfloat16)
+    for call in (lambda: pva.pva_gqa_tree(**t), lambda: pva.pva_block_tables(z(2), z(2, 4), z(2), z(9), z(1), 16),
+                 lambda: pva.pva_rope_axes(x, None, cos, cos, z(1, 3, dtype=torch.int64), q_out=x.clone()),
+                 lambda: pva.pva_kvcache_accept(cache, cache.clone(), z(2), z(2, 3), z(2), z(2), block_table=z(2, 4))):
+        with pytest.raises(pva.PvaError, match="GPU"):
+            call()
+    assert not calls
