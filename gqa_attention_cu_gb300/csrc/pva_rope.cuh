@@ -8,6 +8,8 @@
 //   axes interleaved     axis k mod n where k < n * sections[k mod n], else 0.
 #pragma once
 
+#include <stddef.h>
+
 #include "pva_device.cuh"
 
 namespace pva {
@@ -166,10 +168,12 @@ __device__ __forceinline__ float table_at(const void* t, long long i, int is_f16
 }
 
 // cos and sin of a token's pairs, and whether a position is off the tables.
-struct RopeToken {
+struct alignas(16) RopeToken {
   float2 cs[128];
-  int bad[kMaxAxes];
+  int bad[kMaxAxes];  // read as one int4
 };
+static_assert(kMaxAxes == 4 && offsetof(RopeToken, bad) % 16 == 0 && sizeof(RopeToken) % 16 == 0,
+              "16-byte reads of `bad`");
 
 // Does the tokens first, first + stride, ... (tid: one of kRopeThreads threads,
 // which share `sh` and the named barrier `bar`).  VEC pairs of a head row per
