@@ -8,16 +8,17 @@
 // for cos^2 + sin^2 = 1, and its transpose, the gradient, is this one for any
 // table.
 //
-// Bound by memory: every q, k and v row is read once and written once (twice
-// where a key goes to k_out and the cache).  A CTA takes one token at a time: the
-// cos and sin of its pairs lie in shared memory, fetched while the token before
+// Every q, k and v row is read once and written once (twice where a key goes to
+// k_out and the cache), so memory is the floor; what bounds it now is how many loads
+// are under way (DRAM 57% busy, issue slots 56%).  A CTA takes one token at a time:
+// the cos and sin of its pairs lie in shared memory, fetched while the token before
 // is turned, and its threads walk over the token's head rows with them, so the
-// tables and the axis of each pair are looked up once a token and not once a
-// head; two rows' four loads of 16 bytes are in flight per thread.  16,001 tokens
-// with 32 + 8 + 8 head rows of 128 bf16 and the cache written as well: 84 us, 5.1
-// TB/s of 426 MB.  In the tree step (two parts of q, depths from the parents): 3000
-// tokens of 64 + 8 + 8 rows of 64 f16 in 24 us, 500 tokens of 32 + 8 + 8 rows of
-// 128 in 12 us with its launch.
+// tables and the axis of each pair are looked up once a token and not once a head;
+// two rows' four loads of 16 bytes are in flight per thread.  16,001 tokens with 32
+// + 8 + 8 head rows of 128 bf16 and the cache written as well: 85 us, 5.0 TB/s of
+// 426 MB (63 us at the copy rate).  In the tree step (two parts of q, depths from
+// the parents): 3000 tokens of 64 + 8 + 8 rows of 64 f16 in 24 us, 500 tokens of 32
+// + 8 + 8 rows of 128 in 12 us with its launch.
 #include <limits.h>
 
 #include "pva_rope.cuh"

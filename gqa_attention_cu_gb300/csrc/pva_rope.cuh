@@ -83,7 +83,7 @@ struct RopeStep {
 };
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeCtas = 8;  // CTAs an SM holds
+constexpr int kRopeCtas = 8;  // CTAs an SM holds (64 registers: the 16-byte fp32 form spills 4 bytes)
 constexpr int kRopeRows = 2;  // head rows a thread has in flight
 
 template <typename T>

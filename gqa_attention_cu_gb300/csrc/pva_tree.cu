@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kFrontThreads) pva_tree_small_front_kernel(Tre
 // Lanes hold the weights of 32 parts at a time and V channels of the row, V *
 // 32 at once.  So the work is that of the cut items, however many there are:
 // 15 MB of parts (500-token chunks of 6 sequences) in 12 us after the attention's
-// last CTA, those of 16 sequences of 32 nodes in 7 us.
+// last CTA, those of 16 sequences of 32 nodes in 7 us.  (32 registers,
+// 12 bytes spilled.)
 template <typename T, int V>
 __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
   struct alignas(4 * V) Part { float v[V]; };

@@ -224,9 +224,11 @@ __device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p)
 // us).  The others go over the columns twice, 32 at a time in a loop: reading
 // tensor memory again is about 18 cycles, while unrolled code for every kind of
 // mask and softcap spills and does not stay in the instruction cache (a window and
-// a softcap at d = 64, 500-token chunks: 214 us, in loops 185 us).  Bound by
-// instructions, not by exponentials: a quarter of them by a polynomial on the FMA
-// pipe made those chunks 203 us.
+// a softcap at d = 64, 500-token chunks: 214 us, in loops 185 us).  What bounds
+// those chunks is the chain scores, softmax, P V, next scores of each warpgroup:
+// issue slots are 40% full, the tensor pipe 31%, memory 6%.  Any instruction more
+// lengthens the chain: a quarter of the exponentials by a polynomial on the FMA pipe
+// made them 203 us.
 template <typename T, int N, int CAP, typename Row>
 __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowView& view, int past,
                                                 int k0, uint32_t t_s, float s_mul, float cap_mul,

@@ -389,6 +389,16 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  * a paged or fixed-capacity KV cache: append, rotary embedding and attention,
  * as pva_gqa_kvcache does for a chain of tokens.
  *
+ * On a fixed-capacity cache both take a chain that appends a key for every query.
+ * pva_gqa_tree splits long caches over the GPU for several tokens too and takes such
+ * steps unless they are one sequence's single token or prompt chunks of many
+ * sequences (us, 32 query and 8 kv heads of 128 bf16, rotated, pva_gqa_kvcache
+ * against pva_gqa_tree: 1 sequence on 2000 rows, 1 token 20 and 21, 8 tokens 40 and
+ * 23, on 30,000 rows 351 and 47; 64 on 4000 rows, 1 token 228 and 172, 8 tokens 230
+ * and 182; 500 tokens on 4000 rows, 1 sequence 80 and 66, 8 sequences 336 and 358).
+ * Steps without new keys, or with other numbers of queries and keys, are
+ * pva_gqa_kvcache's.
+ *
  * q     : [B, tokens, num_heads, head_size]
  * k_new, v_new : [B, tokens, kv_num_heads, head_size]
  * k_cache, v_cache, block_table : see "Paged caches" above; max_blocks is the
@@ -413,13 +423,14 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  * scale, softcap, dtype, stream : as pva_forward.
  *
  * Arithmetic: products of dtype (f16/bf16 on tensor cores), scores, softmax and
- * sums in f32; with a softcap a score of f16/bf16 is off by at most 2^-14 and 2^-19
- * of its size (the tanh is taken by a series or by exp, tile by tile).  The softmax weights that multiply V are rounded to dtype
- * (f16/bf16); what rounding takes off the rotated queries is multiplied as well.
- * That costs up to a third of the rate of a long prompt chunk, which queries and
- * keys rotated before by pva_rope_axes (rotary_dim 0 here) do without.  f16
- * queries may rotate past f16's range, to twice 65504 (the second part holds what
- * is above 65504, rounded to f16); the keys may not, which the cache holds as f16.
+ * sums in f32.  With a softcap a score of f16/bf16 is off by at most 2^-14 and 2^-19
+ * of its size: the tanh is taken by a series or by exp, tile by tile.  The softmax
+ * weights that multiply V are rounded to dtype (f16/bf16), the output once more;
+ * what rounding takes off the rotated queries is multiplied as well.  That costs up
+ * to a third of the rate of a long prompt chunk, which queries and keys rotated
+ * before by pva_rope_axes (rotary_dim 0 here) do without.  f16 queries may rotate
+ * past f16's range, to twice 65504 (the second part holds what is above 65504,
+ * rounded to f16); the keys may not, which the cache holds as f16.
  * Results do not depend on timing: parts of a split row are added in order.
  *
  * Limits: f16/bf16: head_size in {64, 96, 128, 192, 256}, 16-byte aligned
@@ -463,6 +474,9 @@ int pva_gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_ca
  * new_lens : device int32 [B]: past_lens[b] + path_lens[b].  Must not overlap
  *         past_lens, path, path_lens or block_table.
  * dtype   : any of the codes; rows are moved bit by bit.
+ * Host errors: null pointers, counts or sizes below 1, extents that do not fit in
+ * int32, layer_stride below a pool's size, a cache off its elements' alignment,
+ * new_lens over an input; B > 65535 is unsupported.
  * A sequence is left as it is, with new_lens[b] = past_lens[b], when past_lens
  * or path_lens is out of range or the path does not rise, starts below 0 or
  * passes the cache's end (PVA_DEV_TREE is latched), when a table entry that it
