@@ -789,7 +789,9 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   p.window = window > 0 ? window : 0;
   const float s = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
   p.scale = fabsf(s);
-  p.softcap = fabsf(softcap);
+  // From 1e34 on a softcap changes no score below 1e30, and its product with log2 e
+  // and its inverse could leave f32's range.
+  p.softcap = fminf(fabsf(softcap), 1e34f);
   if (p.softcap != 0.0f) {  // pva_tree_tile.cuh; and the products' squares have to be finite
     const double cap = p.softcap, t = fmin(0.25, pow(ldexp(1.0, -14) * 315.0 / 17.0 / cap, 1.0 / 7.0));
     p.series_to = (float)fmin(t * cap / p.scale, 1e9);

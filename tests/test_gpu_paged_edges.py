@@ -8,7 +8,7 @@ import torch
 import gqa_attention_cu_gb300 as pva
 from oracle import paged
 from paged_cases import DT, make_tree
-from test_gpu_tree import call
+from test_gpu_tree import call, parity
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -143,3 +143,10 @@ def test_softcapped_tiles_weigh_alike(T, dtype, softcap, d):
     part = torch.expm1(2 * err) + (count + 8) * 2.0 ** -23 + 1.01 * half_step
     tol = mass * part[..., None] + 1.01 * half_step * ref.abs()
     assert torch.isfinite(out).all() and ((out.double().cpu() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("softcap", [1e30, 1e37, 3e38])
+def test_softcaps_that_are_none(dtype, softcap):
+    parity(2, 9, 8, 2, 128, dtype, [200, 3], 17, rot=128, softcap=softcap)
+    parity(1, 70, 8, 2, 64, dtype, [300], 18, chain=True, softcap=-softcap)
