@@ -19,7 +19,7 @@ import torch
 from . import workloads  # noqa: F401  (seeded synthetic inputs)
 
 __all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache",
-           "pva_block_tables", "pva_rope_axes", "pva_gqa_tree", "pva_kvcache_accept",
+           "pva_block_tables", "pva_rope_axes", "pva_norm_rope", "pva_norm_rope_backward", "pva_gqa_tree", "pva_kvcache_accept",
            "pva_get_status", "pva_schedule", "pva_status_string", "pva_last_error",
            "pva_release", "pva_version", "pva_profile", "pva_kernel_times", "pva_selftest_wait",
            "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
@@ -81,6 +81,14 @@ def load_library(path: str | None = None):
         lib.pva_rope_axes.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i64, i64, i64, i64,
                                       i, i, i, i, vp, i, i, i, vp, i64, vp, vp, vp, i, i, i, vp]
         lib.pva_rope_axes.restype = i
+        lib.pva_norm_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i64, i64, i64,
+                                      i64, f, f, i, i, i, i, i, vp, i, i, vp, i64, vp, vp, vp, i, i,
+                                      i, vp]
+        lib.pva_norm_rope.restype = i
+        lib.pva_norm_rope_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i,
+                                               i, i, i64, i64, i64, i64, i64, i64, f, f, i, i, i, i, i,
+                                               vp, i, i, i, vp]
+        lib.pva_norm_rope_backward.restype = i
         lib.pva_gqa_tree.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i,
                                      i, i, i, i, i, i, i, i, vp, i, i, f, f, i, i, vp]
         lib.pva_gqa_tree.restype = i
@@ -355,6 +363,32 @@ def _token_rows(t, name: str, dtype, tokens: int, d: int, at: int):
     return t.data_ptr(), heads, max(s0, heads * d) if tokens <= 1 else s0
 
 
+def _positions(position_ids, sections, tokens: int, at: int):
+    """Address and axes of position_ids [n_axes, tokens]."""
+    _need(position_ids.dim() == 2, "position_ids must be [n_axes, tokens]")
+    n_axes = position_ids.shape[0]
+    _need(sections is None or len(sections) == n_axes, "sections needs one entry per axis")
+    return _plain(position_ids, "position_ids", torch.int64, (n_axes, tokens), at), n_axes
+
+
+def _cache_write(k, v, k_cache, v_cache, slot_map, dt, tokens: int, Hkv: int, d: int, at: int):
+    """(v, its stride, caches, slots, blocks, page) of a write of k and v to the cache."""
+    if k_cache is None:
+        _need(v is None and v_cache is None and slot_map is None,
+              "v, v_cache and slot_map come with k_cache")
+        return None, 0, None, None, None, 0, 0
+    _need(k is not None and v is not None and v_cache is not None and slot_map is not None,
+          "the cache write needs k, v, both caches and slot_map")
+    _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_heads, page, head_size]")
+    blocks, _, page, _ = k_cache.shape
+    kc = _plain(k_cache, "k_cache", dt, (blocks, Hkv, page, d), at)
+    vc = _plain(v_cache, "v_cache", dt, (blocks, Hkv, page, d), at)
+    slots = _plain(slot_map, "slot_map", torch.int64, (tokens,), at)
+    _need(v.shape == k.shape, "v must have k's shape")
+    pv, _, vs = _token_rows(v, "v", dt, tokens, d, at)
+    return pv, vs, kc, vc, slots, blocks, page
+
+
 def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=None, sections=None,
                   rotary_interleaved: bool = False, axes_interleaved: bool = False,
                   inverse: bool = False, v=None, k_cache=None, v_cache=None, slot_map=None,
@@ -372,8 +406,8 @@ def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=No
     dt = first.dtype
     at = _device(first, q_out, k, k_out, v, cos_cache, sin_cache, position_ids, k_cache, v_cache,
                  slot_map)
-    H = Hkv = qs = ks = qos = kos = vs = 0
-    pq = pk = pqo = pko = pv = None
+    H = Hkv = qs = ks = qos = kos = 0
+    pq = pk = pqo = pko = None
     if q is not None:
         pq, H, qs = _token_rows(q, "q", dt, tokens, d, at)
         _need(q_out is not None and q_out.shape == q.shape, "q_out must have q's shape")
@@ -387,26 +421,10 @@ def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=No
             pko, _, kos = _token_rows(k_out, "k_out", dt, tokens, d, at)
     else:
         _need(k_out is None, "k_out without k")
-    _need(position_ids.dim() == 2, "position_ids must be [n_axes, tokens]")
-    n_axes = position_ids.shape[0]
-    _need(sections is None or len(sections) == n_axes, "sections needs one entry per axis")
-    pos = _plain(position_ids, "position_ids", torch.int64, (n_axes, tokens), at)
+    pos, n_axes = _positions(position_ids, sections, tokens, at)
     pc, ps, rot, rows, code, host = _rotary(cos_cache, sin_cache, sections, at)
-    blocks = page = 0
-    kc = vc = slots = None
-    if k_cache is None:
-        _need(v is None and v_cache is None and slot_map is None,
-              "v, v_cache and slot_map come with k_cache")
-    else:
-        _need(k is not None and v is not None and v_cache is not None and slot_map is not None,
-              "the cache write needs k, v, both caches and slot_map")
-        _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_heads, page, head_size]")
-        blocks, _, page, _ = k_cache.shape
-        kc = _plain(k_cache, "k_cache", dt, (blocks, Hkv, page, d), at)
-        vc = _plain(v_cache, "v_cache", dt, (blocks, Hkv, page, d), at)
-        slots = _plain(slot_map, "slot_map", torch.int64, (tokens,), at)
-        _need(v.shape == k.shape, "v must have k's shape")
-        pv, _, vs = _token_rows(v, "v", dt, tokens, d, at)
+    pv, vs, kc, vc, slots, blocks, page = _cache_write(k, v, k_cache, v_cache, slot_map, dt, tokens, Hkv,
+                                                       d, at)
     if tokens == 0:
         return
     _check((_lib or load_library()).pva_rope_axes(
@@ -414,6 +432,111 @@ def pva_rope_axes(q, k, cos_cache, sin_cache, position_ids, q_out=None, k_out=No
         1 if rotary_interleaved else 0, n_axes, host, 1 if axes_interleaved else 0,
         1 if inverse else 0, code, pv, vs, kc, vc, slots, blocks, page, _type_code(first),
         _stream_on(stream, at)))
+
+
+def _norm_weights(q_weight, k_weight, dt, d: int, at: int):
+    """(q_weight, k_weight, type code) of the gains [head_size], both of one type."""
+    w = q_weight if q_weight is not None else k_weight
+    if w is None:
+        return None, None, 0
+    _need(w.dtype is dt or w.dtype is torch.float32, "the weights must be f32 or of the rows' type")
+    return (_plain(q_weight, "q_weight", w.dtype, (d,), at), _plain(k_weight, "k_weight", w.dtype, (d,), at),
+            _type_code(w))
+
+
+def pva_norm_rope(q, k, q_weight, k_weight, q_out=None, k_out=None, cos_cache=None, sin_cache=None,
+                  position_ids=None, eps: float = 1e-6, weight_offset: float = 0.0, sections=None,
+                  rotary_interleaved: bool = False, axes_interleaved: bool = False, v=None,
+                  k_cache=None, v_cache=None, slot_map=None, stream=None) -> None:
+    """Norm every head row of packed q [tokens, H, d] and/or k [tokens, Hkv, d] (token
+    strides allowed), times ``weight_offset`` + weight [d] (f32 or the rows' type;
+    None: gains of one), then rotate as pva_rope_axes does (no tables: norms only),
+    into q_out / k_out and, with v, caches and slot_map, the cache."""
+    first = q if q is not None else k
+    _need(first is not None, "q or k is needed")
+    _need(first.dim() == 3, "q and k must be [tokens, heads, head_size]")
+    tokens, _, d = first.shape
+    dt = first.dtype
+    at = _device(first, q_out, k, k_out, q_weight, k_weight, v, cos_cache, sin_cache, position_ids, k_cache,
+                 v_cache, slot_map)
+    H = Hkv = qs = ks = qos = kos = 0
+    pq = pk = pqo = pko = None
+    if q is not None:
+        pq, H, qs = _token_rows(q, "q", dt, tokens, d, at)
+        _need(q_out is not None and q_out.shape == q.shape, "q_out must have q's shape")
+        pqo, _, qos = _token_rows(q_out, "q_out", dt, tokens, d, at)
+    else:
+        _need(q_out is None, "q and q_out come together")
+    if k is not None:
+        pk, Hkv, ks = _token_rows(k, "k", dt, tokens, d, at)
+        if k_out is not None:
+            _need(k_out.shape == k.shape, "k_out must have k's shape")
+            pko, _, kos = _token_rows(k_out, "k_out", dt, tokens, d, at)
+    else:
+        _need(k_out is None, "k_out without k")
+    wq, wk, w_code = _norm_weights(q_weight, k_weight, dt, d, at)
+    turn = _norm_rotary(cos_cache, sin_cache, position_ids, sections, tokens, at)
+    pos, n_axes, pc, ps, rot, rows, code, host = turn
+    pv, vs, kc, vc, slots, blocks, page = _cache_write(k, v, k_cache, v_cache, slot_map, dt, tokens, Hkv,
+                                                       d, at)
+    if tokens == 0:
+        return
+    _check((_lib or load_library()).pva_norm_rope(
+        pq, pk, wq, wk, pqo, pko, pc, ps, pos, tokens, H, Hkv, d, qs, ks, qos, kos, float(eps),
+        float(weight_offset), w_code, rot, rows, 1 if rotary_interleaved else 0, n_axes, host,
+        1 if axes_interleaved else 0, code, pv, vs, kc, vc, slots, blocks, page, _type_code(first),
+        _stream_on(stream, at)))
+
+
+def _norm_rotary(cos_cache, sin_cache, position_ids, sections, tokens: int, at: int):
+    """(positions, axes, cos, sin, rotary_dim, rows, table type, sections), or no rotation."""
+    if cos_cache is None:
+        _need(sin_cache is None and position_ids is None and sections is None,
+              "positions and sections need the cos and sin tables")
+        return None, 1, None, None, 0, 0, 0, None
+    _need(position_ids is not None, "the rotation needs position_ids")
+    return _positions(position_ids, sections, tokens, at) + _rotary(cos_cache, sin_cache, sections, at)
+
+
+def pva_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, dq, dk, dq_weight=None,
+                           dk_weight=None, cos_cache=None, sin_cache=None, position_ids=None,
+                           eps: float = 1e-6, weight_offset: float = 0.0, sections=None,
+                           rotary_interleaved: bool = False, axes_interleaved: bool = False,
+                           stream=None) -> None:
+    """The gradient of pva_norm_rope: from the gradients dq_out, dk_out of its
+    outputs and the rows q, k that it read, dq and dk (which may take the place of
+    dq_out and dk_out), and f32 dq_weight, dk_weight [d] where they are given.  One
+    side may be None altogether."""
+    first = q if q is not None else k
+    _need(first is not None, "q or k is needed")
+    _need(first.dim() == 3, "q and k must be [tokens, heads, head_size]")
+    tokens, _, d = first.shape
+    dt = first.dtype
+    at = _device(first, dq_out, dk_out, k, dq, dk, q_weight, k_weight, dq_weight, dk_weight, cos_cache,
+                 sin_cache, position_ids)
+
+    def side(x, dy, dx, name):
+        if x is None:
+            _need(dy is None and dx is None, f"{name}, d{name}_out and d{name} come together")
+            return None, None, None, 0, 0, 0, 0
+        _need(dy is not None and dx is not None, f"{name}, d{name}_out and d{name} come together")
+        _need(dy.shape == x.shape and dx.shape == x.shape, f"the gradients of {name} must have its shape")
+        px, heads, sx = _token_rows(x, name, dt, tokens, d, at)
+        py, _, sy = _token_rows(dy, f"d{name}_out", dt, tokens, d, at)
+        pd, _, sd = _token_rows(dx, f"d{name}", dt, tokens, d, at)
+        return px, py, pd, heads, sx, sy, sd
+
+    pq, pqo, pdq, H, qs, qos, dqs = side(q, dq_out, dq, "q")
+    pk, pko, pdk, Hkv, ks, kos, dks = side(k, dk_out, dk, "k")
+    wq, wk, w_code = _norm_weights(q_weight, k_weight, dt, d, at)
+    gq = _plain(dq_weight, "dq_weight", torch.float32, (d,), at)
+    gk = _plain(dk_weight, "dk_weight", torch.float32, (d,), at)
+    pos, n_axes, pc, ps, rot, rows, code, host = _norm_rotary(cos_cache, sin_cache, position_ids, sections,
+                                                              tokens, at)
+    _check((_lib or load_library()).pva_norm_rope_backward(
+        pqo, pko, pq, pk, wq, wk, pdq, pdk, gq, gk, pc, ps, pos, tokens, H, Hkv, d, qos, kos, qs, ks, dqs,
+        dks, float(eps), float(weight_offset), w_code, rot, rows, 1 if rotary_interleaved else 0, n_axes,
+        host, 1 if axes_interleaved else 0, code, _type_code(first), _stream_on(stream, at)))
 
 
 def pva_gqa_tree(q, k_new, v_new, k_cache, v_cache, past_lens, out, num_heads: int,

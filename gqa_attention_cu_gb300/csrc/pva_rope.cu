@@ -128,18 +128,66 @@ int check_rope(const void* cos_cache, const void* sin_cache, int rot, int rows, 
   return PVA_OK;
 }
 
-}  // namespace host
-}  // namespace pva
-
-namespace {
-
-// Element ranges [base, base + extent) of strided [tokens, heads, d] tensors.
-bool apart(const void* a, long long na, const void* b, long long nb, size_t size) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x + (size_t)na * size <= y || y + (size_t)nb * size <= x;
+bool rows_meet(const RowRange& a, const RowRange& b, size_t size) {
+  if (!a.p || !b.p) return false;
+  const long long na = (a.tokens - 1) * a.stride + a.width, nb = (b.tokens - 1) * b.stride + b.width;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  if (x + (size_t)na * size <= y || y + (size_t)nb * size <= x) return false;
+  if (a.stride != b.stride) return true;
+  // rows of one projection interleave: two slices of it do not meet
+  const long long st = a.stride * (long long)size;
+  long long off = ((long long)((intptr_t)b.p - (intptr_t)a.p)) % st;
+  if (off < 0) off += st;
+  return !(off >= a.width * (long long)size && off + b.width * (long long)size <= st);
 }
 
-}  // namespace
+int check_token_rows(const RowsIn& r) {
+  if (r.dtype != PVA_F32 && r.dtype != PVA_F16 && r.dtype != PVA_BF16)
+    return fail(PVA_ERR_INVALID_ARG, "dtype must be 0 (f32), 1 (f16) or 2 (bf16)");
+  if (r.tokens < 0 || r.tokens > INT_MAX - 65536)
+    return fail(PVA_ERR_INVALID_ARG, "tokens must be >= 0 and fit in int32");
+  if (r.tokens == 0) return PVA_OK;
+  if (!r.q && !r.k) return fail(PVA_ERR_INVALID_ARG, "q or k is needed");
+  if ((r.q && r.H < 1) || (r.k && r.Hkv < 1))
+    return fail(PVA_ERR_INVALID_ARG, "head counts must be positive");
+  if (r.d < 2 || r.d > 256 || r.d % 2 != 0)
+    return fail(PVA_ERR_UNSUPPORTED, "head_size must be even, 2 to 256");
+  if ((r.q != nullptr) != (r.q_out != nullptr))
+    return fail(PVA_ERR_INVALID_ARG, "q and q_out come together");
+  const bool cache = r.k_cache || r.v_cache || r.slot_map || r.v;
+  if (cache && !(r.k && r.v && r.k_cache && r.v_cache && r.slot_map))
+    return fail(PVA_ERR_INVALID_ARG, "the cache write needs k, v, both caches and slot_map");
+  if (r.k && !r.k_out && !cache) return fail(PVA_ERR_INVALID_ARG, "k needs k_out or the cache");
+  if (r.k_out && !r.k) return fail(PVA_ERR_INVALID_ARG, "k_out without k");
+  if (cache && (r.n_blocks < 1 || r.page_size < 1))
+    return fail(PVA_ERR_INVALID_ARG, "need n_blocks >= 1 and page_size >= 1");
+  const long long qw = (long long)r.H * r.d, kw = (long long)r.Hkv * r.d;
+  if ((r.q && (r.q_stride < qw || r.q_out_stride < qw)) || (r.k && r.k_stride < kw) ||
+      (r.k_out && r.k_out_stride < kw) || (cache && r.v_stride < kw))
+    return fail(PVA_ERR_INVALID_ARG, "a token stride is smaller than the token's heads");
+  const size_t size = r.dtype == PVA_F32 ? 4 : 2;
+  const uintptr_t mis = (uintptr_t)r.q | (uintptr_t)r.k | (uintptr_t)r.v | (uintptr_t)r.q_out |
+                        (uintptr_t)r.k_out | (uintptr_t)r.k_cache | (uintptr_t)r.v_cache;
+  if (mis % size) return fail(PVA_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+  const RowRange in[3] = {{r.q, r.tokens, r.q_stride, qw},
+                          {r.k, r.tokens, r.k_stride, kw},
+                          {r.v, r.tokens, r.v_stride, kw}};
+  const RowRange out[2] = {{r.q_out, r.tokens, r.q_out_stride, qw},
+                           {r.k_out, r.tokens, r.k_out_stride, kw}};
+  for (int o = 0; o < 2; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      if (o == i && out[o].p == in[i].p && out[o].stride == in[i].stride) continue;
+      if (rows_meet(out[o], in[i], size))
+        return fail(PVA_ERR_INVALID_ARG, "an output overlaps an input it is not in place of");
+    }
+  }
+  if (rows_meet(out[0], out[1], size))
+    return fail(PVA_ERR_INVALID_ARG, "q_out and k_out overlap");
+  return PVA_OK;
+}
+
+}  // namespace host
+}  // namespace pva
 
 extern "C" int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out,
                              const void* cos_cache, const void* sin_cache,
@@ -152,68 +200,19 @@ extern "C" int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_
                              void* v_cache, const int64_t* slot_map, int n_blocks, int page_size,
                              int dtype, void* stream_) {
   return guarded([&]() -> int {
-    if (dtype != PVA_F32 && dtype != PVA_F16 && dtype != PVA_BF16)
-      return fail(PVA_ERR_INVALID_ARG, "dtype must be 0 (f32), 1 (f16) or 2 (bf16)");
-    if (tokens < 0 || tokens > INT_MAX - 65536)
-      return fail(PVA_ERR_INVALID_ARG, "tokens must be >= 0 and fit in int32");
-    if (tokens == 0) return PVA_OK;
-    if (!q && !k) return fail(PVA_ERR_INVALID_ARG, "q or k is needed");
-    if ((q && num_heads < 1) || (k && kv_num_heads < 1))
-      return fail(PVA_ERR_INVALID_ARG, "head counts must be positive");
-    if (head_size < 2 || head_size > 256 || head_size % 2 != 0)
-      return fail(PVA_ERR_UNSUPPORTED, "head_size must be even, 2 to 256");
-    if ((q != nullptr) != (q_out != nullptr))
-      return fail(PVA_ERR_INVALID_ARG, "q and q_out come together");
+    const RowsIn rows{q, k, v, q_out, k_out, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
+                      tokens, num_heads, kv_num_heads, head_size, k_cache, v_cache, slot_map, n_blocks,
+                      page_size, dtype};
+    int rc = check_token_rows(rows);
+    if (rc != PVA_OK || tokens == 0) return rc;
     if (!position_ids) return fail(PVA_ERR_INVALID_ARG, "null position_ids pointer");
-    const bool cache = k_cache || v_cache || slot_map || v;
-    if (cache && !(k && v && k_cache && v_cache && slot_map))
-      return fail(PVA_ERR_INVALID_ARG, "the cache write needs k, v, both caches and slot_map");
+    const bool cache = k_cache != nullptr;
     if (cache && inverse)
       return fail(PVA_ERR_INVALID_ARG, "the inverse rotation does not write the cache");
-    if (k && !k_out && !cache) return fail(PVA_ERR_INVALID_ARG, "k needs k_out or the cache");
-    if (k_out && !k) return fail(PVA_ERR_INVALID_ARG, "k_out without k");
-    if (cache && (n_blocks < 1 || page_size < 1))
-      return fail(PVA_ERR_INVALID_ARG, "need n_blocks >= 1 and page_size >= 1");
-    const long long qw = (long long)num_heads * head_size, kw = (long long)kv_num_heads * head_size;
-    if ((q && (q_stride < qw || q_out_stride < qw)) || (k && k_stride < kw) ||
-        (k_out && k_out_stride < kw) || (cache && v_stride < kw))
-      return fail(PVA_ERR_INVALID_ARG, "a token stride is smaller than the token's heads");
     RopeStep s{};
-    int rc = check_rope(cos_cache, sin_cache, rotary_dim, cache_rows, rotary_interleaved, n_axes,
+    rc = check_rope(cos_cache, sin_cache, rotary_dim, cache_rows, rotary_interleaved, n_axes,
                         sections, axes_interleaved, rotary_dtype, dtype, head_size, &s.rt);
     if (rc != PVA_OK) return rc;
-    const size_t size = dtype == PVA_F32 ? 4 : 2;
-    const uintptr_t mis = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out |
-                          (uintptr_t)k_out | (uintptr_t)k_cache | (uintptr_t)v_cache;
-    if (mis % size) return fail(PVA_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
-    // An output may be its own input (the same address and stride); otherwise
-    // no output may overlap an input or the other output.
-    struct Range { const void* p; long long n, stride; };
-    auto range = [&](const void* p, long long stride, long long w) {
-      return Range{p, p ? (tokens - 1) * stride + w : 0, stride};
-    };
-    const Range in[3] = {range(q, q_stride, qw), range(k, k_stride, kw),
-                         range(cache ? v : nullptr, v_stride, kw)};
-    const Range out[2] = {range(q_out, q_out_stride, qw), range(k_out, k_out_stride, kw)};
-    // rows of one projection interleave: two slices of it do not meet
-    auto meet = [&](const Range& a, long long wa, const Range& b, long long wb) {
-      if (!a.p || !b.p || apart(a.p, a.n, b.p, b.n, size)) return false;
-      if (a.stride != b.stride) return true;
-      const long long st = a.stride * (long long)size;
-      long long off = ((long long)((intptr_t)b.p - (intptr_t)a.p)) % st;
-      if (off < 0) off += st;
-      return !(off >= wa * (long long)size && off + wb * (long long)size <= st);
-    };
-    const long long w_in[3] = {qw, kw, kw}, w_out[2] = {qw, kw};
-    for (int o = 0; o < 2; ++o) {
-      for (int i = 0; i < 3; ++i) {
-        if (o == i && out[o].p == in[i].p && out[o].stride == in[i].stride) continue;
-        if (meet(out[o], w_out[o], in[i], w_in[i]))
-          return fail(PVA_ERR_INVALID_ARG, "an output overlaps an input it is not in place of");
-      }
-    }
-    if (meet(out[0], qw, out[1], kw))
-      return fail(PVA_ERR_INVALID_ARG, "q_out and k_out overlap");
     s.q = q;
     s.k = k;
     s.v = cache ? v : nullptr;

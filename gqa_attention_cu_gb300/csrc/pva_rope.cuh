@@ -427,6 +427,27 @@ namespace host {
 int check_rope(const void* cos_cache, const void* sin_cache, int rot, int rows, int interleaved,
                int n_axes, const int32_t* sections, int axes_interleaved, int rotary_dtype,
                int dtype, int d, RopeTable* t);
+
+// Rows of a [tokens, heads, d] tensor with a token stride: `width` elements of each.
+struct RowRange {
+  const void* p;
+  long long tokens, stride, width;
+};
+bool rows_meet(const RowRange& a, const RowRange& b, size_t size);
+
+// The token rows of a call and where they go, and what every such call checks: an
+// output may be its own input (the same address and stride); otherwise no output may
+// overlap an input or the other output.
+struct RowsIn {
+  const void *q, *k, *v;
+  const void *q_out, *k_out;
+  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int tokens, H, Hkv, d;
+  const void *k_cache, *v_cache;
+  const int64_t* slot_map;
+  int n_blocks, page_size, dtype;
+};
+int check_token_rows(const RowsIn& r);
 }  // namespace host
 
 cudaError_t launch_rope(const RopeStep& s, int dtype, bool tree, int num_sms, cudaStream_t st);

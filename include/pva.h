@@ -385,6 +385,66 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
                   int n_blocks, int page_size, int dtype, void* stream);
 
 /*
+ * pva_norm_rope -- norms of query and key heads, the rotary embedding of
+ * pva_rope_axes and the write of keys and values to a cache, in one pass over
+ * packed token rows.
+ *
+ * A head row x of q becomes R(x * r * w) with r = 1 / sqrt(mean(x^2) + eps) over
+ * its head_size dims, w = weight_offset + q_weight and R the rotation of
+ * pva_rope_axes; k likewise with k_weight.  Everything is f32, rounded once to
+ * dtype.
+ *
+ * q_weight, k_weight : device [head_size] of type weight_dtype (PVA_F32 or
+ *            dtype), the same for all heads; NULL: gains of one (weight_offset is
+ *            then not used).  weight_offset: 0, or 1 for weights that are kept as
+ *            their distance from one (any finite value).
+ * eps      : finite, >= 0.
+ * rotary_dim : as in pva_rope_axes, or 0: norms only (the tables, position_ids and
+ *            sections are then not used).
+ * Everything else, the errors too, as in pva_rope_axes: outputs may take the place
+ * of their own inputs, a token with a position off the tables or a slot off the
+ * cache is left out of all outputs and PVA_DEV_ROPE is latched.
+ */
+int pva_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                  void* q_out, void* k_out, const void* cos_cache, const void* sin_cache,
+                  const int64_t* position_ids, int tokens, int num_heads, int kv_num_heads,
+                  int head_size, int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                  int64_t k_out_stride, float eps, float weight_offset, int weight_dtype,
+                  int rotary_dim, int cache_rows, int rotary_interleaved, int n_axes,
+                  const int32_t* sections, int axes_interleaved, int rotary_dtype, const void* v,
+                  int64_t v_stride, void* k_cache, void* v_cache, const int64_t* slot_map,
+                  int n_blocks, int page_size, int dtype, void* stream);
+
+/*
+ * pva_norm_rope_backward -- the gradient of pva_norm_rope.  With g = R^T dq_out,
+ * n = x r and the names above:
+ *   dq = r (g w - n mean(g w n)),   dq_weight = sum over tokens and heads of g n,
+ * and k likewise; in f32, dq and dk rounded once, the weights' gradients f32.
+ *
+ * dq_out, dk_out : gradients of q_out and k_out, [tokens, heads, head_size] with a
+ *            token stride (dk_out is the gradient of the cached keys too).
+ * q, k     : the rows that pva_norm_rope read (not those it wrote).  A side's
+ *            tensors are all NULL, or none is.
+ * dq, dk   : may take the place of dq_out, dk_out (same address and stride).
+ * dq_weight, dk_weight : device f32 [head_size], written (not added to), or NULL;
+ *            refused where the weight is NULL.  The sums are taken in a fixed
+ *            order: equal calls give equal bits.
+ * A token with a position off the tables is left out of dq and dk and of the sums,
+ * and PVA_DEV_ROPE is latched.  tokens = 0: the weights' gradients are zeros.
+ * The sums use the workspace: its growth follows pva_forward's rules.
+ */
+int pva_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                           const void* q_weight, const void* k_weight, void* dq, void* dk,
+                           float* dq_weight, float* dk_weight, const void* cos_cache,
+                           const void* sin_cache, const int64_t* position_ids, int tokens,
+                           int num_heads, int kv_num_heads, int head_size, int64_t dq_out_stride,
+                           int64_t dk_out_stride, int64_t q_stride, int64_t k_stride,
+                           int64_t dq_stride, int64_t dk_stride, float eps, float weight_offset,
+                           int weight_dtype, int rotary_dim, int cache_rows,
+                           int rotary_interleaved, int n_axes, const int32_t* sections,
+                           int axes_interleaved, int rotary_dtype, int dtype, void* stream);
+
+/*
  * pva_gqa_tree -- one GroupQueryAttention step of a tree of drafted tokens over
  * a paged or fixed-capacity KV cache: append, rotary embedding and attention,
  * as pva_gqa_kvcache does for a chain of tokens.

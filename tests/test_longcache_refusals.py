@@ -1,0 +1,133 @@
+"""Malformed calls of the operators around a long cache are refused on the host, by
+the library (before any CUDA call, so without a GPU) and by the binding."""
+import ctypes
+
+import pytest
+import torch
+
+import gqa_attention_cu_gb300 as pva
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pva.build()
+    return pva.load_library()
+
+
+def ints(*x):
+    return (ctypes.c_int32 * len(x))(*x)
+
+
+def norm(lib, **kw):
+    a = dict(q=1 << 20, k=1 << 24, wq=16, wk=16, qo=1 << 28, ko=1 << 32, cos=16, sin=16, pos=16, N=10, H=4, Hkv=2, d=64, qs=256,
+             ks=128, qos=256, kos=128, eps=1e-6, offset=0.0, w_dtype=2, rot=64, rows=9, inter=0, axes=1, sec=None, ax_inter=0,
+             rot_dtype=0, v=None, vs=0, kc=None, vc=None, slots=None, blocks=0, page=0, dtype=2)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.pva_norm_rope(*a.values(), None)
+
+
+CACHE = dict(v=1 << 36, vs=128, kc=16, vc=16, slots=16, blocks=3, page=16)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None, k=None, qo=None, ko=None), -1), (dict(q=None), -1), (dict(qo=None), -1), (dict(ko=None), -1),
+    (dict(k=None), -1), (dict(pos=None), -1), (dict(N=-1), -1), (dict(H=0), -1), (dict(Hkv=0), -1), (dict(d=63), -2),
+    (dict(d=258), -2), (dict(qs=255), -1), (dict(ks=127), -1), (dict(qos=0), -1), (dict(kos=100), -1), (dict(rot=-2), -1),
+    (dict(rot=66), -1), (dict(rows=0), -1), (dict(cos=None), -1), (dict(dtype=3), -1), (dict(dtype=0, rot_dtype=1, w_dtype=0), -1),
+    (dict(qo=(1 << 20) + 512), -1), (dict(ko=1 << 28), -1), (dict(qo=1 << 20, qos=512), -1), (dict(ko=1 << 20), -1),
+    (dict(qo=(1 << 28) + 1), -1), (dict(eps=-1e-6), -1), (dict(eps=float("nan")), -1), (dict(offset=float("inf")), -1),
+    (dict(w_dtype=1), -1), (dict(w_dtype=7), -1), (dict(wq=17), -1), (dict(w_dtype=0, wk=18), -1), (dict(axes=2), -1),
+    (dict(axes=2, sec=ints(16, 17)), -1), (dict(axes=5), -1), (dict(CACHE, slots=None), -1), (dict(CACHE, v=None), -1),
+    (dict(CACHE, vs=127), -1), (dict(CACHE, page=0), -1), (dict(CACHE, blocks=0), -1), (dict(CACHE, kc=17), -1),
+    (dict(CACHE, v=1 << 28), -1)])
+def test_norm_refusals(lib, kw, code):
+    assert norm(lib, **kw) == code
+    assert pva.pva_last_error() != ""
+
+
+def test_no_tokens_is_a_call_of_nothing(lib):
+    assert norm(lib, N=0, q=None, k=None, qo=None, ko=None) == 0
+
+
+def grad(lib, **kw):
+    a = dict(dqo=1 << 20, dko=1 << 24, q=1 << 28, k=1 << 32, wq=16, wk=16, dq=1 << 36, dk=1 << 40, dwq=1 << 12, dwk=1 << 13,
+             cos=16, sin=16, pos=16, N=10, H=4, Hkv=2, d=64, dqos=256, dkos=128, qs=256, ks=128, dqs=256, dks=128, eps=1e-6,
+             offset=0.0, w_dtype=2, rot=64, rows=9, inter=0, axes=1, sec=None, ax_inter=0, rot_dtype=0, dtype=2)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.pva_norm_rope_backward(*a.values(), None)
+
+
+NO_Q = dict(q=None, dqo=None, dq=None)
+NO_K = dict(k=None, dko=None, dk=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(dqo=None), -1), (dict(dq=None), -1), (dict(dk=None), -1), (dict(NO_Q), -1), (dict(NO_K), -1),
+    ({**NO_Q, **NO_K, "dwq": None, "dwk": None}, -1), (dict(wq=None), -1), (dict(wk=None), -1), (dict(dwq=(1 << 12) + 2), -1),
+    (dict(dwk=(1 << 12) + 128), -1), (dict(N=-2), -1), (dict(H=0), -1), (dict(d=62, dtype=4), -1), (dict(d=1), -2),
+    (dict(qs=200), -1), (dict(ks=1), -1), (dict(dqs=3), -1), (dict(dkos=5), -1), (dict(pos=None), -1), (dict(rows=0), -1),
+    (dict(q=(1 << 28) + 1), -1), (dict(dq=1 << 28), -1), (dict(dk=1 << 28), -1), (dict(dq=1 << 24), -1),
+    (dict(dq=1 << 20, dqs=300), -1), (dict(dk=1 << 36), -1), (dict(eps=-1.0), -1), (dict(offset=float("nan")), -1),
+    (dict(w_dtype=1), -1), (dict(N=0, d=3), -2)])
+def test_norm_gradient_refusals(lib, kw, code):
+    assert grad(lib, **kw) == code
+    assert pva.pva_last_error() != ""
+
+
+# ---- the binding ------------------------------------------------------------------
+class Calls(list):
+    def __getattr__(self, name):
+        return lambda *args: self.append((name, args)) or 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    c = Calls()
+    monkeypatch.setattr(pva, "_lib", c)
+    return c
+
+
+def z(*s, dtype=torch.bfloat16):
+    return torch.zeros(s, dtype=dtype)
+
+
+def norm_arguments():
+    t = z(50, 16, dtype=torch.float32)
+    return dict(q=z(3, 4, 64), k=z(3, 2, 64), q_weight=z(64), k_weight=z(64), q_out=z(3, 4, 64), k_out=z(3, 2, 64), cos_cache=t,
+                sin_cache=t.clone(), position_ids=z(3, 3, dtype=torch.int64), sections=[8, 4, 4], stream=9)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(q_out=None), dict(q_out=z(3, 4, 32)), dict(k_out=z(2, 2, 64)), dict(q=z(3, 4, 64).transpose(1, 2)),
+    dict(k=z(3, 2, 64, dtype=torch.float16)), dict(q_weight=z(32)), dict(q_weight=z(64, dtype=torch.float16)),
+    dict(k_weight=z(64, dtype=torch.float32)), dict(q_weight=z(128)[::2]), dict(sin_cache=None), dict(cos_cache=None),
+    dict(position_ids=None), dict(position_ids=z(3, dtype=torch.int64)), dict(position_ids=z(3, 3, dtype=torch.int32)),
+    dict(sections=[8, 8]), dict(sections=[8.0, 4, 4]), dict(v=z(3, 2, 64)), dict(slot_map=z(3, dtype=torch.int64)),
+    dict(q=z(12, 64)), dict(stream=None)])
+def test_binding_refuses_norm_arguments(calls, kw):
+    with pytest.raises(pva.PvaError):
+        pva.pva_norm_rope(**{**norm_arguments(), **kw})
+    assert not calls
+    pva.pva_norm_rope(**norm_arguments())
+    assert [c[0] for c in calls] == ["pva_norm_rope"]
+
+
+def grad_arguments():
+    a = norm_arguments()
+    del a["q_out"], a["k_out"]
+    return dict(a, dq_out=z(3, 4, 64), dk_out=z(3, 2, 64), dq=z(3, 4, 64), dk=z(3, 2, 64), dq_weight=z(64, dtype=torch.float32),
+                dk_weight=z(64, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(dq=None), dict(dk_out=None), dict(dq=z(3, 4, 32)), dict(dk_out=z(3, 1, 64)),
+    dict(dq=z(3, 4, 64, dtype=torch.float32)), dict(dq_weight=z(64)), dict(dk_weight=z(63, dtype=torch.float32)),
+    dict(position_ids=None), dict(q=z(3, 4, 64).transpose(1, 2)), dict(q=None, dq=None, dq_out=None, k=None, dk=None, dk_out=None)])
+def test_binding_refuses_gradient_arguments(calls, kw):
+    with pytest.raises(pva.PvaError):
+        pva.pva_norm_rope_backward(**{**grad_arguments(), **kw})
+    assert not calls
+    pva.pva_norm_rope_backward(**grad_arguments())
+    assert [c[0] for c in calls] == ["pva_norm_rope_backward"]
