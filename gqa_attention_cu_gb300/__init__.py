@@ -19,7 +19,7 @@ import torch
 from . import workloads  # noqa: F401  (seeded synthetic inputs)
 
 __all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache",
-           "pva_block_tables", "pva_rope_axes", "pva_norm_rope", "pva_norm_rope_backward", "pva_gqa_tree", "pva_kvcache_accept",
+           "pva_block_tables", "pva_rope_axes", "pva_norm_rope", "pva_norm_rope_backward", "pva_gqa_tree", "pva_kvcache_accept", "pva_kvcache_evict",
            "pva_get_status", "pva_schedule", "pva_status_string", "pva_last_error",
            "pva_release", "pva_version", "pva_profile", "pva_kernel_times", "pva_selftest_wait",
            "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
@@ -95,6 +95,9 @@ def load_library(path: str | None = None):
         lib.pva_kvcache_accept.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i64, i, i, i, i, i,
                                            i, vp]
         lib.pva_kvcache_accept.restype = i
+        lib.pva_kvcache_evict.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i64, i,
+                                          i, i, i64, i, i, i, i, i, i, i, i, i, vp]
+        lib.pva_kvcache_evict.restype = i
         lib.pva_get_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.pva_get_status.restype = i
         lib.pva_schedule.argtypes = [vp, vp, i, i, i, i, i, i, i,
@@ -615,6 +618,58 @@ def pva_kvcache_accept(k_cache, v_cache, past_lens, path, path_lens, new_lens, b
         _plain(block_table, "block_table", i32, (B, table_width), at),
         _plain(new_lens, "new_lens", i32, (B,), at), B, width, layers, blocks * Hkv * page * d,
         blocks, Hkv, page, d, table_width, _type_code(k_cache), _stream_on(stream, at)))
+
+
+def pva_kvcache_evict(k_cache, v_cache, weights, lens, keep, new_lens, first: int = 0, last: int = 0,
+                      block_table=None, k_out=None, v_out=None, out_table=None, weights_out=None,
+                      kept=None, stream=None) -> None:
+    """Cut every sequence down to its ``keep`` int32 [B] heaviest cache rows (the
+    ``first`` and ``last`` ones stay in any case), by f32 weights [layers,] [B, Hkv,
+    width].  Caches [layers,] [n_blocks, Hkv, page, d]; in place, or to k_out, v_out
+    and/or the blocks of out_table.  Written: new_lens int32 [B], the rows' weights
+    (weights_out, may be weights) and their old numbers (kept, int32)."""
+    _need(k_cache.dim() in (4, 5), "k_cache must be [layers,] [n_blocks, heads, page, head_size]")
+    shape = k_cache.shape
+    layers = shape[0] if len(shape) == 5 else 1
+    blocks, Hkv, page, d = shape[-4:]
+    _need(lens.dim() == 1, "lens must be [B]")
+    B = lens.shape[0]
+    _need(weights.dim() == len(shape) - 1 or (layers == 1 and weights.dim() in (3, 4)),
+          "weights must be [layers,] [B, kv_heads, width]")
+    width = weights.shape[-1]
+    lead = weights.shape[:-3]
+    _need(not lead or lead[0] == layers, "weights must be [layers,] [B, kv_heads, width]")
+    rows = (*lead, B, Hkv, width)
+    i32, f32, dt = torch.int32, torch.float32, k_cache.dtype
+    at = _device(k_cache, v_cache, weights, lens, keep, new_lens, block_table, k_out, v_out, out_table,
+                 weights_out, kept)
+
+    def table(t, name):
+        if t is None:
+            return None, 0
+        _need(t.dim() == 2, f"{name} must be [B, max_blocks]")
+        return _plain(t, name, i32, (B, t.shape[1]), at), t.shape[1]
+
+    ptable, table_width = table(block_table, "block_table")
+    pout, out_width = table(out_table, "out_table")
+    _need((k_out is None) == (v_out is None), "k_out and v_out come together")
+    out_blocks = out_page = 0
+    po = pvo = None
+    if k_out is not None:
+        out_shape = k_out.shape
+        _need(len(out_shape) == len(shape) and out_shape[-1] == d and out_shape[-3] == Hkv
+              and (len(shape) == 4 or out_shape[0] == layers), "k_out must be a pool like k_cache")
+        out_blocks, out_page = out_shape[-4], out_shape[-2]
+        po = _plain(k_out, "k_out", dt, out_shape, at)
+        pvo = _plain(v_out, "v_out", dt, out_shape, at)
+    _check((_lib or load_library()).pva_kvcache_evict(
+        _plain(k_cache, "k_cache", dt, shape, at), _plain(v_cache, "v_cache", dt, shape, at),
+        _plain(weights, "weights", f32, rows, at), _plain(lens, "lens", i32, (B,), at),
+        _plain(keep, "keep", i32, (B,), at), _plain(new_lens, "new_lens", i32, (B,), at), ptable, po, pvo,
+        pout, _plain(weights_out, "weights_out", f32, rows, at), _plain(kept, "kept", i32, rows, at), B,
+        layers, blocks * Hkv * page * d, blocks, page, table_width, out_blocks * Hkv * out_page * d,
+        out_blocks, out_page, out_width, Hkv, d, width, int(first), int(last), _type_code(k_cache),
+        _stream_on(stream, at)))
 
 
 def pva_forward_noalloc(q, k, v, cu_seqlens_q, cu_seqlens_kv, out, B: int, num_heads: int,

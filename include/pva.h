@@ -50,15 +50,17 @@ typedef enum { PVA_F32 = 0, PVA_F16 = 1, PVA_BF16 = 2 } pva_dtype;
 
 /* Device-side status bits, latched by the on-device scheduler and read with
  * pva_get_status.  When any bit is set the call wrote nothing to `out` (but see
- * pva_rope_axes and pva_kvcache_accept, which leave out single tokens and
- * sequences). */
+ * pva_rope_axes, pva_norm_rope, pva_kvcache_accept and pva_kvcache_evict, which
+ * leave out single tokens and sequences). */
 #define PVA_DEV_CU_Q_START 0x1u   /* cu_seqlens_q[0] != 0 */
 #define PVA_DEV_CU_KV_START 0x2u  /* cu_seqlens_kv[0] != 0 */
 #define PVA_DEV_CU_Q_ORDER 0x4u   /* cu_seqlens_q decreases somewhere */
 #define PVA_DEV_CU_KV_ORDER 0x8u  /* cu_seqlens_kv decreases somewhere */
 #define PVA_DEV_TOO_MANY 0x10u    /* work count does not fit the 32-bit work index */
 #define PVA_DEV_NULL_TENSOR 0x20u /* a NULL q/k/v/out with a nonzero token extent */
-#define PVA_DEV_KV_LEN 0x40u      /* pva_forward_padded: a nonpad length outside [0, kv_seq] */
+#define PVA_DEV_KV_LEN 0x40u      /* pva_forward_padded: a nonpad length outside [0, kv_seq];
+                                     pva_gqa_prefix, pva_kvcache_weights, pva_kvcache_evict: a
+                                     length outside the cache */
 #define PVA_DEV_KV_CACHE 0x80u    /* pva_gqa_kvcache: a step outside the cache's bounds, or one
                                      after such a step (see there) */
 #define PVA_DEV_WAIT_TIMEOUT 0x100u /* a pipeline wait in a kernel gave up (never expected) */
@@ -548,6 +550,50 @@ int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* past_lens,
                        const int32_t* block_table, int32_t* new_lens, int B, int path_width,
                        int layers, int64_t layer_stride, int n_blocks, int kv_num_heads,
                        int page_size, int head_size, int max_blocks, int dtype, void* stream);
+
+/*
+ * pva_kvcache_evict -- cuts caches down to the rows that attention has weighed
+ * most.  Of the lens[b] rows of sequence b, new_lens[b] = min(lens[b], keep[b]) stay
+ * on every (layer, kv head): the first `first` ones, then the last `last` ones, as far
+ * as keep[b] goes, then those of the others with the largest weights (of equal ones
+ * the lower row; a NaN is lighter than every number).  They keep their order and
+ * close up to rows 0 .. new_lens[b] - 1, so that rows may be appended behind them.
+ * Keys keep the rotation of their old position: later queries need position_ids of
+ * their own (pva_gqa_tree) or be rotated before.
+ *
+ * k_cache, v_cache, block_table, page_size, max_blocks, layers, layer_stride : as
+ *         pva_kvcache_accept.
+ * weights : device f32 [layers, B, kv_num_heads, width], row by row, as
+ *         pva_kvcache_weights gives them; width >= lens[b].
+ * lens, keep : device int32 [B]; new_lens : device int32 [B], may be lens or keep.
+ * k_out, v_out, out_table : NULL: the caches are closed up in place, and no block of
+ *         a sequence may be another's too.  Otherwise the rows are copied: to k_out,
+ *         v_out, pools like the caches with sizes of their own (out_blocks,
+ *         out_page_size, out_max_blocks, out_layer_stride), or, with out_table alone,
+ *         to other blocks of the same pools.  Nothing that is written may be among
+ *         what is read.
+ * weights_out : f32 like weights, or NULL; may be weights itself.  Entry i < new_lens
+ *         is the weight of the row that went to i, the others up to lens[b] are zero.
+ * kept    : int32 like weights, or NULL: entry i < new_lens is the row that went to i.
+ * Entries behind these, and cache rows at and behind new_lens[b] that no kept row
+ * came to, are left as they were.
+ * dtype   : any of the codes; rows are moved bit by bit, head_size is any.
+ * Host errors: null pointers, counts or sizes below 1, extents that do not fit in
+ * int32, layer strides below a pool's size, tensors off their elements' alignment,
+ * outputs over inputs; layers * B * kv_num_heads > 65535 is unsupported.
+ * A sequence is left as it is (in place: new_lens[b] = lens[b]; copied: 0, and
+ * nothing is copied) when lens or keep is negative, lens is larger than the cache or
+ * width, new_lens larger than the output (PVA_DEV_KV_LEN is latched), when a table
+ * entry that it needs is outside its pool (PVA_DEV_BLOCKS), or when PVA_DEV_KV_CACHE
+ * is latched on the stream: the rejected step before has not written its rows.
+ */
+int pva_kvcache_evict(void* k_cache, void* v_cache, const float* weights, const int32_t* lens,
+                      const int32_t* keep, int32_t* new_lens, const int32_t* block_table,
+                      void* k_out, void* v_out, const int32_t* out_table, float* weights_out,
+                      int32_t* kept, int B, int layers, int64_t layer_stride, int n_blocks,
+                      int page_size, int max_blocks, int64_t out_layer_stride, int out_blocks,
+                      int out_page_size, int out_max_blocks, int kv_num_heads, int head_size,
+                      int width, int first, int last, int dtype, void* stream);
 
 /*
  * pva_get_status -- synchronises `stream`, then reads and clears the device

@@ -76,6 +76,33 @@ def test_norm_gradient_refusals(lib, kw, code):
     assert pva.pva_last_error() != ""
 
 
+def evict(lib, **kw):
+    a = dict(k=1 << 20, v=1 << 24, w=1 << 28, lens=1 << 12, keep=1 << 13, new=1 << 14, table=1 << 15, ko=None, vo=None, ot=None,
+             wo=1 << 32, kept=1 << 36, B=3, layers=1, stride=0, blocks=9, page=16, tw=4, ostride=0, oblocks=0, opage=0, otw=0,
+             Hkv=2, d=64, width=60, first=0, last=0, dtype=2)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.pva_kvcache_evict(*a.values(), None)
+
+
+OUT = dict(ko=1 << 40, vo=1 << 44, oblocks=3, opage=40)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), -1), (dict(v=None), -1), (dict(w=None), -1), (dict(lens=None), -1), (dict(keep=None), -1), (dict(new=None), -1),
+    (dict(B=0), -1), (dict(layers=0), -1), (dict(blocks=0), -1), (dict(Hkv=0), -1), (dict(page=0), -1), (dict(d=0), -1),
+    (dict(width=0), -1), (dict(first=-1), -1), (dict(last=-1), -1), (dict(dtype=3), -1), (dict(tw=0), -1), (dict(table=None), -1),
+    (dict(layers=1 << 14, stride=1 << 20, Hkv=2), -2), (dict(tw=1 << 28), -1), (dict(blocks=1 << 30, Hkv=4), -1),
+    (dict(layers=2, stride=100), -1), (dict(k=(1 << 20) + 1), -1), (dict(w=(1 << 28) + 2), -1), (dict(wo=(1 << 32) + 1), -1),
+    (dict(wo=(1 << 28) + 4), -1), (dict(kept=1 << 28), -1), (dict(kept=1 << 32), -1), (dict(new=(1 << 15) + 4), -1),
+    (dict(kept=1 << 13), -1), (dict(ko=16), -1), (dict(OUT, oblocks=2), -1), (dict(OUT, opage=0), -1),
+    (dict(OUT, ot=1 << 16, otw=0), -1), (dict(OUT, ot=1 << 14, otw=2), -1), (dict(OUT, layers=2, stride=1 << 20, ostride=5), -1),
+    (dict(OUT, ko=(1 << 40) + 1), -1), (dict(ot=1 << 16), -1)])
+def test_evict_refusals(lib, kw, code):
+    assert evict(lib, **kw) == code
+    assert pva.pva_last_error() != ""
+
+
 # ---- the binding ------------------------------------------------------------------
 class Calls(list):
     def __getattr__(self, name):
@@ -131,3 +158,26 @@ def test_binding_refuses_gradient_arguments(calls, kw):
     assert not calls
     pva.pva_norm_rope_backward(**grad_arguments())
     assert [c[0] for c in calls] == ["pva_norm_rope_backward"]
+
+
+def evict_arguments():
+    i32, f32 = torch.int32, torch.float32
+    return dict(k_cache=z(9, 2, 16, 64), v_cache=z(9, 2, 16, 64), weights=z(3, 2, 60, dtype=f32), lens=z(3, dtype=i32),
+                keep=z(3, dtype=i32), new_lens=z(3, dtype=i32), block_table=z(3, 4, dtype=i32), kept=z(3, 2, 60, dtype=i32),
+                weights_out=z(3, 2, 60, dtype=f32), stream=9)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k_cache=z(9, 2, 16)), dict(v_cache=z(9, 2, 16, 32)), dict(weights=z(3, 2, 60)), dict(weights=z(4, 2, 60, dtype=torch.float32)),
+    dict(weights=z(2, 3, 2, 60, dtype=torch.float32)), dict(weights=z(60, dtype=torch.float32)), dict(lens=z(3)),
+    dict(lens=z(3, 1, dtype=torch.int32)), dict(keep=z(2, dtype=torch.int32)), dict(new_lens=z(3, dtype=torch.int64)),
+    dict(block_table=z(3, dtype=torch.int32)), dict(block_table=z(2, 4, dtype=torch.int32)), dict(k_out=z(3, 2, 40, 64)),
+    dict(k_out=z(3, 2, 40, 32), v_out=z(3, 2, 40, 32)), dict(k_out=z(1, 3, 2, 40, 64), v_out=z(1, 3, 2, 40, 64)),
+    dict(k_out=z(3, 1, 40, 64), v_out=z(3, 1, 40, 64)), dict(out_table=z(4, 4, dtype=torch.int32)),
+    dict(weights_out=z(3, 2, 59, dtype=torch.float32)), dict(kept=z(3, 2, 60, dtype=torch.int64)), dict(stream=None)])
+def test_binding_refuses_evict_arguments(calls, kw):
+    with pytest.raises(pva.PvaError):
+        pva.pva_kvcache_evict(**{**evict_arguments(), **kw})
+    assert not calls
+    pva.pva_kvcache_evict(**evict_arguments())
+    assert [c[0] for c in calls] == ["pva_kvcache_evict"]
