@@ -19,7 +19,7 @@ import torch
 from . import workloads  # noqa: F401  (seeded synthetic inputs)
 
 __all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache",
-           "pva_block_tables", "pva_rope_axes", "pva_norm_rope", "pva_norm_rope_backward", "pva_gqa_tree", "pva_kvcache_accept", "pva_kvcache_evict",
+           "pva_block_tables", "pva_rope_axes", "pva_norm_rope", "pva_norm_rope_backward", "pva_gqa_tree", "pva_kvcache_accept", "pva_kvcache_weights", "pva_kvcache_evict",
            "pva_get_status", "pva_schedule", "pva_status_string", "pva_last_error",
            "pva_release", "pva_version", "pva_profile", "pva_kernel_times", "pva_selftest_wait",
            "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
@@ -95,6 +95,9 @@ def load_library(path: str | None = None):
         lib.pva_kvcache_accept.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i64, i, i, i, i, i,
                                            i, vp]
         lib.pva_kvcache_accept.restype = i
+        lib.pva_kvcache_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f,
+                                            f, f, i, vp]
+        lib.pva_kvcache_weights.restype = i
         lib.pva_kvcache_evict.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i64, i,
                                           i, i, i64, i, i, i, i, i, i, i, i, i, vp]
         lib.pva_kvcache_evict.restype = i
@@ -618,6 +621,36 @@ def pva_kvcache_accept(k_cache, v_cache, past_lens, path, path_lens, new_lens, b
         _plain(block_table, "block_table", i32, (B, table_width), at),
         _plain(new_lens, "new_lens", i32, (B,), at), B, width, layers, blocks * Hkv * page * d,
         blocks, Hkv, page, d, table_width, _type_code(k_cache), _stream_on(stream, at)))
+
+
+def pva_kvcache_weights(q, k_cache, lens, weights, num_heads: int, previous=None, decay: float = 1.0,
+                        lse=None, q_lens=None, block_table=None, scale: float = 0.0,
+                        softcap: float = 0.0, stream=None) -> None:
+    """Add up the attention that queries [B, T, H, d] give to each cache row: weights
+    f32 [B, Hkv, width] = decay * previous (may be weights; None: nothing) + the sum of
+    exp(score - lse) over the tokens and heads of each group, row j < lens int32 [B].
+    The tokens are the last rows (q_lens int32 [B] of them).  lse f32 [B, T, H] as
+    pva_gqa_prefix gives it; None: over the sequence's own rows."""
+    _need(q.dim() == 4, "q must be [B, tokens, num_heads, head_size]")
+    B, T, _, d = q.shape
+    H = int(num_heads)
+    dt, i32, f32 = q.dtype, torch.int32, torch.float32
+    _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_num_heads, page, head_size]")
+    blocks, Hkv, page, _ = k_cache.shape
+    _need(weights.dim() == 3, "weights must be [B, kv_num_heads, width]")
+    rows = (B, Hkv, weights.shape[2])
+    at = _device(q, k_cache, lens, weights, previous, lse, q_lens, block_table)
+    table_width = 0
+    if block_table is not None:
+        _need(block_table.dim() == 2, "block_table must be [B, max_blocks]")
+        table_width = block_table.shape[1]
+    _check((_lib or load_library()).pva_kvcache_weights(
+        _plain(q, "q", dt, (B, T, H, d), at), _plain(k_cache, "k_cache", dt, (blocks, Hkv, page, d), at),
+        _plain(lens, "lens", i32, (B,), at), _plain(q_lens, "q_lens", i32, (B,), at),
+        _plain(block_table, "block_table", i32, (B, table_width), at),
+        _plain(previous, "previous", f32, rows, at), _plain(lse, "lse", f32, (B, T, H), at),
+        _plain(weights, "weights", f32, rows, at), B, T, blocks, page, table_width, H, Hkv, d, rows[2],
+        float(decay), float(scale), float(softcap), _type_code(q), _stream_on(stream, at)))
 
 
 def pva_kvcache_evict(k_cache, v_cache, weights, lens, keep, new_lens, first: int = 0, last: int = 0,

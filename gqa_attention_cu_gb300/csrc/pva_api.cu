@@ -127,6 +127,29 @@ int encode_map(CUtensorMap* map, const void* base, int dtype, int dim, int heads
   return PVA_OK;
 }
 
+// Rank-3 map over [tokens, heads, dim] rows: boxes of box_heads heads of box_tokens
+// tokens, 64 columns and 128-byte swizzle.  Tokens past the last read as zeros.
+int encode_rows_map(CUtensorMap* map, const void* base, int dtype, int dim, int heads,
+                    long long tokens, int box_heads, int box_tokens) {
+  const cuuint64_t gdim[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t gstride[2] = {(cuuint64_t)dim * 2, (cuuint64_t)dim * heads * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const auto encode = g_encode.load();
+  CUresult r = encode(map, dtype == PVA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      3, const_cast<void*>(base), gdim, gstride, box, estride,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char msg[160];
+    snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (%d) dim=%d heads=%d tokens=%lld",
+             (int)r, dim, heads, tokens);
+    return fail(PVA_ERR_CUDA, msg);
+  }
+  return PVA_OK;
+}
+
 // Rank-3 map over a BNSH cache [planes, rows, dim] (plane = sequence * Hkv +
 // kv head, rows = the cache capacity): boxes of box_rows rows of one plane.
 // Rows past the capacity read as zeros.

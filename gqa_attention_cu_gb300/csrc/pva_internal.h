@@ -140,6 +140,8 @@ int cuda_fail(cudaError_t e, const char* what);
 int get_encoder();
 int encode_map(CUtensorMap* map, const void* base, int dtype, int dim, int heads, int box_dim,
                int box_heads, int box_tokens, bool swizzle128);
+int encode_rows_map(CUtensorMap* map, const void* base, int dtype, int dim, int heads,
+                    long long tokens, int box_heads, int box_tokens);
 int encode_plane_map(CUtensorMap* map, const void* base, int dtype, int dim, int rows,
                      long long planes, int box_dim, int box_rows, bool swizzle128);
 // What a call gets from the library for its device and stream (under api_mutex).

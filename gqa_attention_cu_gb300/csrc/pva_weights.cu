@@ -1,0 +1,982 @@
+// The weight that attention gives to each cache row (pva_kvcache_weights):
+//   w[b, h, j] = decay * previous + sum over tokens t and heads g of the group of
+//                exp(score(q[b, t, h G + g], k[j]) - lse[b, t, h G + g]).
+//
+// With lse given, one pass over the keys.  Without, either the scores of the first
+// pass are kept (few query rows: 4 bytes a row and key, against 2 d bytes of the key
+// itself) and a second kernel turns them into weights, or the keys are read twice.
+//
+//   pva_weights_front_kernel  one CTA per sequence: bounds and block table; the last
+//       one cuts the line of key tiles into pieces, one per SM.
+//   pva_weights_tc_kernel     f16/bf16 on tensor cores: Store, Apply, Stats (below).
+//   pva_weights_f32_kernel    f32 on the CUDA cores: Apply and Stats.
+//   pva_weights_rows_kernel   joins the pieces' maxima and sums of each query row.
+//   pva_weights_scores_kernel weights from kept scores.
+//
+// The line: (sequence, kv head, key tile of 128 keys), each tile counted once for
+// every chunk of query rows that it is multiplied with.  A key's weight is written by
+// one thread, chunk after chunk, so results do not depend on timing.
+#include <limits.h>
+#include <math.h>
+
+#include "pva_device.cuh"
+#include "pva_tree.h"
+
+using namespace pva;
+using namespace pva::host;
+
+namespace pva {
+namespace {
+
+constexpr int kKeys = 128;  // of a key tile
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct WeightsParams {
+  const void* q;           // [B, T, H, d]
+  const void* k_cache;
+  const int32_t* lens;     // [B] cache rows
+  const int32_t* q_lens;   // [B] tokens in use, or nullptr: T
+  const int32_t* table;    // [B, max_blocks], or nullptr: block b
+  const float* previous;   // [B, Hkv, width], or nullptr
+  const float* lse;        // [B, T, H], or nullptr
+  float* weights;          // [B, Hkv, width]
+  float decay, scale, softcap;
+  int B, T, H, Hkv, G, d, width;
+  int page, max_blocks, n_blocks;
+  int tokens_at_once;      // of a chunk
+  int pieces;
+  // workspace
+  int32_t* hdr;            // [0] accepted, [1] places, [2] places of a piece
+  int32_t* start;          // [B + 1] first place of each sequence
+  float2* part;            // [B * Hkv + pieces][parts][T * G] (m, l) of a piece's keys
+  int parts;               // that a piece leaves for a row
+  float2* row;             // [B][Hkv][T * G] (m, 1 / l); with lse: not used
+  float* scores;           // [places][rows][128]
+  uint32_t* status;
+};
+
+// A sequence on the line.
+struct Sequence {
+  int n, q;       // cache rows, tokens
+  int chunks;     // of query rows (one at least: the old weights fade in any case)
+  int tiles;      // of keys
+  __device__ __forceinline__ Sequence(const WeightsParams& p, int b)
+      : n(p.lens[b]), q(p.q_lens ? p.q_lens[b] : p.T) {
+    chunks = max(1, (q + p.tokens_at_once - 1) / p.tokens_at_once);
+    tiles = (n + kKeys - 1) / kKeys;
+  }
+  __device__ __forceinline__ int per_head() const { return tiles * chunks; }
+};
+
+// A piece's part of one (sequence, kv head): key tiles [j0, j1).
+struct Segment {
+  int b, h, n, q, chunks, j0, j1, slot;
+};
+// Tiles that begin in the places [from, to) of a head.
+__device__ __forceinline__ int first_tile(int place, int chunks) { return (place + chunks - 1) / chunks; }
+
+// Walks the segments of places [x, end); one warp, the same state in all lanes.
+struct Walk {
+  int piece;
+  long long x, end;
+  int b = -1;
+  __device__ __forceinline__ Walk(const WeightsParams& p, int piece_, long long places, long long chunk)
+      : piece(piece_) {
+    x = piece * chunk;
+    end = x + chunk < places ? x + chunk : places;
+  }
+  __device__ __forceinline__ bool next(const WeightsParams& p, Segment& s) {
+    while (x < end) {
+      if (b < 0) b = tree_find(p.start, p.B, (int)x);
+      while (p.start[b + 1] <= x) ++b;
+      const Sequence seq(p, b);
+      const int rel = (int)x - p.start[b], per = seq.per_head();
+      s.b = b;
+      s.h = rel / per;
+      const int within = rel - s.h * per;
+      const int take = (int)(end - x < per - within ? end - x : per - within);
+      s.n = seq.n;
+      s.q = seq.q;
+      s.chunks = seq.chunks;
+      s.j0 = first_tile(within, seq.chunks);
+      s.j1 = first_tile(within + take, seq.chunks);
+      s.slot = b * p.Hkv + s.h + piece;
+      x += take;
+      if (s.j0 < s.j1) return true;
+    }
+    return false;
+  }
+};
+
+// Keys that token t of a sequence sees.
+__device__ __forceinline__ int keys_of(const Segment& s, int t) { return s.n - s.q + t + 1; }
+
+// Key tiles [j0, end) of chunk c: the first chunk visits all of a segment's.
+__device__ __forceinline__ int chunk_end(const WeightsParams& p, const Segment& s, int c, bool stats) {
+  if (c == 0 && !stats) return s.j1;
+  const int last = min(s.q, (c + 1) * p.tokens_at_once);  // tokens up to here
+  const int tiles = last > 0 ? (keys_of(s, last - 1) + kKeys - 1) / kKeys : 0;
+  return max(s.j0, min(s.j1, tiles));
+}
+
+constexpr int kFrontThreads = 128;
+constexpr int kWordArrived = 16, kWordBad = 17;  // of the status block, zero between calls
+
+__global__ void __launch_bounds__(kFrontThreads) pva_weights_front_kernel(WeightsParams p) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ int s_last;
+  __shared__ long long s_sum[kFrontThreads / 32];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
+  const int n = p.lens[b], q = p.q_lens ? p.q_lens[b] : p.T;
+  uint32_t bad = 0;
+  if (n < 0 || n > p.width || (long long)n > (long long)p.max_blocks * p.page || q < 0 || q > p.T || q > n)
+    bad = PVA_DEV_KV_LEN;
+  bool off = false;
+  if (!bad && p.table)
+    for (int i = tid; i < (n + p.page - 1) / p.page; i += kFrontThreads)
+      off |= (unsigned)p.table[(size_t)b * p.max_blocks + i] >= (unsigned)p.n_blocks;
+  if (__syncthreads_or(off)) bad = PVA_DEV_BLOCKS;
+  auto places = [&](int i) {
+    const Sequence s(p, i);
+    const bool sane = s.n >= 0 && s.q >= 0 && s.n <= p.width && s.q <= p.T;
+    return sane ? (long long)s.per_head() * p.Hkv : 0ll;
+  };
+  if (tid == 0) {
+    if (bad) atomicOr(p.status + kWordBad, bad);
+    __threadfence();
+    s_last = atomicAdd(p.status + kWordArrived, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  long long carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kFrontThreads) {
+    const int i = b0 + tid;
+    const long long x = i < p.B ? places(i) : 0;
+    long long upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if ((tid & 31) >= o) upto += y;
+    }
+    if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
+    __syncthreads();
+    long long before = carry;
+    for (int w = 0; w < kFrontThreads / 32; ++w) {
+      before += w < tid >> 5 ? s_sum[w] : 0;
+      carry += s_sum[w];
+    }
+    if (i < p.B) p.start[i] = (int)min(before + upto - x, (long long)INT_MAX);
+    __syncthreads();
+  }
+  if (tid == 0) {
+    uint32_t found = __ldcg(p.status + kWordBad);
+    p.status[kWordBad] = 0;  // for the next call
+    p.status[kWordArrived] = 0;
+    if (!found && carry > INT_MAX - 4ll * p.pieces) found = PVA_DEV_TOO_MANY;
+    if (found) atomicOr(p.status, found);
+    const int all = found || latched ? 0 : (int)carry;
+    p.start[p.B] = all;
+    p.hdr[0] = all > 0;
+    p.hdr[1] = all;
+    p.hdr[2] = max(1, (all + p.pieces - 1) / p.pieces);
+  }
+}
+
+// score -> natural units, with the softcap.
+template <bool CAP>
+__device__ __forceinline__ float natural(float s, float scale, float softcap, float inv_cap) {
+  const float x = s * scale;
+  return CAP ? softcap * tanhf(x * inv_cap) : x;
+}
+
+// ---------------------------------------------------------------------------
+// Tensor cores.  One CTA per piece, 320 threads:
+//   warp 0      TMA producer: publishes the segments' chunks, loads the chunk's
+//               query rows and then the key tiles through a ring.
+//   warp 1      MMA issuer and TMEM owner; two score buffers.
+//   warps 2..5, 6..9   take the tiles of score buffer 0 and 1.
+// Store and Apply form S^T = K Q^T, 128 keys by N query rows: a thread has a key and
+// adds up over its columns without meeting another.  Stats forms S = Q K^T, 128
+// query rows by 128 keys: a thread has a row and keeps its running maximum and sum.
+// ---------------------------------------------------------------------------
+enum Mode { kStore, kApply, kStats };
+constexpr int kTcThreads = 320;
+constexpr int kItemSlots = 4;
+
+struct ItemSlot {
+  Segment s;
+  int c, end, last;  // chunk, its last key tile + 1; no more work
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2], drain;
+  uint64_t s_full[2], s_free[2];
+  uint64_t ring_full[12], ring_empty[12];
+  uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+  ItemSlot items[kItemSlots];
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int kBarBytes = 1024;
+static_assert(sizeof(Bars) <= kBarBytes, "barriers and segments");
+
+template <int D, int N, int MODE>
+struct WCfg {
+  static constexpr int CH = (D + 63) / 64;
+  static constexpr int Q_CHUNK = N * 128;       // bytes of 64 columns of the query rows
+  static constexpr int Q_TILE = CH * Q_CHUNK;
+  static constexpr int K_CHUNK = kKeys * 128;
+  static constexpr int K_TILE = CH * K_CHUNK;
+  static constexpr int Q_BUFS = 2 * Q_TILE <= 64 * 1024 ? 2 : 1;
+  // barriers, then (Apply) each score warp's copy of the chunk's row values
+  static constexpr int HEAD = kBarBytes + (MODE == kApply ? (8 * N * 8 + 1023) / 1024 * 1024 : 0);
+  static constexpr int OFF_RING = Q_BUFS * Q_TILE;
+  static constexpr int SLOTS_FIT = (232448 - HEAD - OFF_RING) / K_TILE;
+  static constexpr int SLOTS = SLOTS_FIT < 12 ? SLOTS_FIT : 12;
+  static_assert(SLOTS >= 2, "ring depth");
+  static constexpr int SMEM = HEAD + OFF_RING + SLOTS * K_TILE;
+  static constexpr int COLS = MODE == kStats ? kKeys : N;  // of a score buffer
+  static constexpr int TMEM_COLS = 2 * COLS;
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// l = sum of exp(x - m), m = max x: one more x.
+__device__ __forceinline__ void add_score(float& m, float& l, float x) {
+  const float NEG_INF = __int_as_float(0xff800000);
+  if (x == NEG_INF) return;
+  const float d = m - x, e = ex2_approx(-fabsf(d) * kLog2e);  // m = -inf: e = 0
+  l = d >= 0.0f ? l + e : fmaf(l, e, 1.0f);
+  m = fmaxf(m, x);
+}
+__device__ __forceinline__ void join_scores(float& m, float& l, float m2, float l2) {
+  const float NEG_INF = __int_as_float(0xff800000);
+  const float top = fmaxf(m, m2), base = top == NEG_INF ? 0.0f : top;
+  l = l * exp2f((m - base) * kLog2e) + l2 * exp2f((m2 - base) * kLog2e);
+  m = top;
+}
+
+template <typename T, int D, int N, int MODE, bool CAP>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    pva_weights_tc_kernel(WeightsParams p, const __grid_constant__ CUtensorMap tmap_q,
+                          const __grid_constant__ CUtensorMap tmap_k) {
+  using C = WCfg<D, N, MODE>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Bars* bars = reinterpret_cast<Bars*>(smem_raw);
+  uint8_t* smem = smem_raw + C::HEAD;
+  uint8_t* ring = smem + C::OFF_RING;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* status = p.status;
+  volatile int* abort = &bars->abort;
+  if ((smem_u32(smem_raw) & 1023) != 0) {  // the tiles' layout rests on it
+    if (threadIdx.x == 0) {
+      wait_prior_grid();
+      atomicOr(p.status, PVA_DEV_WAIT_TIMEOUT);
+    }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    bars->abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_free[i], 4);
+    }
+    mbar_init(&bars->drain, 1);
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(&bars->ring_full[i], 1);
+      mbar_init(&bars->ring_empty[i], 1);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], 1 + 8);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc<C::TMEM_COLS>(&bars->tmem_base);
+  if (warp == 0 && lane == 0) {
+    prefetch_tensor_map(&tmap_q);
+    prefetch_tensor_map(&tmap_k);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  allow_next_grid();
+  wait_prior_grid();
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, abort, status));
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    Walk walk(p, blockIdx.x, p.hdr[1], p.hdr[2]);
+    const int box = p.table && p.page < kKeys ? p.page : kKeys, copies = kKeys / box;
+    uint32_t loads = 0, published = 0, q_loads = 0;
+    bool ok = true;
+    auto publish = [&](const ItemSlot& v) -> bool {
+      const int sl = published % kItemSlots;
+      if (!wait(&bars->item_empty[sl], ((published / kItemSlots) & 1) ^ 1)) return false;
+      if (lane == 0) {
+        bars->items[sl] = v;
+        mbar_arrive(&bars->item_full[sl]);
+      }
+      __syncwarp();
+      ++published;
+      return true;
+    };
+    ItemSlot v;
+    v.last = 0;
+    while (ok && walk.next(p, v.s)) {
+      const Segment& s = v.s;
+      for (int c = 0; ok && c < s.chunks; ++c) {
+        v.c = c;
+        v.end = chunk_end(p, s, c, MODE == kStats);
+        if (!(ok = publish(v))) break;
+        if (v.end == s.j0) continue;
+        const int qb = q_loads % C::Q_BUFS;
+        if (!(ok = wait(&bars->q_empty[qb], ((q_loads / C::Q_BUFS) & 1) ^ 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[qb], C::CH * (uint32_t)(p.tokens_at_once * p.G) * 128u);
+          for (int x = 0; x < C::CH; ++x)
+            tma_load_3d(smem + qb * C::Q_TILE + x * C::Q_CHUNK, &tmap_q, &bars->q_full[qb], x * 64,
+                        s.h * p.G, s.b * p.T + c * p.tokens_at_once);
+        }
+        __syncwarp();
+        ++q_loads;
+        for (int j = s.j0; j < v.end; ++j, ++loads) {
+          const int sl = loads % C::SLOTS;
+          // a page a lane, or the whole tile
+          const long long r0 = (long long)j * kKeys + lane * box;
+          const bool mine = lane < copies && r0 < s.n;
+          int block = 0, y = 0;
+          if (mine) {
+            const int in = (int)r0 / p.page;
+            block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+            y = (int)r0 - in * p.page;
+          }
+          const uint32_t n_copies = __popc(__ballot_sync(0xffffffffu, mine));
+          if (!(ok = wait(&bars->ring_empty[sl], ((loads / C::SLOTS) & 1) ^ 1))) break;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&bars->ring_full[sl], n_copies * C::CH * (uint32_t)box * 128u);
+          __syncwarp();
+          if (mine) {
+            uint8_t* dst = ring + sl * C::K_TILE + lane * box * 128;
+#pragma unroll
+            for (int x = 0; x < C::CH; ++x)
+              tma_load_3d(dst + x * C::K_CHUNK, &tmap_k, &bars->ring_full[sl], x * 64, y,
+                          block * p.Hkv + s.h);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (ok) {
+      v.last = 1;
+      publish(v);
+    }
+    // Drain: every copy this warp issued must land before the CTA exits.
+    for (int i = 0; i < C::Q_BUFS; ++i) {
+      const uint32_t fills = q_loads > (uint32_t)i ? (q_loads - 1 - i) / C::Q_BUFS + 1 : 0;
+      if (fills) mbar_wait<false>(&bars->q_full[i], (fills - 1) & 1, abort, status);
+    }
+    for (int i = 0; i < C::SLOTS; ++i) {
+      const uint32_t fills = loads > (uint32_t)i ? (loads - 1 - i) / C::SLOTS + 1 : 0;
+      if (fills) mbar_wait<false>(&bars->ring_full[i], (fills - 1) & 1, abort, status);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_sync();
+    constexpr uint32_t idesc = MODE == kStats ? idesc_f16<T>(kTcRows, kKeys, false, false)
+                                              : idesc_f16<T>(kKeys, N, false, false);
+    const uint64_t qdesc = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t kdesc = sdesc_sw128(smem_u32(ring), 16, 1024);
+    uint32_t loads = 0, taken = 0, q_cnt = 0, used0 = 0, used1 = 0;
+    bool ok = true;
+    while (ok) {
+      const int isl = taken % kItemSlots;
+      if (!(ok = wait(&bars->item_full[isl], (taken / kItemSlots) & 1))) break;
+      const int j0 = bars->items[isl].s.j0, end = bars->items[isl].end, last = bars->items[isl].last;
+      __syncwarp();
+      if (leader) mbar_arrive(&bars->item_empty[isl]);
+      ++taken;
+      if (last) break;
+      if (j0 == end) continue;
+      const int qb = q_cnt % C::Q_BUFS;
+      if (!(ok = wait(&bars->q_full[qb], (q_cnt / C::Q_BUFS) & 1))) break;
+      ++q_cnt;
+      const uint64_t qa = sdesc_advance(qdesc, qb * C::Q_TILE);
+      for (int j = j0; j < end; ++j, ++loads) {
+        const int sl = loads % C::SLOTS, buf = j & 1;
+        if (!(ok = wait(&bars->ring_full[sl], (loads / C::SLOTS) & 1))) break;
+        if (!(ok = wait(&bars->s_free[buf], (buf ? used1++ : used0++) & 1 ^ 1))) break;
+        tc_fence_after();
+        const uint64_t ka = sdesc_advance(kdesc, sl * C::K_TILE);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t x = sdesc_advance(qa, (kk >> 2) * C::Q_CHUNK + (kk & 3) * 32);
+            const uint64_t y = sdesc_advance(ka, (kk >> 2) * C::K_CHUNK + (kk & 3) * 32);
+            mma_ss(tmem + buf * C::COLS, MODE == kStats ? x : y, MODE == kStats ? y : x, idesc,
+                   kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&bars->s_full[buf]);
+          mma_commit(&bars->ring_empty[sl]);
+          if (j + 1 == end) mma_commit(&bars->q_empty[qb]);
+        }
+      }
+    }
+    // Drain: all issued MMAs complete before TMEM is released.
+    if (leader) mma_commit(&bars->drain);
+    wait(&bars->drain, 0);
+  } else {
+    // ------------------------------------------------------------ scores
+    const int group = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + group * C::COLS;
+    const float scale = p.scale, cap = p.softcap, inv_cap = CAP ? 1.0f / p.softcap : 0.0f;
+    const float NEG_INF = __int_as_float(0xff800000);
+    float2* rows = reinterpret_cast<float2*>(smem_raw + kBarBytes) + (warp - 2) * N;
+    uint32_t tiles = 0, taken = 0;
+    bool ok = true;
+    while (ok) {
+      const int isl = taken % kItemSlots;
+      if (!(ok = wait(&bars->item_full[isl], (taken / kItemSlots) & 1))) break;
+      const ItemSlot it = bars->items[isl];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->item_empty[isl]);
+      ++taken;
+      if (it.last) break;
+      const Segment& s = it.s;
+      const int t0 = it.c * p.tokens_at_once;
+      const int used = max(0, min(p.tokens_at_once, s.q - t0)) * p.G;  // query rows of the chunk
+      const int row0 = t0 * p.G;
+      if constexpr (MODE == kApply) {
+        __syncwarp();
+        for (int i = lane; i < used; i += 32) {
+          const int t = t0 + i / p.G, g = i % p.G;
+          float2 v;
+          if (p.lse) {
+            // a row that saw nothing (-inf) weighs nothing
+            const float x = p.lse[((size_t)s.b * p.T + t) * p.H + s.h * p.G + g];
+            v = make_float2(x == NEG_INF ? -NEG_INF : x, 1.0f);
+          } else {
+            v = p.row[((size_t)s.b * p.Hkv + s.h) * p.T * p.G + row0 + i];
+          }
+          rows[i] = v;
+        }
+        __syncwarp();
+      }
+      const int free_of_masks = used ? keys_of(s, t0) : 0;  // keys that all rows see
+      // Store: running (m, l) of this key lane's scores, by column; Stats: of this row
+      constexpr int ACC = MODE == kStore ? N : 1;
+      float m[ACC], l[ACC];
+#pragma unroll
+      for (int c = 0; c < ACC; ++c) {
+        m[c] = NEG_INF;
+        l[c] = 0.0f;
+      }
+      const int my_row = t0 + r / p.G;  // Stats: the row's token
+      // Each buffer's tiles are every other one of the keys: a key is always this thread's.
+      for (int j = s.j0 + ((s.j0 ^ group) & 1); j < it.end; j += 2, ++tiles) {
+        const int k0 = j * kKeys, key = k0 + r;
+        const bool all = k0 + kKeys <= free_of_masks;
+        float base = 0.0f;
+        const size_t at = ((size_t)s.b * p.Hkv + s.h) * p.width + key;
+        if (MODE == kApply && key < s.n) {
+          if (it.c > 0) base = p.weights[at];
+          else if (p.previous) base = p.decay * p.previous[at];
+        }
+        if (!(ok = wait(&bars->s_full[group], tiles & 1))) break;
+        tc_fence_after();
+        if (MODE == kStats) {
+          const int hi = r < used ? keys_of(s, my_row) : 0;
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(t_s + c, v);
+            tmem_wait_ld_of(v);
+            if (r < used) {
+              float x[32], top = NEG_INF;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                x[e] = natural<CAP>(__uint_as_float(v[e]), scale, cap, inv_cap);
+                if (!all && k0 + c + e >= hi) x[e] = NEG_INF;
+                top = fmaxf(top, x[e]);
+              }
+              if (top > m[0]) {
+                l[0] *= ex2_approx((m[0] - top) * kLog2e);
+                m[0] = top;
+              }
+              if (m[0] > NEG_INF) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sum += ex2_approx((x[e] - m[0]) * kLog2e);
+                l[0] += sum;
+              }
+            }
+          }
+        } else {
+          float sum = base;
+          float* score = nullptr;
+          if constexpr (MODE == kStore)
+            score = p.scores + ((long long)p.start[s.b] + (long long)s.h * ((s.n + kKeys - 1) / kKeys) + j) *
+                                   p.T * p.G * kKeys + r;
+#pragma unroll 1
+          for (int c = 0; c < N; c += 16) {
+            if (c >= used) break;
+            uint32_t v[16];
+            tmem_ld16(t_s + c, v);
+            asm volatile("tcgen05.wait::ld.sync.aligned;"
+                         : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                           "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                           "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (c + e >= used) break;
+              const float x = natural<CAP>(__uint_as_float(v[e]), scale, cap, inv_cap);
+              const bool seen = all || key < keys_of(s, t0 + (c + e) / p.G);
+              if constexpr (MODE == kApply) {
+                const float2 w = rows[c + e];
+                const float y = ex2_approx((x - w.x) * kLog2e);
+                if (seen) sum = fmaf(y, w.y, sum);
+              } else {
+                const float y = seen ? x : NEG_INF;
+                score[(c + e) * kKeys] = y;
+                add_score(m[e], l[e], y);
+              }
+            }
+          }
+          if (MODE == kApply && key < s.n) p.weights[at] = sum;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_free[group]);
+      }
+      if (!ok) break;
+      // what this group (Stats) or warp (Store) has of each row
+      float2* part = p.part + (size_t)s.slot * p.parts * p.T * p.G + row0;
+      if constexpr (MODE == kStats)
+        if (r < used) part[(size_t)group * p.T * p.G + r] = make_float2(m[0], l[0]);
+      if constexpr (MODE == kStore) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (c >= used) break;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m[c], o), l2 = __shfl_xor_sync(0xffffffffu, l[c], o);
+            join_scores(m[c], l[c], m2, l2);
+          }
+          if (lane == 0) part[(size_t)(warp - 2) * p.T * p.G + c] = make_float2(m[c], l[c]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<C::TMEM_COLS>(tmem);
+}
+
+// ---------------------------------------------------------------------------
+// f32: a thread has a key of a tile of 128, whose rows lie in shared memory, and
+// kRowsF32 query rows at a time.  Exact f32 products.
+// ---------------------------------------------------------------------------
+constexpr int kRowsF32 = 8;
+__host__ __device__ constexpr int f32_row(int d) { return (d + 3) / 4 * 4 + 4; }
+size_t f32_smem(int d) { return sizeof(float) * (size_t)(kKeys + kRowsF32) * f32_row(d) + 4 * kRowsF32 * 16; }
+
+template <int MODE>
+__global__ void __launch_bounds__(kKeys) pva_weights_f32_kernel(WeightsParams p) {
+  extern __shared__ float smem[];
+  __shared__ Segment s_segment;
+  __shared__ int s_more;
+  __shared__ float2 s_rows[kRowsF32];
+  __shared__ int s_hi[kRowsF32];
+  __shared__ float2 s_warp[kKeys / 32][kRowsF32];
+  allow_next_grid();
+  wait_prior_grid();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = p.d, row = f32_row(d);
+  const float NEG_INF = __int_as_float(0xff800000);
+  float* sk = smem;
+  float* sq = smem + (size_t)kKeys * row;
+  const float* kc = static_cast<const float*>(p.k_cache);
+  const float* q = static_cast<const float*>(p.q);
+  for (int i = tid; i < (kKeys + kRowsF32) * (row - d); i += kKeys)
+    smem[(size_t)(i / (row - d)) * row + d + i % (row - d)] = 0.0f;
+  Walk walk(p, blockIdx.x, p.hdr[1], p.hdr[2]);  // the first warp's counts
+  while (true) {
+    __syncthreads();
+    if (warp == 0) {
+      Segment s;
+      const bool more = walk.next(p, s);
+      if (lane == 0) {
+        s_more = more;
+        s_segment = s;
+      }
+    }
+    __syncthreads();
+    if (!s_more) break;
+    const Segment s = s_segment;
+    const int all_rows = s.q * p.G;
+    auto load_keys = [&](int j) {
+      for (int i = warp; i < kKeys; i += kKeys / 32) {
+        const int key = j * kKeys + i;
+        size_t at = 0;
+        if (key < s.n) {
+          const int in = key / p.page;
+          const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+          at = (((size_t)block * p.Hkv + s.h) * p.page + (key - in * p.page)) * d;
+        }
+        for (int c = lane; c < d; c += 32) sk[(size_t)i * row + c] = key < s.n ? kc[at + c] : 0.0f;
+      }
+    };
+    auto load_rows = [&](int r0) {
+      for (int i = warp; i < kRowsF32; i += kKeys / 32) {
+        const int r = r0 + i, t = r / p.G, g = r - t * p.G;
+        const bool there = r < all_rows;
+        const float* src = q + (((size_t)s.b * p.T + t) * p.H + s.h * p.G + g) * d;
+        for (int c = lane; c < d; c += 32) sq[(size_t)i * row + c] = there ? src[c] : 0.0f;
+      }
+      if (tid < kRowsF32) {
+        const int r = r0 + tid, t = r / p.G, g = r - t * p.G;
+        const bool there = r < all_rows;
+        s_hi[tid] = there ? keys_of(s, t) : 0;
+        if (MODE == kApply && there) {
+          if (p.lse) {
+            const float x = p.lse[((size_t)s.b * p.T + t) * p.H + s.h * p.G + g];
+            s_rows[tid] = make_float2(x == NEG_INF ? -NEG_INF : x, 1.0f);
+          } else {
+            s_rows[tid] = p.row[((size_t)s.b * p.Hkv + s.h) * p.T * p.G + r];
+          }
+        }
+      }
+    };
+    auto scores = [&](float (&x)[kRowsF32]) {
+#pragma unroll
+      for (int e = 0; e < kRowsF32; ++e) x[e] = 0.0f;
+      for (int c = 0; c < d; c += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(sk + (size_t)tid * row + c);
+#pragma unroll
+        for (int e = 0; e < kRowsF32; ++e) {
+          const float4 v = *reinterpret_cast<const float4*>(sq + (size_t)e * row + c);
+          x[e] = fmaf(k.w, v.w, fmaf(k.z, v.z, fmaf(k.y, v.y, fmaf(k.x, v.x, x[e]))));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kRowsF32; ++e)
+        x[e] = p.softcap != 0.0f ? natural<true>(x[e], p.scale, p.softcap, 1.0f / p.softcap)
+                                 : natural<false>(x[e], p.scale, 0.0f, 0.0f);
+    };
+    if (MODE == kApply) {
+      for (int j = s.j0; j < s.j1; ++j) {
+        __syncthreads();
+        load_keys(j);
+        const int key = j * kKeys + tid;
+        const size_t at = ((size_t)s.b * p.Hkv + s.h) * p.width + key;
+        float sum = key < s.n && p.previous ? p.decay * p.previous[at] : 0.0f;
+        for (int r0 = 0; r0 < all_rows; r0 += kRowsF32) {
+          if (r0) __syncthreads();
+          load_rows(r0);
+          __syncthreads();
+          float x[kRowsF32];
+          scores(x);
+#pragma unroll
+          for (int e = 0; e < kRowsF32; ++e)
+            if (key < s_hi[e]) sum = fmaf(exp2f((x[e] - s_rows[e].x) * kLog2e), s_rows[e].y, sum);
+        }
+        if (key < s.n) p.weights[at] = sum;
+      }
+    } else {
+      for (int r0 = 0; r0 < all_rows; r0 += kRowsF32) {
+        float m[kRowsF32], l[kRowsF32];
+#pragma unroll
+        for (int e = 0; e < kRowsF32; ++e) {
+          m[e] = NEG_INF;
+          l[e] = 0.0f;
+        }
+        for (int j = s.j0; j < s.j1; ++j) {
+          __syncthreads();
+          if (j == s.j0) load_rows(r0);
+          load_keys(j);
+          __syncthreads();
+          float x[kRowsF32];
+          scores(x);
+#pragma unroll
+          for (int e = 0; e < kRowsF32; ++e) {
+            if (j * kKeys + tid >= s_hi[e]) continue;
+            const float top = fmaxf(m[e], x[e]);
+            l[e] = l[e] * exp2f((m[e] - top) * kLog2e) + exp2f((x[e] - top) * kLog2e);
+            m[e] = top;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kRowsF32; ++e) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m[e], o), l2 = __shfl_xor_sync(0xffffffffu, l[e], o);
+            join_scores(m[e], l[e], m2, l2);
+          }
+          if (lane == 0) s_warp[warp][e] = make_float2(m[e], l[e]);
+        }
+        __syncthreads();
+        if (tid < kRowsF32 && r0 + tid < all_rows) {
+          float2 v = s_warp[0][tid];
+          for (int w = 1; w < kKeys / 32; ++w) join_scores(v.x, v.y, s_warp[w][tid].x, s_warp[w][tid].y);
+          p.part[(size_t)s.slot * p.T * p.G + r0 + tid] = v;
+        }
+      }
+    }
+  }
+}
+
+// (m, 1 / l) of every query row from its pieces', in the order of the line: a warp a row.
+__global__ void __launch_bounds__(256) pva_weights_rows_kernel(WeightsParams p) {
+  allow_next_grid();
+  wait_prior_grid();
+  if (!p.hdr[0]) return;
+  const int lane = threadIdx.x & 31, R = p.T * p.G;
+  const long long chunk = p.hdr[2], rows = (long long)p.B * p.Hkv * R;
+  const float NEG_INF = __int_as_float(0xff800000);
+  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += (long long)gridDim.x * 8) {
+    const int item = (int)(i / R), r = (int)(i - (long long)item * R), b = item / p.Hkv, h = item - b * p.Hkv;
+    const Sequence s(p, b);
+    if (r >= s.q * p.G) continue;
+    const long long x0 = p.start[b] + (long long)h * s.per_head(), x1 = x0 + s.per_head();
+    float m = NEG_INF, l = 0.0f;
+    for (long long pc = x0 / chunk + lane; pc * chunk < x1; pc += 32) {
+      // a piece that holds no tile's first place has no part
+      const long long from = pc * chunk > x0 ? pc * chunk - x0 : 0, to = (pc + 1) * chunk < x1 ? (pc + 1) * chunk - x0 : x1 - x0;
+      if (first_tile((int)from, s.chunks) >= first_tile((int)to, s.chunks)) continue;
+      for (int i = 0; i < p.parts; ++i) {
+        const float2 v = p.part[((size_t)(item + pc) * p.parts + i) * R + r];
+        join_scores(m, l, v.x, v.y);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+      join_scores(m, l, m2, l2);
+    }
+    // a row that saw nothing weighs nothing
+    if (lane == 0) p.row[i] = l == 0.0f ? make_float2(-NEG_INF, 0.0f) : make_float2(m, 1.0f / l);
+  }
+}
+
+// Weights from kept scores: a CTA a run of key tiles, a thread a key.
+__global__ void __launch_bounds__(kKeys) pva_weights_scores_kernel(WeightsParams p) {
+  allow_next_grid();
+  wait_prior_grid();
+  __shared__ float2 s_rows[16];
+  const int places = p.hdr[1], tid = threadIdx.x, R = p.T * p.G;
+  const int run = (places + gridDim.x - 1) / gridDim.x;
+  int x = blockIdx.x * run;
+  const int end = min(x + run, places);
+  int last_item = -1;
+  for (int b = x < end ? tree_find(p.start, p.B, x) : 0; x < end; ++x) {
+    while (p.start[b + 1] <= x) ++b;
+    const Sequence s(p, b);
+    const int rel = x - p.start[b], h = rel / s.tiles, key = (rel - h * s.tiles) * kKeys + tid;
+    const int used = s.q * p.G, item = b * p.Hkv + h;
+    if (item != last_item) {
+      __syncthreads();
+      if (tid < used) s_rows[tid] = p.row[(size_t)item * R + tid];
+      __syncthreads();
+      last_item = item;
+    }
+    if (key >= s.n) continue;
+    const size_t at = (size_t)item * p.width + key;
+    float sum = p.previous ? p.decay * p.previous[at] : 0.0f;
+    const float* score = p.scores + (long long)x * R * kKeys + tid;
+    for (int r = 0; r < used; ++r) sum = fmaf(ex2_approx((score[r * kKeys] - s_rows[r].x) * kLog2e), s_rows[r].y, sum);
+    p.weights[at] = sum;
+  }
+}
+
+template <typename T, int D, int N, int MODE>
+cudaError_t launch_mode(const WeightsParams& p, const CUtensorMap& tq, const CUtensorMap& tk, cudaStream_t s) {
+  constexpr int smem = WCfg<D, N, MODE>::SMEM;
+  auto kern = p.softcap != 0.0f ? pva_weights_tc_kernel<T, D, N, MODE, true> : pva_weights_tc_kernel<T, D, N, MODE, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(p.pieces), dim3(kTcThreads), smem, s, p, tq, tk);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const WeightsParams& p, int mode, int n, const CUtensorMap& tq, const CUtensorMap& tk, cudaStream_t s) {
+  if (mode == kStore) return launch_mode<T, D, 16, kStore>(p, tq, tk, s);
+  if (mode == kStats) return launch_mode<T, D, kTcRows, kStats>(p, tq, tk, s);
+  return n == 16   ? launch_mode<T, D, 16, kApply>(p, tq, tk, s)
+         : n == 32 ? launch_mode<T, D, 32, kApply>(p, tq, tk, s)
+         : n == 64 ? launch_mode<T, D, 64, kApply>(p, tq, tk, s)
+                   : launch_mode<T, D, 128, kApply>(p, tq, tk, s);
+}
+
+template <typename T>
+cudaError_t launch_type(const WeightsParams& p, int mode, int n, const CUtensorMap& tq, const CUtensorMap& tk, cudaStream_t s) {
+  switch (p.d) {
+    case 64: return launch_d<T, 64>(p, mode, n, tq, tk, s);
+    case 96: return launch_d<T, 96>(p, mode, n, tq, tk, s);
+    case 128: return launch_d<T, 128>(p, mode, n, tq, tk, s);
+    case 192: return launch_d<T, 192>(p, mode, n, tq, tk, s);
+    case 256: return launch_d<T, 256>(p, mode, n, tq, tk, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+template <int MODE>
+cudaError_t launch_f32(const WeightsParams& p, cudaStream_t s) {
+  const size_t smem = f32_smem(p.d);
+  cudaError_t e = cudaFuncSetAttribute(pva_weights_f32_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(pva_weights_f32_kernel<MODE>, dim3(p.pieces), dim3(kKeys), smem, s, p);
+}
+
+int weights(const void* q, const void* k_cache, const int32_t* lens, const int32_t* q_lens, const int32_t* table,
+            const float* previous, const float* lse, float* out, int B, int T, int n_blocks, int page, int max_blocks, int H,
+            int Hkv, int d, int width, float decay, float scale, float softcap, int dtype, cudaStream_t stream) {
+  if (!q || !k_cache || !lens || !out) return fail(PVA_ERR_INVALID_ARG, "null q, k_cache, lens or weights pointer");
+  if (B < 1 || T < 1 || n_blocks < 1 || page < 1 || width < 1)
+    return fail(PVA_ERR_INVALID_ARG, "need B >= 1, tokens >= 1, n_blocks >= 1, page_size >= 1, width >= 1");
+  if (H < 1 || Hkv < 1 || H % Hkv != 0)
+    return fail(PVA_ERR_INVALID_ARG, "num_heads must be a positive multiple of a positive kv_num_heads");
+  if (dtype != PVA_F32 && dtype != PVA_F16 && dtype != PVA_BF16)
+    return fail(PVA_ERR_INVALID_ARG, "dtype must be 0 (f32), 1 (f16) or 2 (bf16)");
+  if (!isfinite(scale) || !isfinite(softcap) || !isfinite(decay))
+    return fail(PVA_ERR_INVALID_ARG, "scale, softcap and decay must be finite");
+  const bool tc = dtype != PVA_F32;
+  if (tc ? d != 64 && d != 96 && d != 128 && d != 192 && d != 256 : d < 2 || d > 256 || d % 2 != 0)
+    return fail(PVA_ERR_UNSUPPORTED,
+                "head_size must be 64, 96, 128, 192 or 256 (f16/bf16), or even and at most 256 (f32)");
+  const int G = H / Hkv;
+  if (G > 128) return fail(PVA_ERR_UNSUPPORTED, "num_heads / kv_num_heads must be at most 128");
+  if (table) {
+    if (max_blocks < 1) return fail(PVA_ERR_INVALID_ARG, "max_blocks must be >= 1");
+    if (page < 16 || (page & (page - 1)) != 0)
+      return fail(PVA_ERR_UNSUPPORTED, "page_size must be a power of two of at least 16");
+  } else {
+    if (n_blocks != B)
+      return fail(PVA_ERR_INVALID_ARG, "without a block table the cache has one block a sequence");
+    max_blocks = 1;
+  }
+  if ((long long)B * T > INT_MAX - 65536 || (long long)T * G > INT_MAX / 2 ||
+      (long long)max_blocks * page > INT_MAX - 65536 || (long long)n_blocks * Hkv > INT_MAX ||
+      (long long)B * Hkv > INT_MAX - 65536 || width > INT_MAX - 65536)
+    return fail(PVA_ERR_INVALID_ARG, "cache or token extents do not fit in int32");
+  const size_t size = tc ? 2 : 4;
+  const uintptr_t mis = (uintptr_t)q | (uintptr_t)k_cache;
+  if (tc && (mis & 15)) return fail(PVA_ERR_INVALID_ARG, "q and k_cache must be 16-byte aligned");
+  if (mis % size || ((uintptr_t)out | (uintptr_t)previous | (uintptr_t)lse) & 3)
+    return fail(PVA_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+  auto meets = [](const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + nb && y < x + na;
+  };
+  const size_t all = 4 * (size_t)B * Hkv * width;
+  if ((previous != out && meets(out, all, previous, all)) || meets(out, all, lse, 4 * (size_t)B * T * H) ||
+      meets(out, all, lens, 4 * (size_t)B) || meets(out, all, q_lens, 4 * (size_t)B) ||
+      meets(out, all, table, 4 * (size_t)B * max_blocks))
+    return fail(PVA_ERR_INVALID_ARG, "weights overlap an input (previous may be weights)");
+
+  WeightsParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.lens = lens;
+  p.q_lens = q_lens;
+  p.table = table;
+  p.previous = previous;
+  p.lse = lse;
+  p.weights = out;
+  p.decay = decay;
+  p.scale = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
+  p.softcap = fminf(fabsf(softcap), 1e34f);
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.d = d;
+  p.width = width;
+  p.page = page;
+  p.max_blocks = max_blocks;
+  p.n_blocks = n_blocks;
+  const long long R = (long long)T * G;
+  // query rows of a chunk, and the score columns they take
+  const int n = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
+  p.tokens_at_once = tc ? (R <= 128 ? T : 128 / G) : T;
+  const bool store = tc && !lse && R <= 16;
+
+  std::lock_guard<std::mutex> lock(api_mutex());
+  int rc = sm_count(&p.pieces);
+  if (rc != PVA_OK) return rc;
+  if (!tc) p.pieces *= d <= 128 ? 3 : 1;
+  size_t used = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = used;
+    used += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t at_hdr = take(32), at_start = take(4 * ((size_t)B + 1));
+  p.parts = !tc ? 1 : store ? 8 : 2;
+  const size_t at_part = take(lse ? 0 : 8 * ((size_t)B * Hkv + p.pieces) * p.parts * R);
+  const size_t at_row = take(lse ? 0 : 8 * (size_t)B * Hkv * R);
+  const size_t tiles = ((size_t)(width < (long long)max_blocks * page ? width : (long long)max_blocks * page) + kKeys - 1) / kKeys;
+  const size_t at_scores = take(store ? 4 * (size_t)B * Hkv * tiles * R * kKeys : 0);
+  CallContext c;
+  if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
+  p.status = c.status;
+  p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
+  p.start = reinterpret_cast<int32_t*>(c.buf + at_start);
+  p.part = reinterpret_cast<float2*>(c.buf + at_part);
+  p.row = reinterpret_cast<float2*>(c.buf + at_row);
+  p.scores = reinterpret_cast<float*>(c.buf + at_scores);
+  CUtensorMap tq, tk;
+  if (tc) {
+    const int box = table && page < kKeys ? page : kKeys;
+    if ((rc = get_encoder()) != PVA_OK ||
+        (rc = encode_rows_map(&tq, q, dtype, d, H, (long long)B * T, G, p.tokens_at_once)) != PVA_OK ||
+        (rc = encode_plane_map(&tk, k_cache, dtype, d, page, (long long)n_blocks * Hkv, 64, box, true)) != PVA_OK)
+      return rc;
+  }
+  cudaError_t e = launch_dependent(pva_weights_front_kernel, dim3(B), dim3(kFrontThreads), 0, stream, p);
+  if (e != cudaSuccess) return cuda_fail(e, "weights front-end launch");
+  auto pass = [&](int mode) {
+    if (!tc) return mode == kApply ? launch_f32<kApply>(p, stream) : launch_f32<kStats>(p, stream);
+    return dtype == PVA_BF16 ? launch_type<__nv_bfloat16>(p, mode, n, tq, tk, stream)
+                             : launch_type<__half>(p, mode, n, tq, tk, stream);
+  };
+  if (!lse) {
+    if ((e = pass(store ? kStore : kStats)) != cudaSuccess) return cuda_fail(e, "row sums launch");
+    const long long want = ((long long)B * Hkv * R + 7) / 8;
+    e = launch_dependent(pva_weights_rows_kernel, dim3((unsigned)(want < 4096 ? want : 4096)), dim3(256), 0, stream, p);
+    if (e != cudaSuccess) return cuda_fail(e, "row sums launch");
+  }
+  e = store ? launch_dependent(pva_weights_scores_kernel, dim3(c.num_sms * 16), dim3(kKeys), 0, stream, p) : pass(kApply);
+  return e == cudaSuccess ? PVA_OK : cuda_fail(e, "weights launch");
+}
+
+}  // namespace
+}  // namespace pva
+
+extern "C" int pva_kvcache_weights(const void* q, const void* k_cache, const int32_t* lens, const int32_t* q_lens,
+                                   const int32_t* block_table, const float* previous, const float* lse, float* weights_out,
+                                   int B, int tokens, int n_blocks, int page_size, int max_blocks, int num_heads,
+                                   int kv_num_heads, int head_size, int width, float decay, float scale, float softcap,
+                                   int dtype, void* stream) {
+  return guarded([&]() -> int {
+    return weights(q, k_cache, lens, q_lens, block_table, previous, lse, weights_out, B, tokens, n_blocks, page_size, max_blocks,
+                   num_heads, kv_num_heads, head_size, width, decay, scale, softcap, dtype,
+                   static_cast<cudaStream_t>(stream));
+  });
+}

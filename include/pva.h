@@ -552,6 +552,48 @@ int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* past_lens,
                        int page_size, int head_size, int max_blocks, int dtype, void* stream);
 
 /*
+ * pva_kvcache_weights -- the weight that attention gives to each row of a cache,
+ * added up over the queries: for j < lens[b]
+ *   weights[b][h][j] = decay * previous[b][h][j]
+ *       + sum over tokens t and query heads g of kv head h of exp(s(t, g, j) - L(t, g))
+ * with the scores s of pva_forward (scale, softcap) and L the logarithm of the sum of
+ * exp(s) over the rows that token t sees.
+ *
+ * q       : [B, tokens, num_heads, head_size], rotated as the cached keys are.
+ * q_lens  : device int32 [B], or NULL: sequence b uses its first q_lens[b] tokens
+ *           (NULL: all).  They are its last cache rows: token t sees the rows
+ *           j <= lens[b] - q_lens[b] + t.
+ * k_cache, block_table, page_size, max_blocks : see "Paged caches" above; only keys
+ *           are read.
+ * lens    : device int32 [B]: rows in the cache, q_lens[b] <= lens[b] <= width.
+ * lse     : device f32 [B, tokens, num_heads]: L of every query, as pva_gqa_prefix
+ *           gives it (rows of a shared prefix then have their part of the sum; -inf:
+ *           the query counts nothing), or NULL: L over the sequence's own rows.
+ * previous : device f32 [B, kv_num_heads, width], or NULL (nothing); may be weights:
+ *           a running sum, that fades with decay < 1.
+ * weights : device f32 [B, kv_num_heads, width]; entries at and past lens[b] are left
+ *           as they were.
+ *
+ * Arithmetic: products of dtype (f16/bf16 on tensor cores), all sums f32, in a fixed
+ * order: equal calls give equal bits.  Without lse and with tokens * num_heads /
+ * kv_num_heads <= 16 (f16/bf16) the scores are kept in the workspace: 4 bytes for each
+ * of these query rows and entry of weights.
+ * Limits: head sizes, page sizes and alignment as pva_gqa_tree; num_heads /
+ * kv_num_heads <= 128.
+ * Host errors: null pointers, counts below 1 or out of int32, weights over an input,
+ * and the limits.  Device errors, nothing is then written: a length or token count
+ * out of range (PVA_DEV_KV_LEN), a table entry outside the pool (PVA_DEV_BLOCKS), too
+ * much work for 32-bit indices (PVA_DEV_TOO_MANY), or PVA_DEV_KV_CACHE latched on the
+ * stream: the rejected step before has not written its rows.
+ */
+int pva_kvcache_weights(const void* q, const void* k_cache, const int32_t* lens,
+                        const int32_t* q_lens, const int32_t* block_table, const float* previous,
+                        const float* lse, float* weights, int B, int tokens, int n_blocks,
+                        int page_size, int max_blocks, int num_heads, int kv_num_heads,
+                        int head_size, int width, float decay, float scale, float softcap,
+                        int dtype, void* stream);
+
+/*
  * pva_kvcache_evict -- cuts caches down to the rows that attention has weighed
  * most.  Of the lens[b] rows of sequence b, new_lens[b] = min(lens[b], keep[b]) stay
  * on every (layer, kv head): the first `first` ones, then the last `last` ones, as far

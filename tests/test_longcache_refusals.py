@@ -103,6 +103,28 @@ def test_evict_refusals(lib, kw, code):
     assert pva.pva_last_error() != ""
 
 
+def weights(lib, **kw):
+    a = dict(q=1 << 20, k=1 << 24, lens=1 << 12, used=1 << 13, table=1 << 14, old=1 << 28, lse=1 << 32, to=1 << 36, B=3, T=2, blocks=9,
+             page=16, tw=4, H=8, Hkv=2, d=64, width=60, decay=1.0, scale=0.0, cap=0.0, dtype=2)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.pva_kvcache_weights(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(k=None), -1), (dict(lens=None), -1), (dict(to=None), -1), (dict(B=0), -1), (dict(T=0), -1),
+    (dict(blocks=0), -1), (dict(page=0), -1), (dict(page=8), -2), (dict(page=24), -2), (dict(tw=0), -1), (dict(table=None), -1),
+    (dict(H=7), -1), (dict(Hkv=0), -1), (dict(H=258, Hkv=2), -2), (dict(d=80), -2), (dict(d=31, dtype=0), -2), (dict(d=258, dtype=0), -2),
+    (dict(width=0), -1), (dict(decay=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(cap=float("nan")), -1),
+    (dict(dtype=3), -1), (dict(q=(1 << 20) + 8), -1), (dict(k=(1 << 24) + 2), -1), (dict(to=(1 << 36) + 2), -1),
+    (dict(old=(1 << 28) + 1), -1), (dict(lse=(1 << 32) + 2), -1), (dict(to=(1 << 28) + 4), -1), (dict(to=1 << 32), -1),
+    (dict(to=1 << 12), -1), (dict(to=1 << 14), -1), (dict(B=1 << 20, T=1 << 12), -1), (dict(tw=1 << 28), -1),
+    (dict(blocks=1 << 30, Hkv=4), -1)])
+def test_weights_refusals(lib, kw, code):
+    assert weights(lib, **kw) == code
+    assert pva.pva_last_error() != ""
+
+
 # ---- the binding ------------------------------------------------------------------
 class Calls(list):
     def __getattr__(self, name):
@@ -181,3 +203,23 @@ def test_binding_refuses_evict_arguments(calls, kw):
     assert not calls
     pva.pva_kvcache_evict(**evict_arguments())
     assert [c[0] for c in calls] == ["pva_kvcache_evict"]
+
+
+def weights_arguments():
+    i32, f32 = torch.int32, torch.float32
+    return dict(q=z(3, 2, 8, 64), k_cache=z(9, 2, 16, 64), lens=z(3, dtype=i32), weights=z(3, 2, 60, dtype=f32), num_heads=8,
+                previous=z(3, 2, 60, dtype=f32), lse=z(3, 2, 8, dtype=f32), q_lens=z(3, dtype=i32), block_table=z(3, 4, dtype=i32), stream=9)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=z(3, 2, 512)), dict(num_heads=4), dict(k_cache=z(9, 2, 16, 32)), dict(k_cache=z(9, 2, 16, 64, dtype=torch.float16)),
+    dict(k_cache=z(2, 16, 64)), dict(lens=z(2, dtype=torch.int32)), dict(weights=z(3, 60, dtype=torch.float32)), dict(weights=z(3, 2, 60)),
+    dict(weights=z(3, 4, 60, dtype=torch.float32)), dict(previous=z(3, 2, 61, dtype=torch.float32)), dict(lse=z(3, 2, 4, dtype=torch.float32)),
+    dict(lse=z(3, 2, 8)), dict(q_lens=z(3, dtype=torch.int64)), dict(block_table=z(3, dtype=torch.int32)), dict(stream=None),
+    dict(q=z(3, 8, 2, 64).transpose(1, 2))])
+def test_binding_refuses_weights_arguments(calls, kw):
+    with pytest.raises(pva.PvaError):
+        pva.pva_kvcache_weights(**{**weights_arguments(), **kw})
+    assert not calls
+    pva.pva_kvcache_weights(**weights_arguments())
+    assert [c[0] for c in calls] == ["pva_kvcache_weights"]
