@@ -19,7 +19,8 @@ import torch
 from . import workloads  # noqa: F401  (seeded synthetic inputs)
 
 __all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kvcache",
-           "pva_block_tables", "pva_rope_axes", "pva_norm_rope", "pva_norm_rope_backward", "pva_gqa_tree", "pva_kvcache_accept", "pva_kvcache_weights", "pva_kvcache_evict",
+           "pva_block_tables", "pva_rope_axes", "pva_norm_rope", "pva_norm_rope_backward", "pva_gqa_tree",
+           "pva_gqa_prefix", "pva_kvcache_accept", "pva_kvcache_weights", "pva_kvcache_evict",
            "pva_get_status", "pva_schedule", "pva_status_string", "pva_last_error",
            "pva_release", "pva_version", "pva_profile", "pva_kernel_times", "pva_selftest_wait",
            "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
@@ -31,7 +32,8 @@ PVA_OK, PVA_ERR_INVALID_ARG, PVA_ERR_UNSUPPORTED, PVA_ERR_CUDA, PVA_ERR_OOM = 0,
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 DEV_FLAGS = {"cu_q_start": 0x1, "cu_kv_start": 0x2, "cu_q_order": 0x4, "cu_kv_order": 0x8,
              "too_many": 0x10, "null_tensor": 0x20, "kv_len": 0x40, "kv_cache": 0x80,
-             "wait_timeout": 0x100, "tree": 0x200, "blocks": 0x400, "rope": 0x800}
+             "wait_timeout": 0x100, "tree": 0x200, "blocks": 0x400, "rope": 0x800,
+             "prefix": 0x1000}
 
 _lock = threading.Lock()
 _lib = None
@@ -95,6 +97,9 @@ def load_library(path: str | None = None):
         lib.pva_kvcache_accept.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i64, i, i, i, i, i,
                                            i, vp]
         lib.pva_kvcache_accept.restype = i
+        lib.pva_gqa_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i,
+                                       i, f, f, i, vp]
+        lib.pva_gqa_prefix.restype = i
         lib.pva_kvcache_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f,
                                             f, f, i, vp]
         lib.pva_kvcache_weights.restype = i
@@ -621,6 +626,43 @@ def pva_kvcache_accept(k_cache, v_cache, past_lens, path, path_lens, new_lens, b
         _plain(block_table, "block_table", i32, (B, table_width), at),
         _plain(new_lens, "new_lens", i32, (B,), at), B, width, layers, blocks * Hkv * page * d,
         blocks, Hkv, page, d, table_width, _type_code(k_cache), _stream_on(stream, at)))
+
+
+def pva_gqa_prefix(q, k_cache, v_cache, lens, prefix_lens, out, num_heads: int, kv_num_heads: int,
+                   prefix_start=None, q_lens=None, block_table=None, prefix_table=None, lse=None,
+                   scale: float = 0.0, softcap: float = 0.0, stream=None) -> None:
+    """Attention of q [B, T, H, d] over prefixes that sequences share and then over each
+    one's own rows, lens int32 [B] of them with the tokens (q_lens int32 [B]; None: all)
+    last.  Sequences prefix_start[p] .. prefix_start[p + 1] - 1 (int32 [P + 1]; None: all
+    of one) have prefix p, prefix_lens int32 [P] rows.  Caches [n_blocks, Hkv, page, d]
+    with block_table int32 [B, ...] and prefix_table int32 [P, ...] (None, both: sequence b
+    owns block b, prefix p block B + p); out [B, T, H, d], lse f32 [B, T, H] or None."""
+    _need(q.dim() == 4, "q must be [B, tokens, num_heads, head_size]")
+    B, T, _, d = q.shape
+    H, Hkv = int(num_heads), int(kv_num_heads)
+    dt, i32 = q.dtype, torch.int32
+    _need(k_cache.dim() == 4, "k_cache must be [n_blocks, kv_num_heads, page, head_size]")
+    blocks, _, page, _ = k_cache.shape
+    _need(prefix_lens.dim() == 1, "prefix_lens must be [prefixes]")
+    P = prefix_lens.shape[0]
+    at = _device(q, k_cache, v_cache, lens, prefix_lens, out, prefix_start, q_lens, block_table, prefix_table,
+                 lse)
+    rows, cache = (B, T, H, d), (blocks, Hkv, page, d)
+    _need((block_table is None) == (prefix_table is None), "block_table and prefix_table come together")
+    width = prefix_width = 0
+    if block_table is not None:
+        _need(block_table.dim() == 2 and prefix_table.dim() == 2,
+              "block_table must be [B, max_blocks] and prefix_table [prefixes, max_blocks]")
+        width, prefix_width = block_table.shape[1], prefix_table.shape[1]
+    _check((_lib or load_library()).pva_gqa_prefix(
+        _plain(q, "q", dt, rows, at), _plain(k_cache, "k_cache", dt, cache, at),
+        _plain(v_cache, "v_cache", dt, cache, at), _plain(lens, "lens", i32, (B,), at),
+        _plain(q_lens, "q_lens", i32, (B,), at), _plain(block_table, "block_table", i32, (B, width), at),
+        _plain(prefix_lens, "prefix_lens", i32, (P,), at),
+        _plain(prefix_start, "prefix_start", i32, (P + 1,), at),
+        _plain(prefix_table, "prefix_table", i32, (P, prefix_width), at), _plain(out, "out", dt, rows, at),
+        _plain(lse, "lse", torch.float32, (B, T, H), at), B, T, P, blocks, page, width, prefix_width, H, Hkv, d,
+        float(scale), float(softcap), _type_code(q), _stream_on(stream, at)))
 
 
 def pva_kvcache_weights(q, k_cache, lens, weights, num_heads: int, previous=None, decay: float = 1.0,

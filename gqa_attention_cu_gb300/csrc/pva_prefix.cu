@@ -1,0 +1,336 @@
+// Attention of sequences that share prefixes (pva_gqa_prefix): host side, front end,
+// fp32 attention and the join.
+//
+//   pva_prefix_front_kernel  one CTA per entry (prefix or sequence): bounds and block
+//       table; the last one cuts the line of places (pva_prefix.cuh).
+//   attention                one piece of the line per CTA.
+//   pva_prefix_join_kernel   out and lse of every query row from its parts.
+#include <limits.h>
+#include <math.h>
+
+#include "pva_prefix.cuh"
+#include "pva_tree_f32.cuh"
+
+using namespace pva;
+using namespace pva::host;
+
+namespace pva {
+namespace {
+
+constexpr int kFrontThreads = 128;
+constexpr int kWordArrived = 16, kWordBad = 17;  // of the status block, zero between calls
+
+__global__ void __launch_bounds__(kFrontThreads) pva_prefix_front_kernel(PrefixParams p) {
+  wait_prior_grid();
+  allow_next_grid();
+  __shared__ int s_last;
+  __shared__ long long s_sum[kFrontThreads / 32];
+  const int e = blockIdx.x, tid = threadIdx.x, E = p.P + p.B;
+  const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
+  const bool is_prefix = e < p.P;
+  const int b = is_prefix ? e : e - p.P;
+  const int keys = is_prefix ? p.prefix_keys[b] : p.keys[b];
+  const int32_t* table = is_prefix ? p.prefix_table : p.table;
+  const int width = is_prefix ? p.prefix_blocks : p.max_blocks;
+  uint32_t bad = 0;
+  if (keys < 0 || (long long)keys > (long long)width * p.page) bad = PVA_DEV_KV_LEN;
+  if (!is_prefix) {
+    const int n = tree_nodes(p, b);
+    if (n < 0 || n > p.T || n > keys) bad = PVA_DEV_KV_LEN;
+  } else if (p.prefix_start) {
+    const int first = p.prefix_start[b], end = p.prefix_start[b + 1];
+    if (first < 0 || end < first || end > p.B || (b == 0 && first != 0) || (b == p.P - 1 && end != p.B)) bad |= PVA_DEV_PREFIX;
+  }
+  bool off = false;
+  if (!bad && table)
+    for (int i = tid; i < (keys + p.page - 1) / p.page; i += kFrontThreads)
+      off |= (unsigned)table[(size_t)b * width + i] >= (unsigned)p.n_blocks;
+  if (__syncthreads_or(off)) bad |= PVA_DEV_BLOCKS;
+  if (tid == 0) {
+    if (bad) atomicOr(p.status + kWordBad, bad);
+    __threadfence();
+    s_last = atomicAdd(p.status + kWordArrived, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  const uint32_t found = __ldcg(p.status + kWordBad);
+  long long carry = 0;
+  for (int e0 = 0; e0 < E && !found; e0 += kFrontThreads) {
+    const int i = e0 + tid;
+    const long long x = i < E ? prefix_entry(p, i).per_head(p) * p.Hkv : 0;
+    long long upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if ((tid & 31) >= o) upto += y;
+    }
+    if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
+    __syncthreads();
+    long long before = carry;
+    for (int w = 0; w < kFrontThreads / 32; ++w) {
+      before += w < tid >> 5 ? s_sum[w] : 0;
+      carry += s_sum[w];
+    }
+    if (i < E) p.tile_start[i] = (int)min(before + upto - x, (long long)INT_MAX);
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.status[kWordBad] = 0;  // for the next call
+    p.status[kWordArrived] = 0;
+    const uint32_t all_bad = found | (carry > INT_MAX - 4ll * p.pieces ? PVA_DEV_TOO_MANY : 0u);
+    if (all_bad) atomicOr(p.status, all_bad);
+    const bool ok = !all_bad && !latched;
+    const int all = ok ? (int)carry : 0, even = (all + p.pieces - 1) / p.pieces;
+    p.tile_start[E] = all;
+    p.hdr[0] = ok;
+    p.hdr[1] = all;
+    p.hdr[2] = even > p.min_chunk ? even : p.min_chunk;
+  }
+}
+
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over a row's parts c, the prefix's
+// and then its own, M = max m_c; lse = ln 2 (M + log2 of the lower sum).  One warp per
+// query row: the lanes hold the places and weights of 32 parts at a time, and V
+// channels, V * 32 at once.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) pva_prefix_join_kernel(PrefixParams p) {
+  struct alignas(4 * V) Part { float v[V]; };
+  struct alignas(sizeof(T) * V) Out { T v[V]; };
+  allow_next_grid();
+  wait_prior_grid();
+  if (!p.hdr[0]) return;
+  const int lane = threadIdx.x & 31;
+  const long long at_row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // (token of the batch, head)
+  if (at_row >= (long long)p.B * p.T * p.H) return;
+  const int tok = (int)(at_row / p.H), head = (int)(at_row - (long long)tok * p.H), b = tok / p.T, t = tok - b * p.T;
+  const int h = head / p.G, g = head - h * p.G;
+  const bool used = t < tree_nodes(p, b);
+  const float NEG_INF = __int_as_float(0xff800000);
+  // parts of kind 0 (the prefix) and 1 (own rows): the item's places and pieces
+  int first[2] = {0, 0}, parts[2] = {0, 0}, in_tile[2], per[2], seen[2];
+  long long x0[2];
+  const long long chunk = p.hdr[2];
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const int e = kind ? p.P + b : p.prefix_start ? tree_find(p.prefix_start, p.P, b) : 0;
+    const PrefixEntry entry = prefix_entry(p, e);
+    per[kind] = entry.places(p);
+    if (!used || per[kind] == 0) continue;
+    const int row = (tok - entry.tok0) * p.G + g, qt = row / p.rows;
+    in_tile[kind] = row - qt * p.rows;
+    seen[kind] = entry.seen(p, qt);
+    x0[kind] = p.tile_start[e] + ((long long)h * entry.q_tiles(p) + qt) * per[kind];
+    first[kind] = (int)(x0[kind] / chunk);
+    parts[kind] = (int)((x0[kind] + per[kind] - 1) / chunk) - first[kind] + 1;
+  }
+  // the place of part i, or -1 where a piece holds none of the item's tiles
+  auto place = [&](int i) -> long long {
+    const int kind = i >= parts[0];
+    const int c = kind ? i - parts[0] : i;
+    if (parts[kind] == 1) return p.row_at + (kind ? (long long)p.B * p.T * p.H : 0ll) + at_row;
+    const int piece = first[kind] + c;
+    const long long begin = (long long)piece * chunk - x0[kind];  // places of the item before the piece
+    const int into = begin > 0 ? (int)begin : 0;
+    const int take = (int)(min((long long)per[kind], begin + chunk) - into);
+    int from, to;
+    prefix_tiles(p, into, take, seen[kind], from, to);
+    return from < to ? (long long)tree_slot(piece, into == 0) * p.rows + in_tile[kind] : -1ll;
+  };
+  const int n = parts[0] + parts[1];
+  float m = NEG_INF;
+  for (int i = lane; i < n; i += 32) {
+    const long long at = place(i);
+    if (at >= 0) m = fmaxf(m, p.part_ml[at].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float top = m == NEG_INF ? 0.0f : m;
+  T* out = static_cast<T*>(p.out) + at_row * p.d;
+  float l = 0.0f;
+  for (int d0 = 0; d0 < p.d; d0 += 32 * V) {
+    const int ch = d0 + lane * V;
+    const bool in = ch < p.d;
+    float acc[V];
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float w = 0.0f, wl = 0.0f;
+      long long at = -1;
+      if (i0 + lane < n && (at = place(i0 + lane)) >= 0) {
+        const float2 v = p.part_ml[at];
+        w = exp2f(v.x - top);
+        wl = w * v.y;
+      }
+      const int k = min(32, n - i0);
+#pragma unroll 4
+      for (int i = 0; i < k; ++i) {
+        const long long from = __shfl_sync(0xffffffffu, at, i);
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        l += __shfl_sync(0xffffffffu, wl, i);
+        if (in && from >= 0) {
+          const Part o = *reinterpret_cast<const Part*>(p.part_o + from * p.d + ch);
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(wi, o.v[e], acc[e]);
+        }
+      }
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    if (in) {
+      Out o;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o.v[e] = static_cast<T>(acc[e] * inv);
+      *reinterpret_cast<Out*>(out + ch) = o;
+    }
+  }
+  if (p.lse && lane == 0) p.lse[at_row] = m == NEG_INF ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <typename T, int V>
+cudaError_t launch_join(const PrefixParams& p, cudaStream_t s) {
+  const long long rows = (long long)p.B * p.T * p.H;
+  return launch_dependent(pva_prefix_join_kernel<T, V>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, p);
+}
+
+int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const int32_t* lens, const int32_t* q_lens,
+               const int32_t* block_table, const int32_t* prefix_lens, const int32_t* prefix_start,
+               const int32_t* prefix_table, void* out, float* lse, int B, int T, int P, int n_blocks, int page_size,
+               int max_blocks, int prefix_blocks, int H, int Hkv, int d, float scale, float softcap, int dtype,
+               cudaStream_t stream) {
+  if (!q || !k_cache || !v_cache || !lens || !prefix_lens || !out)
+    return fail(PVA_ERR_INVALID_ARG, "null q, cache, lens, prefix_lens or out pointer");
+  if (B < 1 || T < 1 || P < 1 || n_blocks < 1 || page_size < 1)
+    return fail(PVA_ERR_INVALID_ARG, "need B >= 1, tokens >= 1, prefixes >= 1, n_blocks >= 1, page_size >= 1");
+  if (!prefix_start && P != 1)
+    return fail(PVA_ERR_INVALID_ARG, "several prefixes need prefix_start");
+  if (H < 1 || Hkv < 1 || H % Hkv != 0)
+    return fail(PVA_ERR_INVALID_ARG, "num_heads must be a positive multiple of a positive kv_num_heads");
+  if (dtype != PVA_F32 && dtype != PVA_F16 && dtype != PVA_BF16)
+    return fail(PVA_ERR_INVALID_ARG, "dtype must be 0 (f32), 1 (f16) or 2 (bf16)");
+  if (!isfinite(scale) || !isfinite(softcap))
+    return fail(PVA_ERR_INVALID_ARG, "scale and softcap must be finite");
+  const bool tc = dtype != PVA_F32;
+  if (tc ? d != 64 && d != 96 && d != 128 && d != 192 && d != 256 : d < 2 || d > 256 || d % 2 != 0)
+    return fail(PVA_ERR_UNSUPPORTED,
+                "head_size must be 64, 96, 128, 192 or 256 (f16/bf16), or even and at most 256 (f32)");
+  const int G = H / Hkv;
+  if (G > 128) return fail(PVA_ERR_UNSUPPORTED, "num_heads / kv_num_heads must be at most 128");
+  if ((block_table != nullptr) != (prefix_table != nullptr))
+    return fail(PVA_ERR_INVALID_ARG, "block_table and prefix_table come together");
+  if (block_table) {
+    if (max_blocks < 1 || prefix_blocks < 1) return fail(PVA_ERR_INVALID_ARG, "a table's width must be >= 1");
+    if (page_size < 16 || (page_size & (page_size - 1)) != 0)
+      return fail(PVA_ERR_UNSUPPORTED, "page_size must be a power of two of at least 16");
+  } else {
+    if ((long long)n_blocks != (long long)B + P)
+      return fail(PVA_ERR_INVALID_ARG, "without tables the cache has one block a sequence and then one a prefix");
+    max_blocks = prefix_blocks = 1;
+  }
+  if ((long long)B * T > INT_MAX - 65536 || (long long)B * T * G > INT_MAX / 2 || (long long)B * T * H / 8 > INT_MAX - 8 ||
+      (long long)max_blocks * page_size > INT_MAX - 65536 || (long long)prefix_blocks * page_size > INT_MAX - 65536 ||
+      (long long)n_blocks * Hkv > INT_MAX || (long long)B + P > INT_MAX - 65536)
+    return fail(PVA_ERR_INVALID_ARG, "cache or token extents do not fit in int32");
+  const size_t size = tc ? 2 : 4;
+  const uintptr_t mis = (uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out;
+  if (tc && (mis & 15)) return fail(PVA_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned");
+  if (mis % size || (uintptr_t)lse & 3) return fail(PVA_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+
+  PrefixParams p{};
+  p.keys = lens;
+  p.lens = q_lens;
+  p.table = block_table;
+  p.prefix_keys = prefix_lens;
+  p.prefix_start = prefix_start;
+  p.prefix_table = prefix_table;
+  p.P = P;
+  p.prefix_blocks = prefix_blocks;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.d = d;
+  p.page = page_size;
+  p.max_blocks = max_blocks;
+  p.n_blocks = n_blocks;
+  const float s = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
+  p.negated = tc && s < 0.0f;
+  p.scale = tc ? fabsf(s) : s;
+  p.softcap = fminf(fabsf(softcap), 1e34f);
+  if (p.softcap != 0.0f) {  // as in pva_gqa_tree
+    const double cap = p.softcap, t = fmin(0.25, pow(ldexp(1.0, -14) * 315.0 / 17.0 / cap, 1.0 / 7.0));
+    p.series_to = (float)fmin(t * cap / fabs(p.scale), 1e9);
+  }
+  p.q_parts = 1;
+  const long long R = (long long)B * T * G;
+  p.tile_rows = tc ? G * (kTcRows / G) : R <= 8 ? 8 : R <= 16 ? 16 : 24;
+  p.rows = p.tile_rows;
+  p.item_places = 2;
+  p.bn = tc ? tree_keys(d) : kTreeKeysF32;
+  p.min_chunk = 2;
+  p.q = const_cast<void*>(q);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.out = out;
+  p.lse = lse;
+
+  std::lock_guard<std::mutex> lock(api_mutex());
+  int sms = 0;
+  int rc = sm_count(&sms);
+  if (rc != PVA_OK) return rc;
+  p.pieces = tc ? sms : f32::ctas(p.rows, d) * sms;
+  size_t used = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = used;
+    used += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  p.row_at = 2ll * p.pieces * p.rows;
+  const size_t places = (size_t)p.row_at + 2 * (size_t)B * T * H;
+  const size_t at_hdr = take(32), at_start = take(4 * ((size_t)B + P + 1));
+  const size_t at_o = take(sizeof(float) * places * d), at_ml = take(sizeof(float2) * places);
+  CallContext c;
+  if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
+  p.status = c.status;
+  p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
+  p.tile_start = reinterpret_cast<int32_t*>(c.buf + at_start);
+  p.part_o = reinterpret_cast<float*>(c.buf + at_o);
+  p.part_ml = reinterpret_cast<float2*>(c.buf + at_ml);
+  CUtensorMap tq, tk, tv;
+  if (tc) {
+    const int box = block_table && page_size < p.bn ? page_size : p.bn;
+    const long long planes = (long long)n_blocks * Hkv;
+    if ((rc = get_encoder()) != PVA_OK ||
+        (rc = encode_rows_map(&tq, q, dtype, d, H, (long long)B * T, G, kTcRows / G)) != PVA_OK ||
+        (rc = encode_plane_map(&tk, k_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK ||
+        (rc = encode_plane_map(&tv, v_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK)
+      return rc;
+  }
+  cudaError_t e = launch_dependent(pva_prefix_front_kernel, dim3(P + B), dim3(kFrontThreads), 0, stream, p);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix front-end launch");
+  e = tc ? launch_prefix_tc(p, dtype, tq, tk, tv, stream) : f32::launch<PrefixWork>(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
+  e = dtype == PVA_BF16 ? launch_join<__nv_bfloat16, 4>(p, stream)
+      : dtype == PVA_F16 ? launch_join<__half, 4>(p, stream)
+      // four channels a lane; one where rows of fp32 do not lie on 16-byte boundaries
+      : d % 4 == 0 && ((uintptr_t)out & 15) == 0 ? launch_join<float, 4>(p, stream)
+                                                 : launch_join<float, 1>(p, stream);
+  return e == cudaSuccess ? PVA_OK : cuda_fail(e, "prefix join launch");
+}
+
+}  // namespace
+}  // namespace pva
+
+extern "C" int pva_gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const int32_t* lens,
+                              const int32_t* q_lens, const int32_t* block_table, const int32_t* prefix_lens,
+                              const int32_t* prefix_start, const int32_t* prefix_table, void* out, float* lse, int B,
+                              int tokens, int prefixes, int n_blocks, int page_size, int max_blocks, int prefix_blocks,
+                              int num_heads, int kv_num_heads, int head_size, float scale, float softcap, int dtype,
+                              void* stream) {
+  return guarded([&]() -> int {
+    return gqa_prefix(q, k_cache, v_cache, lens, q_lens, block_table, prefix_lens, prefix_start, prefix_table, out, lse,
+                      B, tokens, prefixes, n_blocks, page_size, max_blocks, prefix_blocks, num_heads, kv_num_heads,
+                      head_size, scale, softcap, dtype, static_cast<cudaStream_t>(stream));
+  });
+}

@@ -203,12 +203,13 @@ struct RowPair {
 // addresses up: the kernels use no other shared memory, whose start then is such
 // a boundary, and refuse to run if it is not.
 constexpr int kHeadBytes = 3 * 1024;
-__device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p) {
+template <typename W>
+__device__ __forceinline__ bool misplaced(const void* smem, const typename W::Params& p) {
   if ((smem_u32(smem) & 1023) == 0) return false;
   if (threadIdx.x == 0) {
     wait_prior_grid();
     atomicOr(p.status, PVA_DEV_WAIT_TIMEOUT);
-    tree_note_cut(p, blockIdx.x, nullptr);
+    W::give_up(p);
   }
   return true;
 }
@@ -216,7 +217,8 @@ __device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p)
 // Softmax of N score columns of this thread's row (TMEM address t_s, keys [k0, k0
 // + N)): P over the first N / 2 of them.  The reference moves where the row's
 // maximum passes it by more than 2^8; alpha is the factor that O then has to be
-// scaled by.  All warps of the rows call; false: a wait was given up.
+// scaled by.  All warps of the rows call; false: a wait was given up.  counts: the
+// row is one of the item's (what the others hold decides nothing).
 //
 // Tiles without a mask are read once and worked on in registers (2048-token
 // chunks of 8 sequences, d = 128, queries rotated before: 1.13 ms, in a loop 1.26
@@ -232,7 +234,7 @@ __device__ __forceinline__ bool misplaced(const void* smem, const TreeParams& p)
 template <typename T, int N, int CAP, typename Row>
 __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowView& view, int past,
                                                 int k0, uint32_t t_s, float s_mul, float cap_mul,
-                                                Row& others, RowState& st, float& alpha) {
+                                                bool counts, Row& others, RowState& st, float& alpha) {
   const float NEG_INF = __int_as_float(0xff800000);
   const bool all = __all_sync(0xffffffffu, view.lo <= k0 && view.hi >= k0 + N);
   float mx = NEG_INF, mn = __int_as_float(0x7f800000), m_eff;
@@ -257,7 +259,7 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
   };
   // a softcap's series has to hold for the warp's own columns
   auto small_scores = [&]() {
-    return CAP && __all_sync(0xffffffffu, mx == NEG_INF || fmaxf(fabsf(mx), fabsf(mn)) <= p.series_to);
+    return CAP && __all_sync(0xffffffffu, !counts || mx == NEG_INF || fmaxf(fabsf(mx), fabsf(mn)) <= p.series_to);
   };
   float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   bool series, done = false;
@@ -410,17 +412,74 @@ struct TileCopies {
   int box, copies;  // rows of one copy, copies side by side
   __device__ __forceinline__ TileCopies(const TreeParams& p, int bn)
       : box(p.table && p.page < bn ? p.page : bn), copies(bn / box) {}
-  __device__ __forceinline__ TileCopy locate(const TreeParams& p, const TreeSegment& s, int bn,
-                                             int j, int lane) const {
+  template <typename W>
+  __device__ __forceinline__ TileCopy locate(const typename W::Params& p, const typename W::Segment& s,
+                                             int bn, int j, int lane) const {
     TileCopy c{false, 0, 0};
     const long long r0 = (long long)j * bn + lane * box;
-    if (lane >= copies || r0 >= s.past + s.n || r0 + box <= s.lo) return c;
+    if (lane >= copies || r0 >= W::total(s) || r0 + box <= s.lo) return c;
     const int in = (int)r0 / p.page;
     c.mine = true;
-    c.block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+    c.block = W::block(p, s, in);
     c.y = (int)r0 - in * p.page;
     return c;
   }
+};
+
+// Where the fp32 kernel leaves a row: its result (ml nullptr), or its unnormalised
+// sums with their maximum and weight.
+struct RowOut {
+  float* o;
+  float2* ml;
+};
+
+// What the kernels ask about their work: pva_gqa_tree's.  (pva_prefix.cuh has another.)
+struct TreeWork {
+  using Params = TreeParams;
+  using Segment = TreeSegment;
+  using Walk = TreeWalk;
+  // keys of the sequence: rows before the step and nodes
+  static __device__ __forceinline__ int total(const Segment& s) { return s.past + s.n; }
+  // the cache block of the sequence's in-th page
+  static __device__ __forceinline__ int block(const Params& p, const Segment& s, int in) {
+    return p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+  }
+  // bytes of 64 columns of a query tile, and their copy (tile y of the item, part of the queries)
+  static __device__ __forceinline__ uint32_t q_bytes(const Params&) { return kTcRows * 128; }
+  static __device__ __forceinline__ void load_q(const Params& p, const Segment& s, int y, int part,
+                                                void* dst, const CUtensorMap* map, uint64_t* bar, int c) {
+    tma_load_3d(dst, map, bar, c * 64, s.t * p.rows + y * kTcRows, (part * p.B + s.b) * p.Hkv + s.h);
+  }
+  static __device__ __forceinline__ uint32_t negate(const Params&) { return 0u; }
+  // the query row (of the sequence's on this kv head) that MMA row r of tile y is
+  static __device__ __forceinline__ int row(const Params& p, const Segment& s, int y, int r) {
+    return s.t * p.rows + y * kTcRows + r;
+  }
+  static __device__ __forceinline__ bool owns(const Params& p, const Segment& s, int r, int row) {
+    return row < s.n * p.G;
+  }
+  // rows of no node are zeros beside others (RopeStep) and so are their scores
+  static __device__ __forceinline__ bool counts(bool) { return true; }
+  static __device__ __forceinline__ RowView view(const Params& p, const Segment& s, int node) {
+    return row_view(p, s, node);
+  }
+  template <typename T, int D>
+  static __device__ __forceinline__ void store(const Params& p, const Segment& s, uint32_t t_o, bool own,
+                                               int row, int node, Columns cols, float m, float l) {
+    store_row<T, D>(p, s, t_o, own, row, node, cols, m, l);
+  }
+  // fp32: a query row, and where its result goes (row lr of the item)
+  static __device__ __forceinline__ const float* q_row(const Params& p, const Segment& s, int row) {
+    return static_cast<const float*>(p.q) + (((size_t)s.b * p.Hkv + s.h) * p.T * p.G + row) * p.d;
+  }
+  static __device__ __forceinline__ RowOut row_out(const Params& p, const Segment& s, int row, int lr) {
+    const int node = row / p.G, g = row - node * p.G;
+    if (s.slot < 0)
+      return {static_cast<float*>(p.out) + (((size_t)s.b * p.T + node) * p.H + (size_t)s.h * p.G + g) * p.d, nullptr};
+    const size_t at = (size_t)s.slot * p.rows + lr;
+    return {p.part_o + at * p.d, p.part_ml + at};
+  }
+  static __device__ __forceinline__ void give_up(const Params& p) { tree_note_cut(p, blockIdx.x, nullptr); }
 };
 
 }  // namespace tile

@@ -67,6 +67,7 @@ typedef enum { PVA_F32 = 0, PVA_F16 = 1, PVA_BF16 = 2 } pva_dtype;
 #define PVA_DEV_TREE 0x200u   /* pva_gqa_tree, pva_kvcache_accept: a bad tree, node count or path */
 #define PVA_DEV_BLOCKS 0x400u /* a block table entry outside the pool; pva_block_tables: see there */
 #define PVA_DEV_ROPE 0x800u   /* a rotary position outside the tables, or a slot outside the cache */
+#define PVA_DEV_PREFIX 0x1000u /* pva_gqa_prefix: prefix_start is no partition of the batch */
 
 /*
  * pva_forward -- out = attention(q, k, v) over packed sequences.
@@ -550,6 +551,53 @@ int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* past_lens,
                        const int32_t* block_table, int32_t* new_lens, int B, int path_width,
                        int layers, int64_t layer_stride, int n_blocks, int kv_num_heads,
                        int page_size, int head_size, int max_blocks, int dtype, void* stream);
+
+/*
+ * pva_gqa_prefix -- attention of a batch whose sequences share long prefixes (a
+ * system prompt, a document, the common part of samples): every sequence sees the
+ * rows of its prefix and then its own, and a prefix's keys and values are read for
+ * all of its sequences together.  The result is that of attention over the rows one
+ * after another.  Nothing is appended or rotated: the cache holds the tokens' own rows
+ * already (pva_norm_rope, pva_rope_axes), and q is rotated as they are.
+ *
+ * q       : [B, tokens, num_heads, head_size]
+ * q_lens  : device int32 [B], or NULL: sequence b uses its first q_lens[b] tokens
+ *           (NULL: all).  They are its last rows: token t sees its prefix and its own
+ *           rows j <= lens[b] - q_lens[b] + t.  What the others hold does not matter;
+ *           their rows of out are zeros, of lse -inf.
+ * k_cache, v_cache, block_table, page_size, max_blocks : see "Paged caches" above, for
+ *           the sequences' own rows.
+ * lens    : device int32 [B]: own rows in the cache, the tokens' among them
+ *           (q_lens[b] <= lens[b]).
+ * prefix_start : device int32 [prefixes + 1]: sequences prefix_start[p] ..
+ *           prefix_start[p + 1] - 1 have prefix p; starts at 0, does not fall, ends at
+ *           B.  NULL: one prefix for the whole batch.
+ * prefix_lens : device int32 [prefixes]: rows of each prefix; 0 is none.
+ * prefix_table : device int32 [prefixes, prefix_blocks]: the prefixes' blocks, in the
+ *           same pool; NULL where block_table is NULL: the pool then has B + prefixes
+ *           blocks, and prefix p owns block B + p alone.
+ * out     : [B, tokens, num_heads, head_size] (every row written).
+ * lse     : device f32 [B, tokens, num_heads], or NULL: the natural logarithm of the
+ *           sum of exp(score) over what the row sees (pva_kvcache_weights takes it).
+ * scale, softcap, dtype, stream : as pva_forward.
+ *
+ * Arithmetic, limits and alignment as pva_gqa_tree without a rotation, and num_heads /
+ * kv_num_heads <= 128.  Results do not depend on timing.  A value row that some token
+ * sees should be finite: an infinity or NaN there can reach its other tokens, and in a
+ * prefix all of its sequences.
+ * Host errors: null pointers, counts below 1 or out of int32, and the limits.  Device
+ * errors, out and lse are then left as they were: a length or token count out of range
+ * (PVA_DEV_KV_LEN), a bad prefix_start (PVA_DEV_PREFIX), a needed table entry outside
+ * the pool (PVA_DEV_BLOCKS), too much work for 32-bit indices (PVA_DEV_TOO_MANY), or
+ * PVA_DEV_KV_CACHE latched on the stream: the rejected step before has not written its
+ * rows.
+ */
+int pva_gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const int32_t* lens,
+                   const int32_t* q_lens, const int32_t* block_table, const int32_t* prefix_lens,
+                   const int32_t* prefix_start, const int32_t* prefix_table, void* out, float* lse,
+                   int B, int tokens, int prefixes, int n_blocks, int page_size, int max_blocks,
+                   int prefix_blocks, int num_heads, int kv_num_heads, int head_size, float scale,
+                   float softcap, int dtype, void* stream);
 
 /*
  * pva_kvcache_weights -- the weight that attention gives to each row of a cache,

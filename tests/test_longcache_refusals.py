@@ -125,6 +125,27 @@ def test_weights_refusals(lib, kw, code):
     assert pva.pva_last_error() != ""
 
 
+def prefix(lib, **kw):
+    a = dict(q=1 << 20, k=1 << 24, v=1 << 28, lens=1 << 12, used=None, table=1 << 13, plens=1 << 14, start=1 << 15, ptable=1 << 16,
+             out=1 << 32, lse=1 << 36, B=3, T=2, P=2, blocks=9, page=16, tw=4, pw=5, H=8, Hkv=2, d=64, scale=0.0, cap=0.0, dtype=2)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return lib.pva_gqa_prefix(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(lens=None), -1), (dict(plens=None), -1), (dict(out=None), -1),
+    (dict(B=0), -1), (dict(T=0), -1), (dict(P=0), -1), (dict(blocks=0), -1), (dict(page=0), -1), (dict(page=8), -2), (dict(page=40), -2),
+    (dict(start=None), -1), (dict(table=None), -1), (dict(ptable=None), -1), (dict(table=None, ptable=None), -1), (dict(tw=0), -1),
+    (dict(pw=0), -1), (dict(H=7), -1), (dict(Hkv=0), -1), (dict(H=258), -2), (dict(d=72), -2), (dict(d=31, dtype=0), -2),
+    (dict(d=258, dtype=0), -2), (dict(dtype=3), -1), (dict(scale=float("nan")), -1), (dict(cap=float("inf")), -1),
+    (dict(q=(1 << 20) + 8), -1), (dict(out=(1 << 32) + 2), -1), (dict(dtype=0, k=(1 << 24) + 2), -1), (dict(lse=(1 << 36) + 2), -1),
+    (dict(B=1 << 20, T=1 << 12), -1), (dict(tw=1 << 28), -1), (dict(pw=1 << 28), -1), (dict(blocks=1 << 30, Hkv=4, H=8), -1)])
+def test_prefix_refusals(lib, kw, code):
+    assert prefix(lib, **kw) == code
+    assert pva.pva_last_error() != ""
+
+
 # ---- the binding ------------------------------------------------------------------
 class Calls(list):
     def __getattr__(self, name):
@@ -223,3 +244,25 @@ def test_binding_refuses_weights_arguments(calls, kw):
     assert not calls
     pva.pva_kvcache_weights(**weights_arguments())
     assert [c[0] for c in calls] == ["pva_kvcache_weights"]
+
+
+def prefix_arguments():
+    i32, f32 = torch.int32, torch.float32
+    return dict(q=z(3, 2, 8, 64), k_cache=z(9, 2, 16, 64), v_cache=z(9, 2, 16, 64), lens=z(3, dtype=i32), prefix_lens=z(2, dtype=i32),
+                out=z(3, 2, 8, 64), num_heads=8, kv_num_heads=2, prefix_start=z(3, dtype=i32), q_lens=z(3, dtype=i32),
+                block_table=z(3, 4, dtype=i32), prefix_table=z(2, 5, dtype=i32), lse=z(3, 2, 8, dtype=f32), stream=9)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=z(3, 2, 512)), dict(num_heads=4), dict(kv_num_heads=4), dict(k_cache=z(2, 16, 64)), dict(v_cache=z(9, 2, 16, 32)),
+    dict(lens=z(3)), dict(prefix_lens=z(2, 1, dtype=torch.int32)), dict(prefix_lens=z(3, dtype=torch.int32)),
+    dict(prefix_start=z(2, dtype=torch.int32)), dict(prefix_start=z(3, dtype=torch.int64)), dict(q_lens=z(2, dtype=torch.int32)),
+    dict(block_table=None), dict(prefix_table=None), dict(prefix_table=z(2, dtype=torch.int32)),
+    dict(prefix_table=z(3, 5, dtype=torch.int32)), dict(block_table=z(2, 4, dtype=torch.int32)), dict(out=z(3, 2, 8, 32)),
+    dict(out=z(3, 2, 8, 64, dtype=torch.float32)), dict(lse=z(3, 2, 8)), dict(lse=z(3, 8, 2, dtype=torch.float32)), dict(stream=None)])
+def test_binding_refuses_prefix_arguments(calls, kw):
+    with pytest.raises(pva.PvaError):
+        pva.pva_gqa_prefix(**{**prefix_arguments(), **kw})
+    assert not calls
+    pva.pva_gqa_prefix(**prefix_arguments())
+    assert [c[0] for c in calls] == ["pva_gqa_prefix"]
