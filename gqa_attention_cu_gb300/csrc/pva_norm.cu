@@ -10,8 +10,18 @@
 // Memory is the floor: each row is read once and written once (twice read in the
 // gradient).  A row lies across a few lanes, 16 bytes of each of the two halves that
 // turn together per lane, so that its sums take log2(lanes) shuffles and the pairs
-// meet in one thread; a warp works on a token's rows by itself, without a barrier,
-// with the token's cos and sin and the gains in registers.
+// meet in one thread.  A warp works on a token's rows by itself: its lanes copy their
+// own packs into their own places of shared memory some row groups ahead
+// (asynchronously, and so across tokens, without registers to hold them and without a
+// barrier), a token's cos and sin are fetched a pair a lane one token ahead, and gain
+// and rotation are one matrix (ca, sb; sa, cb) per pair, made once a token.
+//
+// 16,001 tokens with 32 + 8 + 8 head rows of 128 bf16, keys and values to the cache: 77
+// us, 5.1 TB/s of 394 MB (59 at the copy rate); the gradient of 8190 tokens of 32 + 8
+// rows: 61 us, 4.1 TB/s of 252 MB (38).  What bounds them is instructions beside few
+// warps: 257 a row group of the forward form, a third of them arithmetic, at 16 warps
+// an SM (5 CTAs an SM instead of 4, with 96 registers: 94 us; rows held in registers
+// instead of shared memory: 93 us).  Smaller calls: launch and the caller's side.
 #include <limits.h>
 #include <math.h>
 
@@ -49,49 +59,55 @@ struct NormStep {
   uint32_t* status;
 };
 
+constexpr int kNormCtas = 4, kBackCtas = 3;  // CTAs an SM holds
 constexpr int kNormThreads = 128;
 constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kMaxHalf = 128;  // pairs of a row
+constexpr int kFly = 4, kBackFly = 3;  // row groups whose copies are in flight
 
-// Where the two packs of unit u of a row lie (2 VEC dims of it).
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// VEC floats as pairs for the packed instructions (VEC 1: the second is zero).
 template <int VEC>
-struct Unit {
-  int d0, d1;
-  bool turned;
-  __device__ __forceinline__ Unit(const RopeTable& rt, int u) {
-    const int half = rt.rot / 2;
-    turned = u * VEC < half;
-    if (!turned) {
-      d0 = rt.rot + (u - half / VEC) * 2 * VEC;
-      d1 = d0 + VEC;
-    } else if (rt.interleaved) {
-      d0 = u * 2 * VEC;
-      d1 = d0 + VEC;
-    } else {
-      d0 = u * VEC;
-      d1 = d0 + half;
-    }
+struct Floats {
+  static constexpr int N = (VEC + 1) / 2;
+  float2 v[N];
+  __device__ __forceinline__ float& operator[](int e) { return e % 2 ? v[e / 2].y : v[e / 2].x; }
+  __device__ __forceinline__ float operator[](int e) const { return e % 2 ? v[e / 2].y : v[e / 2].x; }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(0.0f, 0.0f);
   }
 };
 
-// The pairs of a unit, as floats.
-template <typename T, int VEC>
+// The first and second members of a unit's pairs, as floats.
+template <typename T, int VEC, bool NB>
 struct Pairs {
-  float a[VEC], b[VEC];
-  __device__ __forceinline__ void take(Pack<T, VEC> x, Pack<T, VEC> y, bool neighbours) {
-    if (neighbours) split_pairs(x, y);
+  Floats<VEC> a, b;
+  __device__ __forceinline__ void take(Pack<T, VEC> x, Pack<T, VEC> y) {
+    if (NB) split_pairs(x, y);
+    if (VEC == 1) a.clear(), b.clear();
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       a[e] = load_f(x.v[e]);
       b[e] = load_f(y.v[e]);
     }
   }
-  __device__ __forceinline__ void give(Pack<T, VEC>& x, Pack<T, VEC>& y, bool neighbours) const {
+  __device__ __forceinline__ void give(Pack<T, VEC>& x, Pack<T, VEC>& y) const {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       x.v[e] = round_to<T>(a[e]);
       y.v[e] = round_to<T>(b[e]);
     }
-    if (neighbours) join_pairs(x, y);
+    if (NB) join_pairs(x, y);
   }
 };
 
@@ -103,112 +119,130 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// What a lane keeps of a token: cos and sin of its pairs.
-template <int VEC, int U>
-struct Turn {
-  float c[U][VEC], s[U][VEC];
+// What a warp works with: TPR lanes a row, U units of 2 VEC dims a lane, and a
+// token's cos and sin in shared memory.  Lane a < n_axes reads the position on axis
+// a, lane kMaxAxes the slot; the entries of the pairs are fetched a pair a lane, one
+// token ahead of the rows.
+struct NormShared {
+  float gain[2][2 * kMaxHalf];             // of q and k, by dim
+  float2 cs[kNormWarps][kMaxHalf];         // of the warps' tokens
 };
 
-// Positions of token tok on all axes, in bounds or not (the same answer in every lane).
-__device__ __forceinline__ bool token_position(const NormStep& p, int tok, int64_t (&at)[kMaxAxes]) {
-  bool ok = true;
-  if (p.rt.rot) {
-#pragma unroll
-    for (int a = 0; a < kMaxAxes; ++a) {
-      at[a] = 0;
-      if (a < p.rt.n_axes) {
-        at[a] = p.pos[(size_t)a * p.tokens + tok];
-        ok = ok && at[a] >= 0 && at[a] < p.rt.rows;
-      }
-    }
-  }
-  return ok;
-}
-
-// TPR lanes a row, U units of 2 VEC dims a lane.
-template <typename T, int VEC, int TPR, int U>
+// NB: pairs of neighbouring dims (also of those that are not turned).
+template <typename T, int VEC, int TPR, int U, bool NB>
 struct NormLane {
   using P = Pack<T, VEC>;
-  int sub, group;      // lane within the row, row within the warp's 32 / TPR
+  static constexpr int FETCH = kMaxHalf / 32;  // pairs a lane fetches
+  int group;           // row within the warp's 32 / TPR
   bool in[U];          // the unit exists
-  int d0[U], d1[U];
-  bool turned[U], neighbours[U];
-  uint32_t axes[U];    // two bits a pair
+  int d0[U], d1[U], pair[U];
+  bool turned[U];
+  uint32_t axes;       // of the pairs lane, lane + 32, ..., two bits each
   __device__ __forceinline__ NormLane(const NormStep& p) {
-    const int lane = threadIdx.x & 31;
-    sub = lane % TPR;
+    const int lane = threadIdx.x & 31, sub = lane % TPR, half = p.rt.rot / 2;
     group = lane / TPR;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int u = sub + i * TPR;
-      const Unit<VEC> unit(p.rt, u);
       in[i] = u < p.d / (2 * VEC);
-      d0[i] = in[i] ? unit.d0 : 0;
-      d1[i] = in[i] ? unit.d1 : VEC;
-      turned[i] = in[i] && unit.turned;
-      neighbours[i] = p.rt.interleaved && turned[i];
-      axes[i] = 0;
-      if (turned[i])
+      turned[i] = in[i] && u * VEC < half;
+      pair[i] = u * VEC;
+      d0[i] = !in[i] ? 0 : !turned[i] ? p.rt.rot + (u - half / VEC) * 2 * VEC : NB ? u * 2 * VEC : u * VEC;
+      d1[i] = turned[i] && !NB ? d0[i] + half : d0[i] + VEC;
+    }
+    axes = 0;
+    for (int f = 0; f < FETCH; ++f)
+      if (lane + 32 * f < half) axes |= (uint32_t)axis_of_pair(p.rt, lane + 32 * f) << (2 * f);
+  }
+  // lane a < n_axes: the token's position on axis a; lane kMaxAxes: its slot
+  __device__ __forceinline__ int64_t fetch_info(const NormStep& p, long long tok) const {
+    const int lane = threadIdx.x & 31;
+    int64_t x = lane == kMaxAxes ? -1 : 0;
+    if (tok < p.tokens) {
+      if (p.rt.rot && lane < p.rt.n_axes) x = p.pos[(size_t)lane * p.tokens + tok];
+      if (p.slots && lane == kMaxAxes) x = p.slots[tok];
+    }
+    return x;
+  }
+  // all positions on the tables and the slot in the cache
+  __device__ __forceinline__ bool fine(const NormStep& p, int64_t info) const {
+    const int lane = threadIdx.x & 31;
+    const bool bad = lane == kMaxAxes ? info < -1 || info >= p.n_slots
+                                      : p.rt.rot && lane < p.rt.n_axes && (info < 0 || info >= p.rt.rows);
+    return !__any_sync(0xffffffffu, bad);
+  }
+  struct Entries { float2 cs[FETCH]; };
+  __device__ __forceinline__ Entries fetch_entries(const NormStep& p, int64_t info, float sign) const {
+    const int lane = threadIdx.x & 31, half = p.rt.rot / 2;
+    Entries x;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) axes[i] |= (uint32_t)axis_of_pair(p.rt, u * VEC + e) << (2 * e);
+    for (int f = 0; f < FETCH; ++f) {
+      x.cs[f] = make_float2(1.0f, 0.0f);
+      if (32 * f >= half) continue;
+      const int64_t at = __shfl_sync(0xffffffffu, info, axes >> (2 * f) & 3);
+      if (lane + 32 * f < half && at >= 0 && at < p.rt.rows) {
+        const int64_t i = at * half + lane + 32 * f;
+        x.cs[f].x = table_at<false>(p.rt.cos, i, p.rt.is_f16);
+        x.cs[f].y = sign * table_at<false>(p.rt.sin, i, p.rt.is_f16);
+      }
+    }
+    return x;
+  }
+  __device__ __forceinline__ void share(const NormStep& p, const Entries& x, float2* to) const {
+    const int lane = threadIdx.x & 31, half = p.rt.rot / 2;
+    __syncwarp();
+#pragma unroll
+    for (int f = 0; f < FETCH; ++f)
+      if (lane + 32 * f < half) to[lane + 32 * f] = x.cs[f];
+    __syncwarp();
+  }
+  __device__ __forceinline__ void turn(const float2* cs, int i, Floats<VEC>& c, Floats<VEC>& s) const {
+    if (VEC == 1) c.clear(), s.clear();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float2 x = turned[i] ? cs[pair[i] + e] : make_float2(1.0f, 0.0f);
+      c[e] = x.x;
+      s[e] = x.y;
     }
   }
-  // cos and sin of a token (sign -1: the rotation's transpose)
-  __device__ __forceinline__ void turn(const NormStep& p, const int64_t (&at)[kMaxAxes], float sign,
-                                       Turn<VEC, U>& t) const {
-    const int half = p.rt.rot / 2;
+  // where the e-th pair's members lie in the row
+  __device__ __forceinline__ int first(int i, int e) const { return NB ? d0[i] + 2 * e : d0[i] + e; }
+  __device__ __forceinline__ int second(int i, int e) const { return NB ? d0[i] + 2 * e + 1 : d1[i] + e; }
+  __device__ __forceinline__ void gains(const float* w, int i, Floats<VEC>& a, Floats<VEC>& b) const {
+    if (VEC == 1) a.clear(), b.clear();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      a[e] = w[first(i, e)];
+      b[e] = w[second(i, e)];
+    }
+  }
+  // This lane's packs of a row on their way to its own place in shared memory (16
+  // bytes asynchronously, single elements at once); zeros where there is no row.
+  __device__ __forceinline__ void copy_row(const T* src, bool there, P (*to)[U][32]) const {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int u = sub + i * TPR;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        t.c[i][e] = 1.0f;
-        t.s[i][e] = 0.0f;
-        if (turned[i]) {
-          const int a = axes[i] >> (2 * e) & 3;
-          const int64_t row = a == 0 ? at[0] : a == 1 ? at[1] : a == 2 ? at[2] : at[3];
-          const int64_t k = row * half + u * VEC + e;
-          t.c[i][e] = table_at<false>(p.rt.cos, k, p.rt.is_f16);
-          t.s[i][e] = sign * table_at<false>(p.rt.sin, k, p.rt.is_f16);
+      for (int half = 0; half < 2; ++half) {
+        const T* from = src + (half ? d1[i] : d0[i]);
+        P* dst = &to[half][i][lane];
+        const bool valid = there && in[i];
+        if constexpr (sizeof(P) == 16) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(from),
+                       "r"(valid ? 16 : 0)
+                       : "memory");
+        } else {
+          P x;
+          x.v[0] = valid ? *from : round_to<T>(0.0f);
+          *dst = x;
         }
       }
     }
   }
-  __device__ __forceinline__ void gains(const NormStep& p, int which, Pairs<T, VEC> (&w)[U]) const {
+  __device__ __forceinline__ void take_row(const P (*from)[U][32], Pairs<T, VEC, NB> (&v)[U]) const {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int da = neighbours[i] ? d0[i] + 2 * e : d0[i] + e;
-        const int db = neighbours[i] ? d0[i] + 2 * e + 1 : d1[i] + e;
-        float a = 1.0f, b = 1.0f;
-        if (p.w[which] && in[i]) {
-          if (p.w_f32) {
-            a = static_cast<const float*>(p.w[which])[da];
-            b = static_cast<const float*>(p.w[which])[db];
-          } else {
-            a = load_f(static_cast<const T*>(p.w[which])[da]);
-            b = load_f(static_cast<const T*>(p.w[which])[db]);
-          }
-          a += p.offset;
-          b += p.offset;
-        }
-        w[i].a[e] = a;
-        w[i].b[e] = b;
-      }
-    }
-  }
-  __device__ __forceinline__ void load_row(const T* src, bool there, P (&x)[U], P (&y)[U]) const {
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (there && in[i]) {
-        x[i] = *reinterpret_cast<const P*>(src + d0[i]);
-        y[i] = *reinterpret_cast<const P*>(src + d1[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[i].v[e] = y[i].v[e] = round_to<T>(0.0f);
-      }
-    }
+    for (int i = 0; i < U; ++i) v[i].take(from[0][i][lane], from[1][i][lane]);
   }
   __device__ __forceinline__ void store_row(T* dst, const P (&x)[U], const P (&y)[U]) const {
 #pragma unroll
@@ -220,193 +254,339 @@ struct NormLane {
   }
 };
 
-// Rows of one warp pass: 32 / TPR head rows; FLY passes have their loads in flight.
-template <typename T, int VEC, int TPR, int U, int FLY>
-__global__ void __launch_bounds__(kNormThreads) pva_norm_rope_kernel(NormStep p) {
+// The gains of q and k as f32 in shared memory.
+template <typename T>
+__device__ __forceinline__ void share_gains(const NormStep& p, NormShared& sh) {
+  for (int i = threadIdx.x; i < 2 * p.d; i += kNormThreads) {
+    const int which = i >= p.d, c = i - which * p.d;
+    const void* w = p.w[which];
+    sh.gain[which][c] = !w        ? 1.0f
+                        : p.w_f32 ? static_cast<const float*>(w)[c] + p.offset
+                                  : load_f(static_cast<const T*>(w)[c]) + p.offset;
+  }
+  __syncthreads();
+}
+
+// The row groups (32 / TPR rows of q, k or v of a token) that a warp works on, one
+// after another: items are (token, part of its rows), a warp takes every so many.
+// Within a kind of rows only `row` moves on.
+struct NormCursor {
+  long long item;
+  int tok, which, row, n;  // this lane's row, of n
+  int base;                // the warp's first row of the group
+};
+
+// KINDS of rows from kind FIRST on: 0 q, 1 k, 2 v.
+template <int RPP>
+struct NormWalk {
+  long long items, stride;
+  int step, parts, group, first, kinds, n0, n1, n2;
+  __device__ __forceinline__ NormWalk(const NormStep& p, int group_, int first_, int kinds_)
+      : items((long long)p.tokens * p.parts), stride((long long)gridDim.x * kNormWarps), step(p.parts * RPP),
+        parts(p.parts), group(group_), first(first_), kinds(kinds_), n0(p.heads[0]), n1(p.heads[1]),
+        n2(p.v ? p.heads[1] : 0) {}
+  __device__ __forceinline__ int rows_of(int which) const { return which == 0 ? n0 : which == 1 ? n1 : n2; }
+  __device__ __forceinline__ bool more(const NormCursor& c) const { return c.item < items; }
+  // the first group of kind c.which, or of a later one, that has rows
+  __device__ __forceinline__ void settle(NormCursor& c) const {
+    while (true) {
+      c.tok = parts == 1 ? (int)c.item : (int)(c.item / parts);
+      c.base = (int)(c.item - (long long)c.tok * parts) * RPP;
+      c.row = c.base + group;
+      c.n = rows_of(c.which);
+      if (c.base < c.n || !more(c)) return;
+      if (++c.which == first + kinds) {
+        c.which = first;
+        c.item += stride;
+      }
+    }
+  }
+  __device__ __forceinline__ NormCursor begin() const {
+    NormCursor c;
+    c.item = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+    c.which = first;
+    settle(c);
+    return c;
+  }
+  // on to the next group; false: of another kind or token
+  __device__ __forceinline__ bool next(NormCursor& c) const {
+    c.base += step;
+    c.row += step;
+    if (c.base < c.n) return true;
+    if (++c.which == first + kinds) {
+      c.which = first;
+      c.item += stride;
+    }
+    settle(c);
+    return false;
+  }
+};
+
+// FLY row groups have their copies in flight; a lane reads only what it copied.
+template <typename T, int VEC, int TPR, int U, int FLY, bool NB>
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) pva_norm_rope_kernel(NormStep p) {
   using P = Pack<T, VEC>;
-  constexpr int RPP = 32 / TPR;
+  constexpr int RPP = 32 / TPR, N = Floats<VEC>::N;
+  __shared__ NormShared sh;
+  __shared__ P stage[kNormWarps][FLY][2][U][32];
   allow_next_grid();
   wait_prior_grid();
-  const NormLane<T, VEC, TPR, U> me(p);
-  const int lane = threadIdx.x & 31;
-  const int nq = p.heads[0], nk = p.heads[1], nv = p.v ? nk : 0;
-  const long long items = (long long)p.tokens * p.parts;
-  const long long stride = (long long)gridDim.x * kNormWarps;
-  for (long long item = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5); item < items;
-       item += stride) {
-    const int tok = (int)(item / p.parts), part = (int)(item - (long long)tok * p.parts);
-    int64_t at[kMaxAxes];
-    bool ok = token_position(p, tok, at);
-    int64_t slot = -1;
-    if (p.k_cache) {
-      slot = p.slots[tok];
-      ok = ok && slot >= -1 && slot < p.n_slots;
+  const NormLane<T, VEC, TPR, U, NB> me(p);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const NormWalk<RPP> walk(p, me.group, 0, 3);
+  NormCursor ahead = walk.begin(), at = ahead;
+  // where the group's rows come from, at its lane's row
+  auto source = [&](const NormCursor& c) {
+    const T* x = static_cast<const T*>(c.which == 0 ? p.x[0] : c.which == 1 ? p.x[1] : p.v);
+    const long long st = c.which == 0 ? p.x_stride[0] : c.which == 1 ? p.x_stride[1] : p.v_stride;
+    return x + c.tok * st + (size_t)c.row * p.d;
+  };
+  const T* src = walk.more(ahead) ? source(ahead) : nullptr;
+  const int src_step = walk.step * p.d;
+  auto copy = [&](int slot) {
+    if (walk.more(ahead)) {
+      me.copy_row(src, ahead.row < ahead.n, stage[warp][slot]);
+      if (walk.next(ahead))
+        src += src_step;
+      else if (walk.more(ahead))
+        src = source(ahead);
     }
-    if (!ok) {
-      if (lane == 0) atomicOr(p.status, PVA_DEV_ROPE);
-      continue;
-    }
-    const int64_t block = slot < 0 ? 0 : slot / p.page;
-    const size_t cache_row = slot < 0 ? 0 : (size_t)(slot - block * p.page);
-    Turn<VEC, U> t;
-    me.turn(p, at, 1.0f, t);
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const int n = p.heads[which];
-      if (n == 0) continue;
-      Pairs<T, VEC> w[U];
-      me.gains(p, which, w);
-      const T* src = static_cast<const T*>(p.x[which]) + (size_t)tok * p.x_stride[which];
-      T* out = static_cast<T*>(p.out[which]);
-      if (out) out += (size_t)tok * p.out_stride[which];
-      for (int r0 = part * RPP * FLY; r0 < n; r0 += p.parts * RPP * FLY) {
-        P x[FLY][U], y[FLY][U];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-        for (int f = 0; f < FLY; ++f) {
-          const int row = r0 + f * RPP + me.group;
-          me.load_row(src + (size_t)row * p.d, row < n, x[f], y[f]);
+  for (int f = 0; f < FLY - 1; ++f) copy(f);
+  int64_t next_info = me.fetch_info(p, walk.more(at) ? at.tok : p.tokens);
+  auto entries = me.fetch_entries(p, next_info, 1.0f);
+  share_gains<T>(p, sh);
+  int slot = 0;
+  bool fresh = true, ok = false;  // fresh: another kind of rows, or another token
+  long long item = -1;
+  int64_t where = -1;
+  size_t cache_row = 0;  // of head 0
+  T *out = nullptr, *cache = nullptr;
+  const int out_step = walk.step * p.d;
+  const long long cache_step = (long long)walk.step * p.page * p.d;
+  // gain and rotation in one: (a, b) -> r (ca a - sb b, sa a + cb b)
+  Floats<VEC> ca[U], sb[U], sa[U], cb[U];
+  while (walk.more(at)) {
+    copy(slot == 0 ? FLY - 1 : slot - 1);
+    const bool arrived = at.item != item;
+    if (fresh) {
+      if (arrived) {  // a new token: its entries, and the next one's positions on their way
+        item = at.item;
+        const int64_t info = next_info;
+        me.share(p, entries, sh.cs[warp]);
+        // (every item has rows: the next one lies a stride ahead)
+        next_info = me.fetch_info(p, (item + walk.stride) / p.parts);
+        ok = me.fine(p, info);
+        where = __shfl_sync(0xffffffffu, info, kMaxAxes);
+        if (!ok && lane == 0) atomicOr(p.status, PVA_DEV_ROPE);
+        if (ok && where >= 0) {
+          const int64_t block = p.n_slots >> 32 ? where / p.page : (int64_t)((uint32_t)where / (uint32_t)p.page);
+          cache_row = ((size_t)block * walk.n1 * p.page + (size_t)(where - block * p.page)) * p.d;
         }
+      }
+      const int which = at.which;
+      out = which == 2 ? nullptr : static_cast<T*>(which ? p.out[1] : p.out[0]);
+      if (out) out += at.tok * (which ? p.out_stride[1] : p.out_stride[0]) + (size_t)at.row * p.d;
+      cache = nullptr;
+      if (which > 0 && ok && where >= 0)
+        cache = static_cast<T*>(which == 2 ? p.v_cache : p.k_cache) + cache_row + (size_t)at.row * p.page * p.d;
+      if (which < 2) {
 #pragma unroll
-        for (int f = 0; f < FLY; ++f) {
-          const int row = r0 + f * RPP + me.group;
-          Pairs<T, VEC> v[U];
-          float sum = 0.0f;
+        for (int i = 0; i < U; ++i) {
+          Floats<VEC> c, s, wa, wb;
+          me.turn(sh.cs[warp], i, c, s);
+          me.gains(sh.gain[which], i, wa, wb);
 #pragma unroll
-          for (int i = 0; i < U; ++i) {
-            v[i].take(x[f][i], y[f][i], me.neighbours[i]);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sum = fmaf(v[i].a[e], v[i].a[e], fmaf(v[i].b[e], v[i].b[e], sum));
-          }
-          const float r = rsqrtf(fmaf(row_sum<TPR>(sum), p.inv_d, p.eps));
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float a = v[i].a[e] * r * w[i].a[e], b = v[i].b[e] * r * w[i].b[e];
-              v[i].a[e] = t.c[i][e] * a - t.s[i][e] * b;
-              v[i].b[e] = t.s[i][e] * a + t.c[i][e] * b;
-            }
-            v[i].give(x[f][i], y[f][i], me.neighbours[i]);
-          }
-          if (row < n) {
-            if (out) me.store_row(out + (size_t)row * p.d, x[f], y[f]);
-            if (which == 1 && slot >= 0)
-              me.store_row(static_cast<T*>(p.k_cache) +
-                               (((size_t)block * nk + row) * p.page + cache_row) * p.d,
-                           x[f], y[f]);
+          for (int e = 0; e < N; ++e) {
+            ca[i].v[e] = fmul2(c.v[e], wa.v[e]);
+            sa[i].v[e] = fmul2(s.v[e], wa.v[e]);
+            cb[i].v[e] = fmul2(c.v[e], wb.v[e]);
+            sb[i].v[e] = make_float2(-s.v[e].x * wb.v[e].x, -s.v[e].y * wb.v[e].y);
           }
         }
       }
     }
-    if (nv && slot >= 0) {
-      const T* src = static_cast<const T*>(p.v) + (size_t)tok * p.v_stride;
-      for (int row = part * RPP + me.group; row < nv; row += p.parts * RPP) {
-        P x[U], y[U];
-        me.load_row(src + (size_t)row * p.d, true, x, y);
-        me.store_row(static_cast<T*>(p.v_cache) +
-                         (((size_t)block * nk + row) * p.page + cache_row) * p.d,
-                     x, y);
+    asm volatile("cp.async.wait_group %0;" ::"n"(FLY - 1) : "memory");
+    const P(*mine)[U][32] = stage[warp][slot];
+    const bool write = ok && at.row < at.n;
+    P x[U], y[U];
+    if (at.which < 2) {
+      Pairs<T, VEC, NB> v[U];
+      me.take_row(mine, v);
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum = ffma2(v[i].a.v[e], v[i].a.v[e], ffma2(v[i].b.v[e], v[i].b.v[e], sum));
+      const float r = rsqrtf(fmaf(row_sum<TPR>(sum.x + sum.y), p.inv_d, p.eps));
+      const float2 r2 = make_float2(r, r);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float2 a = v[i].a.v[e], b = v[i].b.v[e];
+          v[i].a.v[e] = fmul2(r2, ffma2(ca[i].v[e], a, fmul2(sb[i].v[e], b)));
+          v[i].b.v[e] = fmul2(r2, ffma2(sa[i].v[e], a, fmul2(cb[i].v[e], b)));
+        }
+        v[i].give(x[i], y[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        x[i] = mine[0][i][lane];
+        y[i] = mine[1][i][lane];
       }
     }
-    (void)nq;
+    if (write) {
+      if (out) me.store_row(out, x, y);
+      if (cache) me.store_row(cache, x, y);
+    }
+    if (arrived) entries = me.fetch_entries(p, next_info, 1.0f);  // by now the positions are here
+    fresh = !walk.next(at);
+    if (out) out += out_step;
+    if (cache) cache += cache_step;
+    slot = slot + 1 == FLY ? 0 : slot + 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // The gradient.  Each warp sums g n over its rows in registers, each CTA over its
 // warps, and pva_norm_weights_kernel over the CTAs, always in the same order.
-template <typename T, int VEC, int TPR, int U, int FLY>
-__global__ void __launch_bounds__(kNormThreads) pva_norm_rope_backward_kernel(NormStep p) {
+template <typename T, int VEC, int TPR, int U, int FLY, bool NB>
+__global__ void __launch_bounds__(kNormThreads, kBackCtas) pva_norm_rope_backward_kernel(NormStep p) {
   using P = Pack<T, VEC>;
-  constexpr int RPP = 32 / TPR;
+  constexpr int RPP = 32 / TPR, N = Floats<VEC>::N;
   extern __shared__ float s_sum[];  // [2][warps][d]
+  __shared__ NormShared sh;
+  __shared__ P stage[kNormWarps][FLY][2][2][U][32];
   allow_next_grid();
   wait_prior_grid();
-  const NormLane<T, VEC, TPR, U> me(p);
+  const NormLane<T, VEC, TPR, U, NB> me(p);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long items = (long long)p.tokens * p.parts;
-  const long long stride = (long long)gridDim.x * kNormWarps;
+  share_gains<T>(p, sh);
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int n = p.heads[which];
     if (n == 0) continue;
-    Pairs<T, VEC> w[U], dw[U];
-    me.gains(p, which, w);
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) dw[i].a[e] = dw[i].b[e] = 0.0f;
-    for (long long item = (long long)blockIdx.x * kNormWarps + warp; item < items; item += stride) {
-      const int tok = (int)(item / p.parts), part = (int)(item - (long long)tok * p.parts);
-      int64_t at[kMaxAxes];
-      if (!token_position(p, tok, at)) {
-        if (lane == 0) atomicOr(p.status, PVA_DEV_ROPE);
-        continue;
-      }
-      Turn<VEC, U> t;
-      me.turn(p, at, -1.0f, t);
-      const T* src = static_cast<const T*>(p.x[which]) + (size_t)tok * p.x_stride[which];
-      const T* grad = static_cast<const T*>(p.dy[which]) + (size_t)tok * p.dy_stride[which];
-      T* out = static_cast<T*>(p.out[which]) + (size_t)tok * p.out_stride[which];
-      for (int r0 = part * RPP * FLY; r0 < n; r0 += p.parts * RPP * FLY) {
-        P x[FLY][U], y[FLY][U], gx[FLY][U], gy[FLY][U];
-#pragma unroll
-        for (int f = 0; f < FLY; ++f) {
-          const int row = r0 + f * RPP + me.group;
-          me.load_row(src + (size_t)row * p.d, row < n, x[f], y[f]);
-          me.load_row(grad + (size_t)row * p.d, row < n, gx[f], gy[f]);
-        }
-#pragma unroll
-        for (int f = 0; f < FLY; ++f) {
-          const int row = r0 + f * RPP + me.group;
-          Pairs<T, VEC> v[U], g[U];
-          float sum = 0.0f, inner = 0.0f;
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            v[i].take(x[f][i], y[f][i], me.neighbours[i]);
-            g[i].take(gx[f][i], gy[f][i], me.neighbours[i]);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              sum = fmaf(v[i].a[e], v[i].a[e], fmaf(v[i].b[e], v[i].b[e], sum));
-              const float a = t.c[i][e] * g[i].a[e] - t.s[i][e] * g[i].b[e];
-              const float b = t.s[i][e] * g[i].a[e] + t.c[i][e] * g[i].b[e];
-              g[i].a[e] = a;
-              g[i].b[e] = b;
-              inner = fmaf(a * w[i].a[e], v[i].a[e], fmaf(b * w[i].b[e], v[i].b[e], inner));
-            }
-          }
-          const float r = rsqrtf(fmaf(row_sum<TPR>(sum), p.inv_d, p.eps));
-          // mean(g w n) r, so that n mean(g w n) r = x r^2 mean(g w x) r
-          const float m = row_sum<TPR>(inner) * p.inv_d * r * r;
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              dw[i].a[e] = fmaf(g[i].a[e], v[i].a[e] * r, dw[i].a[e]);
-              dw[i].b[e] = fmaf(g[i].b[e], v[i].b[e] * r, dw[i].b[e]);
-              g[i].a[e] = r * (g[i].a[e] * w[i].a[e] - v[i].a[e] * m);
-              g[i].b[e] = r * (g[i].b[e] * w[i].b[e] - v[i].b[e] * m);
-            }
-            g[i].give(x[f][i], y[f][i], me.neighbours[i]);
-          }
-          if (row < n) me.store_row(out + (size_t)row * p.d, x[f], y[f]);
+    const NormWalk<RPP> walk(p, me.group, which, 1);
+    NormCursor ahead = walk.begin(), at = ahead;
+    const T *src = nullptr, *grad = nullptr;
+    auto source = [&]() {
+      if (!walk.more(ahead)) return;
+      src = static_cast<const T*>(p.x[which]) + ahead.tok * p.x_stride[which] + (size_t)ahead.row * p.d;
+      grad = static_cast<const T*>(p.dy[which]) + ahead.tok * p.dy_stride[which] + (size_t)ahead.row * p.d;
+    };
+    source();
+    const int row_step = walk.step * p.d;
+    auto copy = [&](int slot) {
+      if (walk.more(ahead)) {
+        const bool there = ahead.row < ahead.n;
+        me.copy_row(src, there, stage[warp][slot][0]);
+        me.copy_row(grad, there, stage[warp][slot][1]);
+        if (walk.next(ahead)) {
+          src += row_step;
+          grad += row_step;
+        } else {
+          source();
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int f = 0; f < FLY - 1; ++f) copy(f);
+    long long fetched = walk.more(at) ? at.tok : p.tokens;  // the token of info and entries
+    int64_t next_info = me.fetch_info(p, fetched);
+    auto entries = me.fetch_entries(p, next_info, -1.0f);
+    Floats<VEC> wa[U], wb[U], da[U], db[U], c[U], s[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      me.gains(sh.gain[which], i, wa[i], wb[i]);
+      da[i].clear();
+      db[i].clear();
     }
+    long long item = -1;
+    int slot = 0;
+    bool ok = false;
+    T* out = nullptr;
+    while (walk.more(at)) {
+      copy(slot == 0 ? FLY - 1 : slot - 1);
+      const bool arrived = at.item != item;
+      if (arrived) {
+        item = at.item;
+        out = static_cast<T*>(p.out[which]) + at.tok * p.out_stride[which] + (size_t)at.row * p.d;
+        if (fetched != at.tok) {  // items without rows of this kind were passed over
+          next_info = me.fetch_info(p, at.tok);
+          entries = me.fetch_entries(p, next_info, -1.0f);
+        }
+        me.share(p, entries, sh.cs[warp]);
+        ok = me.fine(p, next_info);
+        if (!ok && lane == 0) atomicOr(p.status, PVA_DEV_ROPE);
+        fetched = (item + walk.stride) / p.parts;
+        next_info = me.fetch_info(p, fetched);
+#pragma unroll
+        for (int i = 0; i < U; ++i) me.turn(sh.cs[warp], i, c[i], s[i]);
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(FLY - 1) : "memory");
+      Pairs<T, VEC, NB> v[U], g[U];
+      me.take_row(stage[warp][slot][0], v);
+      me.take_row(stage[warp][slot][1], g);
+      float2 sum = make_float2(0.0f, 0.0f), inner = sum;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          sum = ffma2(v[i].a.v[e], v[i].a.v[e], ffma2(v[i].b.v[e], v[i].b.v[e], sum));
+          const float2 ga = g[i].a.v[e], gb = g[i].b.v[e], minus = make_float2(-s[i].v[e].x, -s[i].v[e].y);
+          g[i].a.v[e] = ffma2(c[i].v[e], ga, fmul2(minus, gb));
+          g[i].b.v[e] = ffma2(s[i].v[e], ga, fmul2(c[i].v[e], gb));
+          inner = ffma2(fmul2(g[i].a.v[e], wa[i].v[e]), v[i].a.v[e],
+                        ffma2(fmul2(g[i].b.v[e], wb[i].v[e]), v[i].b.v[e], inner));
+        }
+      }
+      const float r = rsqrtf(fmaf(row_sum<TPR>(sum.x + sum.y), p.inv_d, p.eps));
+      // n mean(g w n) r = n (r^2 mean(g w x)), with n = x r
+      const float m = -(row_sum<TPR>(inner.x + inner.y) * p.inv_d * r * r);
+      const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+      P x[U], y[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float2 na = fmul2(v[i].a.v[e], r2), nb = fmul2(v[i].b.v[e], r2);
+          if (ok) {  // (rows that are not there are zeros)
+            da[i].v[e] = ffma2(g[i].a.v[e], na, da[i].v[e]);
+            db[i].v[e] = ffma2(g[i].b.v[e], nb, db[i].v[e]);
+          }
+          g[i].a.v[e] = ffma2(fmul2(g[i].a.v[e], wa[i].v[e]), r2, fmul2(na, m2));
+          g[i].b.v[e] = ffma2(fmul2(g[i].b.v[e], wb[i].v[e]), r2, fmul2(nb, m2));
+        }
+        g[i].give(x[i], y[i]);
+      }
+      if (ok && at.row < at.n) me.store_row(out, x, y);
+      if (arrived) entries = me.fetch_entries(p, next_info, -1.0f);
+      walk.next(at);
+      out += row_step;
+      slot = slot + 1 == FLY ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!p.want_w[which]) continue;
     // the rows of a warp lie TPR lanes apart
 #pragma unroll
     for (int i = 0; i < U; ++i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
+        float a = da[i][e], b = db[i][e];
 #pragma unroll
         for (int o = TPR; o < 32; o <<= 1) {
-          dw[i].a[e] += __shfl_xor_sync(0xffffffffu, dw[i].a[e], o);
-          dw[i].b[e] += __shfl_xor_sync(0xffffffffu, dw[i].b[e], o);
+          a += __shfl_xor_sync(0xffffffffu, a, o);
+          b += __shfl_xor_sync(0xffffffffu, b, o);
         }
         if (me.group == 0 && me.in[i]) {
           float* to = s_sum + ((size_t)which * kNormWarps + warp) * p.d;
-          to[me.neighbours[i] ? me.d0[i] + 2 * e : me.d0[i] + e] = dw[i].a[e];
-          to[me.neighbours[i] ? me.d0[i] + 2 * e + 1 : me.d1[i] + e] = dw[i].b[e];
+          to[me.first(i, e)] = a;
+          to[me.second(i, e)] = b;
         }
       }
     }
@@ -442,21 +622,21 @@ __global__ void __launch_bounds__(1024) pva_norm_weights_kernel(NormStep p, int 
     p.dw[which][blockIdx.x * 32 + threadIdx.y] = x;
 }
 
-constexpr int kNormCtas = 5;  // CTAs an SM is given
-
-int norm_grid(const NormStep& p, int num_sms) {
+int norm_grid(const NormStep& p, int ctas, int num_sms) {
   const long long want = ((long long)p.tokens * p.parts + kNormWarps - 1) / kNormWarps;
-  const long long most = (long long)num_sms * kNormCtas;
+  const long long most = (long long)num_sms * ctas;
   return (int)(want < most ? want : most);
 }
 
 template <typename T, int VEC, int TPR, int U>
 cudaError_t launch_norm(const NormStep& p, bool backward, int grid, cudaStream_t st) {
-  if (!backward)
-    return launch_dependent(pva_norm_rope_kernel<T, VEC, TPR, U, U == 1 ? 4 : 1>, dim3(grid),
-                            dim3(kNormThreads), 0, st, p);
-  return launch_dependent(pva_norm_rope_backward_kernel<T, VEC, TPR, U, U == 1 ? 2 : 1>, dim3(grid),
-                          dim3(kNormThreads), sizeof(float) * 2 * kNormWarps * p.d, st, p);
+  constexpr int F = U == 1 ? kFly : 2, FB = U == 1 ? kBackFly : 2;
+  auto kern = p.rt.interleaved ? pva_norm_rope_kernel<T, VEC, TPR, U, F, true>
+                               : pva_norm_rope_kernel<T, VEC, TPR, U, F, false>;
+  auto back = p.rt.interleaved ? pva_norm_rope_backward_kernel<T, VEC, TPR, U, FB, true>
+                               : pva_norm_rope_backward_kernel<T, VEC, TPR, U, FB, false>;
+  return backward ? launch_dependent(back, dim3(grid), dim3(kNormThreads), sizeof(float) * 2 * kNormWarps * p.d, st, p)
+                  : launch_dependent(kern, dim3(grid), dim3(kNormThreads), 0, st, p);
 }
 
 // 16-byte accesses where sizes and alignment allow, a row across the least power of
@@ -477,7 +657,7 @@ int rows_at_once(const NormStep& p, int dtype, bool wide, bool backward) {
   if (!wide) return 1;
   const int units = p.d / (dtype == PVA_F32 ? 8 : 16);
   const int tpr = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
-  return 32 / tpr * (backward ? 2 : 4);
+  return 32 / tpr;
 }
 
 bool norm_wide(const NormStep& p, int vec) {
@@ -502,10 +682,11 @@ int enqueue_norm(NormStep& p, int dtype, bool backward, cudaStream_t stream) {
   const int at_once = rows_at_once(p, dtype, wide, backward);
   const int rows = p.heads[0] > p.heads[1] ? p.heads[0] : p.heads[1];
   const int most = (rows + at_once - 1) / at_once;
-  const long long warps = (long long)sms * kNormCtas * kNormWarps;
+  const int ctas = backward ? kBackCtas : kNormCtas;
+  const long long warps = (long long)sms * ctas * kNormWarps;
   const long long parts = warps / p.tokens;
   p.parts = (int)(parts < 1 ? 1 : parts < most ? parts : most);
-  const int grid = norm_grid(p, sms);
+  const int grid = norm_grid(p, ctas, sms);
   const bool sums = backward && (p.want_w[0] || p.want_w[1]);
   CallContext c;
   if ((rc = acquire(stream, sums ? sizeof(float) * 2 * p.d * (size_t)grid : 0, &c)) != PVA_OK) return rc;
