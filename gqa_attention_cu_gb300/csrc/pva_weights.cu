@@ -193,17 +193,18 @@ __device__ __forceinline__ float natural(float s, float scale, float softcap, fl
 }
 
 // ---------------------------------------------------------------------------
-// Tensor cores.  One CTA per piece, 320 threads:
+// Tensor cores.  One CTA per piece, 576 threads:
 //   warp 0      TMA producer: publishes the segments' chunks, loads the chunk's
 //               query rows and then the key tiles through a ring.
-//   warp 1      MMA issuer and TMEM owner; two score buffers.
-//   warps 2..5, 6..9   take the tiles of score buffer 0 and 1.
+//   warp 1      MMA issuer and TMEM owner; four score buffers.
+//   warps 2..5, 6..9, ...   take the tiles of score buffer 0, 1, ...
 // Store and Apply form S^T = K Q^T, 128 keys by N query rows: a thread has a key and
 // adds up over its columns without meeting another.  Stats forms S = Q K^T, 128
 // query rows by 128 keys: a thread has a row and keeps its running maximum and sum.
 // ---------------------------------------------------------------------------
 enum Mode { kStore, kApply, kStats };
-constexpr int kTcThreads = 320;
+constexpr int kGroups = 4;  // of four warps, with a score buffer each
+constexpr int kTcThreads = 64 + 128 * kGroups;
 constexpr int kItemSlots = 4;
 
 struct ItemSlot {
@@ -213,7 +214,7 @@ struct ItemSlot {
 
 struct Bars {
   uint64_t q_full[2], q_empty[2], drain;
-  uint64_t s_full[2], s_free[2];
+  uint64_t s_full[kGroups], s_free[kGroups];
   uint64_t ring_full[12], ring_empty[12];
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   ItemSlot items[kItemSlots];
@@ -232,16 +233,29 @@ struct WCfg {
   static constexpr int K_TILE = CH * K_CHUNK;
   static constexpr int Q_BUFS = 2 * Q_TILE <= 64 * 1024 ? 2 : 1;
   // barriers, then (Apply) each score warp's copy of the chunk's row values
-  static constexpr int HEAD = kBarBytes + (MODE == kApply ? (8 * N * 8 + 1023) / 1024 * 1024 : 0);
+  static constexpr int HEAD = kBarBytes + (MODE == kApply ? (4 * kGroups * N * 8 + 1023) / 1024 * 1024 : 0);
   static constexpr int OFF_RING = Q_BUFS * Q_TILE;
   static constexpr int SLOTS_FIT = (232448 - HEAD - OFF_RING) / K_TILE;
   static constexpr int SLOTS = SLOTS_FIT < 12 ? SLOTS_FIT : 12;
   static_assert(SLOTS >= 2, "ring depth");
   static constexpr int SMEM = HEAD + OFF_RING + SLOTS * K_TILE;
   static constexpr int COLS = MODE == kStats ? kKeys : N;  // of a score buffer
-  static constexpr int TMEM_COLS = 2 * COLS;
+  static constexpr int TMEM_COLS = kGroups * COLS;
+  static_assert(TMEM_COLS <= 512, "TMEM budget");
 };
 
+template <int W>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[W]) {
+  if constexpr (W == 32) {
+    tmem_wait_ld_of(r);
+  } else {
+    static_assert(W == 16, "one load");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+  }
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -291,6 +305,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
+    }
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_free[i], 4);
     }
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], 1 + 8);
+      mbar_init(&bars->item_empty[i], 1 + 4 * kGroups);
     }
     fence_mbar_init();
   }
@@ -314,8 +330,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  allow_next_grid();
   wait_prior_grid();
+  allow_next_grid();  // the next kernel looks up at once what the front end has written
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, abort, status));
   };
@@ -324,6 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------------------ producer
     Walk walk(p, blockIdx.x, p.hdr[1], p.hdr[2]);
     const int box = p.table && p.page < kKeys ? p.page : kKeys, copies = kKeys / box;
+    const uint64_t once = read_once_policy();  // keys leave L2 first: scores and weights stay there
     uint32_t loads = 0, published = 0, q_loads = 0;
     bool ok = true;
     auto publish = [&](const ItemSlot& v) -> bool {
@@ -356,17 +373,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
         ++q_loads;
+        // a page a lane, or the whole tile; the next tile's block is looked up while this
+        // one's slot is waited for
+        struct Place {
+          bool mine;
+          int block, y;
+        };
+        auto locate = [&](int j) {
+          const long long r0 = (long long)j * kKeys + lane * box;
+          Place x{lane < copies && r0 < s.n, 0, 0};
+          if (x.mine) {
+            const int in = (int)r0 / p.page;
+            x.block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+            x.y = (int)r0 - in * p.page;
+          }
+          return x;
+        };
+        Place place = locate(s.j0);
         for (int j = s.j0; j < v.end; ++j, ++loads) {
           const int sl = loads % C::SLOTS;
-          // a page a lane, or the whole tile
-          const long long r0 = (long long)j * kKeys + lane * box;
-          const bool mine = lane < copies && r0 < s.n;
-          int block = 0, y = 0;
-          if (mine) {
-            const int in = (int)r0 / p.page;
-            block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
-            y = (int)r0 - in * p.page;
-          }
+          const Place next = locate(j + 1);
+          const bool mine = place.mine;
           const uint32_t n_copies = __popc(__ballot_sync(0xffffffffu, mine));
           if (!(ok = wait(&bars->ring_empty[sl], ((loads / C::SLOTS) & 1) ^ 1))) break;
           if (lane == 0)
@@ -376,10 +403,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* dst = ring + sl * C::K_TILE + lane * box * 128;
 #pragma unroll
             for (int x = 0; x < C::CH; ++x)
-              tma_load_3d(dst + x * C::K_CHUNK, &tmap_k, &bars->ring_full[sl], x * 64, y,
-                          block * p.Hkv + s.h);
+              tma_load_3d_once(dst + x * C::K_CHUNK, &tmap_k, &bars->ring_full[sl], x * 64, place.y,
+                               place.block * p.Hkv + s.h, once);
           }
           __syncwarp();
+          place = next;
         }
       }
     }
@@ -403,7 +431,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                               : idesc_f16<T>(kKeys, N, false, false);
     const uint64_t qdesc = sdesc_sw128(smem_u32(smem), 16, 1024);
     const uint64_t kdesc = sdesc_sw128(smem_u32(ring), 16, 1024);
-    uint32_t loads = 0, taken = 0, q_cnt = 0, used0 = 0, used1 = 0;
+    uint32_t loads = 0, taken = 0, q_cnt = 0;
+    uint32_t turns = 0;  // a byte a score buffer: the parity of its next tile
     bool ok = true;
     while (ok) {
       const int isl = taken % kItemSlots;
@@ -419,9 +448,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ++q_cnt;
       const uint64_t qa = sdesc_advance(qdesc, qb * C::Q_TILE);
       for (int j = j0; j < end; ++j, ++loads) {
-        const int sl = loads % C::SLOTS, buf = j & 1;
+        const int sl = loads % C::SLOTS, buf = j % kGroups;
         if (!(ok = wait(&bars->ring_full[sl], (loads / C::SLOTS) & 1))) break;
-        if (!(ok = wait(&bars->s_free[buf], (buf ? used1++ : used0++) & 1 ^ 1))) break;
+        if (!(ok = wait(&bars->s_free[buf], (turns >> (8 * buf) & 1) ^ 1))) break;
+        turns ^= 1u << (8 * buf);
         tc_fence_after();
         const uint64_t ka = sdesc_advance(kdesc, sl * C::K_TILE);
         if (leader) {
@@ -447,7 +477,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + group * C::COLS;
     const float scale = p.scale, cap = p.softcap, inv_cap = CAP ? 1.0f / p.softcap : 0.0f;
     const float NEG_INF = __int_as_float(0xff800000);
-    float2* rows = reinterpret_cast<float2*>(smem_raw + kBarBytes) + (warp - 2) * N;
+    float* rows = reinterpret_cast<float*>(smem_raw + kBarBytes) + (warp - 2) * N * 2;
+    const float to_base2 = scale * kLog2e;
     uint32_t tiles = 0, taken = 0;
     bool ok = true;
     while (ok) {
@@ -474,7 +505,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           } else {
             v = p.row[((size_t)s.b * p.Hkv + s.h) * p.T * p.G + row0 + i];
           }
-          rows[i] = v;
+          // two columns beside each other: -m log2 e, -m' log2 e, 1 / l, 1 / l'
+          float* to = rows + (i >> 1) * 4 + (i & 1);
+          to[0] = -v.x * kLog2e;
+          to[2] = v.y;
         }
         __syncwarp();
       }
@@ -488,8 +522,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         l[c] = 0.0f;
       }
       const int my_row = t0 + r / p.G;  // Stats: the row's token
-      // Each buffer's tiles are every other one of the keys: a key is always this thread's.
-      for (int j = s.j0 + ((s.j0 ^ group) & 1); j < it.end; j += 2, ++tiles) {
+      // Each buffer's tiles are every kGroups-th of the keys: a key is always this thread's.
+      for (int j = s.j0 + (group + kGroups - s.j0 % kGroups) % kGroups; j < it.end; j += kGroups, ++tiles) {
         const int k0 = j * kKeys, key = k0 + r;
         const bool all = k0 + kKeys <= free_of_masks;
         float base = 0.0f;
@@ -528,37 +562,65 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         } else {
-          float sum = base;
+          // The rows that see this key are those from `from` on: tokens follow each other.
+          const int behind = key - keys_of(s, t0);
+          const int from = key >= s.n ? INT_MAX : behind < 0 ? 0 : (behind + 1) * p.G;
+          // columns [c, c + W) of this thread's key, W at once
+          constexpr int W = N < 32 ? 16 : 32;
+          float2 acc[2] = {make_float2(base, 0.0f), make_float2(0.0f, 0.0f)};
           float* score = nullptr;
           if constexpr (MODE == kStore)
             score = p.scores + ((long long)p.start[s.b] + (long long)s.h * ((s.n + kKeys - 1) / kKeys) + j) *
                                    p.T * p.G * kKeys + r;
 #pragma unroll 1
-          for (int c = 0; c < N; c += 16) {
-            if (c >= used) break;
-            uint32_t v[16];
-            tmem_ld16(t_s + c, v);
-            asm volatile("tcgen05.wait::ld.sync.aligned;"
-                         : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                           "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                           "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+          for (int c = 0; c < used; c += W) {
+            uint32_t v[W];
+            if constexpr (W == 16) tmem_ld16(t_s + c, v); else tmem_ld32(t_s + c, v);
+            tmem_wait(v);
+            if (c + W >= used) {  // the last columns are read: the next product may go over them
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->s_free[group]);
+            }
+            if constexpr (MODE == kApply) {
+              if (all && c + W <= used) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if (c + e >= used) break;
-              const float x = natural<CAP>(__uint_as_float(v[e]), scale, cap, inv_cap);
-              const bool seen = all || key < keys_of(s, t0 + (c + e) / p.G);
-              if constexpr (MODE == kApply) {
-                const float2 w = rows[c + e];
-                const float y = ex2_approx((x - w.x) * kLog2e);
-                if (seen) sum = fmaf(y, w.y, sum);
+                for (int e = 0; e < W; e += 2) {
+                  const float4 w = *reinterpret_cast<const float4*>(rows + (c + e) * 2);
+                  float2 x = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                  if (CAP) x = make_float2(natural<true>(x.x, scale, cap, inv_cap), natural<true>(x.y, scale, cap, inv_cap));
+                  const float mul = CAP ? kLog2e : to_base2;
+                  x = ffma2(x, make_float2(mul, mul), make_float2(w.x, w.y));
+                  acc[(e >> 1) & 1] = ffma2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(w.z, w.w), acc[(e >> 1) & 1]);
+                }
               } else {
-                const float y = seen ? x : NEG_INF;
+#pragma unroll
+                for (int e = 0; e < W; e += 2) {
+                  const int i = c + e;
+                  if (i >= used) break;
+                  const float4 w = *reinterpret_cast<const float4*>(rows + i * 2);
+                  float2 x = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                  if (CAP) x = make_float2(natural<true>(x.x, scale, cap, inv_cap), natural<true>(x.y, scale, cap, inv_cap));
+                  const float mul = CAP ? kLog2e : to_base2;
+                  x = ffma2(x, make_float2(mul, mul), make_float2(w.x, w.y));
+                  x.x = i >= from ? ex2_approx(x.x) * w.z : 0.0f;
+                  x.y = i + 1 >= from && i + 1 < used ? ex2_approx(x.y) * w.w : 0.0f;
+                  acc[(e >> 1) & 1] = fadd2(acc[(e >> 1) & 1], x);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < W; ++e) {
+                if (c + e >= used) break;
+                const float x = natural<CAP>(__uint_as_float(v[e]), scale, cap, inv_cap);
+                const float y = c + e >= from ? x : NEG_INF;
                 score[(c + e) * kKeys] = y;
                 add_score(m[e], l[e], y);
               }
             }
           }
-          if (MODE == kApply && key < s.n) p.weights[at] = sum;
+          if (MODE == kApply && key < s.n) p.weights[at] = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+          if (used > 0) continue;  // (the buffer is given back above)
         }
         tc_fence_before();
         __syncwarp();
@@ -590,30 +652,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// f32: a thread has a key of a tile of 128, whose rows lie in shared memory, and
-// kRowsF32 query rows at a time.  Exact f32 products.
+// f32: a tile of 128 keys lies in shared memory, and 16 query rows at a time; two warps
+// take the first 8 of them and two the others, a thread two keys (64 products for each
+// 10 reads of 16 bytes of shared memory).  Exact f32 products.
 // ---------------------------------------------------------------------------
-constexpr int kRowsF32 = 8;
+constexpr int kRowsF32 = 16, kThreadsF32 = 128;
 __host__ __device__ constexpr int f32_row(int d) { return (d + 3) / 4 * 4 + 4; }
-size_t f32_smem(int d) { return sizeof(float) * (size_t)(kKeys + kRowsF32) * f32_row(d) + 4 * kRowsF32 * 16; }
+size_t f32_smem(int d) { return sizeof(float) * (size_t)(kKeys + kRowsF32) * f32_row(d); }
 
-template <int MODE>
-__global__ void __launch_bounds__(kKeys) pva_weights_f32_kernel(WeightsParams p) {
+// WIDE: rows lie on 16-byte boundaries.
+template <int MODE, bool WIDE>
+__global__ void __launch_bounds__(kThreadsF32) pva_weights_f32_kernel(WeightsParams p) {
   extern __shared__ float smem[];
   __shared__ Segment s_segment;
   __shared__ int s_more;
   __shared__ float2 s_rows[kRowsF32];
   __shared__ int s_hi[kRowsF32];
-  __shared__ float2 s_warp[kKeys / 32][kRowsF32];
+  __shared__ float2 s_half[2][kRowsF32 / 2][2];  // Stats: a row's (m, l) of its two warps
+  __shared__ float s_sum[2][64];                 // Apply: the upper rows' part of the keys' weights
   allow_next_grid();
   wait_prior_grid();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = p.d, row = f32_row(d);
+  const int group = tid >> 6, key0 = tid & 63;  // of the rows; keys key0 and key0 + 64
   const float NEG_INF = __int_as_float(0xff800000);
   float* sk = smem;
   float* sq = smem + (size_t)kKeys * row;
   const float* kc = static_cast<const float*>(p.k_cache);
   const float* q = static_cast<const float*>(p.q);
-  for (int i = tid; i < (kKeys + kRowsF32) * (row - d); i += kKeys)
+  for (int i = tid; i < (kKeys + kRowsF32) * (row - d); i += kThreadsF32)
     smem[(size_t)(i / (row - d)) * row + d + i % (row - d)] = 0.0f;
   Walk walk(p, blockIdx.x, p.hdr[1], p.hdr[2]);  // the first warp's counts
   while (true) {
@@ -630,8 +696,18 @@ __global__ void __launch_bounds__(kKeys) pva_weights_f32_kernel(WeightsParams p)
     if (!s_more) break;
     const Segment s = s_segment;
     const int all_rows = s.q * p.G;
+    auto copy_row = [&](float* dst, const float* src, bool there) {  // a warp
+      if (WIDE) {
+        for (int c = 4 * lane; c < d; c += 128)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + c)), "l"(src + (there ? c : 0)),
+                       "r"(there ? 16 : 0)
+                       : "memory");
+      } else {
+        for (int c = lane; c < d; c += 32) dst[c] = there ? src[c] : 0.0f;
+      }
+    };
     auto load_keys = [&](int j) {
-      for (int i = warp; i < kKeys; i += kKeys / 32) {
+      for (int i = warp; i < kKeys; i += kThreadsF32 / 32) {
         const int key = j * kKeys + i;
         size_t at = 0;
         if (key < s.n) {
@@ -639,15 +715,14 @@ __global__ void __launch_bounds__(kKeys) pva_weights_f32_kernel(WeightsParams p)
           const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
           at = (((size_t)block * p.Hkv + s.h) * p.page + (key - in * p.page)) * d;
         }
-        for (int c = lane; c < d; c += 32) sk[(size_t)i * row + c] = key < s.n ? kc[at + c] : 0.0f;
+        copy_row(sk + (size_t)i * row, kc + at, key < s.n);
       }
     };
     auto load_rows = [&](int r0) {
-      for (int i = warp; i < kRowsF32; i += kKeys / 32) {
+      for (int i = warp; i < kRowsF32; i += kThreadsF32 / 32) {
         const int r = r0 + i, t = r / p.G, g = r - t * p.G;
         const bool there = r < all_rows;
-        const float* src = q + (((size_t)s.b * p.T + t) * p.H + s.h * p.G + g) * d;
-        for (int c = lane; c < d; c += 32) sq[(size_t)i * row + c] = there ? src[c] : 0.0f;
+        copy_row(sq + (size_t)i * row, there ? q + (((size_t)s.b * p.T + t) * p.H + s.h * p.G + g) * d : q, there);
       }
       if (tid < kRowsF32) {
         const int r = r0 + tid, t = r / p.G, g = r - t * p.G;
@@ -662,80 +737,93 @@ __global__ void __launch_bounds__(kKeys) pva_weights_f32_kernel(WeightsParams p)
           }
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     };
-    auto scores = [&](float (&x)[kRowsF32]) {
+    auto scores = [&](float (&x)[2][8]) {
 #pragma unroll
-      for (int e = 0; e < kRowsF32; ++e) x[e] = 0.0f;
+      for (int e = 0; e < 8; ++e) x[0][e] = x[1][e] = 0.0f;
+      const float* qa = sq + (size_t)group * 8 * row;
       for (int c = 0; c < d; c += 4) {
-        const float4 k = *reinterpret_cast<const float4*>(sk + (size_t)tid * row + c);
+        const float4 k0 = *reinterpret_cast<const float4*>(sk + (size_t)key0 * row + c);
+        const float4 k1 = *reinterpret_cast<const float4*>(sk + (size_t)(key0 + 64) * row + c);
 #pragma unroll
-        for (int e = 0; e < kRowsF32; ++e) {
-          const float4 v = *reinterpret_cast<const float4*>(sq + (size_t)e * row + c);
-          x[e] = fmaf(k.w, v.w, fmaf(k.z, v.z, fmaf(k.y, v.y, fmaf(k.x, v.x, x[e]))));
+        for (int e = 0; e < 8; ++e) {
+          const float4 v = *reinterpret_cast<const float4*>(qa + (size_t)e * row + c);
+          x[0][e] = fmaf(k0.w, v.w, fmaf(k0.z, v.z, fmaf(k0.y, v.y, fmaf(k0.x, v.x, x[0][e]))));
+          x[1][e] = fmaf(k1.w, v.w, fmaf(k1.z, v.z, fmaf(k1.y, v.y, fmaf(k1.x, v.x, x[1][e]))));
         }
       }
 #pragma unroll
-      for (int e = 0; e < kRowsF32; ++e)
-        x[e] = p.softcap != 0.0f ? natural<true>(x[e], p.scale, p.softcap, 1.0f / p.softcap)
-                                 : natural<false>(x[e], p.scale, 0.0f, 0.0f);
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[y][e] = p.softcap != 0.0f ? natural<true>(x[y][e], p.scale, p.softcap, 1.0f / p.softcap)
+                                      : natural<false>(x[y][e], p.scale, 0.0f, 0.0f);
     };
-    if (MODE == kApply) {
-      for (int j = s.j0; j < s.j1; ++j) {
-        __syncthreads();
-        load_keys(j);
-        const int key = j * kKeys + tid;
-        const size_t at = ((size_t)s.b * p.Hkv + s.h) * p.width + key;
-        float sum = key < s.n && p.previous ? p.decay * p.previous[at] : 0.0f;
-        for (int r0 = 0; r0 < all_rows; r0 += kRowsF32) {
-          if (r0) __syncthreads();
-          load_rows(r0);
-          __syncthreads();
-          float x[kRowsF32];
-          scores(x);
+    for (int j = s.j0; j < s.j1; ++j) {
+      __syncthreads();
+      load_keys(j);
+      const int key = j * kKeys + key0;
+      const size_t at = ((size_t)s.b * p.Hkv + s.h) * p.width + key;
+      float sum[2] = {0.0f, 0.0f};
+      if (MODE == kApply && p.previous && group == 0)
 #pragma unroll
-          for (int e = 0; e < kRowsF32; ++e)
-            if (key < s_hi[e]) sum = fmaf(exp2f((x[e] - s_rows[e].x) * kLog2e), s_rows[e].y, sum);
-        }
-        if (key < s.n) p.weights[at] = sum;
-      }
-    } else {
+        for (int y = 0; y < 2; ++y)
+          if (key + 64 * y < s.n) sum[y] = p.decay * p.previous[at + 64 * y];
+      if (all_rows == 0) asm volatile("cp.async.wait_all;" ::: "memory");
       for (int r0 = 0; r0 < all_rows; r0 += kRowsF32) {
-        float m[kRowsF32], l[kRowsF32];
+        if (r0) __syncthreads();
+        load_rows(r0);
+        __syncthreads();
+        const bool mine = r0 + group * 8 < all_rows;  // uniform in a warp
+        float x[2][8];
+        if (mine) scores(x);
+        if (MODE == kApply) {
+          if (!mine) continue;
 #pragma unroll
-        for (int e = 0; e < kRowsF32; ++e) {
-          m[e] = NEG_INF;
-          l[e] = 0.0f;
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float2 w = s_rows[group * 8 + e];
+              if (key + 64 * y < s_hi[group * 8 + e]) sum[y] = fmaf(exp2f((x[y][e] - w.x) * kLog2e), w.y, sum[y]);
+            }
+          continue;
         }
-        for (int j = s.j0; j < s.j1; ++j) {
-          __syncthreads();
-          if (j == s.j0) load_rows(r0);
-          load_keys(j);
-          __syncthreads();
-          float x[kRowsF32];
-          scores(x);
+        if (mine) {
 #pragma unroll
-          for (int e = 0; e < kRowsF32; ++e) {
-            if (j * kKeys + tid >= s_hi[e]) continue;
-            const float top = fmaxf(m[e], x[e]);
-            l[e] = l[e] * exp2f((m[e] - top) * kLog2e) + exp2f((x[e] - top) * kLog2e);
-            m[e] = top;
+          for (int e = 0; e < 8; ++e) {
+            const int hi = s_hi[group * 8 + e];
+            const float a = key < hi ? x[0][e] : NEG_INF, b = key + 64 < hi ? x[1][e] : NEG_INF;
+            float m = fmaxf(a, b);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float top = m == NEG_INF ? 0.0f : m;
+            float l = exp2f((a - top) * kLog2e) + exp2f((b - top) * kLog2e);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) s_half[group][e][warp & 1] = make_float2(m, l);
           }
-        }
-#pragma unroll
-        for (int e = 0; e < kRowsF32; ++e) {
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, m[e], o), l2 = __shfl_xor_sync(0xffffffffu, l[e], o);
-            join_scores(m[e], l[e], m2, l2);
-          }
-          if (lane == 0) s_warp[warp][e] = make_float2(m[e], l[e]);
         }
         __syncthreads();
-        if (tid < kRowsF32 && r0 + tid < all_rows) {
-          float2 v = s_warp[0][tid];
-          for (int w = 1; w < kKeys / 32; ++w) join_scores(v.x, v.y, s_warp[w][tid].x, s_warp[w][tid].y);
-          p.part[(size_t)s.slot * p.T * p.G + r0 + tid] = v;
+        if (tid < kRowsF32 && r0 + tid < all_rows) {  // a row's sums are this thread's throughout
+          float2* part = p.part + (size_t)s.slot * p.T * p.G + r0 + tid;
+          float2 v = s_half[tid >> 3][tid & 7][0];
+          const float2 o = s_half[tid >> 3][tid & 7][1];
+          join_scores(v.x, v.y, o.x, o.y);
+          if (j > s.j0) join_scores(v.x, v.y, part->x, part->y);
+          *part = v;
         }
+      }
+      if (MODE == kApply) {
+        if (group == 1) {
+          s_sum[0][key0] = sum[0];
+          s_sum[1][key0] = sum[1];
+        }
+        __syncthreads();
+        if (group == 0)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (key + 64 * y < s.n) p.weights[at + 64 * y] = sum[y] + s_sum[y][key0];
       }
     }
   }
@@ -774,33 +862,75 @@ __global__ void __launch_bounds__(256) pva_weights_rows_kernel(WeightsParams p) 
   }
 }
 
-// Weights from kept scores: a CTA a run of key tiles, a thread a key.
-__global__ void __launch_bounds__(kKeys) pva_weights_scores_kernel(WeightsParams p) {
+// Weights from kept scores: a warp a run of key tiles, a lane every 32nd key of a tile.
+// The rows' maxima and sums are joined from the pieces' by the warp itself, anew for
+// each (sequence, kv head) of its run, eight lanes a row at a time.
+constexpr int kScoreWarps = 4, kStoreRows = 16;
+__global__ void __launch_bounds__(32 * kScoreWarps) pva_weights_scores_kernel(WeightsParams p) {
   allow_next_grid();
-  wait_prior_grid();
-  __shared__ float2 s_rows[16];
-  const int places = p.hdr[1], tid = threadIdx.x, R = p.T * p.G;
-  const int run = (places + gridDim.x - 1) / gridDim.x;
-  int x = blockIdx.x * run;
+  __shared__ float2 s_rows[kScoreWarps][kStoreRows];
+  // The kernel before this one let it start when all work before the scores was done:
+  // only the scores and the rows' sums have to be waited for.
+  const int places = p.hdr[1], lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = p.T * p.G;
+  const int warps = gridDim.x * kScoreWarps, run = (places + warps - 1) / warps, chunk = p.hdr[2];
+  int x = (blockIdx.x * kScoreWarps + warp) * run;
   const int end = min(x + run, places);
-  int last_item = -1;
-  for (int b = x < end ? tree_find(p.start, p.B, x) : 0; x < end; ++x) {
-    while (p.start[b + 1] <= x) ++b;
+  const float NEG_INF = __int_as_float(0xff800000);
+  float2* rows = s_rows[warp];
+  int last_item = -1, b = x < end ? tree_find(p.start, p.B, x) : 0, h = 0, k0 = 0, n = 0, used = 0, tiles = 0;
+  float sum[4];
+  auto look_up = [&](int tile) {
+    while (p.start[b + 1] <= tile) ++b;
     const Sequence s(p, b);
-    const int rel = x - p.start[b], h = rel / s.tiles, key = (rel - h * s.tiles) * kKeys + tid;
-    const int used = s.q * p.G, item = b * p.Hkv + h;
+    const int rel = tile - p.start[b];
+    tiles = s.tiles;
+    h = rel / tiles;
+    k0 = (rel - h * tiles) * kKeys;
+    n = s.n;
+    used = s.q * p.G;
+    const float* old = p.previous + (size_t)(b * p.Hkv + h) * p.width + k0 + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] = p.previous && k0 + lane + 32 * k < n ? p.decay * old[32 * k] : 0.0f;
+  };
+  if (x < end) look_up(x);
+  wait_prior_grid();
+  for (; x < end; ++x) {
+    const int item = b * p.Hkv + h;
+    const float* score = p.scores + (long long)x * R * kKeys + lane;
     if (item != last_item) {
-      __syncthreads();
-      if (tid < used) s_rows[tid] = p.row[(size_t)item * R + tid];
-      __syncthreads();
+      const int first = (p.start[b] + h * tiles) / chunk, pieces = (p.start[b] + (h + 1) * tiles - 1) / chunk - first + 1;
+      __syncwarp();
+      for (int r0 = 0; r0 < used; r0 += 4) {
+        const int r = r0 + lane / 8;
+        float m = NEG_INF, l = 0.0f;
+        if (r < used)
+          for (int i = lane % 8; i < pieces * p.parts; i += 8) {
+            const float2 v = p.part[((size_t)(item + first) * p.parts + i) * R + r];
+            join_scores(m, l, v.x, v.y);
+          }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+          join_scores(m, l, m2, l2);
+        }
+        // a row that saw nothing weighs nothing
+        if (r < used && lane % 8 == 0) rows[r] = l == 0.0f ? make_float2(-NEG_INF, 0.0f) : make_float2(m, 1.0f / l);
+      }
+      __syncwarp();
       last_item = item;
     }
-    if (key >= s.n) continue;
-    const size_t at = (size_t)item * p.width + key;
-    float sum = p.previous ? p.decay * p.previous[at] : 0.0f;
-    const float* score = p.scores + (long long)x * R * kKeys + tid;
-    for (int r = 0; r < used; ++r) sum = fmaf(ex2_approx((score[r * kKeys] - s_rows[r].x) * kLog2e), s_rows[r].y, sum);
-    p.weights[at] = sum;
+#pragma unroll 4
+    for (int r = 0; r < used; ++r) {
+      const float2 w = rows[r];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sum[k] = fmaf(ex2_approx((score[r * kKeys + 32 * k] - w.x) * kLog2e), w.y, sum[k]);
+    }
+    float* to = p.weights + (size_t)item * p.width + k0 + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k0 + lane + 32 * k < n) to[32 * k] = sum[k];
+    if (x + 1 < end) look_up(x + 1);
   }
 }
 
@@ -838,9 +968,11 @@ cudaError_t launch_type(const WeightsParams& p, int mode, int n, const CUtensorM
 template <int MODE>
 cudaError_t launch_f32(const WeightsParams& p, cudaStream_t s) {
   const size_t smem = f32_smem(p.d);
-  cudaError_t e = cudaFuncSetAttribute(pva_weights_f32_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const bool wide = p.d % 4 == 0 && (((uintptr_t)p.q | (uintptr_t)p.k_cache) & 15) == 0;
+  auto kern = wide ? pva_weights_f32_kernel<MODE, true> : pva_weights_f32_kernel<MODE, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(pva_weights_f32_kernel<MODE>, dim3(p.pieces), dim3(kKeys), smem, s, p);
+  return launch_dependent(kern, dim3(p.pieces), dim3(kThreadsF32), smem, s, p);
 }
 
 int weights(const void* q, const void* k_cache, const int32_t* lens, const int32_t* q_lens, const int32_t* table,
@@ -920,7 +1052,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   std::lock_guard<std::mutex> lock(api_mutex());
   int rc = sm_count(&p.pieces);
   if (rc != PVA_OK) return rc;
-  if (!tc) p.pieces *= d <= 128 ? 3 : 1;
+  if (!tc) p.pieces *= (int)((228 * 1024) / (f32_smem(d) + 3072));  // CTAs an SM holds
   size_t used = 0;
   auto take = [&](size_t bytes) {
     const size_t at = used;
@@ -928,7 +1060,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
     return at;
   };
   const size_t at_hdr = take(32), at_start = take(4 * ((size_t)B + 1));
-  p.parts = !tc ? 1 : store ? 8 : 2;
+  p.parts = !tc ? 1 : store ? 4 * kGroups : kGroups;
   const size_t at_part = take(lse ? 0 : 8 * ((size_t)B * Hkv + p.pieces) * p.parts * R);
   const size_t at_row = take(lse ? 0 : 8 * (size_t)B * Hkv * R);
   const size_t tiles = ((size_t)(width < (long long)max_blocks * page ? width : (long long)max_blocks * page) + kKeys - 1) / kKeys;
@@ -958,11 +1090,13 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   };
   if (!lse) {
     if ((e = pass(store ? kStore : kStats)) != cudaSuccess) return cuda_fail(e, "row sums launch");
+  }
+  if (!lse && !store) {
     const long long want = ((long long)B * Hkv * R + 7) / 8;
     e = launch_dependent(pva_weights_rows_kernel, dim3((unsigned)(want < 4096 ? want : 4096)), dim3(256), 0, stream, p);
     if (e != cudaSuccess) return cuda_fail(e, "row sums launch");
   }
-  e = store ? launch_dependent(pva_weights_scores_kernel, dim3(c.num_sms * 16), dim3(kKeys), 0, stream, p) : pass(kApply);
+  e = store ? launch_dependent(pva_weights_scores_kernel, dim3(c.num_sms * 16), dim3(32 * kScoreWarps), 0, stream, p) : pass(kApply);
   return e == cudaSuccess ? PVA_OK : cuda_fail(e, "weights launch");
 }
 
