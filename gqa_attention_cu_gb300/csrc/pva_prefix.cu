@@ -85,7 +85,16 @@ __global__ void __launch_bounds__(kFrontThreads) pva_prefix_front_kernel(PrefixP
     p.tile_start[E] = all;
     p.hdr[0] = ok;
     p.hdr[1] = all;
-    p.hdr[2] = even > p.min_chunk ? even : p.min_chunk;
+    int chunk = even > p.min_chunk ? even : p.min_chunk;
+    // One prefix of several query tiles: where it costs little, its items are all cut
+    // alike, so that the CTAs of the same keys read them at the same time, from L2.
+    const PrefixEntry head = prefix_entry(p, 0);
+    const int per = head.places(p);
+    if (ok && p.P == 1 && head.q_tiles(p) > 1 && per > chunk) {
+      const int alike = (per + per / chunk - 1) / (per / chunk);
+      if (alike <= chunk + chunk / 8) chunk = alike;
+    }
+    p.hdr[2] = chunk;
   }
 }
 
@@ -108,9 +117,8 @@ __global__ void __launch_bounds__(256) pva_prefix_join_kernel(PrefixParams p) {
   const bool used = t < tree_nodes(p, b);
   const float NEG_INF = __int_as_float(0xff800000);
   // parts of kind 0 (the prefix) and 1 (own rows): the item's places and pieces
-  int first[2] = {0, 0}, parts[2] = {0, 0}, in_tile[2], per[2], seen[2];
-  long long x0[2];
-  const long long chunk = p.hdr[2];
+  int first[2] = {0, 0}, parts[2] = {0, 0}, in_tile[2], per[2], seen[2], x0[2];
+  const int chunk = p.hdr[2];
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
     const int e = kind ? p.P + b : p.prefix_start ? tree_find(p.prefix_start, p.P, b) : 0;
@@ -120,9 +128,9 @@ __global__ void __launch_bounds__(256) pva_prefix_join_kernel(PrefixParams p) {
     const int row = (tok - entry.tok0) * p.G + g, qt = row / p.rows;
     in_tile[kind] = row - qt * p.rows;
     seen[kind] = entry.seen(p, qt);
-    x0[kind] = p.tile_start[e] + ((long long)h * entry.q_tiles(p) + qt) * per[kind];
-    first[kind] = (int)(x0[kind] / chunk);
-    parts[kind] = (int)((x0[kind] + per[kind] - 1) / chunk) - first[kind] + 1;
+    x0[kind] = p.tile_start[e] + (h * entry.q_tiles(p) + qt) * per[kind];
+    first[kind] = x0[kind] / chunk;
+    parts[kind] = (x0[kind] + per[kind] - 1) / chunk - first[kind] + 1;
   }
   // the place of part i, or -1 where a piece holds none of the item's tiles
   auto place = [&](int i) -> long long {
@@ -130,11 +138,10 @@ __global__ void __launch_bounds__(256) pva_prefix_join_kernel(PrefixParams p) {
     const int c = kind ? i - parts[0] : i;
     if (parts[kind] == 1) return p.row_at + (kind ? (long long)p.B * p.T * p.H : 0ll) + at_row;
     const int piece = first[kind] + c;
-    const long long begin = (long long)piece * chunk - x0[kind];  // places of the item before the piece
-    const int into = begin > 0 ? (int)begin : 0;
-    const int take = (int)(min((long long)per[kind], begin + chunk) - into);
+    const int begin = piece * chunk - x0[kind];  // places of the item before the piece
+    const int into = max(begin, 0), take = min(per[kind], begin + chunk) - into;
     int from, to;
-    prefix_tiles(p, into, take, seen[kind], from, to);
+    prefix_tiles(p, !kind, into, take, seen[kind], from, to);
     return from < to ? (long long)tree_slot(piece, into == 0) * p.rows + in_tile[kind] : -1ll;
   };
   const int n = parts[0] + parts[1];
@@ -261,14 +268,20 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
   if (p.softcap != 0.0f) {  // as in pva_gqa_tree
     const double cap = p.softcap, t = fmin(0.25, pow(ldexp(1.0, -14) * 315.0 / 17.0 / cap, 1.0 / 7.0));
     p.series_to = (float)fmin(t * cap / fabs(p.scale), 1e9);
+    p.mid_to = (float)fmin(tile::kMidTanh * cap / fabs(p.scale), 1e9);
   }
   p.q_parts = 1;
   const long long R = (long long)B * T * G;
   p.tile_rows = tc ? G * (kTcRows / G) : R <= 8 ? 8 : R <= 16 ? 16 : 24;
-  p.rows = p.tile_rows;
-  p.item_places = 2;
+  p.own_rows = tc && (long long)T * G < p.tile_rows ? T * G : p.tile_rows;
+  const bool pair = tc && d <= 192 && R > 2 * p.tile_rows && p.softcap == 0.0f;
+  p.rows = pair ? 2 * p.tile_rows : p.tile_rows;
   p.bn = tc ? tree_keys(d) : kTreeKeysF32;
-  p.min_chunk = 2;
+  p.tile_cost[0] = 4;
+  p.tile_cost[1] = pair ? 5 : 4;
+  p.item_cost[0] = 8;
+  p.item_cost[1] = 16;
+  p.min_chunk = 2 * p.tile_cost[0];  // two key tiles, as in pva_gqa_tree
   p.q = const_cast<void*>(q);
   p.k_cache = k_cache;
   p.v_cache = v_cache;
@@ -297,19 +310,23 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
   p.tile_start = reinterpret_cast<int32_t*>(c.buf + at_start);
   p.part_o = reinterpret_cast<float*>(c.buf + at_o);
   p.part_ml = reinterpret_cast<float2*>(c.buf + at_ml);
-  CUtensorMap tq, tk, tv;
+  PrefixQueries tq;
+  CUtensorMap tk, tv;
   if (tc) {
     const int box = block_table && page_size < p.bn ? page_size : p.bn;
     const long long planes = (long long)n_blocks * Hkv;
     if ((rc = get_encoder()) != PVA_OK ||
-        (rc = encode_rows_map(&tq, q, dtype, d, H, (long long)B * T, G, kTcRows / G)) != PVA_OK ||
+        (rc = encode_rows_map(&tq.tile, q, dtype, d, H, (long long)B * T, G, p.tile_rows / G)) != PVA_OK ||
+        (rc = encode_rows_map(&tq.own, q, dtype, d, H, (long long)B * T, G, p.own_rows / G)) != PVA_OK ||
         (rc = encode_plane_map(&tk, k_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK ||
         (rc = encode_plane_map(&tv, v_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK)
       return rc;
   }
   cudaError_t e = launch_dependent(pva_prefix_front_kernel, dim3(P + B), dim3(kFrontThreads), 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "prefix front-end launch");
-  e = tc ? launch_prefix_tc(p, dtype, tq, tk, tv, stream) : f32::launch<PrefixWork>(p, stream);
+  e = pair ? launch_prefix_pair(p, dtype, tq, tk, tv, stream)
+      : tc ? launch_prefix_tc(p, dtype, tq, tk, tv, stream)
+           : f32::launch<PrefixWork>(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
   e = dtype == PVA_BF16 ? launch_join<__nv_bfloat16, 4>(p, stream)
       : dtype == PVA_F16 ? launch_join<__half, 4>(p, stream)

@@ -26,9 +26,16 @@ struct PrefixParams : TreeParams {
   const int32_t* prefix_table;  // [P, prefix_blocks], or nullptr: block B + p
   int P, prefix_blocks;
   int tile_rows;                // query rows of an MMA tile: G times tokens
+  int own_rows;                 // of them, those that a sequence of T tokens can have
+  int tile_cost[2], item_cost[2];  // places of a key tile and of an item besides: own rows, prefix
   int negated;                  // a negative scale (tensor cores: as the sign of q)
   long long row_at;             // part_o's and part_ml's first row place, behind the slots
   float* lse;                   // [B, T, H], or nullptr
+};
+
+// Boxes of q: a tile's tokens, and no more than a sequence has (decoding: 1 of 32).
+struct alignas(64) PrefixQueries {
+  CUtensorMap tile, own;
 };
 
 // What an entry comes to.
@@ -40,7 +47,7 @@ struct PrefixEntry {
   __host__ __device__ int tiles(const PrefixParams& p) const { return (keys + p.bn - 1) / p.bn; }
   // places of one of its items
   __host__ __device__ int places(const PrefixParams& p) const {
-    return n > 0 && keys > 0 ? tiles(p) + p.item_places : 0;
+    return n > 0 && keys > 0 ? tiles(p) * p.tile_cost[all] + p.item_cost[all] : 0;
   }
   __host__ __device__ long long per_head(const PrefixParams& p) const {
     return (long long)q_tiles(p) * places(p);
@@ -53,10 +60,13 @@ struct PrefixEntry {
   }
 };
 
-// The key tiles [from, to) that places [into, into + take) of an item stand for.
-__host__ __device__ inline void prefix_tiles(const PrefixParams& p, int into, int take, int seen, int& from, int& to) {
-  from = into > p.item_places ? into - p.item_places : 0;
-  to = into + take > p.item_places ? into + take - p.item_places : 0;
+// The key tiles [from, to) that begin in the places [into, into + take) of an item:
+// first its fixed cost, then tile after tile.
+__host__ __device__ inline void prefix_tiles(const PrefixParams& p, int all, int into, int take, int seen, int& from,
+                                             int& to) {
+  const int item = p.item_cost[all], tile = p.tile_cost[all];
+  from = into > item ? (into - item + tile - 1) / tile : 0;
+  to = into + take > item ? (into + take - item + tile - 1) / tile : 0;
   if (to > seen) to = seen;
 }
 
@@ -77,39 +87,54 @@ __device__ __forceinline__ PrefixEntry prefix_entry(const PrefixParams& p, int e
   return x;
 }
 
-// A CTA's segments: those of its piece of the line.
+// A CTA's segments: those of its piece of the line.  An entry is looked up once for
+// all of its kv heads.
 struct PrefixWalk {
-  int piece, chunk;
-  long long x, end;
-  int e;
-  __device__ __forceinline__ PrefixWalk(const PrefixParams& p, int piece_) : piece(piece_), e(-1) {
-    const int places = p.hdr[1];
-    chunk = p.hdr[2];
-    x = (long long)piece * chunk;
-    end = x + chunk < places ? x + chunk : places;
+  int piece, x, end;
+  int e, start, stop;  // the entry at x and its places [start, stop)
+  PrefixEntry entry;
+  int per, qt, h, t, into;  // places of an item, q tiles; the item at x, places of it before x
+  __device__ __forceinline__ PrefixWalk(const PrefixParams& p, int piece_) : piece(piece_), e(-1), stop(0) {
+    const int places = p.hdr[1], chunk = p.hdr[2];
+    const long long from = (long long)piece * chunk;
+    x = (int)(from < places ? from : places);
+    end = from + chunk < places ? (int)(from + chunk) : places;
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, PrefixSegment& s) {
     while (x < end) {
-      if (e < 0) e = tree_find(p.tile_start, p.P + p.B, (int)x);
-      while (p.tile_start[e + 1] <= x) ++e;
-      const PrefixEntry entry = prefix_entry(p, e);
-      const int per = entry.places(p), qt = entry.q_tiles(p), rel = (int)x - p.tile_start[e];
-      const int item = rel / per, into = rel - item * per;
-      const int take = (int)(end - x < per - into ? end - x : per - into);
+      if (x >= stop) {
+        if (e < 0) e = tree_find(p.tile_start, p.P + p.B, x);
+        else ++e;
+        while ((stop = p.tile_start[e + 1]) <= x) ++e;
+        start = p.tile_start[e];
+        entry = prefix_entry(p, e);
+        per = entry.places(p);
+        qt = entry.q_tiles(p);
+        const int item = (x - start) / per;
+        into = x - start - item * per;
+        h = item / qt;
+        t = item - h * qt;
+      }
+      const int take = end - x < per - into ? end - x : per - into;
       s.b = e;
-      s.h = item / qt;
-      s.t = item - s.h * qt;
+      s.h = h;
+      s.t = t;
       s.all = entry.all;
       s.tok0 = entry.tok0;
       s.n = entry.n;
       s.past = entry.all ? entry.keys : entry.keys - entry.n;
       s.lo = 0;
       int to;
-      prefix_tiles(p, into, take, entry.seen(p, s.t), s.j0, to);
+      prefix_tiles(p, entry.all, into, take, entry.seen(p, t), s.j0, to);
       s.count = to - s.j0;
       s.slot = take == per ? -1 : tree_slot(piece, into == 0);
       s.parts = 0;
       x += take;
+      into = 0;  // (after the last piece of an item, or at the end)
+      if (++t == qt) {
+        t = 0;
+        ++h;
+      }
       if (s.count > 0) return true;
     }
     return false;
@@ -126,10 +151,17 @@ struct PrefixWork {
     const int b = s.b - p.P;
     return p.table ? p.table[(size_t)b * p.max_blocks + in] : b;
   }
-  static __device__ __forceinline__ uint32_t q_bytes(const Params& p) { return (uint32_t)p.tile_rows * 128u; }
+  using Queries = PrefixQueries;
+  static __device__ __forceinline__ void prefetch(const Queries& maps) {
+    prefetch_tensor_map(&maps.tile);
+    prefetch_tensor_map(&maps.own);
+  }
+  static __device__ __forceinline__ uint32_t q_bytes(const Params& p, const Segment& s) {
+    return (uint32_t)(s.all ? p.tile_rows : p.own_rows) * 128u;
+  }
   static __device__ __forceinline__ void load_q(const Params& p, const Segment& s, int y, int, void* dst,
-                                                const CUtensorMap* map, uint64_t* bar, int c) {
-    tma_load_3d(dst, map, bar, c * 64, s.h * p.G, s.tok0 + (s.t * p.rows + y * p.tile_rows) / p.G);
+                                                const Queries& maps, uint64_t* bar, int c) {
+    tma_load_3d(dst, s.all ? &maps.tile : &maps.own, bar, c * 64, s.h * p.G, s.tok0 + (s.t * p.rows + y * p.tile_rows) / p.G);
   }
   static __device__ __forceinline__ uint32_t negate(const Params& p) { return p.negated ? 1u << 13 : 0u; }
   static __device__ __forceinline__ int row(const Params& p, const Segment& s, int y, int r) {
@@ -143,6 +175,7 @@ struct PrefixWork {
     return tok % p.T < p.lens[tok / p.T];
   }
   static __device__ __forceinline__ bool counts(bool own) { return own; }
+  static constexpr bool kMid = true;
   static __device__ __forceinline__ tile::RowView view(const Params& p, const Segment& s, int node) {
     return {0, s.all ? s.past : s.past + node + 1, nullptr};
   }
@@ -183,7 +216,10 @@ struct PrefixWork {
 };
 #endif
 
-cudaError_t launch_prefix_tc(const PrefixParams& p, int dtype, const CUtensorMap& tq, const CUtensorMap& tk,
+cudaError_t launch_prefix_tc(const PrefixParams& p, int dtype, const PrefixQueries& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t s);
+// Two query tiles per item (p.rows = 2 p.tile_rows), head sizes up to 192.
+cudaError_t launch_prefix_pair(const PrefixParams& p, int dtype, const PrefixQueries& tq, const CUtensorMap& tk,
+                               const CUtensorMap& tv, cudaStream_t s);
 
 }  // namespace pva

@@ -8,7 +8,7 @@ namespace {
 using namespace one_tile;
 
 template <typename T, int D>
-cudaError_t launch_d(const PrefixParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_d(const PrefixParams& p, const PrefixQueries& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t s) {
   constexpr int smem = TreeCfg<D>::SMEM;
   const int cap = cap_form(p.softcap);
@@ -21,7 +21,7 @@ cudaError_t launch_d(const PrefixParams& p, const CUtensorMap& tq, const CUtenso
 }
 
 template <typename T>
-cudaError_t launch_type(const PrefixParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_type(const PrefixParams& p, const PrefixQueries& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t s) {
   switch (p.d) {
     case 64: return launch_d<T, 64>(p, tq, tk, tv, s);
@@ -35,7 +35,7 @@ cudaError_t launch_type(const PrefixParams& p, const CUtensorMap& tq, const CUte
 
 }  // namespace
 
-cudaError_t launch_prefix_tc(const PrefixParams& p, int dtype, const CUtensorMap& tq, const CUtensorMap& tk,
+cudaError_t launch_prefix_tc(const PrefixParams& p, int dtype, const PrefixQueries& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t s) {
   return dtype == PVA_BF16 ? launch_type<__nv_bfloat16>(p, tq, tk, tv, s) : launch_type<__half>(p, tq, tk, tv, s);
 }

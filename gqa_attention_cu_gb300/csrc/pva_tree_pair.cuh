@@ -90,7 +90,7 @@ __device__ __forceinline__ bool has_second(const typename W::Params& p, const ty
 
 template <typename T, int D, int PARTS, int CAP, typename W>
 __global__ void __launch_bounds__(kThreads, 1)
-    pva_tree_pair_kernel(typename W::Params p, const __grid_constant__ CUtensorMap tmap_q,
+    pva_tree_pair_kernel(typename W::Params p, const __grid_constant__ typename W::Queries tmap_q,
                          const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v) {
   using C = PairCfg<D, PARTS>;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc<C::TMEM_COLS>(&bars->tmem_base);
   if (warp == 0 && lane == 0) {
-    prefetch_tensor_map(&tmap_q);
+    W::prefetch(tmap_q);
     prefetch_tensor_map(&tmap_k);
     prefetch_tensor_map(&tmap_v);
   }
@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(&bars->q_empty, (q_loads & 1) ^ 1))) break;
       if (lane == 0) {
         const int n_q = has_second<W>(p, s) ? 2 : 1;
-        mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(n_q * PARTS * C::CH) * W::q_bytes(p));
+        mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(n_q * PARTS * C::CH) * W::q_bytes(p, s));
         for (int part = 0; part < PARTS; ++part)
           for (int y = 0; y < n_q; ++y)
             for (int c = 0; c < C::CH; ++c)
-              W::load_q(p, s, y, part, smem + (2 * part + y) * C::Q_TILE + c * C::Q_CHUNK, &tmap_q,
+              W::load_q(p, s, y, part, smem + (2 * part + y) * C::Q_TILE + c * C::Q_CHUNK, tmap_q,
                         &bars->q_full, c);
       }
       __syncwarp();
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any_own) {
           tc_fence_after();
           float alpha;
-          softmax_columns<T, BN, CAP>(p, view, s.past, k0, t_s, s_mul, cap_mul, W::counts(own), alone, st,
+          softmax_columns<T, BN, CAP, W::kMid>(p, view, s.past, k0, t_s, s_mul, cap_mul, W::counts(own), alone, st,
                                       alpha);
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             // O must hold PV(j-1); every earlier phase has passed, since S(j)

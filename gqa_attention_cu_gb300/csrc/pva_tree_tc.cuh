@@ -98,7 +98,7 @@ static_assert(sizeof(Bars<TreeWork>) <= kHeadBytes, "barriers, segments and meet
 
 template <typename T, int D, int CAP, typename W>
 __global__ void __launch_bounds__(kThreads, 1)
-    pva_tree_tc_kernel(typename W::Params p, const __grid_constant__ CUtensorMap tmap_q,
+    pva_tree_tc_kernel(typename W::Params p, const __grid_constant__ typename W::Queries tmap_q,
                        const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v) {
   using C = TreeCfg<D>;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc<C::TMEM_COLS>(&bars->tmem_base);
   if (warp == 0 && lane == 0) {
-    prefetch_tensor_map(&tmap_q);
+    W::prefetch(tmap_q);
     prefetch_tensor_map(&tmap_k);
     prefetch_tensor_map(&tmap_v);
   }
@@ -183,9 +183,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const int part = qs / C::Q_SLOTS, c_lo = (qs % C::Q_SLOTS) * C::Q_PER_SLOT;
           const int c_hi = min(C::CH, c_lo + C::Q_PER_SLOT);
-          mbar_arrive_expect_tx(&bars->ring_full[sl], (uint32_t)(c_hi - c_lo) * W::q_bytes(p));
+          mbar_arrive_expect_tx(&bars->ring_full[sl], (uint32_t)(c_hi - c_lo) * W::q_bytes(p, s));
           for (int c = c_lo; c < c_hi; ++c)
-            W::load_q(p, s, 0, part, smem + sl * C::KV_TILE + (c - c_lo) * C::Q_CHUNK, &tmap_q,
+            W::load_q(p, s, 0, part, smem + sl * C::KV_TILE + (c - c_lo) * C::Q_CHUNK, tmap_q,
                       &bars->ring_full[sl], c);
         }
         __syncwarp();
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars->rest_full, C::REST);
           for (int c = 0; c < C::CH; ++c)
-            W::load_q(p, s, 0, 1, smem + C::OFF_REST + c * C::Q_CHUNK, &tmap_q, &bars->rest_full, c);
+            W::load_q(p, s, 0, 1, smem + C::OFF_REST + c * C::Q_CHUNK, tmap_q, &bars->rest_full, c);
         }
         __syncwarp();
         ++rests;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t t_s = t_lane + C::COL_S + (T_ & 1) * BN + half * (BN / 2);
           float alpha;
-          ok = softmax_columns<T, BN / 2, CAP>(p, view, s.past, k0 + half * (BN / 2), t_s, s_mul, cap_mul,
+          ok = softmax_columns<T, BN / 2, CAP, W::kMid>(p, view, s.past, k0 + half * (BN / 2), t_s, s_mul, cap_mul,
                                             W::counts(own), pair, st, alpha);
           if (!ok) break;
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {

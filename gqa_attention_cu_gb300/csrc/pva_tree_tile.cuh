@@ -41,6 +41,21 @@ __device__ __forceinline__ float tanh_of(float t) {
   return fabsf(t) <= 0.25f ? fmaf(t * w, p, t) : tanh_via_exp2(t);
 }
 
+// c tanh(t) + add for |t| <= kMidTanh: the odd polynomial of degree 9 that is nearest
+// to tanh there (fitted for the least largest error, 1.86e-7; times a softcap of
+// kCapOfExp that is below 2^-14, as the other forms' errors are).  Seven packed
+// instructions for two scores where exp takes four of the special-function unit's.
+constexpr float kMidTanh = 0.75f;
+__device__ __forceinline__ float2 mid_tanh(float2 t, float c, float2 add) {
+  auto both = [](float x) { return make_float2(x, x); };
+  const float2 w = ffma2(t, t, both(0.0f));
+  float2 p = ffma2(w, both(c * 0.012318834077f), both(c * -0.049280449660f));
+  p = ffma2(w, p, both(c * 0.132260917113f));
+  p = ffma2(w, p, both(c * -0.333230764944f));
+  p = ffma2(w, p, both(c * 0.999997228324f));
+  return ffma2(t, p, add);
+}
+
 // Whether a row sees key c of 32, from its mask (one bit per key).
 template <bool MASKED>
 __device__ __forceinline__ bool seen(uint32_t mask, int c) {
@@ -106,7 +121,7 @@ __device__ __forceinline__ void extremes(const uint32_t (&v)[32], uint32_t m, fl
 
 // 2^(x - m) of 32 scores, added to the two partial sums, and P as 16-bit pairs.
 // MODE 0: x = s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by the
-// series' three terms (1), by exp (2) or by tanh_of (3).  P is rounded to the
+// series' three terms (1), by exp (2), by tanh_of (3) or by mid_tanh (4).  P is rounded to the
 // storage type for the tensor-core product: at most half a step of each weight, as
 // V's own elements carry; the row sum adds the fp32 values.
 template <typename T, int MODE, bool MASKED>
@@ -132,6 +147,8 @@ __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], uint32_t m
       } else if (MODE == 1) {
         const float2 w = ffma2(s, s, z);
         x[k] = ffma2(s, ffma2(w, ffma2(w, c5, c3), c1), neg_m);
+      } else if (MODE == 4) {
+        x[k] = mid_tanh(ffma2(s, mul2, z), cap_mul, neg_m);
       } else if (MODE == 2) {
         x[k].x = fmaf(cap_mul, tanh_via_exp2(s.x * s_mul), -m_eff);
         x[k].y = fmaf(cap_mul, tanh_via_exp2(s.y * s_mul), -m_eff);
@@ -231,7 +248,9 @@ __device__ __forceinline__ bool misplaced(const void* smem, const typename W::Pa
 // issue slots are 40% full, the tensor pipe 31%, memory 6%.  Any instruction more
 // lengthens the chain: a quarter of the exponentials by a polynomial on the FMA pipe
 // made them 203 us.
-template <typename T, int N, int CAP, typename Row>
+// MID: between the series and exp there is a third form of the softcap (scores up to
+// p.mid_to).
+template <typename T, int N, int CAP, bool MID, typename Row>
 __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowView& view, int past,
                                                 int k0, uint32_t t_s, float s_mul, float cap_mul,
                                                 bool counts, Row& others, RowState& st, float& alpha) {
@@ -258,9 +277,10 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
     return true;
   };
   // a softcap's series has to hold for the warp's own columns
-  auto small_scores = [&]() {
-    return CAP && __all_sync(0xffffffffu, !counts || mx == NEG_INF || fmaxf(fabsf(mx), fabsf(mn)) <= p.series_to);
+  auto small_scores = [&](float to) {
+    return CAP && __all_sync(0xffffffffu, !counts || mx == NEG_INF || fmaxf(fabsf(mx), fabsf(mn)) <= to);
   };
+  bool mid = false;
   float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   bool series, done = false;
   if (all) {
@@ -272,7 +292,8 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       tmem_wait_ld_of(v[c]);
       extremes<false, CAP>(v[c], 0u, mx, mn);
     }
-    series = small_scores();
+    series = small_scores(p.series_to);
+    if (MID && CAP == kCap && !series) mid = small_scores(p.mid_to);
     if (!new_maximum()) return false;
     if (!CAP || series) {
       done = true;
@@ -280,6 +301,14 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       for (int c = 0; c < N / 32; ++c) {
         uint32_t pw[16];
         exponentials<T, CAP ? 1 : 0, false>(v[c], 0u, s_mul, cap_mul, m_eff, acc, pw);
+        tmem_st16(t_s + c * 16, pw);
+      }
+    } else if (MID && CAP == kCap && mid) {
+      done = true;
+#pragma unroll
+      for (int c = 0; c < N / 32; ++c) {
+        uint32_t pw[16];
+        exponentials<T, 4, false>(v[c], 0u, s_mul, cap_mul, m_eff, acc, pw);
         tmem_st16(t_s + c * 16, pw);
       }
     }
@@ -292,7 +321,8 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       tmem_wait_ld_of(v);
       extremes<true, CAP>(v, mask, mx, mn);
     }
-    series = small_scores();
+    series = small_scores(p.series_to);
+    if (MID && CAP == kCap && !series) mid = small_scores(p.mid_to);
     if (!new_maximum()) return false;
   }
   if (!done) {
@@ -305,6 +335,8 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       uint32_t pw[16];
       if (!CAP)
         exponentials<T, 0, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
+      else if (MID && CAP == kCap && mid)
+        exponentials<T, 4, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       else if (series)
         exponentials<T, 1, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       else
@@ -445,10 +477,12 @@ struct TreeWork {
     return p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
   }
   // bytes of 64 columns of a query tile, and their copy (tile y of the item, part of the queries)
-  static __device__ __forceinline__ uint32_t q_bytes(const Params&) { return kTcRows * 128; }
+  using Queries = CUtensorMap;
+  static __device__ __forceinline__ void prefetch(const Queries& map) { prefetch_tensor_map(&map); }
+  static __device__ __forceinline__ uint32_t q_bytes(const Params&, const Segment&) { return kTcRows * 128; }
   static __device__ __forceinline__ void load_q(const Params& p, const Segment& s, int y, int part,
-                                                void* dst, const CUtensorMap* map, uint64_t* bar, int c) {
-    tma_load_3d(dst, map, bar, c * 64, s.t * p.rows + y * kTcRows, (part * p.B + s.b) * p.Hkv + s.h);
+                                                void* dst, const Queries& map, uint64_t* bar, int c) {
+    tma_load_3d(dst, &map, bar, c * 64, s.t * p.rows + y * kTcRows, (part * p.B + s.b) * p.Hkv + s.h);
   }
   static __device__ __forceinline__ uint32_t negate(const Params&) { return 0u; }
   // the query row (of the sequence's on this kv head) that MMA row r of tile y is
@@ -460,6 +494,7 @@ struct TreeWork {
   }
   // rows of no node are zeros beside others (RopeStep) and so are their scores
   static __device__ __forceinline__ bool counts(bool) { return true; }
+  static constexpr bool kMid = false;
   static __device__ __forceinline__ RowView view(const Params& p, const Segment& s, int node) {
     return row_view(p, s, node);
   }
