@@ -107,30 +107,31 @@ __global__ void __launch_bounds__(256) pva_prefix_join_kernel(PrefixParams p) {
   struct alignas(4 * V) Part { float v[V]; };
   struct alignas(sizeof(T) * V) Out { T v[V]; };
   allow_next_grid();
-  wait_prior_grid();
-  if (!p.hdr[0]) return;
+  // The attention let this kernel start when all work before it was done: only its sums
+  // have to be waited for.
   const int lane = threadIdx.x & 31;
   const long long at_row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // (token of the batch, head)
   if (at_row >= (long long)p.B * p.T * p.H) return;
   const int tok = (int)(at_row / p.H), head = (int)(at_row - (long long)tok * p.H), b = tok / p.T, t = tok - b * p.T;
   const int h = head / p.G, g = head - h * p.G;
-  const bool used = t < tree_nodes(p, b);
   const float NEG_INF = __int_as_float(0xff800000);
   // parts of kind 0 (the prefix) and 1 (own rows): the item's places and pieces
   int first[2] = {0, 0}, parts[2] = {0, 0}, in_tile[2], per[2], seen[2], x0[2];
   const int chunk = p.hdr[2];
+  if (p.hdr[0] && t < tree_nodes(p, b)) {
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int e = kind ? p.P + b : p.prefix_start ? tree_find(p.prefix_start, p.P, b) : 0;
-    const PrefixEntry entry = prefix_entry(p, e);
-    per[kind] = entry.places(p);
-    if (!used || per[kind] == 0) continue;
-    const int row = (tok - entry.tok0) * p.G + g, qt = row / p.rows;
-    in_tile[kind] = row - qt * p.rows;
-    seen[kind] = entry.seen(p, qt);
-    x0[kind] = p.tile_start[e] + (h * entry.q_tiles(p) + qt) * per[kind];
-    first[kind] = x0[kind] / chunk;
-    parts[kind] = (x0[kind] + per[kind] - 1) / chunk - first[kind] + 1;
+    for (int kind = 0; kind < 2; ++kind) {
+      const int e = kind ? p.P + b : p.prefix_start ? tree_find(p.prefix_start, p.P, b) : 0;
+      const PrefixEntry entry = prefix_entry(p, e);
+      per[kind] = entry.places(p);
+      if (per[kind] == 0) continue;
+      const int row = (tok - entry.tok0) * p.G + g, qt = row / p.rows;
+      in_tile[kind] = row - qt * p.rows;
+      seen[kind] = entry.seen(p, qt);
+      x0[kind] = p.tile_start[e] + (h * entry.q_tiles(p) + qt) * per[kind];
+      first[kind] = x0[kind] / chunk;
+      parts[kind] = (x0[kind] + per[kind] - 1) / chunk - first[kind] + 1;
+    }
   }
   // the place of part i, or -1 where a piece holds none of the item's tiles
   auto place = [&](int i) -> long long {
@@ -145,10 +146,14 @@ __global__ void __launch_bounds__(256) pva_prefix_join_kernel(PrefixParams p) {
     return from < to ? (long long)tree_slot(piece, into == 0) * p.rows + in_tile[kind] : -1ll;
   };
   const int n = parts[0] + parts[1];
-  float m = NEG_INF;
-  for (int i = lane; i < n; i += 32) {
-    const long long at = place(i);
-    if (at >= 0) m = fmaxf(m, p.part_ml[at].x);
+  long long at = lane < n ? place(lane) : -1;  // of parts 0 .. 31
+  wait_prior_grid();
+  if (!*(volatile int32_t*)p.hdr) return;  // rejected, or given up
+  float2 ml = at >= 0 ? p.part_ml[at] : make_float2(NEG_INF, 0.0f);
+  float m = ml.x;
+  for (int i = 32 + lane; i < n; i += 32) {
+    const long long x = place(i);
+    if (x >= 0) m = fmaxf(m, p.part_ml[x].x);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -163,15 +168,13 @@ __global__ void __launch_bounds__(256) pva_prefix_join_kernel(PrefixParams p) {
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.0f;
     for (int i0 = 0; i0 < n; i0 += 32) {
-      float w = 0.0f, wl = 0.0f;
-      long long at = -1;
-      if (i0 + lane < n && (at = place(i0 + lane)) >= 0) {
-        const float2 v = p.part_ml[at];
-        w = exp2f(v.x - top);
-        wl = w * v.y;
+      if (n > 32) {
+        at = i0 + lane < n ? place(i0 + lane) : -1;
+        ml = at >= 0 ? p.part_ml[at] : make_float2(NEG_INF, 0.0f);
       }
+      const float w = exp2f(ml.x - top), wl = w * ml.y;  // 0 where there is no part
       const int k = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < k; ++i) {
         const long long from = __shfl_sync(0xffffffffu, at, i);
         const float wi = __shfl_sync(0xffffffffu, w, i);

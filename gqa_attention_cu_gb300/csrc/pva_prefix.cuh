@@ -176,6 +176,11 @@ struct PrefixWork {
   }
   static __device__ __forceinline__ bool counts(bool own) { return own; }
   static constexpr bool kMid = true;
+  // the join looks up at once what the front end has written
+  static __device__ __forceinline__ void start() {
+    wait_prior_grid();
+    allow_next_grid();
+  }
   static __device__ __forceinline__ tile::RowView view(const Params& p, const Segment& s, int node) {
     return {0, s.all ? s.past : s.past + node + 1, nullptr};
   }

@@ -54,8 +54,7 @@ __global__ void __launch_bounds__(kWarps * 32) pva_tree_f32_kernel(typename W::P
   float* sp = skv + 4 * kTile * stride;           // [kRows][36] weights
   __shared__ typename W::Segment s_segment;
   __shared__ int s_more;
-  allow_next_grid();
-  wait_prior_grid();
+  W::start();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float NEG_INF = __int_as_float(0xff800000);
   const float* kc = static_cast<const float*>(p.k_cache);

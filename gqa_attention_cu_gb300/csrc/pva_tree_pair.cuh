@@ -138,8 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  allow_next_grid();
-  wait_prior_grid();
+  W::start();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, abort, status));

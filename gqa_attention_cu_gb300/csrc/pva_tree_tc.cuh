@@ -149,8 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  allow_next_grid();
-  wait_prior_grid();
+  W::start();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer

@@ -495,6 +495,10 @@ struct TreeWork {
   // rows of no node are zeros beside others (RopeStep) and so are their scores
   static __device__ __forceinline__ bool counts(bool) { return true; }
   static constexpr bool kMid = false;
+  static __device__ __forceinline__ void start() {
+    allow_next_grid();
+    wait_prior_grid();
+  }
   static __device__ __forceinline__ RowView view(const Params& p, const Segment& s, int node) {
     return row_view(p, s, node);
   }
