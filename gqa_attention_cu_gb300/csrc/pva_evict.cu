@@ -44,14 +44,16 @@ struct EvictParams {
   int32_t* count;        // [items] rows that stay; workspace
   int32_t* length;       // [items] rows there were; -1: the sequence is left as it is
   int B, layers, Hkv, width, first, last, row_bytes;
+  int held;              // weights that the first kernel's shared memory has room for
   uint32_t* status;
 };
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 1024;  // at most; fewer for short rows of weights
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kPerThread = 8;
-constexpr int kSelectTile = kSelectThreads * kPerThread;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;  // half of them in the last count
+static_assert(kBins / 2 % kSelectThreads == 0, "whole bins a thread");
+constexpr int kHeld = 48 * 1024;  // weights that lie in shared memory after the first count
 
 // Rises with the weight; NaN is below every number, and -0 is 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -78,13 +80,28 @@ __device__ __forceinline__ uint32_t check_sequence(const EvictParams& p, int b, 
   return __syncthreads_or(off) ? PVA_DEV_BLOCKS : 0u;
 }
 
+// Sum of the counts of the warps before this one, and of all: every warp adds up by itself.
+__device__ __forceinline__ int warps_before(const int* counts, int warps, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mine = lane < warps ? counts[lane] : 0;
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  all = __shfl_sync(0xffffffffu, upto, 31);
+  return __shfl_sync(0xffffffffu, upto - mine, warp);
+}
+
 __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictParams p) {
   allow_next_grid();
   wait_prior_grid();
+  extern __shared__ float s_held[];
   __shared__ int s_bins[kBins];
   __shared__ int s_warp[kSelectWarps];
   __shared__ int s_bin, s_above;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads / 32;
   const int item = blockIdx.x, b = item / p.Hkv % p.B;
   const int n = p.lens[b], keep = p.keep[b];
   const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
@@ -108,25 +125,60 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
   const int lo = head, hi = n - tail;
   const int want = stay - head - tail;  // of the rows [lo, hi)
   // The key of the lightest row that stays, bit by bit from the top: `above` of the
-  // rows are heavier than all that share the bits found so far.
+  // rows are heavier than all that share the bits found so far.  The first count is
+  // made while the weights come in, the others go over shared memory, four a thread.
   uint32_t prefix = 0;
   int above = 0;
+  const int held = min(n, p.held);
+  auto bin_of = [&](uint32_t key, int shift, int bins) { return (key >> shift) & (bins - 1); };
+  for (int i = tid; i < kBins; i += threads) s_bins[i] = 0;
+  __syncthreads();
+  for (int j0 = 0; j0 < n; j0 += threads * kPerThread) {
+    float x[kPerThread];
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int j = j0 + k * threads + tid;
+      x[k] = j < n ? w[j] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int j = j0 + k * threads + tid;
+      if (j < held) s_held[j] = x[k];
+      // zeros are often many: one lane adds a warp's
+      const bool counts = j >= lo && j < hi;
+      const uint32_t zeros = __ballot_sync(0xffffffffu, counts && x[k] == 0.0f);
+      if (counts && x[k] != 0.0f) atomicAdd(&s_bins[bin_of(weight_key(x[k]), 21, kBins)], 1);
+      if (lane == 0 && zeros) atomicAdd(&s_bins[bin_of(weight_key(0.0f), 21, kBins)], __popc(zeros));
+    }
+  }
+  auto weight = [&](int j) { return j < held ? s_held[j] : w[j]; };
   if (want > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int top = pass == 0 ? 32 : pass == 1 ? 21 : 10;  // bits above are found
       const int bins = 1 << (top - shift);
-      for (int i = tid; i < bins; i += kSelectThreads) s_bins[i] = 0;
-      __syncthreads();
-      for (int j = lo + tid; j < hi; j += kSelectThreads) {
-        const uint32_t key = weight_key(w[j]);
-        if (top == 32 || key >> top == prefix >> top) atomicAdd(&s_bins[(key >> shift) & (bins - 1)], 1);
+      if (pass > 0) {
+        for (int i = tid; i < bins; i += threads) s_bins[i] = 0;
+        __syncthreads();
+        auto count = [&](float x, int j) {
+          const uint32_t key = weight_key(x);
+          if (key >> top == prefix >> top && j >= lo && j < hi) atomicAdd(&s_bins[bin_of(key, shift, bins)], 1);
+        };
+#pragma unroll 2
+        for (int i = tid; 4 * i < held; i += threads) {
+          const float4 x = reinterpret_cast<const float4*>(s_held)[i];
+          count(x.x, 4 * i);
+          if (4 * i + 1 < held) count(x.y, 4 * i + 1);
+          if (4 * i + 2 < held) count(x.z, 4 * i + 2);
+          if (4 * i + 3 < held) count(x.w, 4 * i + 3);
+        }
+        for (int j = held + tid; j < n; j += threads) count(w[j], j);
       }
       __syncthreads();
       // the bin where the count from the top passes `want`: thread t has bins
       // [per t, per (t + 1)) from the top
-      const int per = bins / kSelectThreads;
+      const int per = bins / threads;
       int mine = 0;
       for (int i = 0; i < per; ++i) mine += s_bins[bins - 1 - (tid * per + i)];
       int upto = mine;
@@ -137,8 +189,8 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
       }
       if (lane == 31) s_warp[warp] = upto;
       __syncthreads();
-      int before = above + upto - mine;
-      for (int x = 0; x < warp; ++x) before += s_warp[x];
+      int all;
+      int before = above + upto - mine + warps_before(s_warp, warps, all);
       if (before < want && before + mine >= want) {
         int i = 0;
         for (; before + s_bins[bins - 1 - (tid * per + i)] < want; ++i)
@@ -149,9 +201,12 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
       __syncthreads();
       prefix |= (uint32_t)s_bin << shift;
       above = s_above;
-      __syncthreads();
     }
   }
+  // As weights: heavier than `limit`, or as heavy (a limit that is NaN is below all
+  // numbers; without a limit nothing is either).
+  const bool none = want == 0, nan_limit = prefix == 0;
+  const float limit = __uint_as_float(prefix & 0x80000000u ? prefix & 0x7fffffffu : ~prefix);
   const int equal = want - above;  // of the rows with this key, the first ones
   // In the rows' order: rows that stay because they are heavier (or first, or last),
   // and those with the key, counted side by side in 16 bits each within a tile.
@@ -159,53 +214,49 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
   float* out = p.weights_out ? p.weights_out + (size_t)item * p.width : nullptr;
   int done_over = 0, done_equal = 0;
 #pragma unroll 1
-  for (int t0 = 0; t0 < n; t0 += kSelectTile) {
+  for (int t0 = 0; t0 < n; t0 += threads * kPerThread) {
     float x[kPerThread];
-    uint32_t over = 0, same = 0;  // bit k: row t0 + warp's + 32 k + lane
+    uint32_t over[kPerThread], same[kPerThread];  // of the warp: bit i is row j0 + 32 k + i - lane
     int in_warp = 0;
     const int j0 = t0 + warp * (32 * kPerThread) + lane;
+    const bool any = j0 - lane < n;
+    if (any) {
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      const int j = j0 + 32 * k;
-      x[k] = j < n ? w[j] : 0.0f;
-      const uint32_t key = weight_key(x[k]);
-      const bool safe = j < n && (j < lo || j >= hi), open = j >= lo && j < hi && want > 0;
-      const uint32_t mo = __ballot_sync(0xffffffffu, safe || (open && key > prefix));
-      const uint32_t me = __ballot_sync(0xffffffffu, open && key == prefix);
-      over |= ((mo >> lane) & 1u) << k;
-      same |= ((me >> lane) & 1u) << k;
-      in_warp += __popc(mo) | __popc(me) << 16;
+      for (int k = 0; k < kPerThread; ++k) {
+        const int j = j0 + 32 * k;
+        x[k] = j < n ? weight(j) : 0.0f;
+        const bool open = j >= lo && j < hi, heavier = nan_limit ? x[k] == x[k] : x[k] > limit;
+        const bool alike = nan_limit ? x[k] != x[k] : x[k] == limit;
+        over[k] = __ballot_sync(0xffffffffu, j < n && (!open || (!none && heavier)));
+        same[k] = __ballot_sync(0xffffffffu, open && !none && alike);
+        in_warp += __popc(over[k]) | __popc(same[k]) << 16;
+      }
     }
     if (lane == 0) s_warp[warp] = in_warp;
     __syncthreads();  // all of the tile's weights have been read
-    int before = 0, all = 0;
+    int all;
+    const int before = warps_before(s_warp, warps, all);
+    if (any) {
+      int n_over = done_over + (before & 0xffff), n_equal = done_equal + (before >> 16);
+      const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
-    for (int y = 0; y < kSelectWarps; ++y) {
-      before += y < warp ? s_warp[y] : 0;
-      all += s_warp[y];
-    }
-    int n_over = done_over + (before & 0xffff), n_equal = done_equal + (before >> 16);
-    const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      const uint32_t mo = __ballot_sync(0xffffffffu, (over >> k) & 1u);
-      const uint32_t me = __ballot_sync(0xffffffffu, (same >> k) & 1u);
-      const int my_over = n_over + __popc(mo & below), my_equal = n_equal + __popc(me & below);
-      const bool stays = ((over >> k) & 1u) || (((same >> k) & 1u) && my_equal < equal);
-      if (stays) {
-        const int to = my_over + min(my_equal, equal);
-        if (rows) rows[to] = j0 + 32 * k;
-        if (out) out[to] = x[k];  // to <= the row itself: behind all that is still read
+      for (int k = 0; k < kPerThread; ++k) {
+        const int my_equal = n_equal + __popc(same[k] & below);
+        if ((over[k] >> lane & 1u) || ((same[k] >> lane & 1u) && my_equal < equal)) {
+          const int to = n_over + __popc(over[k] & below) + min(my_equal, equal);
+          if (rows) rows[to] = j0 + 32 * k;
+          if (out) out[to] = x[k];  // to <= the row itself: behind all that is still read
+        }
+        n_over += __popc(over[k]);
+        n_equal += __popc(same[k]);
       }
-      n_over += __popc(mo);
-      n_equal += __popc(me);
     }
     done_over += all & 0xffff;
     done_equal += all >> 16;
     __syncthreads();  // before the next tile's counts
   }
   if (out)
-    for (int j = stay + tid; j < n; j += kSelectThreads) out[j] = 0.0f;
+    for (int j = stay + tid; j < n; j += threads) out[j] = 0.0f;
 }
 
 // Where row `row` of a sequence's kv head lies, from the start of its layer.
@@ -217,7 +268,7 @@ __device__ __forceinline__ long long row_at(const EvictParams& p, const Pool& po
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveAhead = 4;  // rows a thread has in flight
+constexpr int kMoveAhead = 2;  // rows a thread has in flight
 
 // lanes: threads side by side on a row (a power of two)
 template <typename U>
@@ -309,7 +360,7 @@ cudaError_t launch_move(const EvictParams& p, int items, int num_sms, cudaStream
   while (lanes < units && lanes < 32) lanes *= 2;
   const int chunk = kMoveThreads / lanes * kMoveAhead;
   const int want = (p.width + chunk - 1) / chunk;
-  const int most = (8 * num_sms + items - 1) / items;
+  const int most = (16 * num_sms + items - 1) / items;
   return launch_dependent(pva_evict_move_kernel<U>, dim3(want < most ? want : most, items),
                           dim3(kMoveThreads), 0, s, p, lanes);
 }
@@ -424,8 +475,14 @@ extern "C" int pva_kvcache_evict(void* k_cache, void* v_cache, const float* weig
     p.count = reinterpret_cast<int32_t*>(c.buf);
     p.length = p.count + items;
     p.rows = kept ? kept : reinterpret_cast<int32_t*>(c.buf + head);
-    cudaError_t e = launch_dependent(pva_evict_select_kernel, dim3((unsigned)items), dim3(kSelectThreads), 0,
-                                     stream, p);
+    const long long rows = (long long)max_blocks * page_size < width ? (long long)max_blocks * page_size : width;
+    p.held = (int)(rows < kHeld ? rows : kHeld);
+    const size_t smem = sizeof(float) * (((size_t)p.held + 3) / 4 * 4);
+    const int threads = rows <= 2048 ? 256 : rows <= 8192 ? 512 : kSelectThreads;
+    cudaError_t e = cudaFuncSetAttribute(pva_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(sizeof(float) * kHeld));
+    if (e == cudaSuccess)
+      e = launch_dependent(pva_evict_select_kernel, dim3((unsigned)items), dim3(threads), smem, stream, p);
     if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
     e = mis % 16 == 0  ? launch_move<uint4>(p, (int)items, c.num_sms, stream)
         : mis % 4 == 0 ? launch_move<uint32_t>(p, (int)items, c.num_sms, stream)
