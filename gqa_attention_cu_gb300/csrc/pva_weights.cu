@@ -65,7 +65,7 @@ struct Sequence {
     chunks = max(1, (q + p.tokens_at_once - 1) / p.tokens_at_once);
     tiles = (n + kKeys - 1) / kKeys;
   }
-  __device__ __forceinline__ int per_head() const { return tiles * chunks; }
+  __device__ __forceinline__ long long per_head() const { return (long long)tiles * chunks; }
 };
 
 // A piece's part of one (sequence, kv head): key tiles [j0, j1).
@@ -90,7 +90,7 @@ struct Walk {
       if (b < 0) b = tree_find(p.start, p.B, (int)x);
       while (p.start[b + 1] <= x) ++b;
       const Sequence seq(p, b);
-      const int rel = (int)x - p.start[b], per = seq.per_head();
+      const int rel = (int)x - p.start[b], per = (int)seq.per_head();
       s.b = b;
       s.h = rel / per;
       const int within = rel - s.h * per;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kFrontThreads) pva_weights_front_kernel(Weight
   auto places = [&](int i) {
     const Sequence s(p, i);
     const bool sane = s.n >= 0 && s.q >= 0 && s.n <= p.width && s.q <= p.T;
-    return sane ? (long long)s.per_head() * p.Hkv : 0ll;
+    return sane ? s.per_head() * p.Hkv : 0ll;
   };
   if (tid == 0) {
     if (bad) atomicOr(p.status + kWordBad, bad);
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(256) pva_weights_rows_kernel(WeightsParams p) 
     const int item = (int)(i / R), r = (int)(i - (long long)item * R), b = item / p.Hkv, h = item - b * p.Hkv;
     const Sequence s(p, b);
     if (r >= s.q * p.G) continue;
-    const long long x0 = p.start[b] + (long long)h * s.per_head(), x1 = x0 + s.per_head();
+    const long long x0 = p.start[b] + h * s.per_head(), x1 = x0 + s.per_head();
     float m = NEG_INF, l = 0.0f;
     for (long long pc = x0 / chunk + lane; pc * chunk < x1; pc += 32) {
       // a piece that holds no tile's first place has no part
@@ -1047,7 +1047,11 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   // query rows of a chunk, and the score columns they take
   const int n = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
   p.tokens_at_once = tc ? (R <= 128 ? T : 128 / G) : T;
-  const bool store = tc && !lse && R <= 16;
+  // Scores are kept where there are few rows, and in no more memory than the keys have
+  // or 256 MB (tables may be far wider than the pool).
+  const size_t tiles = ((size_t)(width < (long long)max_blocks * page ? width : (long long)max_blocks * page) + kKeys - 1) / kKeys;
+  const size_t kept = 4 * (size_t)B * Hkv * tiles * R * kKeys, pool = 2 * (size_t)n_blocks * Hkv * page * d;
+  const bool store = tc && !lse && R <= 16 && kept <= (pool > (256u << 20) ? pool : 256u << 20);
 
   std::lock_guard<std::mutex> lock(api_mutex());
   int rc = sm_count(&p.pieces);
@@ -1063,8 +1067,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   p.parts = !tc ? 1 : store ? 4 * kGroups : kGroups;
   const size_t at_part = take(lse ? 0 : 8 * ((size_t)B * Hkv + p.pieces) * p.parts * R);
   const size_t at_row = take(lse ? 0 : 8 * (size_t)B * Hkv * R);
-  const size_t tiles = ((size_t)(width < (long long)max_blocks * page ? width : (long long)max_blocks * page) + kKeys - 1) / kKeys;
-  const size_t at_scores = take(store ? 4 * (size_t)B * Hkv * tiles * R * kKeys : 0);
+  const size_t at_scores = take(store ? kept : 0);
   CallContext c;
   if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
   p.status = c.status;

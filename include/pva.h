@@ -582,7 +582,7 @@ int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* past_lens,
  * scale, softcap, dtype, stream : as pva_forward.
  *
  * Arithmetic, limits and alignment as pva_gqa_tree without a rotation, and num_heads /
- * kv_num_heads <= 128.  Results do not depend on timing.  A value row that some token
+ * kv_num_heads <= 128.  The workspace holds two f32 rows of head_size per query row.  Results do not depend on timing.  A value row that some token
  * sees should be finite: an infinity or NaN there can reach its other tokens, and in a
  * prefix all of its sequences.
  * Host errors: null pointers, counts below 1 or out of int32, and the limits.  Device
@@ -624,8 +624,9 @@ int pva_gqa_prefix(const void* q, const void* k_cache, const void* v_cache, cons
  *
  * Arithmetic: products of dtype (f16/bf16 on tensor cores), all sums f32, in a fixed
  * order: equal calls give equal bits.  Without lse and with tokens * num_heads /
- * kv_num_heads <= 16 (f16/bf16) the scores are kept in the workspace: 4 bytes for each
- * of these query rows and entry of weights.
+ * kv_num_heads <= 16 (f16/bf16) the scores are kept in the workspace, 4 bytes for each
+ * of these query rows and entry of weights, unless that is more than the pool's keys
+ * and than 256 MB; otherwise, and with more query rows, the keys are read twice.
  * Limits: head sizes, page sizes and alignment as pva_gqa_tree; num_heads /
  * kv_num_heads <= 128.
  * Host errors: null pointers, counts below 1 or out of int32, weights over an input,

@@ -82,7 +82,8 @@ CASES = [  # lens, keep, layers, Hkv, d, dtype, page, first, last, kind
     ([5000], [4999], 1, 1, 128, "bf16", 64, 0, 0, "random"), ([5000], [1], 1, 2, 128, "bf16", 64, 0, 0, "ties"),
     ([4096, 4097, 8193], [4000, 100, 4097], 1, 1, 96, "f32", 32, 33, 150, "close"),
     ([60, 61], [20, 20], 3, 3, 30, "f16", 0, 0, 0, "odd"), ([60, 61], [50, 12], 2, 2, 7, "bf16", 16, 2, 0, "odd"),
-    ([90, 200], [40, 40], 1, 2, 5, "f32", 0, 100, 100, "odd"), ([90, 200], [40, 40], 1, 1, 256, "f32", 16, 0, 100, "ties"),
+    ([30000], [12345], 1, 1, 64, "bf16", 64, 9, 77, "ties"), ([9000, 100, 0], [4500, 50, 9], 1, 2, 64, "bf16", 16, 3000, 3000, "odd"),
+    ([12001, 12002], [1, 12001], 1, 1, 64, "f16", 0, 0, 0, "close"), ([90, 200], [40, 40], 1, 2, 5, "f32", 0, 100, 100, "odd"), ([90, 200], [40, 40], 1, 1, 256, "f32", 16, 0, 100, "ties"),
     ([50, 80], [10, 30], 1, 2, 64, "bf16", 16, 4, 20, "ties"), ([9000], [6000], 1, 1, 192, "f32", 128, 5, 5, "close")]
 
 
@@ -177,6 +178,29 @@ def test_after_a_rejected_step_nothing_moves():
     pva.pva_kvcache_evict(k, v, w, lens, keep, new)
     assert pva.pva_get_status() & pva.DEV_FLAGS["kv_cache"]
     assert new.tolist() == [100] and torch.equal(k.cpu(), s["k"])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n", [49_152, 400_001])
+def test_more_weights_than_shared_memory_holds(n, in_place):
+    """One head, many rows: the weights are read again from where they are."""
+    g = torch.Generator(DEV).manual_seed(n)
+    d, keep = 2, n // 3
+    k, v = (torch.randn(1, 1, n, d, generator=g, device=DEV).bfloat16() for _ in range(2))
+    w = (torch.randn(1, 1, n, generator=g, device=DEV) * 50).round()  # many ties
+    x = w[0, 0].clone()
+    x[:7], x[-30:] = math.inf, math.inf
+    rows = torch.sort(torch.sort(x, descending=True, stable=True).indices[:keep]).values
+    ref = [t[0, 0, rows] for t in (k, v)] + [w[0, 0, rows]]
+    wo = w if in_place else torch.empty_like(w)
+    kept = torch.zeros(1, 1, n, dtype=torch.int32, device=DEV)
+    lens, budget, new = (torch.tensor([a], dtype=torch.int32, device=DEV) for a in (n, keep, 0))
+    pva.pva_kvcache_evict(k, v, w, lens, budget, new, first=7, last=30, weights_out=wo, kept=kept)
+    assert pva.pva_get_status() == 0 and new.tolist() == [keep]
+    assert torch.equal(kept[0, 0, :keep].long(), rows)
+    for got, want in zip((k, v, wo), ref):
+        assert torch.equal(got[0, 0, :keep], want)
+    assert (wo[0, 0, keep:] == 0).all()
 
 
 def test_long_rows_and_captured():
