@@ -13,6 +13,13 @@
 //
 // Weights are compared by a 32-bit key that rises with them; equal keys are taken
 // from the lowest row on, so the choice does not depend on timing.
+//
+// 16 prompts of 4000 to 16,000 rows cut to 2048, 8 kv heads of 128 bf16, copied: 70 us.
+// The move is 44 of them, 268 MB at 6.1 TB/s (floor of the whole: 42); the choice 24,
+// bound by the latency of votes and counts with one CTA an SM: 6000 cycles a count, 7000
+// for 8192 rows listed.  (Clusters of four CTAs an item, counts through distributed
+// shared memory: 60 us for the choice.  Four rows in flight a thread and half as many
+// CTAs in the move: 51 us.)  One request of 700 rows: 14 us, of which 8 are launches.
 #include <limits.h>
 
 #include "pva_device.cuh"

@@ -16,6 +16,17 @@
 // The line: (sequence, kv head, key tile of 128 keys), each tile counted once for
 // every chunk of query rows that it is multiplied with.  A key's weight is written by
 // one thread, chunk after chunk, so results do not depend on timing.
+//
+// Memory is the floor: 2 d bytes of a key, 4 or 8 of its weight.  Measured:
+//   a decoding step of 32 sequences of 2000 to 16,000 rows, 32 query and 8 kv heads of
+//     128 bf16, own sums: 120 us, of which the keys are 97 at 6.1 TB/s (91 us is the
+//     floor), the kept scores 13 and the front end 6.  Keys leave L2 first, so that the
+//     37 MB of scores are still there (without: 128 us).
+//   32 tokens on 100,000 rows of one sequence, sums given: 40 us, the kernel 5.4 TB/s
+//     (floor 31).  Of its steps: masks as a bound on the columns instead of a comparison
+//     each 66 to 44 us (the last tile of a head was its CTA's longest), unmasked columns
+//     in pairs without a test 147 to 67.
+//   3 sequences of 300 to 900 rows, f32: 49 us, four launches of a few latencies each.
 #include <limits.h>
 #include <math.h>
 
