@@ -241,3 +241,40 @@ def test_long_rows_and_captured():
             rows = torch.sort(torch.sort(x, descending=True, stable=True).indices[:keep]).values
             assert torch.equal(to[0][0, h], k[0, h, rows]) and torch.equal(to[1][0, h], v[0, h, rows])
             assert torch.equal(wo[0, h, :keep], w[0, h, rows]) and (wo[0, h, keep:] == 0).all()
+
+
+@pytest.mark.parametrize("mode", ["in place", "copied"])
+def test_blocks_behind_two_to_the_31_elements(mode):
+    """Blocks that lie past 2^31 elements of the pools."""
+    s = make([300, 77], [100, 50], 1, 2, 128, "bf16", 128, 41)
+    n = s["k"].shape[1]
+    blocks = 2 ** 31 // (2 * 128 * 128) + n
+    k, v = (torch.zeros(1, blocks, 2, 128, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k[:, -n:], v[:, -n:] = s["k"].to(DEV), s["v"].to(DEV)
+    table = torch.where(s["table"] >= 0, s["table"] + blocks - n, s["table"]).to(DEV)
+    out_table = torch.tensor([[0], [1]], dtype=torch.int32)  # near blocks, unused so far
+    lens, keep = s["lens"].to(DEV), s["keep"].to(DEV)
+    new = torch.zeros_like(lens)
+    pva.pva_kvcache_evict(k, v, s["w"].to(DEV), lens, keep, new, block_table=table,
+                          out_table=out_table.to(DEV) if mode == "copied" else None)
+    assert pva.pva_get_status() == 0
+    zero = torch.zeros(1, 2, 2, 128, 128, dtype=torch.bfloat16)
+    to = (zero, zero, out_table) if mode == "copied" else (s["k"], s["v"], s["table"])
+    ref = expected(s, 0, 0, *to, s["w"], torch.zeros(s["w"].shape, dtype=torch.int32))
+    at = slice(0, 2) if mode == "copied" else slice(-n, None)
+    assert torch.equal(k[:, at].cpu(), ref[0]) and torch.equal(v[:, at].cpu(), ref[1]) and torch.equal(new.cpu(), ref[4])
+
+
+def test_two_streams_at_once():
+    a, b = (make([5000, 800], [700, 300], 1, 2, 64, "bf16", 16, 42 + i) for i in range(2))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    on = [{n: x.to(DEV) for n, x in s.items() if n != "spare"} for s in (a, b)]
+    new = [torch.zeros_like(t["lens"]) for t in on]
+    torch.cuda.synchronize()
+    for t, m, st in zip(on, new, streams):
+        pva.pva_kvcache_evict(t["k"], t["v"], t["w"], t["lens"], t["keep"], m, first=3, last=9, block_table=t["table"], stream=st)
+    torch.cuda.synchronize()
+    for s, t, m, st in zip((a, b), on, new, streams):
+        ref = expected(s, 3, 9, s["k"], s["v"], s["table"], s["w"], torch.zeros(s["w"].shape, dtype=torch.int32))
+        assert pva.pva_get_status(st) == 0
+        assert torch.equal(t["k"].cpu(), ref[0]) and torch.equal(t["v"].cpu(), ref[1]) and torch.equal(m.cpu(), ref[4])

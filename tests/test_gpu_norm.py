@@ -249,3 +249,50 @@ def test_weight_sums_are_repeatable_and_captured():
         torch.cuda.synchronize()
         assert torch.equal(dw[0], dw[2]) and torch.equal(dw[1], dw[3]) and torch.equal(dq, first[0]) and torch.equal(dk, first[1])
     assert pva.pva_get_status(stream) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_stays_in_its_row(dtype):
+    N, H, Hkv, d = 40, 9, 3, 96
+    q, k, _, wq, wk, cos, sin, pos = inputs(N, H, Hkv, d, dtype, 64, 1, 13)
+    c, s, p = gpu(cos, sin, pos)
+    t = gpu(q, k, wq, wk)
+    clean = [torch.empty_like(t[0]), torch.empty_like(t[1])]
+    pva.pva_norm_rope(*t, *clean, c, s, p)
+    t[0][7, 2, 5], t[1][39, 0, 95] = float("nan"), float("inf")
+    out = [torch.empty_like(t[0]), torch.empty_like(t[1])]
+    pva.pva_norm_rope(*t, *out, c, s, p)
+    for got, ref, at in ((out[0], clean[0], (7, 2)), (out[1], clean[1], (39, 0))):
+        rows = torch.ones(ref.shape[:2], dtype=torch.bool, device=DEV)
+        rows[at] = False
+        assert torch.equal(got[rows], ref[rows]) and torch.isnan(got[at]).any()
+    assert pva.pva_get_status() == 0
+
+
+def test_two_streams_at_once():
+    N, H, Hkv, d = 4000, 8, 2, 128
+    q, k, _, wq, wk, cos, sin, pos = inputs(N, H, Hkv, d, "bf16", 128, 1, 14)
+    t = gpu(q, k, q, k, wq, wk)
+    c, s, p = gpu(cos, sin, pos)
+    streams = [None, torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty_like(t[0]), torch.empty_like(t[1]), torch.empty(d, device=DEV), torch.empty(d, device=DEV)] for _ in streams]
+    torch.cuda.synchronize()
+    for o, st in zip(outs, streams):
+        pva.pva_norm_rope_backward(*t, *o, c, s, p, stream=st)
+    torch.cuda.synchronize()
+    for o, st in zip(outs, streams):
+        assert pva.pva_get_status(st) == 0 and all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+def test_rows_behind_two_to_the_31_elements():
+    """Token strides that reach past 2^31 elements."""
+    N, H, d = 3, 2, 64
+    q, _, _, wq, _, cos, sin, pos = inputs(N, H, 1, d, "bf16", 64, 1, 15)
+    far = torch.zeros(2 * (2 ** 30 + 64) + H * d, dtype=torch.bfloat16, device=DEV).as_strided((N, H, d), (2 ** 30 + 64, d, 1))
+    far.copy_(q)
+    c, s, p = gpu(cos, sin, pos)
+    near_out, far_out = torch.empty_like(q, device=DEV), torch.empty_like(q, device=DEV)
+    pva.pva_norm_rope(q.to(DEV), None, wq.to(DEV), None, near_out, None, c, s, p)
+    pva.pva_norm_rope(far, None, wq.to(DEV), None, far_out, None, c, s, p)
+    pva.pva_norm_rope(far, None, wq.to(DEV), None, far, None, c, s, p)
+    assert pva.pva_get_status() == 0 and torch.equal(near_out, far_out) and torch.equal(far, near_out)

@@ -177,3 +177,44 @@ def test_captured_and_on_its_own_stream(T):
         assert torch.equal(to, eager)
     check(eager, s, 2)
     assert pva.pva_get_status(st) == 0
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_blocks_behind_two_to_the_31_elements(T):
+    """A pool whose last blocks lie past 2^31 elements gives the bits of a small one."""
+    s = make([300, 77], T, 8, 2, 128, "bf16", 128, 23)
+    small = run(s, 8)
+    n = s["k"].shape[0]
+    blocks = 2 ** 31 // (2 * 128 * 128) + n
+    k = torch.zeros(blocks, 2, 128, 128, dtype=torch.bfloat16, device=DEV)
+    k[-n:] = s["k"].to(DEV)
+    far = run(dict(s, k=k, table=torch.where(s["table"] >= 0, s["table"] + blocks - n, s["table"])), 8)
+    assert pva.pva_get_status() == 0 and torch.equal(far, small)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, unordered, each with its own workspace: the bits of calls alone."""
+    cases = [make([3000, 900], 1, 8, 2, 128, "bf16", 64, 31), make([400] * 9, 33, 8, 2, 128, "bf16", 64, 32)]
+    alone = [run(s, 8) for s in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    on = [{n: gpu(x) for n, x in s.items() if isinstance(x, torch.Tensor)} for s in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for t, st in zip(on, streams):
+            pva.pva_kvcache_weights(t["q"], t["k"], t["lens"], t["to"], 8, block_table=t["table"], stream=st)
+    torch.cuda.synchronize()
+    for t, st, ref in zip(on, streams, alone):
+        assert pva.pva_get_status(st) == 0 and torch.equal(t["to"], ref)
+
+
+def test_tables_far_wider_than_the_pool():
+    """A wide table over a small pool: the scores are not kept (they would need more
+    memory than the keys), and the weights are as with a narrow one."""
+    s = make([200, 50], 2, 32, 4, 64, "bf16", 16, 33)
+    narrow = run(s, 32)
+    wide = dict(s, table=torch.nn.functional.pad(s["table"], (0, 120_000 - s["table"].shape[1]), value=-1))
+    wide["to"] = torch.nn.functional.pad(s["to"], (0, 1_900_000 - s["to"].shape[2]))
+    got = run(wide, 32)
+    assert pva.pva_get_status() == 0
+    check(got[:, :, :s["to"].shape[2]], s, 4)
+    assert torch.allclose(got[:, :, :200], narrow[:, :, :200], rtol=1e-4, atol=0) and (got[:, :, s["to"].shape[2]:] == 0).all()
