@@ -717,16 +717,18 @@ __global__ void __launch_bounds__(kThreadsF32) pva_weights_f32_kernel(WeightsPar
         for (int c = lane; c < d; c += 32) dst[c] = there ? src[c] : 0.0f;
       }
     };
-    auto load_keys = [&](int j) {
-      for (int i = warp; i < kKeys; i += kThreadsF32 / 32) {
-        const int key = j * kKeys + i;
-        size_t at = 0;
-        if (key < s.n) {
-          const int in = key / p.page;
-          const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
-          at = (((size_t)block * p.Hkv + s.h) * p.page + (key - in * p.page)) * d;
-        }
-        copy_row(sk + (size_t)i * row, kc + at, key < s.n);
+    auto load_keys = [&](int j) {  // a warp 32 of them, whose places its lanes look up side by side
+      static_assert(kKeys == kThreadsF32, "a key a lane");
+      const int key = j * kKeys + tid;
+      long long at = -1;
+      if (key < s.n) {
+        const int in = key / p.page;
+        const int block = p.table ? p.table[(size_t)s.b * p.max_blocks + in] : s.b;
+        at = (((long long)block * p.Hkv + s.h) * p.page + (key - in * p.page)) * d;
+      }
+      for (int i = 0; i < 32; ++i) {
+        const long long from = __shfl_sync(0xffffffffu, at, i);
+        copy_row(sk + (size_t)(warp * 32 + i) * row, kc + (from < 0 ? 0 : from), from >= 0);
       }
     };
     auto load_rows = [&](int r0) {
@@ -754,6 +756,7 @@ __global__ void __launch_bounds__(kThreadsF32) pva_weights_f32_kernel(WeightsPar
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[0][e] = x[1][e] = 0.0f;
       const float* qa = sq + (size_t)group * 8 * row;
+#pragma unroll 2
       for (int c = 0; c < d; c += 4) {
         const float4 k0 = *reinterpret_cast<const float4*>(sk + (size_t)key0 * row + c);
         const float4 k1 = *reinterpret_cast<const float4*>(sk + (size_t)(key0 + 64) * row + c);
