@@ -1,8 +1,8 @@
 // Attention of sequences that share prefixes (pva_gqa_prefix): host side, front end,
 // fp32 attention and the join.
 //
-//   pva_prefix_front_kernel  one CTA per entry (prefix or sequence): bounds and block
-//       table; the last one cuts the line of places (pva_prefix.cuh).
+//   front end (pva_line.cuh)  bounds and block table of every entry (prefix or
+//       sequence), and the line of places (pva_prefix.cuh).
 //   attention                one piece of the line per CTA.
 //   pva_prefix_join_kernel   out and lse of every query row from its parts; it looks up
 //       where they lie while the attention runs (26.5 to 20.4 us for two requests).
@@ -16,6 +16,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include "pva_line.cuh"
 #include "pva_prefix.cuh"
 #include "pva_tree_f32.cuh"
 
@@ -25,86 +26,53 @@ using namespace pva::host;
 namespace pva {
 namespace {
 
-constexpr int kFrontThreads = 128;
-constexpr int kWordArrived = 16, kWordBad = 17;  // of the status block, zero between calls
-
-__global__ void __launch_bounds__(kFrontThreads) pva_prefix_front_kernel(PrefixParams p) {
-  wait_prior_grid();
-  allow_next_grid();
-  __shared__ int s_last;
-  __shared__ long long s_sum[kFrontThreads / 32];
-  const int e = blockIdx.x, tid = threadIdx.x, E = p.P + p.B;
-  const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
-  const bool is_prefix = e < p.P;
-  const int b = is_prefix ? e : e - p.P;
-  const int keys = is_prefix ? p.prefix_keys[b] : p.keys[b];
-  const int32_t* table = is_prefix ? p.prefix_table : p.table;
-  const int width = is_prefix ? p.prefix_blocks : p.max_blocks;
-  uint32_t bad = 0;
-  if (keys < 0 || (long long)keys > (long long)width * p.page) bad = PVA_DEV_KV_LEN;
-  if (!is_prefix) {
-    const int n = tree_nodes(p, b);
-    if (n < 0 || n > p.T || n > keys) bad = PVA_DEV_KV_LEN;
-  } else if (p.prefix_start) {
-    const int first = p.prefix_start[b], end = p.prefix_start[b + 1];
-    if (first < 0 || end < first || end > p.B || (b == 0 && first != 0) || (b == p.P - 1 && end != p.B)) bad |= PVA_DEV_PREFIX;
-  }
-  bool off = false;
-  if (!bad && table)
-    for (int i = tid; i < (keys + p.page - 1) / p.page; i += kFrontThreads)
-      off |= (unsigned)table[(size_t)b * width + i] >= (unsigned)p.n_blocks;
-  if (__syncthreads_or(off)) bad |= PVA_DEV_BLOCKS;
-  if (tid == 0) {
-    if (bad) atomicOr(p.status + kWordBad, bad);
-    __threadfence();
-    s_last = atomicAdd(p.status + kWordArrived, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  const uint32_t found = __ldcg(p.status + kWordBad);
-  long long carry = 0;
-  for (int e0 = 0; e0 < E && !found; e0 += kFrontThreads) {
-    const int i = e0 + tid;
-    const long long x = i < E ? prefix_entry(p, i).per_head(p) * p.Hkv : 0;
-    long long upto = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-      if ((tid & 31) >= o) upto += y;
+// The entries on the line (pva_line.cuh): prefixes, then sequences.
+struct PrefixFront {
+  PrefixParams p;
+  __device__ __forceinline__ int entries() const { return p.P + p.B; }
+  __device__ __forceinline__ int32_t* start() const { return p.tile_start; }
+  __device__ __forceinline__ uint32_t check(int e, int i0, int n, bool& off) const {
+    const bool is_prefix = e < p.P;
+    const int b = is_prefix ? e : e - p.P;
+    const int keys = is_prefix ? p.prefix_keys[b] : p.keys[b];
+    const int32_t* table = is_prefix ? p.prefix_table : p.table;
+    const int width = is_prefix ? p.prefix_blocks : p.max_blocks;
+    uint32_t bad = keys < 0 || (long long)keys > (long long)width * p.page ? PVA_DEV_KV_LEN : 0u;
+    if (!is_prefix) {
+      const int tokens = tree_nodes(p, b);
+      if (tokens < 0 || tokens > p.T || tokens > keys) bad = PVA_DEV_KV_LEN;
+    } else if (p.prefix_start) {
+      const int first = p.prefix_start[b], end = p.prefix_start[b + 1];
+      if (first < 0 || end < first || end > p.B || (b == 0 && first != 0) || (b == p.P - 1 && end != p.B))
+        bad |= PVA_DEV_PREFIX;
     }
-    if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
-    __syncthreads();
-    long long before = carry;
-    for (int w = 0; w < kFrontThreads / 32; ++w) {
-      before += w < tid >> 5 ? s_sum[w] : 0;
-      carry += s_sum[w];
-    }
-    if (i < E) p.tile_start[i] = (int)min(before + upto - x, (long long)INT_MAX);
-    __syncthreads();
+    off = !bad && table && line::off_pool(table + (size_t)b * width, keys, p.page, p.n_blocks, i0, n);
+    return bad;
   }
-  if (tid == 0) {
-    p.status[kWordBad] = 0;  // for the next call
-    p.status[kWordArrived] = 0;
-    const uint32_t all_bad = found | (carry > INT_MAX - 4ll * p.pieces ? PVA_DEV_TOO_MANY : 0u);
-    if (all_bad) atomicOr(p.status, all_bad);
-    const bool ok = !all_bad && !latched;
-    const int all = ok ? (int)carry : 0, even = (all + p.pieces - 1) / p.pieces;
-    p.tile_start[E] = all;
-    p.hdr[0] = ok;
-    p.hdr[1] = all;
+  __device__ __forceinline__ long long places(int e) const { return prefix_entry(p, e).per_head(p) * p.Hkv; }
+  __device__ __forceinline__ void publish(long long sum, uint32_t found, bool latched) const {
+    if (!found && sum > INT_MAX - 4ll * p.pieces) found = PVA_DEV_TOO_MANY;
+    if (found) atomicOr(p.status, found);
+    const bool ok = !found && !latched;
+    const int all = ok ? (int)sum : 0, even = (all + p.pieces - 1) / p.pieces;
     int chunk = even > p.min_chunk ? even : p.min_chunk;
     // One prefix of several query tiles: where it costs little, its items are all cut
-    // alike, so that the CTAs of the same keys read them at the same time, from L2.
-    const PrefixEntry head = prefix_entry(p, 0);
-    const int per = head.places(p);
-    if (ok && p.P == 1 && head.q_tiles(p) > 1 && per > chunk) {
-      const int alike = (per + per / chunk - 1) / (per / chunk);
-      if (alike <= chunk + chunk / 8) chunk = alike;
+    // alike, so that the CTAs of the same keys read them at the same time, from L2 (64
+    // sequences behind 32,768 rows, with item costs that cut them otherwise: 113 to 101 us).
+    if (ok && p.P == 1) {
+      const PrefixEntry head = prefix_entry(p, 0);
+      const int per = head.places(p);
+      if (head.q_tiles(p) > 1 && per > chunk) {
+        const int alike = (per + per / chunk - 1) / (per / chunk);
+        if (alike <= chunk + chunk / 8) chunk = alike;
+      }
     }
+    p.tile_start[entries()] = all;
+    p.hdr[0] = ok;
+    p.hdr[1] = all;
     p.hdr[2] = chunk;
   }
-}
+};
 
 // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over a row's parts c, the prefix's
 // and then its own, M = max m_c; lse = ln 2 (M + log2 of the lower sum).  One warp per
@@ -342,7 +310,8 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
         (rc = encode_plane_map(&tv, v_cache, dtype, d, page_size, planes, 64, box, true)) != PVA_OK)
       return rc;
   }
-  cudaError_t e = launch_dependent(pva_prefix_front_kernel, dim3(P + B), dim3(kFrontThreads), 0, stream, p);
+  cudaError_t e = line::launch_front(PrefixFront{p}, P + B, max_blocks > prefix_blocks ? max_blocks : prefix_blocks, c.status,
+                                     stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefix front-end launch");
   e = pair ? launch_prefix_pair(p, dtype, tq, tk, tv, stream)
       : tc ? launch_prefix_tc(p, dtype, tq, tk, tv, stream)

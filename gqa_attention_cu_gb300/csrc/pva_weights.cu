@@ -6,8 +6,8 @@
 // pass are kept (few query rows: 4 bytes a row and key, against 2 d bytes of the key
 // itself) and a second kernel turns them into weights, or the keys are read twice.
 //
-//   pva_weights_front_kernel  one CTA per sequence: bounds and block table; the last
-//       one cuts the line of key tiles into pieces, one per SM.
+//   front end (pva_line.cuh)  bounds and block tables, and the line of key tiles, which
+//       is cut into a piece per SM.
 //   pva_weights_tc_kernel     f16/bf16 on tensor cores: Store, Apply, Stats (below).
 //   pva_weights_f32_kernel    f32 on the CUDA cores: Apply and Stats.
 //   pva_weights_rows_kernel   joins the pieces' maxima and sums of each query row.
@@ -30,7 +30,7 @@
 #include <limits.h>
 #include <math.h>
 
-#include "pva_device.cuh"
+#include "pva_line.cuh"
 #include "pva_tree.h"
 
 using namespace pva;
@@ -130,71 +130,30 @@ __device__ __forceinline__ int chunk_end(const WeightsParams& p, const Segment& 
   return max(s.j0, min(s.j1, tiles));
 }
 
-constexpr int kFrontThreads = 128;
-constexpr int kWordArrived = 16, kWordBad = 17;  // of the status block, zero between calls
-
-__global__ void __launch_bounds__(kFrontThreads) pva_weights_front_kernel(WeightsParams p) {
-  wait_prior_grid();
-  allow_next_grid();
-  __shared__ int s_last;
-  __shared__ long long s_sum[kFrontThreads / 32];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
-  const int n = p.lens[b], q = p.q_lens ? p.q_lens[b] : p.T;
-  uint32_t bad = 0;
-  if (n < 0 || n > p.width || (long long)n > (long long)p.max_blocks * p.page || q < 0 || q > p.T || q > n)
-    bad = PVA_DEV_KV_LEN;
-  bool off = false;
-  if (!bad && p.table)
-    for (int i = tid; i < (n + p.page - 1) / p.page; i += kFrontThreads)
-      off |= (unsigned)p.table[(size_t)b * p.max_blocks + i] >= (unsigned)p.n_blocks;
-  if (__syncthreads_or(off)) bad = PVA_DEV_BLOCKS;
-  auto places = [&](int i) {
-    const Sequence s(p, i);
-    const bool sane = s.n >= 0 && s.q >= 0 && s.n <= p.width && s.q <= p.T;
-    return sane ? s.per_head() * p.Hkv : 0ll;
-  };
-  if (tid == 0) {
-    if (bad) atomicOr(p.status + kWordBad, bad);
-    __threadfence();
-    s_last = atomicAdd(p.status + kWordArrived, 1u) == gridDim.x - 1;
+// The sequences on the line (pva_line.cuh).
+struct WeightsFront {
+  WeightsParams p;
+  __device__ __forceinline__ int entries() const { return p.B; }
+  __device__ __forceinline__ int32_t* start() const { return p.start; }
+  __device__ __forceinline__ uint32_t check(int b, int i0, int n, bool& off) const {
+    const int rows = p.lens[b], tokens = p.q_lens ? p.q_lens[b] : p.T;
+    if (rows < 0 || rows > p.width || (long long)rows > (long long)p.max_blocks * p.page || tokens < 0 ||
+        tokens > p.T || tokens > rows)
+      return PVA_DEV_KV_LEN;
+    off = p.table && line::off_pool(p.table + (size_t)b * p.max_blocks, rows, p.page, p.n_blocks, i0, n);
+    return 0u;
   }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  long long carry = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kFrontThreads) {
-    const int i = b0 + tid;
-    const long long x = i < p.B ? places(i) : 0;
-    long long upto = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-      if ((tid & 31) >= o) upto += y;
-    }
-    if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
-    __syncthreads();
-    long long before = carry;
-    for (int w = 0; w < kFrontThreads / 32; ++w) {
-      before += w < tid >> 5 ? s_sum[w] : 0;
-      carry += s_sum[w];
-    }
-    if (i < p.B) p.start[i] = (int)min(before + upto - x, (long long)INT_MAX);
-    __syncthreads();
-  }
-  if (tid == 0) {
-    uint32_t found = __ldcg(p.status + kWordBad);
-    p.status[kWordBad] = 0;  // for the next call
-    p.status[kWordArrived] = 0;
-    if (!found && carry > INT_MAX - 4ll * p.pieces) found = PVA_DEV_TOO_MANY;
+  __device__ __forceinline__ long long places(int b) const { return Sequence(p, b).per_head() * p.Hkv; }
+  __device__ __forceinline__ void publish(long long sum, uint32_t found, bool latched) const {
+    if (!found && sum > INT_MAX - 4ll * p.pieces) found = PVA_DEV_TOO_MANY;
     if (found) atomicOr(p.status, found);
-    const int all = found || latched ? 0 : (int)carry;
+    const int all = found || latched ? 0 : (int)sum;
     p.start[p.B] = all;
     p.hdr[0] = all > 0;
     p.hdr[1] = all;
     p.hdr[2] = max(1, (all + p.pieces - 1) / p.pieces);
   }
-}
+};
 
 // score -> natural units, with the softcap.
 template <bool CAP>
@@ -1098,7 +1057,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
         (rc = encode_plane_map(&tk, k_cache, dtype, d, page, (long long)n_blocks * Hkv, 64, box, true)) != PVA_OK)
       return rc;
   }
-  cudaError_t e = launch_dependent(pva_weights_front_kernel, dim3(B), dim3(kFrontThreads), 0, stream, p);
+  cudaError_t e = line::launch_front(WeightsFront{p}, B, max_blocks, c.status, stream);
   if (e != cudaSuccess) return cuda_fail(e, "weights front-end launch");
   auto pass = [&](int mode) {
     if (!tc) return mode == kApply ? launch_f32<kApply>(p, stream) : launch_f32<kStats>(p, stream);
