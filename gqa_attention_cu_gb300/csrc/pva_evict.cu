@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
       if (lane == 0 && zeros) atomicAdd(&s_bins[bin_of(weight_key(0.0f), 21, kBins)], __popc(zeros));
     }
   }
+  __syncthreads();  // the list below reads other threads' weights, also without a further count
   auto weight = [&](int j) { return j < held ? s_held[j] : w[j]; };
   if (want > 0) {
 #pragma unroll 1
@@ -181,8 +182,8 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
           if (4 * i + 3 < held) count(x.w, 4 * i + 3);
         }
         for (int j = held + tid; j < n; j += threads) count(w[j], j);
+        __syncthreads();
       }
-      __syncthreads();
       // the bin where the count from the top passes `want`: thread t has bins
       // [per t, per (t + 1)) from the top
       const int per = bins / threads;

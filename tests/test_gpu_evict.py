@@ -278,3 +278,21 @@ def test_two_streams_at_once():
         ref = expected(s, 3, 9, s["k"], s["v"], s["table"], s["w"], torch.zeros(s["w"].shape, dtype=torch.int32))
         assert pva.pva_get_status(st) == 0
         assert torch.equal(t["k"].cpu(), ref[0]) and torch.equal(t["v"].cpu(), ref[1]) and torch.equal(m.cpu(), ref[4])
+
+
+@pytest.mark.parametrize("width", [700, 2600, 9000])
+def test_all_rows_stay_of_many_sequences(width):
+    """Every row stays, so nothing is counted between the weights' way into shared memory
+    and the list of rows, which reads them in another order."""
+    g = torch.Generator(DEV).manual_seed(width)
+    layers, B, Hkv = 4, 64, 8
+    k, v = (torch.zeros(layers, B, Hkv, width, 2, device=DEV, dtype=torch.float16) for _ in range(2))
+    w = torch.randn(layers, B, Hkv, width, generator=g, device=DEV)
+    lens = torch.full((B,), width, dtype=torch.int32, device=DEV)
+    new_lens, out = torch.empty_like(lens), torch.empty_like(w)
+    for _ in range(10):
+        out.fill_(math.nan)
+        pva.pva_kvcache_evict(k, v, w, lens, lens, new_lens, weights_out=out)
+        assert torch.equal(bits(out), bits(w))
+        assert torch.equal(new_lens, lens)
+    assert pva.pva_get_status() == 0
