@@ -244,8 +244,14 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
   p.negated = tc && s < 0.0f;
   p.scale = tc ? fabsf(s) : s;
   p.softcap = fminf(fabsf(softcap), 1e34f);
-  if (p.softcap != 0.0f) {  // as in pva_gqa_tree
-    const double cap = p.softcap, t = fmin(0.25, pow(ldexp(1.0, -14) * 315.0 / 17.0 / cap, 1.0 / 7.0));
+  if (p.softcap != 0.0f) {
+    // Nearest polynomials up to kNearTanh and kMidTanh (pva_tree_tile.cuh); above
+    // kCapOfExp the series as in pva_gqa_tree, but while softcap times the term that it
+    // leaves out is below 2^-18, for the sums that are given out as f32.
+    const double cap = p.softcap;
+    const double t = tile::cap_form(p.softcap) == tile::kCap
+                         ? tile::kNearTanh
+                         : fmin(0.25, pow(ldexp(1.0, -18) * 315.0 / 17.0 / cap, 1.0 / 7.0));
     p.series_to = (float)fmin(t * cap / fabs(p.scale), 1e9);
     p.mid_to = (float)fmin(tile::kMidTanh * cap / fabs(p.scale), 1e9);
   }

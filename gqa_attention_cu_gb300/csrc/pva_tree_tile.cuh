@@ -41,18 +41,23 @@ __device__ __forceinline__ float tanh_of(float t) {
   return fabsf(t) <= 0.25f ? fmaf(t * w, p, t) : tanh_via_exp2(t);
 }
 
-// c tanh(t) + add for |t| <= kMidTanh: the odd polynomial of degree 9 that is nearest
-// to tanh there (fitted for the least largest error, 1.86e-7; times a softcap of
-// kCapOfExp that is below 2^-14, as the other forms' errors are).  Seven packed
-// instructions for two scores where exp takes four of the special-function unit's.
+// c tanh(t) + add for |t| <= kMidTanh: the odd polynomial of degree 11 that is nearest
+// to tanh there (fitted for the least largest error, 9.6e-9, which is below the rounding
+// of the result).  Eight packed instructions for two scores where exp takes four of the
+// special-function unit's.
 constexpr float kMidTanh = 0.75f;
+
+// Its like of degree 5 for |t| <= kNearTanh (4.9e-8), at the cost of the series' three
+// terms, which are off by 3.3e-6 there.
+constexpr float kNearTanh = 0.25f;
 __device__ __forceinline__ float2 mid_tanh(float2 t, float c, float2 add) {
   auto both = [](float x) { return make_float2(x, x); };
   const float2 w = ffma2(t, t, both(0.0f));
-  float2 p = ffma2(w, both(c * 0.012318834077f), both(c * -0.049280449660f));
-  p = ffma2(w, p, both(c * 0.132260917113f));
-  p = ffma2(w, p, both(c * -0.333230764944f));
-  p = ffma2(w, p, both(c * 0.999997228324f));
+  float2 p = ffma2(w, both(c * -0.004493455708f), both(c * 0.019237236540f));
+  p = ffma2(w, p, both(c * -0.053149261230f));
+  p = ffma2(w, p, both(c * 0.133205796551f));
+  p = ffma2(w, p, both(c * -0.333324708954f));
+  p = ffma2(w, p, both(c * 0.999999832473f));
   return ffma2(t, p, add);
 }
 
@@ -121,9 +126,9 @@ __device__ __forceinline__ void extremes(const uint32_t (&v)[32], uint32_t m, fl
 
 // 2^(x - m) of 32 scores, added to the two partial sums, and P as 16-bit pairs.
 // MODE 0: x = s * s_mul; with a softcap x = cap_mul * tanh(s * s_mul), by the
-// series' three terms (1), by exp (2), by tanh_of (3) or by mid_tanh (4).  P is rounded to the
-// storage type for the tensor-core product: at most half a step of each weight, as
-// V's own elements carry; the row sum adds the fp32 values.
+// series' three terms (1), by exp (2), by tanh_of (3), by mid_tanh (4) or by kNearTanh's
+// polynomial (5).  P is rounded to the storage type for the tensor-core product: at most
+// half a step of each weight, as V's own elements carry; the row sum adds the fp32 values.
 template <typename T, int MODE, bool MASKED>
 __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], uint32_t m, float s_mul,
                                              float cap_mul, float m_eff, float2 (&acc)[2],
@@ -132,8 +137,11 @@ __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], uint32_t m
   const float2 z = make_float2(0.0f, 0.0f);
   const float2 mul2 = make_float2(s_mul, s_mul), neg_m = make_float2(-m_eff, -m_eff);
   // cap_mul * tanh(u) with u = s * s_mul, as a polynomial in s
-  const float q1 = cap_mul * s_mul, q3 = q1 * s_mul * s_mul * (-1.0f / 3.0f);
-  const float q5 = q1 * (s_mul * s_mul) * (s_mul * s_mul) * (2.0f / 15.0f);
+  constexpr float a1 = MODE == 5 ? 0.9999986329869781f : 1.0f;
+  constexpr float a3 = MODE == 5 ? -0.3331570156623851f : -1.0f / 3.0f;
+  constexpr float a5 = MODE == 5 ? 0.1276223218419809f : 2.0f / 15.0f;
+  const float q0 = cap_mul * s_mul, q1 = q0 * a1, q3 = q0 * s_mul * s_mul * a3;
+  const float q5 = q0 * (s_mul * s_mul) * (s_mul * s_mul) * a5;
   const float2 c1 = make_float2(q1, q1), c3 = make_float2(q3, q3), c5 = make_float2(q5, q5);
 #pragma unroll
   for (int g = 0; g < 16; g += 8) {
@@ -144,7 +152,7 @@ __device__ __forceinline__ void exponentials(const uint32_t (&v)[32], uint32_t m
       const float2 s = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
       if (MODE == 0) {
         x[k] = ffma2(s, mul2, neg_m);
-      } else if (MODE == 1) {
+      } else if (MODE == 1 || MODE == 5) {
         const float2 w = ffma2(s, s, z);
         x[k] = ffma2(s, ffma2(w, ffma2(w, c5, c3), c1), neg_m);
       } else if (MODE == 4) {
@@ -248,8 +256,8 @@ __device__ __forceinline__ bool misplaced(const void* smem, const typename W::Pa
 // issue slots are 40% full, the tensor pipe 31%, memory 6%.  Any instruction more
 // lengthens the chain: a quarter of the exponentials by a polynomial on the FMA pipe
 // made them 203 us.
-// MID: between the series and exp there is a third form of the softcap (scores up to
-// p.mid_to).
+// MID: with kCap, nearest polynomials in the series' place and between it and exp (scores
+// up to p.series_to and p.mid_to).
 template <typename T, int N, int CAP, bool MID, typename Row>
 __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowView& view, int past,
                                                 int k0, uint32_t t_s, float s_mul, float cap_mul,
@@ -281,6 +289,7 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
     return CAP && __all_sync(0xffffffffu, !counts || mx == NEG_INF || fmaxf(fabsf(mx), fabsf(mn)) <= to);
   };
   bool mid = false;
+  constexpr int kSeries = MID && CAP == kCap ? 5 : 1;
   float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   bool series, done = false;
   if (all) {
@@ -300,7 +309,7 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
 #pragma unroll
       for (int c = 0; c < N / 32; ++c) {
         uint32_t pw[16];
-        exponentials<T, CAP ? 1 : 0, false>(v[c], 0u, s_mul, cap_mul, m_eff, acc, pw);
+        exponentials<T, CAP ? kSeries : 0, false>(v[c], 0u, s_mul, cap_mul, m_eff, acc, pw);
         tmem_st16(t_s + c * 16, pw);
       }
     } else if (MID && CAP == kCap && mid) {
@@ -338,7 +347,7 @@ __device__ __forceinline__ bool softmax_columns(const TreeParams& p, const RowVi
       else if (MID && CAP == kCap && mid)
         exponentials<T, 4, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       else if (series)
-        exponentials<T, 1, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
+        exponentials<T, kSeries, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       else
         exponentials<T, CAP == kLargeCap ? 3 : 2, true>(v, mask, s_mul, cap_mul, m_eff, acc, pw);
       // over columns whose scores have been read in this pass
