@@ -69,6 +69,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+constexpr uint32_t kLowestKey = 0x00800000u;  // of the finite weights
+
 // What is wrong with sequence b (PVA_DEV_* bits); the whole CTA calls.
 __device__ __forceinline__ uint32_t check_sequence(const EvictParams& p, int b, int n, int keep) {
   const int stay = min(n, keep);
@@ -107,11 +109,23 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
   extern __shared__ float s_held[];
   __shared__ int s_bins[kBins];
   __shared__ int s_warp[kSelectWarps];
-  __shared__ int s_bin, s_above;
+  __shared__ int s_bin, s_above, s_upto;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads / 32;
   const int item = blockIdx.x, b = item / p.Hkv % p.B;
   const int n = p.lens[b], keep = p.keep[b];
   const bool latched = (*(volatile uint32_t*)p.status & PVA_DEV_KV_CACHE) != 0;
+  const float* w = p.weights + (size_t)item * p.width;
+  // The next tile's weights are on their way while the table is checked, or a tile counted.
+  const int there = min(n, p.width);
+  float next[kPerThread];
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int j = j0 + k * threads + tid;
+      next[k] = j < there ? w[j] : 0.0f;
+    }
+  };
+  fetch(0);
   const uint32_t bad = latched ? 0u : check_sequence(p, b, n, keep);
   if (latched || bad) {
     if (tid == 0) {
@@ -128,14 +142,13 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
     p.length[item] = n;
     p.count[item] = stay;
   }
-  const float* w = p.weights + (size_t)item * p.width;
   const int lo = head, hi = n - tail;
   const int want = stay - head - tail;  // of the rows [lo, hi)
   // The key of the lightest row that stays, bit by bit from the top: `above` of the
   // rows are heavier than all that share the bits found so far.  The first count is
   // made while the weights come in, the others go over shared memory, four a thread.
   uint32_t prefix = 0;
-  int above = 0;
+  int above = 0, upto_bin = 0;  // rows of the bits found and above
   const int held = min(n, p.held);
   auto bin_of = [&](uint32_t key, int shift, int bins) { return (key >> shift) & (bins - 1); };
   for (int i = tid; i < kBins; i += threads) s_bins[i] = 0;
@@ -143,10 +156,8 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
   for (int j0 = 0; j0 < n; j0 += threads * kPerThread) {
     float x[kPerThread];
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      const int j = j0 + k * threads + tid;
-      x[k] = j < n ? w[j] : 0.0f;
-    }
+    for (int k = 0; k < kPerThread; ++k) x[k] = next[k];
+    if (j0 + threads * kPerThread < n) fetch(j0 + threads * kPerThread);
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
       const int j = j0 + k * threads + tid;
@@ -205,17 +216,23 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
           before += s_bins[bins - 1 - (tid * per + i)];
         s_bin = bins - 1 - (tid * per + i);
         s_above = before;
+        s_upto = before + s_bins[s_bin];
       }
       __syncthreads();
       prefix |= (uint32_t)s_bin << shift;
       above = s_above;
+      upto_bin = s_upto;
+      // All of the bin stay: its lower end will do as the limit (not below -inf, where
+      // that is no number).  Mostly after the second count.
+      if (upto_bin == want && prefix >= kLowestKey) break;
     }
   }
   // As weights: heavier than `limit`, or as heavy (a limit that is NaN is below all
   // numbers; without a limit nothing is either).
   const bool none = want == 0, nan_limit = prefix == 0;
   const float limit = __uint_as_float(prefix & 0x80000000u ? prefix & 0x7fffffffu : ~prefix);
-  const int equal = want - above;  // of the rows with this key, the first ones
+  const bool ties = upto_bin != want;  // of the rows with this key the first ones alone
+  const int equal = want - above;
   // In the rows' order: rows that stay because they are heavier (or first, or last),
   // and those with the key, counted side by side in 16 bits each within a tile.
   int32_t* rows = p.rows ? p.rows + (size_t)item * p.width : nullptr;
@@ -233,11 +250,17 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
       for (int k = 0; k < kPerThread; ++k) {
         const int j = j0 + 32 * k;
         x[k] = j < n ? weight(j) : 0.0f;
-        const bool open = j >= lo && j < hi, heavier = nan_limit ? x[k] == x[k] : x[k] > limit;
-        const bool alike = nan_limit ? x[k] != x[k] : x[k] == limit;
-        over[k] = __ballot_sync(0xffffffffu, j < n && (!open || (!none && heavier)));
-        same[k] = __ballot_sync(0xffffffffu, open && !none && alike);
-        in_warp += __popc(over[k]) | __popc(same[k]) << 16;
+        const bool open = j >= lo && j < hi;
+        if (ties) {
+          const bool heavier = nan_limit ? x[k] == x[k] : x[k] > limit;
+          const bool alike = nan_limit ? x[k] != x[k] : x[k] == limit;
+          over[k] = __ballot_sync(0xffffffffu, j < n && (!open || heavier));
+          same[k] = __ballot_sync(0xffffffffu, open && alike);
+          in_warp += __popc(over[k]) | __popc(same[k]) << 16;
+        } else {
+          over[k] = __ballot_sync(0xffffffffu, j < n && (!open || (!none && x[k] >= limit)));
+          in_warp += __popc(over[k]);
+        }
       }
     }
     if (lane == 0) s_warp[warp] = in_warp;
@@ -249,14 +272,19 @@ __global__ void __launch_bounds__(kSelectThreads) pva_evict_select_kernel(EvictP
       const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
       for (int k = 0; k < kPerThread; ++k) {
-        const int my_equal = n_equal + __popc(same[k] & below);
-        if ((over[k] >> lane & 1u) || ((same[k] >> lane & 1u) && my_equal < equal)) {
-          const int to = n_over + __popc(over[k] & below) + min(my_equal, equal);
+        int to = n_over + __popc(over[k] & below);
+        bool stays = over[k] >> lane & 1u;
+        if (ties) {
+          const int my_equal = n_equal + __popc(same[k] & below);
+          stays |= (same[k] >> lane & 1u) && my_equal < equal;
+          to += min(my_equal, equal);
+          n_equal += __popc(same[k]);
+        }
+        if (stays) {
           if (rows) rows[to] = j0 + 32 * k;
           if (out) out[to] = x[k];  // to <= the row itself: behind all that is still read
         }
         n_over += __popc(over[k]);
-        n_equal += __popc(same[k]);
       }
     }
     done_over += all & 0xffff;
