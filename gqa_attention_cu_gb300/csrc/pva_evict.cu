@@ -3,8 +3,8 @@
 // order, and close up.
 //
 //   pva_evict_select_kernel  one CTA per (layer, sequence, kv head): the weight of
-//       the last row that stays is found by its bits, from the top (three counts of 11,
-//       11 and 10 bits), then one pass in the rows' order lists those that stay and
+//       the last row that stays is found by its bits, from the top (up to three counts,
+//       of 11, 11 and 10 bits), then one pass in the rows' order lists those that stay and
 //       writes their weights.
 //   pva_evict_move_kernel    copies the listed rows to other blocks, or
 //   pva_evict_close_kernel   closes them up in place: a CTA owns some columns of all
@@ -15,11 +15,14 @@
 // from the lowest row on, so the choice does not depend on timing.
 //
 // 16 prompts of 4000 to 16,000 rows cut to 2048, 8 kv heads of 128 bf16, copied: 70 us.
-// The move is 44 of them, 268 MB at 6.1 TB/s (floor of the whole: 42); the choice 24,
-// bound by the latency of votes and counts with one CTA an SM: 6000 cycles a count, 7000
-// for 8192 rows listed.  (Clusters of four CTAs an item, counts through distributed
-// shared memory: 60 us for the choice.  Four rows in flight a thread and half as many
-// CTAs in the move: 51 us.)  One request of 700 rows: 14 us, of which 8 are launches.
+// The move is 44 of them, 268 MB at 6.1 TB/s (floor of the whole: 42); the choice 20,
+// bound by the latency of votes and counts with one CTA an SM; of 16,000 rows, in cycles:
+// lengths and table 8000, first count 10,000, second 6000, list 10,000.  (Clusters of
+// four CTAs an item, counts through distributed shared memory: 60 us for the choice.
+// Four copies of the first count's bins: no less.  Each CTA copying its own rows: 67
+// against 69 us for 128 items, but 113 against 91 for 160.  Four rows in flight a thread
+// and half as many CTAs in the move: 51 us.)  One request of 700 rows: 13 us, of which 8
+// are launches.
 #include <limits.h>
 
 #include "pva_device.cuh"
