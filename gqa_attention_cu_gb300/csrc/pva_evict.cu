@@ -517,7 +517,11 @@ extern "C" int pva_kvcache_evict(void* k_cache, void* v_cache, const float* weig
     const long long rows = (long long)max_blocks * page_size < width ? (long long)max_blocks * page_size : width;
     p.held = (int)(rows < kHeld ? rows : kHeld);
     const size_t smem = sizeof(float) * (((size_t)p.held + 3) / 4 * 4);
-    const int threads = rows <= 2048 ? 256 : rows <= 8192 ? 512 : kSelectThreads;
+    // 64 registers a thread: an SM holds one CTA of 1024 threads, two of 512, four of 256
+    // (us, 1024, 512 and 256: 160 items of 12,000 rows 91, 84, 98; 512 of 9000 151, 134,
+    // 131; 160 of 30,000 141, 151, 187; 2048 of 2000 287, 231, 211).
+    const bool more = items > c.num_sms;  // up to that 1024 (128 items of up to 16,000: 70 of 71.5)
+    const int threads = rows <= 2048 ? 256 : rows <= 8192 || (more && rows <= 16384) ? 512 : kSelectThreads;
     cudaError_t e = cudaFuncSetAttribute(pva_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)(sizeof(float) * kHeld));
     if (e == cudaSuccess)
