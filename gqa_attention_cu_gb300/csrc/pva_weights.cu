@@ -1029,7 +1029,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   std::lock_guard<std::mutex> lock(api_mutex());
   int rc = sm_count(&p.pieces);
   if (rc != PVA_OK) return rc;
-  if (!tc) p.pieces *= (int)((228 * 1024) / (f32_smem(d) + 3072));  // CTAs an SM holds
+  if (!tc) p.pieces *= (int)((228 * 1024) / (f32_smem(d) + 3 * 1024));  // CTAs an SM holds
   size_t used = 0;
   auto take = [&](size_t bytes) {
     const size_t at = used;
