@@ -49,6 +49,12 @@ def make(lens, keep, layers, Hkv, d, dtype, page, seed, width=None, kind="random
         w = special[torch.randint(0, len(special), w.shape, generator=g)]
     elif kind == "close":
         w = 1 + w.abs().clamp(max=3) * 2.0 ** -20  # alike in their upper bits
+    elif kind == "lowest":
+        w = torch.where(torch.rand(w.shape, generator=g) < 0.7, -math.inf, w)
+    elif kind == "tiny":
+        w = torch.where(torch.rand(w.shape, generator=g) < 0.5, 0.0, w * 1e-39)
+    elif kind == "huge":
+        w = -(w.abs() * 1e30) ** 1.2
     return dict(k=k, v=v, w=w, table=table, spare=spare, lens=torch.tensor(lens, dtype=torch.int32),
                 keep=torch.tensor(keep, dtype=torch.int32))
 
@@ -296,3 +302,20 @@ def test_all_rows_stay_of_many_sequences(width):
         assert torch.equal(bits(out), bits(w))
         assert torch.equal(new_lens, lens)
     assert pva.pva_get_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["lowest", "tiny", "huge"])
+@pytest.mark.parametrize("n,keep", [(300, 299), (2100, 90), (5000, 1500), (9000, 8999), (17000, 2048)])
+def test_limits_at_the_ends_of_the_range(n, keep, kind):
+    """Limits among -inf, denormals and numbers near the largest, where the lower end of
+    a range of bits need not be a weight."""
+    s = make([n], [keep], 1, 3, 2, "f16", 0, n + keep, kind=kind)
+    w_to, kept_to = torch.full_like(s["w"], 9.0), torch.full(s["w"].shape, -7, dtype=torch.int32)
+    ref = expected(s, 2, 3, s["k"], s["v"], None, w_to, kept_to)
+    gpu = {x: None if t is None else t.to(DEV) for x, t in dict(s, kept=kept_to, wo=w_to).items()}
+    new = torch.full_like(gpu["lens"], -5)
+    pva.pva_kvcache_evict(gpu["k"], gpu["v"], gpu["w"], gpu["lens"], gpu["keep"], new, first=2, last=3,
+                          weights_out=gpu["wo"], kept=gpu["kept"])
+    assert pva.pva_get_status() == 0
+    for got, want in zip((gpu["k"], gpu["v"], gpu["wo"], gpu["kept"], new), ref):
+        assert torch.equal(bits(got).cpu(), bits(want))
