@@ -549,13 +549,15 @@ __global__ void __launch_bounds__(kNormThreads, kBackCtas) pva_norm_rope_backwar
       // n mean(g w n) r = n (r^2 mean(g w x)), with n = x r
       const float m = -(row_sum<TPR>(inner.x + inner.y) * p.inv_d * r * r);
       const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+      // Lanes without a row work on zeros, whose r is infinite where eps is 0.
+      const bool mine = ok && at.row < at.n;
       P x[U], y[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float2 na = fmul2(v[i].a.v[e], r2), nb = fmul2(v[i].b.v[e], r2);
-          if (ok) {  // (rows that are not there are zeros)
+          if (mine) {
             da[i].v[e] = ffma2(g[i].a.v[e], na, da[i].v[e]);
             db[i].v[e] = ffma2(g[i].b.v[e], nb, db[i].v[e]);
           }
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kNormThreads, kBackCtas) pva_norm_rope_backwar
         }
         g[i].give(x[i], y[i]);
       }
-      if (ok && at.row < at.n) me.store_row(out, x, y);
+      if (mine) me.store_row(out, x, y);
       if (arrived) entries = me.fetch_entries(p, next_info, -1.0f);
       walk.next(at);
       out += row_step;

@@ -401,7 +401,8 @@ int pva_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const 
  *            dtype), the same for all heads; NULL: gains of one (weight_offset is
  *            then not used).  weight_offset: 0, or 1 for weights that are kept as
  *            their distance from one (any finite value).
- * eps      : finite, >= 0.
+ * eps      : finite, >= 0.  With eps = 0 a row whose squares add up to zero in f32 has
+ *            no norm: it comes out as NaN, and so do its gradient and the weight's.
  * rotary_dim : as in pva_rope_axes, or 0: norms only (the tables, position_ids and
  *            sections are then not used).
  * Everything else, the errors too, as in pva_rope_axes: outputs may take the place

@@ -223,6 +223,49 @@ def test_rows_of_zeros_and_large_values():
     near(out, ref, mass, "f32", 64)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("N,H,Hkv,d,rot,sections,pairs,inter", [
+    (1, 1, 1, 64, 64, None, False, False), (9, 12, 4, 64, 32, [8, 8], True, True), (37, 5, 2, 128, 128, [16, 24, 24], False, False),
+    (700, 6, 3, 96, 64, None, True, False), (3, 3, 1, 256, 0, None, False, False), (40, 9, 3, 30, 22, None, False, False)])
+def test_without_eps(N, H, Hkv, d, rot, sections, pairs, inter, dtype):
+    """eps = 0, rows and gradients, with head counts that leave lanes of a warp without a row."""
+    axes = 1 if sections is None else len(sections)
+    q, k, _, wq, wk, cos, sin, pos = inputs(N, H, Hkv, d, dtype, rot, axes, N + d)
+    g = torch.Generator().manual_seed(d + 1)
+    dyq, dyk = torch.randn(q.shape, generator=g).to(q.dtype), torch.randn(k.shape, generator=g).to(k.dtype)
+    qo, ko, dq, dk = (torch.empty_like(x, device=DEV) for x in (q, k, q, k))
+    dwq, dwk = torch.full((d,), 7.0, device=DEV), torch.full((d,), 7.0, device=DEV)
+    how = dict(eps=0.0, sections=sections, rotary_interleaved=pairs, axes_interleaved=inter)
+    c, s, p = gpu(cos, sin, pos)
+    pva.pva_norm_rope(*gpu(q, k, wq, wk), qo, ko, c, s, p, **how)
+    pva.pva_norm_rope_backward(*gpu(dyq, dyk, q, k, wq, wk), dq, dk, dwq, dwk, c, s, p, **how)
+    assert pva.pva_get_status() == 0
+    turn = dict(cos=cos, sin=sin, positions=pos, sections=sections, pairs_interleaved=pairs, axes_interleaved=inter)
+    for y, dx, dw, dy, x, w in ((qo, dq, dwq, dyq, q, wq), (ko, dk, dwk, dyk, k, wk)):
+        near(y, *longcache.norm_rope(x, w, 0.0, **turn), dtype, d)
+        ref, ref_w, mass, mass_w = longcache.norm_rope_grad(dy, x, w, 0.0, **turn)
+        near(dx, ref, 3 * mass, dtype, d)
+        rows = x.shape[0] * x.shape[1]
+        assert ((dw.cpu().double() - ref_w).abs() <= (rows + d / 2 + 16) * 2.0 ** -24 * mass_w).all()
+
+
+def test_a_row_without_a_norm():
+    """Zeros with eps = 0: NaN for the row and the weight's gradient, the other rows as with it."""
+    x = torch.randn(3, 2, 64, generator=torch.Generator().manual_seed(3))
+    x[1, 0] = 0
+    out, dx, dw = torch.empty_like(x, device=DEV), torch.empty_like(x, device=DEV), torch.empty(64, device=DEV)
+    w = torch.ones(64, device=DEV)
+    pva.pva_norm_rope(x.to(DEV), None, w, None, q_out=out, eps=0.0)
+    pva.pva_norm_rope_backward(x.to(DEV), None, x.to(DEV), None, w, None, dx, None, dw, None, eps=0.0)
+    assert torch.isnan(out[1, 0]).all() and torch.isnan(dx[1, 0]).all() and torch.isnan(dw).all()
+    rows = torch.ones(3, 2, dtype=torch.bool)
+    rows[1, 0] = False
+    ref, mass = longcache.norm_rope(x[rows][:, None], None, 0.0, cos=None, sin=None, positions=None)
+    near(out[rows][:, None], ref, mass, "f32", 64)
+    ref, _, mass, _ = longcache.norm_rope_grad(x[rows][:, None], x[rows][:, None], None, 0.0, cos=None, sin=None, positions=None)
+    near(dx[rows][:, None], ref, 3 * mass, "f32", 64)
+
+
 def test_weight_sums_are_repeatable_and_captured():
     """Equal bits from call to call and from a captured call, on a stream of its own."""
     N, H, Hkv, d = 3000, 8, 2, 128
