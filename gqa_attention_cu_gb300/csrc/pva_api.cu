@@ -797,6 +797,7 @@ int pva_selftest_wait(uint32_t limit_us, void* stream_, uint32_t* device_flags) 
   cudaFree(dev);
   if (e != cudaSuccess) return cuda_fail(e, "wait self-test");
   if (host[1] == 0) return fail(PVA_ERR_CUDA, "wait self-test kernel did not finish");
+  if (host[1] != 2) return fail(PVA_ERR_CUDA, "wait self-test: a wait ended too late or too early");
   *device_flags = host[0];
   return PVA_OK;
 }

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(DecCfg<DK, DV, G>::THREADS, 1)
       }
       for (int s = 0; s < C::STAGES; ++s) {
         const uint32_t fills = cnt > (uint32_t)s ? (cnt - 1 - s) / C::STAGES + 1 : 0;
-        if (fills) mbar_wait(&full[s], (fills - 1) & 1, abort, status);
+        if (fills) mbar_drain(&full[s], (fills - 1) & 1, status);
       }
     }
   } else {

@@ -214,6 +214,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The wait at a kernel's end for what is still in flight (copies into the CTA's shared
+// memory, matrix instructions on it): made also where a role has given up, when
+// mbar_wait would return at once.
+template <bool PARK = true>
+__device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, uint32_t* status,
+                                           uint64_t limit_ns = PVA_WAIT_LIMIT_NS) {
+  const uint64_t t0 = global_timer_ns();
+  while (!(PARK ? mbar_try_wait_sleep(bar, parity, PVA_WAIT_SLICE_NS) : mbar_try_wait(bar, parity))) {
+    if (global_timer_ns() - t0 > limit_ns) {
+      atomicOr(status, PVA_DEV_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tensor memory accelerator) copies global -> shared
 // ---------------------------------------------------------------------------

@@ -252,10 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish(v);
       }
       // Drain: every copy this thread issued must land before the CTA exits.
-      if (items) mbar_wait<false>(&bars->q_full, (items - 1) & 1, abort, status);
+      if (items) mbar_drain<false>(&bars->q_full, (items - 1) & 1, status);
       for (int s = 0; s < C::SLOTS; ++s) {
         const uint32_t fills = loads > (uint32_t)s ? (loads - 1 - s) / C::SLOTS + 1 : 0;
-        if (fills) mbar_wait<false>(&bars->ring_full[s], (fills - 1) & 1, abort, status);
+        if (fills) mbar_drain<false>(&bars->ring_full[s], (fills - 1) & 1, status);
       }
     }
   } else if (warp == 1) {
@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Drain: all issued MMAs complete before TMEM is released.
     commit(&bars->drain);
-    wait(&bars->drain, 0);
+    mbar_drain<false>(&bars->drain, 0, status);
+    __syncwarp();
   } else {
     // ------------------------------------------------- softmax + epilogue
     const int tq = warp >= 6 ? 1 : 0;  // query tile of this warpgroup

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Drain: every copy this thread issued must land before the CTA exits.
       for (int s = 0; s < C::SLOTS; ++s) {
         const uint32_t fills = loads > (uint32_t)s ? (loads - 1 - s) / C::SLOTS + 1 : 0;
-        if (fills) mbar_wait<false>(&bars->ring_full[s], (fills - 1) & 1, abort, status);
+        if (fills) mbar_drain<false>(&bars->ring_full[s], (fills - 1) & 1, status);
       }
     }
   } else if (warp == 1) {
@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Drain: all issued MMAs complete before TMEM is released.
     commit(&bars->drain);
-    wait(&bars->drain, 0);
+    mbar_drain<false>(&bars->drain, 0, status);
+    __syncwarp();
   } else {
     // ------------------------------------------------- softmax + epilogue
     // One thread per TMEM lane (query row).  These warps also move each Q

@@ -569,18 +569,26 @@ namespace pva {
 namespace {
 
 __global__ void pva_wait_selftest_kernel(uint32_t* status, uint64_t limit_ns, int* done) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, late;
   __shared__ int abort_flag;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(&bar, 1);
+    mbar_init(&late, 1);
     fence_mbar_init();
   }
   __syncthreads();
   // Nobody arrives on `bar`: every thread's wait must run out.
   const bool ok = mbar_wait(&bar, 0, &abort_flag, status, limit_ns);
   __syncthreads();
-  if (threadIdx.x == 0) *done = ok ? 1 : 2;
+  // What comes a while after that is waited for all the same.
+  if (threadIdx.x < 32) {
+    const bool drained = mbar_drain<false>(&late, 0, status);
+    if (threadIdx.x == 0) *done = ok ? 1 : drained ? 2 : 3;
+  } else if (threadIdx.x == 32) {
+    for (int i = 0; i < 200; ++i) __nanosleep(1000);
+    mbar_arrive(&late);
+  }
 }
 
 }  // namespace

@@ -232,10 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       W::give_up(p);  // nothing to join
     }
     // Drain: every copy this warp issued must land before the CTA exits.
-    if (rests) mbar_wait<false>(&bars->rest_full, (rests - 1) & 1, abort, status);
+    if (rests) mbar_drain<false>(&bars->rest_full, (rests - 1) & 1, status);
     for (int s = 0; s < C::SLOTS; ++s) {
       const uint32_t fills = loads > (uint32_t)s ? (loads - 1 - s) / C::SLOTS + 1 : 0;
-      if (fills) mbar_wait<false>(&bars->ring_full[s], (fills - 1) & 1, abort, status);
+      if (fills) mbar_drain<false>(&bars->ring_full[s], (fills - 1) & 1, status);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Drain: all issued MMAs complete before TMEM is released.
     if (leader) mma_commit(&bars->drain);
-    wait(&bars->drain, 0);
+    mbar_drain<false>(&bars->drain, 0, status);
+    __syncwarp();
   } else {
     // ------------------------------------------------- softmax + epilogue
     const int half = (warp - 2) >> 2;  // of the columns

@@ -388,11 +388,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Drain: every copy this warp issued must land before the CTA exits.
     for (int i = 0; i < C::Q_BUFS; ++i) {
       const uint32_t fills = q_loads > (uint32_t)i ? (q_loads - 1 - i) / C::Q_BUFS + 1 : 0;
-      if (fills) mbar_wait<false>(&bars->q_full[i], (fills - 1) & 1, abort, status);
+      if (fills) mbar_drain<false>(&bars->q_full[i], (fills - 1) & 1, status);
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       const uint32_t fills = loads > (uint32_t)i ? (loads - 1 - i) / C::SLOTS + 1 : 0;
-      if (fills) mbar_wait<false>(&bars->ring_full[i], (fills - 1) & 1, abort, status);
+      if (fills) mbar_drain<false>(&bars->ring_full[i], (fills - 1) & 1, status);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     // Drain: all issued MMAs complete before TMEM is released.
     if (leader) mma_commit(&bars->drain);
-    wait(&bars->drain, 0);
+    mbar_drain<false>(&bars->drain, 0, status);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ scores
     const int group = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;

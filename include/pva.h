@@ -735,10 +735,12 @@ int pva_kernel_times(float* ms, int capacity);
  * pva_selftest_wait -- exercises the bounded waits that every kernel of this
  * library uses on its pipeline barriers: one CTA waits on an mbarrier that
  * nothing ever completes, with a limit of `limit_us` microseconds
- * (1 .. 1000000).  The wait gives up, latches PVA_DEV_WAIT_TIMEOUT and the
- * kernel returns; *device_flags receives the bits it latched.  Synchronous on
- * `stream`; allocates and frees a few bytes of device memory.  Returns PVA_OK,
- * PVA_ERR_INVALID_ARG (limit out of range) or PVA_ERR_CUDA.
+ * (1 .. 1000000).  The wait gives up and latches PVA_DEV_WAIT_TIMEOUT; the kernel
+ * then waits for an arrival 0.2 ms later, as kernels wait for their copies in flight
+ * even then, and returns.  *device_flags receives the bits it latched.  Synchronous
+ * on `stream`; allocates and frees a few bytes of device memory.  Returns PVA_OK,
+ * PVA_ERR_INVALID_ARG (limit out of range) or PVA_ERR_CUDA (also where one of the
+ * waits ended otherwise).
  */
 int pva_selftest_wait(uint32_t limit_us, void* stream, uint32_t* device_flags);
 
