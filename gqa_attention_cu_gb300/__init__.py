@@ -23,6 +23,7 @@ __all__ = ["pva_forward", "pva_forward_local", "pva_forward_padded", "pva_gqa_kv
            "pva_gqa_prefix", "pva_kvcache_accept", "pva_kvcache_weights", "pva_kvcache_evict",
            "pva_get_status", "pva_schedule", "pva_status_string", "pva_last_error",
            "pva_release", "pva_version", "pva_profile", "pva_kernel_times", "pva_selftest_wait",
+           "pva_selftest_give_up",
            "load_library", "build", "PvaError", "DTYPE_CODES", "DEV_FLAGS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -125,6 +126,8 @@ def load_library(path: str | None = None):
         lib.pva_kernel_times.restype = i
         lib.pva_selftest_wait.argtypes = [ctypes.c_uint32, vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.pva_selftest_wait.restype = i
+        lib.pva_selftest_give_up.argtypes = [ctypes.c_uint32]
+        lib.pva_selftest_give_up.restype = i
         lib.pva_forward_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, f, i,
                                             vp, vp]
         lib.pva_forward_noalloc.restype = i
@@ -801,6 +804,11 @@ def pva_release() -> None:
 
 def pva_version() -> int:
     return int(load_library().pva_version())
+
+
+def pva_selftest_give_up(limit_us: int) -> None:
+    """Have the pipelines of later calls stall for limit_us microseconds and give up (0: no more)."""
+    _check(load_library().pva_selftest_give_up(int(limit_us)))
 
 
 def pva_selftest_wait(limit_us: int = 20000, stream=None) -> int:

@@ -154,6 +154,7 @@ struct CallContext {
 std::mutex& api_mutex();
 int sm_count(int* n);  // of the current device (under api_mutex)
 int acquire(cudaStream_t stream, size_t need, CallContext* c);
+uint64_t selftest_hold_ns();  // pva_selftest_give_up's, 0 in earnest
 // Runs the body of a C entry point: an exception (host memory running out)
 // becomes an error code instead of leaving through the C interface.
 template <typename F>

@@ -56,8 +56,9 @@ struct WeightsParams {
   int page, max_blocks, n_blocks;
   int tokens_at_once;      // of a chunk
   int pieces;
+  uint64_t hold_ns;        // > 0: the score warps wait as long for nothing and give up (pva_selftest_give_up)
   // workspace
-  int32_t* hdr;            // [0] accepted, [1] places, [2] places of a piece
+  int32_t* hdr;            // [0] accepted (until a wait is given up), [1] places, [2] places of a piece
   int32_t* start;          // [B + 1] first place of each sequence
   float2* part;            // [B * Hkv + pieces][parts][T * G] (m, l) of a piece's keys
   int parts;               // that a piece leaves for a row
@@ -183,7 +184,7 @@ struct ItemSlot {
 };
 
 struct Bars {
-  uint64_t q_full[2], q_empty[2], drain;
+  uint64_t q_full[2], q_empty[2], drain, never;
   uint64_t s_full[kGroups], s_free[kGroups];
   uint64_t ring_full[12], ring_empty[12];
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
       wait_prior_grid();
       atomicOr(p.status, PVA_DEV_WAIT_TIMEOUT);
+      atomicExch(p.hdr, 0);
     }
     return;
   }
@@ -281,6 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&bars->s_free[i], 4);
     }
     mbar_init(&bars->drain, 1);
+    mbar_init(&bars->never, 1);
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&bars->ring_full[i], 1);
       mbar_init(&bars->ring_empty[i], 1);
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    Walk walk(p, blockIdx.x, p.hdr[1], p.hdr[2]);
+    Walk walk(p, blockIdx.x, p.hdr[0] ? p.hdr[1] : 0, p.hdr[2]);
     const int box = p.table && p.page < kKeys ? p.page : kKeys, copies = kKeys / box;
     const uint64_t once = read_once_policy();  // keys leave L2 first: scores and weights stay there
     uint32_t loads = 0, published = 0, q_loads = 0;
@@ -460,6 +463,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(&bars->item_empty[isl]);
       ++taken;
       if (it.last) break;
+      if (p.hold_ns && !(ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->never, 0, abort, status, p.hold_ns)))) break;
       const Segment& s = it.s;
       const int t0 = it.c * p.tokens_at_once;
       const int used = max(0, min(p.tokens_at_once, s.q - t0)) * p.G;  // query rows of the chunk
@@ -620,6 +624,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc<C::TMEM_COLS>(tmem);
+  // Whoever gave up: what the later kernels would work with is not there.
+  if (threadIdx.x == 0 && *abort) atomicExch(p.hdr, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -652,7 +658,7 @@ __global__ void __launch_bounds__(kThreadsF32) pva_weights_f32_kernel(WeightsPar
   const float* q = static_cast<const float*>(p.q);
   for (int i = tid; i < (kKeys + kRowsF32) * (row - d); i += kThreadsF32)
     smem[(size_t)(i / (row - d)) * row + d + i % (row - d)] = 0.0f;
-  Walk walk(p, blockIdx.x, p.hdr[1], p.hdr[2]);  // the first warp's counts
+  Walk walk(p, blockIdx.x, p.hdr[0] ? p.hdr[1] : 0, p.hdr[2]);  // the first warp's counts
   while (true) {
     __syncthreads();
     if (warp == 0) {
@@ -868,6 +874,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) pva_weights_scores_kernel(We
   };
   if (x < end) look_up(x);
   wait_prior_grid();
+  if (!*(volatile int32_t*)p.hdr) return;  // (or given up)
   for (; x < end; ++x) {
     const int item = b * p.Hkv + h;
     const float* score = p.scores + (long long)x * R * kKeys + lane;
@@ -1060,6 +1067,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   }
   cudaError_t e = line::launch_front(WeightsFront{p}, B, max_blocks, c.status, stream);
   if (e != cudaSuccess) return cuda_fail(e, "weights front-end launch");
+  p.hold_ns = selftest_hold_ns();
   auto pass = [&](int mode) {
     if (!tc) return mode == kApply ? launch_f32<kApply>(p, stream) : launch_f32<kStats>(p, stream);
     return dtype == PVA_BF16 ? launch_type<__nv_bfloat16>(p, mode, n, tq, tk, stream)
@@ -1067,6 +1075,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   };
   if (!lse) {
     if ((e = pass(store ? kStore : kStats)) != cudaSuccess) return cuda_fail(e, "row sums launch");
+    p.hold_ns = 0;
   }
   if (!lse && !store) {
     const long long want = ((long long)B * Hkv * R + 7) / 8;

@@ -634,7 +634,9 @@ int pva_gqa_prefix(const void* q, const void* k_cache, const void* v_cache, cons
  * and the limits.  Device errors, nothing is then written: a length or token count
  * out of range (PVA_DEV_KV_LEN), a table entry outside the pool (PVA_DEV_BLOCKS), too
  * much work for 32-bit indices (PVA_DEV_TOO_MANY), or PVA_DEV_KV_CACHE latched on the
- * stream: the rejected step before has not written its rows.
+ * stream: the rejected step before has not written its rows.  A wait that is given up
+ * (PVA_DEV_WAIT_TIMEOUT, never expected) leaves weights as they were too, but in the
+ * pass that writes them (with lse the only one): some are then written.
  */
 int pva_kvcache_weights(const void* q, const void* k_cache, const int32_t* lens,
                         const int32_t* q_lens, const int32_t* block_table, const float* previous,
@@ -743,6 +745,14 @@ int pva_kernel_times(float* ms, int capacity);
  * waits ended otherwise).
  */
 int pva_selftest_wait(uint32_t limit_us, void* stream, uint32_t* device_flags);
+
+/*
+ * pva_selftest_give_up -- for tests of what a caller sees when a pipeline stalls: from
+ * the next call on, f16/bf16 pva_kvcache_weights (its first pass over the keys) waits
+ * limit_us microseconds (1 .. 1000000) for an arrival that does not come and gives up,
+ * latching PVA_DEV_WAIT_TIMEOUT; 0: as always again.  For the whole process.
+ */
+int pva_selftest_give_up(uint32_t limit_us);
 
 /* Human-readable text for a pva_status code (static storage). */
 const char* pva_status_string(int code);
