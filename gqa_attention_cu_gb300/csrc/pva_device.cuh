@@ -216,9 +216,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // The wait at a kernel's end for what is still in flight (copies into the CTA's shared
 // memory, matrix instructions on it): made also where a role has given up, when
-// mbar_wait would return at once.
+// mbar_wait would return at once.  Out of line: once a CTA, and inlined its code moves
+// that of the loops before it (softcapped drafts behind prefixes 78 to 86 us).
 template <bool PARK = true>
-__device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, uint32_t* status,
+__device__ __noinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, uint32_t* status,
                                            uint64_t limit_ns = PVA_WAIT_LIMIT_NS) {
   const uint64_t t0 = global_timer_ns();
   while (!(PARK ? mbar_try_wait_sleep(bar, parity, PVA_WAIT_SLICE_NS) : mbar_try_wait(bar, parity))) {
