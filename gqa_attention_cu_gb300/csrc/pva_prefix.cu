@@ -300,6 +300,7 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
   CallContext c;
   if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
   p.status = c.status;
+  p.hold_ns = selftest_hold_ns();
   p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
   p.tile_start = reinterpret_cast<int32_t*>(c.buf + at_start);
   p.part_o = reinterpret_cast<float*>(c.buf + at_o);

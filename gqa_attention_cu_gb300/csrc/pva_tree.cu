@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(256) pva_tree_join_kernel(TreeParams p) {
   wait_prior_grid();
   const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int c0 = blockIdx.x;
+  if (!p.hdr[0]) return;  // rejected, or given up
   const TreeCut it = p.cuts[c0];
   if (r < it.rows) {
     const int row = it.t * p.rows + r, node = row / p.G, n = it.parts;
@@ -578,6 +579,7 @@ int gqa_tree(const void* q, const void* k_new, const void* v_new, void* k_cache,
   if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
   p.status = c.status;
   p.cuts = reinterpret_cast<TreeCut*>(c.buf + at_cuts);
+  p.hold_ns = selftest_hold_ns();
   p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
   p.tile_start = reinterpret_cast<int32_t*>(c.buf + at_tiles);
   p.item_start = reinterpret_cast<int32_t*>(c.buf + at_items);

@@ -71,9 +71,11 @@ struct TreeParams {
   int pieces;              // CTAs of the attention kernel
   int may_take_items;      // the kernel can work by whole items
   int min_chunk;           // key tiles a piece has at least
+  uint64_t hold_ns;        // > 0: the matrix warp waits as long for nothing and gives up
+                           // (pva_selftest_give_up)
   // workspace
-  int32_t* hdr;            // [0] accepted, [1] n_tiles, [2] chunk, [3] items to take (0: by
-                           // pieces), [4] items taken
+  int32_t* hdr;            // [0] accepted (until a wait is given up), [1] n_tiles, [2] chunk,
+                           // [3] items to take (0: by pieces), [4] items taken
   int32_t* item_start;     // [B + 1] first item of each sequence
   int32_t* tile_start;     // [B + 1] first tile of each sequence on the line
   int32_t* q_start;        // [B][QT + 1] tiles before each q tile, within one kv head

@@ -72,7 +72,7 @@ struct ItemSlot {
 
 template <typename W>
 struct Bars {
-  uint64_t q_full, q_empty, drain;
+  uint64_t q_full, q_empty, drain, never;
   uint64_t s_full[2], p_full[2], o_ready[2], o_done[2], o_free[2];
   uint64_t ring_full[16], ring_empty[16];
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->drain, 1);
+    mbar_init(&bars->never, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->p_full[x], kGroupWarps);
@@ -208,8 +209,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       v.last = 1;
       publish(v);
-    } else if (lane == 0) {
-      W::give_up(p);  // nothing to join
     }
     // Drain: every copy this warp issued must land before the CTA exits.
     if (q_loads) mbar_drain<false>(&bars->q_full, (q_loads - 1) & 1, status);
@@ -261,6 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (leader) mbar_arrive(&bars->item_empty[isl]);
       if (last) break;
+      if (p.hold_ns && !(ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->never, 0, abort, status, p.hold_ns))))
+        break;
       const int n = s.count, n_q = has_second<W>(p, s) ? 2 : 1;
       if (!(ok = wait(&bars->q_full, items & 1))) break;
       ++items;
@@ -380,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc<C::TMEM_COLS>(tmem);
+  if (threadIdx.x == 0 && *abort) W::give_up(p);  // whoever gave up: nothing is joined
 }
 
 }  // namespace paired

@@ -83,7 +83,7 @@ struct ItemSlot {
 
 template <typename W>
 struct Bars {
-  uint64_t q_tmem, o_ready, o_done, o_free, drain;
+  uint64_t q_tmem, o_ready, o_done, o_free, drain, never;
   uint64_t rest_full, rest_empty;
   uint64_t s_full[2], p_full[2];
   uint64_t meet[4];
@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->o_free, kSoftmaxWarps);
     for (int w = 0; w < 4; ++w) mbar_init(&bars->meet[w], 2);
     mbar_init(&bars->drain, 1);
+    mbar_init(&bars->never, 1);
     mbar_init(&bars->rest_full, 1);
     mbar_init(&bars->rest_empty, 1);
     for (int b = 0; b < 2; ++b) {
@@ -228,8 +229,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       v.last = 1;
       publish(v);
-    } else if (lane == 0) {
-      W::give_up(p);  // nothing to join
     }
     // Drain: every copy this warp issued must land before the CTA exits.
     if (rests) mbar_drain<false>(&bars->rest_full, (rests - 1) & 1, status);
@@ -290,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) mbar_arrive(&bars->item_empty[isl]);
       ++taken;
       if (last) break;
+      if (p.hold_ns && !(ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->never, 0, abort, status, p.hold_ns))))
+        break;
       // Q is in TMEM once every softmax thread has copied its share.
       if (!(ok = wait(&bars->q_tmem, q_cnt & 1))) break;
       if (rest_in_smem && !(ok = wait(&bars->rest_full, q_cnt & 1))) break;
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc<C::TMEM_COLS>(tmem);
+  if (threadIdx.x == 0 && *abort) W::give_up(p);  // whoever gave up: nothing is joined
 }
 
 }  // namespace one_tile

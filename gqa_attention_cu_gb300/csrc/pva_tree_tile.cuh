@@ -527,7 +527,8 @@ struct TreeWork {
     const size_t at = (size_t)s.slot * p.rows + lr;
     return {p.part_o + at * p.d, p.part_ml + at};
   }
-  static __device__ __forceinline__ void give_up(const Params& p) { tree_note_cut(p, blockIdx.x, nullptr); }
+  // a wait was given up: nothing is joined
+  static __device__ __forceinline__ void give_up(const Params& p) { atomicExch(p.hdr, 0); }
 };
 
 }  // namespace tile

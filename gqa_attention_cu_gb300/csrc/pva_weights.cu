@@ -56,7 +56,7 @@ struct WeightsParams {
   int page, max_blocks, n_blocks;
   int tokens_at_once;      // of a chunk
   int pieces;
-  uint64_t hold_ns;        // > 0: the score warps wait as long for nothing and give up (pva_selftest_give_up)
+  uint64_t hold_ns;        // > 0: the matrix warp waits as long for nothing and gives up (pva_selftest_give_up)
   // workspace
   int32_t* hdr;            // [0] accepted (until a wait is given up), [1] places, [2] places of a piece
   int32_t* start;          // [B + 1] first place of each sequence
@@ -415,6 +415,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (leader) mbar_arrive(&bars->item_empty[isl]);
       ++taken;
       if (last) break;
+      if (p.hold_ns && !(ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->never, 0, abort, status, p.hold_ns))))
+        break;
       if (j0 == end) continue;
       const int qb = q_cnt % C::Q_BUFS;
       if (!(ok = wait(&bars->q_full[qb], (q_cnt / C::Q_BUFS) & 1))) break;
@@ -463,7 +465,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(&bars->item_empty[isl]);
       ++taken;
       if (it.last) break;
-      if (p.hold_ns && !(ok = __all_sync(0xffffffffu, mbar_wait<false>(&bars->never, 0, abort, status, p.hold_ns)))) break;
       const Segment& s = it.s;
       const int t0 = it.c * p.tokens_at_once;
       const int used = max(0, min(p.tokens_at_once, s.q - t0)) * p.G;  // query rows of the chunk

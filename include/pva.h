@@ -51,7 +51,8 @@ typedef enum { PVA_F32 = 0, PVA_F16 = 1, PVA_BF16 = 2 } pva_dtype;
 /* Device-side status bits, latched by the on-device scheduler and read with
  * pva_get_status.  When any bit is set the call wrote nothing to `out` (but see
  * pva_rope_axes, pva_norm_rope, pva_kvcache_accept and pva_kvcache_evict, which
- * leave out single tokens and sequences). */
+ * leave out single tokens and sequences).  After PVA_DEV_WAIT_TIMEOUT (never
+ * expected) some rows of an output may be written. */
 #define PVA_DEV_CU_Q_START 0x1u   /* cu_seqlens_q[0] != 0 */
 #define PVA_DEV_CU_KV_START 0x2u  /* cu_seqlens_kv[0] != 0 */
 #define PVA_DEV_CU_Q_ORDER 0x4u   /* cu_seqlens_q decreases somewhere */
@@ -748,9 +749,10 @@ int pva_selftest_wait(uint32_t limit_us, void* stream, uint32_t* device_flags);
 
 /*
  * pva_selftest_give_up -- for tests of what a caller sees when a pipeline stalls: from
- * the next call on, f16/bf16 pva_kvcache_weights (its first pass over the keys) waits
- * limit_us microseconds (1 .. 1000000) for an arrival that does not come and gives up,
- * latching PVA_DEV_WAIT_TIMEOUT; 0: as always again.  For the whole process.
+ * the next call on, f16/bf16 pva_gqa_tree, pva_gqa_prefix and pva_kvcache_weights (its
+ * first pass over the keys) wait limit_us microseconds (1 .. 1000000) for an arrival
+ * that does not come and give up, latching PVA_DEV_WAIT_TIMEOUT; 0: as always again.
+ * For the whole process.
  */
 int pva_selftest_give_up(uint32_t limit_us);
 
