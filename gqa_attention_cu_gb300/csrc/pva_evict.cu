@@ -316,22 +316,24 @@ __global__ void __launch_bounds__(kMoveThreads) pva_evict_move_kernel(EvictParam
   wait_prior_grid();
   const int item = blockIdx.y, b = item / p.Hkv % p.B, h = item % p.Hkv;
   const long long layer = item / p.Hkv / p.B;
-  const int n = p.count[item];
-  if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && layer == 0) p.new_lens[b] = n;
+  const int stay = p.count[item];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && layer == 0) p.new_lens[b] = stay;
   if (p.length[item] < 0) return;
+  const unsigned n = stay;
   const int32_t* rows = p.rows + (size_t)item * p.width;
   const int units = p.row_bytes / (int)sizeof(U), u0 = threadIdx.x % lanes;
   const int per = kMoveThreads / lanes;  // rows of a CTA at once
   const long long from = layer * p.from.layer_bytes, to = layer * p.to.layer_bytes;
-  for (int i0 = blockIdx.x * per * kMoveAhead + threadIdx.x / lanes; i0 < n;
+  // (a step of all CTAs may lead past 2^31)
+  for (unsigned i0 = blockIdx.x * per * kMoveAhead + threadIdx.x / lanes; i0 < n;
        i0 += gridDim.x * per * kMoveAhead) {
     long long src[kMoveAhead], dst[kMoveAhead];
 #pragma unroll
     for (int a = 0; a < kMoveAhead; ++a) {
-      const int i = i0 + a * per;
+      const unsigned i = i0 + a * per;
       if (i >= n) continue;
       src[a] = from + row_at(p, p.from, b, h, rows[i]);
-      dst[a] = to + row_at(p, p.to, b, h, i);
+      dst[a] = to + row_at(p, p.to, b, h, (int)i);
     }
     for (int u = u0; u < units; u += lanes) {
       U x[kMoveAhead], y[kMoveAhead];

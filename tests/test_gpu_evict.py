@@ -319,3 +319,25 @@ def test_limits_at_the_ends_of_the_range(n, keep, kind):
     assert pva.pva_get_status() == 0
     for got, want in zip((gpu["k"], gpu["v"], gpu["wo"], gpu["kept"], new), ref):
         assert torch.equal(bits(got).cpu(), bits(want))
+
+
+def test_as_many_rows_as_a_call_takes():
+    """Rows up to the end of int32, less what the kernels' steps need, copied without one of them."""
+    n = 2 ** 31 - 1 - 65536
+    k, v = (torch.empty(1, 1, n, 1, dtype=torch.int16, device=DEV).random_(-2 ** 14, 2 ** 14).view(torch.float16) for _ in range(2))
+    w = torch.zeros(1, 1, n, device=DEV)
+    gone = n - 700_000
+    w[0, 0, gone] = -1
+    lens, keep = (torch.tensor([x], dtype=torch.int32, device=DEV) for x in (n, n - 1))
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    kept = torch.full((1, 1, n), -7, dtype=torch.int32, device=DEV)
+    new = torch.zeros_like(lens)
+    pva.pva_kvcache_evict(k, v, w, lens, keep, new, k_out=ko, v_out=vo, kept=kept)
+    assert pva.pva_get_status() == 0 and int(new) == n - 1
+    for a, b in ((k, ko), (v, vo)):
+        a, b = (x.view(-1).view(torch.int16) for x in (a, b))
+        assert torch.equal(a[:gone], b[:gone]) and torch.equal(a[gone + 1:], b[gone:-1]) and int(b[-1]) == 0
+    kept = kept.view(-1)
+    assert int(kept[-1]) == -7 and int(kept[gone - 1]) == gone - 1 and int(kept[-2]) == n - 1
+    del k, v, w, ko, vo, kept, a, b
+    torch.cuda.empty_cache()
