@@ -31,25 +31,44 @@ struct PrefixFront {
   PrefixParams p;
   __device__ __forceinline__ int entries() const { return p.P + p.B; }
   __device__ __forceinline__ int32_t* start() const { return p.tile_start; }
+  // Whether a token in use sees the entry's rows: of the others nothing is read, nor has
+  // their table (or a prefix's length) to be sound.
+  __device__ __forceinline__ bool wanted(int e) const {
+    if (e >= p.P) return tree_nodes(p, e - p.P) != 0;
+    int b = p.prefix_start ? p.prefix_start[e] : 0;
+    const int end = p.prefix_start ? p.prefix_start[e + 1] : p.B;
+    while (b < end && tree_nodes(p, b) == 0) ++b;
+    return b < end;
+  }
+  // (what depends on nothing is loaded first)
   __device__ __forceinline__ uint32_t check(int e, int i0, int n, bool& off) const {
     const bool is_prefix = e < p.P;
     const int b = is_prefix ? e : e - p.P;
     const int keys = is_prefix ? p.prefix_keys[b] : p.keys[b];
     const int32_t* table = is_prefix ? p.prefix_table : p.table;
     const int width = is_prefix ? p.prefix_blocks : p.max_blocks;
-    uint32_t bad = keys < 0 || (long long)keys > (long long)width * p.page ? PVA_DEV_KV_LEN : 0u;
-    if (!is_prefix) {
-      const int tokens = tree_nodes(p, b);
-      if (tokens < 0 || tokens > p.T || tokens > keys) bad = PVA_DEV_KV_LEN;
-    } else if (p.prefix_start) {
-      const int first = p.prefix_start[b], end = p.prefix_start[b + 1];
+    const int first = !is_prefix ? b : p.prefix_start ? p.prefix_start[e] : 0;
+    const int end = !is_prefix ? b + 1 : p.prefix_start ? p.prefix_start[e + 1] : p.B;
+    const int tokens = tree_nodes(p, min(max(first, 0), p.B - 1));
+    const long long room = (long long)width * p.page;
+    const bool some_off = table && line::off_pool(table + (size_t)b * width, (int)min((long long)keys, room), p.page,
+                                                  p.n_blocks, i0, n);
+    if (is_prefix) {
       if (first < 0 || end < first || end > p.B || (b == 0 && first != 0) || (b == p.P - 1 && end != p.B))
-        bad |= PVA_DEV_PREFIX;
+        return PVA_DEV_PREFIX;
+      if (first == end || (tokens == 0 && !wanted(e))) return 0u;
+      if (keys < 0 || keys > room) return PVA_DEV_KV_LEN;
+      off = some_off;
+    } else {
+      if (tokens < 0 || tokens > p.T || tokens > keys || keys < 0 || keys > room) return PVA_DEV_KV_LEN;
+      off = some_off && tokens > 0;
     }
-    off = !bad && table && line::off_pool(table + (size_t)b * width, keys, p.page, p.n_blocks, i0, n);
-    return bad;
+    return 0u;
   }
-  __device__ __forceinline__ long long places(int e) const { return prefix_entry(p, e).per_head(p) * p.Hkv; }
+  __device__ __forceinline__ long long places(int e) const {
+    const PrefixEntry x = prefix_entry(p, e);
+    return wanted(e) ? x.per_head(p) * p.Hkv : 0;
+  }
   __device__ __forceinline__ void publish(long long sum, uint32_t found, bool latched) const {
     if (!found && sum > INT_MAX - 4ll * p.pieces) found = PVA_DEV_TOO_MANY;
     if (found) atomicOr(p.status, found);
@@ -59,7 +78,7 @@ struct PrefixFront {
     // One prefix of several query tiles: where it costs little, its items are all cut
     // alike, so that the CTAs of the same keys read them at the same time, from L2 (64
     // sequences behind 32,768 rows, with item costs that cut them otherwise: 113 to 101 us).
-    if (ok && p.P == 1) {
+    if (all > 0 && p.P == 1) {
       const PrefixEntry head = prefix_entry(p, 0);
       const int per = head.places(p);
       if (head.q_tiles(p) > 1 && per > chunk) {

@@ -587,6 +587,8 @@ int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* past_lens,
  * kv_num_heads <= 128.  The workspace holds two f32 rows of head_size per query row.  Results do not depend on timing.  A value row that some token
  * sees should be finite: an infinity or NaN there can reach its other tokens, and in a
  * prefix all of its sequences.
+ * A prefix none of whose sequences has a token in use needs neither a length nor blocks,
+ * and a sequence without one needs no blocks: both may be stale.
  * Host errors: null pointers, counts below 1 or out of int32, and the limits.  Device
  * errors, out and lse are then left as they were: a length or token count out of range
  * (PVA_DEV_KV_LEN), a bad prefix_start (PVA_DEV_PREFIX), a needed table entry outside

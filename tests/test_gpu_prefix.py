@@ -204,6 +204,37 @@ def test_bad_calls_write_nothing(kind, flag, dtype):
     assert pva.pva_get_status() == 0 and torch.equal(a[0], b[0]) and torch.isfinite(a[0]).all()
 
 
+@pytest.mark.parametrize("many", [False, True])  # front ends of one CTA and of one an entry
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_what_no_token_sees_may_be_stale(dtype, many):
+    """Lengths and tables of prefixes without a token in use, and tables of sequences
+    without one: as if they were sound."""
+    lens, used, start, prefixes = [30, 64, 9, 20, 0], [2, 0, 1, 0, 0], [0, 1, 1, 3, 5], [100, 50, 70, 33]
+    if many:
+        lens, used, start, prefixes = lens + [5] * 40, used + [2] * 40, start + [45], prefixes + [20]
+    s, out = parity(lens, prefixes, 2, 4, 2, 64, dtype, 16, 24, start=start, used=used)
+    for length in (-5, 10 ** 8, 2 ** 31 - 1):
+        s["prefixes"][1] = s["prefixes"][3] = length
+        s["prefix_table"][1], s["prefix_table"][3] = -1, s["k"].shape[0]
+        s["table"][1], s["table"][3] = -1, 2 ** 31 - 1
+        got, _ = call(s, 4, 2)
+        assert pva.pva_get_status() == 0 and torch.equal(got, out)
+    s["used"][1] = 1
+    call(s, 4, 2)
+    assert pva.pva_get_status() == pva.DEV_FLAGS["blocks"]
+    s["used"][1], s["used"][4] = 0, 0
+    s["lens"][1] = -1
+    call(s, 4, 2)
+    assert pva.pva_get_status() == pva.DEV_FLAGS["kv_len"]
+
+
+def test_one_prefix_of_an_idle_batch():
+    s, out = parity([3, 8], [40], 2, 4, 2, 64, "bf16", 16, 25, used=[0, 0])
+    s["prefixes"][0], s["prefix_table"][:], s["table"][:] = 2 ** 31 - 1, -1, -1
+    got, sums = call(s, 4, 2)
+    assert pva.pva_get_status() == 0 and (got == 0).all() and (sums == -math.inf).all()
+
+
 def test_after_a_rejected_step_nothing_is_written():
     s = make([30], [40], 1, 4, 2, 64, "bf16", 16, 19)
     q, c = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16, device=DEV)
