@@ -64,6 +64,7 @@ struct Workspace {
   uint32_t* status = nullptr;  // sticky status word (never moves); 256 bytes, zeroed once
   void* buf = nullptr;         // int region + partials
   size_t bytes = 0;
+  size_t denied = 0;           // the least size that there was no memory for (acquire_most)
   bool in_graph = false;       // handed to a call that was being captured
   std::vector<void*> retired;  // outgrown buffers that a captured graph may still use
 };
@@ -400,6 +401,21 @@ int acquire(cudaStream_t stream, size_t need, CallContext* c) {
   c->status = w->status;
   c->buf = static_cast<uint8_t*>(w->buf);
   return PVA_OK;
+}
+
+int acquire_most(cudaStream_t stream, size_t want, size_t least, CallContext* c, bool* all) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  Workspace& w = g_ws[{dev, stream}];
+  *all = !w.denied || want < w.denied;
+  if (*all) {
+    const int rc = acquire(stream, want, c);
+    if (rc != PVA_ERR_OOM) return rc;
+    w.denied = want;
+    *all = false;
+  }
+  return acquire(stream, least, c);
 }
 
 }  // namespace host

@@ -154,6 +154,10 @@ struct CallContext {
 std::mutex& api_mutex();
 int sm_count(int* n);  // of the current device (under api_mutex)
 int acquire(cudaStream_t stream, size_t need, CallContext* c);
+// The same for a call that can do with `least` bytes where there is no memory for `want`
+// (*all: it got those).  A size that was once denied on a stream is not asked for again
+// until pva_release: later calls neither allocate nor work otherwise than the first.
+int acquire_most(cudaStream_t stream, size_t want, size_t least, CallContext* c, bool* all);
 uint64_t selftest_hold_ns();  // pva_selftest_give_up's, 0 in earnest
 // Runs the body of a C entry point: an exception (host memory running out)
 // becomes an error code instead of leaving through the C interface.

@@ -1030,28 +1030,40 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   const int n = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
   p.tokens_at_once = tc ? (R <= 128 ? T : 128 / G) : T;
   // Scores are kept where there are few rows, and in no more memory than the keys have
-  // or 256 MB (tables may be far wider than the pool).
+  // or 256 MB (tables may be far wider than the pool), if there is as much.
   const size_t tiles = ((size_t)(width < (long long)max_blocks * page ? width : (long long)max_blocks * page) + kKeys - 1) / kKeys;
   const size_t kept = 4 * (size_t)B * Hkv * tiles * R * kKeys, pool = 2 * (size_t)n_blocks * Hkv * page * d;
-  const bool store = tc && !lse && R <= 16 && kept <= (pool > (256u << 20) ? pool : 256u << 20);
+  bool store = tc && !lse && R <= 16 && kept <= (pool > (256u << 20) ? pool : 256u << 20);
 
   std::lock_guard<std::mutex> lock(api_mutex());
   int rc = sm_count(&p.pieces);
   if (rc != PVA_OK) return rc;
   if (!tc) p.pieces *= (int)((228 * 1024) / (f32_smem(d) + 3 * 1024));  // CTAs an SM holds
-  size_t used = 0;
-  auto take = [&](size_t bytes) {
-    const size_t at = used;
-    used += (bytes + 255) / 256 * 256;
-    return at;
+  size_t at_hdr, at_start, at_part, at_row, at_scores;
+  auto lay_out = [&]() {
+    size_t used = 0;
+    auto take = [&](size_t bytes) {
+      const size_t at = used;
+      used += (bytes + 255) / 256 * 256;
+      return at;
+    };
+    at_hdr = take(32), at_start = take(4 * ((size_t)B + 1));
+    p.parts = !tc ? 1 : store ? 4 * kGroups : kGroups;
+    at_part = take(lse ? 0 : 8 * ((size_t)B * Hkv + p.pieces) * p.parts * R);
+    at_row = take(lse ? 0 : 8 * (size_t)B * Hkv * R);
+    at_scores = take(store ? kept : 0);
+    return used;
   };
-  const size_t at_hdr = take(32), at_start = take(4 * ((size_t)B + 1));
-  p.parts = !tc ? 1 : store ? 4 * kGroups : kGroups;
-  const size_t at_part = take(lse ? 0 : 8 * ((size_t)B * Hkv + p.pieces) * p.parts * R);
-  const size_t at_row = take(lse ? 0 : 8 * (size_t)B * Hkv * R);
-  const size_t at_scores = take(store ? kept : 0);
+  const size_t most = lay_out();
   CallContext c;
-  if ((rc = acquire(stream, used, &c)) != PVA_OK) return rc;
+  if (store) {
+    store = false;
+    const size_t least = lay_out();
+    if ((rc = acquire_most(stream, most, least, &c, &store)) != PVA_OK) return rc;
+    lay_out();
+  } else if ((rc = acquire(stream, most, &c)) != PVA_OK) {
+    return rc;
+  }
   p.status = c.status;
   p.hdr = reinterpret_cast<int32_t*>(c.buf + at_hdr);
   p.start = reinterpret_cast<int32_t*>(c.buf + at_start);

@@ -630,7 +630,8 @@ int pva_gqa_prefix(const void* q, const void* k_cache, const void* v_cache, cons
  * order: equal calls give equal bits.  Without lse and with tokens * num_heads /
  * kv_num_heads <= 16 (f16/bf16) the scores are kept in the workspace, 4 bytes for each
  * of these query rows and entry of weights, unless that is more than the pool's keys
- * and than 256 MB; otherwise, and with more query rows, the keys are read twice.
+ * and than 256 MB, or than there was memory for (then also in later calls on the stream,
+ * until pva_release); otherwise, and with more query rows, the keys are read twice.
  * Limits: head sizes, page sizes and alignment as pva_gqa_tree; num_heads /
  * kv_num_heads <= 128.
  * Host errors: null pointers, counts below 1 or out of int32, weights over an input,

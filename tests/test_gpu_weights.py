@@ -218,3 +218,49 @@ def test_tables_far_wider_than_the_pool():
     assert pva.pva_get_status() == 0
     check(got[:, :, :s["to"].shape[2]], s, 4)
     assert torch.allclose(got[:, :, :200], narrow[:, :, :200], rtol=1e-4, atol=0) and (got[:, :, s["to"].shape[2]:] == 0).all()
+
+
+def test_scores_that_find_no_memory():
+    """A cache that leaves no memory for the scores of its capacity: the keys are read
+    twice, now and later, eagerly and captured."""
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    B, H, d, page, lens = 2, 16, 64, 2 ** 20, [300, 77]
+    blocks = int(0.53 * free) // (2 * page * d)  # scores of as many rows do not fit beside that
+    width = blocks * page  # entries of 64 bytes of scores each, as many bytes as the keys have
+    s = make(lens, 1, H, 1, d, "bf16", 512, 35)
+    k = torch.empty(blocks, 1, page, d, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(B, blocks, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        table[b, 0] = b * (blocks - 1)
+        k[table[b, 0], 0, :n] = s["k"][int(s["table"][b, 0]), 0, :n].to(DEV)
+    to = torch.empty(B, 1, width, device=DEV)
+    q, n, t = gpu(s["q"]), gpu(s["lens"]), gpu(table)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def call():
+        pva.pva_kvcache_weights(q, k, n, to, H, block_table=t, stream=stream)
+        stream.synchronize()
+        return to[:, :, :max(lens)].clone()
+
+    def fill():
+        to[:, :, :400] = 7
+        torch.cuda.synchronize()
+    fill()
+    got = call()
+    assert pva.pva_get_status(stream) == 0
+    check(torch.cat([got, gpu(s["to"])[:, :, max(lens):]], 2).where(torch.arange(max(lens) + 2, device=DEV) < n[:, None, None],
+                                                                   gpu(s["to"])), s, 1)
+    assert (to[0, 0, 300:400] == 7).all() and (to[1, 0, 77:400] == 7).all()
+    fill()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        pva.pva_kvcache_weights(q, k, n, to, H, block_table=t, stream=stream)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(to[:, :, :max(lens)], got)
+    fill()
+    assert torch.equal(call(), got) and pva.pva_get_status(stream) == 0
+    del k, to
+    torch.cuda.empty_cache()
