@@ -85,7 +85,12 @@ struct Segment {
   int b, h, n, q, chunks, j0, j1, slot;
 };
 // Tiles that begin in the places [from, to) of a head.
-__device__ __forceinline__ int first_tile(int place, int chunks) { return (place + chunks - 1) / chunks; }
+__host__ __device__ constexpr int first_tile(int place, int chunks) {
+  return (int)(((unsigned)place + (unsigned)chunks - 1u) / (unsigned)chunks);
+}
+// The line may be as long as int32 allows, with more chunks to a tile than are left to its end.
+static_assert(first_tile(INT_MAX - 608, 500000) == 4295 && first_tile(INT_MAX, 1 << 30) == 2 && first_tile(0, 7) == 0 &&
+              first_tile(7, 7) == 1 && first_tile(8, 7) == 2, "tiles that begin before a place");
 
 // Walks the segments of places [x, end); one warp, the same state in all lanes.
 struct Walk {
