@@ -1005,7 +1005,8 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   const size_t all = 4 * (size_t)B * Hkv * width;
   if ((previous != out && meets(out, all, previous, all)) || meets(out, all, lse, 4 * (size_t)B * T * H) ||
       meets(out, all, lens, 4 * (size_t)B) || meets(out, all, q_lens, 4 * (size_t)B) ||
-      meets(out, all, table, 4 * (size_t)B * max_blocks))
+      meets(out, all, table, 4 * (size_t)B * max_blocks) || meets(out, all, q, size * B * T * H * d) ||
+      meets(out, all, k_cache, size * n_blocks * Hkv * page * d))
     return fail(PVA_ERR_INVALID_ARG, "weights overlap an input (previous may be weights)");
 
   WeightsParams p{};

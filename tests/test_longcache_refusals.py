@@ -125,6 +125,11 @@ def test_weights_refusals(lib, kw, code):
     assert pva.pva_last_error() != ""
 
 
+@pytest.mark.parametrize("to", [(1 << 20) + 6140, (1 << 20) - 4, (1 << 24) + 36860, (1 << 24) - 1436])
+def test_weights_over_the_queries_or_keys(lib, to):
+    assert weights(lib, to=to) == -1 and "overlap" in pva.pva_last_error()
+
+
 def prefix(lib, **kw):
     a = dict(q=1 << 20, k=1 << 24, v=1 << 28, lens=1 << 12, used=None, table=1 << 13, plens=1 << 14, start=1 << 15, ptable=1 << 16,
              out=1 << 32, lse=1 << 36, B=3, T=2, P=2, blocks=9, page=16, tw=4, pw=5, H=8, Hkv=2, d=64, scale=0.0, cap=0.0, dtype=2)
