@@ -495,6 +495,19 @@ extern "C" int pva_kvcache_evict(void* k_cache, void* v_cache, const float* weig
                     overlap(written[i].p, written[i].n, keep, 4 * (size_t)B)))
         return fail(PVA_ERR_INVALID_ARG, "weights_out or kept overlaps lens or keep");
     }
+    // the caches, layer by layer (what lies between their layers may be anything)
+    const Span beside[] = {{new_lens, 4 * (size_t)B}, {weights_out, all}, {kept, all}, {weights, all}, {lens, 4 * (size_t)B},
+                           {keep, 4 * (size_t)B}, {block_table, tables}, {out_table, out_tables}};
+    for (const Pool& pool : {p.from, p.to}) {
+      const size_t layer = (size_t)pool.blocks * kv_num_heads * pool.page * p.row_bytes;
+      for (const uint8_t* cache : {pool.k, pool.v})
+        for (const Span& s : beside) {
+          if (!overlap(cache, (layers - 1) * (size_t)pool.layer_bytes + layer, s.p, s.n)) continue;
+          for (int l = 0; l < layers; ++l)
+            if (overlap(cache + l * pool.layer_bytes, layer, s.p, s.n))
+              return fail(PVA_ERR_INVALID_ARG, "a cache overlaps the weights, lengths or tables");
+        }
+    }
     p.weights = weights;
     p.weights_out = weights_out;
     p.lens = lens;

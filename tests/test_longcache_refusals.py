@@ -103,6 +103,15 @@ def test_evict_refusals(lib, kw, code):
     assert pva.pva_last_error() != ""
 
 
+@pytest.mark.parametrize("kw", [
+    dict(new=(1 << 20) + 4), dict(wo=(1 << 24) + 36860), dict(kept=(1 << 24) - 1436), dict(w=1 << 20), dict(lens=(1 << 20) - 8),
+    dict(keep=1 << 24), dict(table=(1 << 20) + 64), dict(OUT, kept=1 << 40), dict(OUT, w=(1 << 44) + 30716), dict(OUT, lens=1 << 40),
+    dict(OUT, ot=1 << 44, otw=3), dict(layers=2, stride=1 << 18, new=(1 << 20) + (1 << 19) + 36860)])
+def test_evict_caches_over_other_tensors(lib, kw):
+    """Written or read, also in a layer behind the first."""
+    assert evict(lib, **kw) == -1 and "overlap" in pva.pva_last_error()
+
+
 def weights(lib, **kw):
     a = dict(q=1 << 20, k=1 << 24, lens=1 << 12, used=1 << 13, table=1 << 14, old=1 << 28, lse=1 << 32, to=1 << 36, B=3, T=2, blocks=9,
              page=16, tw=4, H=8, Hkv=2, d=64, width=60, decay=1.0, scale=0.0, cap=0.0, dtype=2)
