@@ -624,6 +624,15 @@ __global__ void __launch_bounds__(1024) pva_norm_weights_kernel(NormStep p, int 
     p.dw[which][blockIdx.x * 32 + threadIdx.y] = x;
 }
 
+// Whether `bytes` from p on share some with the rows (they may lie between two of them).
+bool span_meets(const void* p, size_t bytes, const RowRange& r, size_t size) {
+  if (!p || !r.p) return false;
+  const long long st = r.stride * (long long)size, wide = r.width * (long long)size;
+  const long long at = (long long)((intptr_t)p - (intptr_t)r.p), end = at + (long long)bytes;
+  if (end <= 0 || at >= (r.tokens - 1) * st + wide) return false;
+  return at < 0 || at % st < wide || at % st + (long long)bytes > st;
+}
+
 int norm_grid(const NormStep& p, int ctas, int num_sms) {
   const long long want = ((long long)p.tokens * p.parts + kNormWarps - 1) / kNormWarps;
   const long long most = (long long)num_sms * ctas;
@@ -826,6 +835,11 @@ extern "C" int pva_norm_rope_backward(const void* dq_out, const void* dk_out, co
         for (const RowRange& b : x)
           if (rows_meet(a, b, size))
             return fail(PVA_ERR_INVALID_ARG, "a gradient overlaps rows that the call reads");
+      const RowRange rows[6] = {x[0], x[1], out[0], out[1], {dq_out, tokens, dq_out_stride, w[0]}, {dk_out, tokens, dk_out_stride, w[1]}};
+      for (const float* dw : {dq_weight, dk_weight})
+        for (const RowRange& a : rows)
+          if (span_meets(dw, sizeof(float) * d, a, size))
+            return fail(PVA_ERR_INVALID_ARG, "a weight's gradient overlaps rows of the call");
     }
     if (dq_weight && dk_weight && (uintptr_t)dq_weight < (uintptr_t)(dk_weight + d) &&
         (uintptr_t)dk_weight < (uintptr_t)(dq_weight + d))

@@ -432,7 +432,7 @@ int pva_norm_rope(const void* q, const void* k, const void* q_weight, const void
  *            tensors are all NULL, or none is.
  * dq, dk   : may take the place of dq_out, dk_out (same address and stride).
  * dq_weight, dk_weight : device f32 [head_size], written (not added to), or NULL;
- *            refused where the weight is NULL.  The sums are taken in a fixed
+ *            refused where the weight is NULL, and over any of the rows.  The sums are taken in a fixed
  *            order: equal calls give equal bits.
  * A token with a position off the tables is left out of dq and dk and of the sums,
  * and PVA_DEV_ROPE is latched.  tokens = 0: the weights' gradients are zeros.

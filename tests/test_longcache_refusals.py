@@ -76,6 +76,13 @@ def test_norm_gradient_refusals(lib, kw, code):
     assert pva.pva_last_error() != ""
 
 
+@pytest.mark.parametrize("kw", [
+    dict(dwq=1 << 36), dict(dwk=(1 << 36) + 5116), dict(dwq=(1 << 40) - 252), dict(dwk=1 << 28), dict(dwq=(1 << 32) + 2556),
+    dict(dwq=1 << 20), dict(dwk=(1 << 24) + 1280), dict(dqs=400, dwq=(1 << 36) + 800 + 508), dict(dqs=400, dwq=(1 << 36) + 800 * 3 - 252)])
+def test_norm_weight_gradient_over_rows(lib, kw):
+    assert grad(lib, **kw) == -1 and "overlaps rows" in pva.pva_last_error()
+
+
 def evict(lib, **kw):
     a = dict(k=1 << 20, v=1 << 24, w=1 << 28, lens=1 << 12, keep=1 << 13, new=1 << 14, table=1 << 15, ko=None, vo=None, ot=None,
              wo=1 << 32, kept=1 << 36, B=3, layers=1, stride=0, blocks=9, page=16, tw=4, ostride=0, oblocks=0, opage=0, otw=0,
