@@ -223,7 +223,7 @@ struct PrefixWork {
 
 cudaError_t launch_prefix_tc(const PrefixParams& p, int dtype, const PrefixQueries& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t s);
-// Two query tiles per item (p.rows = 2 p.tile_rows), head sizes up to 192.
+// Two query tiles per item (p.rows = 2 p.tile_rows), head sizes up to 192, no softcap.
 cudaError_t launch_prefix_pair(const PrefixParams& p, int dtype, const PrefixQueries& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, cudaStream_t s);
 

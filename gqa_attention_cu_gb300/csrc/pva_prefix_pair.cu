@@ -1,4 +1,5 @@
-// The paired kernel (pva_tree_pair.cuh) with the work of pva_gqa_prefix.
+// The paired kernel (pva_tree_pair.cuh) with the work of pva_gqa_prefix, without a softcap
+// (which the one-tile kernel does faster).
 #include "pva_prefix.cuh"
 #include "pva_tree_pair.cuh"
 
@@ -11,10 +12,7 @@ template <typename T, int D>
 cudaError_t launch_d(const PrefixParams& p, const PrefixQueries& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t s) {
   constexpr int smem = PairCfg<D, 1>::SMEM;
-  const int cap = cap_form(p.softcap);
-  auto kern = cap == kNoCap ? pva_tree_pair_kernel<T, D, 1, kNoCap, PrefixWork>
-              : cap == kCap ? pva_tree_pair_kernel<T, D, 1, kCap, PrefixWork>
-                            : pva_tree_pair_kernel<T, D, 1, kLargeCap, PrefixWork>;
+  auto kern = pva_tree_pair_kernel<T, D, 1, kNoCap, PrefixWork>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(p.pieces), dim3(kThreads), smem, s, p, tq, tk, tv);
@@ -36,6 +34,7 @@ cudaError_t launch_type(const PrefixParams& p, const PrefixQueries& tq, const CU
 
 cudaError_t launch_prefix_pair(const PrefixParams& p, int dtype, const PrefixQueries& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, cudaStream_t s) {
+  if (p.softcap != 0.0f) return cudaErrorInvalidValue;
   return dtype == PVA_BF16 ? launch_type<__nv_bfloat16>(p, tq, tk, tv, s) : launch_type<__half>(p, tq, tk, tv, s);
 }
 
