@@ -4,10 +4,11 @@
 // An operation `Op` says how many entries there are, what is wrong with one, how many
 // places it has, where the sums go, and what comes of the total:
 //   int entries() const;
-//   uint32_t check(int e, int i0, int n, bool& off) const;   PVA_DEV_* bits, the same in
-//       all n threads that work on entry e; off: a block table entry that thread i0 has
-//       looked at is outside the pool
-//   long long places(int e) const;   of an entry that is sound
+//   uint32_t check(int e, int i0, int n, bool& off, bool& idle) const;   PVA_DEV_* bits,
+//       the same in all n threads that work on entry e; off: a block table entry that
+//       thread i0 has looked at is outside the pool; idle (in all of them): the entry has
+//       no places, and may be anything
+//   long long places(int e) const;   of an entry that is sound and not idle
 //   int32_t* start() const;          [entries + 1]
 //   void publish(long long all, uint32_t found, bool latched) const;   one thread
 #pragma once
@@ -41,10 +42,11 @@ __global__ void __launch_bounds__(kThreads) pva_line_front_kernel(Op op, uint32_
   __shared__ long long s_sum[kThreads / 32];
   const int tid = threadIdx.x, E = op.entries();
   const bool latched = (*(volatile uint32_t*)status & PVA_DEV_KV_CACHE) != 0;
-  bool off = false;
-  uint32_t bad = op.check(blockIdx.x, tid, kThreads, off);
+  bool off = false, idle = false;
+  uint32_t bad = op.check(blockIdx.x, tid, kThreads, off, idle);
   if (__syncthreads_or(off)) bad |= PVA_DEV_BLOCKS;
   if (tid == 0) {
+    op.start()[blockIdx.x] = idle;  // until the sum takes its place
     if (bad) atomicOr(status + kWordBad, bad);
     __threadfence();
     s_last = atomicAdd(status + kWordArrived, 1u) == gridDim.x - 1;
@@ -56,7 +58,9 @@ __global__ void __launch_bounds__(kThreads) pva_line_front_kernel(Op op, uint32_
   long long carry = 0;
   for (int e0 = 0; e0 < E && !found; e0 += kThreads) {
     const int e = e0 + tid;
-    const long long x = e < E ? op.places(e) : 0, upto = sum_upto(x);
+    const bool none = e >= E || __ldcg(op.start() + e);
+    const long long all = e < E ? op.places(e) : 0;  // (looked up beside that)
+    const long long x = none ? 0 : all, upto = sum_upto(x);
     if ((tid & 31) == 31) s_sum[tid >> 5] = upto;
     __syncthreads();
     long long before = carry;
@@ -87,9 +91,9 @@ __global__ void __launch_bounds__(kSmallThreads) pva_line_small_front_kernel(Op 
   if (tid == 0) s_bad = 0;
   __syncthreads();
   if (e < E) {
-    bool off = false;
-    uint32_t bad = op.check(e, tid - e * group, group, off);
-    if (tid == e * group) s_places[e] = bad ? 0 : op.places(e);
+    bool off = false, idle = false;
+    uint32_t bad = op.check(e, tid - e * group, group, off, idle);
+    if (tid == e * group) s_places[e] = bad || idle ? 0 : op.places(e);
     if (off) bad |= PVA_DEV_BLOCKS;
     if (bad) atomicOr(&s_bad, bad);
   }

@@ -31,17 +31,10 @@ struct PrefixFront {
   PrefixParams p;
   __device__ __forceinline__ int entries() const { return p.P + p.B; }
   __device__ __forceinline__ int32_t* start() const { return p.tile_start; }
-  // Whether a token in use sees the entry's rows: of the others nothing is read, nor has
-  // their table (or a prefix's length) to be sound.
-  __device__ __forceinline__ bool wanted(int e) const {
-    if (e >= p.P) return tree_nodes(p, e - p.P) != 0;
-    int b = p.prefix_start ? p.prefix_start[e] : 0;
-    const int end = p.prefix_start ? p.prefix_start[e + 1] : p.B;
-    while (b < end && tree_nodes(p, b) == 0) ++b;
-    return b < end;
-  }
-  // (what depends on nothing is loaded first)
-  __device__ __forceinline__ uint32_t check(int e, int i0, int n, bool& off) const {
+  // Entries whose rows no token in use sees are idle: nothing of them is read, nor has
+  // their table (or a prefix's length) to be sound.  (What depends on nothing is loaded
+  // first.)
+  __device__ __forceinline__ uint32_t check(int e, int i0, int n, bool& off, bool& idle) const {
     const bool is_prefix = e < p.P;
     const int b = is_prefix ? e : e - p.P;
     const int keys = is_prefix ? p.prefix_keys[b] : p.keys[b];
@@ -49,25 +42,29 @@ struct PrefixFront {
     const int width = is_prefix ? p.prefix_blocks : p.max_blocks;
     const int first = !is_prefix ? b : p.prefix_start ? p.prefix_start[e] : 0;
     const int end = !is_prefix ? b + 1 : p.prefix_start ? p.prefix_start[e + 1] : p.B;
-    const int tokens = tree_nodes(p, min(max(first, 0), p.B - 1));
+    int tokens = tree_nodes(p, min(max(first, 0), p.B - 1));
     const long long room = (long long)width * p.page;
     const bool some_off = table && line::off_pool(table + (size_t)b * width, (int)min((long long)keys, room), p.page,
                                                   p.n_blocks, i0, n);
     if (is_prefix) {
       if (first < 0 || end < first || end > p.B || (b == 0 && first != 0) || (b == p.P - 1 && end != p.B))
         return PVA_DEV_PREFIX;
-      if (first == end || (tokens == 0 && !wanted(e))) return 0u;
+      for (int i = first + 1; tokens == 0 && i < end; ++i) tokens = tree_nodes(p, i);
+      idle = first == end || tokens == 0;
+      if (idle) return 0u;
       if (keys < 0 || keys > room) return PVA_DEV_KV_LEN;
       off = some_off;
     } else {
       if (tokens < 0 || tokens > p.T || tokens > keys || keys < 0 || keys > room) return PVA_DEV_KV_LEN;
-      off = some_off && tokens > 0;
+      idle = tokens == 0;
+      off = some_off && !idle;
     }
     return 0u;
   }
   __device__ __forceinline__ long long places(int e) const {
-    const PrefixEntry x = prefix_entry(p, e);
-    return wanted(e) ? x.per_head(p) * p.Hkv : 0;
+    PrefixEntry x = prefix_entry(p, e);
+    x.keys = min(x.keys, INT_MAX - 65536);  // (an idle prefix's may be anything)
+    return x.per_head(p) * p.Hkv;
   }
   __device__ __forceinline__ void publish(long long sum, uint32_t found, bool latched) const {
     if (!found && sum > INT_MAX - 4ll * p.pieces) found = PVA_DEV_TOO_MANY;

@@ -141,7 +141,7 @@ struct WeightsFront {
   WeightsParams p;
   __device__ __forceinline__ int entries() const { return p.B; }
   __device__ __forceinline__ int32_t* start() const { return p.start; }
-  __device__ __forceinline__ uint32_t check(int b, int i0, int n, bool& off) const {
+  __device__ __forceinline__ uint32_t check(int b, int i0, int n, bool& off, bool&) const {
     const int rows = p.lens[b], tokens = p.q_lens ? p.q_lens[b] : p.T;
     if (rows < 0 || rows > p.width || (long long)rows > (long long)p.max_blocks * p.page || tokens < 0 ||
         tokens > p.T || tokens > rows)
