@@ -14,15 +14,16 @@
 // Weights are compared by a 32-bit key that rises with them; equal keys are taken
 // from the lowest row on, so the choice does not depend on timing.
 //
-// 16 prompts of 4000 to 16,000 rows cut to 2048, 8 kv heads of 128 bf16, copied: 70 us.
-// The move is 44 of them, 268 MB at 6.1 TB/s (floor of the whole: 42); the choice 20,
-// bound by the latency of votes and counts with one CTA an SM; of 16,000 rows, in cycles:
-// lengths and table 8000, first count 10,000, second 6000, list 10,000.  (Clusters of
-// four CTAs an item, counts through distributed shared memory: 60 us for the choice.
-// Four copies of the first count's bins: no less.  Each CTA copying its own rows: 67
-// against 69 us for 128 items, but 113 against 91 for 160.  Four rows in flight a thread
-// and half as many CTAs in the move: 51 us.)  One request of 700 rows: 13 us, of which 8
-// are launches.
+// 16 prompts of 4000 to 16,000 rows cut to 2048, 8 kv heads of 128 bf16, copied: 66 to 70
+// us (floor 42).  The move is 44 of them, 268 MB at 6.1 TB/s; the choice 20, bound by the
+// latency of votes and counts with one CTA an SM; of 16,000 rows, in cycles: lengths and
+// table 8000, first count 10,000, second 6000, list 10,000.  In place: 87 us.  One prompt
+// of 100,000 rows cut to 33,333: copied 138 us (floor 41), in place 353, where 16 CTAs a kv
+// head walk its rows, a barrier every 256 of them.  One request of 700 rows: 13 us, of
+// which 8 are launches.  (Clusters of four CTAs an item, counts through distributed shared
+// memory: 60 us for the choice.  Four copies of the first count's bins: no less.  Each CTA
+// copying its own rows: 67 against 69 us for 128 items, but 113 against 91 for 160.  Four
+// rows in flight a thread and half as many CTAs in the move: 51 us.)
 #include <limits.h>
 
 #include "pva_device.cuh"
@@ -535,6 +536,9 @@ extern "C" int pva_kvcache_evict(void* k_cache, void* v_cache, const float* weig
     // 64 registers a thread: an SM holds one CTA of 1024 threads, two of 512, four of 256
     // (us, 1024, 512 and 256: 160 items of 12,000 rows 91, 84, 98; 512 of 9000 151, 134,
     // 131; 160 of 30,000 141, 151, 187; 2048 of 2000 287, 231, 211).
+    // The rows are those that the tables and weights have room for, lengths being the
+    // device's: with room for 131,072 rows 2048 items of 2000 take 308 us instead of 210, 128
+    // of up to 16,000 77 instead of 70.
     const bool more = items > c.num_sms;  // up to that 1024 (128 items of up to 16,000: 70 of 71.5)
     const int threads = rows <= 2048 ? 256 : rows <= 8192 || (more && rows <= 16384) ? 512 : kSelectThreads;
     cudaError_t e = cudaFuncSetAttribute(pva_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

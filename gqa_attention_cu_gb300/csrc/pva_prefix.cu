@@ -273,14 +273,17 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
   }
   p.q_parts = 1;
   const long long R = (long long)B * T * G;
-  p.tile_rows = tc ? G * (kTcRows / G) : R <= 8 ? 8 : R <= 16 ? 16 : 24;
+  p.tile_rows = tc ? G * (kTcRows / G) : R <= 8 ? 8 : R <= 16 ? 16 : 24;  // f32: R of the whole batch
   p.own_rows = tc && (long long)T * G < p.tile_rows ? T * G : p.tile_rows;
-  // The paired kernel takes prefixes of more than two tiles of rows: its tile pair costs
+  // The paired kernel takes batches of more than two tiles of rows: its tile pair costs
   // 1.7 us where two tiles are 2.6, but a sequence's few own rows have its two score
   // buffers' place alone (d = 128, 32,768 shared rows, us, one-tile and paired kernel: 64
   // sequences of 100 to 2000 own rows x 4 heads 97 and 104, 128 of 100 to 1000 156 and
-  // 134, 256 of 10 to 100 211 and 173).  With a softcap two threads a row share the
-  // special functions in the one-tile kernel (d = 64, 64 sequences: 115 and 126).
+  // 134, 256 of 10 to 100 211 and 173).  So have prefixes with few rows, which the rule
+  // does not tell apart: 128 sequences of 200 own rows behind 2 prefixes of 16,000 rows
+  // 101 and 89, behind 4 or 8 of 8000 79 and 81, 101 and 102, behind 64 of 1000 99 and 113.
+  // With a softcap two threads a row share the special functions in the one-tile kernel
+  // (d = 64, 64 sequences: 115 and 126).
   const bool pair = tc && d <= 192 && R > 2 * p.tile_rows && p.softcap == 0.0f;
   p.rows = pair ? 2 * p.tile_rows : p.tile_rows;
   p.bn = tc ? tree_keys(d) : kTreeKeysF32;

@@ -432,8 +432,8 @@ int pva_norm_rope(const void* q, const void* k, const void* q_weight, const void
  *            tensors are all NULL, or none is.
  * dq, dk   : may take the place of dq_out, dk_out (same address and stride).
  * dq_weight, dk_weight : device f32 [head_size], written (not added to), or NULL;
- *            refused where the weight is NULL, and over any of the rows.  The sums are taken in a fixed
- *            order: equal calls give equal bits.
+ *            refused where the weight is NULL, and over any of the rows.  The sums are
+ *            taken in a fixed order: equal calls give equal bits.
  * A token with a position off the tables is left out of dq and dk and of the sums,
  * and PVA_DEV_ROPE is latched.  tokens = 0: the weights' gradients are zeros.
  * The sums use the workspace: its growth follows pva_forward's rules.
@@ -584,9 +584,10 @@ int pva_kvcache_accept(void* k_cache, void* v_cache, const int32_t* past_lens,
  * scale, softcap, dtype, stream : as pva_forward.
  *
  * Arithmetic, limits and alignment as pva_gqa_tree without a rotation, and num_heads /
- * kv_num_heads <= 128.  The workspace holds two f32 rows of head_size per query row.  Results do not depend on timing.  A value row that some token
- * sees should be finite: an infinity or NaN there can reach its other tokens, and in a
- * prefix all of its sequences.
+ * kv_num_heads <= 128.  The workspace holds two f32 rows of head_size per query row.
+ * Results do not depend on timing.  A value row that some token sees should be finite:
+ * an infinity or NaN there can reach its other tokens, and in a prefix all of its
+ * sequences.
  * A prefix none of whose sequences has a token in use needs neither a length nor blocks,
  * and a sequence without one needs no blocks: both may be stale.
  * Host errors: null pointers, counts below 1 or out of int32, and the limits.  Device
@@ -678,7 +679,8 @@ int pva_kvcache_weights(const void* q, const void* k_cache, const int32_t* lens,
  * dtype   : any of the codes; rows are moved bit by bit, head_size is any.
  * Host errors: null pointers, counts or sizes below 1, extents that do not fit in
  * int32, layer strides below a pool's size, tensors off their elements' alignment,
- * outputs over inputs; layers * B * kv_num_heads > 65535 is unsupported.
+ * outputs over inputs, a cache over any of the other tensors; layers * B *
+ * kv_num_heads > 65535 is unsupported.
  * A sequence is left as it is (in place: new_lens[b] = lens[b]; copied: 0, and
  * nothing is copied) when lens or keep is negative, lens is larger than the cache or
  * width, new_lens larger than the output (PVA_DEV_KV_LEN is latched), when a table
