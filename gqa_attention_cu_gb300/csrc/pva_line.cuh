@@ -5,7 +5,7 @@
 // places it has, where the sums go, and what comes of the total:
 //   int entries() const;
 //   uint32_t check(int e, int i0, int n, bool& off, bool& idle) const;   PVA_DEV_* bits,
-//       the same in all n threads that work on entry e; off: a block table entry that
+//       the same in all n threads (whole warps) that work on entry e; off: a block table entry that
 //       thread i0 has looked at is outside the pool; idle (in all of them): the entry has
 //       no places, and may be anything
 //   long long places(int e) const;   of an entry that is sound and not idle

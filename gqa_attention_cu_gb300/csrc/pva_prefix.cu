@@ -49,7 +49,8 @@ struct PrefixFront {
     if (is_prefix) {
       if (first < 0 || end < first || end > p.B || (b == 0 && first != 0) || (b == p.P - 1 && end != p.B))
         return PVA_DEV_PREFIX;
-      for (int i = first + 1; tokens == 0 && i < end; ++i) tokens = tree_nodes(p, i);
+      for (int i = first + 1 + (int)(threadIdx.x & 31); tokens == 0 && i - (int)(threadIdx.x & 31) < end; i += 32)
+        tokens = __any_sync(0xffffffffu, i < end && tree_nodes(p, i) != 0);
       idle = first == end || tokens == 0;
       if (idle) return 0u;
       if (keys < 0 || keys > room) return PVA_DEV_KV_LEN;
