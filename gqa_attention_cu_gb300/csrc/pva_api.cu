@@ -358,7 +358,7 @@ int prepare(const void* q, const void* k, const void* v, const int32_t* cu_q,
   // scale 0 selects the default 1/sqrt(head_size), computed in f32 as the
   // page does; softcap's sign does not matter (c * tanh(s / c) is even in c).
   P.scale = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
-  P.softcap = fabsf(softcap);
+  P.softcap = softcap_size(softcap, P.scale);
   P.is_causal = is_causal ? 1 : 0;
   P.status = w->status;
   P.ws = static_cast<int32_t*>(w->buf);

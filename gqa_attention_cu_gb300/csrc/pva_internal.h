@@ -151,6 +151,14 @@ struct CallContext {
                                // calls; 18 is what a call's first kernel tells its second
   uint8_t* buf = nullptr;      // workspace of at least the bytes asked for
 };
+// |softcap| within the range that the kernels' products with it and with scale / softcap
+// have: from 1e34 on it changes no score below 1e30, and below 1e-30 of the scale (or of
+// one) every score comes out as nothing beside one.  0: none.
+inline float softcap_size(float softcap, float scale) {
+  const float size = softcap < 0.0f ? -softcap : softcap, by = scale < 0.0f ? -scale : scale;
+  const float least = 1e-30f * (by < 1.0f ? 1.0f : by < 1e10f ? by : 1e10f);
+  return size == 0.0f ? 0.0f : size < least ? least : size < 1e34f ? size : 1e34f;
+}
 std::mutex& api_mutex();
 int sm_count(int* n);  // of the current device (under api_mutex)
 int acquire(cudaStream_t stream, size_t need, CallContext* c);

@@ -141,7 +141,7 @@ extern "C" int pva_forward_noalloc(const void* q, const void* k, const void* v,
   p.d = head_size;
   p.dv = v_head_size;
   p.scale = scale != 0.0f ? scale : 1.0f / sqrtf((float)head_size);
-  p.softcap = fabsf(softcap);
+  p.softcap = softcap_size(softcap, p.scale);
   p.is_causal = is_causal ? 1 : 0;
   p.status = status;
   p.ws = reinterpret_cast<int32_t*>(ds.base + kStatusBytes);

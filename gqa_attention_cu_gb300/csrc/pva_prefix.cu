@@ -260,7 +260,7 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
   const float s = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
   p.negated = tc && s < 0.0f;
   p.scale = tc ? fabsf(s) : s;
-  p.softcap = fminf(fabsf(softcap), 1e34f);
+  p.softcap = softcap_size(softcap, p.scale);
   if (p.softcap != 0.0f) {
     // Nearest polynomials up to kNearTanh and kMidTanh (pva_tree_tile.cuh); above
     // kCapOfExp the series as in pva_gqa_tree, but while softcap times the term that it
@@ -270,6 +270,7 @@ int gqa_prefix(const void* q, const void* k_cache, const void* v_cache, const in
                          ? tile::kNearTanh
                          : fmin(0.25, pow(ldexp(1.0, -18) * 315.0 / 17.0 / cap, 1.0 / 7.0));
     p.series_to = (float)fmin(t * cap / fabs(p.scale), 1e9);
+    if (fabs(p.scale) > 1e7 * cap) p.series_to = -1.0f;  // its coefficients would not be finite
     p.mid_to = (float)fmin(tile::kMidTanh * cap / fabs(p.scale), 1e9);
   }
   p.q_parts = 1;

@@ -1022,7 +1022,7 @@ int weights(const void* q, const void* k_cache, const int32_t* lens, const int32
   p.weights = out;
   p.decay = decay;
   p.scale = scale != 0.0f ? scale : 1.0f / sqrtf((float)d);
-  p.softcap = fminf(fabsf(softcap), 1e34f);
+  p.softcap = softcap_size(softcap, p.scale);
   p.B = B;
   p.T = T;
   p.H = H;
